@@ -27,14 +27,17 @@ plants plausible mistakes here and checks that the pins catch them.
 ``oracle.prefill`` is the same kind of definition for the second workload, fp8 varlen
 prefill attention with query/key head dim 192 and value head dim 128 (aiter PR #7375
 page); it is pinned by tests/test_oracle_prefill_pins.py and
-tests/test_oracle_prefill_mutants.py.  The library has no prefill kernel yet.
+tests/test_oracle_prefill_mutants.py.
+
+``oracle.tree`` (draft trees: attention and verification) and ``oracle.cache`` (the paged
+cache's book-keeping) are pinned by tests/test_oracle_tree_pins.py.
 """
 from .formats import E4M3_TABLE, e4m3_value, bf16_bits_to_f64, bf16_ulp
 from .attention import (kv_head_of, last_visible_key, gather_keys, verify_attention,
                         verify_attention_rows)
 from .metrics import max_err_over_std, excess_over_half_ulp
-from . import prefill
+from . import cache, prefill, tree
 
 __all__ = ["E4M3_TABLE", "e4m3_value", "bf16_bits_to_f64", "bf16_ulp", "kv_head_of",
            "last_visible_key", "gather_keys", "verify_attention", "verify_attention_rows",
-           "max_err_over_std", "excess_over_half_ulp", "prefill"]
+           "max_err_over_std", "excess_over_half_ulp", "cache", "prefill", "tree"]

@@ -1,5 +1,5 @@
 """ctypes loader for libmtpattn.so (the C ABI declared in include/mtpattn.h and
-include/fmha_fp8_varlen.h).
+include/fmha_fp8_varlen.h, include/mtp_tree.h and include/mtp_cache.h).
 
 There is no fallback: if the library is missing the import of this module's
 ``lib()`` raises, so no caller can silently run anything else.
@@ -16,7 +16,7 @@ _c_int, _c_i32, _c_i64, _c_size, _c_float = (ctypes.c_int, ctypes.c_int32, ctype
                                              ctypes.c_size_t, ctypes.c_float)
 _vp = ctypes.c_void_p
 
-# name -> (restype, argtypes), in the order of include/mtpattn.h, then include/fmha_fp8_varlen.h
+# name -> (restype, argtypes), in the order of include/mtpattn.h, then the other headers
 SIGNATURES = {
     "mtp_verify_attn_num_segments": (_c_i32, [_c_i32, _c_i32, _c_i32, _c_i32]),
     "mtp_verify_attn_workspace_size": (_c_size, [_c_i32, _c_i32, _c_i32]),
@@ -58,6 +58,54 @@ SIGNATURES = {
         _c_float, _c_i32,               # softmax_scale, causal
         _vp, _c_i64, _c_i64,            # out, strides (elements)
         _vp, _vp, _vp]),                # lse, status, stream
+    # include/mtp_tree.h
+    "mtp_tree_mask": (_c_int, [_vp, _vp, _c_i32, _c_i32, _vp, _vp, _vp]),
+    "mtp_tree_attn_fwd": (_c_int, [
+        _vp, _c_i64, _c_i64,            # q, strides
+        _vp, _vp, _c_i64,               # k_cache, v_cache, num_pages
+        _vp, _c_i32,                    # block_tables, max_pages_per_seq
+        _vp, _vp, _vp,                  # seq_lens, cu_seqlens_q, tree_mask
+        _c_i32, _c_i32, _c_i32, _c_i32,  # num_seqs, total_q, num_q_heads, num_kv_heads
+        _vp, _vp, _c_float,             # k_descale, v_descale, softmax_scale
+        _vp, _c_size,                   # workspace, workspace_bytes
+        _vp, _c_i64, _c_i64,            # out, strides
+        _vp, _vp]),                     # status, stream
+    "mtp_tree_attn_workspace_size": (_c_size, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
+    "mtp_tree_verify_greedy": (_c_int, [
+        _vp, _c_i32, _c_i64, _c_i32,    # logits, dtype, row_stride, vocab
+        _vp, _vp, _vp,                  # draft_tokens, parents, cu_seqlens_q
+        _c_i32, _c_i32, _c_i32,         # num_seqs, total_q, max_path
+        _vp, _vp, _vp,                  # accept_index, accept_len, out_tokens
+        _vp, _vp]),                     # status, stream
+    "mtp_tree_verify_sample": (_c_int, [
+        _vp, _c_i64, _vp, _c_i64,       # target_probs, stride, draft_probs, stride
+        _c_i32, _c_i32,                 # dtype, vocab
+        _vp, _vp, _vp, _vp,             # draft_tokens, parents, cu_seqlens_q, uniforms
+        _c_i32, _c_i32, _c_i32,         # num_seqs, total_q, max_path
+        _vp, _vp, _vp,                  # accept_index, accept_len, out_tokens
+        _vp, _vp]),                     # status, stream
+    # include/mtp_cache.h
+    "mtp_cache_workspace_size": (_c_size, [_c_i32, _c_i32]),
+    "mtp_cache_resize": (_c_int, [
+        _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i32,  # caches, layers, layer_stride, pages, kv heads
+        _vp, _c_i32, _vp, _c_i32, _vp,  # block_tables, max_pages, seq_lens, num_rows, ref_counts
+        _vp, _vp, _c_size,              # new_lens, workspace, workspace_bytes
+        _vp, _vp]),                     # status, stream
+    "mtp_cache_fork": (_c_int, [
+        _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i32,
+        _vp, _c_i32, _vp, _c_i32, _vp,
+        _vp, _vp, _c_i32, _vp, _c_size,  # src, dst, num_pairs, workspace, workspace_bytes
+        _vp, _vp]),
+    "mtp_cache_copy_pages": (_c_int, [
+        _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i32,
+        _vp, _vp, _c_i32,               # src_pages, dst_pages, num_pairs
+        _vp, _vp]),
+    "mtp_cache_compact": (_c_int, [
+        _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i32,
+        _vp, _c_i32, _vp, _vp,          # block_tables, max_pages, seq_lens, cu_seqlens_q
+        _c_i32, _c_i32,                 # num_seqs, total_q
+        _vp, _vp, _c_i32, _vp,          # accept_index, accept_len, max_path, new_seq_lens
+        _vp, _vp]),
 }
 
 _LIB = None

@@ -321,3 +321,344 @@ def fmha_fwd_fp8_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_des
     if rc != OK:
         raise MtpAttnError(rc)
     return (out, lse) if return_lse else out
+
+
+# ---- draft trees (include/mtp_tree.h) ------------------------------------------------------------
+
+TREE_MAX_NODES = 64
+TREE_MAX_RATIO = 16
+TREE_MAX_VOCAB = 1 << 20
+ERR_PARENT, ERR_ROW = 64, 128
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _int32_vector(name, t, n=None, what="a contiguous int32 vector"):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or \
+            not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be {what}" + (f" of {n}" if n is not None else ""))
+
+
+def _on_call_device(device, stream):
+    """The library launches on the current device: refuse tensors of another one here, where
+    the message can say so (the library would return E_DEVICE)."""
+    if device.type == "cuda" and device.index not in (None, torch.cuda.current_device()):
+        raise ValueError(f"tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if isinstance(stream, torch.cuda.Stream) and device.type == "cuda" and \
+            stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+
+
+def mtp_tree_mask(parents: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                  out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """One word per node of the packed draft trees: its ancestors' bits and its own.
+
+    parents [total_q] int32 (an index within the sequence; the root's entry is not read);
+    cu_seqlens_q [B+1] int32; returns int64 [total_q] (the bits of the uint64 words).
+    """
+    _int32_vector("parents", parents)
+    _int32_vector("cu_seqlens_q", cu_seqlens_q)
+    total_q, num_seqs = parents.numel(), cu_seqlens_q.numel() - 1
+    if num_seqs < 0:
+        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
+    _on_call_device(parents.device, stream)
+    with _temporaries_on(stream, parents.device, out is None):
+        if out is None:
+            out = torch.empty(total_q, dtype=torch.int64, device=parents.device)
+    if out.dtype not in (torch.int64, torch.uint64) or tuple(out.shape) != (total_q,) or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous int64 vector, one word per node")
+    rc = lib().mtp_tree_mask(_ptr(parents), _ptr(cu_seqlens_q), num_seqs, total_q, _ptr(out),
+                             _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+    return out
+
+
+def mtp_tree_attn_workspace_size(num_seqs: int, total_q: int, num_q_heads: int,
+                                 num_kv_heads: int, max_pages_per_seq: int) -> int:
+    return int(lib().mtp_tree_attn_workspace_size(num_seqs, total_q, num_q_heads, num_kv_heads,
+                                                  max_pages_per_seq))
+
+
+def mtp_tree_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                      cu_seqlens_q: torch.Tensor, tree_mask: torch.Tensor, k_descale, v_descale,
+                      softmax_scale: float, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of trees of 1 to 64 drafted tokens over the paged fp8 cache; returns ``out``.
+
+    As mtp_verify_attn_fwd, with any GQA ratio from 1 to 16 and ``tree_mask`` [total_q] int64:
+    node t sees every key before its sequence's tree (the last cu_seqlens_q[b+1] -
+    cu_seqlens_q[b] cached tokens) and the tree's node i where bit i of its word is set
+    (mtp_tree_mask makes the words).  A node that sees nothing gets zeros.  ``workspace``: at
+    least mtp_tree_attn_workspace_size(...) bytes, kept by a decode loop so that no call
+    allocates; it needs no initialisation.
+    """
+    dev = q.device
+    _on_call_device(dev, stream)
+    makes = (out is None or workspace is None or not isinstance(k_descale, torch.Tensor) or
+             not isinstance(v_descale, torch.Tensor))
+    with _temporaries_on(stream, dev, makes):
+        kd = _descale(k_descale, dev)
+        vd = _descale(v_descale, dev)
+        num_seqs, total_q, hq, hkv = _check_args(q, k_cache, v_cache, block_tables, seq_lens,
+                                                 cu_seqlens_q, kd, vd, out)
+        if tree_mask.dtype not in (torch.int64, torch.uint64) or \
+                tuple(tree_mask.shape) != (total_q,) or not tree_mask.is_contiguous():
+            raise ValueError("tree_mask must be a contiguous int64 vector, one word per node")
+        if out is None:
+            out = torch.empty(total_q, hq, HEAD_DIM, dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            need = mtp_tree_attn_workspace_size(num_seqs, total_q, hq, hkv, block_tables.shape[1])
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    rc = lib().mtp_tree_attn_fwd(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0],
+        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q),
+        _ptr(tree_mask), num_seqs, total_q, hq, hkv, _ptr(kd), _ptr(vd), float(softmax_scale),
+        _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(out), out.stride(0), out.stride(1), _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+    return out
+
+
+def _verify_args(rows, name, draft_tokens, parents, cu_seqlens_q, max_path, accept_index,
+                 accept_len, out_tokens, stream):
+    """Checks shared by the two verifications; makes the outputs that were not given."""
+    if rows.dtype not in _DTYPES or rows.dim() != 2 or rows.stride(1) != 1 and rows.shape[1] > 1:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 [total_q, vocab] with unit "
+                         "stride along the vocabulary")
+    total_q = rows.shape[0]
+    _int32_vector("draft_tokens", draft_tokens, total_q)
+    _int32_vector("parents", parents, total_q)
+    _int32_vector("cu_seqlens_q", cu_seqlens_q)
+    num_seqs = cu_seqlens_q.numel() - 1
+    if num_seqs < 0:
+        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
+    dev = rows.device
+    _on_call_device(dev, stream)
+    makes = accept_index is None or accept_len is None or out_tokens is None
+    with _temporaries_on(stream, dev, makes):
+        if accept_index is None:
+            accept_index = torch.empty(num_seqs, max_path, dtype=torch.int32, device=dev)
+        if accept_len is None:
+            accept_len = torch.empty(num_seqs, dtype=torch.int32, device=dev)
+        if out_tokens is None:
+            out_tokens = torch.empty(num_seqs, max_path, dtype=torch.int32, device=dev)
+    for what, t in (("accept_index", accept_index), ("out_tokens", out_tokens)):
+        if t.dtype != torch.int32 or tuple(t.shape) != (num_seqs, max_path) or \
+                not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous int32 [num_seqs, max_path] tensor")
+    _int32_vector("accept_len", accept_len, num_seqs)
+    return total_q, num_seqs, accept_index, accept_len, out_tokens
+
+
+def _row_stride(t):
+    """Elements from row to row; a single row's stride means nothing to torch."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def mtp_tree_verify_greedy(logits: torch.Tensor, draft_tokens: torch.Tensor,
+                           parents: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                           max_path: int = TREE_MAX_NODES,
+                           accept_index: Optional[torch.Tensor] = None,
+                           accept_len: Optional[torch.Tensor] = None,
+                           out_tokens: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None, stream=None):
+    """The path of drafted tokens that are their parents' argmax.
+
+    logits [total_q, vocab] float32, bfloat16 or float16 (the target's, after each node);
+    draft_tokens, parents [total_q] int32; returns (accept_index [B, max_path] int32: the
+    root's 0, the accepted nodes, -1s; accept_len [B] int32; out_tokens [B, max_path] int32: the
+    accepted tokens, the next token, -1s).
+    """
+    total_q, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
+        logits, "logits", draft_tokens, parents, cu_seqlens_q, int(max_path), accept_index,
+        accept_len, out_tokens, stream)
+    rc = lib().mtp_tree_verify_greedy(
+        _ptr(logits), _DTYPES[logits.dtype], _row_stride(logits), logits.shape[1],
+        _ptr(draft_tokens), _ptr(parents), _ptr(cu_seqlens_q), num_seqs, total_q, int(max_path),
+        _ptr(accept_index), _ptr(accept_len), _ptr(out_tokens), _ptr(status),
+        _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+    return accept_index, accept_len, out_tokens
+
+
+def mtp_tree_verify_sample(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor],
+                           draft_tokens: torch.Tensor, parents: torch.Tensor,
+                           cu_seqlens_q: torch.Tensor, uniforms: torch.Tensor,
+                           max_path: int = TREE_MAX_NODES,
+                           accept_index: Optional[torch.Tensor] = None,
+                           accept_len: Optional[torch.Tensor] = None,
+                           out_tokens: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None, stream=None):
+    """The path by rejection sampling from given uniform numbers.
+
+    target_probs [total_q, vocab] float32, bfloat16 or float16: the target's distribution after
+    each node; draft_probs the same shape and type, row i the distribution node i's children
+    were drawn from, or None (children chosen outright); uniforms [total_q] float32 in [0, 1):
+    each node's own number, the root's for the final draw.  Returns as mtp_tree_verify_greedy.
+    """
+    total_q, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
+        target_probs, "target_probs", draft_tokens, parents, cu_seqlens_q, int(max_path),
+        accept_index, accept_len, out_tokens, stream)
+    if draft_probs is not None and (
+            draft_probs.dtype != target_probs.dtype or draft_probs.shape != target_probs.shape or
+            draft_probs.stride(1) != 1 and draft_probs.shape[1] > 1):
+        raise ValueError("draft_probs must have target_probs' type and shape and unit stride along "
+                         "the vocabulary")
+    if uniforms.dtype != torch.float32 or tuple(uniforms.shape) != (total_q,) or \
+            not uniforms.is_contiguous():
+        raise ValueError("uniforms must be a contiguous float32 vector, one number per node")
+    rc = lib().mtp_tree_verify_sample(
+        _ptr(target_probs), _row_stride(target_probs), _ptr(draft_probs),
+        0 if draft_probs is None else _row_stride(draft_probs), _DTYPES[target_probs.dtype],
+        target_probs.shape[1], _ptr(draft_tokens), _ptr(parents), _ptr(cu_seqlens_q),
+        _ptr(uniforms), num_seqs, total_q, int(max_path), _ptr(accept_index), _ptr(accept_len),
+        _ptr(out_tokens), _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+    return accept_index, accept_len, out_tokens
+
+
+# ---- the paged cache's upkeep (include/mtp_cache.h) ----------------------------------------------
+
+CACHE_MAX_ROWS = 8192
+ERR_LEN, ERR_FULL, ERR_REF, ERR_CACHE_ROW = 256, 512, 1024, 2048
+
+
+def _cache_args(k_cache, v_cache, stream):
+    """(layers, layer stride in bytes, pages, KV heads) of one layer's caches [num_pages, 16,
+    H_kv, 256] or of a stack's [num_layers, num_pages, 16, H_kv, 256]."""
+    if k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn) or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache / v_cache must be uint8 or float8_e4m3fn codes")
+    if k_cache.dim() not in (4, 5) or k_cache.shape[-3] != PAGE_SIZE or \
+            k_cache.shape[-1] != HEAD_DIM:
+        raise ValueError("k_cache must be [num_pages, 16, H_kv, 256], or that behind num_layers")
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache must be of the same shape and strides")
+    layer = k_cache[0] if k_cache.dim() == 5 else k_cache
+    if not layer.is_contiguous():
+        raise ValueError("a layer's cache must be contiguous")
+    _on_call_device(k_cache.device, stream)
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    stride = k_cache.stride(0) if layers > 1 else layer.numel()
+    return layers, stride, k_cache.shape[-4], k_cache.shape[-2]
+
+
+def _table_args(block_tables, seq_lens, ref_counts, num_pages):
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
+            not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [num_rows, max_pages] tensor")
+    _int32_vector("seq_lens", seq_lens, block_tables.shape[0])
+    _int32_vector("ref_counts", ref_counts, num_pages)
+
+
+def _cache_workspace(workspace, block_tables, stream):
+    with _temporaries_on(stream, block_tables.device, workspace is None):
+        if workspace is None:
+            workspace = torch.empty(max(mtp_cache_workspace_size(*block_tables.shape), 256),
+                                    dtype=torch.uint8, device=block_tables.device)
+    return workspace
+
+
+def mtp_cache_workspace_size(num_rows: int, max_pages_per_seq: int) -> int:
+    return int(lib().mtp_cache_workspace_size(num_rows, max_pages_per_seq))
+
+
+def mtp_cache_resize(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, ref_counts: torch.Tensor, new_lens: torch.Tensor,
+                     workspace: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Set every row's length, in place: pages are given back and handed out.
+
+    k_cache / v_cache: one layer's caches or a stack's, [num_layers, num_pages, 16, H_kv, 256];
+    block_tables [rows, max_pages], seq_lens [rows], ref_counts [num_pages] int32 are updated;
+    new_lens [rows] int32 (0 frees a row).  A shared, partly filled last page is copied first.
+    With too few free pages nothing is handed out and ERR_FULL is set.
+    """
+    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
+    _table_args(block_tables, seq_lens, ref_counts, pages)
+    _int32_vector("new_lens", new_lens, block_tables.shape[0])
+    workspace = _cache_workspace(workspace, block_tables, stream)
+    rc = lib().mtp_cache_resize(
+        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), block_tables.shape[0], _ptr(ref_counts),
+        _ptr(new_lens), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+
+
+def mtp_cache_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                   seq_lens: torch.Tensor, ref_counts: torch.Tensor, src: torch.Tensor,
+                   dst: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows dst[i] (empty) become copies of rows src[i]: full pages are shared, a partly filled
+    last page is copied.  src, dst int32 vectors of the same length."""
+    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
+    _table_args(block_tables, seq_lens, ref_counts, pages)
+    _int32_vector("src", src)
+    _int32_vector("dst", dst, src.numel())
+    workspace = _cache_workspace(workspace, block_tables, stream)
+    rc = lib().mtp_cache_fork(
+        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), block_tables.shape[0], _ptr(ref_counts),
+        _ptr(src), _ptr(dst), src.numel(), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+
+
+def mtp_cache_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src_pages: torch.Tensor,
+                         dst_pages: torch.Tensor, status: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """Page dst_pages[i] gets the contents of page src_pages[i], in all layers."""
+    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
+    _int32_vector("src_pages", src_pages)
+    _int32_vector("dst_pages", dst_pages, src_pages.numel())
+    rc = lib().mtp_cache_copy_pages(
+        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(src_pages),
+        _ptr(dst_pages), src_pages.numel(), _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+
+
+def mtp_cache_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                      seq_lens: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                      accept_index: torch.Tensor, accept_len: torch.Tensor,
+                      new_seq_lens: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Move the accepted paths' keys and values to the front of their trees' places, in all
+    layers, in place; returns new_seq_lens [B] int32 (the tokens kept).
+
+    accept_index [B, max_path] and accept_len [B] as the verifications return them.  The pages
+    that hold the trees must belong to their rows alone; none are given back here.
+    """
+    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
+    num_seqs = seq_lens.numel()
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != num_seqs or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [B, max_pages] tensor")
+    _int32_vector("seq_lens", seq_lens)
+    _int32_vector("cu_seqlens_q", cu_seqlens_q, num_seqs + 1)
+    _int32_vector("accept_len", accept_len, num_seqs)
+    if accept_index.dtype != torch.int32 or accept_index.dim() != 2 or \
+            accept_index.shape[0] != num_seqs or not accept_index.is_contiguous():
+        raise ValueError("accept_index must be a contiguous int32 [B, max_path] tensor")
+    with _temporaries_on(stream, seq_lens.device, new_seq_lens is None):
+        if new_seq_lens is None:
+            new_seq_lens = torch.empty_like(seq_lens)
+    _int32_vector("new_seq_lens", new_seq_lens, num_seqs)
+    rc = lib().mtp_cache_compact(
+        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q), num_seqs,
+        num_seqs * TREE_MAX_NODES, _ptr(accept_index), _ptr(accept_len), accept_index.shape[1],
+        _ptr(new_seq_lens), _ptr(status), _stream_handle(stream))
+    if rc != OK:
+        raise MtpAttnError(rc)
+    return new_seq_lens

@@ -264,7 +264,7 @@ extern "C" const char* mtp_verify_attn_strerror(int status) {
   switch (status) {
     case MTPATTN_OK: return "ok";
     case MTPATTN_E_ARG: return "invalid argument (null pointer, negative count, stride or alignment)";
-    case MTPATTN_E_UNSUPPORTED: return "unsupported configuration (GQA ratio must be 8 or 16, q_len <= 4, num_segments in [0, 64])";
+    case MTPATTN_E_UNSUPPORTED: return "unsupported configuration (verify attention: GQA ratio 8 or 16, q_len <= 4, num_segments in [0, 64]; other entry points: see their headers)";
     case MTPATTN_E_DEVICE: return "pointer is not device memory of the current CUDA device, or no CUDA device";
     case MTPATTN_E_WORKSPACE: return "workspace missing, smaller than mtp_verify_attn_workspace_size() or not 256-byte aligned";
     case MTPATTN_E_LAUNCH: return "kernel launch failed";

@@ -1,0 +1,589 @@
+// Verification of drafted tokens: the walk down the draft tree, greedy or by rejection
+// sampling (the entry points' formulas are in include/mtp_tree.h).
+//
+// A thread-block cluster takes one sequence: the walk is sequential (a node's row is chosen by
+// the step before), so what can be spread is the row, and only the rows on the path are read.
+// Every CTA of the cluster holds the tree in shared memory and takes the same decisions; a
+// row's scan is split over the CTAs, whose results meet through distributed shared memory.
+//
+// The scan of a row is bound by the latency of its loads: thread t takes elements t, t + T, ...
+// of its CTA's part, kUnroll of them in flight, so any row address and vocabulary will do.
+#include "common.cuh"
+#include "host_checks.cuh"
+
+#include "../../include/mtp_tree.h"
+
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+namespace cg = cooperative_groups;
+
+namespace mtpattn {
+namespace {
+
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kNodes = MTP_TREE_MAX_NODES;
+constexpr int kChunk = 1024;                       // elements whose sum is kept (sampling)
+constexpr int kPerLane = kChunk / 32;
+
+struct VerifyParams {
+  const void* p;             // logits, or the target's probabilities
+  const void* q;             // the drafter's probabilities, or null
+  int64_t p_stride, q_stride;
+  int32_t vocab;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* cu_q;
+  const float* u;
+  int32_t total_q, max_path;
+  int32_t* accept_index;
+  int32_t* accept_len;
+  int32_t* out_tokens;
+  int32_t* status;
+};
+
+// The tree of one sequence and the path found so far; the same in every CTA of the cluster.
+struct Walk {
+  int32_t tok[kNodes], par[kNodes];
+  uint64_t kids[kNodes];     // children of each node, one bit each
+  int32_t path[kNodes];
+  int n, q0;
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+
+// Loads and checks the sequence's tree; false (the same in every thread of the cluster) if it
+// is not one, with the error outputs written.
+__device__ bool load_tree(const VerifyParams& p, int b, bool first_cta, Walk& w) {
+  const int t = threadIdx.x;
+  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+  int err = (q0 < 0 || q1 <= q0 || q1 > p.total_q || q1 - q0 > kNodes) ? MTPATTN_ERR_QLEN : 0;
+  const int n = err ? 0 : q1 - q0;
+  if (t < kNodes) w.kids[t] = 0;
+  if (t == 0) {
+    w.n = n;
+    w.q0 = q0;
+    w.path[0] = 0;
+  }
+  int bad_parent = 0;
+  if (t < n) {
+    w.tok[t] = p.tokens[q0 + t];
+    w.par[t] = t == 0 ? -1 : p.parents[q0 + t];
+    bad_parent = t > 0 && (w.par[t] < 0 || w.par[t] >= t);
+  }
+  if (__syncthreads_or(bad_parent)) err |= MTP_TREE_ERR_PARENT;
+  if (err) {
+    if (first_cta) {
+      if (t == 0) {
+        set_status(p.status, err);
+        p.accept_len[b] = -1;
+      }
+      if (t < p.max_path) {
+        p.accept_index[static_cast<int64_t>(b) * p.max_path + t] = -1;
+        p.out_tokens[static_cast<int64_t>(b) * p.max_path + t] = -1;
+      }
+    }
+    return false;
+  }
+  if (t > 0 && t < n)
+    atomicOr(reinterpret_cast<unsigned long long*>(&w.kids[w.par[t]]), 1ull << t);
+  __syncthreads();
+  return true;
+}
+
+// The outputs of a finished walk of `count` accepted nodes.
+__device__ void emit(const VerifyParams& p, int b, const Walk& w, int count, int next) {
+  const int t = threadIdx.x;
+  if (t == 0) {
+    p.accept_len[b] = count;
+    if (next < 0) set_status(p.status, MTP_TREE_ERR_ROW);
+  }
+  if (t < p.max_path) {
+    const int64_t at = static_cast<int64_t>(b) * p.max_path + t;
+    p.accept_index[at] = t <= count ? w.path[t] : -1;
+    p.out_tokens[at] = t < count ? w.tok[w.path[t + 1]] : (t == count ? next : -1);
+  }
+}
+
+// ---- greedy --------------------------------------------------------------------------------------
+
+// The order of float values as an order of unsigned numbers, both zeros alike; 0 for NaN.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kVerifyThreads)
+verify_greedy_kernel(const VerifyParams p) {
+  constexpr int kUnroll = 16;
+  __shared__ Walk w;
+  __shared__ uint64_t s_warp[kVerifyWarps];
+  __shared__ uint64_t s_best[2][kMaxCluster];      // by step parity: the CTAs' best keys
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = cluster.num_blocks(), part = cluster.block_rank();
+  const int b = blockIdx.x / parts, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const bool ok = load_tree(p, b, part == 0, w);
+  // every CTA of the cluster has to be running before its shared memory is written
+  cluster.sync();
+  if (!ok) return;
+  const int per = (p.vocab + parts - 1) / parts;
+  const int lo = min(p.vocab, part * per), hi = min(p.vocab, lo + per);
+  int cur = 0, count = 0, next = -1;
+  for (int step = 0;; ++step) {
+    const T* row = static_cast<const T*>(p.p) + static_cast<int64_t>(w.q0 + cur) * p.p_stride;
+    uint32_t best = 0, at = 0;
+    for (int i0 = lo + t; i0 < hi; i0 += kUnroll * kVerifyThreads) {
+      T v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (i0 + u * kVerifyThreads < hi) v[u] = row[i0 + u * kVerifyThreads];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (i0 + u * kVerifyThreads < hi) {
+          const uint32_t o = order_of(to_f32(v[u]));
+          if (o > best) {                           // a thread's elements ascend: ties keep the first
+            best = o;
+            at = i0 + u * kVerifyThreads;
+          }
+        }
+    }
+    // largest value, then lowest token; 0: nothing but NaN
+    uint64_t key = best ? (static_cast<uint64_t>(best) << 32 | static_cast<uint32_t>(~at)) : 0ull;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+      key = other > key ? other : key;
+    }
+    if (lane == 0) s_warp[warp] = key;
+    __syncthreads();
+    if (t < parts) {
+      uint64_t k = 0;
+      for (int i = 0; i < kVerifyWarps; ++i) k = s_warp[i] > k ? s_warp[i] : k;
+      *cluster.map_shared_rank(&s_best[step & 1][part], t) = k;
+    }
+    cluster.sync();
+    uint64_t k = 0;
+    for (int i = 0; i < parts; ++i) k = s_best[step & 1][i] > k ? s_best[step & 1][i] : k;
+    next = k ? static_cast<int>(~static_cast<uint32_t>(k)) : -1;
+    if (next < 0 || count == p.max_path - 1) break;
+    int child = -1;
+    for (uint64_t m = w.kids[cur]; m && child < 0; m &= m - 1) {
+      const int i = __ffsll(static_cast<long long>(m)) - 1;
+      if (w.tok[i] == next) child = i;
+    }
+    if (child < 0) break;
+    cur = child;
+    ++count;
+    if (t == 0) w.path[count] = cur;               // read behind later barriers only
+  }
+  __syncthreads();
+  if (part == 0) emit(p, b, w, count, next);
+}
+
+// ---- sampling ------------------------------------------------------------------------------------
+
+// Probabilities in units of 2^-52 (exact for a float of at least 2^-28), NaN as 0.
+__device__ __forceinline__ int64_t fixed_of(float x) {
+  return __float2ll_rn(__saturatef(x) * 4503599627370496.f);
+}
+
+// One sum over a row: w = max(p - S q, 0) with S in units of 2^-57.
+struct Row {
+  const void* p;
+  const void* q;             // null: w = p
+  uint64_t S;
+};
+
+template <class T>
+__device__ __forceinline__ int64_t left_of(const Row& r, float pv, float qv) {
+  int64_t x = fixed_of(pv);
+  if (r.q) {
+    // S q: (q 2^59) (S 2^57) 2^-64, rounded down to a unit; exact for S = 1
+    x -= static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(fixed_of(qv)) << 7, r.S));
+    x = x > 0 ? x : 0;
+  }
+  return x;
+}
+
+// Sums of the CTA's chunks [c_lo, c_hi) of kChunk elements into s_sum (index c - c_lo), a warp a
+// chunk, 32 elements a lane.
+template <class T>
+__device__ void chunk_sums(const Row& r, int vocab, int c_lo, int c_hi, int64_t* s_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T* rp = static_cast<const T*>(r.p);
+  const T* rq = static_cast<const T*>(r.q);
+  for (int c = c_lo + warp; c < c_hi; c += kVerifyWarps) {
+    const int i0 = c * kChunk + lane;
+    int64_t sum = 0;
+#pragma unroll
+    for (int h = 0; h < kPerLane; h += 16) {
+      T pv[16], qv[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int i = i0 + 32 * (h + u);
+        pv[u] = i < vocab ? rp[i] : T(0.f);
+      }
+      if (rq) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int i = i0 + 32 * (h + u);
+          qv[u] = i < vocab ? rq[i] : T(0.f);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) sum += left_of<T>(r, to_f32(pv[u]), rq ? to_f32(qv[u]) : 0.f);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_sum[c - c_lo] = sum;
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kVerifyThreads)
+verify_sample_kernel(const VerifyParams p) {
+  extern __shared__ int64_t s_sum[];               // the CTA's chunk sums
+  __shared__ Walk w;
+  __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];   // p, q of each node's token, its number
+  __shared__ int64_t s_part[2][kMaxCluster];       // by sum parity: the CTAs' sums
+  __shared__ int64_t s_warp[kVerifyWarps];
+  __shared__ int s_next;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = cluster.num_blocks(), part = cluster.block_rank();
+  const int b = blockIdx.x / parts, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const bool ok = load_tree(p, b, part == 0, w);
+  const T* P = static_cast<const T*>(p.p);
+  const T* Q = static_cast<const T*>(p.q);
+  if (ok) {
+    if (t < w.n) {
+      const int tok = w.tok[t];
+      float pv = 0.f, qv = 1.f;
+      if (t > 0 && tok >= 0 && tok < p.vocab) {
+        const int64_t row = w.q0 + w.par[t];
+        pv = __saturatef(to_f32(P[row * p.p_stride + tok]));
+        if (Q) qv = __saturatef(to_f32(Q[row * p.q_stride + tok]));
+      }
+      s_p[t] = pv;
+      s_q[t] = qv;
+      // into [0, 1 - 2^-24]; NaN as 0
+      s_u[t] = fminf(fmaxf(p.u[w.q0 + t], 0.f), 0.999999940395355224609375f);
+    }
+    if (t == 0) s_next = -1;
+  }
+  cluster.sync();                                  // also: every CTA is running
+  if (!ok) return;
+  const int chunks = (p.vocab + kChunk - 1) / kChunk;
+  const int per = (chunks + parts - 1) / parts;
+  const int c_lo = min(chunks, part * per), c_hi = min(chunks, c_lo + per);
+  int sums = 0;                                    // sums taken so far
+  // Sum of the row over the cluster; `before`: the sum of the CTAs ahead of this one.  Refused
+  // tokens (without a drafter) are taken out of their chunks.
+  uint64_t gone = 0;                               // refused children of the node, one bit each
+  auto total_of = [&](const Row& r, int64_t& before) -> int64_t {
+    chunk_sums<T>(r, p.vocab, c_lo, c_hi, s_sum);
+    __syncthreads();
+    if (t == 0 && gone) {
+      for (uint64_t m = gone; m; m &= m - 1) {
+        const int i = __ffsll(static_cast<long long>(m)) - 1;
+        const int c = w.tok[i] / kChunk;
+        if (c >= c_lo && c < c_hi) s_sum[c - c_lo] -= fixed_of(s_p[i]);
+      }
+    }
+    __syncthreads();
+    int64_t mine = 0;
+    for (int c = t; c < c_hi - c_lo; c += kVerifyThreads) mine += s_sum[c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    if (t < parts) {
+      int64_t k = 0;
+      for (int i = 0; i < kVerifyWarps; ++i) k += s_warp[i];
+      *cluster.map_shared_rank(&s_part[sums & 1][part], t) = k;
+    }
+    cluster.sync();
+    int64_t all = 0;
+    before = 0;
+    for (int i = 0; i < parts; ++i) {
+      if (i < part) before += s_part[sums & 1][i];
+      all += s_part[sums & 1][i];
+    }
+    ++sums;
+    return all;
+  };
+
+  int cur = 0, count = 0;
+  Row r;
+  while (true) {                                   // one node of the path per turn
+    r.p = P + static_cast<int64_t>(w.q0 + cur) * p.p_stride;
+    r.q = nullptr;
+    r.S = 0;
+    gone = 0;
+    double left = 1.0;                             // Z: what w sums to
+    int child = -1;
+    uint64_t kids = count == p.max_path - 1 ? 0ull : w.kids[cur];
+    while (kids) {
+      const int i = __ffsll(static_cast<long long>(kids)) - 1;
+      kids &= kids - 1;
+      const bool known = w.tok[i] >= 0 && w.tok[i] < p.vocab;
+      const double u = s_u[i];
+      if (Q) {
+        const double ql = static_cast<double>(s_q[i]);
+        double wl = s_p[i];
+        if (r.S)                                   // S q as in left_of, in units of 2^-52
+          wl = static_cast<double>(max(static_cast<long long>(0), static_cast<long long>(fixed_of(s_p[i]) -
+               static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(fixed_of(s_q[i])) << 7, r.S))))) *
+               2.220446049250313e-16;
+        if (known && u * ql * left < wl) {
+          child = i;
+          break;
+        }
+        r.q = Q + static_cast<int64_t>(w.q0 + cur) * p.q_stride;
+        const uint64_t add = static_cast<uint64_t>(left * 144115188075855872.0);   // Z 2^57, exact
+        r.S = r.S + add < r.S ? ~0ull : r.S + add;
+        if (kids) {
+          int64_t before;
+          left = static_cast<double>(total_of(r, before)) * 2.220446049250313e-16;
+        }
+      } else {
+        bool again = !known;                       // a token that has left the row already
+        for (uint64_t m = gone; m; m &= m - 1)
+          again |= w.tok[__ffsll(static_cast<long long>(m)) - 1] == w.tok[i];
+        const double wl = again ? 0.0 : static_cast<double>(s_p[i]);
+        if (u * left < wl) {
+          child = i;
+          break;
+        }
+        left -= wl;
+        if (!again) gone |= 1ull << i;
+      }
+    }
+    if (child < 0) break;
+    cur = child;
+    ++count;
+    if (t == 0) w.path[count] = cur;
+  }
+  // The final draw from w: its sum, the chunk where the running sum passes u sum, the element.
+  int64_t before, all = total_of(r, before);
+  if (all == 0) {                                  // nothing left of the row: p itself
+    r.q = nullptr;
+    r.S = 0;
+    gone = 0;
+    all = total_of(r, before);
+  }
+  if (all > 0) {
+    // the running sum passes u * all where it passes floor(u * all)
+    const uint64_t u64 = static_cast<uint64_t>(static_cast<double>(s_u[0]) * 18446744073709551616.0);
+    const int64_t goal = static_cast<int64_t>(__umul64hi(u64, static_cast<uint64_t>(all)));
+    if (warp == 0) {
+      int64_t run = before;                        // before the 32 chunks looked at
+      for (int c0 = 0; c0 < c_hi - c_lo; c0 += 32) {
+        const int64_t mine = c0 + lane < c_hi - c_lo ? s_sum[c0 + lane] : 0;
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, run + upto > goal);
+        if (run <= goal && past) {
+          const int f = __ffs(past) - 1;
+          const int c = c_lo + c0 + f;
+          run += __shfl_sync(0xffffffffu, upto - mine, f);
+          // lane l takes the chunk's elements 32 l .. 32 l + 31
+          const T* rp = static_cast<const T*>(r.p);
+          const T* rq = static_cast<const T*>(r.q);
+          const int i0 = c * kChunk + lane * kPerLane;
+          int64_t v[kPerLane], sum = 0;
+#pragma unroll
+          for (int u = 0; u < kPerLane; ++u) {
+            const int i = i0 + u;
+            v[u] = i < p.vocab ? left_of<T>(r, to_f32(rp[i]), rq ? to_f32(rq[i]) : 0.f) : 0;
+            for (uint64_t m = gone; m; m &= m - 1)
+              if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i) v[u] = 0;
+            sum += v[u];
+          }
+          int64_t to = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, to, o);
+            if (lane >= o) to += x;
+          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, run + to > goal);
+          if (lane == __ffs(hit) - 1) {
+            int64_t at = run + to - sum;
+            int found = -1;
+#pragma unroll
+            for (int u = 0; u < kPerLane; ++u) {
+              at += v[u];
+              if (found < 0 && at > goal) found = i0 + u;
+            }
+            *cluster.map_shared_rank(&s_next, 0) = found;
+          }
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+  }
+  cluster.sync();                                  // s_next is in, and no CTA leaves before
+  if (part == 0) emit(p, b, w, count, s_next);
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+
+// CTAs a sequence: as many as there is room for at two CTAs an SM, each with 2048 elements of
+// the row at least.
+int cluster_size(int num_seqs, int vocab) {
+  const int sms = device_sm_count(-1);
+  int c = 1;
+  while (c < kMaxCluster && static_cast<int64_t>(num_seqs) * 2 * c <= 2 * sms && vocab / (2 * c) >= 2048)
+    c *= 2;
+  return c;
+}
+
+template <class K>
+cudaError_t launch(K kernel, const VerifyParams& p, int num_seqs, int cluster, size_t smem,
+                   cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * cluster);
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  return cudaGetLastError();
+}
+
+// The checks both entry points share; MTPATTN_OK with *run = false for an empty batch.
+int check(const void* rows, int64_t stride, int32_t dtype, int32_t vocab, const int32_t* tokens,
+          const int32_t* parents, const int32_t* cu_q, int32_t num_seqs, int32_t total_q,
+          int32_t max_path, const int32_t* accept_index, const int32_t* accept_len,
+          const int32_t* out_tokens, const int32_t* status, bool* run) {
+  *run = false;
+  if (num_seqs < 0 || total_q < 0 || vocab <= 0 || max_path < 1) return MTPATTN_E_ARG;
+  if (num_seqs == 0) return total_q == 0 ? MTPATTN_OK : MTPATTN_E_ARG;
+  if (total_q < num_seqs || !rows || !tokens || !parents || !cu_q || !accept_index ||
+      !accept_len || !out_tokens || stride < vocab)
+    return MTPATTN_E_ARG;
+  if (dtype != MTP_F32 && dtype != MTP_BF16 && dtype != MTP_F16) return MTPATTN_E_UNSUPPORTED;
+  if (!ptr_aligned(rows, dtype == MTP_F32 ? 4 : 2) || !ptr_aligned(tokens, 4) ||
+      !ptr_aligned(parents, 4) || !ptr_aligned(cu_q, 4) || !ptr_aligned(accept_index, 4) ||
+      !ptr_aligned(accept_len, 4) || !ptr_aligned(out_tokens, 4) || !ptr_aligned(status, 4))
+    return MTPATTN_E_ARG;
+  if (total_q > static_cast<int64_t>(num_seqs) * kNodes || max_path > kNodes ||
+      vocab > MTP_TREE_MAX_VOCAB || num_seqs > (1 << 24))
+    return MTPATTN_E_UNSUPPORTED;
+  const int device = current_device();
+  if (device < 0) return MTPATTN_E_DEVICE;
+  const void* const ptrs[] = {rows, tokens, parents, cu_q, accept_index, accept_len, out_tokens};
+  if (!all_on_device(ptrs, device) || (status && !ptr_on_device(status, device)))
+    return MTPATTN_E_DEVICE;
+  *run = true;
+  return MTPATTN_OK;
+}
+
+}  // namespace
+}  // namespace mtpattn
+
+using namespace mtpattn;
+
+extern "C" int mtp_tree_verify_greedy(const void* logits, int32_t dtype, int64_t row_stride,
+                                      int32_t vocab, const int32_t* draft_tokens,
+                                      const int32_t* parents, const int32_t* cu_seqlens_q,
+                                      int32_t num_seqs, int32_t total_q, int32_t max_path,
+                                      int32_t* accept_index, int32_t* accept_len,
+                                      int32_t* out_tokens, int32_t* status, void* stream) {
+  bool run;
+  const int rc = check(logits, row_stride, dtype, vocab, draft_tokens, parents, cu_seqlens_q,
+                       num_seqs, total_q, max_path, accept_index, accept_len, out_tokens, status,
+                       &run);
+  if (rc != MTPATTN_OK || !run) return rc;
+  VerifyParams p{};
+  p.p = logits;
+  p.p_stride = row_stride;
+  p.vocab = vocab;
+  p.tokens = draft_tokens;
+  p.parents = parents;
+  p.cu_q = cu_seqlens_q;
+  p.total_q = total_q;
+  p.max_path = max_path;
+  p.accept_index = accept_index;
+  p.accept_len = accept_len;
+  p.out_tokens = out_tokens;
+  p.status = status;
+  const int c = cluster_size(num_seqs, vocab);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      dtype == MTP_F32 ? launch(verify_greedy_kernel<float>, p, num_seqs, c, 0, st)
+      : dtype == MTP_BF16 ? launch(verify_greedy_kernel<__nv_bfloat16>, p, num_seqs, c, 0, st)
+                          : launch(verify_greedy_kernel<__half>, p, num_seqs, c, 0, st);
+  return e == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
+}
+
+extern "C" int mtp_tree_verify_sample(const void* target_probs, int64_t target_stride,
+                                      const void* draft_probs, int64_t draft_stride, int32_t dtype,
+                                      int32_t vocab, const int32_t* draft_tokens,
+                                      const int32_t* parents, const int32_t* cu_seqlens_q,
+                                      const float* uniforms, int32_t num_seqs, int32_t total_q,
+                                      int32_t max_path, int32_t* accept_index, int32_t* accept_len,
+                                      int32_t* out_tokens, int32_t* status, void* stream) {
+  bool run;
+  const int rc = check(target_probs, target_stride, dtype, vocab, draft_tokens, parents,
+                       cu_seqlens_q, num_seqs, total_q, max_path, accept_index, accept_len,
+                       out_tokens, status, &run);
+  if (rc != MTPATTN_OK && rc != MTPATTN_E_DEVICE) return rc;
+  if (rc == MTPATTN_OK && !run) return rc;
+  if (!uniforms || !ptr_aligned(uniforms, 4) ||
+      (draft_probs && (draft_stride < vocab || !ptr_aligned(draft_probs, dtype == MTP_F32 ? 4 : 2))))
+    return MTPATTN_E_ARG;
+  if (rc != MTPATTN_OK) return rc;
+  const int device = current_device();
+  if (device < 0 || !ptr_on_device(uniforms, device) ||
+      (draft_probs && !ptr_on_device(draft_probs, device)))
+    return MTPATTN_E_DEVICE;
+  VerifyParams p{};
+  p.p = target_probs;
+  p.q = draft_probs;
+  p.p_stride = target_stride;
+  p.q_stride = draft_stride;
+  p.vocab = vocab;
+  p.tokens = draft_tokens;
+  p.parents = parents;
+  p.cu_q = cu_seqlens_q;
+  p.u = uniforms;
+  p.total_q = total_q;
+  p.max_path = max_path;
+  p.accept_index = accept_index;
+  p.accept_len = accept_len;
+  p.out_tokens = out_tokens;
+  p.status = status;
+  const int c = cluster_size(num_seqs, vocab);
+  const int chunks = (vocab + kChunk - 1) / kChunk;
+  const size_t smem = static_cast<size_t>((chunks + c - 1) / c) * sizeof(int64_t);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      dtype == MTP_F32 ? launch(verify_sample_kernel<float>, p, num_seqs, c, smem, st)
+      : dtype == MTP_BF16 ? launch(verify_sample_kernel<__nv_bfloat16>, p, num_seqs, c, smem, st)
+                          : launch(verify_sample_kernel<__half>, p, num_seqs, c, smem, st);
+  return e == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
+}
