@@ -1,23 +1,90 @@
-// Attention of draft trees over the paged cache: the plain kernel.
+// Attention of draft trees over the paged cache, on the sm_100-family tensor cores (tcgen05,
+// TMA, TMEM).
 //
-// One CTA per (node, query head); its eight warps walk the keys of the sequence, a lane holding
-// 8 of the 256 dims, each warp with its own running maximum and sum (one pass over the keys);
-// the warps' partial results are merged by their maxima at the end.
+// Work.  The query rows of a (sequence, KV head) are its nodes times the GQA ratio, row r being
+// node r / ratio, head r % ratio of the group; they are cut into tiles of 128 rows.  A unit is
+// one row tile of one (sequence, KV head); it costs ceil(seq_len / 128) key tiles.  All units'
+// key tiles form one line, which is cut into equal pieces, one per CTA (each CTA works out its
+// piece from seq_lens and cu_seqlens_q on the device, so a captured call follows its buffers).
+// A unit that lies in one piece is written out at once; a unit cut by piece borders leaves one
+// partial output and log-sum-exp per piece in the workspace, and tree_reduce_kernel joins them.
+// A CTA has at most two partial units, the first and the last of its piece: two slots per CTA.
+//
+// Roles (320 threads):
+//   warp 0     K: TMA loads of the K pages (two 128-byte-wide boxes a page, 128B-swizzled);
+//   warp 1     MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
+//   warps 2-5  V: warp w loads page w of each 64-key half tile to registers, a half tile ahead,
+//              widens it to f16 and stores it as PV's operand (no staging of the codes);
+//   warps 6-9  softmax: thread = query row = TMEM lane; also the Q operand and the epilogue.
+//
+// Precision.  K enters as its e4m3 codes, Q as the sum of two e4m3 terms of x = q 2^a (a per row,
+// max |x| in [128, 256)): hi = e4m3(x), lo = e4m3(x - hi), both products into one accumulator.  A
+// bf16 value has 8 significant bits and hi and lo keep 4 each, so x = hi + lo for every element
+// within 2^-10 of the row's largest; below that the error stays under 2^-17 of the largest.
+// P is rounded once, to f16, and V widened to f16 exactly: a second pair of e4m3 terms would be
+// as fast on the tensor cores, but its smallest step, 2^-14 of the reference weight, loses the
+// many small weights behind one large one; f16 keeps weights down to 2^-32 of it.
+//
+// Online softmax in the log2 domain with a lazy reference m: raised, and O rescaled in TMEM, only
+// when a tile's row maximum exceeds it by more than kTau, so p_s = 2^(s - m + kShift) <= 2^14.
+//
+// Masks.  A tile that reaches into the tree takes each row's word, shifted to the tile's keys, as
+// 128 bits.  Places that no row sees in full are kept out of PV by value too, since 0 * NaN is
+// NaN: V rows behind the sequence are stored as zeros, and NaN codes of tree nodes are stored as
+// 0 and put back (per row that sees them) in the epilogue.
+//
+// TMEM: S double buffer at columns 0 and 128 (a tile's P, f16 pairs, overwrites columns 0..63 of
+// its buffer), O at 256..511.  The MMA warp issues QK(u), PV(u-1), QK(u+1), ...: MMAs of one
+// thread execute in issue order, so QK(u+2) overwrites P(u) only after PV(u) has read it.
 #include "common.cuh"
 #include "host_checks.cuh"
+#include "sm100.cuh"
 
 #include "../../include/mtp_tree.h"
 
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <algorithm>
+#include <atomic>
+
 namespace mtpattn {
 namespace {
 
+using namespace sm100;
+
+constexpr int kTreeThreads = 320;
+constexpr int kRows = 128;                         // query rows per tile
+constexpr int kKeys = 128;                         // keys per tile
+constexpr int kTilePages = kKeys / kPage;          // 8
+constexpr int kHalfKeys = 64;                      // V is staged half a tile at a time
+constexpr int kVWarps = 4;
+constexpr int kWarpV = 2, kWarpSoft = kWarpV + kVWarps;
+constexpr int kQHalf = kRows * 128;                // 128 of the 256 dims of one Q term
+constexpr int kQTerm = 2 * kQHalf;                 // 32 KB: hi, then lo
+constexpr int kKHalf = kKeys * 128;
+constexpr int kKTile = 2 * kKHalf;                 // 32 KB per stage
+constexpr int kKStages = 2;
+constexpr int kVAtom = kHalfKeys * 128;            // 64 dims of 64 keys, f16
+constexpr int kVStage = 4 * kVAtom;                // 32 KB per stage
+constexpr int kVStages = 2;
+constexpr int kStagePitch = 36;                    // floats a row of the output staging
+constexpr int kOffQ = 0;
+constexpr int kOffK = kOffQ + 2 * kQTerm;
+constexpr int kOffV = kOffK + kKStages * kKTile;
+constexpr int kOffOut = kOffV + kVStages * kVStage;
+constexpr int kOffBar = kOffOut + 4 * 32 * kStagePitch * 4;
+constexpr int kSmemTree = kOffBar + 512 + 1024;    // + alignment slack
+static_assert(kSmemTree <= 232448, "shared-memory layout");
+constexpr int kSCols = 128, kOCol = 256, kTmemCols = 512;
+constexpr float kTau = 6.f, kShift = 8.f;
+constexpr uint32_t kBadLse = 0x7fd0bad1u;          // a partial of a sequence with a bad page (a NaN
+                                                   // that no arithmetic makes)
+
 struct TreeAttnParams {
+  CUtensorMap tmap_k;
   const __nv_bfloat16* q;
   int64_t q_stride_tok, q_stride_head;
-  const uint8_t* k_cache;
   const uint8_t* v_cache;
   int64_t num_pages;
   const int32_t* block_tables;
@@ -32,92 +99,917 @@ struct TreeAttnParams {
   __nv_bfloat16* out;
   int64_t out_stride_tok, out_stride_head;
   int32_t* status;
+  int32_t ctas;              // pieces of the line
+  float* o_part;             // [ctas][2][128][256]
+  float* lse_part;           // [ctas][2][128]
 };
 
-constexpr int kWarps = 8;
+struct TreeBars {
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t q_ready, o_free, final_mma;
+  uint32_t tmem_base;
+  int32_t abort;
+  int32_t bad[4];            // [segment & 3]: segment + 1 if it met a page outside the pool
+  int32_t nan[4];            // the same if a tree node's V holds a NaN code
+};
+static_assert(sizeof(TreeBars) <= 512, "barrier block");
 
-__device__ __forceinline__ float e4m3_f32(uint8_t c) {
-  __nv_fp8_e4m3 x;
-  x.__x = c;
-  return static_cast<float>(x);
+// ---- the line of key tiles ---------------------------------------------------------------------
+
+// One sequence on the line: T row tiles of nt key tiles for each KV head.  Rows whose place is not
+// known (cu_seqlens_q out of order) take no part; other errors cost one key tile a unit.
+struct Seq {
+  int q0, n, L, T, nt, w, err;
+};
+
+__device__ __forceinline__ Seq seq_of(const TreeAttnParams& p, int q0, int q1, int L) {
+  Seq s;
+  s.q0 = q0;
+  s.n = q1 - q0;
+  s.L = L;
+  s.err = 0;
+  if (q0 < 0 || q1 <= q0 || q1 > p.total_q) {
+    s.err = MTPATTN_ERR_QLEN;
+    s.n = s.T = s.nt = s.w = 0;
+    return s;
+  }
+  if (s.n > MTP_TREE_MAX_NODES) s.err = MTPATTN_ERR_QLEN;
+  else if (s.n > L) s.err = MTPATTN_ERR_QLEN_GT_SEQ;
+  else if (L > p.max_pages * kPage) s.err = MTPATTN_ERR_SEQ_TOO_LONG;
+  s.T = (s.n * p.ratio + kRows - 1) / kRows;
+  s.nt = s.err ? 1 : (L + kKeys - 1) / kKeys;
+  s.w = s.T * s.nt * p.hkv;
+  return s;
 }
 
-__global__ void __launch_bounds__(kWarps * 32)
-tree_attn_plain_kernel(const TreeAttnParams p) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][kHeadDim];
-  __shared__ int s_bad;
-  const int b = blockIdx.x / MTP_TREE_MAX_NODES, i = blockIdx.x % MTP_TREE_MAX_NODES;
-  const int head = blockIdx.y, h = head / p.ratio;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-  if (q0 < 0 || q1 <= q0 || q1 > p.total_q) {
-    if (i == 0 && head == 0 && threadIdx.x == 0) set_status(p.status, MTPATTN_ERR_QLEN);
-    return;
+// Lane l's sequence b0 + l; past the last one of no weight.
+__device__ __forceinline__ Seq seq_at(const TreeAttnParams& p, int b) {
+  if (b < p.num_seqs) return seq_of(p, p.cu_q[b], p.cu_q[b + 1], p.seq_lens[b]);
+  Seq s;
+  s.q0 = s.n = s.L = s.T = s.nt = s.w = s.err = 0;
+  return s;
+}
+
+__device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  const int n = q1 - q0, L = p.seq_lens[b];
-  int err = 0;
-  if (n > MTP_TREE_MAX_NODES) err = MTPATTN_ERR_QLEN;
-  else if (n > L) err = MTPATTN_ERR_QLEN_GT_SEQ;
-  else if ((L + kPage - 1) / kPage > p.max_pages) err = MTPATTN_ERR_SEQ_TOO_LONG;
-  if (threadIdx.x == 0) s_bad = err;
+  return x;
+}
+
+__device__ __forceinline__ int line_length(const TreeAttnParams& p, int lane) {
+  int w = 0;
+  for (int b0 = 0; b0 < p.num_seqs; b0 += 32) w += seq_at(p, b0 + lane).w;
+  return __reduce_add_sync(0xffffffffu, w);
+}
+
+// The line of W is cut into min(CTAs, W) pieces, so none is empty.  First place of piece g:
+__device__ __forceinline__ int piece_start(int g, int pieces, int W) {
+  return static_cast<int>(static_cast<int64_t>(g) * W / pieces);
+}
+
+struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
+  int b, h, m, q0, n, L, err;
+  int t0, t1, nt, T;
+  bool first;                // it starts the CTA's piece
+};
+
+// A warp's walk over the units of its CTA's piece; 32 sequences are held, one a lane.
+struct Walker {
+  int pos, hi, lo;
+  int b0, before;            // the held sequences, and the line before the first of them
+  Seq mine;
+  int upto;                  // running sum of the held sequences' weights
+
+  __device__ __forceinline__ void hold(const TreeAttnParams& p, int lane) {
+    mine = seq_at(p, b0 + lane);
+    upto = warp_scan(mine.w, lane);
+  }
+  __device__ __forceinline__ void start(const TreeAttnParams& p, int lane) {
+    const int W = line_length(p, lane);
+    const int pieces = min(p.ctas, W);
+    const int g = blockIdx.x;
+    lo = pos = g < pieces ? piece_start(g, pieces, W) : W;
+    hi = g < pieces ? piece_start(g + 1, pieces, W) : W;
+    b0 = before = 0;
+    hold(p, lane);
+  }
+  __device__ __forceinline__ bool next(const TreeAttnParams& p, int lane, Segment& s) {
+    if (pos >= hi) return false;
+    while (true) {
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+      if (pos < before + all) break;
+      before += all;
+      b0 += 32;
+      if (b0 >= p.num_seqs) return false;           // lengths changed under the call
+      hold(p, lane);
+    }
+    const int at = pos - before;
+    const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+    const int nt = __shfl_sync(0xffffffffu, mine.nt, f), T = __shfl_sync(0xffffffffu, mine.T, f);
+    const int in = at - __shfl_sync(0xffffffffu, upto - mine.w, f);
+    s.b = b0 + f;
+    s.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
+    s.n = __shfl_sync(0xffffffffu, mine.n, f);
+    s.L = __shfl_sync(0xffffffffu, mine.L, f);
+    s.err = __shfl_sync(0xffffffffu, mine.err, f);
+    const int unit = in / nt;
+    s.h = unit / T;
+    s.m = unit - s.h * T;
+    s.nt = nt;
+    s.T = T;
+    s.t0 = in - unit * nt;
+    s.t1 = min(nt, s.t0 + hi - pos);
+    s.first = pos == lo;
+    pos += s.t1 - s.t0;
+    return true;
+  }
+  // the next segment that has keys to be looked at
+  __device__ __forceinline__ bool next_running(const TreeAttnParams& p, int lane, Segment& s) {
+    while (next(p, lane, s))
+      if (!s.err) return true;
+    return false;
+  }
+};
+
+__device__ __forceinline__ int tile_pages(const Segment& s, int t) {   // pages of key tile t
+  return min(kTilePages, (s.L + kPage - 1) / kPage - t * kTilePages);
+}
+
+// ---- arithmetic --------------------------------------------------------------------------------
+
+__device__ __forceinline__ float exp2_hw(float x) {   // 2^x, hardware approximation
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// (a0, a1) = (a0, a1) * b + c, one instruction for the pair
+__device__ __forceinline__ void fma_pair(float& a0, float& a1, float b, float c) {
+  asm("{\n .reg .b64 ra, rb, rc;\n mov.b64 ra, {%0, %1};\n mov.b64 rb, {%2, %2};\n"
+      " mov.b64 rc, {%3, %3};\n fma.rn.f32x2 ra, ra, rb, rc;\n mov.b64 {%0, %1}, ra;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add_pair(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 ra, rb;\n mov.b64 ra, {%0, %1};\n mov.b64 rb, {%2, %3};\n"
+      " add.rn.f32x2 ra, ra, rb;\n mov.b64 {%0, %1}, ra;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+// two f32 -> f16x2 (a in the low half: the lower K index of a TMEM A-operand cell)
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+// four e4m3 codes (lowest byte first) -> two f16x2 words, exactly
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+// x0..x3 = hi + lo with e4m3 codes (lowest byte first); the remainder is formed in f16, exactly.
+__device__ __forceinline__ void two_terms(float x0, float x1, float x2, float x3, uint32_t& hi,
+                                          uint32_t& lo) {
+  asm("{\n"
+      " .reg .b16 h01, h23, l01, l23;\n"
+      " .reg .b32 x01, x23, g01, g23;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 h01, %3, %2;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 h23, %5, %4;\n"
+      " cvt.rn.f16x2.f32 x01, %3, %2;\n"
+      " cvt.rn.f16x2.f32 x23, %5, %4;\n"
+      " cvt.rn.f16x2.e4m3x2 g01, h01;\n"
+      " cvt.rn.f16x2.e4m3x2 g23, h23;\n"
+      " sub.rn.f16x2 x01, x01, g01;\n"
+      " sub.rn.f16x2 x23, x23, g23;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l01, x01;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l23, x23;\n"
+      " mov.b32 %0, {h01, h23};\n"
+      " mov.b32 %1, {l01, l23};\n"
+      "}\n"
+      : "=r"(hi), "=r"(lo)
+      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+}
+// 0xff in every byte of w that is a NaN code
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// tcgen05.mma kind::f16 (f16 x f16 -> f32), A from tensor memory, B from shared memory.
+__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__global__ void __launch_bounds__(kTreeThreads, 1)
+tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  TreeBars& bars = *reinterpret_cast<TreeBars*>(base + kOffBar);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &bars.abort;
+
+  // ---- set-up ------------------------------------------------------------------------------
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(smem_u32(&bars.k_full[i]), 1);
+      mbar_init(smem_u32(&bars.k_empty[i]), 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(smem_u32(&bars.v_full[i]), kVWarps);
+      mbar_init(smem_u32(&bars.v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.s_full[i]), 1);
+      mbar_init(smem_u32(&bars.p_full[i]), kRows);
+      mbar_init(smem_u32(&bars.pv_done[i]), 1);
+    }
+    mbar_init(smem_u32(&bars.q_ready), kRows);
+    mbar_init(smem_u32(&bars.o_free), kRows);
+    mbar_init(smem_u32(&bars.final_mma), 1);
+    for (int i = 0; i < 4; ++i) bars.bad[i] = bars.nan[i] = 0;
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
   __syncthreads();
-  const int32_t* bt = p.block_tables + static_cast<int64_t>(b) * p.max_pages;
-  const int pages = err ? 0 : (L + kPage - 1) / kPage;
-  for (int j = threadIdx.x; j < pages; j += kWarps * 32)
-    if (bt[j] < 0 || bt[j] >= p.num_pages) atomicOr(&s_bad, MTPATTN_ERR_PAGE);
-  __syncthreads();
-  if (s_bad && i == 0 && head == 0 && threadIdx.x == 0) set_status(p.status, s_bad);
-  // rows past the sequence's 64th node (too many nodes: an error) are zeroed by the slot mod 64
-  for (int t = i; t < n; t += MTP_TREE_MAX_NODES) {
-    __nv_bfloat16* orow = p.out + (int64_t)(q0 + t) * p.out_stride_tok + head * p.out_stride_head;
-    if (s_bad) {
-      if (threadIdx.x < kHeadDim) orow[threadIdx.x] = __float2bfloat16(0.f);
-      continue;
-    }
-    const __nv_bfloat16* qrow = p.q + (int64_t)(q0 + t) * p.q_stride_tok + head * p.q_stride_head;
-    float qv[8], o[8];
-    const float sc = p.scale_log2 * __ldg(p.k_descale);
-    for (int d = 0; d < 8; ++d) {
-      qv[d] = __bfloat162float(qrow[8 * lane + d]);
-      o[d] = 0.f;
-    }
-    const uint64_t see = p.mask[q0 + t];
-    float m = -INFINITY, l = 0.f;
-    for (int j = warp; j < L; j += kWarps) {
-      const int node = j - (L - n);
-      if (node >= 0 && !((see >> node) & 1)) continue;
-      const int64_t off = ((static_cast<int64_t>(bt[j / kPage]) * kPage + j % kPage) * p.hkv + h) * kHeadDim + 8 * lane;
-      const uint2 kw = *reinterpret_cast<const uint2*>(p.k_cache + off);
-      const uint2 vw = *reinterpret_cast<const uint2*>(p.v_cache + off);
-      float s = 0.f;
-      for (int d = 0; d < 8; ++d) s += qv[d] * e4m3_f32((d < 4 ? kw.x : kw.y) >> (8 * (d & 3)) & 0xff);
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= sc;
-      const float mn = s != s ? s : fmaxf(m, s);
-      const float a = m == mn ? 1.f : exp2f(m - mn), e = s == mn ? 1.f : exp2f(s - mn);
-      l = l * a + e;
-      for (int d = 0; d < 8; ++d) o[d] = o[d] * a + e * e4m3_f32((d < 4 ? vw.x : vw.y) >> (8 * (d & 3)) & 0xff);
-      m = mn;
-    }
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
-    }
-    for (int d = 0; d < 8; ++d) s_o[warp][8 * lane + d] = o[d];
-    __syncthreads();
-    if (threadIdx.x < kHeadDim) {
-      float M = -INFINITY, lt = 0.f, ot = 0.f;
-      for (int w = 0; w < kWarps; ++w) M = s_m[w] != s_m[w] ? s_m[w] : fmaxf(M, s_m[w]);
-      for (int w = 0; w < kWarps; ++w)
-        if (s_l[w] != 0.f) {
-          const float e = exp2f(s_m[w] - M);
-          lt += s_l[w] * e;
-          ot += s_o[w][threadIdx.x] * e;
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  // A programmatic dependent of the previous work on the stream: nothing global was touched so
+  // far; and the reduce may be scheduled (it waits for this grid before it reads partials).
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+  Walker walk;
+  Segment s;
+  walk.start(p, lane);
+
+  if (warp == 0) {
+    // ======================================== K producer ==========================================
+    if (lane == 0) prefetch_tmap(&p.tmap_k);
+    if (blockIdx.x == 0)                            // sequences whose rows are not known
+      for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+        const Seq x = seq_at(p, b0 + lane);
+        if (x.err && x.T == 0) set_status(p.status, x.err);
+      }
+    // keys that other row tiles will read again stay in L2
+    const uint64_t once = l2_policy_evict_first();
+    uint64_t again;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
+    uint32_t u = 0;
+    bool stop = false;
+    while (!stop && walk.next_running(p, lane, s)) {
+      const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
+      const uint64_t pol = s.T == 1 ? once : again;
+      for (int t = s.t0; t < s.t1; ++t, ++u) {
+        const int np = tile_pages(s, t), st = u % kKStages;
+        const int phys = lane < np ? bt[t * kTilePages + lane] : 0;
+        bool ok = true;
+        const uint32_t fb = smem_u32(&bars.k_full[st]);
+        if (lane == 0) {
+          ok = mbar_wait(smem_u32(&bars.k_empty[st]), ((u / kKStages) & 1) ^ 1, abort_flag);
+          if (ok) mbar_arrive_expect_tx(fb, np * 2 * 2048);
         }
-      orow[threadIdx.x] = __float2bfloat16(lt == 0.f ? 0.f : ot / lt * __ldg(p.v_descale));
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          stop = true;
+          break;
+        }
+        if (lane < np) {                            // a page outside the pool reads as zeros
+          const uint32_t dst = smem_u32(base + kOffK + st * kKTile) + lane * 2048;
+          tma_load_4d(dst, &p.tmap_k, fb, 0, s.h, 0, phys, pol);
+          tma_load_4d(dst + kKHalf, &p.tmap_k, fb, 128, s.h, 0, phys, pol);
+        }
+      }
     }
-    __syncthreads();
+    // never leave with copies in flight
+    if (lane == 0) {
+      volatile int no_abort = 0;
+      for (uint32_t k = 1; k <= kKStages && k <= u; ++k)
+        mbar_wait(smem_u32(&bars.k_full[(u - k) % kKStages]), ((u - k) / kKStages) & 1, &no_abort);
+    }
+  } else if (warp == 1) {
+    // ======================================== MMA issuer ==========================================
+    constexpr uint32_t kIdescQK = idesc_e4m3_f32(kRows, kKeys, false);
+    constexpr uint32_t kIdescPV = idesc_e4m3_f32(kRows, kHeadDim, true);   // f16: format code 0
+    const uint64_t q_desc = sdesc_sw128(smem_u32(base + kOffQ), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(base + kOffK), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(base + kOffV), kVAtom, 1024);
+    const bool leader = elect_one();
+    auto wait_all = [&](uint64_t& bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abort_flag));
+    };
+    uint32_t u = 0, v = 0;                          // key tiles, half tiles of V
+    auto issue_pv = [&](uint32_t ut, int np, bool first) -> bool {
+      if (!wait_all(bars.p_full[ut & 1], (ut >> 1) & 1)) return false;
+      for (int k0 = 0; k0 < np; k0 += 4, ++v) {     // a half tile: four pages, 16 keys each
+        const int st = v % kVStages;
+        if (!wait_all(bars.v_full[st], (v / kVStages) & 1)) return false;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t p_tmem = tmem + (ut & 1) * kSCols + 8 * k0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k0 + k < np)
+              mma_pv(tmem + kOCol, p_tmem + 8 * k, v_desc + ((st * kVStage + k * 2048) >> 4), kIdescPV,
+                     (first && k0 + k == 0) ? 0u : 1u);
+          mma_commit(smem_u32(&bars.v_empty[st]));
+        }
+        __syncwarp();
+      }
+      if (leader) mma_commit(smem_u32(&bars.pv_done[ut & 1]));
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    uint32_t seg = 0;
+    while (ok && walk.next_running(p, lane, s)) {
+      ok = wait_all(bars.q_ready, seg & 1);
+      for (int t = s.t0; ok && t < s.t1; ++t, ++u) {
+        const int st = u % kKStages;
+        if (!wait_all(bars.k_full[st], (u / kKStages) & 1)) { ok = false; break; }
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {            // hi: dims 32 k .. + 31, then lo
+            const uint32_t a_off = (k >> 3) * kQTerm + ((k >> 2) & 1) * kQHalf + (k & 3) * 32;
+            const uint32_t b_off = st * kKTile + ((k >> 2) & 1) * kKHalf + (k & 3) * 32;
+            mma_f8_ss(tmem + (u & 1) * kSCols, q_desc + (a_off >> 4), k_desc + (b_off >> 4), kIdescQK,
+                      k > 0 ? 1u : 0u);
+          }
+          mma_commit(smem_u32(&bars.s_full[u & 1]));
+          mma_commit(smem_u32(&bars.k_empty[st]));
+        }
+        __syncwarp();
+        if (t > s.t0) {
+          // the segment's first product overwrites O: the epilogue before it has read it
+          if (t == s.t0 + 1 && seg > 0 && !wait_all(bars.o_free, (seg - 1) & 1)) { ok = false; break; }
+          ok = issue_pv(u - 1, tile_pages(s, t - 1), t == s.t0 + 1);
+        }
+      }
+      if (!ok) break;
+      if (s.t1 == s.t0 + 1 && seg > 0 && !wait_all(bars.o_free, (seg - 1) & 1)) break;
+      if (!issue_pv(u - 1, tile_pages(s, s.t1 - 1), s.t1 == s.t0 + 1)) break;
+      ++seg;
+    }
+    if (leader) mma_commit(smem_u32(&bars.final_mma));
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait(smem_u32(&bars.final_mma), 0, &no_abort);
+  } else if (warp < kWarpSoft) {
+    // ========================================= V loads ============================================
+    // A half tile is 16 bytes x 8 a lane: load i holds key 2 i + lane / 16 of the warp's page,
+    // dims 16 (lane % 16) .. + 15, two 16-byte chunks of f16 in 64-dim atom (lane % 16) / 4.
+    const int w = warp - kWarpV;
+    const int c16 = lane & 15, krow = lane >> 4;
+    const int atom = c16 >> 2, ch = 2 * (c16 & 3);
+    // lanes of odd atoms store their second chunk first: the eight lanes of a store phase then
+    // cover all eight chunk positions
+    const int swap = atom & 1;
+    struct Half {
+      uint4 x[8];
+      bool pages;            // the warp has a page in this half tile
+      bool bad;              // ... outside the pool
+      int tree;              // first key of the page that belongs to the tree (16: none)
+    };
+    bool more = walk.next_running(p, lane, s);
+    int hf = more ? 2 * s.t0 : 0, hf_end = 0;       // half tiles of the segment (4 pages each)
+    int seg = 0;
+    auto seg_end = [&]() { return min(2 * s.t1, ((s.L + kPage - 1) / kPage + 3) / 4); };
+    if (more) hf_end = seg_end();
+    int ent = 0, ent_at = -32;                      // lane l: the table entry of half tile ent_at + l
+    auto load = [&](Half& a) {                      // the next half tile; advances
+      if (hf >= ent_at + 32 || hf < ent_at) {
+        ent_at = hf;
+        const int pg = 4 * (hf + lane) + w;
+        ent = pg < (s.L + kPage - 1) / kPage
+                  ? p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + pg] : 0;
+      }
+      const int page = __shfl_sync(0xffffffffu, ent, hf - ent_at);
+      const int pg = 4 * hf + w;
+      const int left = s.L - pg * kPage;            // keys of the page that belong to the sequence
+      a.pages = left > 0;
+      a.tree = min(16, max(0, s.L - s.n - pg * kPage));
+      const bool good = page >= 0 && page < p.num_pages;
+      a.bad = a.pages && !good;
+      const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + krow) * p.hkv + s.h) * kHeadDim + 16 * c16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a.x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (good && 2 * i + krow < left) {
+          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                       : "=r"(a.x[i].x), "=r"(a.x[i].y), "=r"(a.x[i].z), "=r"(a.x[i].w)
+                       : "l"(src + static_cast<int64_t>(2 * i) * p.hkv * kHeadDim));
+        }
+      }
+    };
+    uint32_t v = 0;
+    auto store = [&](Half& a, int sg) -> bool {
+      const int st = v % kVStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.v_empty[st]), ((v / kVStages) & 1) ^ 1, abort_flag)))
+        return false;
+      // Notes are made behind the wait: a slot of the four is then not one that the epilogue has
+      // yet to read (this warp is two half tiles ahead of it at most).
+      if (a.bad && lane == 0) bars.bad[sg & 3] = sg + 1;
+      if (a.pages) {
+        if (a.tree < 16) {                          // NaN codes of tree nodes: 0, and noted
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (2 * i + krow < a.tree) continue;
+            uint32_t* x = reinterpret_cast<uint32_t*>(&a.x[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t bytes = nan_bytes(x[e]);
+              any |= bytes != 0;
+              x[e] &= ~bytes;
+            }
+          }
+          if (any) bars.nan[sg & 3] = sg + 1;
+        }
+        unsigned char* dst = base + kOffV + st * kVStage + atom * kVAtom + w * 16 * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = 2 * i + krow;
+          uint4 c0, c1;
+          widen(a.x[i].x, c0.x, c0.y);
+          widen(a.x[i].y, c0.z, c0.w);
+          widen(a.x[i].z, c1.x, c1.y);
+          widen(a.x[i].w, c1.z, c1.w);
+          const int o0 = key * 128 + ((ch ^ (key & 7)) << 4), o1 = key * 128 + (((ch + 1) ^ (key & 7)) << 4);
+          *reinterpret_cast<uint4*>(dst + (swap ? o1 : o0)) = swap ? c1 : c0;
+          *reinterpret_cast<uint4*>(dst + (swap ? o0 : o1)) = swap ? c0 : c1;
+        }
+        fence_proxy_async_smem();                   // visible to the tensor cores behind v_full
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.v_full[st]));
+      ++v;
+      return true;
+    };
+    auto advance = [&]() {
+      if (++hf >= hf_end) {
+        more = walk.next_running(p, lane, s);
+        if (more) {
+          hf = 2 * s.t0;
+          hf_end = seg_end();
+          ent_at = -32;
+          ++seg;
+        }
+      }
+    };
+    Half cur, nxt;
+    bool have = more;
+    int cur_seg = 0;
+    if (have) {
+      load(cur);
+      cur_seg = seg;
+      advance();
+    }
+    while (have) {
+      const bool have_next = more;
+      int next_seg = 0;
+      if (have_next) {
+        load(nxt);
+        next_seg = seg;
+        advance();
+      }
+      if (!store(cur, cur_seg)) break;
+      cur = nxt;
+      cur_seg = next_seg;
+      have = have_next;
+    }
+  } else {
+    // ======================================= softmax (rows) =======================================
+    const int quad = warp & 3;                      // TMEM lane quarter
+    const int r = 32 * quad + lane;                 // query row of the tile, TMEM lane
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    float* stage = reinterpret_cast<float*>(base + kOffOut) + quad * 32 * kStagePitch;
+    const float sl = p.scale_log2 * __ldg(p.k_descale);
+    const float vd = __ldg(p.v_descale);
+    uint32_t u = 0;                                 // key tiles so far
+    int seg = 0;
+
+    // Zeros for the rows of a sequence that cannot be computed.
+    auto put_zeros = [&](const Segment& y) {
+      const int rr = y.m * kRows + r;
+      if (rr < y.n * p.ratio) {
+        const int t = rr / p.ratio, g = rr - t * p.ratio;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(y.q0 + t) * p.out_stride_tok +
+                                              static_cast<int64_t>(y.h * p.ratio + g) * p.out_stride_head);
+#pragma unroll 1
+        for (int i = 0; i < kHeadDim / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto next_running = [&](Segment& y) -> bool {
+      while (walk.next(p, lane, y)) {
+        if (!y.err) return true;
+        put_zeros(y);
+        if (lane == 0 && quad == 0) set_status(p.status, y.err);
+      }
+      return false;
+    };
+    // The rows of this warp as two e4m3 terms into the Q operand; lane l returns row l's factor
+    // from raw products to log2 units (NaN for a row that is not finite).
+    auto prepare_q = [&](const Segment& y) -> float {
+      float mine = 0.f;
+      const int rows = y.n * p.ratio - y.m * kRows - 32 * quad;      // valid rows of this warp
+      if (rows > 0) {
+        const int half = lane >> 4, chunk = (lane & 15) >> 1;
+        unsigned char* q_hi = base + kOffQ + half * kQHalf + 8 * (lane & 1);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 8) {
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (i0 + i < rows) {
+              const int rr = y.m * kRows + 32 * quad + i0 + i;
+              const int t = rr / p.ratio, g = rr - t * p.ratio;
+              x[i] = __ldg(reinterpret_cast<const uint4*>(
+                  p.q + static_cast<int64_t>(y.q0 + t) * p.q_stride_tok +
+                  static_cast<int64_t>(y.h * p.ratio + g) * p.q_stride_head + 8 * lane));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t top = 0;                        // the largest |q| by its bits (NaN above all)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top = max(top, max((ww[e] << 16) & 0x7fff0000u, ww[e] & 0x7fff0000u));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int e8 = static_cast<int>(top >> 23);              // exponent field
+            // 2^a takes the largest into [128, 256); a row of zeros or subnormals keeps a = 126
+            const int a = top == 0u ? 0 : min(126, 134 - e8);
+            const float f = __int_as_float((a + 127) << 23);
+            uint32_t hi[2], lo[2];
+            two_terms(__uint_as_float(ww[0] << 16) * f, __uint_as_float(ww[0] & 0xffff0000u) * f,
+                      __uint_as_float(ww[1] << 16) * f, __uint_as_float(ww[1] & 0xffff0000u) * f, hi[0], lo[0]);
+            two_terms(__uint_as_float(ww[2] << 16) * f, __uint_as_float(ww[2] & 0xffff0000u) * f,
+                      __uint_as_float(ww[3] << 16) * f, __uint_as_float(ww[3] & 0xffff0000u) * f, hi[1], lo[1]);
+            const int row = 32 * quad + i0 + i;
+            unsigned char* dst = q_hi + row * 128 + ((chunk ^ (row & 7)) << 4);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
+            const float back = e8 == 255 ? __int_as_float(0x7fc00000)
+                                         : sl * __int_as_float((127 - a) << 23);
+            if (lane == i0 + i) mine = back;
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      mbar_arrive(smem_u32(&bars.q_ready));
+      return mine;
+    };
+
+    bool have = next_running(s), alive = true;
+    float sl2 = have ? prepare_q(s) : 0.f;
+    while (have) {
+      const int rr = s.m * kRows + r;
+      const bool valid = rr < s.n * p.ratio;
+      const bool active = __any_sync(0xffffffffu, valid);
+      uint64_t word = 0;
+      if (valid) word = p.mask[s.q0 + rr / p.ratio];
+      if (s.n < 64) word &= (1ull << s.n) - 1ull;
+      const int tree0 = s.L - s.n;                  // first key of the tree
+      float m = -INFINITY, l = 0.f;
+      for (int t = s.t0; t < s.t1; ++t, ++u) {
+        const uint32_t sb = u & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.s_full[sb]), (u >> 1) & 1, abort_flag))) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        // Every phase of pv_done is waited for in its turn, as parities demand; this one is long
+        // complete, its products having been issued before the QK that s_full stands for.
+        if (t > s.t0 + 1 &&
+            !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.pv_done[u & 1]), ((u - 2) >> 1) & 1, abort_flag))) {
+          alive = false;
+          break;
+        }
+        if (active) {
+          const uint32_t s_addr = lane_addr + sb * kSCols;
+          float x[kKeys];
+          {
+            uint32_t v0[32], v1[32], v2[32], v3[32];
+            tmem_ld32(s_addr, v0);
+            tmem_ld32(s_addr + 32, v1);
+            tmem_ld32(s_addr + 64, v2);
+            tmem_ld32(s_addr + 96, v3);
+            tmem_ld_wait(v0);
+            tmem_ld_wait(v1);
+            tmem_ld_wait(v2);
+            tmem_ld_wait(v3);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              x[e] = __uint_as_float(v0[e]);
+              x[32 + e] = __uint_as_float(v1[e]);
+              x[64 + e] = __uint_as_float(v2[e]);
+              x[96 + e] = __uint_as_float(v3[e]);
+            }
+          }
+          // the keys of the tile that this row sees, 32 a word
+          const int off = t * kKeys - tree0;
+          const bool masked = off + kKeys > 0;
+          auto seen = [&](int c) -> uint32_t {
+            const int st = off + 32 * c;
+            if (st <= -32) return 0xffffffffu;
+            if (st < 0) return (static_cast<uint32_t>(word) << -st) | ((1u << -st) - 1u);
+            return st < 64 ? static_cast<uint32_t>(word >> st) : 0u;
+          };
+          const float sgn = sl2 < 0.f ? -1.f : 1.f;  // the largest scaled logit: the row's factor
+          if (masked) {                              // may be negative
+            const float none = -INFINITY * sgn;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t bits = seen(c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) x[32 * c + e] = none;
+            }
+          }
+          float top;
+          if (__all_sync(0xffffffffu, !(sl2 < 0.f))) {
+            float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+#pragma unroll
+            for (int e = 4; e < kKeys; e += 4) {
+              a = max3(a, x[e], x[e + 1]);
+              b = max3(b, x[e + 2], x[e + 3]);
+            }
+            top = fmaxf(a, b) * sl2;
+          } else {
+            float a = x[0] * sgn;
+#pragma unroll
+            for (int e = 1; e < kKeys; ++e) a = fmaxf(a, x[e] * sgn);
+            top = a * sgn * sl2;
+          }
+          if (top != top) top = -INFINITY;           // nothing seen with a factor of 0, or all NaN
+          float alpha = 1.f;
+          bool rescale = false;
+          if (top != -INFINITY && (m == -INFINITY || top > m + kTau)) {
+            if (m != -INFINITY) {
+              alpha = exp2_hw(m - top);
+              rescale = true;
+            }
+            m = top;
+          }
+          if (t > s.t0 && __any_sync(0xffffffffu, rescale)) {
+            // O may be touched once the previous tile's products are in it
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.pv_done[(u - 1) & 1]), ((u - 1) >> 1) & 1, abort_flag))) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kHeadDim / 16; ++c) {  // 16 columns at a time: the logits are live
+              uint32_t o[16];
+              asm volatile(
+                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+                  "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n"
+                  : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                    "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+                    "=r"(o[14]), "=r"(o[15])
+                  : "r"(lane_addr + kOCol + 16 * c)
+                  : "memory");
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(lane_addr + kOCol + 16 * c, o);
+            }
+          }
+          const float moff = m == -INFINITY ? 0.f : kShift - m;
+          float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int e = 32 * c; e < 32 * c + 32; e += 2) fma_pair(x[e], x[e + 1], sl2, moff);
+            if (masked) {
+              const uint32_t bits = seen(c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) x[32 * c + e] = -INFINITY;
+            }
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 32 * c; e < 32 * c + 32; e += 4) {
+              x[e] = exp2_hw(x[e]);
+              x[e + 1] = exp2_hw(x[e + 1]);
+              x[e + 2] = exp2_hw(x[e + 2]);
+              x[e + 3] = exp2_hw(x[e + 3]);
+              add_pair(a0, a1, x[e], x[e + 1]);
+              add_pair(b0, b1, x[e + 2], x[e + 3]);
+              pw[(e - 32 * c) / 2] = half2_of(x[e], x[e + 1]);
+              pw[(e - 32 * c) / 2 + 1] = half2_of(x[e + 2], x[e + 3]);
+            }
+            tmem_st16(s_addr + 16 * c, pw);
+          }
+          l = l * alpha + ((a0 + b0) + (a1 + b1));
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bars.p_full[sb]));
+      }
+      if (!alive) break;
+      // All QK of the segment are complete: Q may be written for the next one while the last
+      // products run.
+      Segment y = s;
+      const uint32_t last = u - 1;
+      have = next_running(y);
+      const float sl2_next = have ? prepare_q(y) : 0.f;
+      // ---- epilogue: o = v_descale O / l, lse = m + log2 l ---------------------------------------
+      if (!__all_sync(0xffffffffu,
+                      (s.t1 == s.t0 + 1 ||
+                       mbar_wait(smem_u32(&bars.pv_done[(last - 1) & 1]), ((last - 1) >> 1) & 1, abort_flag)) &&
+                          mbar_wait(smem_u32(&bars.pv_done[last & 1]), (last >> 1) & 1, abort_flag)))
+        break;
+      tc_fence_after();
+      const bool bad = *reinterpret_cast<volatile int*>(&bars.bad[seg & 3]) == seg + 1;
+      const bool nan_v = *reinterpret_cast<volatile int*>(&bars.nan[seg & 3]) == seg + 1;
+      if (bad && lane == 0) set_status(p.status, MTPATTN_ERR_PAGE);
+      const bool whole = s.t0 == 0 && s.t1 == s.nt;
+      if (active) {
+        const float sc = l != 0.f ? vd / l : 0.f;    // NaN stays NaN
+        const int slot = 2 * blockIdx.x + (s.first ? 0 : 1);
+        const int rows = min(32, s.n * p.ratio - s.m * kRows - 32 * quad);
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lane_addr + kOCol + 32 * c, o);
+          tmem_ld_wait(o);
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] = l == 0.f || bad ? 0.f : __uint_as_float(o[e]) * sc;
+          if (nan_v && !bad && valid) {
+            // NaN values of the nodes that this row sees, dims 32 c .. + 31
+            for (uint64_t w = word; w; w &= w - 1) {
+              const int key = tree0 + __ffsll(static_cast<long long>(w)) - 1;
+              if (key < s.t0 * kKeys || key >= s.t1 * kKeys) continue;
+              const int page = p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + key / kPage];
+              const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim + 32 * c;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((src[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fc00000);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(stage + lane * kStagePitch + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          __syncwarp();
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * i + (lane >> 2), d = 8 * (lane & 3);
+              if (row < rows) {
+                const float* src = stage + row * kStagePitch + d;
+                const float4 fa = *reinterpret_cast<const float4*>(src);
+                const float4 fb = *reinterpret_cast<const float4*>(src + 4);
+                const __nv_bfloat162 h0 = __floats2bfloat162_rn(fa.x, fa.y), h1 = __floats2bfloat162_rn(fa.z, fa.w);
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(fb.x, fb.y), h3 = __floats2bfloat162_rn(fb.z, fb.w);
+                const int ri = s.m * kRows + 32 * quad + row;
+                const int tt = ri / p.ratio, gg = ri - tt * p.ratio;
+                *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.q0 + tt) * p.out_stride_tok +
+                                          static_cast<int64_t>(s.h * p.ratio + gg) * p.out_stride_head + 32 * c + d) =
+                    make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                               *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
+              }
+            }
+          } else {
+            float* dst = p.o_part + (static_cast<int64_t>(slot) * kRows + 32 * quad) * kHeadDim + 32 * c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = 4 * i + (lane >> 3), d = 4 * (lane & 7);
+              if (row < rows)
+                *reinterpret_cast<float4*>(dst + static_cast<int64_t>(row) * kHeadDim + d) =
+                    *reinterpret_cast<const float4*>(stage + row * kStagePitch + d);
+            }
+          }
+        }
+        if (!whole && valid)
+          p.lse_part[slot * kRows + r] = bad ? __uint_as_float(kBadLse)
+                                             : (l != 0.f ? m + log2f(l) - kShift : -INFINITY);
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&bars.o_free));
+      ++seg;
+      s = y;
+      sl2 = sl2_next;
+    }
   }
+
+  // ---- teardown ------------------------------------------------------------------------------
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && tid == 0) set_status(p.status, MTPATTN_ERR_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Join the partials of the units that were cut: a warp a row, 8 dims a lane, all pieces of the
+// row weighted by 2^(lse - max).  A piece of a row that saw none of its keys has lse -inf and
+// counts nothing; a NaN in any other piece stays in the result.
+constexpr int kReduceWarps = 8;
+
+__global__ void __launch_bounds__(kReduceWarps * 32)
+tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kReduceWarps + (threadIdx.x >> 5);
+  const int tok = static_cast<int>(row / p.hq), head = static_cast<int>(row % p.hq);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // the row's sequence, and its unit's place on the line
+  int W = 0, unit0 = 0, nt = 0, rt = 0;
+  bool mine = false;
+  if (tok < p.total_q) {
+    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+      const Seq x = seq_at(p, b0 + lane);
+      const int upto = warp_scan(x.w, lane);
+      const bool here = x.n > 0 && tok >= x.q0 && tok < x.q0 + x.n && !x.err;
+      const uint32_t who = __ballot_sync(0xffffffffu, here);
+      if (who && !mine) {
+        mine = true;
+        const int f = __ffs(who) - 1;
+        nt = __shfl_sync(0xffffffffu, x.nt, f);
+        const int T = __shfl_sync(0xffffffffu, x.T, f);
+        const int h = head / p.ratio;
+        rt = (tok - __shfl_sync(0xffffffffu, x.q0, f)) * p.ratio + head - h * p.ratio;
+        unit0 = W + __shfl_sync(0xffffffffu, upto - x.w, f) + (h * T + rt / kRows) * nt;
+        rt %= kRows;
+      }
+      W += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
+  if (!mine) return;
+  const int pieces = min(p.ctas, W);
+  auto piece_of = [&](int x) {
+    return static_cast<int>(((static_cast<int64_t>(x) + 1) * pieces - 1) / W);
+  };
+  const int g0 = piece_of(unit0), g1 = piece_of(unit0 + nt - 1);
+  if (g0 == g1) return;                              // written whole
+  auto slot_of = [&](int g) {
+    return 2 * g + (unit0 <= piece_start(g, pieces, W) ? 0 : 1);
+  };
+  float M = -INFINITY;
+  bool bad = false;
+  for (int g = g0 + lane; g <= g1; g += 32) {
+    const float x = __ldcg(p.lse_part + slot_of(g) * kRows + rt);
+    bad |= __float_as_uint(x) == kBadLse;
+    M = fmaxf(M, x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  bad = __any_sync(0xffffffffu, bad);
+  float acc[8], wsum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  if (!bad) {
+#pragma unroll 4
+    for (int g = g0; g <= g1; ++g) {
+      const int slot = slot_of(g);
+      const float x = __ldcg(p.lse_part + slot * kRows + rt);
+      const float* o = p.o_part + (static_cast<int64_t>(slot) * kRows + rt) * kHeadDim + 8 * lane;
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(o));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(o + 4));
+      if (x == -INFINITY) continue;
+      const float w = exp2_hw(x - M);                // a NaN lse makes the row NaN
+      wsum += w;
+      acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
+      acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
+      acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
+      acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
+    }
+  }
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    h[e] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(tok) * p.out_stride_tok +
+                            static_cast<int64_t>(head) * p.out_stride_head + 8 * lane) =
+      make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 __global__ void __launch_bounds__(MTP_TREE_MAX_NODES)
@@ -147,6 +1039,37 @@ tree_mask_kernel(const int32_t* parents, const int32_t* cu_q, int32_t total_q, u
     at = up;
   }
   mask[q0 + i] = word;
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+
+// CTAs of a call: one per SM, but no more than the line can have key tiles.
+int64_t line_bound(int32_t num_seqs, int32_t total_q, int32_t hkv, int32_t ratio, int32_t max_pages) {
+  const int64_t row_tiles = static_cast<int64_t>(total_q) * ratio / kRows + num_seqs;
+  return row_tiles * hkv * ((max_pages + kTilePages - 1) / kTilePages);
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+cudaError_t launch_pdl(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                       TreeAttnParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&p};
+  cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -179,7 +1102,12 @@ extern "C" size_t mtp_tree_attn_workspace_size(int32_t num_seqs, int32_t total_q
   if (num_seqs < 0 || total_q < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       max_pages_per_seq < 0 || num_q_heads % num_kv_heads)
     return 0;
-  return 256;
+  const int sms = device_sm_count(-1);
+  if (sms <= 0) return 0;
+  const int64_t ctas = std::min<int64_t>(
+      sms, line_bound(num_seqs, total_q, num_kv_heads, num_q_heads / num_kv_heads, max_pages_per_seq));
+  // partial outputs, then their log-sum-exps; two slots of 128 rows a CTA
+  return align256(static_cast<size_t>(ctas) * 2 * kRows * (kHeadDim + 1) * sizeof(float)) + 256;
 }
 
 extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_head,
@@ -215,7 +1143,8 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
   const int ratio = num_q_heads / num_kv_heads;
   if (ratio > MTP_TREE_MAX_RATIO) return MTPATTN_E_UNSUPPORTED;
   if (total_q > static_cast<int64_t>(num_seqs) * MTP_TREE_MAX_NODES) return MTPATTN_E_UNSUPPORTED;
-  if (num_pages > INT32_MAX || max_pages_per_seq > INT32_MAX / kPage || num_q_heads > 65535)
+  if (num_pages > INT32_MAX || max_pages_per_seq > INT32_MAX / kPage - kTilePages ||
+      line_bound(num_seqs, total_q, num_kv_heads, ratio, max_pages_per_seq) > INT32_MAX)
     return MTPATTN_E_UNSUPPORTED;
   // 3. the workspace
   const int device = current_device();
@@ -230,11 +1159,10 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
   if (!all_on_device(ptrs, device) || (status && !ptr_on_device(status, device)))
     return MTPATTN_E_DEVICE;
 
-  TreeAttnParams p;
+  TreeAttnParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride_tok = q_stride_tok;
   p.q_stride_head = q_stride_head;
-  p.k_cache = static_cast<const uint8_t*>(k_cache);
   p.v_cache = static_cast<const uint8_t*>(v_cache);
   p.num_pages = num_pages;
   p.block_tables = block_tables;
@@ -254,7 +1182,36 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
   p.out_stride_tok = out_stride_tok;
   p.out_stride_head = out_stride_head;
   p.status = status;
-  const dim3 grid(static_cast<unsigned>(num_seqs) * MTP_TREE_MAX_NODES, num_q_heads);
-  tree_attn_plain_kernel<<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
+  p.ctas = static_cast<int32_t>(std::min<int64_t>(
+      device_sm_count(device), line_bound(num_seqs, total_q, num_kv_heads, ratio, max_pages_per_seq)));
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = p.o_part + static_cast<int64_t>(p.ctas) * 2 * kRows * kHeadDim;
+  AttnParams cache{};                                // what the tensor map goes by
+  cache.k_cache = static_cast<const uint8_t*>(k_cache);
+  cache.v_cache = p.v_cache;
+  cache.num_pages = num_pages;
+  cache.num_kv_heads = num_kv_heads;
+  CUtensorMap unused;
+  if (!kv_tensor_maps(cache, device, &p.tmap_k, &unused)) return MTPATTN_E_LAUNCH;
+  static std::atomic<bool> attr_set[64];             // per device; setting it twice is harmless
+  if (device >= 64) return MTPATTN_E_DEVICE;
+  if (!attr_set[device].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTree) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MTPATTN_E_LAUNCH;
+    }
+    attr_set[device].store(true, std::memory_order_release);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (launch_pdl(reinterpret_cast<const void*>(tree_attn_kernel), dim3(p.ctas), kTreeThreads, kSmemTree,
+                 st, p) != cudaSuccess)
+    return MTPATTN_E_LAUNCH;
+  // sequences of one key tile are never cut
+  if (max_pages_per_seq <= kTilePages) return MTPATTN_OK;
+  const int64_t rows = static_cast<int64_t>(total_q) * num_q_heads;
+  const dim3 grid(static_cast<unsigned>((rows + kReduceWarps - 1) / kReduceWarps));
+  return launch_pdl(reinterpret_cast<const void*>(tree_reduce_kernel), grid, kReduceWarps * 32, 0, st, p) ==
+                 cudaSuccess
+             ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
