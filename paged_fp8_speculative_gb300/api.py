@@ -324,29 +324,56 @@ def fmha_fwd_fp8_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_des
 
 
 # ---- draft trees (include/mtp_tree.h) ------------------------------------------------------------
+#
+# These calls are short: the checks are written for few Python operations (an attribute of a
+# tensor costs 0.1 us, torch.cuda.current_stream() 3 us, torch.empty 1.6 us on a Grace core).
 
 TREE_MAX_NODES = 64
 TREE_MAX_RATIO = 16
 TREE_MAX_VOCAB = 1 << 20
 ERR_PARENT, ERR_ROW = 64, 128
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_I32, _BF16 = torch.int32, torch.bfloat16
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_WORDS = (torch.int64, torch.uint64)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _int32_vector(name, t, n=None, what="a contiguous int32 vector"):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or \
-            not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{name} must be {what}" + (f" of {n}" if n is not None else ""))
+def _call_stream(device: int, stream):
+    """The stream's handle for a call on tensors of this device (-1: the CPU, which the library
+    refuses).  The library launches on the current device: tensors of another one are refused
+    here, where the message can say so."""
+    if device >= 0 and device != _current_device():
+        raise ValueError(f"tensors are on cuda:{device}, the current device is "
+                         f"cuda:{_current_device()}")
+    if stream is None:
+        if device < 0:
+            return None
+        return _raw_stream(device) if _raw_stream else torch.cuda.current_stream().cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        if device >= 0 and stream.device.index != device:
+            raise ValueError(f"stream is on {stream.device}, tensors are on cuda:{device}")
+        return stream.cuda_stream
+    return int(stream)
 
 
-def _on_call_device(device, stream):
-    """The library launches on the current device: refuse tensors of another one here, where
-    the message can say so (the library would return E_DEVICE)."""
-    if device.type == "cuda" and device.index not in (None, torch.cuda.current_device()):
-        raise ValueError(f"tensors are on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    if isinstance(stream, torch.cuda.Stream) and device.type == "cuda" and \
-            stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+def _vector(name, t, n):
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n}")
+
+
+def _sequences(cu_seqlens_q) -> int:
+    shape = cu_seqlens_q.shape
+    if cu_seqlens_q.dtype is not _I32 or len(shape) != 1 or shape[0] < 1 or \
+            not cu_seqlens_q.is_contiguous():
+        raise ValueError("cu_seqlens_q must be a contiguous int32 vector of num_seqs + 1")
+    return shape[0] - 1
+
+
+def _words(name, t, n):
+    if t.dtype not in _WORDS or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int64 vector, one word per node")
 
 
 def mtp_tree_mask(parents: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -357,20 +384,16 @@ def mtp_tree_mask(parents: torch.Tensor, cu_seqlens_q: torch.Tensor,
     parents [total_q] int32 (an index within the sequence; the root's entry is not read);
     cu_seqlens_q [B+1] int32; returns int64 [total_q] (the bits of the uint64 words).
     """
-    _int32_vector("parents", parents)
-    _int32_vector("cu_seqlens_q", cu_seqlens_q)
-    total_q, num_seqs = parents.numel(), cu_seqlens_q.numel() - 1
-    if num_seqs < 0:
-        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
-    _on_call_device(parents.device, stream)
-    with _temporaries_on(stream, parents.device, out is None):
-        if out is None:
+    total_q = parents.numel()
+    _vector("parents", parents, total_q)
+    num_seqs = _sequences(cu_seqlens_q)
+    if out is None:
+        with _temporaries_on(stream, parents.device, stream is not None):
             out = torch.empty(total_q, dtype=torch.int64, device=parents.device)
-    if out.dtype not in (torch.int64, torch.uint64) or tuple(out.shape) != (total_q,) or \
-            not out.is_contiguous():
-        raise ValueError("out must be a contiguous int64 vector, one word per node")
-    rc = lib().mtp_tree_mask(_ptr(parents), _ptr(cu_seqlens_q), num_seqs, total_q, _ptr(out),
-                             _ptr(status), _stream_handle(stream))
+    _words("out", out, total_q)
+    rc = lib().mtp_tree_mask(parents.data_ptr(), cu_seqlens_q.data_ptr(), num_seqs, total_q,
+                             out.data_ptr(), _ptr(status),
+                             _call_stream(parents.get_device(), stream))
     if rc != OK:
         raise MtpAttnError(rc)
     return out
@@ -397,29 +420,48 @@ def mtp_tree_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     least mtp_tree_attn_workspace_size(...) bytes, kept by a decode loop so that no call
     allocates; it needs no initialisation.
     """
-    dev = q.device
-    _on_call_device(dev, stream)
-    makes = (out is None or workspace is None or not isinstance(k_descale, torch.Tensor) or
-             not isinstance(v_descale, torch.Tensor))
-    with _temporaries_on(stream, dev, makes):
-        kd = _descale(k_descale, dev)
-        vd = _descale(v_descale, dev)
-        num_seqs, total_q, hq, hkv = _check_args(q, k_cache, v_cache, block_tables, seq_lens,
-                                                 cu_seqlens_q, kd, vd, out)
-        if tree_mask.dtype not in (torch.int64, torch.uint64) or \
-                tuple(tree_mask.shape) != (total_q,) or not tree_mask.is_contiguous():
-            raise ValueError("tree_mask must be a contiguous int64 vector, one word per node")
-        if out is None:
-            out = torch.empty(total_q, hq, HEAD_DIM, dtype=torch.bfloat16, device=dev)
-        if workspace is None:
-            need = mtp_tree_attn_workspace_size(num_seqs, total_q, hq, hkv, block_tables.shape[1])
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    device = q.get_device()
+    handle = _call_stream(device, stream)
+    shape, cache = q.shape, k_cache.shape
+    if q.dtype is not _BF16 or len(shape) != 3 or shape[2] != HEAD_DIM or q.stride(2) != 1:
+        raise ValueError("q must be bf16 [total_q, H_q, 256] with unit stride on head_dim")
+    if k_cache.dtype not in _CODES or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache / v_cache must be uint8 or float8_e4m3fn codes")
+    if len(cache) != 4 or cache[1] != PAGE_SIZE or cache[3] != HEAD_DIM:
+        raise ValueError("k_cache must be [num_pages, 16, H_kv, 256]")
+    if v_cache.shape != cache or not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("k_cache and v_cache must be contiguous and of the same shape")
+    total_q, hq, _ = shape
+    num_seqs = _sequences(cu_seqlens_q)
+    _vector("seq_lens", seq_lens, num_seqs)
+    table = block_tables.shape
+    if block_tables.dtype is not _I32 or len(table) != 2 or table[0] != num_seqs or \
+            not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [B, max_pages] tensor")
+    _words("tree_mask", tree_mask, total_q)
+    if out is None or workspace is None or not isinstance(k_descale, torch.Tensor) or \
+            not isinstance(v_descale, torch.Tensor):
+        dev = q.device
+        with _temporaries_on(stream, dev, stream is not None):
+            k_descale, v_descale = _descale(k_descale, dev), _descale(v_descale, dev)
+            if out is None:
+                out = torch.empty(shape, dtype=_BF16, device=dev)
+            if workspace is None:
+                need = mtp_tree_attn_workspace_size(num_seqs, total_q, hq, cache[2], table[1])
+                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    for name, t in (("k_descale", k_descale), ("v_descale", v_descale)):
+        if t.dtype is not torch.float32 or t.numel() != 1:
+            raise ValueError(f"{name} must be a 1-element float32 tensor")
+    if out.dtype is not _BF16 or out.shape != shape or out.stride(2) != 1:
+        raise ValueError("out must be bf16 [total_q, H_q, 256] with unit stride on head_dim")
+    q_tok, q_head, _ = q.stride()
+    o_tok, o_head, _ = out.stride()
     rc = lib().mtp_tree_attn_fwd(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0],
-        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q),
-        _ptr(tree_mask), num_seqs, total_q, hq, hkv, _ptr(kd), _ptr(vd), float(softmax_scale),
-        _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(out), out.stride(0), out.stride(1), _ptr(status), _stream_handle(stream))
+        q.data_ptr(), q_tok, q_head, k_cache.data_ptr(), v_cache.data_ptr(), cache[0],
+        block_tables.data_ptr(), table[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
+        tree_mask.data_ptr(), num_seqs, total_q, hq, cache[2], k_descale.data_ptr(),
+        v_descale.data_ptr(), softmax_scale, workspace.data_ptr(), workspace.nbytes,
+        out.data_ptr(), o_tok, o_head, _ptr(status), handle)
     if rc != OK:
         raise MtpAttnError(rc)
     return out
@@ -427,33 +469,30 @@ def mtp_tree_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 
 def _verify_args(rows, name, draft_tokens, parents, cu_seqlens_q, max_path, accept_index,
                  accept_len, out_tokens, stream):
-    """Checks shared by the two verifications; makes the outputs that were not given."""
-    if rows.dtype not in _DTYPES or rows.dim() != 2 or rows.stride(1) != 1 and rows.shape[1] > 1:
+    """Checks shared by the two verifications; makes the outputs that were not given.  Returns
+    (dtype, total_q, vocab, row stride, num_seqs, the outputs)."""
+    dtype, shape = _DTYPES.get(rows.dtype), rows.shape
+    if dtype is None or len(shape) != 2 or shape[1] > 1 and rows.stride(1) != 1:
         raise ValueError(f"{name} must be float32, bfloat16 or float16 [total_q, vocab] with unit "
                          "stride along the vocabulary")
-    total_q = rows.shape[0]
-    _int32_vector("draft_tokens", draft_tokens, total_q)
-    _int32_vector("parents", parents, total_q)
-    _int32_vector("cu_seqlens_q", cu_seqlens_q)
-    num_seqs = cu_seqlens_q.numel() - 1
-    if num_seqs < 0:
-        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
-    dev = rows.device
-    _on_call_device(dev, stream)
-    makes = accept_index is None or accept_len is None or out_tokens is None
-    with _temporaries_on(stream, dev, makes):
-        if accept_index is None:
-            accept_index = torch.empty(num_seqs, max_path, dtype=torch.int32, device=dev)
-        if accept_len is None:
-            accept_len = torch.empty(num_seqs, dtype=torch.int32, device=dev)
-        if out_tokens is None:
-            out_tokens = torch.empty(num_seqs, max_path, dtype=torch.int32, device=dev)
+    total_q, vocab = shape
+    _vector("draft_tokens", draft_tokens, total_q)
+    _vector("parents", parents, total_q)
+    num_seqs = _sequences(cu_seqlens_q)
+    if accept_index is None or accept_len is None or out_tokens is None:
+        dev = rows.device
+        with _temporaries_on(stream, dev, stream is not None):
+            if accept_index is None:
+                accept_index = torch.empty((num_seqs, max_path), dtype=_I32, device=dev)
+            if accept_len is None:
+                accept_len = torch.empty(num_seqs, dtype=_I32, device=dev)
+            if out_tokens is None:
+                out_tokens = torch.empty((num_seqs, max_path), dtype=_I32, device=dev)
     for what, t in (("accept_index", accept_index), ("out_tokens", out_tokens)):
-        if t.dtype != torch.int32 or tuple(t.shape) != (num_seqs, max_path) or \
-                not t.is_contiguous():
+        if t.dtype is not _I32 or t.shape != (num_seqs, max_path) or not t.is_contiguous():
             raise ValueError(f"{what} must be a contiguous int32 [num_seqs, max_path] tensor")
-    _int32_vector("accept_len", accept_len, num_seqs)
-    return total_q, num_seqs, accept_index, accept_len, out_tokens
+    _vector("accept_len", accept_len, num_seqs)
+    return dtype, total_q, vocab, _row_stride(rows), num_seqs, accept_index, accept_len, out_tokens
 
 
 def _row_stride(t):
@@ -475,14 +514,14 @@ def mtp_tree_verify_greedy(logits: torch.Tensor, draft_tokens: torch.Tensor,
     root's 0, the accepted nodes, -1s; accept_len [B] int32; out_tokens [B, max_path] int32: the
     accepted tokens, the next token, -1s).
     """
-    total_q, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
-        logits, "logits", draft_tokens, parents, cu_seqlens_q, int(max_path), accept_index,
-        accept_len, out_tokens, stream)
+    handle = _call_stream(logits.get_device(), stream)
+    dtype, total_q, vocab, stride, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
+        logits, "logits", draft_tokens, parents, cu_seqlens_q, max_path, accept_index, accept_len,
+        out_tokens, stream)
     rc = lib().mtp_tree_verify_greedy(
-        _ptr(logits), _DTYPES[logits.dtype], _row_stride(logits), logits.shape[1],
-        _ptr(draft_tokens), _ptr(parents), _ptr(cu_seqlens_q), num_seqs, total_q, int(max_path),
-        _ptr(accept_index), _ptr(accept_len), _ptr(out_tokens), _ptr(status),
-        _stream_handle(stream))
+        logits.data_ptr(), dtype, stride, vocab, draft_tokens.data_ptr(), parents.data_ptr(),
+        cu_seqlens_q.data_ptr(), num_seqs, total_q, max_path, accept_index.data_ptr(),
+        accept_len.data_ptr(), out_tokens.data_ptr(), _ptr(status), handle)
     if rc != OK:
         raise MtpAttnError(rc)
     return accept_index, accept_len, out_tokens
@@ -503,23 +542,25 @@ def mtp_tree_verify_sample(target_probs: torch.Tensor, draft_probs: Optional[tor
     were drawn from, or None (children chosen outright); uniforms [total_q] float32 in [0, 1):
     each node's own number, the root's for the final draw.  Returns as mtp_tree_verify_greedy.
     """
-    total_q, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
-        target_probs, "target_probs", draft_tokens, parents, cu_seqlens_q, int(max_path),
-        accept_index, accept_len, out_tokens, stream)
-    if draft_probs is not None and (
-            draft_probs.dtype != target_probs.dtype or draft_probs.shape != target_probs.shape or
-            draft_probs.stride(1) != 1 and draft_probs.shape[1] > 1):
-        raise ValueError("draft_probs must have target_probs' type and shape and unit stride along "
-                         "the vocabulary")
-    if uniforms.dtype != torch.float32 or tuple(uniforms.shape) != (total_q,) or \
+    handle = _call_stream(target_probs.get_device(), stream)
+    dtype, total_q, vocab, stride, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
+        target_probs, "target_probs", draft_tokens, parents, cu_seqlens_q, max_path, accept_index,
+        accept_len, out_tokens, stream)
+    draft, draft_stride = None, 0
+    if draft_probs is not None:
+        if draft_probs.dtype is not target_probs.dtype or draft_probs.shape != (total_q, vocab) or \
+                vocab > 1 and draft_probs.stride(1) != 1:
+            raise ValueError("draft_probs must have target_probs' type and shape and unit stride "
+                             "along the vocabulary")
+        draft, draft_stride = draft_probs.data_ptr(), _row_stride(draft_probs)
+    if uniforms.dtype is not torch.float32 or uniforms.shape != (total_q,) or \
             not uniforms.is_contiguous():
         raise ValueError("uniforms must be a contiguous float32 vector, one number per node")
     rc = lib().mtp_tree_verify_sample(
-        _ptr(target_probs), _row_stride(target_probs), _ptr(draft_probs),
-        0 if draft_probs is None else _row_stride(draft_probs), _DTYPES[target_probs.dtype],
-        target_probs.shape[1], _ptr(draft_tokens), _ptr(parents), _ptr(cu_seqlens_q),
-        _ptr(uniforms), num_seqs, total_q, int(max_path), _ptr(accept_index), _ptr(accept_len),
-        _ptr(out_tokens), _ptr(status), _stream_handle(stream))
+        target_probs.data_ptr(), stride, draft, draft_stride, dtype, vocab,
+        draft_tokens.data_ptr(), parents.data_ptr(), cu_seqlens_q.data_ptr(), uniforms.data_ptr(),
+        num_seqs, total_q, max_path, accept_index.data_ptr(), accept_len.data_ptr(),
+        out_tokens.data_ptr(), _ptr(status), handle)
     if rc != OK:
         raise MtpAttnError(rc)
     return accept_index, accept_len, out_tokens
@@ -531,39 +572,39 @@ CACHE_MAX_ROWS = 8192
 ERR_LEN, ERR_FULL, ERR_REF, ERR_CACHE_ROW = 256, 512, 1024, 2048
 
 
-def _cache_args(k_cache, v_cache, stream):
-    """(layers, layer stride in bytes, pages, KV heads) of one layer's caches [num_pages, 16,
-    H_kv, 256] or of a stack's [num_layers, num_pages, 16, H_kv, 256]."""
-    if k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn) or v_cache.dtype != k_cache.dtype:
+def _cache_args(k_cache, v_cache):
+    """(K's and V's address, layers, layer stride in bytes, pages, KV heads) of one layer's caches
+    [num_pages, 16, H_kv, 256] or of a stack's [num_layers, num_pages, 16, H_kv, 256]."""
+    shape = k_cache.shape
+    if k_cache.dtype not in _CODES or v_cache.dtype is not k_cache.dtype:
         raise ValueError("k_cache / v_cache must be uint8 or float8_e4m3fn codes")
-    if k_cache.dim() not in (4, 5) or k_cache.shape[-3] != PAGE_SIZE or \
-            k_cache.shape[-1] != HEAD_DIM:
+    if len(shape) not in (4, 5) or shape[-3] != PAGE_SIZE or shape[-1] != HEAD_DIM:
         raise ValueError("k_cache must be [num_pages, 16, H_kv, 256], or that behind num_layers")
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+    stride = k_cache.stride()
+    if v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must be of the same shape and strides")
-    layer = k_cache[0] if k_cache.dim() == 5 else k_cache
-    if not layer.is_contiguous():
+    layers = shape[0] if len(shape) == 5 else 1
+    pages, hkv = shape[-4], shape[-2]
+    if not k_cache.is_contiguous() and layers > 0 and \
+            not (k_cache[0] if len(shape) == 5 else k_cache).is_contiguous():
         raise ValueError("a layer's cache must be contiguous")
-    _on_call_device(k_cache.device, stream)
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    stride = k_cache.stride(0) if layers > 1 else layer.numel()
-    return layers, stride, k_cache.shape[-4], k_cache.shape[-2]
+    layer = stride[0] if layers > 1 else pages * hkv * (PAGE_SIZE * HEAD_DIM)
+    return k_cache.data_ptr(), v_cache.data_ptr(), layers, layer, pages, hkv
 
 
 def _table_args(block_tables, seq_lens, ref_counts, num_pages):
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
-            not block_tables.is_contiguous():
+    shape = block_tables.shape
+    if block_tables.dtype is not _I32 or len(shape) != 2 or not block_tables.is_contiguous():
         raise ValueError("block_tables must be a contiguous int32 [num_rows, max_pages] tensor")
-    _int32_vector("seq_lens", seq_lens, block_tables.shape[0])
-    _int32_vector("ref_counts", ref_counts, num_pages)
+    _vector("seq_lens", seq_lens, shape[0])
+    _vector("ref_counts", ref_counts, num_pages)
+    return shape
 
 
-def _cache_workspace(workspace, block_tables, stream):
-    with _temporaries_on(stream, block_tables.device, workspace is None):
-        if workspace is None:
-            workspace = torch.empty(max(mtp_cache_workspace_size(*block_tables.shape), 256),
-                                    dtype=torch.uint8, device=block_tables.device)
-    return workspace
+def _cache_workspace(block_tables, shape, stream):
+    with _temporaries_on(stream, block_tables.device, stream is not None):
+        return torch.empty(max(mtp_cache_workspace_size(*shape), 256), dtype=torch.uint8,
+                           device=block_tables.device)
 
 
 def mtp_cache_workspace_size(num_rows: int, max_pages_per_seq: int) -> int:
@@ -581,15 +622,16 @@ def mtp_cache_resize(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     new_lens [rows] int32 (0 frees a row).  A shared, partly filled last page is copied first.
     With too few free pages nothing is handed out and ERR_FULL is set.
     """
-    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
-    _table_args(block_tables, seq_lens, ref_counts, pages)
-    _int32_vector("new_lens", new_lens, block_tables.shape[0])
-    workspace = _cache_workspace(workspace, block_tables, stream)
+    handle = _call_stream(block_tables.get_device(), stream)
+    cache = _cache_args(k_cache, v_cache)
+    shape = _table_args(block_tables, seq_lens, ref_counts, cache[4])
+    rows, width = shape
+    _vector("new_lens", new_lens, rows)
+    if workspace is None:
+        workspace = _cache_workspace(block_tables, shape, stream)
     rc = lib().mtp_cache_resize(
-        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(block_tables),
-        block_tables.shape[1], _ptr(seq_lens), block_tables.shape[0], _ptr(ref_counts),
-        _ptr(new_lens), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(status), _stream_handle(stream))
+        *cache, block_tables.data_ptr(), width, seq_lens.data_ptr(), rows, ref_counts.data_ptr(),
+        new_lens.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(status), handle)
     if rc != OK:
         raise MtpAttnError(rc)
 
@@ -600,16 +642,19 @@ def mtp_cache_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows dst[i] (empty) become copies of rows src[i]: full pages are shared, a partly filled
     last page is copied.  src, dst int32 vectors of the same length."""
-    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
-    _table_args(block_tables, seq_lens, ref_counts, pages)
-    _int32_vector("src", src)
-    _int32_vector("dst", dst, src.numel())
-    workspace = _cache_workspace(workspace, block_tables, stream)
+    handle = _call_stream(block_tables.get_device(), stream)
+    cache = _cache_args(k_cache, v_cache)
+    shape = _table_args(block_tables, seq_lens, ref_counts, cache[4])
+    rows, width = shape
+    pairs = src.numel()
+    _vector("src", src, pairs)
+    _vector("dst", dst, pairs)
+    if workspace is None:
+        workspace = _cache_workspace(block_tables, shape, stream)
     rc = lib().mtp_cache_fork(
-        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(block_tables),
-        block_tables.shape[1], _ptr(seq_lens), block_tables.shape[0], _ptr(ref_counts),
-        _ptr(src), _ptr(dst), src.numel(), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), _stream_handle(stream))
+        *cache, block_tables.data_ptr(), width, seq_lens.data_ptr(), rows, ref_counts.data_ptr(),
+        src.data_ptr(), dst.data_ptr(), pairs, workspace.data_ptr(), workspace.nbytes,
+        _ptr(status), handle)
     if rc != OK:
         raise MtpAttnError(rc)
 
@@ -618,12 +663,13 @@ def mtp_cache_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src_pages
                          dst_pages: torch.Tensor, status: Optional[torch.Tensor] = None,
                          stream=None) -> None:
     """Page dst_pages[i] gets the contents of page src_pages[i], in all layers."""
-    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
-    _int32_vector("src_pages", src_pages)
-    _int32_vector("dst_pages", dst_pages, src_pages.numel())
-    rc = lib().mtp_cache_copy_pages(
-        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(src_pages),
-        _ptr(dst_pages), src_pages.numel(), _ptr(status), _stream_handle(stream))
+    handle = _call_stream(k_cache.get_device(), stream)
+    cache = _cache_args(k_cache, v_cache)
+    pairs = src_pages.numel()
+    _vector("src_pages", src_pages, pairs)
+    _vector("dst_pages", dst_pages, pairs)
+    rc = lib().mtp_cache_copy_pages(*cache, src_pages.data_ptr(), dst_pages.data_ptr(), pairs,
+                                    _ptr(status), handle)
     if rc != OK:
         raise MtpAttnError(rc)
 
@@ -639,26 +685,28 @@ def mtp_cache_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables
     accept_index [B, max_path] and accept_len [B] as the verifications return them.  The pages
     that hold the trees must belong to their rows alone; none are given back here.
     """
-    layers, stride, pages, hkv = _cache_args(k_cache, v_cache, stream)
-    num_seqs = seq_lens.numel()
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
-            block_tables.shape[0] != num_seqs or not block_tables.is_contiguous():
-        raise ValueError("block_tables must be a contiguous int32 [B, max_pages] tensor")
-    _int32_vector("seq_lens", seq_lens)
-    _int32_vector("cu_seqlens_q", cu_seqlens_q, num_seqs + 1)
-    _int32_vector("accept_len", accept_len, num_seqs)
-    if accept_index.dtype != torch.int32 or accept_index.dim() != 2 or \
-            accept_index.shape[0] != num_seqs or not accept_index.is_contiguous():
+    handle = _call_stream(k_cache.get_device(), stream)
+    cache = _cache_args(k_cache, v_cache)
+    num_seqs = _sequences(cu_seqlens_q)
+    table, path = block_tables.shape, accept_index.shape
+    if block_tables.dtype is not _I32 or len(table) != 2 or table[0] != num_seqs or \
+            not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [B, max_pages] tensor, "
+                         "cu_seqlens_q [B + 1]")
+    _vector("seq_lens", seq_lens, num_seqs)
+    _vector("accept_len", accept_len, num_seqs)
+    if accept_index.dtype is not _I32 or len(path) != 2 or path[0] != num_seqs or \
+            not accept_index.is_contiguous():
         raise ValueError("accept_index must be a contiguous int32 [B, max_path] tensor")
-    with _temporaries_on(stream, seq_lens.device, new_seq_lens is None):
-        if new_seq_lens is None:
+    if new_seq_lens is None:
+        with _temporaries_on(stream, seq_lens.device, stream is not None):
             new_seq_lens = torch.empty_like(seq_lens)
-    _int32_vector("new_seq_lens", new_seq_lens, num_seqs)
+    else:
+        _vector("new_seq_lens", new_seq_lens, num_seqs)
     rc = lib().mtp_cache_compact(
-        _ptr(k_cache), _ptr(v_cache), layers, stride, pages, hkv, _ptr(block_tables),
-        block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q), num_seqs,
-        num_seqs * TREE_MAX_NODES, _ptr(accept_index), _ptr(accept_len), accept_index.shape[1],
-        _ptr(new_seq_lens), _ptr(status), _stream_handle(stream))
+        *cache, block_tables.data_ptr(), table[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
+        num_seqs, num_seqs * TREE_MAX_NODES, accept_index.data_ptr(), accept_len.data_ptr(),
+        path[1], new_seq_lens.data_ptr(), _ptr(status), handle)
     if rc != OK:
         raise MtpAttnError(rc)
     return new_seq_lens
