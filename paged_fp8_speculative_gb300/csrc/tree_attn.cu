@@ -10,12 +10,17 @@
 // partial output and log-sum-exp per piece in the workspace, and tree_reduce_kernel joins them.
 // A CTA has at most two partial units, the first and the last of its piece: two slots per CTA.
 //
-// Roles (320 threads):
-//   warp 0     K: TMA loads of the K pages (two 128-byte-wide boxes a page, 128B-swizzled);
-//   warp 1     MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
-//   warps 2-5  V: warp w loads page w of each 64-key half tile to registers, a half tile ahead,
-//              widens it to f16 and stores it as PV's operand (no staging of the codes);
-//   warps 6-9  softmax: thread = query row = TMEM lane; also the Q operand and the epilogue.
+// Roles (576 threads):
+//   warp 0       K: TMA loads of the K pages (two 128-byte-wide boxes a page, 128B-swizzled);
+//   warp 1       MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
+//   warps 2-9    V, two groups of four that take the 64-key half tiles in turn: warp w of a group
+//                loads page w of its half tile to registers, one ahead, widens it to f16 and
+//                stores it as PV's operand (no staging of the codes);
+//   warps 10-17  softmax: thread = query row = TMEM lane, two warps a row quarter that take 64 of a
+//                tile's 128 keys each and exchange their maxima; also the Q operand, and half of
+//                the output's dims each.
+// One warp an SM quarter for softmax and for V took twice the tensor cores' time (both are chains
+// of dependent work on one row, or one page), hence two of each.
 //
 // Precision.  K enters as its e4m3 codes, Q as the sum of two e4m3 terms of x = q 2^a (a per row,
 // max |x| in [128, 256)): hi = e4m3(x), lo = e4m3(x - hi), both products into one accumulator.  A
@@ -53,13 +58,13 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTreeThreads = 320;
+constexpr int kTreeThreads = 576;
 constexpr int kRows = 128;                         // query rows per tile
 constexpr int kKeys = 128;                         // keys per tile
 constexpr int kTilePages = kKeys / kPage;          // 8
 constexpr int kHalfKeys = 64;                      // V is staged half a tile at a time
-constexpr int kVWarps = 4;
-constexpr int kWarpV = 2, kWarpSoft = kWarpV + kVWarps;
+constexpr int kVGroup = 4;                         // V warps of a group, a page each
+constexpr int kWarpV = 2, kWarpSoft = kWarpV + 2 * kVGroup, kSoftWarps = 8;
 constexpr int kQHalf = kRows * 128;                // 128 of the 256 dims of one Q term
 constexpr int kQTerm = 2 * kQHalf;                 // 32 KB: hi, then lo
 constexpr int kKHalf = kKeys * 128;
@@ -67,13 +72,15 @@ constexpr int kKTile = 2 * kKHalf;                 // 32 KB per stage
 constexpr int kKStages = 2;
 constexpr int kVAtom = kHalfKeys * 128;            // 64 dims of 64 keys, f16
 constexpr int kVStage = 4 * kVAtom;                // 32 KB per stage
-constexpr int kVStages = 2;
-constexpr int kStagePitch = 36;                    // floats a row of the output staging
+constexpr int kVStages = 2;                        // one per group
+constexpr int kOutCols = 16;                       // output columns staged at a time
+constexpr int kStagePitch = 20;                    // floats a row there (eight rows: all 32 banks)
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kQTerm;
 constexpr int kOffV = kOffK + kKStages * kKTile;
 constexpr int kOffOut = kOffV + kVStages * kVStage;
-constexpr int kOffBar = kOffOut + 4 * 32 * kStagePitch * 4;
+constexpr int kOffXch = kOffOut + kSoftWarps * 32 * kStagePitch * 4;
+constexpr int kOffBar = kOffXch + 2 * 2 * kRows * 4;   // exchange: [parity][half][row] floats
 constexpr int kSmemTree = kOffBar + 512 + 1024;    // + alignment slack
 static_assert(kSmemTree <= 232448, "shared-memory layout");
 constexpr int kSCols = 128, kOCol = 256, kTmemCols = 512;
@@ -108,6 +115,7 @@ struct TreeBars {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_ready, o_free, final_mma;
+  uint64_t xch[4][2];        // a row quarter's two warps meet, in turn on two barriers
   uint32_t tmem_base;
   int32_t abort;
   int32_t bad[4];            // [segment & 3]: segment + 1 if it met a page outside the pool
@@ -189,13 +197,13 @@ struct Walker {
     upto = warp_scan(mine.w, lane);
   }
   __device__ __forceinline__ void start(const TreeAttnParams& p, int lane) {
-    const int W = line_length(p, lane);
+    b0 = before = 0;
+    hold(p, lane);
+    const int W = p.num_seqs <= 32 ? __shfl_sync(0xffffffffu, upto, 31) : line_length(p, lane);
     const int pieces = min(p.ctas, W);
     const int g = blockIdx.x;
     lo = pos = g < pieces ? piece_start(g, pieces, W) : W;
     hi = g < pieces ? piece_start(g + 1, pieces, W) : W;
-    b0 = before = 0;
-    hold(p, lane);
   }
   __device__ __forceinline__ bool next(const TreeAttnParams& p, int lane, Segment& s) {
     if (pos >= hi) return false;
@@ -334,16 +342,17 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       mbar_init(smem_u32(&bars.k_empty[i]), 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(smem_u32(&bars.v_full[i]), kVWarps);
+      mbar_init(smem_u32(&bars.v_full[i]), kVGroup);
       mbar_init(smem_u32(&bars.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.s_full[i]), 1);
-      mbar_init(smem_u32(&bars.p_full[i]), kRows);
+      mbar_init(smem_u32(&bars.p_full[i]), kSoftWarps);
       mbar_init(smem_u32(&bars.pv_done[i]), 1);
     }
-    mbar_init(smem_u32(&bars.q_ready), kRows);
-    mbar_init(smem_u32(&bars.o_free), kRows);
+    mbar_init(smem_u32(&bars.q_ready), kSoftWarps);
+    mbar_init(smem_u32(&bars.o_free), kSoftWarps);
+    for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&bars.xch[i >> 1][i & 1]), 2);
     mbar_init(smem_u32(&bars.final_mma), 1);
     for (int i = 0; i < 4; ++i) bars.bad[i] = bars.nan[i] = 0;
     bars.abort = 0;
@@ -476,9 +485,9 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     mbar_wait(smem_u32(&bars.final_mma), 0, &no_abort);
   } else if (warp < kWarpSoft) {
     // ========================================= V loads ============================================
-    // A half tile is 16 bytes x 8 a lane: load i holds key 2 i + lane / 16 of the warp's page,
+    // A page is 16 bytes x 8 a lane: load i holds key 2 i + lane / 16 of the warp's page,
     // dims 16 (lane % 16) .. + 15, two 16-byte chunks of f16 in 64-dim atom (lane % 16) / 4.
-    const int w = warp - kWarpV;
+    const int w = (warp - kWarpV) & (kVGroup - 1), group = (warp - kWarpV) / kVGroup;
     const int c16 = lane & 15, krow = lane >> 4;
     const int atom = c16 >> 2, ch = 2 * (c16 & 3);
     // lanes of odd atoms store their second chunk first: the eight lanes of a store phase then
@@ -496,7 +505,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     auto seg_end = [&]() { return min(2 * s.t1, ((s.L + kPage - 1) / kPage + 3) / 4); };
     if (more) hf_end = seg_end();
     int ent = 0, ent_at = -32;                      // lane l: the table entry of half tile ent_at + l
-    auto load = [&](Half& a) {                      // the next half tile; advances
+    auto load = [&](Half& a) {
       if (hf >= ent_at + 32 || hf < ent_at) {
         ent_at = hf;
         const int pg = 4 * (hf + lane) + w;
@@ -521,11 +530,12 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         }
       }
     };
-    uint32_t v = 0;
+    const int st = group;
+    uint32_t parity = 1;
     auto store = [&](Half& a, int sg) -> bool {
-      const int st = v % kVStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.v_empty[st]), ((v / kVStages) & 1) ^ 1, abort_flag)))
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.v_empty[st]), parity, abort_flag)))
         return false;
+      parity ^= 1;
       // Notes are made behind the wait: a slot of the four is then not one that the epilogue has
       // yet to read (this warp is two half tiles ahead of it at most).
       if (a.bad && lane == 0) bars.bad[sg & 3] = sg + 1;
@@ -562,7 +572,6 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.v_full[st]));
-      ++v;
       return true;
     };
     auto advance = [&]() {
@@ -576,37 +585,49 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         }
       }
     };
-    Half cur, nxt;
-    bool have = more;
-    int cur_seg = 0;
-    if (have) {
-      load(cur);
-      cur_seg = seg;
-      advance();
-    }
-    while (have) {
-      const bool have_next = more;
-      int next_seg = 0;
-      if (have_next) {
-        load(nxt);
-        next_seg = seg;
-        advance();
-      }
-      if (!store(cur, cur_seg)) break;
-      cur = nxt;
-      cur_seg = next_seg;
-      have = have_next;
+    // Two buffers in turn, so that one's loads are in flight while the other is widened (a copy
+    // between them would wait for the loads).
+    Half buf0, buf1;
+    int seg0 = 0, seg1 = 0;
+    auto fetch = [&](Half& a, int& sg) -> bool {
+      if (!more) return false;
+      load(a);
+      sg = seg;
+      advance();                                    // past this group's and the other one's
+      if (more) advance();
+      return true;
+    };
+    if (group == 1 && more) advance();
+    bool have0 = fetch(buf0, seg0), have1;
+    while (have0) {
+      have1 = fetch(buf1, seg1);
+      if (!store(buf0, seg0) || !have1) break;
+      have0 = fetch(buf0, seg0);
+      if (!store(buf1, seg1)) break;
     }
   } else {
     // ======================================= softmax (rows) =======================================
     const int quad = warp & 3;                      // TMEM lane quarter
+    const int half = (warp - kWarpSoft) >> 2;       // keys 64 half .. + 63, output dims 128 half ..
     const int r = 32 * quad + lane;                 // query row of the tile, TMEM lane
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    float* stage = reinterpret_cast<float*>(base + kOffOut) + quad * 32 * kStagePitch;
+    float* stage = reinterpret_cast<float*>(base + kOffOut) + (warp - kWarpSoft) * 32 * kStagePitch;
+    float* xch = reinterpret_cast<float*>(base + kOffXch);
     const float sl = p.scale_log2 * __ldg(p.k_descale);
     const float vd = __ldg(p.v_descale);
     uint32_t u = 0;                                 // key tiles so far
     int seg = 0;
+    // The two warps of a row quarter meet: what each wrote to shared memory before, the other
+    // sees after.  Bounded like every wait.
+    uint32_t meets = 0;
+    auto meet = [&]() -> bool {
+      const uint32_t bar = smem_u32(&bars.xch[quad][meets & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, (meets >> 1) & 1, abort_flag));
+      ++meets;
+      return ok;
+    };
 
     // Zeros for the rows of a sequence that cannot be computed.
     auto put_zeros = [&](const Segment& y) {
@@ -616,38 +637,40 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(y.q0 + t) * p.out_stride_tok +
                                               static_cast<int64_t>(y.h * p.ratio + g) * p.out_stride_head);
 #pragma unroll 1
-        for (int i = 0; i < kHeadDim / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < kHeadDim / 16; ++i) dst[half * (kHeadDim / 16) + i] = make_uint4(0u, 0u, 0u, 0u);
       }
     };
     auto next_running = [&](Segment& y) -> bool {
       while (walk.next(p, lane, y)) {
         if (!y.err) return true;
         put_zeros(y);
-        if (lane == 0 && quad == 0) set_status(p.status, y.err);
+        if (lane == 0 && warp == kWarpSoft) set_status(p.status, y.err);
       }
       return false;
     };
-    // The rows of this warp as two e4m3 terms into the Q operand; lane l returns row l's factor
-    // from raw products to log2 units (NaN for a row that is not finite).
-    auto prepare_q = [&](const Segment& y) -> float {
-      float mine = 0.f;
-      const int rows = y.n * p.ratio - y.m * kRows - 32 * quad;      // valid rows of this warp
-      if (rows > 0) {
-        const int half = lane >> 4, chunk = (lane & 15) >> 1;
-        unsigned char* q_hi = base + kOffQ + half * kQHalf + 8 * (lane & 1);
+    // Half of the row quarter's rows as two e4m3 terms into the Q operand, a row at a time by the
+    // whole warp (8 dims a lane); their factors from raw products to log2 units (NaN for a row that
+    // is not finite) to the exchange, from where `factor` gets this thread's row's.
+    auto prepare_q = [&](const Segment& y, float& factor) -> bool {
+      const int row0 = 32 * quad + 16 * half;
+      const int rows = y.n * p.ratio - y.m * kRows - row0;           // valid rows from there on
+      float* to = xch + (meets & 1) * 2 * kRows;
+      // a row quarter without any valid row is not computed; one with some is finite throughout
+      if (rows + 16 * half > 0) {
+        const int mine = y.m * kRows + row0 + (lane & 15);
+        const int t = mine / p.ratio, g = mine - t * p.ratio;
+        const int64_t at = static_cast<int64_t>(y.q0 + t) * p.q_stride_tok +
+                           static_cast<int64_t>(y.h * p.ratio + g) * p.q_stride_head;
+        const int chunk = (lane & 15) >> 1;
+        unsigned char* q_hi = base + kOffQ + (lane >> 4) * kQHalf + row0 * 128 + 8 * (lane & 1);
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += 8) {
+        for (int i0 = 0; i0 < 16; i0 += 8) {
           uint4 x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
+            const int64_t src = __shfl_sync(0xffffffffu, at, i0 + i);
             x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (i0 + i < rows) {
-              const int rr = y.m * kRows + 32 * quad + i0 + i;
-              const int t = rr / p.ratio, g = rr - t * p.ratio;
-              x[i] = __ldg(reinterpret_cast<const uint4*>(
-                  p.q + static_cast<int64_t>(y.q0 + t) * p.q_stride_tok +
-                  static_cast<int64_t>(y.h * p.ratio + g) * p.q_stride_head + 8 * lane));
-            }
+            if (i0 + i < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + src + 8 * lane));
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -658,7 +681,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
               top = max(top, max((ww[e] << 16) & 0x7fff0000u, ww[e] & 0x7fff0000u));
             top = __reduce_max_sync(0xffffffffu, top);
             const int e8 = static_cast<int>(top >> 23);              // exponent field
-            // 2^a takes the largest into [128, 256); a row of zeros or subnormals keeps a = 126
+            // 2^a takes the largest into [128, 256), as far as a = 126 does
             const int a = top == 0u ? 0 : min(126, 134 - e8);
             const float f = __int_as_float((a + 127) << 23);
             uint32_t hi[2], lo[2];
@@ -666,24 +689,28 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
                       __uint_as_float(ww[1] << 16) * f, __uint_as_float(ww[1] & 0xffff0000u) * f, hi[0], lo[0]);
             two_terms(__uint_as_float(ww[2] << 16) * f, __uint_as_float(ww[2] & 0xffff0000u) * f,
                       __uint_as_float(ww[3] << 16) * f, __uint_as_float(ww[3] & 0xffff0000u) * f, hi[1], lo[1]);
-            const int row = 32 * quad + i0 + i;
+            const int row = i0 + i;
             unsigned char* dst = q_hi + row * 128 + ((chunk ^ (row & 7)) << 4);
             *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
-            const float back = e8 == 255 ? __int_as_float(0x7fc00000)
+            if (lane == row)
+              to[row0 + row] = e8 == 255 ? __int_as_float(0x7fc00000)
                                          : sl * __int_as_float((127 - a) << 23);
-            if (lane == i0 + i) mine = back;
           }
         }
         fence_proxy_async_smem();
       }
-      mbar_arrive(smem_u32(&bars.q_ready));
-      return mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.q_ready));
+      if (!meet()) return false;
+      factor = to[r];
+      return true;
     };
 
     bool have = next_running(s), alive = true;
-    float sl2 = have ? prepare_q(s) : 0.f;
-    while (have) {
+    float sl2 = 0.f;
+    if (have) alive = prepare_q(s, sl2);
+    while (have && alive) {
       const int rr = s.m * kRows + r;
       const bool valid = rr < s.n * p.ratio;
       const bool active = __any_sync(0xffffffffu, valid);
@@ -708,28 +735,22 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         }
         if (active) {
           const uint32_t s_addr = lane_addr + sb * kSCols;
-          float x[kKeys];
+          float x[64];
           {
-            uint32_t v0[32], v1[32], v2[32], v3[32];
-            tmem_ld32(s_addr, v0);
-            tmem_ld32(s_addr + 32, v1);
-            tmem_ld32(s_addr + 64, v2);
-            tmem_ld32(s_addr + 96, v3);
+            uint32_t v0[32], v1[32];
+            tmem_ld32(s_addr + 64 * half, v0);
+            tmem_ld32(s_addr + 64 * half + 32, v1);
             tmem_ld_wait(v0);
             tmem_ld_wait(v1);
-            tmem_ld_wait(v2);
-            tmem_ld_wait(v3);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               x[e] = __uint_as_float(v0[e]);
               x[32 + e] = __uint_as_float(v1[e]);
-              x[64 + e] = __uint_as_float(v2[e]);
-              x[96 + e] = __uint_as_float(v3[e]);
             }
           }
-          // the keys of the tile that this row sees, 32 a word
-          const int off = t * kKeys - tree0;
-          const bool masked = off + kKeys > 0;
+          // the keys of this half tile that the row sees, 32 a word
+          const int off = t * kKeys + 64 * half - tree0;
+          const bool masked = off + 64 > 0;
           auto seen = [&](int c) -> uint32_t {
             const int st = off + 32 * c;
             if (st <= -32) return 0xffffffffu;
@@ -740,7 +761,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
           if (masked) {                              // may be negative
             const float none = -INFINITY * sgn;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
               const uint32_t bits = seen(c);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -751,7 +772,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
           if (__all_sync(0xffffffffu, !(sl2 < 0.f))) {
             float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
 #pragma unroll
-            for (int e = 4; e < kKeys; e += 4) {
+            for (int e = 4; e < 64; e += 4) {
               a = max3(a, x[e], x[e + 1]);
               b = max3(b, x[e + 2], x[e + 3]);
             }
@@ -759,10 +780,19 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
           } else {
             float a = x[0] * sgn;
 #pragma unroll
-            for (int e = 1; e < kKeys; ++e) a = fmaxf(a, x[e] * sgn);
+            for (int e = 1; e < 64; ++e) a = fmaxf(a, x[e] * sgn);
             top = a * sgn * sl2;
           }
           if (top != top) top = -INFINITY;           // nothing seen with a factor of 0, or all NaN
+          // the row's maximum over both halves; behind it both warps have read their logits, so
+          // P may be written over them
+          float* both = xch + (meets & 1) * 2 * kRows;
+          both[half * kRows + r] = top;
+          if (!meet()) {
+            alive = false;
+            break;
+          }
+          top = fmaxf(top, both[(half ^ 1) * kRows + r]);
           float alpha = 1.f;
           bool rescale = false;
           if (top != -INFINITY && (m == -INFINITY || top > m + kTau)) {
@@ -780,7 +810,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kHeadDim / 16; ++c) {  // 16 columns at a time: the logits are live
+            for (int c = 0; c < kHeadDim / 32; ++c) {  // 16 columns at a time: the logits are live
+              const uint32_t o_addr = lane_addr + kOCol + 128 * half + 16 * c;
               uint32_t o[16];
               asm volatile(
                   "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -788,17 +819,17 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
                   : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
                     "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
                     "=r"(o[14]), "=r"(o[15])
-                  : "r"(lane_addr + kOCol + 16 * c)
+                  : "r"(o_addr)
                   : "memory");
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st16(lane_addr + kOCol + 16 * c, o);
+              tmem_st16(o_addr, o);
             }
           }
           const float moff = m == -INFINITY ? 0.f : kShift - m;
           float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
 #pragma unroll
             for (int e = 32 * c; e < 32 * c + 32; e += 2) fma_pair(x[e], x[e + 1], sl2, moff);
             if (masked) {
@@ -819,13 +850,14 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
               pw[(e - 32 * c) / 2] = half2_of(x[e], x[e + 1]);
               pw[(e - 32 * c) / 2 + 1] = half2_of(x[e + 2], x[e + 3]);
             }
-            tmem_st16(s_addr + 16 * c, pw);
+            tmem_st16(s_addr + 32 * half + 16 * c, pw);
           }
           l = l * alpha + ((a0 + b0) + (a1 + b1));
           tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&bars.p_full[sb]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[sb]));
       }
       if (!alive) break;
       // All QK of the segment are complete: Q may be written for the next one while the last
@@ -833,7 +865,15 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       Segment y = s;
       const uint32_t last = u - 1;
       have = next_running(y);
-      const float sl2_next = have ? prepare_q(y) : 0.f;
+      float sl2_next = 0.f;
+      if (have && !prepare_q(y, sl2_next)) break;
+      // the row's sum over both halves
+      if (active) {
+        float* both = xch + (meets & 1) * 2 * kRows;
+        both[half * kRows + r] = l;
+        if (!meet()) break;
+        l += both[(half ^ 1) * kRows + r];
+      }
       // ---- epilogue: o = v_descale O / l, lse = m + log2 l ---------------------------------------
       if (!__all_sync(0xffffffffu,
                       (s.t1 == s.t0 + 1 ||
@@ -843,72 +883,80 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       tc_fence_after();
       const bool bad = *reinterpret_cast<volatile int*>(&bars.bad[seg & 3]) == seg + 1;
       const bool nan_v = *reinterpret_cast<volatile int*>(&bars.nan[seg & 3]) == seg + 1;
-      if (bad && lane == 0) set_status(p.status, MTPATTN_ERR_PAGE);
+      if (bad && lane == 0 && half == 0) set_status(p.status, MTPATTN_ERR_PAGE);
       const bool whole = s.t0 == 0 && s.t1 == s.nt;
       if (active) {
         const float sc = l != 0.f ? vd / l : 0.f;    // NaN stays NaN
         const int slot = 2 * blockIdx.x + (s.first ? 0 : 1);
         const int rows = min(32, s.n * p.ratio - s.m * kRows - 32 * quad);
+        const int node = rr / p.ratio;
+        const int64_t out_at = static_cast<int64_t>(s.q0 + node) * p.out_stride_tok +
+                               static_cast<int64_t>(s.h * p.ratio + rr - node * p.ratio) * p.out_stride_head;
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(lane_addr + kOCol + 32 * c, o);
-          tmem_ld_wait(o);
-          float f[32];
+        for (int c = 0; c < kHeadDim / 2 / kOutCols; ++c) {
+          const int d0 = kHeadDim / 2 * half + kOutCols * c;
+          uint32_t o[16];
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+              "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n"
+              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+                "=r"(o[14]), "=r"(o[15])
+              : "r"(lane_addr + kOCol + d0)
+              : "memory");
+          float f[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = l == 0.f || bad ? 0.f : __uint_as_float(o[e]) * sc;
+          for (int e = 0; e < 16; ++e) f[e] = l == 0.f || bad ? 0.f : __uint_as_float(o[e]) * sc;
           if (nan_v && !bad && valid) {
-            // NaN values of the nodes that this row sees, dims 32 c .. + 31
+            // NaN values of the nodes that this row sees, dims d0 .. + 15
             for (uint64_t w = word; w; w &= w - 1) {
               const int key = tree0 + __ffsll(static_cast<long long>(w)) - 1;
               if (key < s.t0 * kKeys || key >= s.t1 * kKeys) continue;
               const int page = p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + key / kPage];
-              const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim + 32 * c;
+              const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim + d0;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
+              for (int e = 0; e < 16; ++e)
                 if ((src[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fc00000);
             }
           }
           __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
+          for (int e = 0; e < 16; e += 4)
             *reinterpret_cast<float4*>(stage + lane * kStagePitch + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
           __syncwarp();
-          if (whole) {
+          if (whole) {                               // two lanes a row
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 8 * i + (lane >> 2), d = 8 * (lane & 3);
-              if (row < rows) {
-                const float* src = stage + row * kStagePitch + d;
-                const float4 fa = *reinterpret_cast<const float4*>(src);
-                const float4 fb = *reinterpret_cast<const float4*>(src + 4);
-                const __nv_bfloat162 h0 = __floats2bfloat162_rn(fa.x, fa.y), h1 = __floats2bfloat162_rn(fa.z, fa.w);
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(fb.x, fb.y), h3 = __floats2bfloat162_rn(fb.z, fb.w);
-                const int ri = s.m * kRows + 32 * quad + row;
-                const int tt = ri / p.ratio, gg = ri - tt * p.ratio;
-                *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.q0 + tt) * p.out_stride_tok +
-                                          static_cast<int64_t>(s.h * p.ratio + gg) * p.out_stride_head + 32 * c + d) =
+            for (int i = 0; i < 2; ++i) {
+              const int row = 16 * i + (lane >> 1), d = 8 * (lane & 1);
+              const int64_t at = __shfl_sync(0xffffffffu, out_at, row);
+              const float* src = stage + row * kStagePitch + d;
+              const float4 fa = *reinterpret_cast<const float4*>(src);
+              const float4 fb = *reinterpret_cast<const float4*>(src + 4);
+              const __nv_bfloat162 h0 = __floats2bfloat162_rn(fa.x, fa.y), h1 = __floats2bfloat162_rn(fa.z, fa.w);
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(fb.x, fb.y), h3 = __floats2bfloat162_rn(fb.z, fb.w);
+              if (row < rows)
+                *reinterpret_cast<uint4*>(p.out + at + d0 + d) =
                     make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
                                *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
-              }
             }
-          } else {
-            float* dst = p.o_part + (static_cast<int64_t>(slot) * kRows + 32 * quad) * kHeadDim + 32 * c;
+          } else {                                   // four lanes a row
+            float* dst = p.o_part + (static_cast<int64_t>(slot) * kRows + 32 * quad) * kHeadDim + d0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = 4 * i + (lane >> 3), d = 4 * (lane & 7);
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * i + (lane >> 2), d = 4 * (lane & 3);
               if (row < rows)
                 *reinterpret_cast<float4*>(dst + static_cast<int64_t>(row) * kHeadDim + d) =
                     *reinterpret_cast<const float4*>(stage + row * kStagePitch + d);
             }
           }
         }
-        if (!whole && valid)
+        if (!whole && valid && half == 0)
           p.lse_part[slot * kRows + r] = bad ? __uint_as_float(kBadLse)
                                              : (l != 0.f ? m + log2f(l) - kShift : -INFINITY);
       }
       tc_fence_before();
-      mbar_arrive(smem_u32(&bars.o_free));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.o_free));
       ++seg;
       s = y;
       sl2 = sl2_next;
@@ -967,15 +1015,24 @@ tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
   };
   const int g0 = piece_of(unit0), g1 = piece_of(unit0 + nt - 1);
   if (g0 == g1) return;                              // written whole
+  // lane i looks after piece g0 + i (and 32 further, ...): its slot and log-sum-exp
   auto slot_of = [&](int g) {
     return 2 * g + (unit0 <= piece_start(g, pieces, W) ? 0 : 1);
   };
+  const int n = g1 - g0 + 1;
   float M = -INFINITY;
   bool bad = false;
-  for (int g = g0 + lane; g <= g1; g += 32) {
-    const float x = __ldcg(p.lse_part + slot_of(g) * kRows + rt);
+  int slot = 0;
+  float lse = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const int sl = slot_of(g0 + i);
+    const float x = __ldcg(p.lse_part + sl * kRows + rt);
     bad |= __float_as_uint(x) == kBadLse;
     M = fmaxf(M, x);
+    if (i < 32) {
+      slot = sl;
+      lse = x;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -983,23 +1040,40 @@ tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
   float acc[8], wsum = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  if (!bad) {
-#pragma unroll 4
-    for (int g = g0; g <= g1; ++g) {
-      const int slot = slot_of(g);
-      const float x = __ldcg(p.lse_part + slot * kRows + rt);
-      const float* o = p.o_part + (static_cast<int64_t>(slot) * kRows + rt) * kHeadDim + 8 * lane;
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(o));
-      const float4 b = __ldcg(reinterpret_cast<const float4*>(o + 4));
-      if (x == -INFINITY) continue;
-      const float w = exp2_hw(x - M);                // a NaN lse makes the row NaN
-      wsum += w;
-      acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
-      acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
-      acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
-      acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
+  for (int i0 = 0; i0 < n && !bad; i0 += 32) {
+    if (i0 > 0) {
+      slot = i0 + lane < n ? slot_of(g0 + i0 + lane) : 0;
+      lse = i0 + lane < n ? __ldcg(p.lse_part + slot * kRows + rt) : -INFINITY;
+    }
+    const float weight = lse == -INFINITY ? 0.f : exp2_hw(lse - M);   // NaN makes the row NaN
+    wsum += weight;
+    const int m = min(32, n - i0);
+    for (int j0 = 0; j0 < m; j0 += 8) {              // eight pieces' loads in flight
+      float4 a[8], b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int sl = __shfl_sync(0xffffffffu, slot, (j0 + j) & 31);
+        const float* o = p.o_part + (static_cast<int64_t>(sl) * kRows + rt) * kHeadDim + 8 * lane;
+        if (j0 + j < m) {
+          a[j] = __ldcg(reinterpret_cast<const float4*>(o));
+          b[j] = __ldcg(reinterpret_cast<const float4*>(o + 4));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = __shfl_sync(0xffffffffu, weight, (j0 + j) & 31);
+        const float x = __shfl_sync(0xffffffffu, lse, (j0 + j) & 31);
+        if (j0 + j < m && x != -INFINITY) {          // (an empty piece's values are not used)
+          acc[0] = fmaf(w, a[j].x, acc[0]); acc[1] = fmaf(w, a[j].y, acc[1]);
+          acc[2] = fmaf(w, a[j].z, acc[2]); acc[3] = fmaf(w, a[j].w, acc[3]);
+          acc[4] = fmaf(w, b[j].x, acc[4]); acc[5] = fmaf(w, b[j].y, acc[5]);
+          acc[6] = fmaf(w, b[j].z, acc[6]); acc[7] = fmaf(w, b[j].w, acc[7]);
+        }
+      }
     }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   uint32_t h[4];
 #pragma unroll
