@@ -10,17 +10,16 @@
 // partial output and log-sum-exp per piece in the workspace, and tree_reduce_kernel joins them.
 // A CTA has at most two partial units, the first and the last of its piece: two slots per CTA.
 //
-// Roles (576 threads):
+// Roles (448 threads):
 //   warp 0       K: TMA loads of the K pages (two 128-byte-wide boxes a page, 128B-swizzled);
 //   warp 1       MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
-//   warps 2-9    V, two groups of four that take the 64-key half tiles in turn: warp w of a group
-//                loads page w of its half tile to registers, one ahead, widens it to f16 and
-//                stores it as PV's operand (no staging of the codes);
-//   warps 10-17  softmax: thread = query row = TMEM lane, two warps a row quarter that take 64 of a
+//   warps 2-5    V: warp w loads page w of each 64-key half tile to registers, a half tile ahead,
+//                widens it to f16 and stores it as PV's operand (no staging of the codes);
+//   warps 6-13   softmax: thread = query row = TMEM lane, two warps a row quarter that take 64 of a
 //                tile's 128 keys each and exchange their maxima; also the Q operand, and half of
 //                the output's dims each.
-// One warp an SM quarter for softmax and for V took twice the tensor cores' time (both are chains
-// of dependent work on one row, or one page), hence two of each.
+// The block's 215 KB of shared memory leave 12 KB of L1: a spilled register costs an L2 access, so
+// the thread count is what leaves the softmax its 128 registers.
 //
 // Precision.  K enters as its e4m3 codes, Q as the sum of two e4m3 terms of x = q 2^a (a per row,
 // max |x| in [128, 256)): hi = e4m3(x), lo = e4m3(x - hi), both products into one accumulator.  A
@@ -58,13 +57,13 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTreeThreads = 576;
+constexpr int kTreeThreads = 448;
 constexpr int kRows = 128;                         // query rows per tile
 constexpr int kKeys = 128;                         // keys per tile
 constexpr int kTilePages = kKeys / kPage;          // 8
 constexpr int kHalfKeys = 64;                      // V is staged half a tile at a time
-constexpr int kVGroup = 4;                         // V warps of a group, a page each
-constexpr int kWarpV = 2, kWarpSoft = kWarpV + 2 * kVGroup, kSoftWarps = 8;
+constexpr int kVWarps = 4;                         // a page of a half tile each
+constexpr int kWarpV = 2, kWarpSoft = kWarpV + kVWarps, kSoftWarps = 8;
 constexpr int kQHalf = kRows * 128;                // 128 of the 256 dims of one Q term
 constexpr int kQTerm = 2 * kQHalf;                 // 32 KB: hi, then lo
 constexpr int kKHalf = kKeys * 128;
@@ -72,7 +71,7 @@ constexpr int kKTile = 2 * kKHalf;                 // 32 KB per stage
 constexpr int kKStages = 2;
 constexpr int kVAtom = kHalfKeys * 128;            // 64 dims of 64 keys, f16
 constexpr int kVStage = 4 * kVAtom;                // 32 KB per stage
-constexpr int kVStages = 2;                        // one per group
+constexpr int kVStages = 2;
 constexpr int kOutCols = 16;                       // output columns staged at a time
 constexpr int kStagePitch = 20;                    // floats a row there (eight rows: all 32 banks)
 constexpr int kOffQ = 0;
@@ -81,7 +80,8 @@ constexpr int kOffV = kOffK + kKStages * kKTile;
 constexpr int kOffOut = kOffV + kVStages * kVStage;
 constexpr int kOffXch = kOffOut + kSoftWarps * 32 * kStagePitch * 4;
 constexpr int kOffBar = kOffXch + 2 * 2 * kRows * 4;   // exchange: [parity][half][row] floats
-constexpr int kSmemTree = kOffBar + 512 + 1024;    // + alignment slack
+constexpr int kBarBytes = 1024;
+constexpr int kSmemTree = kOffBar + kBarBytes + 1024;  // + alignment slack
 static_assert(kSmemTree <= 232448, "shared-memory layout");
 constexpr int kSCols = 128, kOCol = 256, kTmemCols = 512;
 constexpr float kTau = 6.f, kShift = 8.f;
@@ -111,17 +111,27 @@ struct TreeAttnParams {
   float* lse_part;           // [ctas][2][128]
 };
 
+struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
+  int b, h, q0, n, L;
+  int m, t0, t1, nt, T;
+  int first;                 // it starts the CTA's piece
+  int end;                   // no segment: the piece is done
+};
+constexpr int kSegRing = 8;
+
 struct TreeBars {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_ready, o_free, final_mma;
   uint64_t xch[4][2];        // a row quarter's two warps meet, in turn on two barriers
+  uint64_t seg_full[kSegRing], seg_free[kSegRing];
+  Segment seg[kSegRing];     // written by the K producer, given back by the softmax warps
   uint32_t tmem_base;
   int32_t abort;
   int32_t bad[4];            // [segment & 3]: segment + 1 if it met a page outside the pool
   int32_t nan[4];            // the same if a tree node's V holds a NaN code
 };
-static_assert(sizeof(TreeBars) <= 512, "barrier block");
+static_assert(sizeof(TreeBars) <= kBarBytes, "barrier block");
 
 // ---- the line of key tiles ---------------------------------------------------------------------
 
@@ -168,24 +178,12 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
   return x;
 }
 
-__device__ __forceinline__ int line_length(const TreeAttnParams& p, int lane) {
-  int w = 0;
-  for (int b0 = 0; b0 < p.num_seqs; b0 += 32) w += seq_at(p, b0 + lane).w;
-  return __reduce_add_sync(0xffffffffu, w);
-}
-
 // The line of W is cut into min(CTAs, W) pieces, so none is empty.  First place of piece g:
 __device__ __forceinline__ int piece_start(int g, int pieces, int W) {
   return static_cast<int>(static_cast<int64_t>(g) * W / pieces);
 }
 
-struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
-  int b, h, m, q0, n, L, err;
-  int t0, t1, nt, T;
-  bool first;                // it starts the CTA's piece
-};
-
-// A warp's walk over the units of its CTA's piece; 32 sequences are held, one a lane.
+// The K producer's walk over the units of its CTA's piece; 32 sequences are held, one a lane.
 struct Walker {
   int pos, hi, lo;
   int b0, before;            // the held sequences, and the line before the first of them
@@ -197,22 +195,32 @@ struct Walker {
     upto = warp_scan(mine.w, lane);
   }
   __device__ __forceinline__ void start(const TreeAttnParams& p, int lane) {
+    int W = 0;
     b0 = before = 0;
     hold(p, lane);
-    const int W = p.num_seqs <= 32 ? __shfl_sync(0xffffffffu, upto, 31) : line_length(p, lane);
+    if (p.num_seqs <= 32) {
+      W = __shfl_sync(0xffffffffu, upto, 31);
+    } else {
+#pragma unroll 1
+      for (int c0 = 0; c0 < p.num_seqs; c0 += 32) W += seq_at(p, c0 + lane).w;
+      W = __reduce_add_sync(0xffffffffu, W);
+    }
     const int pieces = min(p.ctas, W);
     const int g = blockIdx.x;
     lo = pos = g < pieces ? piece_start(g, pieces, W) : W;
     hi = g < pieces ? piece_start(g + 1, pieces, W) : W;
   }
-  __device__ __forceinline__ bool next(const TreeAttnParams& p, int lane, Segment& s) {
-    if (pos >= hi) return false;
+  // The next segment; s.end if there is none.  Returns the sequence's error bits.
+  __device__ __forceinline__ int next(const TreeAttnParams& p, int lane, Segment& s) {
+    s.end = 1;
+    if (pos >= hi) return 0;
+#pragma unroll 1
     while (true) {
       const int all = __shfl_sync(0xffffffffu, upto, 31);
       if (pos < before + all) break;
       before += all;
       b0 += 32;
-      if (b0 >= p.num_seqs) return false;           // lengths changed under the call
+      if (b0 >= p.num_seqs) return 0;               // lengths changed under the call
       hold(p, lane);
     }
     const int at = pos - before;
@@ -223,7 +231,6 @@ struct Walker {
     s.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
     s.n = __shfl_sync(0xffffffffu, mine.n, f);
     s.L = __shfl_sync(0xffffffffu, mine.L, f);
-    s.err = __shfl_sync(0xffffffffu, mine.err, f);
     const int unit = in / nt;
     s.h = unit / T;
     s.m = unit - s.h * T;
@@ -232,19 +239,14 @@ struct Walker {
     s.t0 = in - unit * nt;
     s.t1 = min(nt, s.t0 + hi - pos);
     s.first = pos == lo;
+    s.end = 0;
     pos += s.t1 - s.t0;
-    return true;
-  }
-  // the next segment that has keys to be looked at
-  __device__ __forceinline__ bool next_running(const TreeAttnParams& p, int lane, Segment& s) {
-    while (next(p, lane, s))
-      if (!s.err) return true;
-    return false;
+    return __shfl_sync(0xffffffffu, mine.err, f);
   }
 };
 
-__device__ __forceinline__ int tile_pages(const Segment& s, int t) {   // pages of key tile t
-  return min(kTilePages, (s.L + kPage - 1) / kPage - t * kTilePages);
+__device__ __forceinline__ int tile_pages(int L, int t) {   // pages of key tile t
+  return min(kTilePages, (L + kPage - 1) / kPage - t * kTilePages);
 }
 
 // ---- arithmetic --------------------------------------------------------------------------------
@@ -307,9 +309,18 @@ __device__ __forceinline__ void two_terms(float x0, float x1, float x2, float x3
       : "=r"(hi), "=r"(lo)
       : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
 }
-// 0xff in every byte of w that is a NaN code
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+// mbar_wait of sm100.cuh in fewer instructions (there are many waits, and the loops of all the
+// roles share one instruction cache): a 32-bit clock, in which kWaitCycles fits.
+static_assert(kWaitCycles < (1ll << 32), "32-bit clock");
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (static_cast<uint32_t>(clock()) - t0 > static_cast<uint32_t>(kWaitCycles)) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
 }
 
 // tcgen05.mma kind::f16 (f16 x f16 -> f32), A from tensor memory, B from shared memory.
@@ -342,7 +353,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       mbar_init(smem_u32(&bars.k_empty[i]), 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(smem_u32(&bars.v_full[i]), kVGroup);
+      mbar_init(smem_u32(&bars.v_full[i]), kVWarps);
       mbar_init(smem_u32(&bars.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -353,6 +364,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     mbar_init(smem_u32(&bars.q_ready), kSoftWarps);
     mbar_init(smem_u32(&bars.o_free), kSoftWarps);
     for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&bars.xch[i >> 1][i & 1]), 2);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(smem_u32(&bars.seg_full[i]), 1);
+      mbar_init(smem_u32(&bars.seg_free[i]), kSoftWarps);
+    }
     mbar_init(smem_u32(&bars.final_mma), 1);
     for (int i = 0; i < 4; ++i) bars.bad[i] = bars.nan[i] = 0;
     bars.abort = 0;
@@ -367,41 +382,62 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-  Walker walk;
-  Segment s;
-  walk.start(p, lane);
+  // Segment e as the K producer published it; false after an abort.
+  auto seg_wait = [&](int e) -> bool {
+    return __all_sync(0xffffffffu, wait_for(smem_u32(&bars.seg_full[e % kSegRing]),
+                                             (e / kSegRing) & 1, abort_flag));
+  };
 
   if (warp == 0) {
-    // ======================================== K producer ==========================================
+    // ============================== K producer, and the CTA's walk ================================
     if (lane == 0) prefetch_tmap(&p.tmap_k);
-    if (blockIdx.x == 0)                            // sequences whose rows are not known
-      for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-        const Seq x = seq_at(p, b0 + lane);
-        if (x.err && x.T == 0) set_status(p.status, x.err);
-      }
+    Walker walk;
+    walk.start(p, lane);
     // keys that other row tiles will read again stay in L2
     const uint64_t once = l2_policy_evict_first();
     uint64_t again;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
     uint32_t u = 0;
-    bool stop = false;
-    while (!stop && walk.next_running(p, lane, s)) {
+    int e = 0;
+    bool ok = true;
+    while (ok) {
+      Segment s;
+      const int err = walk.next(p, lane, s);
+      if (err && !s.end) {
+        // zeros for the rows of a sequence that cannot be computed, here: it has no key tiles
+        if (lane == 0) set_status(p.status, err);
+        const int rows = min(kRows, s.n * p.ratio - s.m * kRows);
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i) {
+          const int rr = s.m * kRows + i, t = rr / p.ratio;
+          reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.q0 + t) * p.out_stride_tok +
+                                   static_cast<int64_t>(s.h * p.ratio + rr - t * p.ratio) * p.out_stride_head)[lane] =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      ok = __all_sync(0xffffffffu, wait_for(smem_u32(&bars.seg_free[e % kSegRing]),
+                                             ((e / kSegRing) & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (lane == 0) {
+        bars.seg[e % kSegRing] = s;
+        mbar_arrive(smem_u32(&bars.seg_full[e % kSegRing]));
+      }
+      if (s.end) break;
+      ++e;
       const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
       const uint64_t pol = s.T == 1 ? once : again;
+#pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++u) {
-        const int np = tile_pages(s, t), st = u % kKStages;
+        const int np = tile_pages(s.L, t), st = u % kKStages;
         const int phys = lane < np ? bt[t * kTilePages + lane] : 0;
-        bool ok = true;
         const uint32_t fb = smem_u32(&bars.k_full[st]);
         if (lane == 0) {
-          ok = mbar_wait(smem_u32(&bars.k_empty[st]), ((u / kKStages) & 1) ^ 1, abort_flag);
+          ok = wait_for(smem_u32(&bars.k_empty[st]), ((u / kKStages) & 1) ^ 1, abort_flag);
           if (ok) mbar_arrive_expect_tx(fb, np * 2 * 2048);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          stop = true;
-          break;
-        }
+        if (!ok) break;
         if (lane < np) {                            // a page outside the pool reads as zeros
           const uint32_t dst = smem_u32(base + kOffK + st * kKTile) + lane * 2048;
           tma_load_4d(dst, &p.tmap_k, fb, 0, s.h, 0, phys, pol);
@@ -409,11 +445,17 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         }
       }
     }
+    if (blockIdx.x == 0)                            // sequences whose rows are not known
+#pragma unroll 1
+      for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+        const Seq x = seq_at(p, b0 + lane);
+        if (x.err && x.T == 0) set_status(p.status, x.err);
+      }
     // never leave with copies in flight
     if (lane == 0) {
       volatile int no_abort = 0;
       for (uint32_t k = 1; k <= kKStages && k <= u; ++k)
-        mbar_wait(smem_u32(&bars.k_full[(u - k) % kKStages]), ((u - k) / kKStages) & 1, &no_abort);
+        wait_for(smem_u32(&bars.k_full[(u - k) % kKStages]), ((u - k) / kKStages) & 1, &no_abort);
     }
   } else if (warp == 1) {
     // ======================================== MMA issuer ==========================================
@@ -424,7 +466,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     const uint64_t v_desc = sdesc_sw128(smem_u32(base + kOffV), kVAtom, 1024);
     const bool leader = elect_one();
     auto wait_all = [&](uint64_t& bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abort_flag));
+      return __all_sync(0xffffffffu, wait_for(smem_u32(&bar), parity, abort_flag));
     };
     uint32_t u = 0, v = 0;                          // key tiles, half tiles of V
     auto issue_pv = [&](uint32_t ut, int np, bool first) -> bool {
@@ -448,13 +490,26 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       __syncwarp();
       return true;
     };
-    bool ok = true;
-    uint32_t seg = 0;
-    while (ok && walk.next_running(p, lane, s)) {
-      ok = wait_all(bars.q_ready, seg & 1);
-      for (int t = s.t0; ok && t < s.t1; ++t, ++u) {
+    // A turn is QK of a tile and the products of the tile before it; a segment's last products
+    // go out in a turn of their own, before the next segment is waited for.
+    int seg = 0, t0 = 0, t1 = 0, t = 0, L = 0;
+    int pv_pages = 0;                               // of tile u - 1, 0: nothing outstanding
+    bool pv_first = false;                          // ... which starts its segment
+    while (true) {
+      const bool more = t < t1 || pv_pages == 0;
+      if (t >= t1 && more) {
+        if (!seg_wait(seg)) break;
+        const Segment& s = bars.seg[seg % kSegRing];
+        if (s.end) break;
+        t = t0 = s.t0;
+        t1 = s.t1;
+        L = s.L;
+        if (!wait_all(bars.q_ready, seg & 1)) break;
+        ++seg;
+      }
+      if (more) {
         const int st = u % kKStages;
-        if (!wait_all(bars.k_full[st], (u / kKStages) & 1)) { ok = false; break; }
+        if (!wait_all(bars.k_full[st], (u / kKStages) & 1)) break;
         tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -468,26 +523,28 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
           mma_commit(smem_u32(&bars.k_empty[st]));
         }
         __syncwarp();
-        if (t > s.t0) {
-          // the segment's first product overwrites O: the epilogue before it has read it
-          if (t == s.t0 + 1 && seg > 0 && !wait_all(bars.o_free, (seg - 1) & 1)) { ok = false; break; }
-          ok = issue_pv(u - 1, tile_pages(s, t - 1), t == s.t0 + 1);
-        }
       }
-      if (!ok) break;
-      if (s.t1 == s.t0 + 1 && seg > 0 && !wait_all(bars.o_free, (seg - 1) & 1)) break;
-      if (!issue_pv(u - 1, tile_pages(s, s.t1 - 1), s.t1 == s.t0 + 1)) break;
-      ++seg;
+      if (pv_pages > 0) {
+        // a segment's first products overwrite O: the epilogue before it has read it
+        if (pv_first && seg > 1 && !wait_all(bars.o_free, (seg - 2) & 1)) break;
+        if (!issue_pv(u - 1, pv_pages, pv_first)) break;
+      }
+      pv_pages = more ? tile_pages(L, t) : 0;
+      if (more) {
+        pv_first = t == t0;
+        ++t;
+        ++u;
+      }
     }
     if (leader) mma_commit(smem_u32(&bars.final_mma));
     __syncwarp();
     volatile int no_abort = 0;
-    mbar_wait(smem_u32(&bars.final_mma), 0, &no_abort);
+    wait_for(smem_u32(&bars.final_mma), 0, &no_abort);
   } else if (warp < kWarpSoft) {
     // ========================================= V loads ============================================
     // A page is 16 bytes x 8 a lane: load i holds key 2 i + lane / 16 of the warp's page,
     // dims 16 (lane % 16) .. + 15, two 16-byte chunks of f16 in 64-dim atom (lane % 16) / 4.
-    const int w = (warp - kWarpV) & (kVGroup - 1), group = (warp - kWarpV) / kVGroup;
+    const int w = warp - kWarpV;
     const int c16 = lane & 15, krow = lane >> 4;
     const int atom = c16 >> 2, ch = 2 * (c16 & 3);
     // lanes of odd atoms store their second chunk first: the eight lanes of a store phase then
@@ -498,63 +555,70 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       bool pages;            // the warp has a page in this half tile
       bool bad;              // ... outside the pool
       int tree;              // first key of the page that belongs to the tree (16: none)
+      int seg;
     };
-    bool more = walk.next_running(p, lane, s);
-    int hf = more ? 2 * s.t0 : 0, hf_end = 0;       // half tiles of the segment (4 pages each)
-    int seg = 0;
-    auto seg_end = [&]() { return min(2 * s.t1, ((s.L + kPage - 1) / kPage + 3) / 4); };
-    if (more) hf_end = seg_end();
-    int ent = 0, ent_at = -32;                      // lane l: the table entry of half tile ent_at + l
+    // The half tiles (4 pages each) in order.
+    int seg = -1, hf = 0, hf_end = 0;               // the segment at hand and the next half tile in it
+    int L = 0, tree0 = 0;
+    int64_t head = 0;                               // byte offset of the segment's head and this lane
+    const int32_t* bt = nullptr;
+    int ent = 0, ent_at = 0;                        // lane l: the table entry of half tile ent_at + l
+    const int64_t row_bytes = static_cast<int64_t>(p.hkv) * kHeadDim;
+    // To the next half tile, into the next segment if need be.  1: there; 0: the piece is done;
+    // -1: the next segment is not known yet (only if !wait).
+    auto seek = [&](bool wait) -> int {
+      if (++hf < hf_end) return 1;
+      hf = hf_end;
+      const int e = seg + 1;
+      if (!wait && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bars.seg_full[e % kSegRing]), (e / kSegRing) & 1)))
+        return -1;
+      if (!seg_wait(e)) return 0;
+      const Segment& s = bars.seg[e % kSegRing];
+      if (s.end) return 0;
+      seg = e;
+      L = s.L;
+      tree0 = s.L - s.n;
+      head = (static_cast<int64_t>(krow) * p.hkv + s.h) * kHeadDim + 16 * c16;
+      bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
+      hf = 2 * s.t0;
+      hf_end = min(2 * s.t1, ((L + kPage - 1) / kPage + 3) / 4);
+      ent_at = hf - 32;
+      return 1;
+    };
     auto load = [&](Half& a) {
-      if (hf >= ent_at + 32 || hf < ent_at) {
+      if (hf >= ent_at + 32) {
         ent_at = hf;
         const int pg = 4 * (hf + lane) + w;
-        ent = pg < (s.L + kPage - 1) / kPage
-                  ? p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + pg] : 0;
+        ent = pg < (L + kPage - 1) / kPage ? bt[pg] : 0;
       }
       const int page = __shfl_sync(0xffffffffu, ent, hf - ent_at);
-      const int pg = 4 * hf + w;
-      const int left = s.L - pg * kPage;            // keys of the page that belong to the sequence
+      const int key0 = (4 * hf + w) * kPage;
+      const int left = L - key0;                    // keys of the page that belong to the sequence
       a.pages = left > 0;
-      a.tree = min(16, max(0, s.L - s.n - pg * kPage));
+      a.tree = min(16, max(0, tree0 - key0));
+      a.seg = seg;
       const bool good = page >= 0 && page < p.num_pages;
       a.bad = a.pages && !good;
-      const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + krow) * p.hkv + s.h) * kHeadDim + 16 * c16;
+      const uint8_t* src = p.v_cache + page * (kPage * row_bytes) + head;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         a.x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (good && 2 * i + krow < left) {
+        if (good && 2 * i + krow < left)
           asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                        : "=r"(a.x[i].x), "=r"(a.x[i].y), "=r"(a.x[i].z), "=r"(a.x[i].w)
-                       : "l"(src + static_cast<int64_t>(2 * i) * p.hkv * kHeadDim));
-        }
+                       : "l"(src + 2 * i * row_bytes));
       }
     };
-    const int st = group;
-    uint32_t parity = 1;
-    auto store = [&](Half& a, int sg) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.v_empty[st]), parity, abort_flag)))
+    uint32_t v = 0;
+    auto store = [&](Half& a) -> bool {
+      const int st = v % kVStages;
+      if (!__all_sync(0xffffffffu, wait_for(smem_u32(&bars.v_empty[st]), ((v / kVStages) & 1) ^ 1, abort_flag)))
         return false;
-      parity ^= 1;
+      ++v;
       // Notes are made behind the wait: a slot of the four is then not one that the epilogue has
       // yet to read (this warp is two half tiles ahead of it at most).
-      if (a.bad && lane == 0) bars.bad[sg & 3] = sg + 1;
+      if (a.bad && lane == 0) bars.bad[a.seg & 3] = a.seg + 1;
       if (a.pages) {
-        if (a.tree < 16) {                          // NaN codes of tree nodes: 0, and noted
-          bool any = false;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (2 * i + krow < a.tree) continue;
-            uint32_t* x = reinterpret_cast<uint32_t*>(&a.x[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t bytes = nan_bytes(x[e]);
-              any |= bytes != 0;
-              x[e] &= ~bytes;
-            }
-          }
-          if (any) bars.nan[sg & 3] = sg + 1;
-        }
         unsigned char* dst = base + kOffV + st * kVStage + atom * kVAtom + w * 16 * 128;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -568,42 +632,61 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
           *reinterpret_cast<uint4*>(dst + (swap ? o1 : o0)) = swap ? c1 : c0;
           *reinterpret_cast<uint4*>(dst + (swap ? o0 : o1)) = swap ? c0 : c1;
         }
+        if (a.tree < 16) {                          // NaN codes of tree nodes: noted, and 0 instead
+          uint32_t any = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (2 * i + krow >= a.tree)
+              any |= (((a.x[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((a.x[i].y & 0x7f7f7f7fu) + 0x01010101u) |
+                      ((a.x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((a.x[i].w & 0x7f7f7f7fu) + 0x01010101u));
+          if (any & 0x80808080u) {
+            bars.nan[a.seg & 3] = a.seg + 1;
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {          // this lane's chunks, as they were stored
+              const int key = 2 * (i >> 1) + krow;
+              uint32_t* x = reinterpret_cast<uint32_t*>(dst + key * 128 + (((ch + (i & 1)) ^ (key & 7)) << 4));
+              if (key >= a.tree)
+#pragma unroll 1
+                for (int d = 0; d < 4; ++d) {
+                  const uint32_t h = x[d];
+                  x[d] = ((h & 0x7fffu) > 0x7c00u ? 0u : h & 0xffffu) |
+                         ((h & 0x7fff0000u) > 0x7c000000u ? 0u : h & 0xffff0000u);
+                }
+            }
+          }
+        }
         fence_proxy_async_smem();                   // visible to the tensor cores behind v_full
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.v_full[st]));
       return true;
     };
-    auto advance = [&]() {
-      if (++hf >= hf_end) {
-        more = walk.next_running(p, lane, s);
-        if (more) {
-          hf = 2 * s.t0;
-          hf_end = seg_end();
-          ent_at = -32;
-          ++seg;
-        }
-      }
-    };
     // Two buffers in turn, so that one's loads are in flight while the other is widened (a copy
-    // between them would wait for the loads).
+    // between them would wait for the loads).  A segment that is not known yet is waited for only
+    // with nothing left to store: what publishes it may itself wait for these stores.
     Half buf0, buf1;
-    int seg0 = 0, seg1 = 0;
-    auto fetch = [&](Half& a, int& sg) -> bool {
-      if (!more) return false;
-      load(a);
-      sg = seg;
-      advance();                                    // past this group's and the other one's
-      if (more) advance();
-      return true;
+    auto fetch = [&](Half& a, bool wait) -> int {
+      const int r = seek(wait);
+      if (r > 0) load(a);
+      return r;
     };
-    if (group == 1 && more) advance();
-    bool have0 = fetch(buf0, seg0), have1;
-    while (have0) {
-      have1 = fetch(buf1, seg1);
-      if (!store(buf0, seg0) || !have1) break;
-      have0 = fetch(buf0, seg0);
-      if (!store(buf1, seg1)) break;
+    bool full0 = false, full1 = false, good = true;
+    while (good) {
+      int r;
+      do {
+        r = fetch(buf0, !full1);
+        if (full1) good = store(buf1);
+        full1 = false;
+      } while (r < 0 && good);
+      if (r <= 0 || !good) break;
+      full0 = true;
+      do {
+        r = fetch(buf1, !full0);
+        if (full0) good = store(buf0);
+        full0 = false;
+      } while (r < 0 && good);
+      if (r <= 0) break;
+      full1 = true;
     }
   } else {
     // ======================================= softmax (rows) =======================================
@@ -613,10 +696,13 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quad) << 16);
     float* stage = reinterpret_cast<float*>(base + kOffOut) + (warp - kWarpSoft) * 32 * kStagePitch;
     float* xch = reinterpret_cast<float*>(base + kOffXch);
-    const float sl = p.scale_log2 * __ldg(p.k_descale);
+    // A negative factor goes into Q, so that the factors are positive; one of 0 is taken as the
+    // smallest float, under which all logits are alike.
+    const float sl_in = p.scale_log2 * __ldg(p.k_descale);
+    const float sl = fmaxf(fabsf(sl_in), 1.17549435e-38f);
+    const uint32_t flip = sl_in < 0.f ? 0x80000000u : 0u;
     const float vd = __ldg(p.v_descale);
     uint32_t u = 0;                                 // key tiles so far
-    int seg = 0;
     // The two warps of a row quarter meet: what each wrote to shared memory before, the other
     // sees after.  Bounded like every wait.
     uint32_t meets = 0;
@@ -624,30 +710,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       const uint32_t bar = smem_u32(&bars.xch[quad][meets & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, (meets >> 1) & 1, abort_flag));
+      const bool ok = __all_sync(0xffffffffu, wait_for(bar, (meets >> 1) & 1, abort_flag));
       ++meets;
       return ok;
     };
 
-    // Zeros for the rows of a sequence that cannot be computed.
-    auto put_zeros = [&](const Segment& y) {
-      const int rr = y.m * kRows + r;
-      if (rr < y.n * p.ratio) {
-        const int t = rr / p.ratio, g = rr - t * p.ratio;
-        uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(y.q0 + t) * p.out_stride_tok +
-                                              static_cast<int64_t>(y.h * p.ratio + g) * p.out_stride_head);
-#pragma unroll 1
-        for (int i = 0; i < kHeadDim / 16; ++i) dst[half * (kHeadDim / 16) + i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    auto next_running = [&](Segment& y) -> bool {
-      while (walk.next(p, lane, y)) {
-        if (!y.err) return true;
-        put_zeros(y);
-        if (lane == 0 && warp == kWarpSoft) set_status(p.status, y.err);
-      }
-      return false;
-    };
     // Half of the row quarter's rows as two e4m3 terms into the Q operand, a row at a time by the
     // whole warp (8 dims a lane); their factors from raw products to log2 units (NaN for a row that
     // is not finite) to the exchange, from where `factor` gets this thread's row's.
@@ -683,7 +750,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             const int e8 = static_cast<int>(top >> 23);              // exponent field
             // 2^a takes the largest into [128, 256), as far as a = 126 does
             const int a = top == 0u ? 0 : min(126, 134 - e8);
-            const float f = __int_as_float((a + 127) << 23);
+            const float f = __uint_as_float(static_cast<uint32_t>(a + 127) << 23 | flip);
             uint32_t hi[2], lo[2];
             two_terms(__uint_as_float(ww[0] << 16) * f, __uint_as_float(ww[0] & 0xffff0000u) * f,
                       __uint_as_float(ww[1] << 16) * f, __uint_as_float(ww[1] & 0xffff0000u) * f, hi[0], lo[0]);
@@ -694,8 +761,9 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
             if (lane == row)
-              to[row0 + row] = e8 == 255 ? __int_as_float(0x7fc00000)
-                                         : sl * __int_as_float((127 - a) << 23);
+              to[row0 + row] = e8 == 255 || sl_in != sl_in
+                                   ? __int_as_float(0x7fc00000)
+                                   : fmaxf(sl * __int_as_float((127 - a) << 23), 1.17549435e-38f);
           }
         }
         fence_proxy_async_smem();
@@ -707,29 +775,141 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       return true;
     };
 
-    bool have = next_running(s), alive = true;
-    float sl2 = 0.f;
-    if (have) alive = prepare_q(s, sl2);
-    while (have && alive) {
-      const int rr = s.m * kRows + r;
-      const bool valid = rr < s.n * p.ratio;
-      const bool active = __any_sync(0xffffffffu, valid);
-      uint64_t word = 0;
-      if (valid) word = p.mask[s.q0 + rr / p.ratio];
-      if (s.n < 64) word &= (1ull << s.n) - 1ull;
-      const int tree0 = s.L - s.n;                  // first key of the tree
-      float m = -INFINITY, l = 0.f;
-      for (int t = s.t0; t < s.t1; ++t, ++u) {
+    float m = -INFINITY, l = 0.f;                   // of this thread's row in the segment at hand
+    uint64_t word = 0;                              // the tree nodes it sees
+    bool valid = false, active = false, nan_row = false, alive = true;
+    // A turn: the next segment's Q while the last products of the one before run, that one's
+    // epilogue, then the segment's tiles.  The first turn has no epilogue, the last nothing else.
+#pragma unroll 1
+    for (int e = 0; alive; ++e) {
+      if (!seg_wait(e)) break;
+      const Segment& y = bars.seg[e % kSegRing];
+      const bool end = y.end != 0;
+      float sl2_next = 0.f;
+      if (!end && !prepare_q(y, sl2_next)) break;
+      if (e > 0) {
+        const Segment& s = bars.seg[(e - 1) % kSegRing];
+        // the row's sum over both halves
+        if (active) {
+          float* both = xch + (meets & 1) * 2 * kRows;
+          both[half * kRows + r] = l;
+          if (!meet()) break;
+          l += both[(half ^ 1) * kRows + r];
+          if (nan_row && l != 0.f) l = __int_as_float(0x7fc00000);
+        }
+        const uint32_t last = u - 1;
+        // ---- epilogue: o = v_descale O / l, lse = m + log2 l ---------------------------------------
+        if (!__all_sync(0xffffffffu,
+                        (s.t1 == s.t0 + 1 ||
+                         wait_for(smem_u32(&bars.pv_done[(last - 1) & 1]), ((last - 1) >> 1) & 1, abort_flag)) &&
+                            wait_for(smem_u32(&bars.pv_done[last & 1]), (last >> 1) & 1, abort_flag)))
+          break;
+        tc_fence_after();
+        const bool bad = *reinterpret_cast<volatile int*>(&bars.bad[(e - 1) & 3]) == e;
+        const bool nan_v = *reinterpret_cast<volatile int*>(&bars.nan[(e - 1) & 3]) == e;
+        if (bad && lane == 0 && half == 0) set_status(p.status, MTPATTN_ERR_PAGE);
+        const bool whole = s.t0 == 0 && s.t1 == s.nt;
+        if (active) {
+          const float sc = l != 0.f ? vd / l : 0.f;    // NaN stays NaN
+          const int slot = 2 * blockIdx.x + (s.first ? 0 : 1);
+          const int rows = min(32, s.n * p.ratio - s.m * kRows - 32 * quad);
+          const int rr = s.m * kRows + r, node = rr / p.ratio;
+          const int64_t out_at = static_cast<int64_t>(s.q0 + node) * p.out_stride_tok +
+                                 static_cast<int64_t>(s.h * p.ratio + rr - node * p.ratio) * p.out_stride_head;
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim / 2 / kOutCols; ++c) {
+            const int d0 = kHeadDim / 2 * half + kOutCols * c;
+            uint32_t o[16];
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+                "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n"
+                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                  "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+                  "=r"(o[14]), "=r"(o[15])
+                : "r"(lane_addr + kOCol + d0)
+                : "memory");
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = l == 0.f || bad ? 0.f : __uint_as_float(o[i]) * sc;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(stage + lane * kStagePitch + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+            if (nan_v && !bad && valid) {
+              // NaN values of the nodes that this row sees, dims d0 .. + 15
+#pragma unroll 1
+              for (uint64_t w = word; w; w &= w - 1) {
+                const int key = s.L - s.n + __ffsll(static_cast<long long>(w)) - 1;
+                if (key < s.t0 * kKeys || key >= s.t1 * kKeys) continue;
+                const int page = p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + key / kPage];
+                const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim + d0;
+#pragma unroll 1
+                for (int d = 0; d < kOutCols; ++d)
+                  if ((src[d] & 0x7f) == 0x7f) stage[lane * kStagePitch + d] = __int_as_float(0x7fc00000);
+              }
+            }
+            __syncwarp();
+            if (whole) {                               // two lanes a row
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int row = 16 * i + (lane >> 1), d = 8 * (lane & 1);
+                const int64_t at = __shfl_sync(0xffffffffu, out_at, row);
+                const float* src = stage + row * kStagePitch + d;
+                const float4 fa = *reinterpret_cast<const float4*>(src);
+                const float4 fb = *reinterpret_cast<const float4*>(src + 4);
+                const __nv_bfloat162 h0 = __floats2bfloat162_rn(fa.x, fa.y), h1 = __floats2bfloat162_rn(fa.z, fa.w);
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(fb.x, fb.y), h3 = __floats2bfloat162_rn(fb.z, fb.w);
+                if (row < rows)
+                  *reinterpret_cast<uint4*>(p.out + at + d0 + d) =
+                      make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                                 *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
+              }
+            } else {                                   // four lanes a row
+              float* dst = p.o_part + (static_cast<int64_t>(slot) * kRows + 32 * quad) * kHeadDim + d0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 8 * i + (lane >> 2), d = 4 * (lane & 3);
+                if (row < rows)
+                  *reinterpret_cast<float4*>(dst + static_cast<int64_t>(row) * kHeadDim + d) =
+                      *reinterpret_cast<const float4*>(stage + row * kStagePitch + d);
+              }
+            }
+          }
+          if (!whole && valid && half == 0)
+            p.lse_part[slot * kRows + r] = bad ? __uint_as_float(kBadLse)
+                                               : (l != 0.f ? m + log2f(l) - kShift : -INFINITY);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars.o_free));
+          mbar_arrive(smem_u32(&bars.seg_free[(e - 1) % kSegRing]));
+        }
+      }
+      if (end) break;
+      const int rr = y.m * kRows + r;
+      valid = rr < y.n * p.ratio;
+      active = __any_sync(0xffffffffu, valid);
+      word = valid ? p.mask[y.q0 + rr / p.ratio] : 0ull;
+      if (y.n < 64) word &= (1ull << y.n) - 1ull;
+      const int tree0 = y.L - y.n;                  // first key of the tree
+      const int t0 = y.t0, t1 = y.t1;
+      nan_row = sl2_next != sl2_next;
+      const float sl2 = nan_row ? 1.f : sl2_next;
+      m = -INFINITY;
+      l = 0.f;
+#pragma unroll 1
+      for (int t = t0; t < t1; ++t, ++u) {
         const uint32_t sb = u & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.s_full[sb]), (u >> 1) & 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, wait_for(smem_u32(&bars.s_full[sb]), (u >> 1) & 1, abort_flag))) {
           alive = false;
           break;
         }
         tc_fence_after();
         // Every phase of pv_done is waited for in its turn, as parities demand; this one is long
         // complete, its products having been issued before the QK that s_full stands for.
-        if (t > s.t0 + 1 &&
-            !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.pv_done[u & 1]), ((u - 2) >> 1) & 1, abort_flag))) {
+        if (t > t0 + 1 &&
+            !__all_sync(0xffffffffu, wait_for(smem_u32(&bars.pv_done[u & 1]), ((u - 2) >> 1) & 1, abort_flag))) {
           alive = false;
           break;
         }
@@ -757,33 +937,23 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             if (st < 0) return (static_cast<uint32_t>(word) << -st) | ((1u << -st) - 1u);
             return st < 64 ? static_cast<uint32_t>(word >> st) : 0u;
           };
-          const float sgn = sl2 < 0.f ? -1.f : 1.f;  // the largest scaled logit: the row's factor
-          if (masked) {                              // may be negative
-            const float none = -INFINITY * sgn;
+          if (masked) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const uint32_t bits = seen(c);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!((bits >> e) & 1u)) x[32 * c + e] = none;
+                if (!((bits >> e) & 1u)) x[32 * c + e] = -INFINITY;
             }
           }
-          float top;
-          if (__all_sync(0xffffffffu, !(sl2 < 0.f))) {
-            float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+          float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
 #pragma unroll
-            for (int e = 4; e < 64; e += 4) {
-              a = max3(a, x[e], x[e + 1]);
-              b = max3(b, x[e + 2], x[e + 3]);
-            }
-            top = fmaxf(a, b) * sl2;
-          } else {
-            float a = x[0] * sgn;
-#pragma unroll
-            for (int e = 1; e < 64; ++e) a = fmaxf(a, x[e] * sgn);
-            top = a * sgn * sl2;
+          for (int e = 4; e < 64; e += 4) {
+            a = max3(a, x[e], x[e + 1]);
+            b = max3(b, x[e + 2], x[e + 3]);
           }
-          if (top != top) top = -INFINITY;           // nothing seen with a factor of 0, or all NaN
+          float top = fmaxf(a, b) * sl2;
+          if (top != top) top = -INFINITY;           // all NaN
           // the row's maximum over both halves; behind it both warps have read their logits, so
           // P may be written over them
           float* both = xch + (meets & 1) * 2 * kRows;
@@ -802,9 +972,9 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             }
             m = top;
           }
-          if (t > s.t0 && __any_sync(0xffffffffu, rescale)) {
+          if (t > t0 && __any_sync(0xffffffffu, rescale)) {
             // O may be touched once the previous tile's products are in it
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.pv_done[(u - 1) & 1]), ((u - 1) >> 1) & 1, abort_flag))) {
+            if (!__all_sync(0xffffffffu, wait_for(smem_u32(&bars.pv_done[(u - 1) & 1]), ((u - 1) >> 1) & 1, abort_flag))) {
               alive = false;
               break;
             }
@@ -827,17 +997,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             }
           }
           const float moff = m == -INFINITY ? 0.f : kShift - m;
-          float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
 #pragma unroll
             for (int e = 32 * c; e < 32 * c + 32; e += 2) fma_pair(x[e], x[e + 1], sl2, moff);
-            if (masked) {
-              const uint32_t bits = seen(c);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((bits >> e) & 1u)) x[32 * c + e] = -INFINITY;
-            }
             uint32_t pw[16];
 #pragma unroll
             for (int e = 32 * c; e < 32 * c + 32; e += 4) {
@@ -845,121 +1009,20 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
               x[e + 1] = exp2_hw(x[e + 1]);
               x[e + 2] = exp2_hw(x[e + 2]);
               x[e + 3] = exp2_hw(x[e + 3]);
-              add_pair(a0, a1, x[e], x[e + 1]);
-              add_pair(b0, b1, x[e + 2], x[e + 3]);
+              add_pair(l0, l1, x[e], x[e + 1]);
+              add_pair(l2, l3, x[e + 2], x[e + 3]);
               pw[(e - 32 * c) / 2] = half2_of(x[e], x[e + 1]);
               pw[(e - 32 * c) / 2 + 1] = half2_of(x[e + 2], x[e + 3]);
             }
             tmem_st16(s_addr + 32 * half + 16 * c, pw);
           }
-          l = l * alpha + ((a0 + b0) + (a1 + b1));
+          l = l * alpha + ((l0 + l2) + (l1 + l3));
           tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[sb]));
       }
-      if (!alive) break;
-      // All QK of the segment are complete: Q may be written for the next one while the last
-      // products run.
-      Segment y = s;
-      const uint32_t last = u - 1;
-      have = next_running(y);
-      float sl2_next = 0.f;
-      if (have && !prepare_q(y, sl2_next)) break;
-      // the row's sum over both halves
-      if (active) {
-        float* both = xch + (meets & 1) * 2 * kRows;
-        both[half * kRows + r] = l;
-        if (!meet()) break;
-        l += both[(half ^ 1) * kRows + r];
-      }
-      // ---- epilogue: o = v_descale O / l, lse = m + log2 l ---------------------------------------
-      if (!__all_sync(0xffffffffu,
-                      (s.t1 == s.t0 + 1 ||
-                       mbar_wait(smem_u32(&bars.pv_done[(last - 1) & 1]), ((last - 1) >> 1) & 1, abort_flag)) &&
-                          mbar_wait(smem_u32(&bars.pv_done[last & 1]), (last >> 1) & 1, abort_flag)))
-        break;
-      tc_fence_after();
-      const bool bad = *reinterpret_cast<volatile int*>(&bars.bad[seg & 3]) == seg + 1;
-      const bool nan_v = *reinterpret_cast<volatile int*>(&bars.nan[seg & 3]) == seg + 1;
-      if (bad && lane == 0 && half == 0) set_status(p.status, MTPATTN_ERR_PAGE);
-      const bool whole = s.t0 == 0 && s.t1 == s.nt;
-      if (active) {
-        const float sc = l != 0.f ? vd / l : 0.f;    // NaN stays NaN
-        const int slot = 2 * blockIdx.x + (s.first ? 0 : 1);
-        const int rows = min(32, s.n * p.ratio - s.m * kRows - 32 * quad);
-        const int node = rr / p.ratio;
-        const int64_t out_at = static_cast<int64_t>(s.q0 + node) * p.out_stride_tok +
-                               static_cast<int64_t>(s.h * p.ratio + rr - node * p.ratio) * p.out_stride_head;
-#pragma unroll 1
-        for (int c = 0; c < kHeadDim / 2 / kOutCols; ++c) {
-          const int d0 = kHeadDim / 2 * half + kOutCols * c;
-          uint32_t o[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-              "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n"
-              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
-                "=r"(o[14]), "=r"(o[15])
-              : "r"(lane_addr + kOCol + d0)
-              : "memory");
-          float f[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] = l == 0.f || bad ? 0.f : __uint_as_float(o[e]) * sc;
-          if (nan_v && !bad && valid) {
-            // NaN values of the nodes that this row sees, dims d0 .. + 15
-            for (uint64_t w = word; w; w &= w - 1) {
-              const int key = tree0 + __ffsll(static_cast<long long>(w)) - 1;
-              if (key < s.t0 * kKeys || key >= s.t1 * kKeys) continue;
-              const int page = p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + key / kPage];
-              const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim + d0;
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if ((src[e] & 0x7f) == 0x7f) f[e] = __int_as_float(0x7fc00000);
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(stage + lane * kStagePitch + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-          __syncwarp();
-          if (whole) {                               // two lanes a row
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = 16 * i + (lane >> 1), d = 8 * (lane & 1);
-              const int64_t at = __shfl_sync(0xffffffffu, out_at, row);
-              const float* src = stage + row * kStagePitch + d;
-              const float4 fa = *reinterpret_cast<const float4*>(src);
-              const float4 fb = *reinterpret_cast<const float4*>(src + 4);
-              const __nv_bfloat162 h0 = __floats2bfloat162_rn(fa.x, fa.y), h1 = __floats2bfloat162_rn(fa.z, fa.w);
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(fb.x, fb.y), h3 = __floats2bfloat162_rn(fb.z, fb.w);
-              if (row < rows)
-                *reinterpret_cast<uint4*>(p.out + at + d0 + d) =
-                    make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
-                               *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
-            }
-          } else {                                   // four lanes a row
-            float* dst = p.o_part + (static_cast<int64_t>(slot) * kRows + 32 * quad) * kHeadDim + d0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 8 * i + (lane >> 2), d = 4 * (lane & 3);
-              if (row < rows)
-                *reinterpret_cast<float4*>(dst + static_cast<int64_t>(row) * kHeadDim + d) =
-                    *reinterpret_cast<const float4*>(stage + row * kStagePitch + d);
-            }
-          }
-        }
-        if (!whole && valid && half == 0)
-          p.lse_part[slot * kRows + r] = bad ? __uint_as_float(kBadLse)
-                                             : (l != 0.f ? m + log2f(l) - kShift : -INFINITY);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.o_free));
-      ++seg;
-      s = y;
-      sl2 = sl2_next;
     }
   }
 
