@@ -427,10 +427,23 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       ++e;
       const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
       const uint64_t pol = s.T == 1 ? once : again;
+      // Table entries, a lane one of four tiles' 32, with the next 32 on the way: a load of its own
+      // per tile would put its latency, some 2000 cycles, into every turn.
+      const int pages = (s.L + kPage - 1) / kPage;
+      auto entries = [&](int t) -> int {
+        const int pg = t * kTilePages + lane;
+        return pg < pages ? bt[pg] : 0;
+      };
+      int now = entries(s.t0), ahead = entries(s.t0 + 4);
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++u) {
         const int np = tile_pages(s.L, t), st = u % kKStages;
-        const int phys = lane < np ? bt[t * kTilePages + lane] : 0;
+        const int four = (t - s.t0) & 3;
+        if (four == 0 && t > s.t0) {
+          now = ahead;
+          ahead = entries(t + 4);
+        }
+        const int phys = __shfl_sync(0xffffffffu, now, (four * kTilePages + lane) & 31);
         const uint32_t fb = smem_u32(&bars.k_full[st]);
         if (lane == 0) {
           ok = wait_for(smem_u32(&bars.k_empty[st]), ((u / kKStages) & 1) ^ 1, abort_flag);
