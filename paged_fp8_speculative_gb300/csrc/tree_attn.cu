@@ -10,16 +10,18 @@
 // partial output and log-sum-exp per piece in the workspace, and tree_reduce_kernel joins them.
 // A CTA has at most two partial units, the first and the last of its piece: two slots per CTA.
 //
-// Roles (448 threads):
-//   warp 0       K: TMA loads of the K pages (two 128-byte-wide boxes a page, 128B-swizzled);
-//   warp 1       MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
-//   warps 2-5    V: warp w loads page w of each 64-key half tile to registers, a half tile ahead,
-//                widens it to f16 and stores it as PV's operand (no staging of the codes);
-//   warps 6-13   softmax: thread = query row = TMEM lane, two warps a row quarter that take 64 of a
-//                tile's 128 keys each and exchange their maxima; also the Q operand, and half of
-//                the output's dims each.
-// The block's 215 KB of shared memory leave 12 KB of L1: a spilled register costs an L2 access, so
-// the thread count is what leaves the softmax its 128 registers.
+// Roles (512 threads; warp 3 idle):
+//   warp 0      the CTA's walk over its piece, published segment by segment, and the K pages by
+//               TMA (two 128-byte-wide boxes a page, 128B-swizzled), whole key tiles;
+//   warp 1      MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
+//   warp 2      the V pages by TMA, 64 keys (half a tile) a stage;
+//   warps 4-7   widen each half tile of V to f16, PV's operand;
+//   warps 8-15  softmax: thread = query row = TMEM lane, two warps a row quarter that take 64 of a
+//               tile's 128 keys each and exchange their maxima; also the Q operand, and half of
+//               the output's dims each.
+// The block takes all of the shared memory, which leaves 5 KB of L1: a spilled register costs an L2
+// access, and the roles' loops have to share the instruction cache, so one warp alone walks over the
+// sequences and every role's loop is written once.
 //
 // Precision.  K enters as its e4m3 codes, Q as the sum of two e4m3 terms of x = q 2^a (a per row,
 // max |x| in [128, 256)): hi = e4m3(x), lo = e4m3(x - hi), both products into one accumulator.  A
@@ -57,39 +59,38 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTreeThreads = 448;
+constexpr int kTreeThreads = 512;
 constexpr int kRows = 128;                         // query rows per tile
 constexpr int kKeys = 128;                         // keys per tile
 constexpr int kTilePages = kKeys / kPage;          // 8
 constexpr int kHalfKeys = 64;                      // V is staged half a tile at a time
-constexpr int kVWarps = 4;                         // a page of a half tile each
-constexpr int kWarpV = 2, kWarpSoft = kWarpV + kVWarps, kSoftWarps = 8;
+constexpr int kWarpWiden = 4, kWidenWarps = 4, kWarpSoft = 8, kSoftWarps = 8;
 constexpr int kQHalf = kRows * 128;                // 128 of the 256 dims of one Q term
 constexpr int kQTerm = 2 * kQHalf;                 // 32 KB: hi, then lo
 constexpr int kKHalf = kKeys * 128;
 constexpr int kKTile = 2 * kKHalf;                 // 32 KB per stage
 constexpr int kKStages = 2;
+constexpr int kV8Half = kHalfKeys * 128;           // 128 dims of 64 keys, e4m3
+constexpr int kV8Stage = 2 * kV8Half;              // 16 KB per stage
 constexpr int kVAtom = kHalfKeys * 128;            // 64 dims of 64 keys, f16
 constexpr int kVStage = 4 * kVAtom;                // 32 KB per stage
-constexpr int kVStages = 2;
-constexpr int kOutCols = 16;                       // output columns staged at a time
-constexpr int kStagePitch = 20;                    // floats a row there (eight rows: all 32 banks)
+constexpr int kVStages = 2;                        // of the codes, and of the operand
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kQTerm;
-constexpr int kOffV = kOffK + kKStages * kKTile;
-constexpr int kOffOut = kOffV + kVStages * kVStage;
-constexpr int kOffXch = kOffOut + kSoftWarps * 32 * kStagePitch * 4;
+constexpr int kOffV8 = kOffK + kKStages * kKTile;
+constexpr int kOffV = kOffV8 + kVStages * kV8Stage;
+constexpr int kOffXch = kOffV + kVStages * kVStage;
 constexpr int kOffBar = kOffXch + 2 * 2 * kRows * 4;   // exchange: [parity][half][row] floats
 constexpr int kBarBytes = 1024;
-constexpr int kSmemTree = kOffBar + kBarBytes + 1024;  // + alignment slack
-static_assert(kSmemTree <= 232448, "shared-memory layout");
+constexpr int kSmemTree = kOffBar + kBarBytes;
+static_assert(kSmemTree == 232448, "all that a block may have");
 constexpr int kSCols = 128, kOCol = 256, kTmemCols = 512;
 constexpr float kTau = 6.f, kShift = 8.f;
 constexpr uint32_t kBadLse = 0x7fd0bad1u;          // a partial of a sequence with a bad page (a NaN
                                                    // that no arithmetic makes)
 
 struct TreeAttnParams {
-  CUtensorMap tmap_k;
+  CUtensorMap tmap_k, tmap_v;
   const __nv_bfloat16* q;
   int64_t q_stride_tok, q_stride_head;
   const uint8_t* v_cache;
@@ -116,11 +117,14 @@ struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
   int m, t0, t1, nt, T;
   int first;                 // it starts the CTA's piece
   int end;                   // no segment: the piece is done
+  int bad;                   // set on the way: it met a page outside the pool
+  int nan;                   // ... the V of one of its tree nodes holds a NaN code
 };
 constexpr int kSegRing = 8;
 
 struct TreeBars {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t v8_full[kVStages], v8_empty[kVStages];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_ready, o_free, final_mma;
   uint64_t xch[4][2];        // a row quarter's two warps meet, in turn on two barriers
@@ -128,8 +132,7 @@ struct TreeBars {
   Segment seg[kSegRing];     // written by the K producer, given back by the softmax warps
   uint32_t tmem_base;
   int32_t abort;
-  int32_t bad[4];            // [segment & 3]: segment + 1 if it met a page outside the pool
-  int32_t nan[4];            // the same if a tree node's V holds a NaN code
+  int32_t v8_note[kVStages][4];   // of a stage: keys of the sequence, first key of the tree, segment
 };
 static_assert(sizeof(TreeBars) <= kBarBytes, "barrier block");
 
@@ -239,7 +242,7 @@ struct Walker {
     s.t0 = in - unit * nt;
     s.t1 = min(nt, s.t0 + hi - pos);
     s.first = pos == lo;
-    s.end = 0;
+    s.end = s.bad = s.nan = 0;
     pos += s.t1 - s.t0;
     return __shfl_sync(0xffffffffu, mine.err, f);
   }
@@ -335,9 +338,11 @@ __device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t a_tmem, uint64_
 
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* base = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) unsigned char base[];
+  if (smem_u32(base) & 1023) {                     // the operands' swizzle needs it; no kernel sets
+    if (threadIdx.x == 0) set_status(p.status, MTPATTN_ERR_TIMEOUT);   // other shared memory aside
+    return;
+  }
   TreeBars& bars = *reinterpret_cast<TreeBars*>(base + kOffBar);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &bars.abort;
@@ -353,8 +358,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       mbar_init(smem_u32(&bars.k_empty[i]), 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(smem_u32(&bars.v_full[i]), kVWarps);
+      mbar_init(smem_u32(&bars.v_full[i]), kWidenWarps);
       mbar_init(smem_u32(&bars.v_empty[i]), 1);
+      mbar_init(smem_u32(&bars.v8_full[i]), 1);
+      mbar_init(smem_u32(&bars.v8_empty[i]), kWidenWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.s_full[i]), 1);
@@ -369,7 +376,6 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       mbar_init(smem_u32(&bars.seg_free[i]), kSoftWarps);
     }
     mbar_init(smem_u32(&bars.final_mma), 1);
-    for (int i = 0; i < 4; ++i) bars.bad[i] = bars.nan[i] = 0;
     bars.abort = 0;
     fence_mbar_init();
   }
@@ -553,161 +559,145 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     __syncwarp();
     volatile int no_abort = 0;
     wait_for(smem_u32(&bars.final_mma), 0, &no_abort);
-  } else if (warp < kWarpSoft) {
-    // ========================================= V loads ============================================
-    // A page is 16 bytes x 8 a lane: load i holds key 2 i + lane / 16 of the warp's page,
-    // dims 16 (lane % 16) .. + 15, two 16-byte chunks of f16 in 64-dim atom (lane % 16) / 4.
-    const int w = warp - kWarpV;
-    const int c16 = lane & 15, krow = lane >> 4;
-    const int atom = c16 >> 2, ch = 2 * (c16 & 3);
-    // lanes of odd atoms store their second chunk first: the eight lanes of a store phase then
-    // cover all eight chunk positions
-    const int swap = atom & 1;
-    struct Half {
-      uint4 x[8];
-      bool pages;            // the warp has a page in this half tile
-      bool bad;              // ... outside the pool
-      int tree;              // first key of the page that belongs to the tree (16: none)
-      int seg;
-    };
-    // The half tiles (4 pages each) in order.
-    int seg = -1, hf = 0, hf_end = 0;               // the segment at hand and the next half tile in it
-    int L = 0, tree0 = 0;
-    int64_t head = 0;                               // byte offset of the segment's head and this lane
-    const int32_t* bt = nullptr;
-    int ent = 0, ent_at = 0;                        // lane l: the table entry of half tile ent_at + l
-    const int64_t row_bytes = static_cast<int64_t>(p.hkv) * kHeadDim;
-    // To the next half tile, into the next segment if need be.  1: there; 0: the piece is done;
-    // -1: the next segment is not known yet (only if !wait).
-    auto seek = [&](bool wait) -> int {
-      if (++hf < hf_end) return 1;
-      hf = hf_end;
-      const int e = seg + 1;
-      if (!wait && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bars.seg_full[e % kSegRing]), (e / kSegRing) & 1)))
-        return -1;
-      if (!seg_wait(e)) return 0;
-      const Segment& s = bars.seg[e % kSegRing];
-      if (s.end) return 0;
-      seg = e;
-      L = s.L;
-      tree0 = s.L - s.n;
-      head = (static_cast<int64_t>(krow) * p.hkv + s.h) * kHeadDim + 16 * c16;
-      bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
-      hf = 2 * s.t0;
-      hf_end = min(2 * s.t1, ((L + kPage - 1) / kPage + 3) / 4);
-      ent_at = hf - 32;
-      return 1;
-    };
-    auto load = [&](Half& a) {
-      if (hf >= ent_at + 32) {
-        ent_at = hf;
-        const int pg = 4 * (hf + lane) + w;
-        ent = pg < (L + kPage - 1) / kPage ? bt[pg] : 0;
-      }
-      const int page = __shfl_sync(0xffffffffu, ent, hf - ent_at);
-      const int key0 = (4 * hf + w) * kPage;
-      const int left = L - key0;                    // keys of the page that belong to the sequence
-      a.pages = left > 0;
-      a.tree = min(16, max(0, tree0 - key0));
-      a.seg = seg;
-      const bool good = page >= 0 && page < p.num_pages;
-      a.bad = a.pages && !good;
-      const uint8_t* src = p.v_cache + page * (kPage * row_bytes) + head;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a.x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (good && 2 * i + krow < left)
-          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                       : "=r"(a.x[i].x), "=r"(a.x[i].y), "=r"(a.x[i].z), "=r"(a.x[i].w)
-                       : "l"(src + 2 * i * row_bytes));
-      }
-    };
-    uint32_t v = 0;
-    auto store = [&](Half& a) -> bool {
-      const int st = v % kVStages;
-      if (!__all_sync(0xffffffffu, wait_for(smem_u32(&bars.v_empty[st]), ((v / kVStages) & 1) ^ 1, abort_flag)))
-        return false;
-      ++v;
-      // Notes are made behind the wait: a slot of the four is then not one that the epilogue has
-      // yet to read (this warp is two half tiles ahead of it at most).
-      if (a.bad && lane == 0) bars.bad[a.seg & 3] = a.seg + 1;
-      if (a.pages) {
-        unsigned char* dst = base + kOffV + st * kVStage + atom * kVAtom + w * 16 * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int key = 2 * i + krow;
-          uint4 c0, c1;
-          widen(a.x[i].x, c0.x, c0.y);
-          widen(a.x[i].y, c0.z, c0.w);
-          widen(a.x[i].z, c1.x, c1.y);
-          widen(a.x[i].w, c1.z, c1.w);
-          const int o0 = key * 128 + ((ch ^ (key & 7)) << 4), o1 = key * 128 + (((ch + 1) ^ (key & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst + (swap ? o1 : o0)) = swap ? c1 : c0;
-          *reinterpret_cast<uint4*>(dst + (swap ? o0 : o1)) = swap ? c0 : c1;
+  } else if (warp == 2) {
+    // ======================================== V producer ==========================================
+    if (lane == 0) prefetch_tmap(&p.tmap_v);
+    const uint64_t once = l2_policy_evict_first();
+    uint64_t again;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
+    uint32_t v = 0;                                 // half tiles
+    bool ok = true;
+#pragma unroll 1
+    for (int e = 0; ok; ++e) {
+      if (!seg_wait(e)) break;
+      Segment& s = bars.seg[e % kSegRing];
+      if (s.end) break;
+      const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
+      const uint64_t pol = s.T == 1 ? once : again;
+      const int pages = (s.L + kPage - 1) / kPage, h = s.h, L = s.L, tree0 = s.L - s.n;
+      const int h0 = 2 * s.t0, h1 = min(2 * s.t1, (pages + 3) / 4);
+      auto entries = [&](int hf) -> int {           // of eight half tiles, the next eight ahead
+        const int pg = 4 * hf + lane;
+        return pg < pages ? bt[pg] : 0;
+      };
+      int now = entries(h0), ahead = entries(h0 + 8);
+#pragma unroll 1
+      for (int hf = h0; hf < h1; ++hf, ++v) {
+        const int np = min(4, pages - 4 * hf), st = v % kVStages;
+        const int eight = (hf - h0) & 7;
+        if (eight == 0 && hf > h0) {
+          now = ahead;
+          ahead = entries(hf + 8);
         }
-        if (a.tree < 16) {                          // NaN codes of tree nodes: noted, and 0 instead
-          uint32_t any = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (2 * i + krow >= a.tree)
-              any |= (((a.x[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((a.x[i].y & 0x7f7f7f7fu) + 0x01010101u) |
-                      ((a.x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((a.x[i].w & 0x7f7f7f7fu) + 0x01010101u));
-          if (any & 0x80808080u) {
-            bars.nan[a.seg & 3] = a.seg + 1;
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i) {          // this lane's chunks, as they were stored
-              const int key = 2 * (i >> 1) + krow;
-              uint32_t* x = reinterpret_cast<uint32_t*>(dst + key * 128 + (((ch + (i & 1)) ^ (key & 7)) << 4));
-              if (key >= a.tree)
-#pragma unroll 1
-                for (int d = 0; d < 4; ++d) {
-                  const uint32_t h = x[d];
-                  x[d] = ((h & 0x7fffu) > 0x7c00u ? 0u : h & 0xffffu) |
-                         ((h & 0x7fff0000u) > 0x7c000000u ? 0u : h & 0xffff0000u);
-                }
-            }
+        const int phys = __shfl_sync(0xffffffffu, now, (4 * eight + lane) & 31);
+        const bool bad = __any_sync(0xffffffffu, lane < np && (phys < 0 || phys >= p.num_pages));
+        const uint32_t fb = smem_u32(&bars.v8_full[st]);
+        if (lane == 0) {
+          ok = wait_for(smem_u32(&bars.v8_empty[st]), ((v / kVStages) & 1) ^ 1, abort_flag);
+          if (ok) {
+            if (bad) s.bad = 1;
+            bars.v8_note[st][0] = L - hf * kHalfKeys;
+            bars.v8_note[st][1] = tree0 - hf * kHalfKeys;
+            bars.v8_note[st][2] = e % kSegRing;
+            mbar_arrive_expect_tx(fb, np * 2 * 2048);
           }
         }
-        fence_proxy_async_smem();                   // visible to the tensor cores behind v_full
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (lane < np) {
+          const uint32_t dst = smem_u32(base + kOffV8 + st * kV8Stage) + lane * 2048;
+          tma_load_4d(dst, &p.tmap_v, fb, 0, h, 0, phys, pol);
+          tma_load_4d(dst + kV8Half, &p.tmap_v, fb, 128, h, 0, phys, pol);
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.v_full[st]));
-      return true;
-    };
-    // Two buffers in turn, so that one's loads are in flight while the other is widened (a copy
-    // between them would wait for the loads).  A segment that is not known yet is waited for only
-    // with nothing left to store: what publishes it may itself wait for these stores.
-    Half buf0, buf1;
-    auto fetch = [&](Half& a, bool wait) -> int {
-      const int r = seek(wait);
-      if (r > 0) load(a);
-      return r;
-    };
-    bool full0 = false, full1 = false, good = true;
-    while (good) {
-      int r;
-      do {
-        r = fetch(buf0, !full1);
-        if (full1) good = store(buf1);
-        full1 = false;
-      } while (r < 0 && good);
-      if (r <= 0 || !good) break;
-      full0 = true;
-      do {
-        r = fetch(buf1, !full0);
-        if (full0) good = store(buf0);
-        full0 = false;
-      } while (r < 0 && good);
-      if (r <= 0) break;
-      full1 = true;
     }
-  } else {
+    // the last stages' copies, and the end for the widening warps (which have seen those by then)
+    if (lane == 0) {
+      volatile int no_abort = 0;
+      for (uint32_t k = 1; k <= kVStages && k <= v; ++k)
+        wait_for(smem_u32(&bars.v8_full[(v - k) % kVStages]), ((v - k) / kVStages) & 1, &no_abort);
+      const int st = v % kVStages;
+      if (ok && wait_for(smem_u32(&bars.v8_empty[st]), ((v / kVStages) & 1) ^ 1, abort_flag)) {
+        bars.v8_note[st][2] = -1;
+        mbar_arrive(smem_u32(&bars.v8_full[st]));
+      }
+    }
+  } else if (warp >= kWarpWiden && warp < kWarpSoft) {
+    // ======================================== V widening ==========================================
+    // Thread c takes 16-byte slot c % 8 of the keys c / 8 + 16 i of both 128-dim halves: all have
+    // the same key % 8, hence the same swizzled chunk (16 dims) and the same two positions in the
+    // f16 operand's 64-dim atoms.
+    const int c = threadIdx.x - kWarpWiden * 32;
+    const int key0 = c >> 3, x7 = key0 & 7;
+    const int chunk = (c & 7) ^ x7;                 // dims 16 chunk .. + 15 of the half
+    const uint32_t from = key0 * 128 + (c & 7) * 16;
+    const uint32_t to = (chunk >> 2) * kVAtom + key0 * 128;
+    const uint32_t to0 = to + (((2 * (chunk & 3)) ^ x7) << 4), to1 = to + (((2 * (chunk & 3) + 1) ^ x7) << 4);
+#pragma unroll 1
+    for (uint32_t v = 0;; ++v) {
+      const int st = v % kVStages;
+      const uint32_t parity = (v / kVStages) & 1;
+      if (!__all_sync(0xffffffffu, wait_for(smem_u32(&bars.v8_full[st]), parity, abort_flag))) break;
+      const int keys = bars.v8_note[st][0], tree = bars.v8_note[st][1], seg = bars.v8_note[st][2];
+      if (seg < 0) break;
+      const unsigned char* src = base + kOffV8 + st * kV8Stage + from;
+      unsigned char* dst = base + kOffV + st * kVStage;
+      uint4 a[8];                                   // keys key0 + 16 (i % 4), half i / 4
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const uint4*>(src + (i >> 2) * kV8Half + (i & 3) * 2048);
+      if (keys < kHalfKeys) {                       // places behind the sequence: zeros
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (key0 + 16 * (i & 3) >= keys) a[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      bool nan = false;
+      if (tree < kHalfKeys) {                       // NaN codes of tree nodes: noted, and 0 instead
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t any = ((a[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((a[i].y & 0x7f7f7f7fu) + 0x01010101u) |
+                               ((a[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((a[i].w & 0x7f7f7f7fu) + 0x01010101u);
+          nan |= key0 + 16 * (i & 3) >= tree && (any & 0x80808080u);
+        }
+      }
+      if (!__all_sync(0xffffffffu, wait_for(smem_u32(&bars.v_empty[st]), parity ^ 1, abort_flag))) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint4 c0, c1;
+        widen(a[i].x, c0.x, c0.y);
+        widen(a[i].y, c0.z, c0.w);
+        widen(a[i].z, c1.x, c1.y);
+        widen(a[i].w, c1.z, c1.w);
+        unsigned char* d = dst + (i >> 2) * 2 * kVAtom + (i & 3) * 2048;
+        *reinterpret_cast<uint4*>(d + to0) = c0;
+        *reinterpret_cast<uint4*>(d + to1) = c1;
+      }
+      if (nan) {                                    // this thread's chunks once more, as they were stored
+        bars.seg[seg].nan = 1;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(dst + (i >> 3) * 2 * kVAtom + (i & 3) * 2048 + ((i & 4) ? to1 : to0));
+          if (key0 + 16 * (i & 3) >= tree)
+#pragma unroll 1
+            for (int d = 0; d < 4; ++d) {
+              const uint32_t h = x[d];
+              x[d] = ((h & 0x7fffu) > 0x7c00u ? 0u : h & 0xffffu) |
+                     ((h & 0x7fff0000u) > 0x7c000000u ? 0u : h & 0xffff0000u);
+            }
+        }
+      }
+      fence_proxy_async_smem();                     // visible to the tensor cores behind v_full
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&bars.v_full[st]));
+        mbar_arrive(smem_u32(&bars.v8_empty[st]));
+      }
+    }
+  } else if (warp >= kWarpSoft) {
     // ======================================= softmax (rows) =======================================
     const int quad = warp & 3;                      // TMEM lane quarter
     const int half = (warp - kWarpSoft) >> 2;       // keys 64 half .. + 63, output dims 128 half ..
     const int r = 32 * quad + lane;                 // query row of the tile, TMEM lane
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    float* stage = reinterpret_cast<float*>(base + kOffOut) + (warp - kWarpSoft) * 32 * kStagePitch;
     float* xch = reinterpret_cast<float*>(base + kOffXch);
     // A negative factor goes into Q, so that the factors are positive; one of 0 is taken as the
     // smallest float, under which all logits are alike.
@@ -818,75 +808,63 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
                             wait_for(smem_u32(&bars.pv_done[last & 1]), (last >> 1) & 1, abort_flag)))
           break;
         tc_fence_after();
-        const bool bad = *reinterpret_cast<volatile int*>(&bars.bad[(e - 1) & 3]) == e;
-        const bool nan_v = *reinterpret_cast<volatile int*>(&bars.nan[(e - 1) & 3]) == e;
+        const bool bad = *reinterpret_cast<const volatile int*>(&s.bad) != 0;
+        const bool nan_v = *reinterpret_cast<const volatile int*>(&s.nan) != 0;
         if (bad && lane == 0 && half == 0) set_status(p.status, MTPATTN_ERR_PAGE);
         const bool whole = s.t0 == 0 && s.t1 == s.nt;
         if (active) {
-          const float sc = l != 0.f ? vd / l : 0.f;    // NaN stays NaN
+          const float sc = l != 0.f && !bad ? vd / l : 0.f;   // NaN stays NaN
           const int slot = 2 * blockIdx.x + (s.first ? 0 : 1);
-          const int rows = min(32, s.n * p.ratio - s.m * kRows - 32 * quad);
+          const int rows = s.n * p.ratio - s.m * kRows - 32 * quad;   // valid rows of this quarter
           const int rr = s.m * kRows + r, node = rr / p.ratio;
-          const int64_t out_at = static_cast<int64_t>(s.q0 + node) * p.out_stride_tok +
-                                 static_cast<int64_t>(s.h * p.ratio + rr - node * p.ratio) * p.out_stride_head;
+          // where this thread's row goes: an output row, or a partial one
+          const int64_t at = whole ? static_cast<int64_t>(s.q0 + node) * p.out_stride_tok +
+                                         static_cast<int64_t>(s.h * p.ratio + rr - node * p.ratio) * p.out_stride_head
+                                   : (static_cast<int64_t>(slot) * kRows + r) * kHeadDim;
+          // 16 rows x 64 dims a step: four lanes hold 8 consecutive dims of a row
 #pragma unroll 1
-          for (int c = 0; c < kHeadDim / 2 / kOutCols; ++c) {
-            const int d0 = kHeadDim / 2 * half + kOutCols * c;
-            uint32_t o[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-                "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n"
-                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                  "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
-                  "=r"(o[14]), "=r"(o[15])
-                : "r"(lane_addr + kOCol + d0)
-                : "memory");
-            float f[16];
+          for (int c = 0; c < 4; ++c) {
+            const int d0 = 128 * half + 64 * (c >> 1);
+            const int row = 16 * (c & 1) + (lane >> 2);              // and row + 8
+            uint32_t o[32];
+            tmem_ld16x256_x8(lane_addr + (static_cast<uint32_t>(16 * (c & 1)) << 16) + kOCol + d0, o);
+            const float sc0 = __shfl_sync(0xffffffffu, sc, row), sc1 = __shfl_sync(0xffffffffu, sc, row + 8);
+            const int64_t at0 = __shfl_sync(0xffffffffu, at, row) + d0 + 2 * (lane & 3);
+            const int64_t at1 = __shfl_sync(0xffffffffu, at, row + 8) + d0 + 2 * (lane & 3);
+            tmem_ld_wait(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = l == 0.f || bad ? 0.f : __uint_as_float(o[i]) * sc;
+            for (int k = 0; k < 8; ++k) {
+              // a factor of 0 (no key seen, or a bad page) gives zeros, whatever the sums hold
+              const float f0 = sc0 == 0.f ? 0.f : __uint_as_float(o[4 * k]) * sc0;
+              const float f1 = sc0 == 0.f ? 0.f : __uint_as_float(o[4 * k + 1]) * sc0;
+              const float f2 = sc1 == 0.f ? 0.f : __uint_as_float(o[4 * k + 2]) * sc1;
+              const float f3 = sc1 == 0.f ? 0.f : __uint_as_float(o[4 * k + 3]) * sc1;
+              if (whole) {
+                if (row < rows) *reinterpret_cast<__nv_bfloat162*>(p.out + at0 + 8 * k) = __floats2bfloat162_rn(f0, f1);
+                if (row + 8 < rows) *reinterpret_cast<__nv_bfloat162*>(p.out + at1 + 8 * k) = __floats2bfloat162_rn(f2, f3);
+              } else {
+                if (row < rows) *reinterpret_cast<float2*>(p.o_part + at0 + 8 * k) = make_float2(f0, f1);
+                if (row + 8 < rows) *reinterpret_cast<float2*>(p.o_part + at1 + 8 * k) = make_float2(f2, f3);
+              }
+            }
+          }
+          if (nan_v && !bad) {
+            // NaN values of the nodes that this thread's row sees, behind the stores above
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(stage + lane * kStagePitch + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-            if (nan_v && !bad && valid) {
-              // NaN values of the nodes that this row sees, dims d0 .. + 15
+            if (valid)
 #pragma unroll 1
               for (uint64_t w = word; w; w &= w - 1) {
                 const int key = s.L - s.n + __ffsll(static_cast<long long>(w)) - 1;
                 if (key < s.t0 * kKeys || key >= s.t1 * kKeys) continue;
                 const int page = p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + key / kPage];
-                const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim + d0;
+                const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim;
 #pragma unroll 1
-                for (int d = 0; d < kOutCols; ++d)
-                  if ((src[d] & 0x7f) == 0x7f) stage[lane * kStagePitch + d] = __int_as_float(0x7fc00000);
+                for (int d = 128 * half; d < 128 * half + 128; ++d)
+                  if ((src[d] & 0x7f) == 0x7f) {
+                    if (whole) p.out[at + d] = __float2bfloat16(__int_as_float(0x7fc00000));
+                    else p.o_part[at + d] = __int_as_float(0x7fc00000);
+                  }
               }
-            }
-            __syncwarp();
-            if (whole) {                               // two lanes a row
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int row = 16 * i + (lane >> 1), d = 8 * (lane & 1);
-                const int64_t at = __shfl_sync(0xffffffffu, out_at, row);
-                const float* src = stage + row * kStagePitch + d;
-                const float4 fa = *reinterpret_cast<const float4*>(src);
-                const float4 fb = *reinterpret_cast<const float4*>(src + 4);
-                const __nv_bfloat162 h0 = __floats2bfloat162_rn(fa.x, fa.y), h1 = __floats2bfloat162_rn(fa.z, fa.w);
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(fb.x, fb.y), h3 = __floats2bfloat162_rn(fb.z, fb.w);
-                if (row < rows)
-                  *reinterpret_cast<uint4*>(p.out + at + d0 + d) =
-                      make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
-                                 *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
-              }
-            } else {                                   // four lanes a row
-              float* dst = p.o_part + (static_cast<int64_t>(slot) * kRows + 32 * quad) * kHeadDim + d0;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = 8 * i + (lane >> 2), d = 4 * (lane & 3);
-                if (row < rows)
-                  *reinterpret_cast<float4*>(dst + static_cast<int64_t>(row) * kHeadDim + d) =
-                      *reinterpret_cast<const float4*>(stage + row * kStagePitch + d);
-              }
-            }
           }
           if (!whole && valid && half == 0)
             p.lse_part[slot * kRows + r] = bad ? __uint_as_float(kBadLse)
@@ -1341,8 +1319,7 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
   cache.v_cache = p.v_cache;
   cache.num_pages = num_pages;
   cache.num_kv_heads = num_kv_heads;
-  CUtensorMap unused;
-  if (!kv_tensor_maps(cache, device, &p.tmap_k, &unused)) return MTPATTN_E_LAUNCH;
+  if (!kv_tensor_maps(cache, device, &p.tmap_k, &p.tmap_v)) return MTPATTN_E_LAUNCH;
   static std::atomic<bool> attr_set[64];             // per device; setting it twice is harmless
   if (device >= 64) return MTPATTN_E_DEVICE;
   if (!attr_set[device].load(std::memory_order_acquire)) {
