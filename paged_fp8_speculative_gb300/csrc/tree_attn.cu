@@ -69,7 +69,7 @@ constexpr int kQHalf = kRows * 128;                // 128 of the 256 dims of one
 constexpr int kQTerm = 2 * kQHalf;                 // 32 KB: hi, then lo
 constexpr int kKHalf = kKeys * 128;
 constexpr int kKTile = 2 * kKHalf;                 // 32 KB per stage
-constexpr int kKStages = 2;
+constexpr int kKStages = 2;                        // as many as S buffers
 constexpr int kV8Half = kHalfKeys * 128;           // 128 dims of 64 keys, e4m3
 constexpr int kV8Stage = 2 * kV8Half;              // 16 KB per stage
 constexpr int kVAtom = kHalfKeys * 128;            // 64 dims of 64 keys, f16
@@ -123,7 +123,7 @@ struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
 constexpr int kSegRing = 8;
 
 struct TreeBars {
-  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t k_full[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t v8_full[kVStages], v8_empty[kVStages];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_ready, o_free, final_mma;
@@ -353,10 +353,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(smem_u32(&bars.k_full[i]), 1);
-      mbar_init(smem_u32(&bars.k_empty[i]), 1);
-    }
+    for (int i = 0; i < kKStages; ++i) mbar_init(smem_u32(&bars.k_full[i]), 1);
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(smem_u32(&bars.v_full[i]), kWidenWarps);
       mbar_init(smem_u32(&bars.v_empty[i]), 1);
@@ -452,7 +449,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         const int phys = __shfl_sync(0xffffffffu, now, (four * kTilePages + lane) & 31);
         const uint32_t fb = smem_u32(&bars.k_full[st]);
         if (lane == 0) {
-          ok = wait_for(smem_u32(&bars.k_empty[st]), ((u / kKStages) & 1) ^ 1, abort_flag);
+          // tile u - 2, of the same stage, has been multiplied when its S is there
+          ok = u < kKStages || wait_for(smem_u32(&bars.s_full[st]), ((u / kKStages) & 1) ^ 1, abort_flag);
           if (ok) mbar_arrive_expect_tx(fb, np * 2 * 2048);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -483,82 +481,82 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     const uint64_t q_desc = sdesc_sw128(smem_u32(base + kOffQ), 16, 1024);
     const uint64_t k_desc = sdesc_sw128(smem_u32(base + kOffK), 16, 1024);
     const uint64_t v_desc = sdesc_sw128(smem_u32(base + kOffV), kVAtom, 1024);
-    const bool leader = elect_one();
-    auto wait_all = [&](uint64_t& bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, wait_for(smem_u32(&bar), parity, abort_flag));
-    };
-    uint32_t u = 0, v = 0;                          // key tiles, half tiles of V
-    auto issue_pv = [&](uint32_t ut, int np, bool first) -> bool {
-      if (!wait_all(bars.p_full[ut & 1], (ut >> 1) & 1)) return false;
-      for (int k0 = 0; k0 < np; k0 += 4, ++v) {     // a half tile: four pages, 16 keys each
-        const int st = v % kVStages;
-        if (!wait_all(bars.v_full[st], (v / kVStages) & 1)) return false;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t p_tmem = tmem + (ut & 1) * kSCols + 8 * k0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k0 + k < np)
-              mma_pv(tmem + kOCol, p_tmem + 8 * k, v_desc + ((st * kVStage + k * 2048) >> 4), kIdescPV,
-                     (first && k0 + k == 0) ? 0u : 1u);
-          mma_commit(smem_u32(&bars.v_empty[st]));
+    // One thread runs the whole loop: whatever it does between products leaves the tensor cores
+    // idle once their short queue is empty, so it takes no votes and as few commits as it can (a
+    // K stage is free when its S buffer is full: both are tile u's, u mod 2).
+    if (elect_one()) {
+      auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
+        return wait_for(smem_u32(&bar), parity, abort_flag);
+      };
+      // A turn is QK of a tile and the products of the tile before it; a segment's last products
+      // go out in a turn of their own, before the next segment is waited for.
+      uint32_t u = 0, v = 0;                        // key tiles, half tiles of V
+      int seg = 0, t = 0, t0 = 0, t1 = 0, pages = 0;
+      int pv_pages = 0;                             // of tile u - 1, 0: nothing outstanding
+      uint32_t pv_acc = 0;                          // ... 0: it starts its segment's sums
+      while (true) {
+        const bool more = t < t1 || pv_pages == 0;
+        if (t >= t1 && more) {
+          if (!wait(bars.seg_full[seg % kSegRing], (seg / kSegRing) & 1)) break;
+          const Segment& s = bars.seg[seg % kSegRing];
+          if (s.end) break;
+          t = t0 = s.t0;
+          t1 = s.t1;
+          pages = (s.L + kPage - 1) / kPage;
+          if (!wait(bars.q_ready, seg & 1)) break;
+          ++seg;
         }
-        __syncwarp();
-      }
-      if (leader) mma_commit(smem_u32(&bars.pv_done[ut & 1]));
-      __syncwarp();
-      return true;
-    };
-    // A turn is QK of a tile and the products of the tile before it; a segment's last products
-    // go out in a turn of their own, before the next segment is waited for.
-    int seg = 0, t0 = 0, t1 = 0, t = 0, L = 0;
-    int pv_pages = 0;                               // of tile u - 1, 0: nothing outstanding
-    bool pv_first = false;                          // ... which starts its segment
-    while (true) {
-      const bool more = t < t1 || pv_pages == 0;
-      if (t >= t1 && more) {
-        if (!seg_wait(seg)) break;
-        const Segment& s = bars.seg[seg % kSegRing];
-        if (s.end) break;
-        t = t0 = s.t0;
-        t1 = s.t1;
-        L = s.L;
-        if (!wait_all(bars.q_ready, seg & 1)) break;
-        ++seg;
-      }
-      if (more) {
-        const int st = u % kKStages;
-        if (!wait_all(bars.k_full[st], (u / kKStages) & 1)) break;
-        tc_fence_after();
-        if (leader) {
+        if (more) {
+          const int st = u % kKStages;
+          if (!wait(bars.k_full[st], (u / kKStages) & 1)) break;
+          tc_fence_after();
+          const uint64_t kd = k_desc + (st * kKTile >> 4);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {            // hi: dims 32 k .. + 31, then lo
             const uint32_t a_off = (k >> 3) * kQTerm + ((k >> 2) & 1) * kQHalf + (k & 3) * 32;
-            const uint32_t b_off = st * kKTile + ((k >> 2) & 1) * kKHalf + (k & 3) * 32;
-            mma_f8_ss(tmem + (u & 1) * kSCols, q_desc + (a_off >> 4), k_desc + (b_off >> 4), kIdescQK,
+            const uint32_t b_off = ((k >> 2) & 1) * kKHalf + (k & 3) * 32;
+            mma_f8_ss(tmem + (u & 1) * kSCols, q_desc + (a_off >> 4), kd + (b_off >> 4), kIdescQK,
                       k > 0 ? 1u : 0u);
           }
           mma_commit(smem_u32(&bars.s_full[u & 1]));
-          mma_commit(smem_u32(&bars.k_empty[st]));
         }
-        __syncwarp();
+        if (pv_pages > 0) {
+          const uint32_t ut = u - 1;
+          // a segment's first products overwrite O: the epilogue before it has read it
+          if (pv_acc == 0 && seg > 1 && !wait(bars.o_free, (seg - 2) & 1)) break;
+          if (!wait(bars.p_full[ut & 1], (ut >> 1) & 1)) break;
+          bool ok = true;
+#pragma unroll 1
+          for (int k0 = 0; k0 < pv_pages; k0 += 4, ++v) {   // a half tile: four pages, 16 keys each
+            const int st = v % kVStages;
+            ok = wait(bars.v_full[st], (v / kVStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t p_tmem = tmem + (ut & 1) * kSCols + 8 * k0;
+            const uint64_t vd = v_desc + (st * kVStage >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k0 + k < pv_pages) mma_pv(tmem + kOCol, p_tmem + 8 * k, vd + (k * 2048 >> 4), kIdescPV, pv_acc);
+              pv_acc = 1;
+            }
+            mma_commit(smem_u32(&bars.v_empty[st]));
+          }
+          if (!ok) break;
+          mma_commit(smem_u32(&bars.pv_done[ut & 1]));
+        }
+        pv_pages = 0;
+        if (more) {
+          pv_pages = min(kTilePages, pages - t * kTilePages);
+          pv_acc = t != t0;
+          ++t;
+          ++u;
+        }
       }
-      if (pv_pages > 0) {
-        // a segment's first products overwrite O: the epilogue before it has read it
-        if (pv_first && seg > 1 && !wait_all(bars.o_free, (seg - 2) & 1)) break;
-        if (!issue_pv(u - 1, pv_pages, pv_first)) break;
-      }
-      pv_pages = more ? tile_pages(L, t) : 0;
-      if (more) {
-        pv_first = t == t0;
-        ++t;
-        ++u;
-      }
+      mma_commit(smem_u32(&bars.final_mma));
+      volatile int no_abort = 0;
+      wait_for(smem_u32(&bars.final_mma), 0, &no_abort);
     }
-    if (leader) mma_commit(smem_u32(&bars.final_mma));
     __syncwarp();
-    volatile int no_abort = 0;
-    wait_for(smem_u32(&bars.final_mma), 0, &no_abort);
   } else if (warp == 2) {
     // ======================================== V producer ==========================================
     if (lane == 0) prefetch_tmap(&p.tmap_v);
@@ -633,6 +631,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     const uint32_t from = key0 * 128 + (c & 7) * 16;
     const uint32_t to = (chunk >> 2) * kVAtom + key0 * 128;
     const uint32_t to0 = to + (((2 * (chunk & 3)) ^ x7) << 4), to1 = to + (((2 * (chunk & 3) + 1) ^ x7) << 4);
+    // The eight threads of a store phase reach two atoms, whose equal positions share banks: those
+    // of the second atom store their second chunk first, and the phase covers all eight positions.
+    const bool swap = (chunk & 4) != 0;
+    const uint32_t first = swap ? to1 : to0, second = swap ? to0 : to1;
 #pragma unroll 1
     for (uint32_t v = 0;; ++v) {
       const int st = v % kVStages;
@@ -668,8 +670,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         widen(a[i].z, c1.x, c1.y);
         widen(a[i].w, c1.z, c1.w);
         unsigned char* d = dst + (i >> 2) * 2 * kVAtom + (i & 3) * 2048;
-        *reinterpret_cast<uint4*>(d + to0) = c0;
-        *reinterpret_cast<uint4*>(d + to1) = c1;
+        *reinterpret_cast<uint4*>(d + first) = swap ? c1 : c0;
+        *reinterpret_cast<uint4*>(d + second) = swap ? c0 : c1;
       }
       if (nan) {                                    // this thread's chunks once more, as they were stored
         bars.seg[seg].nan = 1;
