@@ -326,6 +326,14 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
+// A load that stays before the arrival behind it (volatile, as that is)
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // tcgen05.mma kind::f16 (f16 x f16 -> f32), A from tensor memory, B from shared memory.
 __device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -622,19 +630,17 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     }
   } else if (warp >= kWarpWiden && warp < kWarpSoft) {
     // ======================================== V widening ==========================================
-    // Thread c takes 16-byte slot c % 8 of the keys c / 8 + 16 i of both 128-dim halves: all have
-    // the same key % 8, hence the same swizzled chunk (16 dims) and the same two positions in the
-    // f16 operand's 64-dim atoms.
+    // A thread takes one 16-byte chunk (16 dims) of the keys key0 + 16 i in both 128-dim halves: all
+    // have the same key % 8, hence the same swizzled positions.  The eight threads of a load or
+    // store phase take chunks 0-3 of a key and 4-7 of its neighbour (or the other way round): these
+    // lie in all eight 16-byte positions of the codes' rows, and, as the operand's two f16 chunks
+    // each, of its 64-dim atoms too.
     const int c = threadIdx.x - kWarpWiden * 32;
-    const int key0 = c >> 3, x7 = key0 & 7;
-    const int chunk = (c & 7) ^ x7;                 // dims 16 chunk .. + 15 of the half
-    const uint32_t from = key0 * 128 + (c & 7) * 16;
+    const int key0 = 2 * (c >> 4) + ((c >> 2) & 1), x7 = key0 & 7;
+    const int chunk = (c & 7) ^ (((c >> 3) & 1) << 2);
+    const uint32_t from = key0 * 128 + ((chunk ^ x7) << 4);
     const uint32_t to = (chunk >> 2) * kVAtom + key0 * 128;
     const uint32_t to0 = to + (((2 * (chunk & 3)) ^ x7) << 4), to1 = to + (((2 * (chunk & 3) + 1) ^ x7) << 4);
-    // The eight threads of a store phase reach two atoms, whose equal positions share banks: those
-    // of the second atom store their second chunk first, and the phase covers all eight positions.
-    const bool swap = (chunk & 4) != 0;
-    const uint32_t first = swap ? to1 : to0, second = swap ? to0 : to1;
 #pragma unroll 1
     for (uint32_t v = 0;; ++v) {
       const int st = v % kVStages;
@@ -646,7 +652,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       unsigned char* dst = base + kOffV + st * kVStage;
       uint4 a[8];                                   // keys key0 + 16 (i % 4), half i / 4
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const uint4*>(src + (i >> 2) * kV8Half + (i & 3) * 2048);
+      for (int i = 0; i < 8; ++i)
+        a[i] = lds128(smem_u32(src) + (i >> 2) * kV8Half + (i & 3) * 2048);
+      // the codes are in registers: the stage can be loaded again while they are widened
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.v8_empty[st]));
       if (keys < kHalfKeys) {                       // places behind the sequence: zeros
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -670,8 +680,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         widen(a[i].z, c1.x, c1.y);
         widen(a[i].w, c1.z, c1.w);
         unsigned char* d = dst + (i >> 2) * 2 * kVAtom + (i & 3) * 2048;
-        *reinterpret_cast<uint4*>(d + first) = swap ? c1 : c0;
-        *reinterpret_cast<uint4*>(d + second) = swap ? c0 : c1;
+        *reinterpret_cast<uint4*>(d + to0) = c0;
+        *reinterpret_cast<uint4*>(d + to1) = c1;
       }
       if (nan) {                                    // this thread's chunks once more, as they were stored
         bars.seg[seg].nan = 1;
@@ -689,10 +699,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       }
       fence_proxy_async_smem();                     // visible to the tensor cores behind v_full
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&bars.v_full[st]));
-        mbar_arrive(smem_u32(&bars.v8_empty[st]));
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&bars.v_full[st]));
     }
   } else if (warp >= kWarpSoft) {
     // ======================================= softmax (rows) =======================================
