@@ -4,13 +4,15 @@
 // Work.  The query rows of a (sequence, KV head) are its nodes times the GQA ratio, row r being
 // node r / ratio, head r % ratio of the group; they are cut into tiles of 128 rows.  A unit is
 // one row tile of one (sequence, KV head); it costs ceil(seq_len / 128) key tiles.  All units'
-// key tiles form one line, which is cut into equal pieces, one per CTA (each CTA works out its
-// piece from seq_lens and cu_seqlens_q on the device, so a captured call follows its buffers).
-// A unit that lies in one piece is written out at once; a unit cut by piece borders leaves one
-// partial output and log-sum-exp per piece in the workspace, and tree_reduce_kernel joins them.
-// A CTA has at most two partial units, the first and the last of its piece: two slots per CTA.
+// key tiles form one line, which is cut into equal pieces, one per CTA (worked out from seq_lens
+// and cu_seqlens_q on the device, so a captured call follows its buffers).  A unit that lies in one
+// piece is written out at once; a unit cut by piece borders leaves one partial output and
+// log-sum-exp per piece in the workspace, and tree_reduce_kernel joins them.  A CTA has at most two
+// partial units, the first and the last of its piece: two slots per CTA.  Where whole units, one a
+// CTA, take at most kCutTiles tiles longer than equal pieces, they are not cut: joining costs the
+// time of about so many tiles (a tile 1.25 us; the join 6 to 10 us).
 //
-// Roles (512 threads; warp 3 idle):
+// Roles (512 threads; warp 3 of the first CTA writes down what the reduce goes by):
 //   warp 0      the CTA's walk over its piece, published segment by segment, and the K pages by
 //               TMA (two 128-byte-wide boxes a page, 128B-swizzled), whole key tiles;
 //   warp 1      MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
@@ -86,6 +88,7 @@ constexpr int kSmemTree = kOffBar + kBarBytes;
 static_assert(kSmemTree == 232448, "all that a block may have");
 constexpr int kSCols = 128, kOCol = 256, kTmemCols = 512;
 constexpr float kTau = 6.f, kShift = 8.f;
+constexpr int kCutTiles = 8;
 constexpr uint32_t kBadLse = 0x7fd0bad1u;          // a partial of a sequence with a bad page (a NaN
                                                    // that no arithmetic makes)
 
@@ -107,9 +110,14 @@ struct TreeAttnParams {
   __nv_bfloat16* out;
   int64_t out_stride_tok, out_stride_head;
   int32_t* status;
-  int32_t ctas;              // pieces of the line
+  int32_t ctas;              // pieces of the line, at most
   float* o_part;             // [ctas][2][128][256]
   float* lse_part;           // [ctas][2][128]
+  // For the reduce, written by the main kernel's first CTA: the piece length (0: nothing was cut)
+  // and, per node, its sequence's place on the line, key tiles (0: nothing to join), row tiles and
+  // first row.
+  int32_t* piece;
+  int4* nodes;               // [total_q]
 };
 
 struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
@@ -181,9 +189,35 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
   return x;
 }
 
-// The line of W is cut into min(CTAs, W) pieces, so none is empty.  First place of piece g:
-__device__ __forceinline__ int piece_start(int g, int pieces, int W) {
-  return static_cast<int>(static_cast<int64_t>(g) * W / pieces);
+// How the line is cut: pieces of C tiles, piece g from g C on.  With V > 0 every unit takes V
+// places on the line, and so a piece of its own.
+struct Cut {
+  int C, V, length;
+};
+__device__ __forceinline__ int weight_of(const Seq& s, int hkv, int V) { return V ? s.T * hkv * V : s.w; }
+
+// By the whole warp; `mine` is lane l's sequence l (of the first 32).
+__device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const Seq& mine) {
+  int W = mine.w, U = mine.T * p.hkv, longest = mine.nt;
+#pragma unroll 1
+  for (int b0 = 32; b0 < p.num_seqs; b0 += 32) {
+    const Seq x = seq_at(p, b0 + lane);
+    W += x.w;
+    U += x.T * p.hkv;
+    longest = max(longest, x.nt);
+  }
+  W = __reduce_add_sync(0xffffffffu, W);
+  U = __reduce_add_sync(0xffffffffu, U);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  Cut c;
+  c.C = max(1, (W + p.ctas - 1) / p.ctas);
+  c.V = 0;
+  c.length = W;
+  if (U <= p.ctas && longest <= c.C + kCutTiles) {
+    c.C = c.V = longest;
+    c.length = U * longest;
+  }
+  return c;
 }
 
 // The K producer's walk over the units of its CTA's piece; 32 sequences are held, one a lane.
@@ -192,59 +226,56 @@ struct Walker {
   int b0, before;            // the held sequences, and the line before the first of them
   Seq mine;
   int upto;                  // running sum of the held sequences' weights
+  Cut cut;
 
-  __device__ __forceinline__ void hold(const TreeAttnParams& p, int lane) {
-    mine = seq_at(p, b0 + lane);
-    upto = warp_scan(mine.w, lane);
-  }
   __device__ __forceinline__ void start(const TreeAttnParams& p, int lane) {
-    int W = 0;
     b0 = before = 0;
-    hold(p, lane);
-    if (p.num_seqs <= 32) {
-      W = __shfl_sync(0xffffffffu, upto, 31);
-    } else {
-#pragma unroll 1
-      for (int c0 = 0; c0 < p.num_seqs; c0 += 32) W += seq_at(p, c0 + lane).w;
-      W = __reduce_add_sync(0xffffffffu, W);
-    }
-    const int pieces = min(p.ctas, W);
-    const int g = blockIdx.x;
-    lo = pos = g < pieces ? piece_start(g, pieces, W) : W;
-    hi = g < pieces ? piece_start(g + 1, pieces, W) : W;
+    mine = seq_at(p, lane);
+    cut = cut_line(p, lane, mine);
+    upto = warp_scan(weight_of(mine, p.hkv, cut.V), lane);
+    lo = pos = min(static_cast<int64_t>(cut.length), static_cast<int64_t>(blockIdx.x) * cut.C);
+    hi = min(static_cast<int64_t>(cut.length), static_cast<int64_t>(lo) + cut.C);
   }
   // The next segment; s.end if there is none.  Returns the sequence's error bits.
   __device__ __forceinline__ int next(const TreeAttnParams& p, int lane, Segment& s) {
     s.end = 1;
-    if (pos >= hi) return 0;
 #pragma unroll 1
-    while (true) {
+    while (pos < hi) {
       const int all = __shfl_sync(0xffffffffu, upto, 31);
-      if (pos < before + all) break;
-      before += all;
-      b0 += 32;
-      if (b0 >= p.num_seqs) return 0;               // lengths changed under the call
-      hold(p, lane);
+      if (pos >= before + all) {
+        before += all;
+        b0 += 32;
+        if (b0 >= p.num_seqs) return 0;             // lengths changed under the call
+        mine = seq_at(p, b0 + lane);
+        upto = warp_scan(weight_of(mine, p.hkv, cut.V), lane);
+        continue;
+      }
+      const int at = pos - before;
+      const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+      const int nt = __shfl_sync(0xffffffffu, mine.nt, f), T = __shfl_sync(0xffffffffu, mine.T, f);
+      const int places = cut.V ? cut.V : nt;        // of a unit on the line
+      const int in = at - (f ? __shfl_sync(0xffffffffu, upto, f - 1) : 0);
+      const int unit = in / places;
+      s.t0 = in - unit * places;
+      if (s.t0 >= nt) {                             // the rest of a unit's place
+        pos += places - s.t0;
+        continue;
+      }
+      s.b = b0 + f;
+      s.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
+      s.n = __shfl_sync(0xffffffffu, mine.n, f);
+      s.L = __shfl_sync(0xffffffffu, mine.L, f);
+      s.h = unit / T;
+      s.m = unit - s.h * T;
+      s.nt = nt;
+      s.T = T;
+      s.t1 = min(nt, s.t0 + hi - pos);
+      s.first = pos == lo;
+      s.end = s.bad = s.nan = 0;
+      pos += s.t1 - s.t0;
+      return __shfl_sync(0xffffffffu, mine.err, f);
     }
-    const int at = pos - before;
-    const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
-    const int nt = __shfl_sync(0xffffffffu, mine.nt, f), T = __shfl_sync(0xffffffffu, mine.T, f);
-    const int in = at - __shfl_sync(0xffffffffu, upto - mine.w, f);
-    s.b = b0 + f;
-    s.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
-    s.n = __shfl_sync(0xffffffffu, mine.n, f);
-    s.L = __shfl_sync(0xffffffffu, mine.L, f);
-    const int unit = in / nt;
-    s.h = unit / T;
-    s.m = unit - s.h * T;
-    s.nt = nt;
-    s.T = T;
-    s.t0 = in - unit * nt;
-    s.t1 = min(nt, s.t0 + hi - pos);
-    s.first = pos == lo;
-    s.end = s.bad = s.nan = 0;
-    pos += s.t1 - s.t0;
-    return __shfl_sync(0xffffffffu, mine.err, f);
+    return 0;
   }
 };
 
@@ -470,12 +501,6 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         }
       }
     }
-    if (blockIdx.x == 0)                            // sequences whose rows are not known
-#pragma unroll 1
-      for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-        const Seq x = seq_at(p, b0 + lane);
-        if (x.err && x.T == 0) set_status(p.status, x.err);
-      }
     // never leave with copies in flight
     if (lane == 0) {
       volatile int no_abort = 0;
@@ -628,6 +653,33 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         mbar_arrive(smem_u32(&bars.v8_full[st]));
       }
     }
+  } else if (warp == 3) {
+    // ================================ what the reduce goes by =====================================
+    if (blockIdx.x == 0) {
+      Seq x = seq_at(p, lane);
+      const Cut cut = cut_line(p, lane, x);
+      if (lane == 0) *p.piece = cut.V ? 0 : cut.C;
+      if (!cut.V)
+        for (int i = lane; i < p.total_q; i += 32) p.nodes[i] = make_int4(0, 0, 0, 0);
+      __syncwarp();
+      int before = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+        if (b0 > 0) x = seq_at(p, b0 + lane);
+        if (x.err && x.T == 0) set_status(p.status, x.err);   // rows whose place is not known
+        const int upto = warp_scan(x.w, lane);
+        if (!cut.V)
+#pragma unroll 1
+          for (int f = 0; f < min(32, p.num_seqs - b0); ++f) {
+            const int n = __shfl_sync(0xffffffffu, x.n, f), q0 = __shfl_sync(0xffffffffu, x.q0, f);
+            const int4 node = make_int4(before + (f ? __shfl_sync(0xffffffffu, upto, max(0, f - 1)) : 0),
+                                        __shfl_sync(0xffffffffu, x.err ? 0 : x.nt, f),
+                                        __shfl_sync(0xffffffffu, x.T, f), q0);
+            for (int i = lane; i < n; i += 32) p.nodes[q0 + i] = node;
+          }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
   } else if (warp >= kWarpWiden && warp < kWarpSoft) {
     // ======================================== V widening ==========================================
     // A thread takes one 16-byte chunk (16 dims) of the keys key0 + 16 i in both 128-dim halves: all
@@ -727,9 +779,13 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       return ok;
     };
 
-    // Half of the row quarter's rows as two e4m3 terms into the Q operand, a row at a time by the
-    // whole warp (8 dims a lane); their factors from raw products to log2 units (NaN for a row that
-    // is not finite) to the exchange, from where `factor` gets this thread's row's.
+    // Half of the row quarter's rows as two e4m3 terms into the Q operand.  The warp's 16 rows fill
+    // four blocks of 2 KB there (terms x 128-dim halves), as many bytes as the bf16 rows have: these
+    // are first copied to where their own terms will be, all rows in flight, and then taken a row
+    // at a time by the whole warp (8 dims a lane).  Loops stay rolled: fetching straight-line code
+    // for 8 rows at a time cost 9000 cycles at the start of every CTA.  The rows' factors from raw
+    // products to log2 units (NaN for a row that is not finite) go to the exchange, from where
+    // `factor` gets this thread's row's.
     auto prepare_q = [&](const Segment& y, float& factor) -> bool {
       const int row0 = 32 * quad + 16 * half;
       const int rows = y.n * p.ratio - y.m * kRows - row0;           // valid rows from there on
@@ -740,43 +796,45 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         const int t = mine / p.ratio, g = mine - t * p.ratio;
         const int64_t at = static_cast<int64_t>(y.q0 + t) * p.q_stride_tok +
                            static_cast<int64_t>(y.h * p.ratio + g) * p.q_stride_head;
+        // 16 bytes a lane: block lane / 8 of the four, 16 (lane % 8) bytes into the row's 128 there
+        const uint32_t own = smem_u32(base + kOffQ) + (lane >> 4) * kQTerm + ((lane >> 3) & 1) * kQHalf +
+                             row0 * 128 + (lane & 7) * 16;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int64_t src = __shfl_sync(0xffffffffu, at, i);
+          const uint32_t bytes = i < rows ? 16u : 0u;                // 0: zeros are written
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(own + i * 128),
+                       "l"(p.q + (i < rows ? src : 0) + 8 * lane), "r"(bytes) : "memory");
+        }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
         const int chunk = (lane & 15) >> 1;
         unsigned char* q_hi = base + kOffQ + (lane >> 4) * kQHalf + row0 * 128 + 8 * (lane & 1);
-#pragma unroll 1
-        for (int i0 = 0; i0 < 16; i0 += 8) {
-          uint4 x[8];
+#pragma unroll 2
+        for (int i = 0; i < 16; ++i) {
+          const uint4 x = lds128(own + i * 128);
+          const uint32_t ww[4] = {x.x, x.y, x.z, x.w};
+          uint32_t top = 0;                          // the largest |q| by its bits (NaN above all)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int64_t src = __shfl_sync(0xffffffffu, at, i0 + i);
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (i0 + i < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + src + 8 * lane));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t top = 0;                        // the largest |q| by its bits (NaN above all)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = max(top, max((ww[e] << 16) & 0x7fff0000u, ww[e] & 0x7fff0000u));
-            top = __reduce_max_sync(0xffffffffu, top);
-            const int e8 = static_cast<int>(top >> 23);              // exponent field
-            // 2^a takes the largest into [128, 256), as far as a = 126 does
-            const int a = top == 0u ? 0 : min(126, 134 - e8);
-            const float f = __uint_as_float(static_cast<uint32_t>(a + 127) << 23 | flip);
-            uint32_t hi[2], lo[2];
-            two_terms(__uint_as_float(ww[0] << 16) * f, __uint_as_float(ww[0] & 0xffff0000u) * f,
-                      __uint_as_float(ww[1] << 16) * f, __uint_as_float(ww[1] & 0xffff0000u) * f, hi[0], lo[0]);
-            two_terms(__uint_as_float(ww[2] << 16) * f, __uint_as_float(ww[2] & 0xffff0000u) * f,
-                      __uint_as_float(ww[3] << 16) * f, __uint_as_float(ww[3] & 0xffff0000u) * f, hi[1], lo[1]);
-            const int row = i0 + i;
-            unsigned char* dst = q_hi + row * 128 + ((chunk ^ (row & 7)) << 4);
-            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
-            if (lane == row)
-              to[row0 + row] = e8 == 255 || sl_in != sl_in
-                                   ? __int_as_float(0x7fc00000)
-                                   : fmaxf(sl * __int_as_float((127 - a) << 23), 1.17549435e-38f);
-          }
+          for (int e = 0; e < 4; ++e)
+            top = max(top, max((ww[e] << 16) & 0x7fff0000u, ww[e] & 0x7fff0000u));
+          top = __reduce_max_sync(0xffffffffu, top);   // (every lane has read its part)
+          const int e8 = static_cast<int>(top >> 23);                // exponent field
+          // 2^a takes the largest into [128, 256), as far as a = 126 does
+          const int a = top == 0u ? 0 : min(126, 134 - e8);
+          const float f = __uint_as_float(static_cast<uint32_t>(a + 127) << 23 | flip);
+          uint32_t hi[2], lo[2];
+          two_terms(__uint_as_float(ww[0] << 16) * f, __uint_as_float(ww[0] & 0xffff0000u) * f,
+                    __uint_as_float(ww[1] << 16) * f, __uint_as_float(ww[1] & 0xffff0000u) * f, hi[0], lo[0]);
+          two_terms(__uint_as_float(ww[2] << 16) * f, __uint_as_float(ww[2] & 0xffff0000u) * f,
+                    __uint_as_float(ww[3] << 16) * f, __uint_as_float(ww[3] & 0xffff0000u) * f, hi[1], lo[1]);
+          unsigned char* dst = q_hi + i * 128 + ((chunk ^ (i & 7)) << 4);
+          __syncwarp();
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
+          if (lane == i)
+            to[row0 + i] = e8 == 255 || sl_in != sl_in
+                               ? __int_as_float(0x7fc00000)
+                               : fmaxf(sl * __int_as_float((127 - a) << 23), 1.17549435e-38f);
         }
         fence_proxy_async_smem();
       }
@@ -838,22 +896,35 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             uint32_t o[32];
             tmem_ld16x256_x8(lane_addr + (static_cast<uint32_t>(16 * (c & 1)) << 16) + kOCol + d0, o);
             const float sc0 = __shfl_sync(0xffffffffu, sc, row), sc1 = __shfl_sync(0xffffffffu, sc, row + 8);
-            const int64_t at0 = __shfl_sync(0xffffffffu, at, row) + d0 + 2 * (lane & 3);
-            const int64_t at1 = __shfl_sync(0xffffffffu, at, row + 8) + d0 + 2 * (lane & 3);
+            const int64_t at0 = __shfl_sync(0xffffffffu, at, row), at1 = __shfl_sync(0xffffffffu, at, row + 8);
             tmem_ld_wait(o);
+            // Lane pairs trade 8-dim blocks: the even one takes the pair's 4 dims of block 2 k, the odd
+            // one those of block 2 k + 1, so that a store is 16 bytes and four lanes fill 64 of a row.
+            const int d = d0 + 8 * (lane & 1) + 4 * ((lane >> 1) & 1);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              // a factor of 0 (no key seen, or a bad page) gives zeros, whatever the sums hold
-              const float f0 = sc0 == 0.f ? 0.f : __uint_as_float(o[4 * k]) * sc0;
-              const float f1 = sc0 == 0.f ? 0.f : __uint_as_float(o[4 * k + 1]) * sc0;
-              const float f2 = sc1 == 0.f ? 0.f : __uint_as_float(o[4 * k + 2]) * sc1;
-              const float f3 = sc1 == 0.f ? 0.f : __uint_as_float(o[4 * k + 3]) * sc1;
-              if (whole) {
-                if (row < rows) *reinterpret_cast<__nv_bfloat162*>(p.out + at0 + 8 * k) = __floats2bfloat162_rn(f0, f1);
-                if (row + 8 < rows) *reinterpret_cast<__nv_bfloat162*>(p.out + at1 + 8 * k) = __floats2bfloat162_rn(f2, f3);
-              } else {
-                if (row < rows) *reinterpret_cast<float2*>(p.o_part + at0 + 8 * k) = make_float2(f0, f1);
-                if (row + 8 < rows) *reinterpret_cast<float2*>(p.o_part + at1 + 8 * k) = make_float2(f2, f3);
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {          // the row, and the one 8 below
+                const float scale = b ? sc1 : sc0;
+                float f[4];                          // own 2 dims of blocks 2 k and 2 k + 1
+#pragma unroll
+                for (int q = 0; q < 4; ++q)          // a factor of 0 (no key seen, or a bad page)
+                  f[q] = scale == 0.f ? 0.f          // gives zeros, whatever the sums hold
+                                      : __uint_as_float(o[8 * k + 4 * (q >> 1) + 2 * b + (q & 1)]) * scale;
+                const bool odd = lane & 1;
+                const float g0 = __shfl_xor_sync(0xffffffffu, odd ? f[0] : f[2], 1);
+                const float g1 = __shfl_xor_sync(0xffffffffu, odd ? f[1] : f[3], 1);
+                const float4 v = odd ? make_float4(g0, g1, f[2], f[3]) : make_float4(f[0], f[1], g0, g1);
+                if (row + 8 * b < rows) {
+                  const int64_t to = (b ? at1 : at0) + d + 16 * k;
+                  if (whole) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), z = __floats2bfloat162_rn(v.z, v.w);
+                    *reinterpret_cast<uint2*>(p.out + to) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                                                       *reinterpret_cast<const uint32_t*>(&z));
+                  } else {
+                    *reinterpret_cast<float4*>(p.o_part + to) = v;
+                  }
+                }
               }
             }
           }
@@ -1037,111 +1108,121 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   }
 }
 
-// Join the partials of the units that were cut: a warp a row, 8 dims a lane, all pieces of the
-// row weighted by 2^(lse - max).  A piece of a row that saw none of its keys has lse -inf and
-// counts nothing; a NaN in any other piece stays in the result.
-constexpr int kReduceWarps = 8;
+// Join the partials of the units that were cut, all pieces of a row weighted by 2^(lse - max).  A
+// piece of a row that saw none of its keys has lse -inf and counts nothing; a NaN in any other
+// piece stays in the result.  kWarps warps a row take its pieces in turn, 8 dims a lane, kAhead
+// pieces' loads in flight together with the log-sum-exps: what bounds it is that chain of two
+// round trips to L2 (the node's entry, then these), so many rows have to be in flight.  Few rows
+// (then cut into many pieces) get four warps each, many rows one.
+constexpr int kReduceThreads = 256, kAhead = 4;
 
-__global__ void __launch_bounds__(kReduceWarps * 32)
+template <int kWarps>
+__global__ void __launch_bounds__(kReduceThreads)
 tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kReduceWarps + (threadIdx.x >> 5);
-  const int tok = static_cast<int>(row / p.hq), head = static_cast<int>(row % p.hq);
+  __shared__ float s_acc[kReduceThreads / 32][kHeadDim];
+  __shared__ float s_sum[kReduceThreads / 32], s_top[kReduceThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kWarps;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kReduceThreads / 32 / kWarps) + warp / kWarps;
+  const int tok = static_cast<int>(row / p.hq), head = static_cast<int>(row - static_cast<int64_t>(tok) * p.hq);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  // the row's sequence, and its unit's place on the line
-  int W = 0, unit0 = 0, nt = 0, rt = 0;
-  bool mine = false;
-  if (tok < p.total_q) {
-    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-      const Seq x = seq_at(p, b0 + lane);
-      const int upto = warp_scan(x.w, lane);
-      const bool here = x.n > 0 && tok >= x.q0 && tok < x.q0 + x.n && !x.err;
-      const uint32_t who = __ballot_sync(0xffffffffu, here);
-      if (who && !mine) {
-        mine = true;
-        const int f = __ffs(who) - 1;
-        nt = __shfl_sync(0xffffffffu, x.nt, f);
-        const int T = __shfl_sync(0xffffffffu, x.T, f);
-        const int h = head / p.ratio;
-        rt = (tok - __shfl_sync(0xffffffffu, x.q0, f)) * p.ratio + head - h * p.ratio;
-        unit0 = W + __shfl_sync(0xffffffffu, upto - x.w, f) + (h * T + rt / kRows) * nt;
-        rt %= kRows;
-      }
-      W += __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
-  if (!mine) return;
-  const int pieces = min(p.ctas, W);
-  auto piece_of = [&](int x) {
-    return static_cast<int>(((static_cast<int64_t>(x) + 1) * pieces - 1) / W);
-  };
-  const int g0 = piece_of(unit0), g1 = piece_of(unit0 + nt - 1);
-  if (g0 == g1) return;                              // written whole
-  // lane i looks after piece g0 + i (and 32 further, ...): its slot and log-sum-exp
-  auto slot_of = [&](int g) {
-    return 2 * g + (unit0 <= piece_start(g, pieces, W) ? 0 : 1);
-  };
-  const int n = g1 - g0 + 1;
-  float M = -INFINITY;
-  bool bad = false;
-  int slot = 0;
-  float lse = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const int sl = slot_of(g0 + i);
-    const float x = __ldcg(p.lse_part + sl * kRows + rt);
-    bad |= __float_as_uint(x) == kBadLse;
-    M = fmaxf(M, x);
-    if (i < 32) {
-      slot = sl;
-      lse = x;
+  const int C = __ldcg(p.piece);
+  if (C == 0) return;                                // every unit was written whole
+  int n = 0, g0 = 0, unit0 = 0, rt = 0;              // pieces of the row, 0: nothing to join
+  if (tok < p.total_q) {
+    const int4 node = __ldcg(p.nodes + tok);
+    if (node.y > 0) {
+      const int h = head / p.ratio;
+      rt = (tok - node.w) * p.ratio + head - h * p.ratio;
+      unit0 = node.x + (h * node.z + rt / kRows) * node.y;
+      rt %= kRows;
+      g0 = unit0 / C;
+      n = (unit0 + node.y - 1) / C - g0 + 1;
+      if (n == 1) n = 0;                             // written whole
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  bad = __any_sync(0xffffffffu, bad);
-  float acc[8], wsum = 0.f;
+  // the unit starts its piece g, or lies across its start, in slot 0; else it is the last one in it
+  auto slot_of = [&](int g) -> int64_t {
+    return (static_cast<int64_t>(2 * g + (unit0 <= g * C ? 0 : 1)) * kRows + rt);
+  };
+  float acc[8], top = -INFINITY, sum = 0.f;
+  bool bad = false;
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < n && !bad; i0 += 32) {
-    if (i0 > 0) {
-      slot = i0 + lane < n ? slot_of(g0 + i0 + lane) : 0;
-      lse = i0 + lane < n ? __ldcg(p.lse_part + slot * kRows + rt) : -INFINITY;
+#pragma unroll 1
+  for (int i0 = part; i0 < n; i0 += kWarps * kAhead) {
+    float4 a[kAhead], b[kAhead];
+    float lse[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      lse[j] = -INFINITY;
+      if (i0 + j * kWarps < n) {
+        const int64_t at = slot_of(g0 + i0 + j * kWarps);
+        const float* o = p.o_part + at * kHeadDim + 8 * lane;
+        lse[j] = __ldcg(p.lse_part + at);
+        a[j] = __ldcg(reinterpret_cast<const float4*>(o));
+        b[j] = __ldcg(reinterpret_cast<const float4*>(o + 4));
+      }
     }
-    const float weight = lse == -INFINITY ? 0.f : exp2_hw(lse - M);   // NaN makes the row NaN
-    wsum += weight;
-    const int m = min(32, n - i0);
-    for (int j0 = 0; j0 < m; j0 += 8) {              // eight pieces' loads in flight
-      float4 a[8], b[8];
+    float t = top;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int sl = __shfl_sync(0xffffffffu, slot, (j0 + j) & 31);
-        const float* o = p.o_part + (static_cast<int64_t>(sl) * kRows + rt) * kHeadDim + 8 * lane;
-        if (j0 + j < m) {
-          a[j] = __ldcg(reinterpret_cast<const float4*>(o));
-          b[j] = __ldcg(reinterpret_cast<const float4*>(o + 4));
-        }
-      }
+    for (int j = 0; j < kAhead; ++j) {
+      bad |= __float_as_uint(lse[j]) == kBadLse;
+      t = fmaxf(t, lse[j]);                          // (NaN is passed over)
+    }
+    const float back = t == top ? 1.f : exp2_hw(top - t);
+    top = t;
+    sum *= back;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = __shfl_sync(0xffffffffu, weight, (j0 + j) & 31);
-        const float x = __shfl_sync(0xffffffffu, lse, (j0 + j) & 31);
-        if (j0 + j < m && x != -INFINITY) {          // (an empty piece's values are not used)
-          acc[0] = fmaf(w, a[j].x, acc[0]); acc[1] = fmaf(w, a[j].y, acc[1]);
-          acc[2] = fmaf(w, a[j].z, acc[2]); acc[3] = fmaf(w, a[j].w, acc[3]);
-          acc[4] = fmaf(w, b[j].x, acc[4]); acc[5] = fmaf(w, b[j].y, acc[5]);
-          acc[6] = fmaf(w, b[j].z, acc[6]); acc[7] = fmaf(w, b[j].w, acc[7]);
-        }
-      }
+    for (int e = 0; e < 8; ++e) acc[e] *= back;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (lse[j] == -INFINITY) continue;             // (an empty piece's values are not used)
+      const float w = exp2_hw(lse[j] - top);         // NaN makes the row NaN
+      sum += w;
+      acc[0] = fmaf(w, a[j].x, acc[0]); acc[1] = fmaf(w, a[j].y, acc[1]);
+      acc[2] = fmaf(w, a[j].z, acc[2]); acc[3] = fmaf(w, a[j].w, acc[3]);
+      acc[4] = fmaf(w, b[j].x, acc[4]); acc[5] = fmaf(w, b[j].y, acc[5]);
+      acc[6] = fmaf(w, b[j].z, acc[6]); acc[7] = fmaf(w, b[j].w, acc[7]);
     }
   }
+  if (kWarps > 1) {
+    if (lane == 0) {
+      s_sum[warp] = bad ? __uint_as_float(kBadLse) : sum;
+      s_top[warp] = top;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
-  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    for (int e = 0; e < 8; e += 4)
+      *reinterpret_cast<float4*>(&s_acc[warp][8 * lane + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+    __syncthreads();
+    if (part > 0) return;
+    float t = top;
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) t = fmaxf(t, s_top[warp + k]);
+    if (top != t) {
+      const float back = exp2_hw(top - t);
+      sum *= back;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] *= back;
+    }
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) {
+      const float x = s_sum[warp + k];
+      bad |= __float_as_uint(x) == kBadLse;
+      if (s_sum[warp + k] == 0.f) continue;          // none of its pieces counted
+      const float w = s_top[warp + k] == t ? 1.f : exp2_hw(s_top[warp + k] - t);
+      sum = fmaf(w, x, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, s_acc[warp + k][8 * lane + e], acc[e]);
+    }
+  }
+  if (n == 0) return;
+  const float inv = sum == 0.f || bad ? 0.f : 1.f / sum;
   uint32_t h[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    const __nv_bfloat162 v = inv == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
+                                        : __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     h[e] = *reinterpret_cast<const uint32_t*>(&v);
   }
   *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(tok) * p.out_stride_tok +
@@ -1244,7 +1325,9 @@ extern "C" size_t mtp_tree_attn_workspace_size(int32_t num_seqs, int32_t total_q
   const int64_t ctas = std::min<int64_t>(
       sms, line_bound(num_seqs, total_q, num_kv_heads, num_q_heads / num_kv_heads, max_pages_per_seq));
   // partial outputs, then their log-sum-exps; two slots of 128 rows a CTA
-  return align256(static_cast<size_t>(ctas) * 2 * kRows * (kHeadDim + 1) * sizeof(float)) + 256;
+  // then the nodes' entries and the piece length
+  return align256(static_cast<size_t>(ctas) * 2 * kRows * (kHeadDim + 1) * sizeof(float)) +
+         align256(static_cast<size_t>(total_q) * sizeof(int4)) + 256;
 }
 
 extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_head,
@@ -1323,6 +1406,9 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
       device_sm_count(device), line_bound(num_seqs, total_q, num_kv_heads, ratio, max_pages_per_seq)));
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = p.o_part + static_cast<int64_t>(p.ctas) * 2 * kRows * kHeadDim;
+  p.piece = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + need - 256);
+  p.nodes = reinterpret_cast<int4*>(static_cast<char*>(workspace) + need - 256 -
+                                    align256(static_cast<size_t>(total_q) * sizeof(int4)));
   AttnParams cache{};                                // what the tensor map goes by
   cache.k_cache = static_cast<const uint8_t*>(k_cache);
   cache.v_cache = p.v_cache;
@@ -1343,11 +1429,13 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
   if (launch_pdl(reinterpret_cast<const void*>(tree_attn_kernel), dim3(p.ctas), kTreeThreads, kSmemTree,
                  st, p) != cudaSuccess)
     return MTPATTN_E_LAUNCH;
-  // sequences of one key tile are never cut
+  // units of one key tile are never cut
   if (max_pages_per_seq <= kTilePages) return MTPATTN_OK;
   const int64_t rows = static_cast<int64_t>(total_q) * num_q_heads;
-  const dim3 grid(static_cast<unsigned>((rows + kReduceWarps - 1) / kReduceWarps));
-  return launch_pdl(reinterpret_cast<const void*>(tree_reduce_kernel), grid, kReduceWarps * 32, 0, st, p) ==
-                 cudaSuccess
-             ? MTPATTN_OK : MTPATTN_E_LAUNCH;
+  const int warps = rows < 4096 ? 4 : 1;             // a row
+  const int per = kReduceThreads / 32 / warps;
+  const dim3 grid(static_cast<unsigned>((rows + per - 1) / per));
+  const void* kernel = warps == 4 ? reinterpret_cast<const void*>(tree_reduce_kernel<4>)
+                                  : reinterpret_cast<const void*>(tree_reduce_kernel<1>);
+  return launch_pdl(kernel, grid, kReduceThreads, 0, st, p) == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
