@@ -3,16 +3,17 @@
 //
 // Work.  The query rows of a (sequence, KV head) are its nodes times the GQA ratio, row r being
 // node r / ratio, head r % ratio of the group; they are cut into tiles of 128 rows.  A unit is
-// one row tile of one (sequence, KV head); it costs ceil(seq_len / 128) key tiles.  All units'
-// key tiles form one line, which is cut into equal pieces, one per CTA (worked out from seq_lens
-// and cu_seqlens_q on the device, so a captured call follows its buffers).  A unit that lies in one
-// piece is written out at once; a unit cut by piece borders leaves one partial output and
-// log-sum-exp per piece in the workspace, and tree_reduce_kernel joins them.  A CTA has at most two
-// partial units, the first and the last of its piece: two slots per CTA.  Where whole units, one a
-// CTA, take at most kCutTiles tiles longer than equal pieces, they are not cut: joining costs the
-// time of about so many tiles (a tile 1.25 us; the join 6 to 10 us).
+// one row tile of one (sequence, KV head); it takes ceil(seq_len / 128) key tiles, and about
+// kUnitTiles' time more for its Q and its output.  All units stand in a line, a place for each of
+// these, which is cut into equal pieces, one per CTA (worked out from seq_lens and cu_seqlens_q on
+// the device, so a captured call follows its buffers).  A unit whose key tiles lie in one piece is
+// written out at once; a unit cut by piece borders leaves one partial output and log-sum-exp per
+// piece in the workspace, and tree_reduce_kernel joins them: the CTA behind a unit's first cut
+// leaves a note for it.  A CTA has at most two partial units, the first and the last of its piece:
+// two slots per CTA.  Where whole units, one a CTA, take at most kCutTiles tiles longer than equal
+// pieces, they are not cut (joining takes about as long).
 //
-// Roles (512 threads; warp 3 of the first CTA writes down what the reduce goes by):
+// Roles (512 threads; warp 3 only reports sequences whose rows are not known):
 //   warp 0      the CTA's walk over its piece, published segment by segment, and the K pages by
 //               TMA (two 128-byte-wide boxes a page, 128B-swizzled), whole key tiles;
 //   warp 1      MMA: one elected lane issues tcgen05.mma and commits; owns the TMEM allocation;
@@ -88,9 +89,17 @@ constexpr int kSmemTree = kOffBar + kBarBytes;
 static_assert(kSmemTree == 232448, "all that a block may have");
 constexpr int kSCols = 128, kOCol = 256, kTmemCols = 512;
 constexpr float kTau = 6.f, kShift = 8.f;
-constexpr int kCutTiles = 8;
+constexpr int kCutTiles = 6, kUnitTiles = 3;
 constexpr uint32_t kBadLse = 0x7fd0bad1u;          // a partial of a sequence with a bad page (a NaN
                                                    // that no arithmetic makes)
+
+// What CTA g leaves for the reduce: the unit whose first cut is at the start of piece g.
+struct JoinNote {
+  int pieces;                // it lies in, 0: there is none
+  int first, first_slot;     // the first of them, and the unit's slot there (in the others, 0)
+  int q0, h, m, rows;        // its first node, KV head, row tile; valid rows of the tile
+  int pad;
+};
 
 struct TreeAttnParams {
   CUtensorMap tmap_k, tmap_v;
@@ -111,13 +120,9 @@ struct TreeAttnParams {
   int64_t out_stride_tok, out_stride_head;
   int32_t* status;
   int32_t ctas;              // pieces of the line, at most
-  float* o_part;             // [ctas][2][128][256]
+  float* o_part;             // [ctas][2][64][128][4]: blocks of 4 dims, rows, dims
   float* lse_part;           // [ctas][2][128]
-  // For the reduce, written by the main kernel's first CTA: the piece length (0: nothing was cut)
-  // and, per node, its sequence's place on the line, key tiles (0: nothing to join), row tiles and
-  // first row.
-  int32_t* piece;
-  int4* nodes;               // [total_q]
+  struct JoinNote* notes;    // [ctas]
 };
 
 struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
@@ -168,7 +173,7 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnParams& p, int q0, int q1, i
   else if (L > p.max_pages * kPage) s.err = MTPATTN_ERR_SEQ_TOO_LONG;
   s.T = (s.n * p.ratio + kRows - 1) / kRows;
   s.nt = s.err ? 1 : (L + kKeys - 1) / kKeys;
-  s.w = s.T * s.nt * p.hkv;
+  s.w = s.T * (s.nt + kUnitTiles) * p.hkv;
   return s;
 }
 
@@ -189,7 +194,7 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
   return x;
 }
 
-// How the line is cut: pieces of C tiles, piece g from g C on.  With V > 0 every unit takes V
+// How the line is cut: pieces of C places, piece g from g C on.  With V > 0 every unit takes V
 // places on the line, and so a piece of its own.
 struct Cut {
   int C, V, length;
@@ -213,7 +218,7 @@ __device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const
   c.C = max(1, (W + p.ctas - 1) / p.ctas);
   c.V = 0;
   c.length = W;
-  if (U <= p.ctas && longest <= c.C + kCutTiles) {
+  if (U <= p.ctas && longest + kUnitTiles <= c.C + kCutTiles) {
     c.C = c.V = longest;
     c.length = U * longest;
   }
@@ -226,10 +231,11 @@ struct Walker {
   int b0, before;            // the held sequences, and the line before the first of them
   Seq mine;
   int upto;                  // running sum of the held sequences' weights
+  int unit0, unit_places;    // of the last segment's unit, on the line
   Cut cut;
 
   __device__ __forceinline__ void start(const TreeAttnParams& p, int lane) {
-    b0 = before = 0;
+    b0 = before = unit0 = unit_places = 0;
     mine = seq_at(p, lane);
     cut = cut_line(p, lane, mine);
     upto = warp_scan(weight_of(mine, p.hkv, cut.V), lane);
@@ -253,14 +259,17 @@ struct Walker {
       const int at = pos - before;
       const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
       const int nt = __shfl_sync(0xffffffffu, mine.nt, f), T = __shfl_sync(0xffffffffu, mine.T, f);
-      const int places = cut.V ? cut.V : nt;        // of a unit on the line
+      const int extra = cut.V ? 0 : kUnitTiles;     // places ahead of the unit's key tiles
+      const int places = cut.V ? cut.V : nt + extra;
       const int in = at - (f ? __shfl_sync(0xffffffffu, upto, f - 1) : 0);
-      const int unit = in / places;
-      s.t0 = in - unit * places;
-      if (s.t0 >= nt) {                             // the rest of a unit's place
-        pos += places - s.t0;
-        continue;
-      }
+      const int unit = in / places, in_unit = in - unit * places;
+      unit0 = pos - in_unit;
+      unit_places = places;
+      const int to = min(places, in_unit + hi - pos);                // of the unit, in this piece
+      s.t0 = max(0, in_unit - extra);
+      s.t1 = min(nt, to - extra);
+      pos += to - in_unit;
+      if (s.t0 >= s.t1) continue;                   // none of its key tiles
       s.b = b0 + f;
       s.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
       s.n = __shfl_sync(0xffffffffu, mine.n, f);
@@ -269,13 +278,25 @@ struct Walker {
       s.m = unit - s.h * T;
       s.nt = nt;
       s.T = T;
-      s.t1 = min(nt, s.t0 + hi - pos);
-      s.first = pos == lo;
+      s.first = unit0 <= lo;
       s.end = s.bad = s.nan = 0;
-      pos += s.t1 - s.t0;
       return __shfl_sync(0xffffffffu, mine.err, f);
     }
     return 0;
+  }
+  // What the reduce has to know of the CTA's first segment.
+  __device__ __forceinline__ JoinNote note(const TreeAttnParams& p, const Segment& s) const {
+    JoinNote n;
+    const int g = blockIdx.x;
+    n.first = (unit0 + kUnitTiles) / cut.C;
+    n.pieces = !s.end && !cut.V && s.t0 > 0 && n.first == g - 1 ? (unit0 + unit_places - 1) / cut.C - n.first + 1 : 0;
+    n.first_slot = unit0 <= n.first * cut.C ? 0 : 1;
+    n.q0 = s.q0;
+    n.h = s.h;
+    n.m = s.m;
+    n.rows = min(kRows, s.n * p.ratio - s.m * kRows);
+    n.pad = 0;
+    return n;
   }
 };
 
@@ -441,10 +462,14 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
     uint32_t u = 0;
     int e = 0;
-    bool ok = true;
+    bool ok = true, noted = false;
     while (ok) {
       Segment s;
       const int err = walk.next(p, lane, s);
+      if (!noted) {
+        noted = true;
+        if (lane == 0) p.notes[blockIdx.x] = walk.note(p, s);
+      }
       if (err && !s.end) {
         // zeros for the rows of a sequence that cannot be computed, here: it has no key tiles
         if (lane == 0) set_status(p.status, err);
@@ -654,32 +679,13 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       }
     }
   } else if (warp == 3) {
-    // ================================ what the reduce goes by =====================================
-    if (blockIdx.x == 0) {
-      Seq x = seq_at(p, lane);
-      const Cut cut = cut_line(p, lane, x);
-      if (lane == 0) *p.piece = cut.V ? 0 : cut.C;
-      if (!cut.V)
-        for (int i = lane; i < p.total_q; i += 32) p.nodes[i] = make_int4(0, 0, 0, 0);
-      __syncwarp();
-      int before = 0;
+    // ============================ sequences whose rows are not known ==============================
+    if (blockIdx.x == 0)
 #pragma unroll 1
       for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-        if (b0 > 0) x = seq_at(p, b0 + lane);
-        if (x.err && x.T == 0) set_status(p.status, x.err);   // rows whose place is not known
-        const int upto = warp_scan(x.w, lane);
-        if (!cut.V)
-#pragma unroll 1
-          for (int f = 0; f < min(32, p.num_seqs - b0); ++f) {
-            const int n = __shfl_sync(0xffffffffu, x.n, f), q0 = __shfl_sync(0xffffffffu, x.q0, f);
-            const int4 node = make_int4(before + (f ? __shfl_sync(0xffffffffu, upto, max(0, f - 1)) : 0),
-                                        __shfl_sync(0xffffffffu, x.err ? 0 : x.nt, f),
-                                        __shfl_sync(0xffffffffu, x.T, f), q0);
-            for (int i = lane; i < n; i += 32) p.nodes[q0 + i] = node;
-          }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        const Seq x = seq_at(p, b0 + lane);
+        if (x.err && x.T == 0) set_status(p.status, x.err);
       }
-    }
   } else if (warp >= kWarpWiden && warp < kWarpSoft) {
     // ======================================== V widening ==========================================
     // A thread takes one 16-byte chunk (16 dims) of the keys key0 + 16 i in both 128-dim halves: all
@@ -809,32 +815,43 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         asm volatile("cp.async.wait_all;\n" ::: "memory");
         const int chunk = (lane & 15) >> 1;
         unsigned char* q_hi = base + kOffQ + (lane >> 4) * kQHalf + row0 * 128 + 8 * (lane & 1);
-#pragma unroll 2
-        for (int i = 0; i < 16; ++i) {
-          const uint4 x = lds128(own + i * 128);
-          const uint32_t ww[4] = {x.x, x.y, x.z, x.w};
-          uint32_t top = 0;                          // the largest |q| by its bits (NaN above all)
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 4) {         // four rows' chains of steps side by side
+          uint4 x[4];
+          uint32_t top[4];                           // the largest |q| by its bits (NaN above all)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = max(top, max((ww[e] << 16) & 0x7fff0000u, ww[e] & 0x7fff0000u));
-          top = __reduce_max_sync(0xffffffffu, top);   // (every lane has read its part)
-          const int e8 = static_cast<int>(top >> 23);                // exponent field
-          // 2^a takes the largest into [128, 256), as far as a = 126 does
-          const int a = top == 0u ? 0 : min(126, 134 - e8);
-          const float f = __uint_as_float(static_cast<uint32_t>(a + 127) << 23 | flip);
-          uint32_t hi[2], lo[2];
-          two_terms(__uint_as_float(ww[0] << 16) * f, __uint_as_float(ww[0] & 0xffff0000u) * f,
-                    __uint_as_float(ww[1] << 16) * f, __uint_as_float(ww[1] & 0xffff0000u) * f, hi[0], lo[0]);
-          two_terms(__uint_as_float(ww[2] << 16) * f, __uint_as_float(ww[2] & 0xffff0000u) * f,
-                    __uint_as_float(ww[3] << 16) * f, __uint_as_float(ww[3] & 0xffff0000u) * f, hi[1], lo[1]);
-          unsigned char* dst = q_hi + i * 128 + ((chunk ^ (i & 7)) << 4);
-          __syncwarp();
-          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
-          if (lane == i)
-            to[row0 + i] = e8 == 255 || sl_in != sl_in
-                               ? __int_as_float(0x7fc00000)
-                               : fmaxf(sl * __int_as_float((127 - a) << 23), 1.17549435e-38f);
+          for (int i = 0; i < 4; ++i) x[i] = lds128(own + (i0 + i) * 128);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            top[i] = max(max(max((x[i].x << 16) & 0x7fff0000u, x[i].x & 0x7fff0000u),
+                             max((x[i].y << 16) & 0x7fff0000u, x[i].y & 0x7fff0000u)),
+                         max(max((x[i].z << 16) & 0x7fff0000u, x[i].z & 0x7fff0000u),
+                             max((x[i].w << 16) & 0x7fff0000u, x[i].w & 0x7fff0000u)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+          __syncwarp();                              // every lane has read its part of the rows
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = i0 + i;
+            const int e8 = static_cast<int>(top[i] >> 23);           // exponent field
+            // 2^a takes the largest into [128, 256), as far as a = 126 does
+            const int a = top[i] == 0u ? 0 : min(126, 134 - e8);
+            const float f = __uint_as_float(static_cast<uint32_t>(a + 127) << 23 | flip);
+            const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              two_terms(__uint_as_float(ww[2 * k] << 16) * f, __uint_as_float(ww[2 * k] & 0xffff0000u) * f,
+                        __uint_as_float(ww[2 * k + 1] << 16) * f, __uint_as_float(ww[2 * k + 1] & 0xffff0000u) * f,
+                        hi[k], lo[k]);
+            unsigned char* dst = q_hi + row * 128 + ((chunk ^ (row & 7)) << 4);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
+            if (lane == row)
+              to[row0 + row] = e8 == 255 || sl_in != sl_in
+                                   ? __int_as_float(0x7fc00000)
+                                   : fmaxf(sl * __int_as_float((127 - a) << 23), 1.17549435e-38f);
+          }
         }
         fence_proxy_async_smem();
       }
@@ -882,69 +899,55 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
         if (active) {
           const float sc = l != 0.f && !bad ? vd / l : 0.f;   // NaN stays NaN
           const int slot = 2 * blockIdx.x + (s.first ? 0 : 1);
-          const int rows = s.n * p.ratio - s.m * kRows - 32 * quad;   // valid rows of this quarter
           const int rr = s.m * kRows + r, node = rr / p.ratio;
-          // where this thread's row goes: an output row, or a partial one
-          const int64_t at = whole ? static_cast<int64_t>(s.q0 + node) * p.out_stride_tok +
-                                         static_cast<int64_t>(s.h * p.ratio + rr - node * p.ratio) * p.out_stride_head
-                                   : (static_cast<int64_t>(slot) * kRows + r) * kHeadDim;
-          // 16 rows x 64 dims a step: four lanes hold 8 consecutive dims of a row
+          // where this thread's row goes: an output row, or dims 0 .. 3 of a partial one, whose blocks
+          // of 4 dims are 128 rows apart, so that a warp's store is 512 bytes in a piece
+          __nv_bfloat16* row_out = p.out + static_cast<int64_t>(s.q0 + node) * p.out_stride_tok +
+                                   static_cast<int64_t>(s.h * p.ratio + rr - node * p.ratio) * p.out_stride_head;
+          float* row_part = p.o_part + (static_cast<int64_t>(slot) * (kHeadDim / 4) * kRows + r) * 4;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            const int d0 = 128 * half + 64 * (c >> 1);
-            const int row = 16 * (c & 1) + (lane >> 2);              // and row + 8
+            const int d0 = 128 * half + 32 * c;
             uint32_t o[32];
-            tmem_ld16x256_x8(lane_addr + (static_cast<uint32_t>(16 * (c & 1)) << 16) + kOCol + d0, o);
-            const float sc0 = __shfl_sync(0xffffffffu, sc, row), sc1 = __shfl_sync(0xffffffffu, sc, row + 8);
-            const int64_t at0 = __shfl_sync(0xffffffffu, at, row), at1 = __shfl_sync(0xffffffffu, at, row + 8);
+            tmem_ld32(lane_addr + kOCol + d0, o);
             tmem_ld_wait(o);
-            // Lane pairs trade 8-dim blocks: the even one takes the pair's 4 dims of block 2 k, the odd
-            // one those of block 2 k + 1, so that a store is 16 bytes and four lanes fill 64 of a row.
-            const int d = d0 + 8 * (lane & 1) + 4 * ((lane >> 1) & 1);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int i = 0; i < 32; ++i)             // a factor of 0 (no key seen, or a bad page) gives
+              o[i] = sc == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * sc);   // zeros in any case
+            if (valid) {
+              if (whole) {
 #pragma unroll
-              for (int b = 0; b < 2; ++b) {          // the row, and the one 8 below
-                const float scale = b ? sc1 : sc0;
-                float f[4];                          // own 2 dims of blocks 2 k and 2 k + 1
+                for (int i = 0; i < 32; i += 8) {
+                  uint32_t w[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)          // a factor of 0 (no key seen, or a bad page)
-                  f[q] = scale == 0.f ? 0.f          // gives zeros, whatever the sums hold
-                                      : __uint_as_float(o[8 * k + 4 * (q >> 1) + 2 * b + (q & 1)]) * scale;
-                const bool odd = lane & 1;
-                const float g0 = __shfl_xor_sync(0xffffffffu, odd ? f[0] : f[2], 1);
-                const float g1 = __shfl_xor_sync(0xffffffffu, odd ? f[1] : f[3], 1);
-                const float4 v = odd ? make_float4(g0, g1, f[2], f[3]) : make_float4(f[0], f[1], g0, g1);
-                if (row + 8 * b < rows) {
-                  const int64_t to = (b ? at1 : at0) + d + 16 * k;
-                  if (whole) {
-                    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), z = __floats2bfloat162_rn(v.z, v.w);
-                    *reinterpret_cast<uint2*>(p.out + to) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
-                                                                       *reinterpret_cast<const uint32_t*>(&z));
-                  } else {
-                    *reinterpret_cast<float4*>(p.o_part + to) = v;
+                  for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1]));
+                    w[k] = *reinterpret_cast<const uint32_t*>(&x);
                   }
+                  *reinterpret_cast<uint4*>(row_out + d0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  *reinterpret_cast<uint4*>(row_part + (d0 + i) * kRows) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
               }
             }
           }
-          if (nan_v && !bad) {
-            // NaN values of the nodes that this thread's row sees, behind the stores above
-            __syncwarp();
-            if (valid)
+          if (nan_v && !bad && valid) {
+            // NaN values of the nodes that this row sees
 #pragma unroll 1
-              for (uint64_t w = word; w; w &= w - 1) {
-                const int key = s.L - s.n + __ffsll(static_cast<long long>(w)) - 1;
-                if (key < s.t0 * kKeys || key >= s.t1 * kKeys) continue;
-                const int page = p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + key / kPage];
-                const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim;
+            for (uint64_t w = word; w; w &= w - 1) {
+              const int key = s.L - s.n + __ffsll(static_cast<long long>(w)) - 1;
+              if (key < s.t0 * kKeys || key >= s.t1 * kKeys) continue;
+              const int page = p.block_tables[static_cast<int64_t>(s.b) * p.max_pages + key / kPage];
+              const uint8_t* src = p.v_cache + ((static_cast<int64_t>(page) * kPage + key % kPage) * p.hkv + s.h) * kHeadDim;
 #pragma unroll 1
-                for (int d = 128 * half; d < 128 * half + 128; ++d)
-                  if ((src[d] & 0x7f) == 0x7f) {
-                    if (whole) p.out[at + d] = __float2bfloat16(__int_as_float(0x7fc00000));
-                    else p.o_part[at + d] = __int_as_float(0x7fc00000);
-                  }
-              }
+              for (int d = 128 * half; d < 128 * half + 128; ++d)
+                if ((src[d] & 0x7f) == 0x7f) {
+                  if (whole) row_out[d] = __float2bfloat16(__int_as_float(0x7fc00000));
+                  else row_part[(d / 4) * 4 * kRows + d % 4] = __int_as_float(0x7fc00000);
+                }
+            }
           }
           if (!whole && valid && half == 0)
             p.lse_part[slot * kRows + r] = bad ? __uint_as_float(kBadLse)
@@ -1108,126 +1111,89 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   }
 }
 
-// Join the partials of the units that were cut, all pieces of a row weighted by 2^(lse - max).  A
+// Join the partials of the units that were cut, a row's pieces weighted by 2^(lse - max).  A CTA
+// takes 32 rows and 32 dims of a unit: thread = row (lane) and 4 dims (warp), so every load of a
+// piece is 512 bytes in a piece, kAhead of them in flight; the weights are made once per CTA.  A
 // piece of a row that saw none of its keys has lse -inf and counts nothing; a NaN in any other
-// piece stays in the result.  kWarps warps a row take its pieces in turn, 8 dims a lane, kAhead
-// pieces' loads in flight together with the log-sum-exps: what bounds it is that chain of two
-// round trips to L2 (the node's entry, then these), so many rows have to be in flight.  Few rows
-// (then cut into many pieces) get four warps each, many rows one.
-constexpr int kReduceThreads = 256, kAhead = 4;
+// piece stays in the result.
+constexpr int kReduceThreads = 256, kAhead = 8, kReduceCtas = 4 * (kHeadDim / 32);   // a unit
 
-template <int kWarps>
 __global__ void __launch_bounds__(kReduceThreads)
 tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
-  __shared__ float s_acc[kReduceThreads / 32][kHeadDim];
-  __shared__ float s_sum[kReduceThreads / 32], s_top[kReduceThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kWarps;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kReduceThreads / 32 / kWarps) + warp / kWarps;
-  const int tok = static_cast<int>(row / p.hq), head = static_cast<int>(row - static_cast<int64_t>(tok) * p.hq);
+  extern __shared__ float s_w[];                     // [pieces][32 rows]: lse, then weights
+  __shared__ float s_top[kReduceThreads / 32][32], s_sum[kReduceThreads / 32][32];
+  __shared__ int s_bad;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = blockIdx.y / (kHeadDim / 32), d = 32 * (blockIdx.y % (kHeadDim / 32)) + 4 * warp;
+  const int r = 32 * q + lane;                       // row of the unit
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (threadIdx.x == 0) s_bad = 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
-  const int C = __ldcg(p.piece);
-  if (C == 0) return;                                // every unit was written whole
-  int n = 0, g0 = 0, unit0 = 0, rt = 0;              // pieces of the row, 0: nothing to join
-  if (tok < p.total_q) {
-    const int4 node = __ldcg(p.nodes + tok);
-    if (node.y > 0) {
-      const int h = head / p.ratio;
-      rt = (tok - node.w) * p.ratio + head - h * p.ratio;
-      unit0 = node.x + (h * node.z + rt / kRows) * node.y;
-      rt %= kRows;
-      g0 = unit0 / C;
-      n = (unit0 + node.y - 1) / C - g0 + 1;
-      if (n == 1) n = 0;                             // written whole
-    }
-  }
-  // the unit starts its piece g, or lies across its start, in slot 0; else it is the last one in it
-  auto slot_of = [&](int g) -> int64_t {
-    return (static_cast<int64_t>(2 * g + (unit0 <= g * C ? 0 : 1)) * kRows + rt);
-  };
-  float acc[8], top = -INFINITY, sum = 0.f;
+  const int4 n0 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x));
+  const int n = n0.x;                                // pieces
+  if (n == 0) return;                                // (the same for the whole CTA)
+  const int4 n1 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x) + 1);
+  const int q0 = n0.w, h = n1.x, m = n1.y, rows = n1.z;
+  if (32 * q >= rows) return;
+  auto slot_of = [&](int i) -> int64_t { return 2 * (n0.y + i) + (i == 0 ? n0.z : 0); };
+  float top = -INFINITY;
   bool bad = false;
+  __syncthreads();
+  for (int i = warp; i < n; i += kReduceThreads / 32) {
+    const float x = __ldcg(p.lse_part + slot_of(i) * kRows + r);
+    s_w[i * 32 + lane] = x;
+    if (r < rows) bad |= __float_as_uint(x) == kBadLse;
+    top = fmaxf(top, x);                             // (NaN is passed over)
+  }
+  s_top[warp][lane] = top;
+  if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
+  // the pieces' own loads do not wait for the weights
+  const float* src = p.o_part + (static_cast<int64_t>(d / 4) * kRows + r) * 4;
+  constexpr int64_t kSlot = static_cast<int64_t>(kHeadDim) * kRows;
+  float4 a[kAhead];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  for (int j = 0; j < kAhead; ++j)
+    if (j < n) a[j] = __ldcg(reinterpret_cast<const float4*>(src + slot_of(j) * kSlot));
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kReduceThreads / 32; ++w) top = fmaxf(top, s_top[w][lane]);
+  float sum = 0.f;
+  for (int i = warp; i < n; i += kReduceThreads / 32) {
+    const float x = s_w[i * 32 + lane];
+    const float w = x == -INFINITY ? 0.f : exp2_hw(x - top);   // a NaN makes the row NaN
+    s_w[i * 32 + lane] = w;
+    sum += w;
+  }
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kReduceThreads / 32; ++w) sum += s_sum[w][lane];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int i0 = part; i0 < n; i0 += kWarps * kAhead) {
-    float4 a[kAhead], b[kAhead];
-    float lse[kAhead];
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    if (i0 > 0) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      lse[j] = -INFINITY;
-      if (i0 + j * kWarps < n) {
-        const int64_t at = slot_of(g0 + i0 + j * kWarps);
-        const float* o = p.o_part + at * kHeadDim + 8 * lane;
-        lse[j] = __ldcg(p.lse_part + at);
-        a[j] = __ldcg(reinterpret_cast<const float4*>(o));
-        b[j] = __ldcg(reinterpret_cast<const float4*>(o + 4));
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j < n) a[j] = __ldcg(reinterpret_cast<const float4*>(src + slot_of(i0 + j) * kSlot));
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i0 + j < n) {
+        const float w = s_w[(i0 + j) * 32 + lane];
+        // (the values of a piece without weight may be anything only where it is empty: then zeros)
+        acc.x = fmaf(w, a[j].x, acc.x); acc.y = fmaf(w, a[j].y, acc.y);
+        acc.z = fmaf(w, a[j].z, acc.z); acc.w = fmaf(w, a[j].w, acc.w);
       }
-    }
-    float t = top;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      bad |= __float_as_uint(lse[j]) == kBadLse;
-      t = fmaxf(t, lse[j]);                          // (NaN is passed over)
-    }
-    const float back = t == top ? 1.f : exp2_hw(top - t);
-    top = t;
-    sum *= back;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= back;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (lse[j] == -INFINITY) continue;             // (an empty piece's values are not used)
-      const float w = exp2_hw(lse[j] - top);         // NaN makes the row NaN
-      sum += w;
-      acc[0] = fmaf(w, a[j].x, acc[0]); acc[1] = fmaf(w, a[j].y, acc[1]);
-      acc[2] = fmaf(w, a[j].z, acc[2]); acc[3] = fmaf(w, a[j].w, acc[3]);
-      acc[4] = fmaf(w, b[j].x, acc[4]); acc[5] = fmaf(w, b[j].y, acc[5]);
-      acc[6] = fmaf(w, b[j].z, acc[6]); acc[7] = fmaf(w, b[j].w, acc[7]);
-    }
   }
-  if (kWarps > 1) {
-    if (lane == 0) {
-      s_sum[warp] = bad ? __uint_as_float(kBadLse) : sum;
-      s_top[warp] = top;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e += 4)
-      *reinterpret_cast<float4*>(&s_acc[warp][8 * lane + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-    __syncthreads();
-    if (part > 0) return;
-    float t = top;
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) t = fmaxf(t, s_top[warp + k]);
-    if (top != t) {
-      const float back = exp2_hw(top - t);
-      sum *= back;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] *= back;
-    }
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) {
-      const float x = s_sum[warp + k];
-      bad |= __float_as_uint(x) == kBadLse;
-      if (s_sum[warp + k] == 0.f) continue;          // none of its pieces counted
-      const float w = s_top[warp + k] == t ? 1.f : exp2_hw(s_top[warp + k] - t);
-      sum = fmaf(w, x, sum);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, s_acc[warp + k][8 * lane + e], acc[e]);
-    }
-  }
-  if (n == 0) return;
-  const float inv = sum == 0.f || bad ? 0.f : 1.f / sum;
-  uint32_t h[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 v = inv == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
-                                        : __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    h[e] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(tok) * p.out_stride_tok +
-                            static_cast<int64_t>(head) * p.out_stride_head + 8 * lane) =
-      make_uint4(h[0], h[1], h[2], h[3]);
+  if (r >= rows) return;
+  const float inv = sum == 0.f || s_bad ? 0.f : 1.f / sum;
+  const __nv_bfloat162 x = inv == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 y = inv == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  const int rr = m * kRows + r, node = rr / p.ratio;
+  *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q0 + node) * p.out_stride_tok +
+                            static_cast<int64_t>(h * p.ratio + rr - node * p.ratio) * p.out_stride_head + d) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
 __global__ void __launch_bounds__(MTP_TREE_MAX_NODES)
@@ -1324,10 +1290,9 @@ extern "C" size_t mtp_tree_attn_workspace_size(int32_t num_seqs, int32_t total_q
   if (sms <= 0) return 0;
   const int64_t ctas = std::min<int64_t>(
       sms, line_bound(num_seqs, total_q, num_kv_heads, num_q_heads / num_kv_heads, max_pages_per_seq));
-  // partial outputs, then their log-sum-exps; two slots of 128 rows a CTA
-  // then the nodes' entries and the piece length
+  // partial outputs, then their log-sum-exps, two slots of 128 rows a CTA; then the join's notes
   return align256(static_cast<size_t>(ctas) * 2 * kRows * (kHeadDim + 1) * sizeof(float)) +
-         align256(static_cast<size_t>(total_q) * sizeof(int4)) + 256;
+         align256(static_cast<size_t>(ctas) * sizeof(JoinNote));
 }
 
 extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_head,
@@ -1406,9 +1371,8 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
       device_sm_count(device), line_bound(num_seqs, total_q, num_kv_heads, ratio, max_pages_per_seq)));
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = p.o_part + static_cast<int64_t>(p.ctas) * 2 * kRows * kHeadDim;
-  p.piece = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + need - 256);
-  p.nodes = reinterpret_cast<int4*>(static_cast<char*>(workspace) + need - 256 -
-                                    align256(static_cast<size_t>(total_q) * sizeof(int4)));
+  p.notes = reinterpret_cast<JoinNote*>(static_cast<char*>(workspace) + need -
+                                        align256(static_cast<size_t>(p.ctas) * sizeof(JoinNote)));
   AttnParams cache{};                                // what the tensor map goes by
   cache.k_cache = static_cast<const uint8_t*>(k_cache);
   cache.v_cache = p.v_cache;
@@ -1431,11 +1395,7 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
     return MTPATTN_E_LAUNCH;
   // units of one key tile are never cut
   if (max_pages_per_seq <= kTilePages) return MTPATTN_OK;
-  const int64_t rows = static_cast<int64_t>(total_q) * num_q_heads;
-  const int warps = rows < 4096 ? 4 : 1;             // a row
-  const int per = kReduceThreads / 32 / warps;
-  const dim3 grid(static_cast<unsigned>((rows + per - 1) / per));
-  const void* kernel = warps == 4 ? reinterpret_cast<const void*>(tree_reduce_kernel<4>)
-                                  : reinterpret_cast<const void*>(tree_reduce_kernel<1>);
-  return launch_pdl(kernel, grid, kReduceThreads, 0, st, p) == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
+  return launch_pdl(reinterpret_cast<const void*>(tree_reduce_kernel), dim3(p.ctas, kReduceCtas), kReduceThreads,
+                    static_cast<size_t>(p.ctas) * 32 * sizeof(float), st, p) == cudaSuccess
+             ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
