@@ -8,8 +8,8 @@
 // these, which is cut into equal pieces, one per CTA (worked out from seq_lens and cu_seqlens_q on
 // the device, so a captured call follows its buffers).  A unit whose key tiles lie in one piece is
 // written out at once; a unit cut by piece borders leaves one partial output and log-sum-exp per
-// piece in the workspace, and tree_reduce_kernel joins them: the CTA behind a unit's first cut
-// leaves a note for it.  A CTA has at most two partial units, the first and the last of its piece:
+// piece in the workspace, and tree_reduce_kernel joins them: the CTA that has a unit's first
+// key tile leaves a note on it.  A CTA has at most two partial units, the first and the last of its piece:
 // two slots per CTA.  Where whole units, one a CTA, take at most kCutTiles tiles longer than equal
 // pieces, they are not cut (joining takes about as long).
 //
@@ -93,9 +93,9 @@ constexpr int kCutTiles = 6, kUnitTiles = 3;
 constexpr uint32_t kBadLse = 0x7fd0bad1u;          // a partial of a sequence with a bad page (a NaN
                                                    // that no arithmetic makes)
 
-// What CTA g leaves for the reduce: the unit whose first cut is at the start of piece g.
+// What the reduce goes by: a unit's note, written by the CTA that has its first key tile.
 struct JoinNote {
-  int pieces;                // it lies in, 0: there is none
+  int pieces;                // it lies in; 1: written out whole
   int first, first_slot;     // the first of them, and the unit's slot there (in the others, 0)
   int q0, h, m, rows;        // its first node, KV head, row tile; valid rows of the tile
   int pad;
@@ -122,7 +122,9 @@ struct TreeAttnParams {
   int32_t ctas;              // pieces of the line, at most
   float* o_part;             // [ctas][2][64][128][4]: blocks of 4 dims, rows, dims
   float* lse_part;           // [ctas][2][128]
-  struct JoinNote* notes;    // [ctas]
+  int32_t* units;            // for the reduce: the number of units (0: none was cut),
+  JoinNote* notes;           // [units], at most unit_bound of them
+  int32_t unit_bound;
 };
 
 struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
@@ -197,7 +199,7 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
 // How the line is cut: pieces of C places, piece g from g C on.  With V > 0 every unit takes V
 // places on the line, and so a piece of its own.
 struct Cut {
-  int C, V, length;
+  int C, V, length, units;
 };
 __device__ __forceinline__ int weight_of(const Seq& s, int hkv, int V) { return V ? s.T * hkv * V : s.w; }
 
@@ -218,6 +220,7 @@ __device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const
   c.C = max(1, (W + p.ctas - 1) / p.ctas);
   c.V = 0;
   c.length = W;
+  c.units = U;
   if (U <= p.ctas && longest + kUnitTiles <= c.C + kCutTiles) {
     c.C = c.V = longest;
     c.length = U * longest;
@@ -229,16 +232,18 @@ __device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const
 struct Walker {
   int pos, hi, lo;
   int b0, before;            // the held sequences, and the line before the first of them
+  int units_before;          // ... and the units
   Seq mine;
-  int upto;                  // running sum of the held sequences' weights
-  int unit0, unit_places;    // of the last segment's unit, on the line
+  int upto, units_upto;      // running sums of the held sequences' weights and units
+  int unit, unit0, unit_places;  // the last segment's unit: its number, and place on the line
   Cut cut;
 
   __device__ __forceinline__ void start(const TreeAttnParams& p, int lane) {
-    b0 = before = unit0 = unit_places = 0;
+    b0 = before = units_before = unit = unit0 = unit_places = 0;
     mine = seq_at(p, lane);
     cut = cut_line(p, lane, mine);
     upto = warp_scan(weight_of(mine, p.hkv, cut.V), lane);
+    units_upto = warp_scan(mine.T * p.hkv, lane);
     lo = pos = min(static_cast<int64_t>(cut.length), static_cast<int64_t>(blockIdx.x) * cut.C);
     hi = min(static_cast<int64_t>(cut.length), static_cast<int64_t>(lo) + cut.C);
   }
@@ -250,10 +255,12 @@ struct Walker {
       const int all = __shfl_sync(0xffffffffu, upto, 31);
       if (pos >= before + all) {
         before += all;
+        units_before += __shfl_sync(0xffffffffu, units_upto, 31);
         b0 += 32;
         if (b0 >= p.num_seqs) return 0;             // lengths changed under the call
         mine = seq_at(p, b0 + lane);
         upto = warp_scan(weight_of(mine, p.hkv, cut.V), lane);
+        units_upto = warp_scan(mine.T * p.hkv, lane);
         continue;
       }
       const int at = pos - before;
@@ -262,7 +269,8 @@ struct Walker {
       const int extra = cut.V ? 0 : kUnitTiles;     // places ahead of the unit's key tiles
       const int places = cut.V ? cut.V : nt + extra;
       const int in = at - (f ? __shfl_sync(0xffffffffu, upto, f - 1) : 0);
-      const int unit = in / places, in_unit = in - unit * places;
+      const int nth = in / places, in_unit = in - nth * places;
+      unit = units_before + nth + (f ? __shfl_sync(0xffffffffu, units_upto, f - 1) : 0);
       unit0 = pos - in_unit;
       unit_places = places;
       const int to = min(places, in_unit + hi - pos);                // of the unit, in this piece
@@ -274,8 +282,8 @@ struct Walker {
       s.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
       s.n = __shfl_sync(0xffffffffu, mine.n, f);
       s.L = __shfl_sync(0xffffffffu, mine.L, f);
-      s.h = unit / T;
-      s.m = unit - s.h * T;
+      s.h = nth / T;
+      s.m = nth - s.h * T;
       s.nt = nt;
       s.T = T;
       s.first = unit0 <= lo;
@@ -284,13 +292,12 @@ struct Walker {
     }
     return 0;
   }
-  // What the reduce has to know of the CTA's first segment.
+  // What the reduce has to know of the last segment's unit.
   __device__ __forceinline__ JoinNote note(const TreeAttnParams& p, const Segment& s) const {
     JoinNote n;
-    const int g = blockIdx.x;
-    n.first = (unit0 + kUnitTiles) / cut.C;
-    n.pieces = !s.end && !cut.V && s.t0 > 0 && n.first == g - 1 ? (unit0 + unit_places - 1) / cut.C - n.first + 1 : 0;
-    n.first_slot = unit0 <= n.first * cut.C ? 0 : 1;
+    n.first = blockIdx.x;
+    n.pieces = cut.V ? 1 : (unit0 + unit_places - 1) / cut.C - n.first + 1;
+    n.first_slot = s.first ? 0 : 1;
     n.q0 = s.q0;
     n.h = s.h;
     n.m = s.m;
@@ -342,27 +349,40 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
-// x0..x3 = hi + lo with e4m3 codes (lowest byte first); the remainder is formed in f16, exactly.
-__device__ __forceinline__ void two_terms(float x0, float x1, float x2, float x3, uint32_t& hi,
-                                          uint32_t& lo) {
+// Four bf16 values (two words) scaled by f (bf16x2, powers of two: exact) as e4m3 codes hi + lo,
+// lowest byte first.  In f16 a scaled value is exact down to 2^-17, and so is the remainder.
+__device__ __forceinline__ void two_terms(uint32_t w0, uint32_t w1, uint32_t f, uint32_t& hi, uint32_t& lo) {
   asm("{\n"
-      " .reg .b16 h01, h23, l01, l23;\n"
-      " .reg .b32 x01, x23, g01, g23;\n"
-      " cvt.rn.satfinite.e4m3x2.f32 h01, %3, %2;\n"
-      " cvt.rn.satfinite.e4m3x2.f32 h23, %5, %4;\n"
-      " cvt.rn.f16x2.f32 x01, %3, %2;\n"
-      " cvt.rn.f16x2.f32 x23, %5, %4;\n"
-      " cvt.rn.f16x2.e4m3x2 g01, h01;\n"
-      " cvt.rn.f16x2.e4m3x2 g23, h23;\n"
-      " sub.rn.f16x2 x01, x01, g01;\n"
-      " sub.rn.f16x2 x23, x23, g23;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l01, x01;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l23, x23;\n"
-      " mov.b32 %0, {h01, h23};\n"
-      " mov.b32 %1, {l01, l23};\n"
+      " .reg .b16 a0, a1, b0, b1, h0, h1, l0, l1, z;\n"
+      " .reg .b32 x0, x1, e0, e1, e2, e3, g0, g1;\n"
+      " mul.rn.bf16x2 x0, %2, %4;\n"
+      " mul.rn.bf16x2 x1, %3, %4;\n"
+      " mov.b16 z, 0;\n"
+      " mov.b32 {a0, a1}, x0;\n"
+      " mov.b32 {b0, b1}, x1;\n"
+      " mov.b32 e0, {z, a0};\n"
+      " mov.b32 e1, {z, a1};\n"
+      " mov.b32 e2, {z, b0};\n"
+      " mov.b32 e3, {z, b1};\n"
+      " cvt.rn.f16x2.f32 x0, e1, e0;\n"
+      " cvt.rn.f16x2.f32 x1, e3, e2;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h0, x0;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h1, x1;\n"
+      " cvt.rn.f16x2.e4m3x2 g0, h0;\n"
+      " cvt.rn.f16x2.e4m3x2 g1, h1;\n"
+      " sub.rn.f16x2 x0, x0, g0;\n"
+      " sub.rn.f16x2 x1, x1, g1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l0, x0;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l1, x1;\n"
+      " mov.b32 %0, {h0, h1};\n"
+      " mov.b32 %1, {l0, l1};\n"
       "}\n"
       : "=r"(hi), "=r"(lo)
-      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+      : "r"(w0), "r"(w1), "r"(f));
+}
+// The larger |value| of two bf16 pairs, half by half; NaN is above all.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
 }
 // mbar_wait of sm100.cuh in fewer instructions (there are many waits, and the loops of all the
 // roles share one instruction cache): a 32-bit clock, in which kWaitCycles fits.
@@ -456,20 +476,19 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     if (lane == 0) prefetch_tmap(&p.tmap_k);
     Walker walk;
     walk.start(p, lane);
+    if (blockIdx.x == 0 && lane == 0) *p.units = walk.cut.V ? 0 : min(walk.cut.units, p.unit_bound);
     // keys that other row tiles will read again stay in L2
     const uint64_t once = l2_policy_evict_first();
     uint64_t again;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
     uint32_t u = 0;
     int e = 0;
-    bool ok = true, noted = false;
+    bool ok = true;
     while (ok) {
       Segment s;
       const int err = walk.next(p, lane, s);
-      if (!noted) {
-        noted = true;
-        if (lane == 0) p.notes[blockIdx.x] = walk.note(p, s);
-      }
+      if (lane == 0 && !s.end && s.t0 == 0 && !walk.cut.V && walk.unit < p.unit_bound)
+        p.notes[walk.unit] = walk.note(p, s);
       if (err && !s.end) {
         // zeros for the rows of a sequence that cannot be computed, here: it has no key tiles
         if (lane == 0) set_status(p.status, err);
@@ -770,7 +789,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     // smallest float, under which all logits are alike.
     const float sl_in = p.scale_log2 * __ldg(p.k_descale);
     const float sl = fmaxf(fabsf(sl_in), 1.17549435e-38f);
-    const uint32_t flip = sl_in < 0.f ? 0x80000000u : 0u;
+    const uint32_t flip = sl_in < 0.f ? 0x80008000u : 0u;
     const float vd = __ldg(p.v_descale);
     uint32_t u = 0;                                 // key tiles so far
     // The two warps of a row quarter meet: what each wrote to shared memory before, the other
@@ -823,10 +842,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
           for (int i = 0; i < 4; ++i) x[i] = lds128(own + (i0 + i) * 128);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            top[i] = max(max(max((x[i].x << 16) & 0x7fff0000u, x[i].x & 0x7fff0000u),
-                             max((x[i].y << 16) & 0x7fff0000u, x[i].y & 0x7fff0000u)),
-                         max(max((x[i].z << 16) & 0x7fff0000u, x[i].z & 0x7fff0000u),
-                             max((x[i].w << 16) & 0x7fff0000u, x[i].w & 0x7fff0000u)));
+          {
+            const uint32_t m = max_abs2(max_abs2(x[i].x, x[i].y), max_abs2(x[i].z, x[i].w));
+            top[i] = max(m << 16, m & 0xffff0000u);  // as an f32's bits
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
           __syncwarp();                              // every lane has read its part of the rows
@@ -836,14 +855,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
             const int e8 = static_cast<int>(top[i] >> 23);           // exponent field
             // 2^a takes the largest into [128, 256), as far as a = 126 does
             const int a = top[i] == 0u ? 0 : min(126, 134 - e8);
-            const float f = __uint_as_float(static_cast<uint32_t>(a + 127) << 23 | flip);
-            const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const uint32_t f = (static_cast<uint32_t>(a + 127) << 7) * 0x10001u | flip;
             uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              two_terms(__uint_as_float(ww[2 * k] << 16) * f, __uint_as_float(ww[2 * k] & 0xffff0000u) * f,
-                        __uint_as_float(ww[2 * k + 1] << 16) * f, __uint_as_float(ww[2 * k + 1] & 0xffff0000u) * f,
-                        hi[k], lo[k]);
+            two_terms(x[i].x, x[i].y, f, hi[0], lo[0]);
+            two_terms(x[i].z, x[i].w, f, hi[1], lo[1]);
             unsigned char* dst = q_hi + row * 128 + ((chunk ^ (row & 7)) << 4);
             *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
@@ -1111,89 +1126,89 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   }
 }
 
-// Join the partials of the units that were cut, a row's pieces weighted by 2^(lse - max).  A CTA
-// takes 32 rows and 32 dims of a unit: thread = row (lane) and 4 dims (warp), so every load of a
-// piece is 512 bytes in a piece, kAhead of them in flight; the weights are made once per CTA.  A
-// piece of a row that saw none of its keys has lse -inf and counts nothing; a NaN in any other
-// piece stays in the result.
-constexpr int kReduceThreads = 256, kAhead = 8, kReduceCtas = 4 * (kHeadDim / 32);   // a unit
+// Join the partials of the units that were cut, a row's pieces weighted by 2^(lse - max).  Thread =
+// row (lane) and 4 kVec dims (warp) of a unit, so every load of a piece is 512 bytes in a piece;
+// all of a step's loads, the log-sum-exps among them, are in flight together, and no thread waits
+// for another: the chain of note, then steps of kAhead pieces is what bounds it.  A piece of a row
+// that saw none of its keys has lse -inf and zeros, and counts nothing; a NaN in any other piece
+// stays in the result.
+constexpr int kReduceThreads = 256;
+constexpr int reduce_ctas(int vec) { return 4 * (kHeadDim / (4 * vec * (kReduceThreads / 32))); }   // a unit
 
+template <int kVec, int kAhead>
 __global__ void __launch_bounds__(kReduceThreads)
 tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
-  extern __shared__ float s_w[];                     // [pieces][32 rows]: lse, then weights
-  __shared__ float s_top[kReduceThreads / 32][32], s_sum[kReduceThreads / 32][32];
-  __shared__ int s_bad;
+  constexpr int kCtaDims = 4 * kVec * (kReduceThreads / 32);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q = blockIdx.y / (kHeadDim / 32), d = 32 * (blockIdx.y % (kHeadDim / 32)) + 4 * warp;
+  const int q = blockIdx.y / (kHeadDim / kCtaDims);
+  const int d = kCtaDims * (blockIdx.y % (kHeadDim / kCtaDims)) + 4 * kVec * warp;
   const int r = 32 * q + lane;                       // row of the unit
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (threadIdx.x == 0) s_bad = 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
+  const int units = __ldcg(p.units);
   const int4 n0 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x));
-  const int n = n0.x;                                // pieces
-  if (n == 0) return;                                // (the same for the whole CTA)
   const int4 n1 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x) + 1);
-  const int q0 = n0.w, h = n1.x, m = n1.y, rows = n1.z;
-  if (32 * q >= rows) return;
+  if (static_cast<int>(blockIdx.x) >= units || n0.x <= 1) return;
+  const int n = n0.x, q0 = n0.w, h = n1.x, m = n1.y, rows = n1.z;
+  if (r >= rows) return;
   auto slot_of = [&](int i) -> int64_t { return 2 * (n0.y + i) + (i == 0 ? n0.z : 0); };
-  float top = -INFINITY;
-  bool bad = false;
-  __syncthreads();
-  for (int i = warp; i < n; i += kReduceThreads / 32) {
-    const float x = __ldcg(p.lse_part + slot_of(i) * kRows + r);
-    s_w[i * 32 + lane] = x;
-    if (r < rows) bad |= __float_as_uint(x) == kBadLse;
-    top = fmaxf(top, x);                             // (NaN is passed over)
-  }
-  s_top[warp][lane] = top;
-  if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
-  // the pieces' own loads do not wait for the weights
   const float* src = p.o_part + (static_cast<int64_t>(d / 4) * kRows + r) * 4;
   constexpr int64_t kSlot = static_cast<int64_t>(kHeadDim) * kRows;
-  float4 a[kAhead];
+  float acc[4 * kVec], top = -INFINITY, sum = 0.f;
+  bool bad = false;
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j)
-    if (j < n) a[j] = __ldcg(reinterpret_cast<const float4*>(src + slot_of(j) * kSlot));
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kReduceThreads / 32; ++w) top = fmaxf(top, s_top[w][lane]);
-  float sum = 0.f;
-  for (int i = warp; i < n; i += kReduceThreads / 32) {
-    const float x = s_w[i * 32 + lane];
-    const float w = x == -INFINITY ? 0.f : exp2_hw(x - top);   // a NaN makes the row NaN
-    s_w[i * 32 + lane] = w;
-    sum += w;
-  }
-  s_sum[warp][lane] = sum;
-  __syncthreads();
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kReduceThreads / 32; ++w) sum += s_sum[w][lane];
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e = 0; e < 4 * kVec; ++e) acc[e] = 0.f;
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += kAhead) {
-    if (i0 > 0) {
+    float4 a[kAhead][kVec];
+    float lse[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (i0 + j < n) a[j] = __ldcg(reinterpret_cast<const float4*>(src + slot_of(i0 + j) * kSlot));
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
+    for (int j = 0; j < kAhead; ++j) {
+      lse[j] = -INFINITY;
       if (i0 + j < n) {
-        const float w = s_w[(i0 + j) * 32 + lane];
-        // (the values of a piece without weight may be anything only where it is empty: then zeros)
-        acc.x = fmaf(w, a[j].x, acc.x); acc.y = fmaf(w, a[j].y, acc.y);
-        acc.z = fmaf(w, a[j].z, acc.z); acc.w = fmaf(w, a[j].w, acc.w);
+        lse[j] = __ldcg(p.lse_part + slot_of(i0 + j) * kRows + r);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+          a[j][k] = __ldcg(reinterpret_cast<const float4*>(src + slot_of(i0 + j) * kSlot + k * 4 * kRows));
       }
+    }
+    float t = top;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      bad |= __float_as_uint(lse[j]) == kBadLse;
+      t = fmaxf(t, lse[j]);                          // (NaN is passed over)
+    }
+    const float back = t == top ? 1.f : exp2_hw(top - t);
+    top = t;
+    sum *= back;
+#pragma unroll
+    for (int e = 0; e < 4 * kVec; ++e) acc[e] *= back;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (lse[j] == -INFINITY) continue;             // (or past the last piece)
+      const float w = exp2_hw(lse[j] - top);         // NaN makes the row NaN
+      sum += w;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        acc[4 * k] = fmaf(w, a[j][k].x, acc[4 * k]);
+        acc[4 * k + 1] = fmaf(w, a[j][k].y, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(w, a[j][k].z, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(w, a[j][k].w, acc[4 * k + 3]);
+      }
+    }
   }
-  if (r >= rows) return;
-  const float inv = sum == 0.f || s_bad ? 0.f : 1.f / sum;
-  const __nv_bfloat162 x = inv == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 y = inv == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  const float inv = sum == 0.f || bad ? 0.f : 1.f / sum;
   const int rr = m * kRows + r, node = rr / p.ratio;
-  *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q0 + node) * p.out_stride_tok +
-                            static_cast<int64_t>(h * p.ratio + rr - node * p.ratio) * p.out_stride_head + d) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  __nv_bfloat16* out = p.out + static_cast<int64_t>(q0 + node) * p.out_stride_tok +
+                       static_cast<int64_t>(h * p.ratio + rr - node * p.ratio) * p.out_stride_head + d;
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    const float f0 = inv == 0.f ? 0.f : acc[4 * k] * inv, f1 = inv == 0.f ? 0.f : acc[4 * k + 1] * inv;
+    const float f2 = inv == 0.f ? 0.f : acc[4 * k + 2] * inv, f3 = inv == 0.f ? 0.f : acc[4 * k + 3] * inv;
+    const __nv_bfloat162 x = __floats2bfloat162_rn(f0, f1), y = __floats2bfloat162_rn(f2, f3);
+    *reinterpret_cast<uint2*>(out + 4 * k) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
 }
 
 __global__ void __launch_bounds__(MTP_TREE_MAX_NODES)
@@ -1228,9 +1243,11 @@ tree_mask_kernel(const int32_t* parents, const int32_t* cu_q, int32_t total_q, u
 // ---- host side -----------------------------------------------------------------------------------
 
 // CTAs of a call: one per SM, but no more than the line can have key tiles.
+int64_t units_bound(int32_t num_seqs, int32_t total_q, int32_t hkv, int32_t ratio) {
+  return (static_cast<int64_t>(total_q) * ratio / kRows + num_seqs) * hkv;
+}
 int64_t line_bound(int32_t num_seqs, int32_t total_q, int32_t hkv, int32_t ratio, int32_t max_pages) {
-  const int64_t row_tiles = static_cast<int64_t>(total_q) * ratio / kRows + num_seqs;
-  return row_tiles * hkv * ((max_pages + kTilePages - 1) / kTilePages);
+  return units_bound(num_seqs, total_q, hkv, ratio) * ((max_pages + kTilePages - 1) / kTilePages + kUnitTiles);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1290,9 +1307,11 @@ extern "C" size_t mtp_tree_attn_workspace_size(int32_t num_seqs, int32_t total_q
   if (sms <= 0) return 0;
   const int64_t ctas = std::min<int64_t>(
       sms, line_bound(num_seqs, total_q, num_kv_heads, num_q_heads / num_kv_heads, max_pages_per_seq));
-  // partial outputs, then their log-sum-exps, two slots of 128 rows a CTA; then the join's notes
+  // partial outputs, then their log-sum-exps, two slots of 128 rows a CTA; the units' notes; their
+  // number
+  const int64_t units = units_bound(num_seqs, total_q, num_kv_heads, num_q_heads / num_kv_heads);
   return align256(static_cast<size_t>(ctas) * 2 * kRows * (kHeadDim + 1) * sizeof(float)) +
-         align256(static_cast<size_t>(ctas) * sizeof(JoinNote));
+         align256(static_cast<size_t>(units) * sizeof(JoinNote)) + 256;
 }
 
 extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_head,
@@ -1371,8 +1390,10 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
       device_sm_count(device), line_bound(num_seqs, total_q, num_kv_heads, ratio, max_pages_per_seq)));
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = p.o_part + static_cast<int64_t>(p.ctas) * 2 * kRows * kHeadDim;
-  p.notes = reinterpret_cast<JoinNote*>(static_cast<char*>(workspace) + need -
-                                        align256(static_cast<size_t>(p.ctas) * sizeof(JoinNote)));
+  p.unit_bound = static_cast<int32_t>(units_bound(num_seqs, total_q, num_kv_heads, ratio));
+  p.units = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + need - 256);
+  p.notes = reinterpret_cast<JoinNote*>(static_cast<char*>(workspace) + need - 256 -
+                                        align256(static_cast<size_t>(p.unit_bound) * sizeof(JoinNote)));
   AttnParams cache{};                                // what the tensor map goes by
   cache.k_cache = static_cast<const uint8_t*>(k_cache);
   cache.v_cache = p.v_cache;
@@ -1395,7 +1416,10 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
     return MTPATTN_E_LAUNCH;
   // units of one key tile are never cut
   if (max_pages_per_seq <= kTilePages) return MTPATTN_OK;
-  return launch_pdl(reinterpret_cast<const void*>(tree_reduce_kernel), dim3(p.ctas, kReduceCtas), kReduceThreads,
-                    static_cast<size_t>(p.ctas) * 32 * sizeof(float), st, p) == cudaSuccess
+  // Few units are cut into many pieces each: many CTAs of few dims then; many units into few.
+  const bool few = p.unit_bound <= 64;
+  const void* kernel = few ? reinterpret_cast<const void*>(tree_reduce_kernel<1, 8>)
+                           : reinterpret_cast<const void*>(tree_reduce_kernel<4, 2>);
+  return launch_pdl(kernel, dim3(p.unit_bound, reduce_ctas(few ? 1 : 4)), kReduceThreads, 0, st, p) == cudaSuccess
              ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
