@@ -6,8 +6,9 @@
 // Every CTA of the cluster holds the tree in shared memory and takes the same decisions; a
 // row's scan is split over the CTAs, whose results meet through distributed shared memory.
 //
-// The scan of a row is bound by the latency of its loads: thread t takes elements t, t + T, ...
-// of its CTA's part, kUnroll of them in flight, so any row address and vocabulary will do.
+// Rows are read in 16-byte blocks at the addresses' own alignment, whatever the row's: block k holds
+// the elements k * kVec - skew .. + kVec - 1, skew being how far the row's start lies into one, and
+// the two blocks at the row's ends are read an element at a time.
 #include "common.cuh"
 #include "host_checks.cuh"
 
@@ -16,6 +17,7 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -112,19 +114,85 @@ __device__ void emit(const VerifyParams& p, int b, const Walk& w, int count, int
   }
 }
 
+// ---- rows ----------------------------------------------------------------------------------------
+
+// A row of `vocab` elements in blocks of kVec (16 bytes).
+template <class T>
+struct RowOf {
+  static constexpr int kVec = 16 / sizeof(T);
+  const T* at;               // the row's first element, less skew: 16-byte aligned
+  int skew, end;             // elements of the row: skew .. end - 1
+  __device__ __forceinline__ RowOf(const T* row, int vocab) {
+    skew = static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T) % kVec);
+    at = row - skew;
+    end = skew + vocab;
+  }
+  __device__ __forceinline__ int blocks() const { return (end + kVec - 1) / kVec; }
+  // Block k; places outside the row hold `fill`.
+  __device__ __forceinline__ uint4 block(int k, T fill) const {
+    const int i0 = k * kVec;
+    if (i0 >= skew && i0 + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(at + i0));
+    union { uint4 v; T x[kVec]; } u;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) u.x[i] = i0 + i >= skew && i0 + i < end ? at[i0 + i] : fill;
+    return u.v;
+  }
+};
+
+// Element i of a block.
+template <class T>
+__device__ __forceinline__ float element(const uint4& v, int i);
+template <>
+__device__ __forceinline__ float element<float>(const uint4& v, int i) {
+  return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+}
+template <>
+__device__ __forceinline__ float element<__nv_bfloat16>(const uint4& v, int i) {
+  const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+  return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+}
+template <>
+__device__ __forceinline__ float element<__half>(const uint4& v, int i) {
+  const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? w >> 16 : w)));
+}
+
+// The largest element of a block, NaN passed over (NaN if there is nothing else).
+__device__ __forceinline__ float top_of(const uint4& v, float) {
+  return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+template <class T2>
+__device__ __forceinline__ T2 pair_of(uint32_t w) {
+  T2 p;
+  memcpy(&p, &w, 4);
+  return p;
+}
+__device__ __forceinline__ float top_of(const uint4& v, __nv_bfloat16) {
+  const __nv_bfloat162 m = __hmax2(__hmax2(pair_of<__nv_bfloat162>(v.x), pair_of<__nv_bfloat162>(v.y)),
+                                   __hmax2(pair_of<__nv_bfloat162>(v.z), pair_of<__nv_bfloat162>(v.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float top_of(const uint4& v, __half) {
+  const __half2 m = __hmax2(__hmax2(pair_of<__half2>(v.x), pair_of<__half2>(v.y)),
+                            __hmax2(pair_of<__half2>(v.z), pair_of<__half2>(v.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
 // ---- greedy --------------------------------------------------------------------------------------
 
-// The order of float values as an order of unsigned numbers, both zeros alike; 0 for NaN.
+// The order of float values as an order of unsigned numbers above 0, both zeros alike.
 __device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// A thread looks at its blocks' largest elements, and keeps the block that first has the largest
+// of them; where in it, is looked up once at the end.  kUnroll blocks are in flight: what bounds a
+// step is that latency, then two meetings of the cluster.
 template <class T>
 __global__ void __launch_bounds__(kVerifyThreads)
 verify_greedy_kernel(const VerifyParams p) {
-  constexpr int kUnroll = 16;
+  constexpr int kUnroll = 8, kVec = RowOf<T>::kVec;
   __shared__ Walk w;
   __shared__ uint64_t s_warp[kVerifyWarps];
   __shared__ uint64_t s_best[2][kMaxCluster];      // by step parity: the CTAs' best keys
@@ -135,29 +203,38 @@ verify_greedy_kernel(const VerifyParams p) {
   // every CTA of the cluster has to be running before its shared memory is written
   cluster.sync();
   if (!ok) return;
-  const int per = (p.vocab + parts - 1) / parts;
-  const int lo = min(p.vocab, part * per), hi = min(p.vocab, lo + per);
+  const T lowest = T(-INFINITY);
   int cur = 0, count = 0, next = -1;
   for (int step = 0;; ++step) {
-    const T* row = static_cast<const T*>(p.p) + static_cast<int64_t>(w.q0 + cur) * p.p_stride;
-    uint32_t best = 0, at = 0;
-    for (int i0 = lo + t; i0 < hi; i0 += kUnroll * kVerifyThreads) {
-      T v[kUnroll];
+    const RowOf<T> row(static_cast<const T*>(p.p) + static_cast<int64_t>(w.q0 + cur) * p.p_stride, p.vocab);
+    const int blocks = row.blocks(), per = (blocks + parts - 1) / parts;
+    const int lo = min(blocks, part * per), hi = min(blocks, lo + per);
+    float best = -INFINITY;
+    int at = lo + t;                               // (what -inf leaves: this thread's first block)
+    for (int k0 = lo + t; k0 < hi; k0 += kUnroll * kVerifyThreads) {
+      uint4 v[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
-        if (i0 + u * kVerifyThreads < hi) v[u] = row[i0 + u * kVerifyThreads];
+        if (k0 + u * kVerifyThreads < hi) v[u] = row.block(k0 + u * kVerifyThreads, lowest);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
-        if (i0 + u * kVerifyThreads < hi) {
-          const uint32_t o = order_of(to_f32(v[u]));
-          if (o > best) {                           // a thread's elements ascend: ties keep the first
-            best = o;
-            at = i0 + u * kVerifyThreads;
+        if (k0 + u * kVerifyThreads < hi) {
+          const float m = top_of(v[u], T(0.f));
+          if (m > best) {                           // a thread's blocks ascend: ties keep the first
+            best = m;
+            at = k0 + u * kVerifyThreads;
           }
         }
     }
     // largest value, then lowest token; 0: nothing but NaN
-    uint64_t key = best ? (static_cast<uint64_t>(best) << 32 | static_cast<uint32_t>(~at)) : 0ull;
+    uint64_t key = 0;
+    for (int k = at; k < hi && key == 0; k += kVerifyThreads) {   // (one block, unless best is -inf)
+      const uint4 v = row.block(k, T(NAN));
+#pragma unroll
+      for (int i = kVec - 1; i >= 0; --i)
+        if (element<T>(v, i) == best)
+          key = static_cast<uint64_t>(order_of(best)) << 32 | static_cast<uint32_t>(~(k * kVec + i - row.skew));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
@@ -190,58 +267,108 @@ verify_greedy_kernel(const VerifyParams p) {
 }
 
 // ---- sampling ------------------------------------------------------------------------------------
+//
+// w = max(p - S q, 0) is taken to a whole number of units of 2^-45, element by element, so sums are
+// exact in 64 bits and the order of summation is free.  The number is made of two digits without a
+// conversion instruction (these run at a quarter rate, and one to 64 bits at half of that): with
+// w = d + e, d in f32 and e its error, the low 23 bits of 1 + d are d to units of 2^-23, and what
+// that leaves, with e, is at most 2^-24 + 2^-25 and becomes the second digit as the low bits of
+// r 2^45 + 3 * 2^22.  A lane's digits are summed in 32 bits over a chunk, offsets and all.
 
-// Probabilities in units of 2^-52 (exact for a float of at least 2^-28), NaN as 0.
-__device__ __forceinline__ int64_t fixed_of(float x) {
-  return __float2ll_rn(__saturatef(x) * 4503599627370496.f);
-}
-
-// One sum over a row: w = max(p - S q, 0) with S in units of 2^-57.
 struct Row {
   const void* p;
   const void* q;             // null: w = p
-  uint64_t S;
+  uint64_t S;                // in units of 2^-57
+  float s_hi, s_lo;          // S as the sum of two floats
+  __device__ __forceinline__ void set(uint64_t s) {
+    S = s;
+    const double x = static_cast<double>(s) * 6.938893903907228e-18;     // 2^-57
+    s_hi = static_cast<float>(x);
+    s_lo = static_cast<float>(x - static_cast<double>(s_hi));
+  }
 };
 
-template <class T>
-__device__ __forceinline__ int64_t left_of(const Row& r, float pv, float qv) {
-  int64_t x = fixed_of(pv);
-  if (r.q) {
-    // S q: (q 2^59) (S 2^57) 2^-64, rounded down to a unit; exact for S = 1
-    x -= static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(fixed_of(qv)) << 7, r.S));
-    x = x > 0 ? x : 0;
-  }
-  return x;
+struct Digits {
+  uint32_t a, b;             // low 23 bits of a: units of 2^-23; b - 0x4B400000: units of 2^-45, signed
+};
+constexpr uint32_t kDigitA = 0x3F800000u, kDigitB = 0x4B400000u;          // what w = 0 gives
+constexpr double kUnit = 2.8421709430404007e-14;                          // 2^-45
+
+__device__ __forceinline__ Digits digits_of(float d, float e) {           // d + e, 0 <= d <= 1
+  const float a = __fadd_rn(d, 1.f);
+  const float r = __fadd_rn(__fsub_rn(d, __fsub_rn(a, 1.f)), e);
+  return {__float_as_uint(a), __float_as_uint(__fmaf_rn(r, 35184372088832.f, 12582912.f))};
+}
+template <bool kQ>
+__device__ __forceinline__ Digits left_of(const Row& r, float pv, float qv) {
+  pv = __saturatef(pv);                              // into [0, 1]; NaN as 0
+  if (!kQ) return digits_of(pv, 0.f);
+  qv = __saturatef(qv);
+  const float h = __fmul_rn(r.s_hi, qv);             // S q = h + l
+  const float l = __fmaf_rn(r.s_lo, qv, __fmaf_rn(r.s_hi, qv, -h));
+  float d = __fsub_rn(pv, h);
+  float e = __fsub_rn(__fsub_rn(__fsub_rn(pv, d), h), l);                 // exact but for l where d > 0
+  const bool some = __fadd_rn(d, e) > 0.f && d >= 0.f;
+  d = some ? d : 0.f;
+  e = some ? e : 0.f;
+  return digits_of(d, e);
+}
+__device__ __forceinline__ int64_t fixed_of(uint32_t a, uint32_t b, int n) {   // sums over n elements
+  return (static_cast<int64_t>(a - static_cast<uint32_t>(n) * kDigitA) << 22) +
+         static_cast<int32_t>(b - static_cast<uint32_t>(n) * kDigitB);
+}
+__device__ __forceinline__ int64_t fixed_left(const Row& r, float pv, float qv) {
+  const Digits x = r.q ? left_of<true>(r, pv, qv) : left_of<false>(r, pv, qv);
+  return fixed_of(x.a, x.b, 1);
 }
 
-// Sums of the CTA's chunks [c_lo, c_hi) of kChunk elements into s_sum (index c - c_lo), a warp a
-// chunk, 32 elements a lane.
-template <class T>
-__device__ void chunk_sums(const Row& r, int vocab, int c_lo, int c_hi, int64_t* s_sum) {
+// Sums of the CTA's chunks [c_lo, c_hi) of kChunk places into s_sum (index c - c_lo), a warp a chunk,
+// its lanes taking blocks in turn.  Chunks are of the target's row in its own alignment; the
+// drafter's row is read beside it, in blocks where it is aligned alike, else an element at a time.
+template <class T, bool kQ>
+__device__ __noinline__ void chunk_sums(const Row& r, int vocab, int c_lo, int c_hi, int64_t* s_sum) {
+  constexpr int kVec = RowOf<T>::kVec, kLaneBlocks = kChunk / kVec / 32, kAhead = kQ ? 4 : 8;
+  static_assert(kLaneBlocks % 4 == 0, "chunk");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T* rp = static_cast<const T*>(r.p);
-  const T* rq = static_cast<const T*>(r.q);
+  const RowOf<T> rp(static_cast<const T*>(r.p), vocab);
+  const RowOf<T> rq(kQ ? static_cast<const T*>(r.q) : static_cast<const T*>(r.p), vocab);
+  const bool alike = rp.skew == rq.skew;
+  const T zero = T(0.f);
   for (int c = c_lo + warp; c < c_hi; c += kVerifyWarps) {
-    const int i0 = c * kChunk + lane;
-    int64_t sum = 0;
+    uint32_t a = 0, b = 0;
+#pragma unroll 1
+    for (int h = 0; h < kLaneBlocks; h += (kAhead < kLaneBlocks ? kAhead : kLaneBlocks)) {
+      constexpr int kNow = kAhead < kLaneBlocks ? kAhead : kLaneBlocks;
+      uint4 pv[kNow], qv[kNow];
+      const int k0 = c * (kChunk / kVec) + h * 32 + lane;
 #pragma unroll
-    for (int h = 0; h < kPerLane; h += 16) {
-      T pv[16], qv[16];
+      for (int u = 0; u < kNow; ++u) pv[u] = rp.block(k0 + 32 * u, zero);
+      if (kQ) {
+        if (alike) {
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        const int i = i0 + 32 * (h + u);
-        pv[u] = i < vocab ? rp[i] : T(0.f);
-      }
-      if (rq) {
+          for (int u = 0; u < kNow; ++u) qv[u] = rq.block(k0 + 32 * u, zero);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const int i = i0 + 32 * (h + u);
-          qv[u] = i < vocab ? rq[i] : T(0.f);
+          for (int u = 0; u < kNow; ++u) {
+            union { uint4 v; T x[kVec]; } z;
+            const int i0 = (k0 + 32 * u) * kVec - rp.skew;              // element of the row
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+              z.x[i] = i0 + i >= 0 && i0 + i < vocab ? static_cast<const T*>(r.q)[i0 + i] : zero;
+            qv[u] = z.v;
+          }
         }
       }
 #pragma unroll
-      for (int u = 0; u < 16; ++u) sum += left_of<T>(r, to_f32(pv[u]), rq ? to_f32(qv[u]) : 0.f);
+      for (int u = 0; u < kNow; ++u)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const Digits x = left_of<kQ>(r, element<T>(pv[u], i), kQ ? element<T>(qv[u], i) : 0.f);
+          a += x.a;
+          b += x.b;
+        }
     }
+    int64_t sum = fixed_of(a, b, kLaneBlocks * kVec);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[c - c_lo] = sum;
@@ -281,21 +408,24 @@ verify_sample_kernel(const VerifyParams p) {
   }
   cluster.sync();                                  // also: every CTA is running
   if (!ok) return;
-  const int chunks = (p.vocab + kChunk - 1) / kChunk;
-  const int per = (chunks + parts - 1) / parts;
-  const int c_lo = min(chunks, part * per), c_hi = min(chunks, c_lo + per);
+  int c_lo = 0, c_hi = 0;                          // the CTA's chunks of the row
   int sums = 0;                                    // sums taken so far
   // Sum of the row over the cluster; `before`: the sum of the CTAs ahead of this one.  Refused
   // tokens (without a drafter) are taken out of their chunks.
   uint64_t gone = 0;                               // refused children of the node, one bit each
   auto total_of = [&](const Row& r, int64_t& before) -> int64_t {
-    chunk_sums<T>(r, p.vocab, c_lo, c_hi, s_sum);
+    const RowOf<T> rp(static_cast<const T*>(r.p), p.vocab);
+    const int chunks = (rp.end + kChunk - 1) / kChunk, per = (chunks + parts - 1) / parts;
+    c_lo = min(chunks, part * per);
+    c_hi = min(chunks, c_lo + per);
+    if (r.q) chunk_sums<T, true>(r, p.vocab, c_lo, c_hi, s_sum);
+    else chunk_sums<T, false>(r, p.vocab, c_lo, c_hi, s_sum);
     __syncthreads();
     if (t == 0 && gone) {
       for (uint64_t m = gone; m; m &= m - 1) {
         const int i = __ffsll(static_cast<long long>(m)) - 1;
-        const int c = w.tok[i] / kChunk;
-        if (c >= c_lo && c < c_hi) s_sum[c - c_lo] -= fixed_of(s_p[i]);
+        const int c = (w.tok[i] + rp.skew) / kChunk;
+        if (c >= c_lo && c < c_hi) s_sum[c - c_lo] -= fixed_left(r, s_p[i], 0.f);
       }
     }
     __syncthreads();
@@ -326,7 +456,7 @@ verify_sample_kernel(const VerifyParams p) {
   while (true) {                                   // one node of the path per turn
     r.p = P + static_cast<int64_t>(w.q0 + cur) * p.p_stride;
     r.q = nullptr;
-    r.S = 0;
+    r.set(0);
     gone = 0;
     double left = 1.0;                             // Z: what w sums to
     int child = -1;
@@ -338,21 +468,17 @@ verify_sample_kernel(const VerifyParams p) {
       const double u = s_u[i];
       if (Q) {
         const double ql = static_cast<double>(s_q[i]);
-        double wl = s_p[i];
-        if (r.S)                                   // S q as in left_of, in units of 2^-52
-          wl = static_cast<double>(max(static_cast<long long>(0), static_cast<long long>(fixed_of(s_p[i]) -
-               static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(fixed_of(s_q[i])) << 7, r.S))))) *
-               2.220446049250313e-16;
+        const double wl = r.q ? static_cast<double>(fixed_left(r, s_p[i], s_q[i])) * kUnit : s_p[i];
         if (known && u * ql * left < wl) {
           child = i;
           break;
         }
         r.q = Q + static_cast<int64_t>(w.q0 + cur) * p.q_stride;
         const uint64_t add = static_cast<uint64_t>(left * 144115188075855872.0);   // Z 2^57, exact
-        r.S = r.S + add < r.S ? ~0ull : r.S + add;
+        r.set(r.S + add < r.S ? ~0ull : r.S + add);
         if (kids) {
           int64_t before;
-          left = static_cast<double>(total_of(r, before)) * 2.220446049250313e-16;
+          left = static_cast<double>(total_of(r, before)) * kUnit;
         }
       } else {
         bool again = !known;                       // a token that has left the row already
@@ -376,7 +502,7 @@ verify_sample_kernel(const VerifyParams p) {
   int64_t before, all = total_of(r, before);
   if (all == 0) {                                  // nothing left of the row: p itself
     r.q = nullptr;
-    r.S = 0;
+    r.set(0);
     gone = 0;
     all = total_of(r, before);
   }
@@ -397,21 +523,21 @@ verify_sample_kernel(const VerifyParams p) {
         const uint32_t past = __ballot_sync(0xffffffffu, run + upto > goal);
         if (run <= goal && past) {
           const int f = __ffs(past) - 1;
-          const int c = c_lo + c0 + f;
           run += __shfl_sync(0xffffffffu, upto - mine, f);
-          // lane l takes the chunk's elements 32 l .. 32 l + 31
+          // lane l takes the chunk's places 32 l .. 32 l + 31
           const T* rp = static_cast<const T*>(r.p);
           const T* rq = static_cast<const T*>(r.q);
-          const int i0 = c * kChunk + lane * kPerLane;
-          int64_t v[kPerLane], sum = 0;
-#pragma unroll
-          for (int u = 0; u < kPerLane; ++u) {
-            const int i = i0 + u;
-            v[u] = i < p.vocab ? left_of<T>(r, to_f32(rp[i]), rq ? to_f32(rq[i]) : 0.f) : 0;
+          const RowOf<T> row(rp, p.vocab);
+          const int i0 = (c_lo + c0 + f) * kChunk + lane * kPerLane - row.skew;
+          int64_t sum = 0;
+          auto value = [&](int i) -> int64_t {
+            if (i < 0 || i >= p.vocab) return 0;
             for (uint64_t m = gone; m; m &= m - 1)
-              if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i) v[u] = 0;
-            sum += v[u];
-          }
+              if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i) return 0;
+            return fixed_left(r, to_f32(rp[i]), rq ? to_f32(rq[i]) : 0.f);
+          };
+#pragma unroll 8
+          for (int u = 0; u < kPerLane; ++u) sum += value(i0 + u);
           int64_t to = sum;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -422,10 +548,10 @@ verify_sample_kernel(const VerifyParams p) {
           if (lane == __ffs(hit) - 1) {
             int64_t at = run + to - sum;
             int found = -1;
-#pragma unroll
-            for (int u = 0; u < kPerLane; ++u) {
-              at += v[u];
-              if (found < 0 && at > goal) found = i0 + u;
+#pragma unroll 1
+            for (int u = 0; u < kPerLane && found < 0; ++u) {
+              at += value(i0 + u);
+              if (at > goal) found = i0 + u;
             }
             *cluster.map_shared_rank(&s_next, 0) = found;
           }
@@ -578,7 +704,7 @@ extern "C" int mtp_tree_verify_sample(const void* target_probs, int64_t target_s
   p.out_tokens = out_tokens;
   p.status = status;
   const int c = cluster_size(num_seqs, vocab);
-  const int chunks = (vocab + kChunk - 1) / kChunk;
+  const int chunks = (vocab + 8 + kChunk - 1) / kChunk;   // (a row may start up to 7 places into a block)
   const size_t smem = static_cast<size_t>((chunks + c - 1) / c) * sizeof(int64_t);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
