@@ -7,8 +7,8 @@
 // row's scan is split over the CTAs, whose results meet through distributed shared memory.
 //
 // Rows are read in 16-byte blocks at the addresses' own alignment, whatever the row's: block k holds
-// the elements k * kVec - skew .. + kVec - 1, skew being how far the row's start lies into one, and
-// the two blocks at the row's ends are read an element at a time.
+// the elements k * kVec - skew .. + kVec - 1, skew being how far the row's start lies into one.  The
+// blocks at the row's ends, which may not be whole, are read an element at a time.
 #include "common.cuh"
 #include "host_checks.cuh"
 
@@ -30,8 +30,7 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = MTP_TREE_MAX_NODES;
-constexpr int kChunk = 1024;                       // elements whose sum is kept (sampling)
-constexpr int kPerLane = kChunk / 32;
+constexpr int kChunk = 512;                        // places whose sum is kept (sampling)
 
 struct VerifyParams {
   const void* p;             // logits, or the target's probabilities
@@ -127,16 +126,10 @@ struct RowOf {
     at = row - skew;
     end = skew + vocab;
   }
-  __device__ __forceinline__ int blocks() const { return (end + kVec - 1) / kVec; }
-  // Block k; places outside the row hold `fill`.
-  __device__ __forceinline__ uint4 block(int k, T fill) const {
-    const int i0 = k * kVec;
-    if (i0 >= skew && i0 + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(at + i0));
-    union { uint4 v; T x[kVec]; } u;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) u.x[i] = i0 + i >= skew && i0 + i < end ? at[i0 + i] : fill;
-    return u.v;
-  }
+  // Whole blocks: first .. last - 1.
+  __device__ __forceinline__ int first() const { return skew ? 1 : 0; }
+  __device__ __forceinline__ int last() const { return end / kVec; }
+  __device__ __forceinline__ uint4 block(int k) const { return __ldg(reinterpret_cast<const uint4*>(at) + k); }
 };
 
 // Element i of a block.
@@ -186,11 +179,12 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// A thread looks at its blocks' largest elements, and keeps the block that first has the largest
-// of them; where in it, is looked up once at the end.  kUnroll blocks are in flight: what bounds a
-// step is that latency, then two meetings of the cluster.
+// A thread looks at its whole blocks' largest elements, and keeps the block that first has the
+// largest of them; where in it, is looked up once at the end.  kUnroll blocks are in flight: what
+// bounds a step is that latency, then two meetings of the cluster.  The elements before the first
+// and behind the last whole block, at most 2 kVec - 2, are a thread's each.
 template <class T>
-__global__ void __launch_bounds__(kVerifyThreads)
+__global__ void __launch_bounds__(kVerifyThreads, 2)
 verify_greedy_kernel(const VerifyParams p) {
   constexpr int kUnroll = 8, kVec = RowOf<T>::kVec;
   __shared__ Walk w;
@@ -203,19 +197,30 @@ verify_greedy_kernel(const VerifyParams p) {
   // every CTA of the cluster has to be running before its shared memory is written
   cluster.sync();
   if (!ok) return;
-  const T lowest = T(-INFINITY);
   int cur = 0, count = 0, next = -1;
   for (int step = 0;; ++step) {
     const RowOf<T> row(static_cast<const T*>(p.p) + static_cast<int64_t>(w.q0 + cur) * p.p_stride, p.vocab);
-    const int blocks = row.blocks(), per = (blocks + parts - 1) / parts;
-    const int lo = min(blocks, part * per), hi = min(blocks, lo + per);
+    const int first = row.first(), last = max(first, row.last()), per = (last - first + parts - 1) / parts;
+    const int lo = min(last, first + part * per), hi = min(last, lo + per);
+    auto key_of = [&](float x, int place) -> uint64_t {   // largest value, then lowest token
+      return static_cast<uint64_t>(order_of(x)) << 32 | static_cast<uint32_t>(~(place - row.skew));
+    };
+    uint64_t key = 0;                              // 0: nothing but NaN
+    if (part == 0) {
+      const int place = t < kVec ? row.skew + t : last * kVec + t - kVec;   // before, and behind
+      if (t < 2 * kVec && place < row.end && place >= row.skew && (t >= kVec || place < first * kVec)) {
+        const float x = to_f32(row.at[place]);
+        if (x == x) key = key_of(x, place);
+      }
+    }
     float best = -INFINITY;
     int at = lo + t;                               // (what -inf leaves: this thread's first block)
+#pragma unroll 1
     for (int k0 = lo + t; k0 < hi; k0 += kUnroll * kVerifyThreads) {
       uint4 v[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
-        if (k0 + u * kVerifyThreads < hi) v[u] = row.block(k0 + u * kVerifyThreads, lowest);
+        if (k0 + u * kVerifyThreads < hi) v[u] = row.block(k0 + u * kVerifyThreads);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
         if (k0 + u * kVerifyThreads < hi) {
@@ -226,14 +231,16 @@ verify_greedy_kernel(const VerifyParams p) {
           }
         }
     }
-    // largest value, then lowest token; 0: nothing but NaN
-    uint64_t key = 0;
-    for (int k = at; k < hi && key == 0; k += kVerifyThreads) {   // (one block, unless best is -inf)
-      const uint4 v = row.block(k, T(NAN));
+#pragma unroll 1
+    for (int k = at, found = 0; k < hi && !found; k += kVerifyThreads) {   // (one block, unless best is -inf)
+      const uint4 v = row.block(k);
 #pragma unroll
       for (int i = kVec - 1; i >= 0; --i)
-        if (element<T>(v, i) == best)
-          key = static_cast<uint64_t>(order_of(best)) << 32 | static_cast<uint32_t>(~(k * kVec + i - row.skew));
+        if (element<T>(v, i) == best) found = i + 1;
+      if (found) {
+        const uint64_t x = key_of(best, k * kVec + found - 1);
+        key = x > key ? x : key;
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -273,7 +280,9 @@ verify_greedy_kernel(const VerifyParams p) {
 // conversion instruction (these run at a quarter rate, and one to 64 bits at half of that): with
 // w = d + e, d in f32 and e its error, the low 23 bits of 1 + d are d to units of 2^-23, and what
 // that leaves, with e, is at most 2^-24 + 2^-25 and becomes the second digit as the low bits of
-// r 2^45 + 3 * 2^22.  A lane's digits are summed in 32 bits over a chunk, offsets and all.
+// r 2^45 + 3 * 2^22.  A lane's digits are summed in 32 bits over a chunk, offsets and all.  Steps
+// that are the same for all elements are made for two at a time (f32x2): a sum costs 9 (S = 1) or 15
+// instructions an element, and is bound by them once the rows are in L2.
 
 struct Row {
   const void* p;
@@ -286,89 +295,119 @@ struct Row {
     s_hi = static_cast<float>(x);
     s_lo = static_cast<float>(x - static_cast<double>(s_hi));
   }
+  // 0: w = p; 1: S = 1, what the first refusal leaves; 2: any S
+  __device__ __forceinline__ int mode() const { return !q ? 0 : S == (1ull << 57) ? 1 : 2; }
 };
 
-struct Digits {
-  uint32_t a, b;             // low 23 bits of a: units of 2^-23; b - 0x4B400000: units of 2^-45, signed
-};
 constexpr uint32_t kDigitA = 0x3F800000u, kDigitB = 0x4B400000u;          // what w = 0 gives
 constexpr double kUnit = 2.8421709430404007e-14;                          // 2^-45
 
-__device__ __forceinline__ Digits digits_of(float d, float e) {           // d + e, 0 <= d <= 1
-  const float a = __fadd_rn(d, 1.f);
-  const float r = __fadd_rn(__fsub_rn(d, __fsub_rn(a, 1.f)), e);
-  return {__float_as_uint(a), __float_as_uint(__fmaf_rn(r, 35184372088832.f, 12582912.f))};
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{\n .reg .b64 ra, rb, rc;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mov.b64 rc, {%6, %7};\n"
+      " fma.rn.f32x2 ra, ra, rb, rc;\n mov.b64 {%0, %1}, ra;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
-template <bool kQ>
-__device__ __forceinline__ Digits left_of(const Row& r, float pv, float qv) {
-  pv = __saturatef(pv);                              // into [0, 1]; NaN as 0
-  if (!kQ) return digits_of(pv, 0.f);
-  qv = __saturatef(qv);
-  const float h = __fmul_rn(r.s_hi, qv);             // S q = h + l
-  const float l = __fmaf_rn(r.s_lo, qv, __fmaf_rn(r.s_hi, qv, -h));
-  float d = __fsub_rn(pv, h);
-  float e = __fsub_rn(__fsub_rn(__fsub_rn(pv, d), h), l);                 // exact but for l where d > 0
-  const bool some = __fadd_rn(d, e) > 0.f && d >= 0.f;
-  d = some ? d : 0.f;
-  e = some ? e : 0.f;
-  return digits_of(d, e);
+__device__ __forceinline__ F2 both(float x) { return {x, x}; }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return fma2(a, both(1.f), b); }
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, both(-1.f), a); }
+
+// The digits of two elements added to (a, b).
+template <int kMode>
+__device__ __forceinline__ void add_left(const Row& r, F2 p, F2 q, uint32_t& a, uint32_t& b) {
+  p = {__saturatef(p.x), __saturatef(p.y)};          // into [0, 1]; NaN as 0
+  F2 d = p, e = both(0.f);
+  if (kMode == 1) {
+    q = {fminf(fmaxf(q.x, 0.f), p.x), fminf(fmaxf(q.y, 0.f), p.y)};      // p - min(q, p): never below 0
+    d = sub2(p, q);
+    e = sub2(sub2(p, d), q);                         // exact
+  }
+  if (kMode == 2) {
+    q = {__saturatef(q.x), __saturatef(q.y)};
+    const F2 s = both(r.s_hi), h = fma2(s, q, both(0.f));                // S q = h + l
+    const F2 l = fma2(both(r.s_lo), q, fma2(s, q, {-h.x, -h.y}));
+    d = sub2(p, h);
+    e = sub2(sub2(sub2(p, d), h), l);                // exact but for l where d > 0
+    const F2 w = add2(d, e);
+    const bool some_x = w.x > 0.f && d.x >= 0.f, some_y = w.y > 0.f && d.y >= 0.f;
+    d = {some_x ? d.x : 0.f, some_y ? d.y : 0.f};
+    e = {some_x ? e.x : 0.f, some_y ? e.y : 0.f};
+  }
+  const F2 one = add2(d, both(1.f));
+  F2 rest = sub2(d, sub2(one, both(1.f)));
+  if (kMode != 0) rest = add2(rest, e);
+  const F2 low = fma2(rest, both(35184372088832.f), both(12582912.f));   // 2^45, 3 * 2^22
+  a += __float_as_uint(one.x);
+  a += __float_as_uint(one.y);
+  b += __float_as_uint(low.x);
+  b += __float_as_uint(low.y);
 }
 __device__ __forceinline__ int64_t fixed_of(uint32_t a, uint32_t b, int n) {   // sums over n elements
   return (static_cast<int64_t>(a - static_cast<uint32_t>(n) * kDigitA) << 22) +
          static_cast<int32_t>(b - static_cast<uint32_t>(n) * kDigitB);
 }
-__device__ __forceinline__ int64_t fixed_left(const Row& r, float pv, float qv) {
-  const Digits x = r.q ? left_of<true>(r, pv, qv) : left_of<false>(r, pv, qv);
-  return fixed_of(x.a, x.b, 1);
+// One element (a second one of 0 beside it).
+__device__ __noinline__ int64_t fixed_left(const Row& r, float p, float q) {
+  uint32_t a = 0, b = 0;
+  const int mode = r.mode();
+  if (mode == 0) add_left<0>(r, {p, 0.f}, {0.f, 0.f}, a, b);
+  else if (mode == 1) add_left<1>(r, {p, 0.f}, {q, 0.f}, a, b);
+  else add_left<2>(r, {p, 0.f}, {q, 0.f}, a, b);
+  return fixed_of(a, b, 2);
 }
 
 // Sums of the CTA's chunks [c_lo, c_hi) of kChunk places into s_sum (index c - c_lo), a warp a chunk,
-// its lanes taking blocks in turn.  Chunks are of the target's row in its own alignment; the
-// drafter's row is read beside it, in blocks where it is aligned alike, else an element at a time.
-template <class T, bool kQ>
+// its lanes taking blocks in turn.  Chunks are of the target's row in its own alignment; a chunk
+// with a block that is not whole, or beside a drafter's row of another alignment, is read an
+// element at a time.
+template <class T, int kMode>
 __device__ __noinline__ void chunk_sums(const Row& r, int vocab, int c_lo, int c_hi, int64_t* s_sum) {
-  constexpr int kVec = RowOf<T>::kVec, kLaneBlocks = kChunk / kVec / 32, kAhead = kQ ? 4 : 8;
-  static_assert(kLaneBlocks % 4 == 0, "chunk");
+  constexpr int kVec = RowOf<T>::kVec, kBlocks = kChunk / kVec / 32;   // blocks a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const RowOf<T> rp(static_cast<const T*>(r.p), vocab);
-  const RowOf<T> rq(kQ ? static_cast<const T*>(r.q) : static_cast<const T*>(r.p), vocab);
+  const T* P = static_cast<const T*>(r.p);
+  const T* Q = static_cast<const T*>(r.q);
+  const RowOf<T> rp(P, vocab);
+  const RowOf<T> rq(kMode ? Q : P, vocab);
   const bool alike = rp.skew == rq.skew;
-  const T zero = T(0.f);
+#pragma unroll 1
   for (int c = c_lo + warp; c < c_hi; c += kVerifyWarps) {
     uint32_t a = 0, b = 0;
+    const int k0 = c * (kChunk / kVec);
+    if (alike && k0 >= rp.first() && k0 + kChunk / kVec <= rp.last()) {
+      uint4 pv[kBlocks], qv[kBlocks];
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) pv[u] = rp.block(k0 + 32 * u + lane);
+      if (kMode)
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u) qv[u] = rq.block(k0 + 32 * u + lane);
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u)
+#pragma unroll
+        for (int i = 0; i < kVec; i += 2)
+          add_left<kMode>(r, {element<T>(pv[u], i), element<T>(pv[u], i + 1)},
+                          kMode ? F2{element<T>(qv[u], i), element<T>(qv[u], i + 1)} : both(0.f), a, b);
+    } else {
+      const int i0 = c * kChunk - rp.skew + lane;
 #pragma unroll 1
-    for (int h = 0; h < kLaneBlocks; h += (kAhead < kLaneBlocks ? kAhead : kLaneBlocks)) {
-      constexpr int kNow = kAhead < kLaneBlocks ? kAhead : kLaneBlocks;
-      uint4 pv[kNow], qv[kNow];
-      const int k0 = c * (kChunk / kVec) + h * 32 + lane;
+      for (int h = 0; h < kChunk / 32; h += 8) {
+        float pv[8], qv[8];
 #pragma unroll
-      for (int u = 0; u < kNow; ++u) pv[u] = rp.block(k0 + 32 * u, zero);
-      if (kQ) {
-        if (alike) {
-#pragma unroll
-          for (int u = 0; u < kNow; ++u) qv[u] = rq.block(k0 + 32 * u, zero);
-        } else {
-#pragma unroll
-          for (int u = 0; u < kNow; ++u) {
-            union { uint4 v; T x[kVec]; } z;
-            const int i0 = (k0 + 32 * u) * kVec - rp.skew;              // element of the row
-#pragma unroll
-            for (int i = 0; i < kVec; ++i)
-              z.x[i] = i0 + i >= 0 && i0 + i < vocab ? static_cast<const T*>(r.q)[i0 + i] : zero;
-            qv[u] = z.v;
-          }
+        for (int u = 0; u < 8; ++u) {
+          const int i = i0 + 32 * (h + u);
+          const bool in = i >= 0 && i < vocab;
+          pv[u] = in ? to_f32(P[i]) : 0.f;
+          qv[u] = kMode && in ? to_f32(Q[i]) : 0.f;
         }
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) add_left<kMode>(r, {pv[u], pv[u + 1]}, {qv[u], qv[u + 1]}, a, b);
       }
-#pragma unroll
-      for (int u = 0; u < kNow; ++u)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const Digits x = left_of<kQ>(r, element<T>(pv[u], i), kQ ? element<T>(qv[u], i) : 0.f);
-          a += x.a;
-          b += x.b;
-        }
     }
-    int64_t sum = fixed_of(a, b, kLaneBlocks * kVec);
+    int64_t sum = fixed_of(a, b, kChunk / 32);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[c - c_lo] = sum;
@@ -376,13 +415,15 @@ __device__ __noinline__ void chunk_sums(const Row& r, int vocab, int c_lo, int c
 }
 
 template <class T>
-__global__ void __launch_bounds__(kVerifyThreads)
+__global__ void __launch_bounds__(kVerifyThreads, 2)
 verify_sample_kernel(const VerifyParams p) {
   extern __shared__ int64_t s_sum[];               // the CTA's chunk sums
   __shared__ Walk w;
   __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];   // p, q of each node's token, its number
   __shared__ int64_t s_part[2][kMaxCluster];       // by sum parity: the CTAs' sums
   __shared__ int64_t s_warp[kVerifyWarps];
+  constexpr int kSteps = kChunk / 32;
+  __shared__ int64_t s_val[kSteps][33];            // the values of the chunk drawn from
   __shared__ int s_next;
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), part = cluster.block_rank();
@@ -418,8 +459,10 @@ verify_sample_kernel(const VerifyParams p) {
     const int chunks = (rp.end + kChunk - 1) / kChunk, per = (chunks + parts - 1) / parts;
     c_lo = min(chunks, part * per);
     c_hi = min(chunks, c_lo + per);
-    if (r.q) chunk_sums<T, true>(r, p.vocab, c_lo, c_hi, s_sum);
-    else chunk_sums<T, false>(r, p.vocab, c_lo, c_hi, s_sum);
+    const int mode = r.mode();
+    if (mode == 0) chunk_sums<T, 0>(r, p.vocab, c_lo, c_hi, s_sum);
+    else if (mode == 1) chunk_sums<T, 1>(r, p.vocab, c_lo, c_hi, s_sum);
+    else chunk_sums<T, 2>(r, p.vocab, c_lo, c_hi, s_sum);
     __syncthreads();
     if (t == 0 && gone) {
       for (uint64_t m = gone; m; m &= m - 1) {
@@ -524,37 +567,50 @@ verify_sample_kernel(const VerifyParams p) {
         if (run <= goal && past) {
           const int f = __ffs(past) - 1;
           run += __shfl_sync(0xffffffffu, upto - mine, f);
-          // lane l takes the chunk's places 32 l .. 32 l + 31
+          // The chunk's values once more, 32 consecutive ones a step, into shared memory; then lane l
+          // sums those of step l, and the 32 of the step that passes the goal are looked at.
           const T* rp = static_cast<const T*>(r.p);
           const T* rq = static_cast<const T*>(r.q);
           const RowOf<T> row(rp, p.vocab);
-          const int i0 = (c_lo + c0 + f) * kChunk + lane * kPerLane - row.skew;
-          int64_t sum = 0;
-          auto value = [&](int i) -> int64_t {
-            if (i < 0 || i >= p.vocab) return 0;
-            for (uint64_t m = gone; m; m &= m - 1)
-              if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i) return 0;
-            return fixed_left(r, to_f32(rp[i]), rq ? to_f32(rq[i]) : 0.f);
-          };
-#pragma unroll 8
-          for (int u = 0; u < kPerLane; ++u) sum += value(i0 + u);
-          int64_t to = sum;
+          const int i0 = (c_lo + c0 + f) * kChunk - row.skew;
+          float pv[kSteps], qv[kSteps];
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, to, o);
-            if (lane >= o) to += x;
+          for (int u = 0; u < kSteps; ++u) {
+            const int i = i0 + 32 * u + lane;
+            const bool in = i >= 0 && i < p.vocab;
+            pv[u] = in ? to_f32(rp[i]) : 0.f;
+            qv[u] = in && rq ? to_f32(rq[i]) : 0.f;
           }
-          const uint32_t hit = __ballot_sync(0xffffffffu, run + to > goal);
-          if (lane == __ffs(hit) - 1) {
-            int64_t at = run + to - sum;
-            int found = -1;
+#pragma unroll
+          for (int u = 0; u < kSteps; ++u) s_val[u][lane] = static_cast<int64_t>(__float_as_uint(pv[u])) << 32 | __float_as_uint(qv[u]);
+          __syncwarp();
 #pragma unroll 1
-            for (int u = 0; u < kPerLane && found < 0; ++u) {
-              at += value(i0 + u);
-              if (at > goal) found = i0 + u;
-            }
-            *cluster.map_shared_rank(&s_next, 0) = found;
+          for (int u = 0; u < kSteps; ++u) {
+            const int64_t x = s_val[u][lane];
+            int64_t v = fixed_left(r, __uint_as_float(static_cast<uint32_t>(x >> 32)), __uint_as_float(static_cast<uint32_t>(x)));
+            for (uint64_t m = gone; m; m &= m - 1)
+              if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i0 + 32 * u + lane) v = 0;
+            s_val[u][lane] = v;
           }
+          __syncwarp();
+          int64_t sum = 0;
+          if (lane < kSteps)
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) sum += s_val[lane][i];
+          auto first_past = [&](int64_t v, int64_t& at) -> int {      // at: before lane 0, then before it
+            int64_t to = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int64_t x = __shfl_up_sync(0xffffffffu, to, o);
+              if (lane >= o) to += x;
+            }
+            const int k = __ffs(__ballot_sync(0xffffffffu, at + to > goal)) - 1;
+            at += __shfl_sync(0xffffffffu, to - v, max(k, 0));
+            return k;
+          };
+          const int step = first_past(sum, run);
+          const int nth = step < 0 ? -1 : first_past(s_val[step][lane], run);
+          if (lane == 0 && nth >= 0) *cluster.map_shared_rank(&s_next, 0) = i0 + 32 * step + nth;
           break;
         }
         run += __shfl_sync(0xffffffffu, upto, 31);
