@@ -325,55 +325,42 @@ def fmha_fwd_fp8_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_des
 
 # ---- draft trees (include/mtp_tree.h) ------------------------------------------------------------
 #
-# These calls are short: the checks are written for few Python operations (an attribute of a
-# tensor costs 0.1 us, torch.cuda.current_stream() 3 us, torch.empty 1.6 us on a Grace core).
+# These calls are short, so their checks, the outputs that are not given and the call itself are in
+# csrc/binding.cpp (arguments by position; None: not given).
 
 TREE_MAX_NODES = 64
 TREE_MAX_RATIO = 16
 TREE_MAX_VOCAB = 1 << 20
 ERR_PARENT, ERR_ROW = 64, 128
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_I32, _BF16 = torch.int32, torch.bfloat16
-_CODES = (torch.uint8, torch.float8_e4m3fn)
-_WORDS = (torch.int64, torch.uint64)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+_BINDING = None
 
 
-def _call_stream(device: int, stream):
-    """The stream's handle for a call on tensors of this device (-1: the CPU, which the library
-    refuses).  The library launches on the current device: tensors of another one are refused
-    here, where the message can say so."""
-    if device >= 0 and device != _current_device():
-        raise ValueError(f"tensors are on cuda:{device}, the current device is "
-                         f"cuda:{_current_device()}")
-    if stream is None:
-        if device < 0:
-            return None
-        return _raw_stream(device) if _raw_stream else torch.cuda.current_stream().cuda_stream
+def binding():
+    """The compiled part of the binding (raises RuntimeError if it has not been built)."""
+    global _BINDING
+    if _BINDING is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the compiled binding is missing or does not load "
+                               f"({e}): build it with `python -m paged_fp8_speculative_gb300.build`")
+        _binding.set_error(MtpAttnError)
+        _BINDING = _binding
+    return _BINDING
+
+
+def _on_stream(call, args, stream, device):
+    """``call`` on a stream that was given: its handle goes last, and what the call makes is made on
+    that stream (see _temporaries_on)."""
     if isinstance(stream, torch.cuda.Stream):
-        if device >= 0 and stream.device.index != device:
-            raise ValueError(f"stream is on {stream.device}, tensors are on cuda:{device}")
-        return stream.cuda_stream
-    return int(stream)
-
-
-def _vector(name, t, n):
-    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector of {n}")
-
-
-def _sequences(cu_seqlens_q) -> int:
-    shape = cu_seqlens_q.shape
-    if cu_seqlens_q.dtype is not _I32 or len(shape) != 1 or shape[0] < 1 or \
-            not cu_seqlens_q.is_contiguous():
-        raise ValueError("cu_seqlens_q must be a contiguous int32 vector of num_seqs + 1")
-    return shape[0] - 1
-
-
-def _words(name, t, n):
-    if t.dtype not in _WORDS or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int64 vector, one word per node")
+        if device.type == "cuda" and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
+    with _temporaries_on(stream, device, True):
+        return call(*args, handle)
 
 
 def mtp_tree_mask(parents: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -384,19 +371,10 @@ def mtp_tree_mask(parents: torch.Tensor, cu_seqlens_q: torch.Tensor,
     parents [total_q] int32 (an index within the sequence; the root's entry is not read);
     cu_seqlens_q [B+1] int32; returns int64 [total_q] (the bits of the uint64 words).
     """
-    total_q = parents.numel()
-    _vector("parents", parents, total_q)
-    num_seqs = _sequences(cu_seqlens_q)
-    if out is None:
-        with _temporaries_on(stream, parents.device, stream is not None):
-            out = torch.empty(total_q, dtype=torch.int64, device=parents.device)
-    _words("out", out, total_q)
-    rc = lib().mtp_tree_mask(parents.data_ptr(), cu_seqlens_q.data_ptr(), num_seqs, total_q,
-                             out.data_ptr(), _ptr(status),
-                             _call_stream(parents.get_device(), stream))
-    if rc != OK:
-        raise MtpAttnError(rc)
-    return out
+    call = (_BINDING or binding()).tree_mask
+    if stream is None:
+        return call(parents, cu_seqlens_q, out, status, None)
+    return _on_stream(call, (parents, cu_seqlens_q, out, status), stream, parents.device)
 
 
 def mtp_tree_attn_workspace_size(num_seqs: int, total_q: int, num_q_heads: int,
@@ -420,84 +398,16 @@ def mtp_tree_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     least mtp_tree_attn_workspace_size(...) bytes, kept by a decode loop so that no call
     allocates; it needs no initialisation.
     """
-    device = q.get_device()
-    handle = _call_stream(device, stream)
-    shape, cache = q.shape, k_cache.shape
-    if q.dtype is not _BF16 or len(shape) != 3 or shape[2] != HEAD_DIM or q.stride(2) != 1:
-        raise ValueError("q must be bf16 [total_q, H_q, 256] with unit stride on head_dim")
-    if k_cache.dtype not in _CODES or v_cache.dtype is not k_cache.dtype:
-        raise ValueError("k_cache / v_cache must be uint8 or float8_e4m3fn codes")
-    if len(cache) != 4 or cache[1] != PAGE_SIZE or cache[3] != HEAD_DIM:
-        raise ValueError("k_cache must be [num_pages, 16, H_kv, 256]")
-    if v_cache.shape != cache or not k_cache.is_contiguous() or not v_cache.is_contiguous():
-        raise ValueError("k_cache and v_cache must be contiguous and of the same shape")
-    total_q, hq, _ = shape
-    num_seqs = _sequences(cu_seqlens_q)
-    _vector("seq_lens", seq_lens, num_seqs)
-    table = block_tables.shape
-    if block_tables.dtype is not _I32 or len(table) != 2 or table[0] != num_seqs or \
-            not block_tables.is_contiguous():
-        raise ValueError("block_tables must be a contiguous int32 [B, max_pages] tensor")
-    _words("tree_mask", tree_mask, total_q)
-    if out is None or workspace is None or not isinstance(k_descale, torch.Tensor) or \
-            not isinstance(v_descale, torch.Tensor):
-        dev = q.device
-        with _temporaries_on(stream, dev, stream is not None):
-            k_descale, v_descale = _descale(k_descale, dev), _descale(v_descale, dev)
-            if out is None:
-                out = torch.empty(shape, dtype=_BF16, device=dev)
-            if workspace is None:
-                need = mtp_tree_attn_workspace_size(num_seqs, total_q, hq, cache[2], table[1])
-                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    for name, t in (("k_descale", k_descale), ("v_descale", v_descale)):
-        if t.dtype is not torch.float32 or t.numel() != 1:
-            raise ValueError(f"{name} must be a 1-element float32 tensor")
-    if out.dtype is not _BF16 or out.shape != shape or out.stride(2) != 1:
-        raise ValueError("out must be bf16 [total_q, H_q, 256] with unit stride on head_dim")
-    q_tok, q_head, _ = q.stride()
-    o_tok, o_head, _ = out.stride()
-    rc = lib().mtp_tree_attn_fwd(
-        q.data_ptr(), q_tok, q_head, k_cache.data_ptr(), v_cache.data_ptr(), cache[0],
-        block_tables.data_ptr(), table[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
-        tree_mask.data_ptr(), num_seqs, total_q, hq, cache[2], k_descale.data_ptr(),
-        v_descale.data_ptr(), softmax_scale, workspace.data_ptr(), workspace.nbytes,
-        out.data_ptr(), o_tok, o_head, _ptr(status), handle)
-    if rc != OK:
-        raise MtpAttnError(rc)
-    return out
-
-
-def _verify_args(rows, name, draft_tokens, parents, cu_seqlens_q, max_path, accept_index,
-                 accept_len, out_tokens, stream):
-    """Checks shared by the two verifications; makes the outputs that were not given.  Returns
-    (dtype, total_q, vocab, row stride, num_seqs, the outputs)."""
-    dtype, shape = _DTYPES.get(rows.dtype), rows.shape
-    if dtype is None or len(shape) != 2 or shape[1] > 1 and rows.stride(1) != 1:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16 [total_q, vocab] with unit "
-                         "stride along the vocabulary")
-    total_q, vocab = shape
-    _vector("draft_tokens", draft_tokens, total_q)
-    _vector("parents", parents, total_q)
-    num_seqs = _sequences(cu_seqlens_q)
-    if accept_index is None or accept_len is None or out_tokens is None:
-        dev = rows.device
-        with _temporaries_on(stream, dev, stream is not None):
-            if accept_index is None:
-                accept_index = torch.empty((num_seqs, max_path), dtype=_I32, device=dev)
-            if accept_len is None:
-                accept_len = torch.empty(num_seqs, dtype=_I32, device=dev)
-            if out_tokens is None:
-                out_tokens = torch.empty((num_seqs, max_path), dtype=_I32, device=dev)
-    for what, t in (("accept_index", accept_index), ("out_tokens", out_tokens)):
-        if t.dtype is not _I32 or t.shape != (num_seqs, max_path) or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous int32 [num_seqs, max_path] tensor")
-    _vector("accept_len", accept_len, num_seqs)
-    return dtype, total_q, vocab, _row_stride(rows), num_seqs, accept_index, accept_len, out_tokens
-
-
-def _row_stride(t):
-    """Elements from row to row; a single row's stride means nothing to torch."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    call = (_BINDING or binding()).tree_attn
+    if not (isinstance(k_descale, torch.Tensor) and isinstance(v_descale, torch.Tensor)):
+        with _temporaries_on(stream, q.device, True):
+            k_descale, v_descale = _descale(k_descale, q.device), _descale(v_descale, q.device)
+    if stream is None:
+        return call(q, k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q, tree_mask,
+                    k_descale, v_descale, softmax_scale, out, workspace, status, None)
+    return _on_stream(call, (q, k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q, tree_mask,
+                             k_descale, v_descale, softmax_scale, out, workspace, status), stream,
+                      q.device)
 
 
 def mtp_tree_verify_greedy(logits: torch.Tensor, draft_tokens: torch.Tensor,
@@ -514,17 +424,12 @@ def mtp_tree_verify_greedy(logits: torch.Tensor, draft_tokens: torch.Tensor,
     root's 0, the accepted nodes, -1s; accept_len [B] int32; out_tokens [B, max_path] int32: the
     accepted tokens, the next token, -1s).
     """
-    handle = _call_stream(logits.get_device(), stream)
-    dtype, total_q, vocab, stride, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
-        logits, "logits", draft_tokens, parents, cu_seqlens_q, max_path, accept_index, accept_len,
-        out_tokens, stream)
-    rc = lib().mtp_tree_verify_greedy(
-        logits.data_ptr(), dtype, stride, vocab, draft_tokens.data_ptr(), parents.data_ptr(),
-        cu_seqlens_q.data_ptr(), num_seqs, total_q, max_path, accept_index.data_ptr(),
-        accept_len.data_ptr(), out_tokens.data_ptr(), _ptr(status), handle)
-    if rc != OK:
-        raise MtpAttnError(rc)
-    return accept_index, accept_len, out_tokens
+    call = (_BINDING or binding()).verify_greedy
+    if stream is None:
+        return call(logits, draft_tokens, parents, cu_seqlens_q, max_path, accept_index,
+                    accept_len, out_tokens, status, None)
+    return _on_stream(call, (logits, draft_tokens, parents, cu_seqlens_q, max_path, accept_index,
+                             accept_len, out_tokens, status), stream, logits.device)
 
 
 def mtp_tree_verify_sample(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor],
@@ -542,69 +447,19 @@ def mtp_tree_verify_sample(target_probs: torch.Tensor, draft_probs: Optional[tor
     were drawn from, or None (children chosen outright); uniforms [total_q] float32 in [0, 1):
     each node's own number, the root's for the final draw.  Returns as mtp_tree_verify_greedy.
     """
-    handle = _call_stream(target_probs.get_device(), stream)
-    dtype, total_q, vocab, stride, num_seqs, accept_index, accept_len, out_tokens = _verify_args(
-        target_probs, "target_probs", draft_tokens, parents, cu_seqlens_q, max_path, accept_index,
-        accept_len, out_tokens, stream)
-    draft, draft_stride = None, 0
-    if draft_probs is not None:
-        if draft_probs.dtype is not target_probs.dtype or draft_probs.shape != (total_q, vocab) or \
-                vocab > 1 and draft_probs.stride(1) != 1:
-            raise ValueError("draft_probs must have target_probs' type and shape and unit stride "
-                             "along the vocabulary")
-        draft, draft_stride = draft_probs.data_ptr(), _row_stride(draft_probs)
-    if uniforms.dtype is not torch.float32 or uniforms.shape != (total_q,) or \
-            not uniforms.is_contiguous():
-        raise ValueError("uniforms must be a contiguous float32 vector, one number per node")
-    rc = lib().mtp_tree_verify_sample(
-        target_probs.data_ptr(), stride, draft, draft_stride, dtype, vocab,
-        draft_tokens.data_ptr(), parents.data_ptr(), cu_seqlens_q.data_ptr(), uniforms.data_ptr(),
-        num_seqs, total_q, max_path, accept_index.data_ptr(), accept_len.data_ptr(),
-        out_tokens.data_ptr(), _ptr(status), handle)
-    if rc != OK:
-        raise MtpAttnError(rc)
-    return accept_index, accept_len, out_tokens
+    call = (_BINDING or binding()).verify_sample
+    if stream is None:
+        return call(target_probs, draft_probs, draft_tokens, parents, cu_seqlens_q, uniforms,
+                    max_path, accept_index, accept_len, out_tokens, status, None)
+    return _on_stream(call, (target_probs, draft_probs, draft_tokens, parents, cu_seqlens_q,
+                             uniforms, max_path, accept_index, accept_len, out_tokens, status),
+                      stream, target_probs.device)
 
 
-# ---- the paged cache's upkeep (include/mtp_cache.h) ----------------------------------------------
+# ---- the paged cache's upkeep (include/mtp_cache.h; checks and calls in csrc/binding.cpp) ---------
 
 CACHE_MAX_ROWS = 8192
 ERR_LEN, ERR_FULL, ERR_REF, ERR_CACHE_ROW = 256, 512, 1024, 2048
-
-
-def _cache_args(k_cache, v_cache):
-    """(K's and V's address, layers, layer stride in bytes, pages, KV heads) of one layer's caches
-    [num_pages, 16, H_kv, 256] or of a stack's [num_layers, num_pages, 16, H_kv, 256]."""
-    shape = k_cache.shape
-    if k_cache.dtype not in _CODES or v_cache.dtype is not k_cache.dtype:
-        raise ValueError("k_cache / v_cache must be uint8 or float8_e4m3fn codes")
-    if len(shape) not in (4, 5) or shape[-3] != PAGE_SIZE or shape[-1] != HEAD_DIM:
-        raise ValueError("k_cache must be [num_pages, 16, H_kv, 256], or that behind num_layers")
-    stride = k_cache.stride()
-    if v_cache.shape != shape or v_cache.stride() != stride:
-        raise ValueError("k_cache and v_cache must be of the same shape and strides")
-    layers = shape[0] if len(shape) == 5 else 1
-    pages, hkv = shape[-4], shape[-2]
-    if not k_cache.is_contiguous() and layers > 0 and \
-            not (k_cache[0] if len(shape) == 5 else k_cache).is_contiguous():
-        raise ValueError("a layer's cache must be contiguous")
-    layer = stride[0] if layers > 1 else pages * hkv * (PAGE_SIZE * HEAD_DIM)
-    return k_cache.data_ptr(), v_cache.data_ptr(), layers, layer, pages, hkv
-
-
-def _table_args(block_tables, seq_lens, ref_counts, num_pages):
-    shape = block_tables.shape
-    if block_tables.dtype is not _I32 or len(shape) != 2 or not block_tables.is_contiguous():
-        raise ValueError("block_tables must be a contiguous int32 [num_rows, max_pages] tensor")
-    _vector("seq_lens", seq_lens, shape[0])
-    _vector("ref_counts", ref_counts, num_pages)
-    return shape
-
-
-def _cache_workspace(block_tables, shape, stream):
-    with _temporaries_on(stream, block_tables.device, stream is not None):
-        return torch.empty(max(mtp_cache_workspace_size(*shape), 256), dtype=torch.uint8,
-                           device=block_tables.device)
 
 
 def mtp_cache_workspace_size(num_rows: int, max_pages_per_seq: int) -> int:
@@ -617,23 +472,17 @@ def mtp_cache_resize(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
                      status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Set every row's length, in place: pages are given back and handed out.
 
-    k_cache / v_cache: one layer's caches or a stack's, [num_layers, num_pages, 16, H_kv, 256];
-    block_tables [rows, max_pages], seq_lens [rows], ref_counts [num_pages] int32 are updated;
-    new_lens [rows] int32 (0 frees a row).  A shared, partly filled last page is copied first.
-    With too few free pages nothing is handed out and ERR_FULL is set.
+    k_cache / v_cache: one layer's caches [num_pages, 16, H_kv, 256] or a stack's, behind
+    num_layers; block_tables [rows, max_pages], seq_lens [rows], ref_counts [num_pages] int32 are
+    updated; new_lens [rows] int32 (0 frees a row).  A shared, partly filled last page is copied
+    first.  With too few free pages nothing is handed out and ERR_FULL is set.
     """
-    handle = _call_stream(block_tables.get_device(), stream)
-    cache = _cache_args(k_cache, v_cache)
-    shape = _table_args(block_tables, seq_lens, ref_counts, cache[4])
-    rows, width = shape
-    _vector("new_lens", new_lens, rows)
-    if workspace is None:
-        workspace = _cache_workspace(block_tables, shape, stream)
-    rc = lib().mtp_cache_resize(
-        *cache, block_tables.data_ptr(), width, seq_lens.data_ptr(), rows, ref_counts.data_ptr(),
-        new_lens.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(status), handle)
-    if rc != OK:
-        raise MtpAttnError(rc)
+    call = (_BINDING or binding()).cache_resize
+    if stream is None:
+        return call(k_cache, v_cache, block_tables, seq_lens, ref_counts, new_lens, workspace,
+                    status, None)
+    return _on_stream(call, (k_cache, v_cache, block_tables, seq_lens, ref_counts, new_lens,
+                             workspace, status), stream, block_tables.device)
 
 
 def mtp_cache_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -642,36 +491,23 @@ def mtp_cache_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows dst[i] (empty) become copies of rows src[i]: full pages are shared, a partly filled
     last page is copied.  src, dst int32 vectors of the same length."""
-    handle = _call_stream(block_tables.get_device(), stream)
-    cache = _cache_args(k_cache, v_cache)
-    shape = _table_args(block_tables, seq_lens, ref_counts, cache[4])
-    rows, width = shape
-    pairs = src.numel()
-    _vector("src", src, pairs)
-    _vector("dst", dst, pairs)
-    if workspace is None:
-        workspace = _cache_workspace(block_tables, shape, stream)
-    rc = lib().mtp_cache_fork(
-        *cache, block_tables.data_ptr(), width, seq_lens.data_ptr(), rows, ref_counts.data_ptr(),
-        src.data_ptr(), dst.data_ptr(), pairs, workspace.data_ptr(), workspace.nbytes,
-        _ptr(status), handle)
-    if rc != OK:
-        raise MtpAttnError(rc)
+    call = (_BINDING or binding()).cache_fork
+    if stream is None:
+        return call(k_cache, v_cache, block_tables, seq_lens, ref_counts, src, dst, workspace,
+                    status, None)
+    return _on_stream(call, (k_cache, v_cache, block_tables, seq_lens, ref_counts, src, dst,
+                             workspace, status), stream, block_tables.device)
 
 
 def mtp_cache_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src_pages: torch.Tensor,
                          dst_pages: torch.Tensor, status: Optional[torch.Tensor] = None,
                          stream=None) -> None:
     """Page dst_pages[i] gets the contents of page src_pages[i], in all layers."""
-    handle = _call_stream(k_cache.get_device(), stream)
-    cache = _cache_args(k_cache, v_cache)
-    pairs = src_pages.numel()
-    _vector("src_pages", src_pages, pairs)
-    _vector("dst_pages", dst_pages, pairs)
-    rc = lib().mtp_cache_copy_pages(*cache, src_pages.data_ptr(), dst_pages.data_ptr(), pairs,
-                                    _ptr(status), handle)
-    if rc != OK:
-        raise MtpAttnError(rc)
+    call = (_BINDING or binding()).cache_copy_pages
+    if stream is None:
+        return call(k_cache, v_cache, src_pages, dst_pages, status, None)
+    return _on_stream(call, (k_cache, v_cache, src_pages, dst_pages, status), stream,
+                      k_cache.device)
 
 
 def mtp_cache_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -685,28 +521,9 @@ def mtp_cache_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables
     accept_index [B, max_path] and accept_len [B] as the verifications return them.  The pages
     that hold the trees must belong to their rows alone; none are given back here.
     """
-    handle = _call_stream(k_cache.get_device(), stream)
-    cache = _cache_args(k_cache, v_cache)
-    num_seqs = _sequences(cu_seqlens_q)
-    table, path = block_tables.shape, accept_index.shape
-    if block_tables.dtype is not _I32 or len(table) != 2 or table[0] != num_seqs or \
-            not block_tables.is_contiguous():
-        raise ValueError("block_tables must be a contiguous int32 [B, max_pages] tensor, "
-                         "cu_seqlens_q [B + 1]")
-    _vector("seq_lens", seq_lens, num_seqs)
-    _vector("accept_len", accept_len, num_seqs)
-    if accept_index.dtype is not _I32 or len(path) != 2 or path[0] != num_seqs or \
-            not accept_index.is_contiguous():
-        raise ValueError("accept_index must be a contiguous int32 [B, max_path] tensor")
-    if new_seq_lens is None:
-        with _temporaries_on(stream, seq_lens.device, stream is not None):
-            new_seq_lens = torch.empty_like(seq_lens)
-    else:
-        _vector("new_seq_lens", new_seq_lens, num_seqs)
-    rc = lib().mtp_cache_compact(
-        *cache, block_tables.data_ptr(), table[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
-        num_seqs, num_seqs * TREE_MAX_NODES, accept_index.data_ptr(), accept_len.data_ptr(),
-        path[1], new_seq_lens.data_ptr(), _ptr(status), handle)
-    if rc != OK:
-        raise MtpAttnError(rc)
-    return new_seq_lens
+    call = (_BINDING or binding()).cache_compact
+    if stream is None:
+        return call(k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q, accept_index,
+                    accept_len, new_seq_lens, status, None)
+    return _on_stream(call, (k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q, accept_index,
+                             accept_len, new_seq_lens, status), stream, k_cache.device)

@@ -1,22 +1,26 @@
 """Build libmtpattn.so in-tree with nvcc for sm_103a (no CMake, no torch extension).
 
 Every ``csrc/*.cu`` file compiles to an object in parallel, then one link makes
-``paged_fp8_speculative_gb300/libmtpattn.so``.  Run as ``python -m
+``paged_fp8_speculative_gb300/libmtpattn.so``; beside them g++ compiles ``csrc/binding.cpp``, the
+compiled part of the Python binding, linked to that library.  Run as ``python -m
 paged_fp8_speculative_gb300.build`` or through ``__graft_entry__.build()``.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmtpattn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -28,6 +32,30 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libmtpattn.so")
+
+
+def _torch_dir() -> str:
+    """PyTorch's folder, without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: the Python binding is compiled against it")
+    return list(spec.submodule_search_locations)[0]
+
+
+def binding_commands():
+    """g++ command lines: compile csrc/binding.cpp, link it."""
+    torch_dir = _torch_dir()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD, "binding.o")
+    includes = [os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", *[f"-I{d}" for d in includes], "-c",
+                os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    link = ["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L", PKG, "-lmtpattn",
+            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
 
 
 def build(verbose: bool = False, extra_flags=(), lib_path: str = LIB) -> str:
@@ -48,6 +76,13 @@ def build(verbose: bool = False, extra_flags=(), lib_path: str = LIB) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    product = lib_path == LIB
+    if product:
+        compile_binding, link_binding = binding_commands()
+        if verbose:
+            print(" ".join(compile_binding), flush=True)
+        procs.append(("binding.cpp", subprocess.Popen(compile_binding, stdout=subprocess.PIPE,
+                                                      stderr=subprocess.STDOUT)))
     failed = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -56,13 +91,16 @@ def build(verbose: bool = False, extra_flags=(), lib_path: str = LIB) -> str:
         if pr.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compiling failed for {failed}")
     tmp = lib_path + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, lib_path)
+    if product:
+        subprocess.check_call(link_binding)
+        os.replace(BINDING + ".tmp", BINDING)
     return lib_path
 
 
