@@ -33,6 +33,7 @@ extern "C" {
 #endif
 
 #define MTP_CACHE_MAX_ROWS 8192
+#define MTP_CACHE_MAX_PAGES (1 << 22)   /* of one layer: 8 layers of one head that long fill the GPU */
 
 /* Device-side error bits (next to MTPATTN_ERR_* of mtpattn.h). */
 #define MTP_CACHE_ERR_LEN 256    /* a length outside [0, 16 * max_pages_per_seq], or an accepted

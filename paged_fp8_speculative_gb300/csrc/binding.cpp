@@ -73,7 +73,7 @@ int32_t* ints_out(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr
 int32_t* status_of(PyObject* o) {
   if (!given(o)) return nullptr;
   const at::Tensor& t = tensor(o, "status");
-  REFUSE_IF(t.numel() < 1, "status must hold an int32 word");
+  REFUSE_IF(t.scalar_type() != at::kInt || t.numel() < 1, "status must be an int32 tensor of one word");
   return static_cast<int32_t*>(t.data_ptr());
 }
 

@@ -4,10 +4,20 @@
 //
 // resize and fork run a planning kernel and a copying kernel.  The plan is one thread-block
 // cluster, because every page handed out depends on all the counts below it: its CTAs first
-// give pages back (resize), meet, count their part of the pool's free pages, exchange the
-// counts through distributed shared memory, and then know each free page's rank; page of rank k
-// goes to the k-th place wanted, found by a search over the rows' running sums of wants.  The
-// pages to copy are left in the workspace, one (from, to) pair a row, for the copying kernel.
+// give pages back (resize), meet, mark their part of the pool's free pages in shared memory, tell
+// one another how many they found, meet again, and then know each free page's rank; the page of
+// rank k goes to the k-th place wanted, found by a search over the rows' running sums of wants.
+// The pages to copy are left in the workspace, one (from, to) pair a row, for the copying kernel,
+// which is launched beside the plan and starts when the plan has ended.
+//
+// What bounds a plan is its chain of dependent memory accesses (lengths, table entry, count,
+// rank, place: about 0.5 us each) and the meetings, not the bytes: so what a row asks for is
+// worked out once by every CTA and stays in shared memory, and loads that do not depend on a
+// meeting are issued before it.  Three calls (rows freed and trimmed, forked, grown) take 16.5 us
+// in a CUDA graph for 4 rows and a pool of 512 pages, 29 us for 256 rows, 128 forks and 16384
+// pages; with the items read again at each step, four meetings and the copying kernel launched
+// after the plan it was 33 and 48 us.  One CTA instead of the cluster's 8 is no faster for the
+// small table (16.5 us) and takes 72 us for the large one; 1024 threads a CTA 18.0 and 29.9 us.
 #include "common.cuh"
 #include "host_checks.cuh"
 
@@ -23,9 +33,9 @@ namespace cg = cooperative_groups;
 namespace mtpattn {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kMaxPlanCtas = 8;
+constexpr int kPlanCtas = 8;
 constexpr int kCopyThreads = 256;
 
 struct PlanParams {
@@ -40,142 +50,132 @@ struct PlanParams {
   const int32_t* dst;
   int32_t items;             // rows (resize) or pairs (fork)
   int2* copies;              // workspace: [items] pages (from, to), from < 0: none
-  int32_t* claim;            // workspace: [rows] (fork) the first pair that names a dst
   int32_t* status;
 };
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
 
-// Inclusive running sums of want[0 .. n) in place, by the whole CTA; returns their total. Sums
-// past 2^31 - 1 stay there: such a total is more than any pool has, and no sum is used then.
-__device__ int64_t scan_wants(int* want, int n, int64_t* s_warp) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  int64_t carry = 0;
-  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
-    int64_t v = i0 + t < n ? want[i0 + t] : 0;
+// A plan's shared memory. An item is a row (resize) or a pair of rows (fork).
+struct PlanSmem {
+  uint32_t* free;            // [mask_words] a bit for each page of this CTA's part of the pool
+  int* sum;                  // [items] what the items want, then the running sums
+  int* tail;                 // [items] the page to be copied, or -1
+  int* slot;                 // [items] table position of the first page handed out; -1: not live
+  int* claim;                // [rows], fork: the first pair that names a dst
+  uint8_t* bad;              // [items], fork: the source row has a bad entry
+};
+__host__ __device__ inline int mask_words(int num_pages) {
+  const int per = (num_pages + kPlanCtas - 1) / kPlanCtas;
+  return ((per + kPlanWarps - 1) / kPlanWarps + 31) / 32 * kPlanWarps;
+}
+inline size_t plan_smem(bool fork, int num_pages, int items, int rows) {
+  return 4 * (static_cast<size_t>(mask_words(num_pages)) + 3 * static_cast<size_t>(items)) +
+         (fork ? 4 * static_cast<size_t>(rows) + (items + 3) / 4 * 4 : 0);
+}
+
+// Sums of wants stop at this: more than any pool has, and two of them fit in 32 bits.
+constexpr uint32_t kManyPages = 1u << 30;
+static_assert(MTP_CACHE_MAX_PAGES < (1 << 30));
+__device__ __forceinline__ uint32_t add_wants(uint32_t a, uint32_t b) { return min(a + b, kManyPages); }
+__device__ __forceinline__ uint32_t warp_sums(uint32_t v, int lane) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += x;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = add_wants(v, x);
+  }
+  return v;
+}
+
+// Inclusive running sums of want[0 .. n) in place, by the whole CTA; returns their total.
+__device__ uint32_t scan_wants(int* want, int n, uint32_t* s_warp) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  uint32_t carry = 0;
+  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+    const uint32_t v = warp_sums(i0 + t < n ? min(static_cast<uint32_t>(want[i0 + t]), kManyPages) : 0, lane);
     if (lane == 31) s_warp[warp] = v;
     __syncthreads();
-    int64_t below = carry, all = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-      if (w < warp) below += s_warp[w];
-      all += s_warp[w];
-    }
-    if (i0 + t < n) want[i0 + t] = static_cast<int>(min(v + below, static_cast<int64_t>(INT32_MAX)));
-    carry += all;
+    const uint32_t w = warp_sums(lane < kPlanWarps ? s_warp[lane] : 0u, lane);
+    const uint32_t below = __shfl_sync(0xffffffffu, w, max(warp, 1) - 1);
+    const uint32_t before = warp ? add_wants(carry, below) : carry;
+    if (i0 + t < n) want[i0 + t] = static_cast<int>(add_wants(v, before));
+    carry = add_wants(carry, __shfl_sync(0xffffffffu, w, 31));
     __syncthreads();
   }
   return carry;
 }
 
-// What item i asks for.  resize: the row's pages beyond those it keeps, and a page for its last
-// one if that is shared; fork: a page for the last, partly filled one.
-struct Item {
-  int row, from;             // the row that gets pages; fork: the row they are copied from
-  int kept, len;             // tokens kept, tokens afterwards
-  int tail;                  // the page to be copied, or -1
-  int slot;                  // the table position of the first page handed out
-  int want;
-  bool live;
-};
-
-template <bool Fork>
-__device__ __forceinline__ Item item_of(const PlanParams& p, int i) {
-  Item x;
-  x.live = true;
-  x.tail = -1;
-  x.want = 0;
-  if (Fork) {
-    x.from = p.src[i];
-    x.row = p.dst[i];
-    x.live = x.from >= 0 && x.from < p.rows && x.row >= 0 && x.row < p.rows && x.from != x.row &&
-             p.seq_lens[x.row] == 0 && p.claim[x.row] == i;
-    x.kept = x.len = x.live ? p.seq_lens[x.from] : 0;
-    x.slot = x.kept / kPage;
-    if (x.live && (x.len < 0 || x.len > static_cast<int64_t>(p.max_pages) * kPage)) {
-      x.live = false;
-      x.len = x.kept = x.slot = 0;
-    }
-    if (x.live && x.kept % kPage != 0) {
-      x.tail = p.bt[static_cast<int64_t>(x.from) * p.max_pages + x.slot];
-      x.want = 1;
-    }
-  } else {
-    x.row = x.from = i;
-    const int old = p.seq_lens[i];
-    x.len = p.new_lens[i];
-    const int64_t top = static_cast<int64_t>(p.max_pages) * kPage;
-    x.live = old >= 0 && old <= top && x.len >= 0 && x.len <= top;
-    if (!x.live) x.len = old;
-    x.kept = min(old, x.len);
-    x.slot = pages_of(x.kept);
-    if (x.live) {
-      x.want = pages_of(x.len) - x.slot;
-      if (x.kept % kPage != 0) {
-        const int page = p.bt[static_cast<int64_t>(i) * p.max_pages + x.slot - 1];
-        if (page >= 0 && page < p.num_pages && p.ref[page] > 1) {
-          x.tail = page;
-          --x.slot;
-          ++x.want;
-        }
-      }
-    }
+// The free pages of this CTA's part of the pool, marked in shared memory; returns how many this
+// warp found.  A warp has a contiguous piece of `words` words.
+__device__ __forceinline__ int mark_free(const PlanParams& p, uint32_t* mine, int words, int lo, int end, int lane) {
+  int count = 0;
+#pragma unroll 4
+  for (int w = 0; w < words; ++w) {
+    const int page = lo + 32 * w + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, page < end && __ldcg(p.ref + page) == 0);
+    if (lane == 0) mine[w] = m;
+    count += __popc(m);
   }
-  return x;
+  return count;
 }
 
 template <bool Fork>
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
 cache_plan_kernel(const PlanParams p) {
-  extern __shared__ int s_want[];                  // running sums of the items' wants
-  __shared__ int64_t s_warp[kPlanWarps];
+  extern __shared__ uint32_t s_plan[];
+  __shared__ uint32_t s_warp[kPlanWarps];
   __shared__ int s_base[kPlanWarps];
-  __shared__ int s_free[kMaxPlanCtas];
+  __shared__ int s_free[kPlanCtas];
   cg::cluster_group cluster = cg::this_cluster();
-  const int parts = cluster.num_blocks(), part = cluster.block_rank();
+  constexpr int parts = kPlanCtas;
+  const int part = cluster.block_rank();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int gwarp = part * kPlanWarps + warp, gwarps = parts * kPlanWarps;
   const int gt = part * kPlanThreads + t, gthreads = parts * kPlanThreads;
+  const int words = mask_words(p.num_pages) / kPlanWarps;    // a warp's
+  PlanSmem s;
+  s.free = s_plan;
+  s.sum = reinterpret_cast<int*>(s.free + words * kPlanWarps);
+  s.tail = s.sum + p.items;
+  s.slot = s.tail + p.items;
+  s.claim = s.slot + p.items;
+  s.bad = reinterpret_cast<uint8_t*>(s.claim + p.rows);
+  const int64_t top = static_cast<int64_t>(p.max_pages) * kPage;
+  const int per = (p.num_pages + parts - 1) / parts;
+  const int end = min(static_cast<int64_t>(p.num_pages), static_cast<int64_t>(part + 1) * per);
+  const int lo = static_cast<int>(min(static_cast<int64_t>(end),
+                                      static_cast<int64_t>(part) * per + static_cast<int64_t>(warp) * words * 32));
+  uint32_t* mine = s.free + warp * words;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  // The cluster meets twice.  Before the first meeting: resize gives the surplus pages back, a warp
+  // a row; fork tells all its CTAs which pairs have a source row with a bad entry.
+  int found;
   if (Fork) {
-    // the first pair of a dst stands
-    for (int i = gt; i < p.rows; i += gthreads) p.claim[i] = 0x7fffffff;
-    __threadfence();
-    cluster.sync();
-    for (int i = gt; i < p.items; i += gthreads) {
+    cluster.barrier_arrive();                      // all have started: their memory can be written
+    for (int i = t; i < p.rows; i += kPlanThreads) s.claim[i] = INT32_MAX;
+    __syncthreads();
+    for (int i = t; i < p.items; i += kPlanThreads) {
       const int d = p.dst[i];
-      if (d >= 0 && d < p.rows) atomicMin(&p.claim[d], i);
+      if (d >= 0 && d < p.rows) atomicMin(&s.claim[d], i);
     }
-    __threadfence();
-    cluster.sync();
-    // a source row with a bad entry: nobody's (a claim below 0 is no pair's)
+    found = mark_free(p, mine, words, lo, end, lane);
+    cluster.barrier_wait();
     for (int i = gwarp; i < p.items; i += gwarps) {
-      const int s = p.src[i], d = p.dst[i];
+      const int src = p.src[i];
       bool bad = false;
-      if (s >= 0 && s < p.rows && d >= 0 && d < p.rows) {
-        const int len = p.seq_lens[s];
-        const int n = len > 0 && len <= static_cast<int64_t>(p.max_pages) * kPage ? pages_of(len) : 0;
-        for (int j = lane; j < n; j += 32) {
-          const int page = p.bt[static_cast<int64_t>(s) * p.max_pages + j];
-          bad |= page < 0 || page >= p.num_pages;
-        }
+      if (src >= 0 && src < p.rows) {
+        const int len = p.seq_lens[src];
+        const int n = len > 0 && len <= top ? pages_of(len) : 0;
+        const int32_t* row = p.bt + static_cast<int64_t>(src) * p.max_pages;
+#pragma unroll 4
+        for (int j = lane; j < n; j += 32) bad |= static_cast<uint32_t>(row[j]) >= static_cast<uint32_t>(p.num_pages);
         bad = __any_sync(0xffffffffu, bad);
-        if (bad && lane == 0 && s != d && p.seq_lens[d] == 0 &&
-            atomicCAS(&p.claim[d], i, -1) == i)
-          set_status(p.status, MTPATTN_ERR_PAGE);
       }
+      if (lane < parts) *cluster.map_shared_rank(&s.bad[i], lane) = bad;
     }
-    __threadfence();
-    cluster.sync();
   } else {
-    // give the surplus pages back, a warp a row
     for (int i = gwarp; i < p.rows; i += gwarps) {
       const int old = p.seq_lens[i], len = p.new_lens[i];
-      const int64_t top = static_cast<int64_t>(p.max_pages) * kPage;
       if (old < 0 || old > top || len < 0 || len > top) {
         if (lane == 0) set_status(p.status, MTP_CACHE_ERR_LEN);
         continue;
@@ -193,118 +193,124 @@ cache_plan_kernel(const PlanParams p) {
       }
     }
     __threadfence();
-    cluster.sync();
+    cluster.barrier_arrive();
+    // What the rows ask for: the pages beyond those they keep, and one for the last kept page where
+    // it is partly filled and shared (looked at after the meeting).
+    for (int i = t; i < p.items; i += kPlanThreads) {
+      const int old = p.seq_lens[i], len = p.new_lens[i];
+      const bool live = old >= 0 && old <= top && len >= 0 && len <= top;
+      const int kept = min(old, len), have = live ? pages_of(kept) : -1;
+      s.sum[i] = live ? pages_of(len) - have : 0;
+      s.slot[i] = have;
+      s.tail[i] = live && kept % kPage != 0 ? p.bt[static_cast<int64_t>(i) * p.max_pages + have - 1] : -1;
+    }
+    cluster.barrier_wait();
+    for (int i = t; i < p.items; i += kPlanThreads) {
+      const int page = s.tail[i];
+      if (page >= 0 && page < p.num_pages && __ldcg(p.ref + page) > 1) {
+        ++s.sum[i];
+        --s.slot[i];
+      } else {
+        s.tail[i] = -1;
+      }
+    }
+    found = mark_free(p, mine, words, lo, end, lane);
   }
-
-  // the items' wants, every CTA for itself
-  for (int i = t; i < p.items; i += kPlanThreads) s_want[i] = item_of<Fork>(p, i).want;
+  if (lane == 0) s_base[warp] = found;
   __syncthreads();
-  const int64_t total = scan_wants(s_want, p.items, s_warp);
-
-  // this CTA's part of the pool, a contiguous piece a warp
-  const int per = (p.num_pages + parts - 1) / parts;
-  const int w_per = ((per + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
-  const int64_t base = static_cast<int64_t>(part) * per;
-  const int end = static_cast<int>(min(static_cast<int64_t>(p.num_pages), base + per));
-  const int64_t w_lo64 = base + static_cast<int64_t>(warp) * w_per;
-  const int w_lo = static_cast<int>(min(static_cast<int64_t>(end), w_lo64));
-  const int w_hi = static_cast<int>(min(static_cast<int64_t>(end), w_lo64 + w_per));
-  int count = 0;
-  #pragma unroll 8
-  for (int i = w_lo + lane; i < w_hi; i += 32) count += p.ref[i] == 0;
+  if (warp == 0) {
+    int all = lane < kPlanWarps ? s_base[lane] : 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
-  if (lane == 0) s_base[warp] = count;
-  __syncthreads();
-  if (t < parts) {
-    int all = 0;
-    for (int w = 0; w < kPlanWarps; ++w) all += s_base[w];
-    *cluster.map_shared_rank(&s_free[part], t) = all;
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane < parts) *cluster.map_shared_rank(&s_free[part], lane) = all;
   }
-  cluster.sync();                                  // also: every item has been read
+  cluster.sync();                                  // resize: all lengths and counts have been read
+
+  int err = 0, my_row = -1, my_len = 0;
+  if (Fork) {
+    for (int i = t; i < p.items; i += kPlanThreads) {
+      const int src = p.src[i], row = p.dst[i];      // item gt is this thread's own one
+      const bool rows = src >= 0 && src < p.rows && row >= 0 && row < p.rows && src != row &&
+                        s.claim[row] == i && p.seq_lens[row] == 0;
+      const int len = rows ? p.seq_lens[src] : 0;
+      const bool fits_table = len >= 0 && len <= top;
+      if (!rows) err |= MTP_CACHE_ERR_ROW;
+      else if (!fits_table) err |= MTP_CACHE_ERR_LEN;
+      else if (s.bad[i]) err |= MTPATTN_ERR_PAGE;
+      const bool live = rows && fits_table && !s.bad[i];
+      const bool part_full = live && len % kPage != 0;
+      s.slot[i] = live ? len / kPage : -1;
+      s.tail[i] = part_full ? p.bt[static_cast<int64_t>(src) * p.max_pages + len / kPage] : -1;
+      s.sum[i] = part_full;
+      if (i == gt && live) {
+        my_row = row;
+        my_len = len;
+      }
+    }
+    __syncthreads();
+    cluster.barrier_arrive();                      // this CTA has read the lengths
+  }
+  const uint32_t total = scan_wants(s.sum, p.items, s_warp);
   int rank = 0, all_free = 0;                      // free pages before this warp's, of the pool
   for (int i = 0; i < parts; ++i) {
     if (i < part) rank += s_free[i];
     all_free += s_free[i];
   }
-  for (int w = 0; w < warp; ++w) rank += s_base[w];
-  const bool fits = total <= all_free;
-  if (!fits && part == 0 && t == 0) set_status(p.status, MTP_CACHE_ERR_FULL);
+  rank += __reduce_add_sync(0xffffffffu, lane < warp ? s_base[lane] : 0);
+  const bool fits = total <= static_cast<uint32_t>(all_free);
+  if (part == 0) {
+    if (!fits) err |= MTP_CACHE_ERR_FULL;
+    err = __reduce_or_sync(0xffffffffu, err);
+    if (err && lane == 0) set_status(p.status, err);
+  }
 
-  // What an item gets is written by the warps that hold the pages.  Nothing that item_of reads
-  // changes meanwhile: copied pages take their places, and lengths change, afterwards.
-  for (int i = gt; i < p.items; i += gthreads) p.copies[i] = make_int2(-1, -1);
-  __threadfence();
-  cluster.sync();
-  if (fits && rank < total) {
-    for (int i0 = w_lo; i0 < w_hi && rank < total; i0 += 32) {
-      const int page = i0 + lane;
-      const bool is_free = page < w_hi && p.ref[page] == 0;
-      const uint32_t m = __ballot_sync(0xffffffffu, is_free);
-      const int k = rank + __popc(m & ((1u << lane) - 1u));
-      if (is_free && k < total) {
-        int lo = 0, hi = p.items - 1;              // the first item whose running sum passes k
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2;
-          if (s_want[mid] > k) hi = mid; else lo = mid + 1;
+  if (fits)
+    for (int w = 0; w < words && static_cast<uint32_t>(rank) < total; ++w) {
+      const uint32_t m = mine[w];
+      const int k = rank + __popc(m & ((1u << lane) - 1u)), page = lo + 32 * w + lane;
+      if ((m >> lane & 1u) && static_cast<uint32_t>(k) < total) {
+        int a = 0, z = p.items - 1;                // the first item whose running sum passes k
+        while (a < z) {
+          const int mid = (a + z) / 2;
+          if (s.sum[mid] > k) z = mid; else a = mid + 1;
         }
-        const Item x = item_of<Fork>(p, lo);
-        const int nth = k - (lo ? s_want[lo - 1] : 0);
+        const int nth = k - (a ? s.sum[a - 1] : 0), tail = s.tail[a];
         p.ref[page] = 1;
-        if (x.tail >= 0 && nth == 0) p.copies[lo] = make_int2(x.tail, page);
-        else p.bt[static_cast<int64_t>(x.row) * p.max_pages + x.slot + nth] = page;
+        p.bt[static_cast<int64_t>(Fork ? p.dst[a] : a) * p.max_pages + s.slot[a] + nth] = page;
+        if (tail >= 0 && nth == 0) {
+          p.copies[a] = make_int2(tail, page);
+          if (!Fork) atomicSub(&p.ref[tail], 1);
+        }
       }
       rank += __popc(m);
     }
-  }
-  __threadfence();
-  cluster.sync();
-  // The copied pages take their places; shared pages are counted; lengths change last.
+  for (int i = gt; i < p.items; i += gthreads)
+    if (!fits || s.tail[i] < 0) p.copies[i] = make_int2(-1, -1);
+
+  // Shared pages are counted; lengths change last.
   if (Fork) {
     if (fits)
       for (int i = gwarp; i < p.items; i += gwarps) {
-        const Item x = item_of<Fork>(p, i);
-        if (!x.live) {
-          const int s = p.src[i], d = p.dst[i];
-          const bool known = s >= 0 && s < p.rows && d >= 0 && d < p.rows;
-          const bool page_err = known && p.claim[d] == -1;
-          const bool len_err = known && (p.seq_lens[s] < 0 || p.seq_lens[s] > static_cast<int64_t>(p.max_pages) * kPage);
-          if (lane == 0 && !page_err) set_status(p.status, len_err ? MTP_CACHE_ERR_LEN : MTP_CACHE_ERR_ROW);
-          continue;
-        }
-        const int32_t* from = p.bt + static_cast<int64_t>(x.from) * p.max_pages;
-        int32_t* to = p.bt + static_cast<int64_t>(x.row) * p.max_pages;
-        for (int j = lane; j < x.kept / kPage; j += 32) {
+        if (s.slot[i] < 0) continue;
+        const int32_t* from = p.bt + static_cast<int64_t>(p.src[i]) * p.max_pages;
+        int32_t* to = p.bt + static_cast<int64_t>(p.dst[i]) * p.max_pages;
+#pragma unroll 4
+        for (int j = lane; j < s.slot[i]; j += 32) {
           const int page = from[j];
           to[j] = page;
           atomicAdd(&p.ref[page], 1);
         }
-        if (x.tail >= 0 && lane == 0) to[x.slot] = p.copies[i].y;
       }
-    // A thread has one pair at most; all lengths are read before the first is written (a
-    // source row may be the dst of another pair).
-    int row = -1, len = 0;
-    if (fits && gt < p.items) {
-      const Item x = item_of<Fork>(p, gt);
-      if (x.live) {
-        row = x.row;
-        len = x.len;
-      }
-    }
-    cluster.sync();
-    if (row >= 0) p.seq_lens[row] = len;
+    // A source row may be the dst of another pair: its length has been read by every CTA before
+    // one is written. A thread has one pair at most.
+    cluster.barrier_wait();
+    if (fits && my_row >= 0) p.seq_lens[my_row] = my_len;
   } else {
-    for (int i = gt; i < p.rows; i += gthreads) {
-      const int2 c = p.copies[i];
-      const int old = p.seq_lens[i], len = p.new_lens[i];
-      const int64_t top = static_cast<int64_t>(p.max_pages) * kPage;
-      if (old < 0 || old > top || len < 0 || len > top) continue;
-      if (c.x >= 0) {
-        atomicSub(&p.ref[c.x], 1);
-        p.bt[static_cast<int64_t>(i) * p.max_pages + (min(old, len) - 1) / kPage] = c.y;
+    for (int i = gt; i < p.rows; i += gthreads)
+      if (s.slot[i] >= 0) {
+        const int len = p.new_lens[i];
+        p.seq_lens[i] = fits ? len : min(p.seq_lens[i], len);
       }
-      p.seq_lens[i] = fits ? len : min(old, len);
-    }
   }
 }
 
@@ -327,6 +333,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 cache_copy_kernel(const CopyParams p) {
   const int i = blockIdx.x;
   int from, to;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan, where there is one, has ended
   if (p.copies) {
     const int2 c = p.copies[i];
     if (c.x < 0) return;
@@ -431,7 +438,7 @@ cache_compact_kernel(const CompactParams p) {
 int check_caches(const void* k, const void* v, int32_t layers, int64_t layer_stride,
                  int64_t num_pages, int32_t hkv) {
   if (!k || !v || layers <= 0 || num_pages <= 0 || hkv <= 0) return MTPATTN_E_ARG;
-  if (num_pages > INT32_MAX || hkv > 65535) return MTPATTN_E_UNSUPPORTED;
+  if (num_pages > MTP_CACHE_MAX_PAGES || hkv > 65535) return MTPATTN_E_UNSUPPORTED;
   if (!ptr_aligned(k, 16) || !ptr_aligned(v, 16)) return MTPATTN_E_ARG;
   const int64_t bytes = num_pages * kPage * hkv * kHeadDim;
   if (layers > 1 && (layer_stride < bytes || layer_stride % 16)) return MTPATTN_E_ARG;
@@ -440,33 +447,44 @@ int check_caches(const void* k, const void* v, int32_t layers, int64_t layer_str
 
 template <bool Fork>
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
-  // one CTA while its 32 warps hold the whole pool in a few loads each, else the largest
-  // portable cluster
-  const int parts = p.num_pages <= 4096 && p.rows <= 64 ? 1 : kMaxPlanCtas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(parts);
+  cfg.gridDim = dim3(kPlanCtas);
   cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.items) * sizeof(int);
+  cfg.dynamicSmemBytes = plan_smem(Fork, p.num_pages, p.items, p.rows);
   cfg.stream = stream;
+  if (cfg.dynamicSmemBytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel<Fork>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(cfg.dynamicSmemBytes));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.x = kPlanCtas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cache_plan_kernel<Fork>, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return e;
-  }
-  return cudaGetLastError();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_plan_kernel<Fork>, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_copy(const CopyParams& p, cudaStream_t stream) {
-  const dim3 grid(p.items, std::min(2 * p.layers, 65535));
-  cache_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.items, std::min(2 * p.layers, 65535));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.copies ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_copy_kernel, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 int plan_and_copy(bool fork, PlanParams& p, CopyParams& c, void* workspace, size_t bytes,
@@ -480,7 +498,6 @@ int plan_and_copy(bool fork, PlanParams& p, CopyParams& c, void* workspace, size
             : !ptr_on_device(p.new_lens, device)))
     return MTPATTN_E_DEVICE;
   p.copies = static_cast<int2*>(workspace);
-  p.claim = reinterpret_cast<int32_t*>(p.copies + p.rows);
   c.copies = p.copies;
   c.items = p.items;
   if ((fork ? launch_plan<true>(p, stream) : launch_plan<false>(p, stream)) != cudaSuccess)
@@ -503,7 +520,7 @@ using namespace mtpattn;
 
 extern "C" size_t mtp_cache_workspace_size(int32_t num_rows, int32_t max_pages_per_seq) {
   if (num_rows < 0 || num_rows > MTP_CACHE_MAX_ROWS || max_pages_per_seq < 0) return 0;
-  const size_t bytes = static_cast<size_t>(num_rows) * (sizeof(int2) + sizeof(int32_t));
+  const size_t bytes = static_cast<size_t>(num_rows) * sizeof(int2);
   return (bytes + 255) / 256 * 256 + 256;
 }
 
