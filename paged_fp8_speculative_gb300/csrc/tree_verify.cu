@@ -289,18 +289,50 @@ struct Row {
   const void* q;             // null: w = p
   uint64_t S;                // in units of 2^-57
   float s_hi, s_lo;          // S as the sum of two floats
-  __device__ __forceinline__ void set(uint64_t s) {
+  __device__ __forceinline__ void set(uint64_t s) {                      // (its 24 top bits, the rest)
     S = s;
-    const double x = static_cast<double>(s) * 6.938893903907228e-18;     // 2^-57
-    s_hi = static_cast<float>(x);
-    s_lo = static_cast<float>(x - static_cast<double>(s_hi));
+    const int below = max(0, 40 - __clzll(static_cast<long long>(s)));
+    const uint64_t top = s >> below;
+    constexpr float kUnitS = 6.938893903907228e-18f;                     // 2^-57
+    s_hi = static_cast<float>(static_cast<uint32_t>(top)) * kUnitS * __uint_as_float((127u + below) << 23);
+    s_lo = __ull2float_rn(s - (top << below)) * kUnitS;
   }
   // 0: w = p; 1: S = 1, what the first refusal leaves; 2: any S
   __device__ __forceinline__ int mode() const { return !q ? 0 : S == (1ull << 57) ? 1 : 2; }
 };
 
 constexpr uint32_t kDigitA = 0x3F800000u, kDigitB = 0x4B400000u;          // what w = 0 gives
-constexpr double kUnit = 2.8421709430404007e-14;                          // 2^-45
+
+// A node's number times the drafter's probability of its token, exactly: m 2^-e. The walk's comparisons
+// are made in integers, by every thread; FP64 instructions would cost a CTA 256 clocks each, 16 warps
+// at two lanes a clock, and with some 20 of them a refusal took 4.6 us where it now takes @@ us (one
+// sequence, 32000 tokens).
+struct Product {
+  uint64_t m;                // 48 bits
+  int e;
+};
+__device__ __forceinline__ int scale_of(float x, uint32_t& m) {          // x >= 0 is m 2^-scale
+  const uint32_t b = __float_as_uint(x), ex = b >> 23;
+  m = (b & 0x7fffffu) | (ex ? 0x800000u : 0u);
+  return 150 - static_cast<int>(max(ex, 1u));
+}
+__device__ __forceinline__ Product product_of(float u, float q) {
+  uint32_t a, b;
+  const int e = scale_of(u, a) + scale_of(q, b);
+  return {static_cast<uint64_t>(a) * b, e};
+}
+// x < p, and x z < w for z, w in units of 2^-45
+__device__ __forceinline__ bool below(const Product& x, float p) {
+  uint32_t m;
+  const int d = x.e - scale_of(p, m);
+  if (d >= 0) return (d < 64 ? x.m >> d : 0) < m;
+  return x.m == 0 ? m > 0 : x.m < (1u << 24) && d > -24 && x.m << -d < m;
+}
+__device__ __forceinline__ bool below(const Product& x, int64_t z, int64_t w) {
+  const uint64_t lo = x.m * static_cast<uint64_t>(z), hi = __umul64hi(x.m, static_cast<uint64_t>(z));
+  const uint64_t v = x.e >= 128 ? 0 : x.e >= 64 ? hi >> (x.e - 64) : lo >> x.e | hi << (64 - x.e);   // x.e >= 47
+  return static_cast<int64_t>(v) < w;
+}
 
 struct F2 {
   float x, y;
@@ -361,12 +393,25 @@ __device__ __noinline__ int64_t fixed_left(const Row& r, float p, float q) {
   return fixed_of(a, b, 2);
 }
 
+// Sums over the warp's lanes, by redux: of 48 bits and a sign; of digits of up to 16 elements a lane.
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0xffffffu);
+  return (static_cast<int64_t>(__reduce_add_sync(0xffffffffu, static_cast<int32_t>(v >> 24))) << 24) + lo;
+}
+__device__ __forceinline__ int64_t warp_fixed(uint32_t a, uint32_t b, int n) {
+  a -= static_cast<uint32_t>(n) * kDigitA;          // up to 2^27, |b| up to 3 2^24
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, a & 0xffffu), hi = __reduce_add_sync(0xffffffffu, a >> 16);
+  const int32_t low = __reduce_add_sync(0xffffffffu, static_cast<int32_t>(b - static_cast<uint32_t>(n) * kDigitB));
+  return (static_cast<int64_t>(hi) << 38) + (static_cast<int64_t>(lo) << 22) + low;
+}
+static_assert(kChunk / 32 <= 16);
+
 // Sums of the CTA's chunks [c_lo, c_hi) of kChunk places into s_sum (index c - c_lo), a warp a chunk,
-// its lanes taking blocks in turn.  Chunks are of the target's row in its own alignment; a chunk
+// its lanes taking blocks in turn; returns the sum of the warp's chunks.  Chunks are of the target's row in its own alignment; a chunk
 // with a block that is not whole, or beside a drafter's row of another alignment, is read an
 // element at a time.
 template <class T, int kMode>
-__device__ __noinline__ void chunk_sums(const Row& r, int vocab, int c_lo, int c_hi, int64_t* s_sum) {
+__device__ __noinline__ int64_t chunk_sums(const Row& r, int vocab, int c_lo, int c_hi, int64_t* s_sum) {
   constexpr int kVec = RowOf<T>::kVec, kBlocks = kChunk / kVec / 32;   // blocks a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* P = static_cast<const T*>(r.p);
@@ -374,6 +419,7 @@ __device__ __noinline__ void chunk_sums(const Row& r, int vocab, int c_lo, int c
   const RowOf<T> rp(P, vocab);
   const RowOf<T> rq(kMode ? Q : P, vocab);
   const bool alike = rp.skew == rq.skew;
+  int64_t all = 0;
 #pragma unroll 1
   for (int c = c_lo + warp; c < c_hi; c += kVerifyWarps) {
     uint32_t a = 0, b = 0;
@@ -407,11 +453,11 @@ __device__ __noinline__ void chunk_sums(const Row& r, int vocab, int c_lo, int c
         for (int u = 0; u < 8; u += 2) add_left<kMode>(r, {pv[u], pv[u + 1]}, {qv[u], qv[u + 1]}, a, b);
       }
     }
-    int64_t sum = fixed_of(a, b, kChunk / 32);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int64_t sum = warp_fixed(a, b, kChunk / 32);
     if (lane == 0) s_sum[c - c_lo] = sum;
+    all += sum;
   }
+  return all;
 }
 
 template <class T>
@@ -420,10 +466,11 @@ verify_sample_kernel(const VerifyParams p) {
   extern __shared__ int64_t s_sum[];               // the CTA's chunk sums
   __shared__ Walk w;
   __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];   // p, q of each node's token, its number
-  __shared__ int64_t s_part[2][kMaxCluster];       // by sum parity: the CTAs' sums
+  __shared__ Product s_x[kNodes];                  // u q of each node's token
+  __shared__ int64_t s_part[2][kMaxCluster][kVerifyWarps];   // by sum parity: the warps' sums
   __shared__ int64_t s_warp[kVerifyWarps];
-  constexpr int kSteps = kChunk / 32;
-  __shared__ int64_t s_val[kSteps][33];            // the values of the chunk drawn from
+  constexpr int kSteps = kChunk / 32;              // 32 values a step, a warp a step
+  static_assert(kSteps == kVerifyWarps);
   __shared__ int s_next;
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), part = cluster.block_rank();
@@ -443,7 +490,9 @@ verify_sample_kernel(const VerifyParams p) {
       s_p[t] = pv;
       s_q[t] = qv;
       // into [0, 1 - 2^-24]; NaN as 0
-      s_u[t] = fminf(fmaxf(p.u[w.q0 + t], 0.f), 0.999999940395355224609375f);
+      const float u = fminf(fmaxf(p.u[w.q0 + t], 0.f), 0.999999940395355224609375f);
+      s_u[t] = u;
+      s_x[t] = product_of(u, qv);
     }
     if (t == 0) s_next = -1;
   }
@@ -460,160 +509,147 @@ verify_sample_kernel(const VerifyParams p) {
     c_lo = min(chunks, part * per);
     c_hi = min(chunks, c_lo + per);
     const int mode = r.mode();
-    if (mode == 0) chunk_sums<T, 0>(r, p.vocab, c_lo, c_hi, s_sum);
-    else if (mode == 1) chunk_sums<T, 1>(r, p.vocab, c_lo, c_hi, s_sum);
-    else chunk_sums<T, 2>(r, p.vocab, c_lo, c_hi, s_sum);
-    __syncthreads();
-    if (t == 0 && gone) {
-      for (uint64_t m = gone; m; m &= m - 1) {
-        const int i = __ffsll(static_cast<long long>(m)) - 1;
-        const int c = (w.tok[i] + rp.skew) / kChunk;
-        if (c >= c_lo && c < c_hi) s_sum[c - c_lo] -= fixed_left(r, s_p[i], 0.f);
+    int64_t mine = mode == 0   ? chunk_sums<T, 0>(r, p.vocab, c_lo, c_hi, s_sum)
+                   : mode == 1 ? chunk_sums<T, 1>(r, p.vocab, c_lo, c_hi, s_sum)
+                               : chunk_sums<T, 2>(r, p.vocab, c_lo, c_hi, s_sum);
+    if (gone) {
+      __syncthreads();
+      if (warp == 0) {
+        int64_t out = 0;
+        for (uint64_t m = gone; m; m &= m - 1) {
+          const int i = __ffsll(static_cast<long long>(m)) - 1;
+          const int c = (w.tok[i] + rp.skew) / kChunk;
+          if (c >= c_lo && c < c_hi) {
+            const int64_t x = fixed_left(r, s_p[i], 0.f);
+            if (lane == 0) s_sum[c - c_lo] -= x;
+            out += x;
+          }
+        }
+        mine -= out;
       }
     }
-    __syncthreads();
-    int64_t mine = 0;
-    for (int c = t; c < c_hi - c_lo; c += kVerifyThreads) mine += s_sum[c];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_warp[warp] = mine;
-    __syncthreads();
-    if (t < parts) {
-      int64_t k = 0;
-      for (int i = 0; i < kVerifyWarps; ++i) k += s_warp[i];
-      *cluster.map_shared_rank(&s_part[sums & 1][part], t) = k;
-    }
+    if (lane < parts) cluster.map_shared_rank(&s_part[sums & 1][part][warp], lane)[0] = mine;
     cluster.sync();
-    int64_t all = 0;
-    before = 0;
-    for (int i = 0; i < parts; ++i) {
-      if (i < part) before += s_part[sums & 1][i];
-      all += s_part[sums & 1][i];
-    }
+    const int64_t* from = &s_part[sums & 1][0][0];
+    int64_t x = 0, ahead = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxCluster * kVerifyWarps; i += 32)
+      if (i + lane < parts * kVerifyWarps) {
+        const int64_t v = from[i + lane];
+        x += v;
+        if (i + lane < part * kVerifyWarps) ahead += v;
+      }
+    before = warp_sum(ahead);
     ++sums;
-    return all;
+    return warp_sum(x);
   };
 
+  // The node the walk stands at, and what its refused children have left of its row.
   int cur = 0, count = 0;
   Row r;
-  while (true) {                                   // one node of the path per turn
-    r.p = P + static_cast<int64_t>(w.q0 + cur) * p.p_stride;
+  int64_t left;                                    // Z, what w sums to, in units of 2^-45
+  float left_hi, left_lo;                          // (without a drafter: the sum of two floats)
+  uint64_t kids;                                   // children not looked at yet
+  auto arrive = [&](int node) {
+    cur = node;
+    r.p = P + static_cast<int64_t>(w.q0 + node) * p.p_stride;
     r.q = nullptr;
     r.set(0);
     gone = 0;
-    double left = 1.0;                             // Z: what w sums to
-    int child = -1;
-    uint64_t kids = count == p.max_path - 1 ? 0ull : w.kids[cur];
-    while (kids) {
+    left = 1ll << 45;
+    left_hi = 1.f;
+    left_lo = 0.f;
+    kids = count == p.max_path - 1 ? 0ull : w.kids[node];
+  };
+  arrive(0);
+  int64_t before, all;
+  for (bool ended = false;;) {                     // (one place that takes sums: its code is large)
+    bool sum = false;
+    while (!sum && !ended) {
+      if (!kids) {
+        ended = true;
+        break;
+      }
       const int i = __ffsll(static_cast<long long>(kids)) - 1;
       kids &= kids - 1;
       const bool known = w.tok[i] >= 0 && w.tok[i] < p.vocab;
-      const double u = s_u[i];
-      if (Q) {
-        const double ql = static_cast<double>(s_q[i]);
-        const double wl = r.q ? static_cast<double>(fixed_left(r, s_p[i], s_q[i])) * kUnit : s_p[i];
-        if (known && u * ql * left < wl) {
-          child = i;
-          break;
-        }
-        r.q = Q + static_cast<int64_t>(w.q0 + cur) * p.q_stride;
-        const uint64_t add = static_cast<uint64_t>(left * 144115188075855872.0);   // Z 2^57, exact
-        r.set(r.S + add < r.S ? ~0ull : r.S + add);
-        if (kids) {
-          int64_t before;
-          left = static_cast<double>(total_of(r, before)) * kUnit;
-        }
-      } else {
-        bool again = !known;                       // a token that has left the row already
-        for (uint64_t m = gone; m; m &= m - 1)
+      bool accepted, again = !known;
+      float wl = 0.f;
+      if (Q) {                                     // u q Z < w
+        accepted = known && (r.q ? below(s_x[i], left, fixed_left(r, s_p[i], s_q[i])) : below(s_x[i], s_p[i]));
+      } else {                                     // u Z < w
+        for (uint64_t m = gone; m; m &= m - 1)     // a token that has left the row already
           again |= w.tok[__ffsll(static_cast<long long>(m)) - 1] == w.tok[i];
-        const double wl = again ? 0.0 : static_cast<double>(s_p[i]);
-        if (u * left < wl) {
-          child = i;
-          break;
-        }
-        left -= wl;
+        wl = again ? 0.f : s_p[i];
+        const float u = s_u[i], h = __fmul_rn(u, left_hi), l = fmaf(u, left_lo, fmaf(u, left_hi, -h));
+        accepted = __fadd_rn(h, -wl) + l < 0.f;
+      }
+      if (accepted) {
+        ++count;
+        if (t == 0) w.path[count] = i;
+        arrive(i);
+      } else if (Q) {
+        r.q = Q + static_cast<int64_t>(w.q0 + cur) * p.q_stride;
+        const uint64_t add = static_cast<uint64_t>(left) << 12;
+        r.set(r.S + add < r.S ? ~0ull : r.S + add);
+        sum = kids != 0;
+      } else {                                     // Z - w in two floats
+        const float d = __fadd_rn(left_hi, -wl), v = __fadd_rn(d, -left_hi);
+        const float e = __fadd_rn(__fadd_rn(left_hi, -__fadd_rn(d, -v)), -__fadd_rn(wl, v)) + left_lo;
+        left_hi = __fadd_rn(d, e);
+        left_lo = __fadd_rn(e, -__fadd_rn(left_hi, -d));
         if (!again) gone |= 1ull << i;
       }
     }
-    if (child < 0) break;
-    cur = child;
-    ++count;
-    if (t == 0) w.path[count] = cur;
-  }
-  // The final draw from w: its sum, the chunk where the running sum passes u sum, the element.
-  int64_t before, all = total_of(r, before);
-  if (all == 0) {                                  // nothing left of the row: p itself
-    r.q = nullptr;
-    r.set(0);
-    gone = 0;
     all = total_of(r, before);
+    if (!ended) left = all;
+    else if (all == 0 && (r.q || gone)) {                // nothing left of the row: p itself
+      r.q = nullptr;
+      r.set(0);
+      gone = 0;
+    } else break;
   }
+  // The final draw from w: the chunk where the running sum passes u sum, the element.
   if (all > 0) {
     // the running sum passes u * all where it passes floor(u * all)
-    const uint64_t u64 = static_cast<uint64_t>(static_cast<double>(s_u[0]) * 18446744073709551616.0);
+    const uint64_t u64 = __float2ull_rz(s_u[0] * 18446744073709551616.f);     // u 2^64, exact
     const int64_t goal = static_cast<int64_t>(__umul64hi(u64, static_cast<uint64_t>(all)));
-    if (warp == 0) {
-      int64_t run = before;                        // before the 32 chunks looked at
-      for (int c0 = 0; c0 < c_hi - c_lo; c0 += 32) {
-        const int64_t mine = c0 + lane < c_hi - c_lo ? s_sum[c0 + lane] : 0;
-        int64_t upto = mine;
+    // which of 32 values in a row passes the goal; at: the sum before lane 0, then before that value
+    auto first_past = [&](int64_t v, int64_t& at) -> int {
+      int64_t to = v;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += v;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, run + upto > goal);
-        if (run <= goal && past) {
-          const int f = __ffs(past) - 1;
-          run += __shfl_sync(0xffffffffu, upto - mine, f);
-          // The chunk's values once more, 32 consecutive ones a step, into shared memory; then lane l
-          // sums those of step l, and the 32 of the step that passes the goal are looked at.
-          const T* rp = static_cast<const T*>(r.p);
-          const T* rq = static_cast<const T*>(r.q);
-          const RowOf<T> row(rp, p.vocab);
-          const int i0 = (c_lo + c0 + f) * kChunk - row.skew;
-          float pv[kSteps], qv[kSteps];
-#pragma unroll
-          for (int u = 0; u < kSteps; ++u) {
-            const int i = i0 + 32 * u + lane;
-            const bool in = i >= 0 && i < p.vocab;
-            pv[u] = in ? to_f32(rp[i]) : 0.f;
-            qv[u] = in && rq ? to_f32(rq[i]) : 0.f;
-          }
-#pragma unroll
-          for (int u = 0; u < kSteps; ++u) s_val[u][lane] = static_cast<int64_t>(__float_as_uint(pv[u])) << 32 | __float_as_uint(qv[u]);
-          __syncwarp();
-#pragma unroll 1
-          for (int u = 0; u < kSteps; ++u) {
-            const int64_t x = s_val[u][lane];
-            int64_t v = fixed_left(r, __uint_as_float(static_cast<uint32_t>(x >> 32)), __uint_as_float(static_cast<uint32_t>(x)));
-            for (uint64_t m = gone; m; m &= m - 1)
-              if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i0 + 32 * u + lane) v = 0;
-            s_val[u][lane] = v;
-          }
-          __syncwarp();
-          int64_t sum = 0;
-          if (lane < kSteps)
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) sum += s_val[lane][i];
-          auto first_past = [&](int64_t v, int64_t& at) -> int {      // at: before lane 0, then before it
-            int64_t to = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const int64_t x = __shfl_up_sync(0xffffffffu, to, o);
-              if (lane >= o) to += x;
-            }
-            const int k = __ffs(__ballot_sync(0xffffffffu, at + to > goal)) - 1;
-            at += __shfl_sync(0xffffffffu, to - v, max(k, 0));
-            return k;
-          };
-          const int step = first_past(sum, run);
-          const int nth = step < 0 ? -1 : first_past(s_val[step][lane], run);
-          if (lane == 0 && nth >= 0) *cluster.map_shared_rank(&s_next, 0) = i0 + 32 * step + nth;
-          break;
-        }
-        run += __shfl_sync(0xffffffffu, upto, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += x;
+      }
+      const int k = __ffs(__ballot_sync(0xffffffffu, at + to > goal)) - 1;
+      at += __shfl_sync(0xffffffffu, to - v, max(k, 0));
+      if (k < 0) at += __shfl_sync(0xffffffffu, to, 31);
+      return k;
+    };
+    int64_t run = before;                          // before the 32 chunks looked at
+    int chunk = -1;
+    if (before <= goal)
+      for (int c0 = 0; c0 < c_hi - c_lo && chunk < 0; c0 += 32) {
+        const int f = first_past(c0 + lane < c_hi - c_lo ? s_sum[c0 + lane] : 0, run);
+        if (f >= 0) chunk = c0 + f;
+      }
+    if (chunk >= 0) {                              // the same in all warps: in this CTA, or not
+      const T* rp = static_cast<const T*>(r.p);
+      const T* rq = static_cast<const T*>(r.q);
+      const RowOf<T> row(rp, p.vocab);
+      const int i0 = (c_lo + chunk) * kChunk - row.skew, i = i0 + 32 * warp + lane;
+      const bool in = i >= 0 && i < p.vocab;
+      int64_t v = fixed_left(r, in ? to_f32(rp[i]) : 0.f, in && rq ? to_f32(rq[i]) : 0.f);
+      for (uint64_t m = gone; m; m &= m - 1)
+        if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i) v = 0;
+      const int64_t sum = warp_sum(v);
+      if (lane == 0) s_warp[warp] = sum;
+      __syncthreads();
+      const int step = first_past(lane < kSteps ? s_warp[lane] : 0, run);
+      if (step == warp) {
+        const int nth = first_past(v, run);
+        if (lane == 0 && nth >= 0) *cluster.map_shared_rank(&s_next, 0) = i0 + 32 * step + nth;
       }
     }
   }
