@@ -28,6 +28,8 @@ namespace {
 
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kSampleThreads = 256, kSampleCtas = 2;   // (an SM)
+constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = MTP_TREE_MAX_NODES;
 constexpr int kChunk = 512;                        // places whose sum is kept (sampling)
@@ -304,9 +306,8 @@ struct Row {
 constexpr uint32_t kDigitA = 0x3F800000u, kDigitB = 0x4B400000u;          // what w = 0 gives
 
 // A node's number times the drafter's probability of its token, exactly: m 2^-e. The walk's comparisons
-// are made in integers, by every thread; FP64 instructions would cost a CTA 256 clocks each, 16 warps
-// at two lanes a clock, and with some 20 of them a refusal took 4.6 us where it now takes @@ us (one
-// sequence, 32000 tokens).
+// are made in integers, by every thread: FP64 instructions take two lanes a clock, so that the 20 or so
+// of a refusal, in 16 warps, were most of its 4.6 us (one sequence, 32000 tokens; 2.4 us without).
 struct Product {
   uint64_t m;                // 48 bits
   int e;
@@ -421,7 +422,7 @@ __device__ __noinline__ int64_t chunk_sums(const Row& r, int vocab, int c_lo, in
   const bool alike = rp.skew == rq.skew;
   int64_t all = 0;
 #pragma unroll 1
-  for (int c = c_lo + warp; c < c_hi; c += kVerifyWarps) {
+  for (int c = c_lo + warp; c < c_hi; c += kSampleWarps) {
     uint32_t a = 0, b = 0;
     const int k0 = c * (kChunk / kVec);
     if (alike && k0 >= rp.first() && k0 + kChunk / kVec <= rp.last()) {
@@ -460,17 +461,25 @@ __device__ __noinline__ int64_t chunk_sums(const Row& r, int vocab, int c_lo, in
   return all;
 }
 
+// A refusal or draw over a row of one sequence takes 1.6 us, 1.2 us of them whatever the row's length
+// (dependent steps: the meeting, the decision), up to 32000 tokens, 3.6 us at 131072; 64 sequences
+// together are bound by the L2 cache (9 us a refusal, 7 TB/s), and a batch of trees by its longest
+// path of refusals (64 trees of 26 nodes over 131072 tokens: 64 us).  256 threads twice an SM leave
+// 128 registers a thread and half as many warps to repeat the decision; 512 threads twice: 68.6 us,
+// 256 four times: 62.3 us but 7.2 instead of 6.5 us for a chain over 32000 tokens.  The next chunk
+// loaded while one is summed made it slower (75 to 98 us): the loads of a chunk at once are enough,
+// and the registers are not.
 template <class T>
-__global__ void __launch_bounds__(kVerifyThreads, 2)
+__global__ void __launch_bounds__(kSampleThreads, kSampleCtas)
 verify_sample_kernel(const VerifyParams p) {
   extern __shared__ int64_t s_sum[];               // the CTA's chunk sums
   __shared__ Walk w;
   __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];   // p, q of each node's token, its number
   __shared__ Product s_x[kNodes];                  // u q of each node's token
-  __shared__ int64_t s_part[2][kMaxCluster][kVerifyWarps];   // by sum parity: the warps' sums
-  __shared__ int64_t s_warp[kVerifyWarps];
+  __shared__ int64_t s_part[2][kMaxCluster][kSampleWarps];   // by sum parity: the warps' sums
   constexpr int kSteps = kChunk / 32;              // 32 values a step, a warp a step
-  static_assert(kSteps == kVerifyWarps);
+  static_assert(kSteps % kSampleWarps == 0);
+  __shared__ int64_t s_step[kSteps];
   __shared__ int s_next;
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), part = cluster.block_rank();
@@ -505,7 +514,7 @@ verify_sample_kernel(const VerifyParams p) {
   uint64_t gone = 0;                               // refused children of the node, one bit each
   auto total_of = [&](const Row& r, int64_t& before) -> int64_t {
     const RowOf<T> rp(static_cast<const T*>(r.p), p.vocab);
-    const int chunks = (rp.end + kChunk - 1) / kChunk, per = (chunks + parts - 1) / parts;
+    const int chunks = (rp.end + kChunk - 1) / kChunk, per = (chunks + parts - 1) >> (31 - __clz(parts));
     c_lo = min(chunks, part * per);
     c_hi = min(chunks, c_lo + per);
     const int mode = r.mode();
@@ -533,11 +542,11 @@ verify_sample_kernel(const VerifyParams p) {
     const int64_t* from = &s_part[sums & 1][0][0];
     int64_t x = 0, ahead = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxCluster * kVerifyWarps; i += 32)
-      if (i + lane < parts * kVerifyWarps) {
+    for (int i = 0; i < kMaxCluster * kSampleWarps; i += 32)
+      if (i + lane < parts * kSampleWarps) {
         const int64_t v = from[i + lane];
         x += v;
-        if (i + lane < part * kVerifyWarps) ahead += v;
+        if (i + lane < part * kSampleWarps) ahead += v;
       }
     before = warp_sum(ahead);
     ++sums;
@@ -638,19 +647,26 @@ verify_sample_kernel(const VerifyParams p) {
       const T* rp = static_cast<const T*>(r.p);
       const T* rq = static_cast<const T*>(r.q);
       const RowOf<T> row(rp, p.vocab);
-      const int i0 = (c_lo + chunk) * kChunk - row.skew, i = i0 + 32 * warp + lane;
-      const bool in = i >= 0 && i < p.vocab;
-      int64_t v = fixed_left(r, in ? to_f32(rp[i]) : 0.f, in && rq ? to_f32(rq[i]) : 0.f);
-      for (uint64_t m = gone; m; m &= m - 1)
-        if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i) v = 0;
-      const int64_t sum = warp_sum(v);
-      if (lane == 0) s_warp[warp] = sum;
-      __syncthreads();
-      const int step = first_past(lane < kSteps ? s_warp[lane] : 0, run);
-      if (step == warp) {
-        const int nth = first_past(v, run);
-        if (lane == 0 && nth >= 0) *cluster.map_shared_rank(&s_next, 0) = i0 + 32 * step + nth;
+      const int i0 = (c_lo + chunk) * kChunk - row.skew + lane;
+      int64_t v[kSteps / kSampleWarps];
+#pragma unroll
+      for (int h = 0; h < kSteps / kSampleWarps; ++h) {
+        const int step = h * kSampleWarps + warp, i = i0 + 32 * step;
+        const bool in = i >= 0 && i < p.vocab;
+        v[h] = fixed_left(r, in ? to_f32(rp[i]) : 0.f, in && rq ? to_f32(rq[i]) : 0.f);
+        for (uint64_t m = gone; m; m &= m - 1)
+          if (w.tok[__ffsll(static_cast<long long>(m)) - 1] == i) v[h] = 0;
+        const int64_t sum = warp_sum(v[h]);
+        if (lane == 0) s_step[step] = sum;
       }
+      __syncthreads();
+      const int step = first_past(lane < kSteps ? s_step[lane] : 0, run);
+#pragma unroll
+      for (int h = 0; h < kSteps / kSampleWarps; ++h)
+        if (step == h * kSampleWarps + warp) {
+          const int nth = first_past(v[h], run);
+          if (lane == 0 && nth >= 0) *cluster.map_shared_rank(&s_next, 0) = i0 + 32 * step + nth;
+        }
     }
   }
   cluster.sync();                                  // s_next is in, and no CTA leaves before
@@ -659,22 +675,22 @@ verify_sample_kernel(const VerifyParams p) {
 
 // ---- host side -----------------------------------------------------------------------------------
 
-// CTAs a sequence: as many as there is room for at two CTAs an SM, each with 2048 elements of
+// CTAs a sequence: as many as there is room for at per_sm CTAs an SM, each with 2048 elements of
 // the row at least.
-int cluster_size(int num_seqs, int vocab) {
+int cluster_size(int num_seqs, int vocab, int per_sm) {
   const int sms = device_sm_count(-1);
   int c = 1;
-  while (c < kMaxCluster && static_cast<int64_t>(num_seqs) * 2 * c <= 2 * sms && vocab / (2 * c) >= 2048)
+  while (c < kMaxCluster && static_cast<int64_t>(num_seqs) * 2 * c <= per_sm * sms && vocab / (2 * c) >= 2048)
     c *= 2;
   return c;
 }
 
 template <class K>
-cudaError_t launch(K kernel, const VerifyParams& p, int num_seqs, int cluster, size_t smem,
+cudaError_t launch(K kernel, const VerifyParams& p, int num_seqs, int threads, int cluster, size_t smem,
                    cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * cluster);
-  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -749,12 +765,12 @@ extern "C" int mtp_tree_verify_greedy(const void* logits, int32_t dtype, int64_t
   p.accept_len = accept_len;
   p.out_tokens = out_tokens;
   p.status = status;
-  const int c = cluster_size(num_seqs, vocab);
+  const int c = cluster_size(num_seqs, vocab, 2);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      dtype == MTP_F32 ? launch(verify_greedy_kernel<float>, p, num_seqs, c, 0, st)
-      : dtype == MTP_BF16 ? launch(verify_greedy_kernel<__nv_bfloat16>, p, num_seqs, c, 0, st)
-                          : launch(verify_greedy_kernel<__half>, p, num_seqs, c, 0, st);
+      dtype == MTP_F32 ? launch(verify_greedy_kernel<float>, p, num_seqs, kVerifyThreads, c, 0, st)
+      : dtype == MTP_BF16 ? launch(verify_greedy_kernel<__nv_bfloat16>, p, num_seqs, kVerifyThreads, c, 0, st)
+                          : launch(verify_greedy_kernel<__half>, p, num_seqs, kVerifyThreads, c, 0, st);
   return e == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
 
@@ -795,13 +811,13 @@ extern "C" int mtp_tree_verify_sample(const void* target_probs, int64_t target_s
   p.accept_len = accept_len;
   p.out_tokens = out_tokens;
   p.status = status;
-  const int c = cluster_size(num_seqs, vocab);
+  const int c = cluster_size(num_seqs, vocab, kSampleCtas);
   const int chunks = (vocab + 8 + kChunk - 1) / kChunk;   // (a row may start up to 7 places into a block)
   const size_t smem = static_cast<size_t>((chunks + c - 1) / c) * sizeof(int64_t);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      dtype == MTP_F32 ? launch(verify_sample_kernel<float>, p, num_seqs, c, smem, st)
-      : dtype == MTP_BF16 ? launch(verify_sample_kernel<__nv_bfloat16>, p, num_seqs, c, smem, st)
-                          : launch(verify_sample_kernel<__half>, p, num_seqs, c, smem, st);
+      dtype == MTP_F32 ? launch(verify_sample_kernel<float>, p, num_seqs, kSampleThreads, c, smem, st)
+      : dtype == MTP_BF16 ? launch(verify_sample_kernel<__nv_bfloat16>, p, num_seqs, kSampleThreads, c, smem, st)
+                          : launch(verify_sample_kernel<__half>, p, num_seqs, kSampleThreads, c, smem, st);
   return e == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
