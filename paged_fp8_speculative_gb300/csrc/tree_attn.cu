@@ -1126,88 +1126,148 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   }
 }
 
-// Join the partials of the units that were cut, a row's pieces weighted by 2^(lse - max).  Thread =
-// row (lane) and 4 kVec dims (warp) of a unit, so every load of a piece is 512 bytes in a piece;
-// all of a step's loads, the log-sum-exps among them, are in flight together, and no thread waits
-// for another: the chain of note, then steps of kAhead pieces is what bounds it.  A piece of a row
-// that saw none of its keys has lse -inf and zeros, and counts nothing; a NaN in any other piece
-// stays in the result.
-constexpr int kReduceThreads = 256;
-constexpr int reduce_ctas(int vec) { return 4 * (kHeadDim / (4 * vec * (kReduceThreads / 32))); }   // a unit
+// The join: out = sum_j w_j o_j / sum_j w_j over a unit's pieces, w_j = 2^(lse_j - max lse).
+//
+// A CTA takes 32 rows (lane = row) and kDims dims of a unit.  Its warps first share out the pieces
+// and leave their weights in shared memory, while the first partials are already on their way;
+// then a warp adds kVec blocks of 4 dims of every kGroups-th piece, kAhead pieces in flight.
+// Rows leave through shared memory, 2 kDims bytes each side by side: written from the registers,
+// 8 bytes a row, the stores were most of the time.  The kernel reads what the main kernel has
+// just written, out of L2.
+constexpr int kReduceThreads = 256, kReduceWarps = kReduceThreads / 32;
+constexpr int kMaxPieces = 160;                      // of a unit: no more than there are CTAs
+template <int kDims, int kVec>
+constexpr int reduce_groups() {
+  return kReduceWarps / (kDims / 4 / kVec);
+}
+constexpr int reduce_ctas(int dims) { return (kRows / 32) * (kHeadDim / dims); }   // a unit
 
-template <int kVec, int kAhead>
+template <int kDims, int kVec, int kAhead>
 __global__ void __launch_bounds__(kReduceThreads)
 tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int kCtaDims = 4 * kVec * (kReduceThreads / 32);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q = blockIdx.y / (kHeadDim / kCtaDims);
-  const int d = kCtaDims * (blockIdx.y % (kHeadDim / kCtaDims)) + 4 * kVec * warp;
-  const int r = 32 * q + lane;                       // row of the unit
+  constexpr int kDimWarps = kDims / 4 / kVec, kGroups = reduce_groups<kDims, kVec>();
+  static_assert(kDimWarps * kGroups == kReduceWarps);
+  constexpr int kPitch = 2 * kDims + 16;             // bytes a row in shared memory
+  __shared__ float s_w[kMaxPieces][32];
+  __shared__ float s_top[kReduceWarps][32], s_sum[kReduceWarps][32];
+  __shared__ float4 s_acc[kGroups > 1 ? kGroups - 1 : 1][kGroups > 1 ? kDimWarps * kVec : 1][32];
+  __shared__ alignas(16) unsigned char s_out[32 * kPitch];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int dw = warp % kDimWarps, g = warp / kDimWarps;
+  const int quad = blockIdx.y / (kHeadDim / kDims), d0 = kDims * (blockIdx.y % (kHeadDim / kDims));
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
   const int units = __ldcg(p.units);
   const int4 n0 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x));
   const int4 n1 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x) + 1);
   if (static_cast<int>(blockIdx.x) >= units || n0.x <= 1) return;
-  const int n = n0.x, q0 = n0.w, h = n1.x, m = n1.y, rows = n1.z;
-  if (r >= rows) return;
+  const int n = min(n0.x, kMaxPieces), q0 = n0.w, h = n1.x, m = n1.y;
+  const int r0 = 32 * quad, rows = min(32, n1.z - r0);   // rows of the unit's, of this quarter
+  if (rows <= 0) return;
+  const bool mine = lane < rows;
   auto slot_of = [&](int i) -> int64_t { return 2 * (n0.y + i) + (i == 0 ? n0.z : 0); };
-  const float* src = p.o_part + (static_cast<int64_t>(d / 4) * kRows + r) * 4;
+  const float* src = p.o_part + (static_cast<int64_t>(d0 / 4 + dw * kVec) * kRows + r0 + lane) * 4;
   constexpr int64_t kSlot = static_cast<int64_t>(kHeadDim) * kRows;
-  float acc[4 * kVec], top = -INFINITY, sum = 0.f;
-  bool bad = false;
+  float4 a[kAhead][kVec];
+  auto load = [&](int i0) {                          // pieces i0, i0 + kGroups, ...
 #pragma unroll
-  for (int e = 0; e < 4 * kVec; ++e) acc[e] = 0.f;
-#pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
-    float4 a[kAhead][kVec];
-    float lse[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      lse[j] = -INFINITY;
-      if (i0 + j < n) {
-        lse[j] = __ldcg(p.lse_part + slot_of(i0 + j) * kRows + r);
+    for (int j = 0; j < kAhead; ++j)
+      if (mine && i0 + j * kGroups < n)
 #pragma unroll
         for (int k = 0; k < kVec; ++k)
-          a[j][k] = __ldcg(reinterpret_cast<const float4*>(src + slot_of(i0 + j) * kSlot + k * 4 * kRows));
-      }
+          a[j][k] = __ldcg(reinterpret_cast<const float4*>(src + slot_of(i0 + j * kGroups) * kSlot + k * 4 * kRows));
+  };
+  load(g);
+  float top = -INFINITY;
+  bool bad = false;
+  constexpr int kLse = 8;                            // a warp's in flight
+#pragma unroll 1
+  for (int i0 = warp; i0 < n; i0 += kLse * kReduceWarps) {
+    float l[kLse];
+#pragma unroll
+    for (int j = 0; j < kLse; ++j) {
+      const int i = i0 + j * kReduceWarps;
+      l[j] = mine && i < n ? __ldcg(p.lse_part + slot_of(i) * kRows + r0 + lane) : -INFINITY;
     }
-    float t = top;
+#pragma unroll
+    for (int j = 0; j < kLse; ++j) {
+      const int i = i0 + j * kReduceWarps;
+      bad |= __float_as_uint(l[j]) == kBadLse;
+      if (i < n) s_w[i][lane] = l[j];
+      top = fmaxf(top, l[j]);                        // (NaN is passed over)
+    }
+  }
+  s_top[warp][lane] = top;
+  bad = __syncthreads_or(bad);                       // (all rows of a sequence with a bad page are)
+#pragma unroll
+  for (int i = 0; i < kReduceWarps; ++i) top = fmaxf(top, s_top[i][lane]);
+  float sum = 0.f;
+#pragma unroll 1
+  for (int i = warp; i < n; i += kReduceWarps) {
+    const float l = s_w[i][lane];
+    const float w = l == -INFINITY ? 0.f : exp2_hw(l - top);         // NaN makes the row NaN
+    s_w[i][lane] = w;
+    sum += w;
+  }
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  float4 acc[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int i0 = g; i0 < n; i0 += kAhead * kGroups) {
+    if (i0 > g) load(i0);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      bad |= __float_as_uint(lse[j]) == kBadLse;
-      t = fmaxf(t, lse[j]);                          // (NaN is passed over)
-    }
-    const float back = t == top ? 1.f : exp2_hw(top - t);
-    top = t;
-    sum *= back;
-#pragma unroll
-    for (int e = 0; e < 4 * kVec; ++e) acc[e] *= back;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (lse[j] == -INFINITY) continue;             // (or past the last piece)
-      const float w = exp2_hw(lse[j] - top);         // NaN makes the row NaN
-      sum += w;
+      const float w = i0 + j * kGroups < n ? s_w[i0 + j * kGroups][lane] : 0.f;
+      if (w == 0.f) continue;                        // (a piece without keys for the row holds anything)
 #pragma unroll
       for (int k = 0; k < kVec; ++k) {
-        acc[4 * k] = fmaf(w, a[j][k].x, acc[4 * k]);
-        acc[4 * k + 1] = fmaf(w, a[j][k].y, acc[4 * k + 1]);
-        acc[4 * k + 2] = fmaf(w, a[j][k].z, acc[4 * k + 2]);
-        acc[4 * k + 3] = fmaf(w, a[j][k].w, acc[4 * k + 3]);
+        acc[k].x = fmaf(w, a[j][k].x, acc[k].x);
+        acc[k].y = fmaf(w, a[j][k].y, acc[k].y);
+        acc[k].z = fmaf(w, a[j][k].z, acc[k].z);
+        acc[k].w = fmaf(w, a[j][k].w, acc[k].w);
       }
     }
   }
-  const float inv = sum == 0.f || bad ? 0.f : 1.f / sum;
-  const int rr = m * kRows + r, node = rr / p.ratio;
-  __nv_bfloat16* out = p.out + static_cast<int64_t>(q0 + node) * p.out_stride_tok +
-                       static_cast<int64_t>(h * p.ratio + rr - node * p.ratio) * p.out_stride_head + d;
+  if (kGroups > 1) {
+    if (g > 0)
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const float f0 = inv == 0.f ? 0.f : acc[4 * k] * inv, f1 = inv == 0.f ? 0.f : acc[4 * k + 1] * inv;
-    const float f2 = inv == 0.f ? 0.f : acc[4 * k + 2] * inv, f3 = inv == 0.f ? 0.f : acc[4 * k + 3] * inv;
-    const __nv_bfloat162 x = __floats2bfloat162_rn(f0, f1), y = __floats2bfloat162_rn(f2, f3);
-    *reinterpret_cast<uint2*>(out + 4 * k) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      for (int k = 0; k < kVec; ++k) s_acc[g - 1][dw * kVec + k][lane] = acc[k];
+    __syncthreads();
+    if (g == 0)
+#pragma unroll 1
+      for (int o = 0; o < kGroups - 1; ++o)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+          const float4 x = s_acc[o][dw * kVec + k][lane];
+          acc[k].x += x.x;
+          acc[k].y += x.y;
+          acc[k].z += x.z;
+          acc[k].w += x.w;
+        }
+  }
+  if (g == 0) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kReduceWarps; ++i) sum += s_sum[i][lane];
+    const float inv = sum == 0.f || bad ? 0.f : 1.f / sum;   // no key, or a bad page: zeros
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      if (inv == 0.f) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
+      const __nv_bfloat162 y = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
+      *reinterpret_cast<uint2*>(s_out + lane * kPitch + (dw * kVec + k) * 8) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+  }
+  __syncthreads();
+  constexpr int kBlocks = kDims / 8;                 // of 16 bytes a row
+  for (int i = t; i < rows * kBlocks; i += kReduceThreads) {
+    const int row = i / kBlocks, b = i % kBlocks, rr = m * kRows + r0 + row, node = rr / p.ratio;
+    __nv_bfloat16* out = p.out + static_cast<int64_t>(q0 + node) * p.out_stride_tok +
+                         static_cast<int64_t>(h * p.ratio + rr - node * p.ratio) * p.out_stride_head + d0 + 8 * b;
+    *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(s_out + row * kPitch + 16 * b);
   }
 }
 
@@ -1303,7 +1363,7 @@ extern "C" size_t mtp_tree_attn_workspace_size(int32_t num_seqs, int32_t total_q
   if (num_seqs < 0 || total_q < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       max_pages_per_seq < 0 || num_q_heads % num_kv_heads)
     return 0;
-  const int sms = device_sm_count(-1);
+  const int sms = std::min(device_sm_count(-1), kMaxPieces);
   if (sms <= 0) return 0;
   const int64_t ctas = std::min<int64_t>(
       sms, line_bound(num_seqs, total_q, num_kv_heads, num_q_heads / num_kv_heads, max_pages_per_seq));
@@ -1387,7 +1447,7 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
   p.out_stride_head = out_stride_head;
   p.status = status;
   p.ctas = static_cast<int32_t>(std::min<int64_t>(
-      device_sm_count(device), line_bound(num_seqs, total_q, num_kv_heads, ratio, max_pages_per_seq)));
+      std::min(device_sm_count(device), kMaxPieces), line_bound(num_seqs, total_q, num_kv_heads, ratio, max_pages_per_seq)));
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = p.o_part + static_cast<int64_t>(p.ctas) * 2 * kRows * kHeadDim;
   p.unit_bound = static_cast<int32_t>(units_bound(num_seqs, total_q, num_kv_heads, ratio));
@@ -1418,8 +1478,8 @@ extern "C" int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_
   if (max_pages_per_seq <= kTilePages) return MTPATTN_OK;
   // Few units are cut into many pieces each: many CTAs of few dims then; many units into few.
   const bool few = p.unit_bound <= 64;
-  const void* kernel = few ? reinterpret_cast<const void*>(tree_reduce_kernel<1, 8>)
-                           : reinterpret_cast<const void*>(tree_reduce_kernel<4, 2>);
-  return launch_pdl(kernel, dim3(p.unit_bound, reduce_ctas(few ? 1 : 4)), kReduceThreads, 0, st, p) == cudaSuccess
+  const void* kernel = few ? reinterpret_cast<const void*>(tree_reduce_kernel<32, 4, 2>)
+                           : reinterpret_cast<const void*>(tree_reduce_kernel<128, 4, 1>);
+  return launch_pdl(kernel, dim3(p.unit_bound, reduce_ctas(few ? 32 : 128)), kReduceThreads, 0, st, p) == cudaSuccess
              ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
