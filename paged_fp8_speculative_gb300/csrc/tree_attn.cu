@@ -130,12 +130,13 @@ struct TreeAttnParams {
 struct Segment {             // part of one unit, key tiles t0 .. t1 - 1 of nt
   int b, h, q0, n, L;
   int m, t0, t1, nt, T;
-  int first;                 // it starts the CTA's piece
-  int end;                   // no segment: the piece is done
-  int bad;                   // set on the way: it met a page outside the pool
-  int nan;                   // ... the V of one of its tree nodes holds a NaN code
+  int16_t first;             // it starts the CTA's piece
+  int16_t end;               // no segment: the piece is done
+  int16_t bad;               // set on the way: it met a page outside the pool
+  int16_t nan;               // ... the V of one of its tree nodes holds a NaN code
 };
 constexpr int kSegRing = 8;
+constexpr int kNoScale = -128;
 
 struct TreeBars {
   uint64_t k_full[kKStages], v_full[kVStages], v_empty[kVStages];
@@ -147,6 +148,7 @@ struct TreeBars {
   Segment seg[kSegRing];     // written by the K producer, given back by the softmax warps
   uint32_t tmem_base;
   int32_t abort;
+  int8_t q_scale[2][kRows];  // by segment parity: a of each row's x = q 2^a; kNoScale: not finite
   int32_t v8_note[kVStages][4];   // of a stage: keys of the sequence, first key of the tree, segment
 };
 static_assert(sizeof(TreeBars) <= kBarBytes, "barrier block");
@@ -804,76 +806,73 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       return ok;
     };
 
-    // Half of the row quarter's rows as two e4m3 terms into the Q operand.  The warp's 16 rows fill
-    // four blocks of 2 KB there (terms x 128-dim halves), as many bytes as the bf16 rows have: these
-    // are first copied to where their own terms will be, all rows in flight, and then taken a row
-    // at a time by the whole warp (8 dims a lane).  Loops stay rolled: fetching straight-line code
-    // for 8 rows at a time cost 9000 cycles at the start of every CTA.  The rows' factors from raw
-    // products to log2 units (NaN for a row that is not finite) go to the exchange, from where
-    // `factor` gets this thread's row's.
-    auto prepare_q = [&](const Segment& y, float& factor) -> bool {
-      const int row0 = 32 * quad + 16 * half;
-      const int rows = y.n * p.ratio - y.m * kRows - row0;           // valid rows from there on
-      float* to = xch + (meets & 1) * 2 * kRows;
+    // The rows as two e4m3 terms into the Q operand: warp w of the 8 takes rows w, w + 8, ..., so that
+    // few rows are soon done (by quarters the warps of a full tile take as long, those of 64 rows
+    // twice as long).  A row fills four 128-byte lines there (terms x 128-dim halves), as many bytes
+    // as in bf16: the rows are first copied to where their own terms will be, all in flight, and then
+    // taken four at a time by the whole warp (8 dims a lane).  Loops stay rolled: fetching
+    // straight-line code for 8 rows at a time cost 9000 cycles at the start of every CTA.  What a
+    // row was scaled by goes to q_scale, from where `factor`, this thread's row's factor from raw products
+    // to log2 units (NaN for a row that is not finite), is made when all warps are done.
+    auto prepare_q = [&](const Segment& y, int e, float& factor) -> bool {
+      const int w = warp - kWarpSoft;
+      const int rows = y.n * p.ratio - y.m * kRows;                  // valid rows of the tile, or more
       // a row quarter without any valid row is not computed; one with some is finite throughout
-      if (rows + 16 * half > 0) {
-        const int mine = y.m * kRows + row0 + (lane & 15);
-        const int t = mine / p.ratio, g = mine - t * p.ratio;
-        const int64_t at = static_cast<int64_t>(y.q0 + t) * p.q_stride_tok +
-                           static_cast<int64_t>(y.h * p.ratio + g) * p.q_stride_head;
-        // 16 bytes a lane: block lane / 8 of the four, 16 (lane % 8) bytes into the row's 128 there
-        const uint32_t own = smem_u32(base + kOffQ) + (lane >> 4) * kQTerm + ((lane >> 3) & 1) * kQHalf +
-                             row0 * 128 + (lane & 7) * 16;
+      const int upto = 4 * min(4, (rows + 31) >> 5);
+      const int mine = y.m * kRows + 8 * (lane & 15) + w;
+      const int t = mine / p.ratio, g = mine - t * p.ratio;
+      const int64_t at = static_cast<int64_t>(y.q0 + t) * p.q_stride_tok +
+                         static_cast<int64_t>(y.h * p.ratio + g) * p.q_stride_head;
+      // 16 bytes a lane: block lane / 8 of the four, 16 (lane % 8) bytes into the row's 128 there
+      const uint32_t own = smem_u32(base + kOffQ) + (lane >> 4) * kQTerm + ((lane >> 3) & 1) * kQHalf +
+                           w * 128 + (lane & 7) * 16;
 #pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          const int64_t src = __shfl_sync(0xffffffffu, at, i);
-          const uint32_t bytes = i < rows ? 16u : 0u;                // 0: zeros are written
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(own + i * 128),
-                       "l"(p.q + (i < rows ? src : 0) + 8 * lane), "r"(bytes) : "memory");
-        }
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
-        const int chunk = (lane & 15) >> 1;
-        unsigned char* q_hi = base + kOffQ + (lane >> 4) * kQHalf + row0 * 128 + 8 * (lane & 1);
-#pragma unroll 1
-        for (int i0 = 0; i0 < 16; i0 += 4) {         // four rows' chains of steps side by side
-          uint4 x[4];
-          uint32_t top[4];                           // the largest |q| by its bits (NaN above all)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = lds128(own + (i0 + i) * 128);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-          {
-            const uint32_t m = max_abs2(max_abs2(x[i].x, x[i].y), max_abs2(x[i].z, x[i].w));
-            top[i] = max(m << 16, m & 0xffff0000u);  // as an f32's bits
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
-          __syncwarp();                              // every lane has read its part of the rows
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = i0 + i;
-            const int e8 = static_cast<int>(top[i] >> 23);           // exponent field
-            // 2^a takes the largest into [128, 256), as far as a = 126 does
-            const int a = top[i] == 0u ? 0 : min(126, 134 - e8);
-            const uint32_t f = (static_cast<uint32_t>(a + 127) << 7) * 0x10001u | flip;
-            uint32_t hi[2], lo[2];
-            two_terms(x[i].x, x[i].y, f, hi[0], lo[0]);
-            two_terms(x[i].z, x[i].w, f, hi[1], lo[1]);
-            unsigned char* dst = q_hi + row * 128 + ((chunk ^ (row & 7)) << 4);
-            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
-            if (lane == row)
-              to[row0 + row] = e8 == 255 || sl_in != sl_in
-                                   ? __int_as_float(0x7fc00000)
-                                   : fmaxf(sl * __int_as_float((127 - a) << 23), 1.17549435e-38f);
-          }
-        }
-        fence_proxy_async_smem();
+      for (int i = 0; i < upto; ++i) {
+        const int64_t src = __shfl_sync(0xffffffffu, at, i);
+        const bool in = 8 * i + w < rows;                            // if not, zeros are written
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(own + i * 1024),
+                     "l"(p.q + (in ? src : 0) + 8 * lane), "r"(in ? 16u : 0u) : "memory");
       }
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
+      unsigned char* q_hi = base + kOffQ + (lane >> 4) * kQHalf + w * 128 + 8 * (lane & 1) +
+                            ((((lane & 15) >> 1) ^ w) << 4);
+#pragma unroll 1
+      for (int i0 = 0; i0 < upto; i0 += 4) {         // four rows' chains of steps side by side
+        uint4 x[4];
+        uint32_t top[4];                             // the largest |q| by its bits (NaN above all)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = lds128(own + (i0 + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t m = max_abs2(max_abs2(x[i].x, x[i].y), max_abs2(x[i].z, x[i].w));
+          top[i] = max(m << 16, m & 0xffff0000u);    // as an f32's bits
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+        __syncwarp();                                // every lane has read its part of the rows
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e8 = static_cast<int>(top[i] >> 23);             // exponent field
+          // 2^a takes the largest into [128, 256), as far as a = 126 does
+          const int a = top[i] == 0u ? 0 : min(126, 134 - e8);
+          const uint32_t f = (static_cast<uint32_t>(a + 127) << 7) * 0x10001u | flip;
+          uint32_t hi[2], lo[2];
+          two_terms(x[i].x, x[i].y, f, hi[0], lo[0]);
+          two_terms(x[i].z, x[i].w, f, hi[1], lo[1]);
+          unsigned char* dst = q_hi + (i0 + i) * 1024;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(dst + kQTerm) = make_uint2(lo[0], lo[1]);
+          if (lane == i) bars.q_scale[e & 1][8 * (i0 + i) + w] = static_cast<int8_t>(e8 == 255 ? kNoScale : a);
+        }
+      }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.q_ready));
-      if (!meet()) return false;
-      factor = to[r];
+      const uint32_t bar = smem_u32(&bars.q_ready);
+      if (lane == 0) mbar_arrive(bar);
+      if (!__all_sync(0xffffffffu, wait_for(bar, e & 1, abort_flag))) return false;
+      const int a = *reinterpret_cast<const volatile int8_t*>(&bars.q_scale[e & 1][r]);
+      factor = a == kNoScale || sl_in != sl_in ? __int_as_float(0x7fc00000)
+                                               : fmaxf(sl * __int_as_float((127 - a) << 23), 1.17549435e-38f);
       return true;
     };
 
@@ -888,7 +887,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       const Segment& y = bars.seg[e % kSegRing];
       const bool end = y.end != 0;
       float sl2_next = 0.f;
-      if (!end && !prepare_q(y, sl2_next)) break;
+      if (!end && !prepare_q(y, e, sl2_next)) break;
       if (e > 0) {
         const Segment& s = bars.seg[(e - 1) % kSegRing];
         // the row's sum over both halves
@@ -907,8 +906,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
                             wait_for(smem_u32(&bars.pv_done[last & 1]), (last >> 1) & 1, abort_flag)))
           break;
         tc_fence_after();
-        const bool bad = *reinterpret_cast<const volatile int*>(&s.bad) != 0;
-        const bool nan_v = *reinterpret_cast<const volatile int*>(&s.nan) != 0;
+        const bool bad = *reinterpret_cast<const volatile int16_t*>(&s.bad) != 0;
+        const bool nan_v = *reinterpret_cast<const volatile int16_t*>(&s.nan) != 0;
         if (bad && lane == 0 && half == 0) set_status(p.status, MTPATTN_ERR_PAGE);
         const bool whole = s.t0 == 0 && s.t1 == s.nt;
         if (active) {
