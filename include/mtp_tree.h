@@ -141,7 +141,8 @@ int mtp_tree_verify_greedy(const void* logits, int32_t dtype, int64_t row_stride
  *  uniforms     device float32 [total_q] in [0, 1): node i's own number, the root's for the
  *               final draw.  Taken into [0, 1 - 2^-24]; NaN counts as 0.
  * Sums are exact: each w is taken to a whole number of units of 2^-45 and these are summed in
- * 64-bit integers, so the result does not depend on the order of summation.
+ * 64-bit integers, so the result does not depend on the order of summation.  Rows need not sum to
+ * 1; a row's sum has to stay below 2^18.
  */
 int mtp_tree_verify_sample(const void* target_probs, int64_t target_stride,
                            const void* draft_probs, int64_t draft_stride, int32_t dtype,

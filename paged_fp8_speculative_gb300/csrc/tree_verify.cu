@@ -26,7 +26,7 @@ namespace cg = cooperative_groups;
 namespace mtpattn {
 namespace {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256, kVerifyCtas = 4;   // (an SM)
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kSampleThreads = 256, kSampleCtas = 2;   // (an SM)
 constexpr int kSampleWarps = kSampleThreads / 32;
@@ -186,7 +186,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 // bounds a step is that latency, then two meetings of the cluster.  The elements before the first
 // and behind the last whole block, at most 2 kVec - 2, are a thread's each.
 template <class T>
-__global__ void __launch_bounds__(kVerifyThreads, 2)
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
 verify_greedy_kernel(const VerifyParams p) {
   constexpr int kUnroll = 8, kVec = RowOf<T>::kVec;
   __shared__ Walk w;
@@ -289,18 +289,18 @@ verify_greedy_kernel(const VerifyParams p) {
 struct Row {
   const void* p;
   const void* q;             // null: w = p
-  uint64_t S;                // in units of 2^-57
+  uint64_t S;                // in units of 2^-45, as its parts are
   float s_hi, s_lo;          // S as the sum of two floats
   __device__ __forceinline__ void set(uint64_t s) {                      // (its 24 top bits, the rest)
     S = s;
     const int below = max(0, 40 - __clzll(static_cast<long long>(s)));
     const uint64_t top = s >> below;
-    constexpr float kUnitS = 6.938893903907228e-18f;                     // 2^-57
+    constexpr float kUnitS = 2.8421709430404007e-14f;                    // 2^-45
     s_hi = static_cast<float>(static_cast<uint32_t>(top)) * kUnitS * __uint_as_float((127u + below) << 23);
     s_lo = __ull2float_rn(s - (top << below)) * kUnitS;
   }
   // 0: w = p; 1: S = 1, what the first refusal leaves; 2: any S
-  __device__ __forceinline__ int mode() const { return !q ? 0 : S == (1ull << 57) ? 1 : 2; }
+  __device__ __forceinline__ int mode() const { return !q ? 0 : S == (1ull << 45) ? 1 : 2; }
 };
 
 constexpr uint32_t kDigitA = 0x3F800000u, kDigitB = 0x4B400000u;          // what w = 0 gives
@@ -332,7 +332,7 @@ __device__ __forceinline__ bool below(const Product& x, float p) {
 __device__ __forceinline__ bool below(const Product& x, int64_t z, int64_t w) {
   const uint64_t lo = x.m * static_cast<uint64_t>(z), hi = __umul64hi(x.m, static_cast<uint64_t>(z));
   const uint64_t v = x.e >= 128 ? 0 : x.e >= 64 ? hi >> (x.e - 64) : lo >> x.e | hi << (64 - x.e);   // x.e >= 47
-  return static_cast<int64_t>(v) < w;
+  return v < static_cast<uint64_t>(w);              // (neither is negative)
 }
 
 struct F2 {
@@ -394,10 +394,12 @@ __device__ __noinline__ int64_t fixed_left(const Row& r, float p, float q) {
   return fixed_of(a, b, 2);
 }
 
-// Sums over the warp's lanes, by redux: of 48 bits and a sign; of digits of up to 16 elements a lane.
+// Sums over the warp's lanes, by redux: of 64 bits; of the digits of up to 16 elements a lane.
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
-  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0xffffffu);
-  return (static_cast<int64_t>(__reduce_add_sync(0xffffffffu, static_cast<int32_t>(v >> 24))) << 24) + lo;
+  const uint32_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0xffffffu);
+  const uint32_t b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 24) & 0xffffffu);
+  const uint32_t c = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 48));
+  return static_cast<int64_t>((static_cast<uint64_t>(c) << 48) + (static_cast<uint64_t>(b) << 24) + a);
 }
 __device__ __forceinline__ int64_t warp_fixed(uint32_t a, uint32_t b, int n) {
   a -= static_cast<uint32_t>(n) * kDigitA;          // up to 2^27, |b| up to 3 2^24
@@ -599,7 +601,7 @@ verify_sample_kernel(const VerifyParams p) {
         arrive(i);
       } else if (Q) {
         r.q = Q + static_cast<int64_t>(w.q0 + cur) * p.q_stride;
-        const uint64_t add = static_cast<uint64_t>(left) << 12;
+        const uint64_t add = static_cast<uint64_t>(left);
         r.set(r.S + add < r.S ? ~0ull : r.S + add);
         sum = kids != 0;
       } else {                                     // Z - w in two floats
@@ -765,7 +767,7 @@ extern "C" int mtp_tree_verify_greedy(const void* logits, int32_t dtype, int64_t
   p.accept_len = accept_len;
   p.out_tokens = out_tokens;
   p.status = status;
-  const int c = cluster_size(num_seqs, vocab, 2);
+  const int c = cluster_size(num_seqs, vocab, kVerifyCtas);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       dtype == MTP_F32 ? launch(verify_greedy_kernel<float>, p, num_seqs, kVerifyThreads, c, 0, st)
