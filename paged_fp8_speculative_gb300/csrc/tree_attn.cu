@@ -10,8 +10,13 @@
 // written out at once; a unit cut by piece borders leaves one partial output and log-sum-exp per
 // piece in the workspace, and tree_reduce_kernel joins them: the CTA that has a unit's first
 // key tile leaves a note on it.  A CTA has at most two partial units, the first and the last of its piece:
-// two slots per CTA.  Where whole units, one a CTA, take at most kCutTiles tiles longer than equal
-// pieces, they are not cut (joining takes about as long).
+// two slots per CTA.  Units are not cut, and get a CTA each, where the longest of them takes no more
+// tiles longer than equal pieces than joining costs: kCutTiles, and one for kCutPieces full tiles
+// of 128 rows written and read as partials.  Measured, whole units against pieces: 2 tiles of
+// 64 rows 10.5 and 11.0 us, 3 tiles 11.6 and 11.2; 40 units of 8 tiles of 64 rows 21.2 and 17.6;
+// 76 units of 20 full tiles 40.5 and 36.0, 100 units 42.4 and 43.3, 140 units 46.2 and 54.3; 128
+// units of 65 full tiles 97.8 and 101.5.  A unit weighs kUnitTiles tiles more than it has (its rows'
+// preparation and its output): with 2 the ragged batch takes 46.3 instead of 44.9 us, with 4 or 5 the same.
 //
 // Roles (512 threads; warp 3 only reports sequences whose rows are not known):
 //   warp 0      the CTA's walk over its piece, published segment by segment, and the K pages by
@@ -89,7 +94,7 @@ constexpr int kSmemTree = kOffBar + kBarBytes;
 static_assert(kSmemTree == 232448, "all that a block may have");
 constexpr int kSCols = 128, kOCol = 256, kTmemCols = 512;
 constexpr float kTau = 6.f, kShift = 8.f;
-constexpr int kCutTiles = 6, kUnitTiles = 3;
+constexpr int kCutTiles = 4, kCutPieces = 40, kUnitTiles = 3;
 constexpr uint32_t kBadLse = 0x7fd0bad1u;          // a partial of a sequence with a bad page (a NaN
                                                    // that no arithmetic makes)
 
@@ -223,7 +228,11 @@ __device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const
   c.V = 0;
   c.length = W;
   c.units = U;
-  if (U <= p.ctas && longest + kUnitTiles <= c.C + kCutTiles) {
+  // What cutting costs, in tiles: the join, and its bytes (pieces, less for tiles that are not full).
+  const float rows = static_cast<float>(p.total_q) * static_cast<float>(p.ratio * p.hkv);
+  const float full = fminf(1.f, rows / static_cast<float>(kRows * max(U, 1)));
+  const int join = kCutTiles + static_cast<int>(static_cast<float>(U + p.ctas) * full * (1.f / kCutPieces));
+  if (U <= p.ctas && longest + kUnitTiles <= c.C + join) {
     c.C = c.V = longest;
     c.length = U * longest;
   }
