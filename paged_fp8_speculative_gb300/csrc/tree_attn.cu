@@ -675,6 +675,9 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
           now = ahead;
           ahead = entries(hf + 8);
         }
+#ifdef MTPATTN_TEST_STALL
+        if (blockIdx.x == 0 && v == 0) continue;    // test builds: the wait for these codes runs out
+#endif
         const int phys = __shfl_sync(0xffffffffu, now, (4 * eight + lane) & 31);
         const bool bad = __any_sync(0xffffffffu, lane < np && (phys < 0 || phys >= p.num_pages));
         const uint32_t fb = smem_u32(&bars.v8_full[st]);
@@ -1169,7 +1172,12 @@ tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
   const int4 n0 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x));
   const int4 n1 = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x) + 1);
   if (static_cast<int>(blockIdx.x) >= units || n0.x <= 1) return;
-  const int n = min(n0.x, kMaxPieces), q0 = n0.w, h = n1.x, m = n1.y;
+  const int n = n0.x, q0 = n0.w, h = n1.x, m = n1.y;
+  // A CTA whose wait ran out may have left no note: what stands there then is not followed.
+  if (n > p.ctas || n0.y < 0 || n0.y > p.ctas - n || (n0.z & ~1) || q0 < 0 || h < 0 || h >= p.hkv || m < 0 ||
+      m >= MTP_TREE_MAX_NODES * MTP_TREE_MAX_RATIO / kRows || n1.z <= 0 || n1.z > kRows ||
+      q0 > p.total_q - 1 - (m * kRows + n1.z - 1) / p.ratio)
+    return;
   const int r0 = 32 * quad, rows = min(32, n1.z - r0);   // rows of the unit's, of this quarter
   if (rows <= 0) return;
   const bool mine = lane < rows;
