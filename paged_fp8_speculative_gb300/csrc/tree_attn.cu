@@ -498,9 +498,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
     while (ok) {
       Segment s;
       const int err = walk.next(p, lane, s);
-      if (lane == 0 && !s.end && s.t0 == 0 && !walk.cut.V && walk.unit < p.unit_bound)
-        p.notes[walk.unit] = walk.note(p, s);
+      auto leave_note = [&]() {
+        if (lane == 0 && s.t0 == 0 && !walk.cut.V && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
+      };
       if (err && !s.end) {
+        leave_note();
         // zeros for the rows of a sequence that cannot be computed, here: it has no key tiles
         if (lane == 0) set_status(p.status, err);
         const int rows = min(kRows, s.n * p.ratio - s.m * kRows);
@@ -522,6 +524,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
       }
       if (s.end) break;
       ++e;
+      leave_note();
       const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
       const uint64_t pol = s.T == 1 ? once : again;
       // Table entries, a lane one of four tiles' 32, with the next 32 on the way: a load of its own
