@@ -226,10 +226,14 @@ cache_plan_kernel(const PlanParams p) {
   }
   cluster.sync();                                  // resize: all lengths and counts have been read
 
-  int err = 0, my_row = -1, my_len = 0;
+  constexpr int kOwn = MTP_CACHE_MAX_ROWS / (kPlanThreads * kPlanCtas);      // items a thread, at most
+  static_assert(kOwn * kPlanThreads * kPlanCtas == MTP_CACHE_MAX_ROWS);
+  int err = 0, my_row[kOwn], my_len[kOwn];
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) my_row[o] = -1;
   if (Fork) {
     for (int i = t; i < p.items; i += kPlanThreads) {
-      const int src = p.src[i], row = p.dst[i];      // item gt is this thread's own one
+      const int src = p.src[i], row = p.dst[i];
       const bool rows = src >= 0 && src < p.rows && row >= 0 && row < p.rows && src != row &&
                         s.claim[row] == i && p.seq_lens[row] == 0;
       const int len = rows ? p.seq_lens[src] : 0;
@@ -242,10 +246,12 @@ cache_plan_kernel(const PlanParams p) {
       s.slot[i] = live ? len / kPage : -1;
       s.tail[i] = part_full ? p.bt[static_cast<int64_t>(src) * p.max_pages + len / kPage] : -1;
       s.sum[i] = part_full;
-      if (i == gt && live) {
-        my_row = row;
-        my_len = len;
-      }
+#pragma unroll
+      for (int o = 0; o < kOwn; ++o)
+        if (i == gt + o * gthreads && live) {
+          my_row[o] = row;
+          my_len[o] = len;
+        }
     }
     __syncthreads();
     cluster.barrier_arrive();                      // this CTA has read the lengths
@@ -302,9 +308,11 @@ cache_plan_kernel(const PlanParams p) {
         }
       }
     // A source row may be the dst of another pair: its length has been read by every CTA before
-    // one is written. A thread has one pair at most.
+    // one is written.
     cluster.barrier_wait();
-    if (fits && my_row >= 0) p.seq_lens[my_row] = my_len;
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o)
+      if (fits && my_row[o] >= 0) p.seq_lens[my_row[o]] = my_len[o];
   } else {
     for (int i = gt; i < p.rows; i += gthreads)
       if (s.slot[i] >= 0) {

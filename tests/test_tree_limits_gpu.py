@@ -115,6 +115,14 @@ def test_the_largest_table():
     assert not c.counts.any()
 
 
+def test_forks_of_a_few_rows_into_all_others():
+    """More pairs than a plan has threads."""
+    c = Pair(8192, 2, 9000, layers=1, hkv=1, seed=6)
+    c.resize([17, 5, 32, 16] + [0] * 8188)
+    c.fork([int(x) for x in np.random.default_rng(6).integers(0, 4, 8188)], list(range(4, 8192)))
+    assert min(c.lens) == 5
+
+
 def test_two_streams_side_by_side():
     """Calls on two streams, issued by two host threads, each with outputs and workspaces of its own."""
     batches = [Batch([3000, 40], [16, 5], 1, 16, seed=21), Batch([2500], [64], 2, 8, seed=22)]
