@@ -130,7 +130,8 @@ int mtp_tree_verify_greedy(const void* logits, int32_t dtype, int64_t row_stride
  *   child i with token x is accepted if uniforms[i] * q(x) * Z < w(x); if not,
  *   S += Z, w = max(p - S q, 0), Z = sum w.
  * (w / Z is the residual distribution after each refusal.)  Without draft_probs q is 1 at the
- * child's own token and 0 elsewhere: refused tokens leave the row.  If no child is accepted the
+ * child's own token and 0 elsewhere: a refused token leaves the row, and Z falls by what it had
+ * there.  A token outside [0, vocab) is never accepted.  If no child is accepted the
  * next token is the first x whose running sum of w exceeds uniforms[root] * sum w; if w has no
  * mass left, w = p is used instead, and if p has none, the token is -1 with MTP_TREE_ERR_ROW.
  *  target_probs device [total_q][vocab] of `dtype` (MTP_F32, _BF16 or _F16): row i is the

@@ -593,7 +593,7 @@ verify_sample_kernel(const VerifyParams p) {
           again |= w.tok[__ffsll(static_cast<long long>(m)) - 1] == w.tok[i];
         wl = again ? 0.f : s_p[i];
         const float u = s_u[i], h = __fmul_rn(u, left_hi), l = fmaf(u, left_lo, fmaf(u, left_hi, -h));
-        accepted = __fadd_rn(h, -wl) + l < 0.f;
+        accepted = known && __fadd_rn(h, -wl) + l < 0.f;   // (so Z stays above 0: refused, w <= u Z < Z)
       }
       if (accepted) {
         ++count;

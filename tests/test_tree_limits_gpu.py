@@ -208,6 +208,16 @@ def test_rows_that_are_no_distributions():
         sample(clean(p), None if drafter is None else clean(q), trees, tokens, u)
 
 
+def test_a_token_outside_is_refused_whatever_the_row_sums_to():
+    """Without a drafter, behind refused children that had nearly all, or more than all, of the mass."""
+    p = torch.zeros(5, 10, device="cuda")
+    for first, second in ((0.875, 0.124), (1.0 - 2.0 ** -23, 2.0 ** -30), (0.75, 0.125)):
+        p[0, :3] = torch.tensor([first, second, 0.5])
+        u = torch.tensor([0.5, 1 - 2.0 ** -24, 1 - 2.0 ** -24, 0.0, 0.5], device="cuda")
+        for last in ([10, -1], [1 << 30, 10]):
+            assert sample(p, None, [[-1, 0, 0, 0, 0]], [0, 0, 1] + last, u)[1][1].item() == 0
+
+
 def test_the_same_rows_whatever_the_batch():
     """A sequence's result does not depend on how many CTAs it gets: alone, and among 200."""
     p, q, trees, tokens, u = draw([26], 20000, 51, spread=1.0)
