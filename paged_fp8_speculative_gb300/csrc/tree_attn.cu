@@ -10,13 +10,15 @@
 // written out at once; a unit cut by piece borders leaves one partial output and log-sum-exp per
 // piece in the workspace, and tree_reduce_kernel joins them: the CTA that has a unit's first
 // key tile leaves a note on it.  A CTA has at most two partial units, the first and the last of its piece:
-// two slots per CTA.  Units are not cut, and get a CTA each, where the longest of them takes no more
-// tiles longer than equal pieces than joining costs: kCutTiles, and one for kCutPieces full tiles
-// of 128 rows written and read as partials.  Measured, whole units against pieces: 2 tiles of
-// 64 rows 10.5 and 11.0 us, 3 tiles 11.6 and 11.2; 40 units of 8 tiles of 64 rows 21.2 and 17.6;
-// 76 units of 20 full tiles 40.5 and 36.0, 100 units 42.4 and 43.3, 140 units 46.2 and 54.3; 128
-// units of 65 full tiles 97.8 and 101.5.  A unit weighs kUnitTiles tiles more than it has (its rows'
-// preparation and its output): with 2 the ragged batch takes 46.3 instead of 44.9 us, with 4 or 5 the same.
+// two slots per CTA.  Units are not cut, and the CTAs get as many each, where so many of the longest
+// take no more tiles longer than equal pieces than joining costs: kCutTiles, and one for kCutPieces
+// full tiles of 128 rows written and read as partials, divided by the units a CTA gets.  Measured,
+// whole units against pieces: 2 tiles of 64 rows 10.5 and 11.0 us, 3 tiles 11.6 and 11.2; 40 units of
+// 8 tiles of 64 rows 21.2 and 17.6; 76 units of 20 full tiles 40.5 and 36.0, 100 units 42.4 and 43.3,
+// 140 units 46.2 and 54.3; 128 units of 65 full tiles 97.8 and 101.5; 160 units of 4 full tiles 35.4
+// and 34.0; 256 units of 3 tiles of 32 rows 26.5 and 30.7, 1024 of them 92.2 and 98.0.  A unit weighs
+// kUnitTiles tiles more than it has (its rows' preparation and its output): with 2 the ragged batch
+// takes 46.3 instead of 44.9 us, with 4 or 5 the same.
 //
 // Roles (512 threads; warp 3 only reports sequences whose rows are not known):
 //   warp 0      the CTA's walk over its piece, published segment by segment, and the K pages by
@@ -204,7 +206,7 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
 }
 
 // How the line is cut: pieces of C places, piece g from g C on.  With V > 0 every unit takes V
-// places on the line, and so a piece of its own.
+// places on the line, and C is a multiple of V: no unit is cut.
 struct Cut {
   int C, V, length, units;
 };
@@ -232,8 +234,10 @@ __device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const
   const float rows = static_cast<float>(p.total_q) * static_cast<float>(p.ratio * p.hkv);
   const float full = fminf(1.f, rows / static_cast<float>(kRows * max(U, 1)));
   const int join = kCutTiles + static_cast<int>(static_cast<float>(U + p.ctas) * full * (1.f / kCutPieces));
-  if (U <= p.ctas && longest + kUnitTiles <= c.C + join) {
-    c.C = c.V = longest;
+  const int each = max(1, (U + p.ctas - 1) / p.ctas);
+  if (static_cast<int64_t>(each) * (longest + kUnitTiles) <= c.C + join / each) {
+    c.V = longest;
+    c.C = each * longest;
     c.length = U * longest;
   }
   return c;
