@@ -12,7 +12,7 @@ import torch
 import oracle
 from paged_fp8_speculative_gb300 import api
 from tests.test_cache_pages_gpu import Pair
-from tests.test_tree_attn_gpu import Batch, run
+from tests.test_tree_attn_gpu import Batch, check, run
 from tests.test_tree_verify_gpu import draw, greedy, packed, sample, trees_of, walkable
 
 pytestmark = pytest.mark.gpu
@@ -40,6 +40,19 @@ def test_calls_with_nothing_to_do():
     assert api.mtp_cache_compact(k, k, i32([]).view(0, 3), none, cu, i32([]).view(0, 8), none).shape == (0,)
     torch.cuda.synchronize()
     assert not k.any() and not refs.any()
+
+
+@pytest.mark.parametrize("lens,nodes,hkv,ratio", [
+    ([300] * 400, [3] * 400, 1, 8),                 # several whole units a CTA
+    ([260 + 7 * (i % 20) for i in range(310)], [1 + i % 9 for i in range(310)], 1, 16),
+    ([129] * 33 + [128] * 100 + [640] * 70, [2] * 203, 2, 4),
+    ([64 + i for i in range(90)], [64] * 90, 1, 16),   # eight row tiles a sequence
+    ([120000], [9], 1, 2),                          # one unit, a piece for every CTA
+    ([50000, 33], [64, 33], 1, 16),
+], ids=["whole", "mixed", "short", "wide", "long", "longwide"])
+def test_many_units_and_long_ones(lens, nodes, hkv, ratio):
+    batch = Batch(lens, nodes, hkv, ratio, seed=len(lens))
+    check(run(batch), batch)
 
 
 @pytest.fixture(scope="module")
