@@ -74,9 +74,10 @@ int mtp_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q, int32_t n
  *               must use different workspaces.
  * Sequences with a device-side error (MTPATTN_ERR_QLEN: node count outside [1, 64];
  * _QLEN_GT_SEQ; _SEQ_TOO_LONG; _PAGE) get zeros, except that the rows of a sequence whose
- * cu_seqlens_q entries are not ascending within total_q are unknown and not written.  Rows
+ * cu_seqlens_q entries are not ascending within total_q are unknown and not written.  (Where the
+ * sequences claim more than twice total_q rows in all, nothing is written, with _QLEN.)  Rows
  * that belong to no sequence are not written.  Results are the same bits in every call with the
- * same arguments.  Two kernels are launched on `stream`.
+ * same arguments.  One or two kernels are launched on `stream`.
  */
 int mtp_tree_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_head,
                       const void* k_cache, const void* v_cache, int64_t num_pages,

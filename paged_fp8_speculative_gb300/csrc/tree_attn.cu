@@ -212,17 +212,33 @@ struct Cut {
 };
 __device__ __forceinline__ int weight_of(const Seq& s, int hkv, int V) { return V ? s.T * hkv * V : s.w; }
 
+// Sum over the warp of numbers from 0 to 2^31 - 1.
+__device__ __forceinline__ int64_t warp_total(int v) {
+  return (static_cast<int64_t>(__reduce_add_sync(0xffffffffu, v >> 16)) << 16) + __reduce_add_sync(0xffffffffu, v & 0xffff);
+}
+__device__ __forceinline__ int add_up_to_max(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), static_cast<uint32_t>(INT32_MAX)));
+}
+
 // By the whole warp; `mine` is lane l's sequence l (of the first 32).
 __device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const Seq& mine) {
-  int W = mine.w, U = mine.T * p.hkv, longest = mine.nt;
+  int W = mine.w, N = mine.n, U = mine.T * p.hkv, longest = mine.nt;
 #pragma unroll 1
   for (int b0 = 32; b0 < p.num_seqs; b0 += 32) {
     const Seq x = seq_at(p, b0 + lane);
-    W += x.w;
+    W = add_up_to_max(W, x.w);
+    N = add_up_to_max(N, x.n);
     U += x.T * p.hkv;
     longest = max(longest, x.nt);
   }
-  W = __reduce_add_sync(0xffffffffu, W);
+  // Sequences that claim the same rows again and again (cu_seqlens_q far out of order) could make the line
+  // longer than any call's is: then nothing is computed.
+  const int64_t all = warp_total(W);
+  if (all > INT32_MAX || warp_total(N) > 2ll * p.total_q) {
+    if (blockIdx.x == 0 && lane == 0) set_status(p.status, MTPATTN_ERR_QLEN);
+    return {1, 1, 0, 0};
+  }
+  W = static_cast<int>(all);
   U = __reduce_add_sync(0xffffffffu, U);
   longest = __reduce_max_sync(0xffffffffu, longest);
   Cut c;
@@ -235,7 +251,8 @@ __device__ __forceinline__ Cut cut_line(const TreeAttnParams& p, int lane, const
   const float full = fminf(1.f, rows / static_cast<float>(kRows * max(U, 1)));
   const int join = kCutTiles + static_cast<int>(static_cast<float>(U + p.ctas) * full * (1.f / kCutPieces));
   const int each = max(1, (U + p.ctas - 1) / p.ctas);
-  if (static_cast<int64_t>(each) * (longest + kUnitTiles) <= c.C + join / each) {
+  if (static_cast<int64_t>(each) * (longest + kUnitTiles) <= c.C + join / each &&
+      static_cast<int64_t>(U) * longest <= INT32_MAX) {
     c.V = longest;
     c.C = each * longest;
     c.length = U * longest;

@@ -55,6 +55,20 @@ def test_many_units_and_long_ones(lens, nodes, hkv, ratio):
     check(run(batch), batch)
 
 
+def test_sequences_that_claim_the_same_rows_again_and_again():
+    """cu_seqlens_q 0, 320, 0, 320, ...: nothing is computed; the next call is as ever."""
+    batch = Batch([200] * 64, [5] * 64, 1, 8, seed=9)
+    want = run(batch)
+    args = batch.device()
+    good = args["cu_seqlens_q"]
+    args["cu_seqlens_q"] = i32([0] + [320, 0] * 32)
+    out, status = torch.full_like(want, 5.0), i32([0])
+    api.mtp_tree_attn_fwd(**args, out=out, status=status)
+    assert status.item() == api.ERR_QLEN and bool((out == 5.0).all())
+    args["cu_seqlens_q"] = good
+    assert torch.equal(api.mtp_tree_attn_fwd(**args, out=out), want)
+
+
 @pytest.fixture(scope="module")
 def huge():
     """A cache of 66000 pages of 32 KB: byte offsets of the last ones pass 2^31 (and 2^32 in all)."""
