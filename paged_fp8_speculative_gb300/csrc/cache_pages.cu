@@ -53,6 +53,7 @@ struct PlanParams {
   int32_t* status;
 };
 
+// (of a length that has been compared with its table's: the sum passes 32 bits for others)
 __device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
 
 // A plan's shared memory. An item is a row (resize) or a pair of rows (fork).
@@ -400,7 +401,7 @@ cache_compact_kernel(const CompactParams p) {
   int err = 0;
   if (q0 < 0 || q1 <= q0 || q1 > p.total_q || n > MTP_TREE_MAX_NODES) err = MTPATTN_ERR_QLEN;
   else if (n > L) err = MTPATTN_ERR_QLEN_GT_SEQ;
-  else if (pages_of(L) > p.max_pages) err = MTPATTN_ERR_SEQ_TOO_LONG;
+  else if (L > p.max_pages * kPage) err = MTPATTN_ERR_SEQ_TOO_LONG;   // (within 32 bits: checked by the host)
   else if (m < 0 || m >= n || m >= p.max_path) err = MTP_CACHE_ERR_LEN;
   const int start = L - n;
   int mine = 0;
