@@ -27,6 +27,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 namespace cg = cooperative_groups;
 
@@ -65,11 +66,11 @@ struct PlanSmem {
   int* claim;                // [rows], fork: the first pair that names a dst
   uint8_t* bad;              // [items], fork: the source row has a bad entry
 };
-__host__ __device__ inline int mask_words(int num_pages) {
+__host__ __device__ constexpr int mask_words(int num_pages) {
   const int per = (num_pages + kPlanCtas - 1) / kPlanCtas;
   return ((per + kPlanWarps - 1) / kPlanWarps + 31) / 32 * kPlanWarps;
 }
-inline size_t plan_smem(bool fork, int num_pages, int items, int rows) {
+constexpr size_t plan_smem(bool fork, int num_pages, int items, int rows) {
   return 4 * (static_cast<size_t>(mask_words(num_pages)) + 3 * static_cast<size_t>(items)) +
          (fork ? 4 * static_cast<size_t>(rows) + (items + 3) / 4 * 4 : 0);
 }
@@ -455,21 +456,31 @@ int check_caches(const void* k, const void* v, int32_t layers, int64_t layer_str
   return MTPATTN_OK;
 }
 
+// A kernel has 48 KB of shared memory, its static part counted, unless it asks for more.  The plans ask
+// once per device for the most that any takes (200 KB): a call that asked for its own size could take back
+// what another host thread has just asked for, and is about to launch with.
+constexpr int kMaxDevices = 64;
+constexpr size_t kMostPlanSmem = plan_smem(true, MTP_CACHE_MAX_PAGES, MTP_CACHE_MAX_ROWS, MTP_CACHE_MAX_ROWS);
+static_assert(kMostPlanSmem + 1024 <= 227 * 1024, "a plan's shared memory");
 template <bool Fork>
-cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
+cudaError_t allow_plan_smem(int device) {
+  static std::atomic<bool> allowed[kMaxDevices];     // setting it twice is harmless
+  if (allowed[device].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel<Fork>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kMostPlanSmem));
+  if (e != cudaSuccess) cudaGetLastError();
+  else allowed[device].store(true, std::memory_order_release);
+  return e;
+}
+
+template <bool Fork>
+cudaError_t launch_plan(const PlanParams& p, int device, cudaStream_t stream) {
+  if (const cudaError_t e = allow_plan_smem<Fork>(device); e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPlanCtas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = plan_smem(Fork, p.num_pages, p.items, p.rows);
   cfg.stream = stream;
-  if (cfg.dynamicSmemBytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel<Fork>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(cfg.dynamicSmemBytes));
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
-    }
-  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kPlanCtas;
@@ -501,7 +512,7 @@ int plan_and_copy(bool fork, PlanParams& p, CopyParams& c, void* workspace, size
                   int device, cudaStream_t stream) {
   const size_t need = mtp_cache_workspace_size(p.rows, p.max_pages);
   if (!workspace || !ptr_aligned(workspace, 256) || bytes < need) return MTPATTN_E_WORKSPACE;
-  if (device < 0) return MTPATTN_E_DEVICE;
+  if (device < 0 || device >= kMaxDevices) return MTPATTN_E_DEVICE;
   const void* const ptrs[] = {c.k, c.v, p.bt, p.seq_lens, p.ref, workspace};
   if (!all_on_device(ptrs, device) || (p.status && !ptr_on_device(p.status, device)) ||
       (fork ? !ptr_on_device(p.src, device) || !ptr_on_device(p.dst, device)
@@ -510,7 +521,7 @@ int plan_and_copy(bool fork, PlanParams& p, CopyParams& c, void* workspace, size
   p.copies = static_cast<int2*>(workspace);
   c.copies = p.copies;
   c.items = p.items;
-  if ((fork ? launch_plan<true>(p, stream) : launch_plan<false>(p, stream)) != cudaSuccess)
+  if ((fork ? launch_plan<true>(p, device, stream) : launch_plan<false>(p, device, stream)) != cudaSuccess)
     return MTPATTN_E_LAUNCH;
   return launch_copy(c, stream) == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
