@@ -96,3 +96,31 @@ def test_plans_of_several_threads():
     for t in threads:
         t.join()
     assert not said, (len(said), said[:3])
+
+
+def test_the_largest_pool_and_table():
+    """2^22 pages, the free ones at their end, and 8192 rows, all resized and half of them forked: the
+    largest plan there is.  No row has a partly filled page, so the caches' contents are not touched."""
+    lib, pages, rows, width = _lib.lib(), 1 << 22, 8192, 4
+    cache = torch.zeros(16 * 256, dtype=torch.uint8, device="cuda")
+    table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
+    lens, half = ints([0] * rows), rows // 2
+    refs = torch.ones(pages, dtype=torch.int32, device="cuda")
+    first = pages - half * width - 5
+    refs[first:] = 0
+    ws = torch.empty(api.mtp_cache_workspace_size(rows, width), dtype=torch.uint8, device="cuda")
+    status, stream = ints([0]), torch.cuda.current_stream().cuda_stream
+    pool = (cache.data_ptr(), cache.data_ptr(), 1, pages * 16 * 256, pages, 1, table.data_ptr(), width, lens.data_ptr(), rows,
+            refs.data_ptr())
+    tail = (ws.data_ptr(), ws.numel(), status.data_ptr(), stream)
+    new = ints([16 * width] * half + [0] * half)
+    src, dst = ints(list(range(half))), ints(list(range(half, rows)))
+    assert lib.mtp_cache_resize(*pool, new.data_ptr(), *tail) == 0
+    assert lib.mtp_cache_fork(*pool, src.data_ptr(), dst.data_ptr(), half, *tail) == 0
+    want = torch.arange(half * width, device="cuda").int().view(half, width) + first
+    assert status.item() == 0
+    assert torch.equal(table, torch.cat([want, want])) and (lens == 16 * width).all()
+    assert (refs[first:-5] == 2).all() and (refs[-5:] == 0).all() and (refs[:first] == 1).all()
+    new.zero_()
+    assert lib.mtp_cache_resize(*pool, new.data_ptr(), *tail) == 0
+    assert status.item() == 0 and not lens.any() and (table == -1).all() and not refs[first:].any()
