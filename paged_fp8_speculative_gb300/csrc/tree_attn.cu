@@ -1175,6 +1175,8 @@ template <int kDims, int kVec>
 constexpr int reduce_groups() {
   return kReduceWarps / (kDims / 4 / kVec);
 }
+constexpr float kNoKey = -1.f;                       // in a weight's place: the row sees no key of the piece
+__device__ __forceinline__ float nan_of(float x) { return x != x ? x : 0.f; }
 constexpr int reduce_ctas(int dims) { return (kRows / 32) * (kHeadDim / dims); }   // a unit
 
 template <int kDims, int kVec, int kAhead>
@@ -1246,7 +1248,7 @@ tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
   for (int i = warp; i < n; i += kReduceWarps) {
     const float l = s_w[i][lane];
     const float w = l == -INFINITY ? 0.f : exp2_hw(l - top);         // NaN makes the row NaN
-    s_w[i][lane] = w;
+    s_w[i][lane] = l == -INFINITY ? kNoKey : w;
     sum += w;
   }
   s_sum[warp][lane] = sum;
@@ -1259,8 +1261,18 @@ tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
     if (i0 > g) load(i0);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const float w = i0 + j * kGroups < n ? s_w[i0 + j * kGroups][lane] : 0.f;
-      if (w == 0.f) continue;                        // (a piece without keys for the row holds anything)
+      const float w = i0 + j * kGroups < n ? s_w[i0 + j * kGroups][lane] : kNoKey;
+      if (w == kNoKey) continue;                     // (a piece without keys for the row holds anything)
+      if (w == 0.f) {                                // far below the others: what is NaN there stays NaN
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+          acc[k].x += nan_of(a[j][k].x);
+          acc[k].y += nan_of(a[j][k].y);
+          acc[k].z += nan_of(a[j][k].z);
+          acc[k].w += nan_of(a[j][k].w);
+        }
+        continue;
+      }
 #pragma unroll
       for (int k = 0; k < kVec; ++k) {
         acc[k].x = fmaf(w, a[j][k].x, acc[k].x);
