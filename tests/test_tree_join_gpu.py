@@ -1,13 +1,85 @@
-"""Tree attention over sequences that are cut into pieces: what a row sees in a piece of no weight is
-not lost."""
+"""Tree attention over sequences that are cut into pieces: every key counts once, in whatever piece,
+and what a row sees in a piece of no weight is not lost.
+
+The keys of `Told` batches are told apart in the output.  K has one dim that is not 0, which goes
+through SIZES by turns of 48 keys, so that logits lie within a unit and each is one product; V has a 1
+in one dim only, key j's being j // ceil(L / 256).  Output dim d is then the weight of its own run of
+keys, at most 469 of them, and a page of 16 keys that is left out, or counted twice, changes it by
+a few percent.  (With random values an output is the mean of many that cancel: the same bound, which
+goes by the values' sizes, is then half as large as the output itself, and a lost piece is within it.)
+
+Tolerance: that of tests/test_tree_attn_gpu.py.  With one product a logit, `reach` is the row's largest
+|q| (about 4) x 1.5 x SCALE x KD, 0.6, and W is the output itself: about
+2^-8 + 2^-11 + 2 x 0.6 (2^-17 + 2^-15) + 4 sqrt(n) 2^-24 = 0.0045 of it.
+"""
 from __future__ import annotations
+
+import functools
 
 import numpy as np
 import pytest
 import torch
 
+import oracle
 from paged_fp8_speculative_gb300 import api
-from tests.test_tree_attn_gpu import KD, NAN_CODE, Batch
+from tests.test_tree_attn_gpu import KD, NAN_CODE, SCALE, VD, Batch, bound, check, run
+
+SIZES = (0.0, 1.5, -1.0, 0.5, -1.5, 1.0, -0.5)
+ONE = 0x38                                         # e4m3 1.0
+
+
+class Told(Batch):
+    def __init__(self, lens, nodes, hkv, ratio, seed=0):
+        super().__init__(lens, nodes, hkv, ratio, seed=seed, poison=False)
+        steps = np.array([int(np.nonzero(oracle.E4M3_TABLE == x)[0][0]) for x in SIZES], np.uint8)
+        self.k[:], self.v[:] = 0, 0
+        for b, L in enumerate(lens):
+            j = np.arange(L)
+            page, at = self.bt[b, j // 16], j % 16
+            self.k[page, at, :, 3] = steps[j // 48 % len(SIZES)][:, None]
+            for h in range(hkv):
+                self.v[page, at, h, j // -(-L // 256)] = ONE
+
+
+# what the call makes of them: one unit over every CTA; two row tiles a unit's sequence; three long
+# ones that CTAs share; long and short together; units that are cut once or not at all; two KV heads
+CUT = [([120000], [9], 1, 2), ([50000, 33], [64, 33], 1, 16), ([9100, 12001, 30003], [16, 5, 11], 1, 16),
+       ([20011, 40, 3000, 17], [64, 2, 7, 9], 1, 16), ([1290] * 40, [3] * 40, 2, 8),
+       ([40001, 2500], [4, 20], 2, 5)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,nodes,hkv,ratio", CUT, ids=[f"{len(c[0])}x{max(c[0])}" for c in CUT])
+def test_every_key_counts_once(lens, nodes, hkv, ratio):
+    batch = Told(lens, nodes, hkv, ratio, seed=len(lens))
+    check(run(batch), batch)
+
+
+@functools.lru_cache
+def told_one():
+    """One long sequence: (batch, oracle's output, bound)."""
+    batch = Told([120000], [2], 1, 2, seed=1)
+    out, weight, reach = batch.exact()
+    return batch, out, bound(out, weight, reach, batch.lens)
+
+
+@pytest.mark.parametrize("first,count,times", [(0, 768, 0), (5376, 768, 0), (119296, 704, 0), (768, 768, 2),
+                                               (64000, 128, 0), (64000, 128, 2), (31999 * 2, 16, 0), (31999 * 2, 16, 2)])
+def test_the_bound_notices_keys_left_out_or_counted_twice(first, count, times):
+    """A piece of 768 keys, a key tile, a page: the oracle's own sum without them, or with them twice."""
+    batch, out, limit = told_one()
+    L = batch.lens[0]
+    q = batch.q.double().numpy()[:, :, 3]          # K's dim
+    s = SCALE * KD * q[:, :, None] * np.array(SIZES)[np.arange(L) // 48 % len(SIZES)]
+    e = np.exp(s)
+    e[:, :, L - 2:] *= np.array([[1, 0], [1, 1]])[:, None, :]            # the root does not see its child
+    mine = np.arange(L) // -(-L // 256)
+    sums = lambda w: VD * np.stack([np.bincount(mine, r, minlength=256) for r in w.reshape(-1, L)]).reshape(2, 2, 256) / \
+        w.sum(-1, keepdims=True)
+    assert (np.abs(sums(e) - out) <= 1e-9).all()   # the same definition
+    e[:, :, first:first + count] *= times
+    off = np.abs(sums(e) - out) / limit
+    assert off.max() > (2.0 if count > 16 else 1.2), off.max()
 
 
 @pytest.mark.gpu
