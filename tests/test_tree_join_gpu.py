@@ -114,3 +114,20 @@ def test_a_nan_in_a_piece_of_no_weight_is_seen(lens, nodes):
         hit[:, :, dims] = sees[:, None, None]
         assert got[hit].isnan().all(), (key, got[hit])
         assert torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.gpu
+def test_sequences_whose_places_are_not_in_order():
+    """cu_seqlens_q 0, 30, 14, 20 of 20 rows: the first two sequences' rows are not known and not
+    written; the third's are the attention of that sequence."""
+    batch = Batch([100, 300, 40], [5, 9, 6], 2, 8, seed=16)
+    args = batch.device()
+    args["cu_seqlens_q"][1] = 30
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(args["q"], 5.0)
+    api.mtp_tree_attn_fwd(**args, out=out, status=status)
+    assert status.item() == api.ERR_QLEN
+    assert (out[:14] == 5.0).all()
+    exact, weight, reach = (x[14:] for x in batch.exact())
+    off = np.abs(out[14:].float().cpu().numpy() - exact) / bound(exact, weight, reach, batch.lens)
+    assert off.max() <= 1.0
