@@ -10,6 +10,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -212,13 +214,12 @@ int64_t row_stride(const at::Tensor& t) {  // a single row's stride means nothin
   return t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1));
 }
 
-// A contiguous tensor of its own over a part of another's memory.
-at::Tensor part_of(const at::Tensor& memory, int64_t offset, at::IntArrayRef sizes) {
-  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(memory.storage()), memory.key_set(),
-                                                          memory.dtype());
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-  t.unsafeGetTensorImpl()->set_storage_offset(offset);
-  return t;
+// An int32 tensor on like's device, every element of which the call writes: at::empty without the way
+// through the dispatcher.  stream_of has made sure that a CUDA device is the current one.
+at::Tensor ints_like(const at::Tensor& like, at::IntArrayRef sizes) {
+  if (!like.is_cuda()) return at::empty(sizes, like.options().dtype(at::kInt));
+  return at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(),
+                                   c10::DispatchKeySet(c10::DispatchKey::CUDA), at::kInt, std::nullopt);
 }
 
 // tokens, parents, cu, max_path, accept_index, accept_len, out_tokens at a
@@ -235,19 +236,10 @@ Verify verify_args(const at::Tensor& rows, const char* name, PyObject* const* a)
   r.seqs = sequences(tensor(a[2], "cu_seqlens_q"));
   r.width = integer(a[3], "max_path");
   REFUSE_IF(r.width < 1 || r.width > MTP_TREE_MAX_NODES, "max_path must be 1 to 64");
-  const at::TensorOptions opts = rows.options().dtype(at::kInt);
-  const int64_t all = static_cast<int64_t>(r.seqs) * r.width;
-  if (!given(a[4]) && !given(a[5]) && !given(a[6])) {
-    // one allocation for the three (1.2 us of host time each)
-    const at::Tensor memory = at::empty({2 * all + r.seqs}, opts);
-    r.index = part_of(memory, 0, {r.seqs, r.width});
-    r.said = part_of(memory, all, {r.seqs, r.width});
-    r.count = part_of(memory, 2 * all, {r.seqs});
-  } else {
-    r.index = given(a[4]) ? tensor(a[4], "accept_index") : at::empty({r.seqs, r.width}, opts);
-    r.count = given(a[5]) ? tensor(a[5], "accept_len") : at::empty({r.seqs}, opts);
-    r.said = given(a[6]) ? tensor(a[6], "out_tokens") : at::empty({r.seqs, r.width}, opts);
-  }
+  // (a storage each: one that is kept, or grows in place, does not touch the others)
+  r.index = given(a[4]) ? tensor(a[4], "accept_index") : ints_like(rows, {r.seqs, r.width});
+  r.count = given(a[5]) ? tensor(a[5], "accept_len") : ints_like(rows, {r.seqs});
+  r.said = given(a[6]) ? tensor(a[6], "out_tokens") : ints_like(rows, {r.seqs, r.width});
   for (const auto& [t, what] : {std::pair<const at::Tensor&, const char*>(r.index, "accept_index"),
                                 std::pair<const at::Tensor&, const char*>(r.said, "out_tokens")})
     REFUSE_IF(t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != r.seqs || t.size(1) != r.width || !t.is_contiguous(),
