@@ -6,7 +6,7 @@
 //
 // Functions take positional arguments only (the wrappers in api.py give them names, defaults and
 // documentation); None stands for what is not given.  A refused argument is a ValueError, a status
-// of the library the class that set_error was given.
+// of the library the class that set_error was given, an error of torch's what torch makes of it.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -119,8 +120,8 @@ PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t) {
     return kBody(args);
   } catch (const Refused& r) {
     PyErr_SetString(PyExc_ValueError, r.what.c_str());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {              // torch's own: torch.OutOfMemoryError among them
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
