@@ -2,8 +2,10 @@
 
 Every ``csrc/*.cu`` file compiles to an object in parallel, then one link makes
 ``paged_fp8_speculative_gb300/libmtpattn.so``; beside them g++ compiles ``csrc/binding.cpp``, the
-compiled part of the Python binding, linked to that library.  Run as ``python -m
-paged_fp8_speculative_gb300.build`` or through ``__graft_entry__.build()``.
+compiled part of the Python binding, linked to that library.  The library needs neither PyTorch nor
+Python's headers: it is linked first, and is there for C programs where the binding cannot be built
+(which is an error all the same).  Run as ``python -m paged_fp8_speculative_gb300.build`` or through
+``__graft_entry__.build()``.
 """
 from __future__ import annotations
 
@@ -20,7 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmtpattn.so")
-BINDING = os.path.join(PKG, "_binding.so")
+# with the interpreter's own suffix, so that no other version of Python takes it for its own
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -77,19 +80,25 @@ def build(verbose: bool = False, extra_flags=(), lib_path: str = LIB) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     product = lib_path == LIB
+    binding, no_binding = None, ""
     if product:
-        compile_binding, link_binding = binding_commands()
-        if verbose:
-            print(" ".join(compile_binding), flush=True)
-        procs.append(("binding.cpp", subprocess.Popen(compile_binding, stdout=subprocess.PIPE,
-                                                      stderr=subprocess.STDOUT)))
-    failed = []
-    for src, pr in procs:
+        try:
+            compile_binding, link_binding = binding_commands()
+            if verbose:
+                print(" ".join(compile_binding), flush=True)
+            binding = subprocess.Popen(compile_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        except (RuntimeError, OSError) as e:         # no PyTorch, no g++
+            no_binding = str(e)
+
+    def ended(pr) -> bool:
         out, _ = pr.communicate()
         if pr.returncode != 0 or (verbose and out):
             sys.stdout.write(out.decode(errors="replace"))
-        if pr.returncode != 0:
-            failed.append(src)
+        return pr.returncode == 0
+
+    failed = [src for src, pr in procs if not ended(pr)]
+    if binding and not ended(binding):
+        no_binding = "compiling csrc/binding.cpp failed"
     if failed:
         raise RuntimeError(f"compiling failed for {failed}")
     tmp = lib_path + ".tmp"
@@ -99,8 +108,14 @@ def build(verbose: bool = False, extra_flags=(), lib_path: str = LIB) -> str:
     subprocess.check_call(cmd)
     os.replace(tmp, lib_path)
     if product:
-        subprocess.check_call(link_binding)
+        if not no_binding and subprocess.call(link_binding) != 0:
+            no_binding = "linking it failed"
+        if no_binding:
+            raise RuntimeError(f"{os.path.basename(lib_path)} is built, the Python binding is not: {no_binding}")
         os.replace(BINDING + ".tmp", BINDING)
+        untagged = os.path.join(PKG, "_binding.so")  # what builds made before the name had a suffix
+        if os.path.exists(untagged):
+            os.remove(untagged)
     return lib_path
 
 
