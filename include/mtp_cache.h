@@ -54,7 +54,8 @@ size_t mtp_cache_workspace_size(int32_t num_rows, int32_t max_pages_per_seq);
  * filled page (at the smaller of the two lengths) is shared gets a copy of it first, in all
  * layers.  If the free pages (after what is given back) do not suffice, no page is handed out or
  * copied, MTP_CACHE_ERR_FULL is set and every row stays at the smaller of its two lengths.
- *  new_lens   device int32 [num_rows]; a row to be left alone gets its own length.
+ *  new_lens   device int32 [num_rows], apart from seq_lens (else MTPATTN_E_ARG); a row to be left
+ *             alone gets its own length.
  *  workspace  device, >= mtp_cache_workspace_size(num_rows, ..) bytes, 256-byte aligned, not
  *             initialised; calls that overlap on the GPU must use different ones.
  * A table entry outside [0, num_pages) that would be given back sets MTPATTN_ERR_PAGE and is
@@ -104,7 +105,7 @@ int mtp_cache_copy_pages(void* k_cache, void* v_cache, int32_t num_layers, int64
  * their row alone.
  *  accept_index device int32 [num_seqs][max_path] and accept_len [num_seqs], as the verification
  *               entry points of mtp_tree.h write them: accept_index[b][0] = 0, ascending.
- *  new_seq_lens device int32 [num_seqs], not seq_lens itself.
+ *  new_seq_lens device int32 [num_seqs], apart from all inputs (else MTPATTN_E_ARG).
  * A sequence whose path is not strictly ascending from 0 within its n_b nodes (or accept_len -1)
  * sets MTP_CACHE_ERR_LEN, one with a bad node count or length MTPATTN_ERR_QLEN, _QLEN_GT_SEQ or
  * _SEQ_TOO_LONG, one with a table entry outside [0, num_pages) under its tree MTPATTN_ERR_PAGE;

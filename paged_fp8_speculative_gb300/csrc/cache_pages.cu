@@ -555,8 +555,8 @@ extern "C" int mtp_cache_resize(void* k_cache, void* v_cache, int32_t num_layers
   if (rc == MTPATTN_OK) rc = check_table(block_tables, max_pages_per_seq, seq_lens, num_rows);
   if (rc != MTPATTN_OK) return rc;
   if (num_rows == 0) return MTPATTN_OK;
-  if (!ref_counts || !new_lens || new_lens == seq_lens || !ptr_aligned(ref_counts, 4) ||
-      !ptr_aligned(new_lens, 4) || !ptr_aligned(status, 4))
+  if (!ref_counts || !new_lens || words_overlap(new_lens, num_rows, seq_lens, num_rows) ||
+      !ptr_aligned(ref_counts, 4) || !ptr_aligned(new_lens, 4) || !ptr_aligned(status, 4))
     return MTPATTN_E_ARG;
   PlanParams p{};
   p.bt = block_tables;
@@ -657,7 +657,7 @@ extern "C" int mtp_cache_compact(void* k_cache, void* v_cache, int32_t num_layer
   if (num_seqs < 0 || total_q < 0 || max_pages_per_seq < 0 || max_path < 1) return MTPATTN_E_ARG;
   if (num_seqs == 0) return total_q == 0 ? MTPATTN_OK : MTPATTN_E_ARG;
   if (total_q < num_seqs || !block_tables || !seq_lens || !cu_seqlens_q || !accept_index ||
-      !accept_len || !new_seq_lens || new_seq_lens == seq_lens || max_pages_per_seq == 0)
+      !accept_len || !new_seq_lens || max_pages_per_seq == 0)
     return MTPATTN_E_ARG;
   if (!ptr_aligned(block_tables, 4) || !ptr_aligned(seq_lens, 4) || !ptr_aligned(cu_seqlens_q, 4) ||
       !ptr_aligned(accept_index, 4) || !ptr_aligned(accept_len, 4) ||
@@ -667,6 +667,15 @@ extern "C" int mtp_cache_compact(void* k_cache, void* v_cache, int32_t num_layer
       total_q > static_cast<int64_t>(num_seqs) * MTP_TREE_MAX_NODES ||
       static_cast<int64_t>(num_layers) * 2 * num_kv_heads > (1 << 28))
     return MTPATTN_E_UNSUPPORTED;
+  // every CTA of a sequence reads its inputs, and one of them writes the new length
+  const int64_t table_words = static_cast<int64_t>(num_seqs) * max_pages_per_seq;
+  const int64_t path_words = static_cast<int64_t>(num_seqs) * max_path;
+  if (words_overlap(new_seq_lens, num_seqs, seq_lens, num_seqs) ||
+      words_overlap(new_seq_lens, num_seqs, accept_len, num_seqs) ||
+      words_overlap(new_seq_lens, num_seqs, cu_seqlens_q, static_cast<int64_t>(num_seqs) + 1) ||
+      words_overlap(new_seq_lens, num_seqs, accept_index, path_words) ||
+      words_overlap(new_seq_lens, num_seqs, block_tables, table_words))
+    return MTPATTN_E_ARG;
   const int device = current_device();
   if (device < 0) return MTPATTN_E_DEVICE;
   const void* const ptrs[] = {k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q,

@@ -12,6 +12,12 @@ inline bool ptr_aligned(const void* p, size_t a) {
   return reinterpret_cast<uintptr_t>(p) % a == 0;
 }
 
+// Whether two runs of 32-bit words have a word in common.
+inline bool words_overlap(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * static_cast<uintptr_t>(m) && y < x + 4 * static_cast<uintptr_t>(n);
+}
+
 // The current device, or -1.
 inline int current_device() {
   int device = -1;
