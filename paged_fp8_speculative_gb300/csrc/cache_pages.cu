@@ -13,8 +13,8 @@
 // What bounds a plan is its chain of dependent memory accesses (lengths, table entry, count,
 // rank, place: about 0.5 us each) and the meetings, not the bytes: so what a row asks for is
 // worked out once by every CTA and stays in shared memory, and loads that do not depend on a
-// meeting are issued before it.  Three calls (rows freed and trimmed, forked, grown) take 16.5 us
-// in a CUDA graph for 4 rows and a pool of 512 pages, 29 us for 256 rows, 128 forks and 16384
+// meeting are issued before it.  Three calls (rows freed and trimmed, forked, grown) take 16.5 to
+// 17.2 us in a CUDA graph for 4 rows and a pool of 512 pages, 29 us for 256 rows, 128 forks and 16384
 // pages; with the items read again at each step, four meetings and the copying kernel launched
 // after the plan it was 33 and 48 us.  One CTA instead of the cluster's 8 is no faster for the
 // small table (16.5 us) and takes 72 us for the large one; 1024 threads a CTA 18.0 and 29.9 us.
