@@ -102,7 +102,7 @@ def test_the_largest_pool_and_table():
     """2^22 pages, the free ones at their end, and 8192 rows, all resized and half of them forked: the
     largest plan there is.  No row has a partly filled page, so the caches' contents are not touched."""
     lib, pages, rows, width = _lib.lib(), 1 << 22, 8192, 4
-    cache = torch.zeros(16 * 256, dtype=torch.uint8, device="cuda")
+    cache = torch.empty(pages * 16 * 256, dtype=torch.uint8, device="cuda")     # 16 GB, K's and V's
     table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
     lens, half = ints([0] * rows), rows // 2
     refs = torch.ones(pages, dtype=torch.int32, device="cuda")
