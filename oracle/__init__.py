@@ -36,8 +36,9 @@ from .formats import E4M3_TABLE, e4m3_value, bf16_bits_to_f64, bf16_ulp
 from .attention import (kv_head_of, last_visible_key, gather_keys, verify_attention,
                         verify_attention_rows)
 from .metrics import max_err_over_std, excess_over_half_ulp
-from . import cache, prefill, tree
+from . import cache, latent, prefill, rope, tree
 
 __all__ = ["E4M3_TABLE", "e4m3_value", "bf16_bits_to_f64", "bf16_ulp", "kv_head_of",
            "last_visible_key", "gather_keys", "verify_attention", "verify_attention_rows",
-           "max_err_over_std", "excess_over_half_ulp", "cache", "prefill", "tree"]
+           "max_err_over_std", "excess_over_half_ulp", "cache", "latent",
+           "prefill", "rope", "tree"]

@@ -1,5 +1,6 @@
 """ctypes loader for libmtpattn.so (the C ABI declared in include/mtpattn.h and
-include/fmha_fp8_varlen.h, include/mtp_tree.h and include/mtp_cache.h).
+include/fmha_fp8_varlen.h, include/mtp_tree.h, include/mtp_cache.h, include/mtp_rope.h and
+include/mtp_latent.h).
 
 There is no fallback: if the library is missing the import of this module's
 ``lib()`` raises, so no caller can silently run anything else.
@@ -106,6 +107,47 @@ SIGNATURES = {
         _c_i32, _c_i32,                 # num_seqs, total_q
         _vp, _vp, _c_i32, _vp,          # accept_index, accept_len, max_path, new_seq_lens
         _vp, _vp]),
+    # include/mtp_rope.h
+    "mtp_rope_freqs": (_c_int, [_vp, _c_i32, _vp]),
+    "mtp_rope_append": (_c_int, [
+        _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64,  # q, k, v, strides
+        _c_i32, _vp, _vp,               # dtype, positions, freqs
+        _c_i32, _c_i32, _c_float,       # rot_dim, interleaved, mscale
+        _vp, _vp, _c_i64, _vp, _c_i32,  # k_cache, v_cache, num_pages, block_tables, max_pages
+        _vp, _vp,                       # seq_lens, cu_seqlens_q
+        _c_i32, _c_i32, _c_i32, _c_i32,  # num_seqs, total_q, num_q_heads, num_kv_heads
+        _vp, _vp,                       # k_descale, v_descale
+        _vp, _c_i64, _c_i64,            # q_out, strides
+        _vp, _vp]),                     # status, stream
+    "mtp_rope_latent_append": (_c_int, [
+        _vp, _c_i64, _c_i64,            # q_rope, strides
+        _vp, _c_i64, _vp, _c_i64,       # latent, k_rope, strides
+        _c_i32, _vp, _vp,               # dtype, positions, freqs
+        _c_i32, _c_float,               # interleaved, mscale
+        _vp, _c_i64, _vp, _c_i32,       # cache, num_pages, block_tables, max_pages
+        _vp, _vp,                       # seq_lens, cu_seqlens_q
+        _c_i32, _c_i32, _c_i32,         # num_seqs, total_q, num_heads
+        _vp,                            # descale
+        _vp, _c_i64, _c_i64,            # q_out, strides
+        _vp, _vp]),                     # status, stream
+    "mtp_rope_prefill": (_c_int, [
+        _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64,   # q, k, strides
+        _vp, _c_i64, _vp, _c_i64, _c_i64,           # k_rope, v, strides
+        _c_i32, _vp, _vp, _c_i32, _c_float,         # dtype, positions, freqs, interleaved, mscale
+        _c_i32, _c_i32, _c_i32,         # total, num_q_heads, num_kv_heads
+        _vp, _vp, _vp,                  # descales
+        _vp, _vp, _vp, _vp]),           # q8, k8, v8, stream
+    # include/mtp_latent.h
+    "mtp_latent_attn_fwd": (_c_int, [
+        _vp, _c_i64, _c_i64,            # q, strides
+        _vp, _c_i64, _vp, _c_i32,       # cache, num_pages, block_tables, max_pages_per_seq
+        _vp, _vp, _vp,                  # seq_lens, cu_seqlens_q, tree_mask
+        _c_i32, _c_i32, _c_i32,         # num_seqs, total_q, num_heads
+        _vp, _c_float,                  # descale, softmax_scale
+        _vp, _c_size,                   # workspace, workspace_bytes
+        _vp, _c_i64, _c_i64,            # out, strides
+        _vp, _vp]),                     # status, stream
+    "mtp_latent_attn_workspace_size": (_c_size, [_c_i32, _c_i32, _c_i32, _c_i32]),
 }
 
 _LIB = None

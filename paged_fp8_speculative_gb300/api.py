@@ -7,6 +7,7 @@ the library's CUDA kernels.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import math
 from typing import Optional
 
@@ -527,3 +528,132 @@ def mtp_cache_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables
                     accept_len, new_seq_lens, status, None)
     return _on_stream(call, (k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q, accept_index,
                              accept_len, new_seq_lens, status), stream, k_cache.device)
+
+
+# ---- rotary positions and new tokens (include/mtp_rope.h; checks and calls in csrc/binding.cpp) ------
+
+
+def mtp_rope_freqs(inv_freq, device=None) -> torch.Tensor:
+    """The angles of rotary positions as the calls below take them: int64 [pairs], whole numbers of
+    2^-64 turns a position, from radians a position (``inv_freq``: numbers or a tensor, 0 to 2^20;
+    rope.inv_freq makes the usual ones).  Made once and kept."""
+    values = inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else [float(x) for x in inv_freq]
+    n = len(values)
+    radians, out = (ctypes.c_double * n)(*values), (ctypes.c_int64 * n)()
+    rc = lib().mtp_rope_freqs(ctypes.cast(radians, ctypes.c_void_p), n, ctypes.cast(out, ctypes.c_void_p))
+    if rc != OK:
+        raise ValueError("inv_freq must be finite, 0 to 2^20 radians a position")
+    return torch.tensor(list(out), dtype=torch.int64, device=device)
+
+
+def _descales(device, stream, *values):
+    if all(isinstance(x, torch.Tensor) for x in values):
+        return values
+    with _temporaries_on(stream, device, True):
+        return tuple(_descale(x, device) for x in values)
+
+
+def mtp_rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                    positions: torch.Tensor, freqs: Optional[torch.Tensor], k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                    cu_seqlens_q: torch.Tensor, k_descale, v_descale, mscale: float = 1.0,
+                    interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """New tokens into one layer's K/V cache, with rotary positions on q and k; returns q_out.
+
+    q [total_q, H_q, 256] (None: no q), k and v [total_q, H_kv, 256]: bfloat16, float16 or float32, all
+    the same, unit stride along the head (views of a joint projection will do); positions [total_q]
+    int32; freqs int64 [pairs] (mtp_rope_freqs; the first 2 * pairs elements of a head are rotated, a
+    multiple of 16; None: none); the caches, tables, lengths (the new tokens included) and cu_seqlens_q
+    of the attention calls, with any number of tokens a sequence; descales as there.  Pairs are elements
+    2i and 2i + 1 (interleaved) or i and i + pairs; mscale is a factor on sines and cosines.  q_out
+    (bf16) may be q itself.
+    """
+    call = (_BINDING or binding()).rope_append
+    k_descale, v_descale = _descales(k.device, stream, k_descale, v_descale)
+    if stream is None:
+        return call(q, k, v, positions, freqs, k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q,
+                    k_descale, v_descale, mscale, interleaved, q_out, status, None)
+    return _on_stream(call, (q, k, v, positions, freqs, k_cache, v_cache, block_tables, seq_lens,
+                             cu_seqlens_q, k_descale, v_descale, mscale, interleaved, q_out, status),
+                      stream, k.device)
+
+
+def mtp_rope_latent_append(q_rope: Optional[torch.Tensor], latent: torch.Tensor,
+                           k_rope: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+                           cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           cu_seqlens_q: torch.Tensor, descale, mscale: float = 1.0,
+                           interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None,
+                           stream=None) -> Optional[torch.Tensor]:
+    """New tokens into a latent cache (mtp_latent_attn_fwd reads it); returns q_out.
+
+    latent [total_q, 512] and k_rope [total_q, 64] (rotated on the way) become the 576 codes of a token
+    in cache [num_pages, 16, 576]; q_rope [total_q, H, 64] (None: no q) is rotated into q_out (bf16;
+    pass the last 64 elements of the attention's rows of 576, or q_rope itself).  All else as in
+    mtp_rope_append; freqs has 32 entries.
+    """
+    call = (_BINDING or binding()).rope_latent_append
+    descale, = _descales(latent.device, stream, descale)
+    if stream is None:
+        return call(q_rope, latent, k_rope, positions, freqs, cache, block_tables, seq_lens,
+                    cu_seqlens_q, descale, mscale, interleaved, q_out, status, None)
+    return _on_stream(call, (q_rope, latent, k_rope, positions, freqs, cache, block_tables, seq_lens,
+                             cu_seqlens_q, descale, mscale, interleaved, q_out, status), stream,
+                      latent.device)
+
+
+def mtp_rope_prefill(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                     positions: torch.Tensor, freqs: torch.Tensor, q_descale, k_descale, v_descale,
+                     mscale: float = 1.0, interleaved: bool = False,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     v_out: Optional[torch.Tensor] = None, stream=None):
+    """fmha_fwd_fp8_varlen's operands from the projections' outputs; returns (q, k, v) as e4m3 codes.
+
+    q [tokens, H_q, 192] (its last 64 elements are rotated), k [tokens, H_kv, 128], k_rope [tokens, 64]
+    (rotated, shared by all heads), v [tokens, H_kv, 128]: bfloat16, float16 or float32, all the same;
+    freqs has 32 entries.  The outputs are contiguous [tokens, H_q, 192], [tokens, H_kv, 192] and
+    [tokens, H_kv, 128].
+    """
+    call = (_BINDING or binding()).rope_prefill
+    q_descale, k_descale, v_descale = _descales(q.device, stream, q_descale, k_descale, v_descale)
+    if stream is None:
+        return call(q, k, k_rope, v, positions, freqs, q_descale, k_descale, v_descale, mscale,
+                    interleaved, q_out, k_out, v_out, None)
+    return _on_stream(call, (q, k, k_rope, v, positions, freqs, q_descale, k_descale, v_descale, mscale,
+                             interleaved, q_out, k_out, v_out), stream, q.device)
+
+
+# ---- latent attention (include/mtp_latent.h) ------------------------------------------------------
+
+LATENT_DIM, LATENT_ROPE_DIM, LATENT_MAX_HEADS = 512, 64, 128
+
+
+def mtp_latent_attn_workspace_size(num_seqs: int, total_q: int, num_heads: int,
+                                   max_pages_per_seq: int) -> int:
+    return int(lib().mtp_latent_attn_workspace_size(num_seqs, total_q, num_heads, max_pages_per_seq))
+
+
+def mtp_latent_attn_fwd(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Tensor,
+                        seq_lens: torch.Tensor, cu_seqlens_q: torch.Tensor, descale,
+                        softmax_scale: float, tree_mask: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of 1 to 64 new tokens a sequence over a paged cache of latent vectors, in the absorbed
+    form; returns ``out`` [total_q, H, 512] bf16.
+
+    q [total_q, H, 576] bf16, H to 128: a head's query in the latent space, then its rotated part (64);
+    cache [num_pages, 16, 576] uint8 or float8_e4m3fn codes, with ``descale``; tables, lengths and
+    cu_seqlens_q as in mtp_verify_attn_fwd.  Token i of a sequence's new ones (its last in the cache)
+    sees what is before them and the new ones up to itself, or those of its word of ``tree_mask``
+    [total_q] int64 (mtp_tree_mask).  ``workspace``: at least mtp_latent_attn_workspace_size(...) bytes,
+    kept by a decode loop so that no call allocates; it needs no initialisation.
+    """
+    call = (_BINDING or binding()).latent_attn
+    descale, = _descales(q.device, stream, descale)
+    if stream is None:
+        return call(q, cache, block_tables, seq_lens, cu_seqlens_q, descale, softmax_scale, tree_mask, out,
+                    workspace, status, None)
+    return _on_stream(call, (q, cache, block_tables, seq_lens, cu_seqlens_q, descale, softmax_scale,
+                             tree_mask, out, workspace, status), stream, q.device)

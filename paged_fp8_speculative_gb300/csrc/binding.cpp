@@ -1,5 +1,5 @@
-// The Python binding of the draft-tree and cache entry points (include/mtp_tree.h,
-// include/mtp_cache.h): argument checks, the outputs that were not given, and the call.  These calls
+// The Python binding of the draft-tree, cache, rotary and latent entry points (include/mtp_tree.h,
+// include/mtp_cache.h, include/mtp_rope.h, include/mtp_latent.h): argument checks, the outputs that were not given, and the call.  These calls
 // take 3 to 20 us on the GPU; the same steps in Python took 10 to 17 us of host time a call on a
 // Grace core (an attribute of a tensor 0.1 us, torch.empty 1.6 us, a call through ctypes 1.5 us).
 // Nothing is computed here.
@@ -21,6 +21,8 @@
 #include <string>
 
 #include "../../include/mtp_cache.h"
+#include "../../include/mtp_latent.h"
+#include "../../include/mtp_rope.h"
 #include "../../include/mtp_tree.h"
 
 namespace {
@@ -407,6 +409,241 @@ PyObject* cache_compact(PyObject* const* a) {
   return finish(rc, rc ? nullptr : THPVariable_Wrap(std::move(out)));
 }
 
+// ---- rotary positions and new tokens (include/mtp_rope.h) ----------------------------------------
+
+float number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw Refused{std::string(name) + " must be a number"};
+  }
+  return static_cast<float>(v);
+}
+int32_t truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw Refused{std::string(name) + " must be a truth value"};
+  }
+  return v;
+}
+const float* one_float(PyObject* o, const char* name) {
+  const at::Tensor& t = tensor(o, name);
+  REFUSE_IF(t.scalar_type() != at::kFloat || t.numel() != 1, std::string(name) + " must be a 1-element float32 tensor");
+  return static_cast<const float*>(t.const_data_ptr());
+}
+
+// [tokens, heads, dim], or without heads [tokens, dim] where dim alone is a row.  An axis of one element
+// has a stride that means nothing to torch: it gets one that the library takes.
+struct Rows {
+  const void* p;
+  int64_t tokens, tok, head;
+  int32_t heads;
+};
+Rows rows_of(const at::Tensor& t, const char* name, at::ScalarType type, int64_t tokens, int64_t dim, bool headed) {
+  const int64_t n = headed ? 3 : 2;
+  REFUSE_IF(t.scalar_type() != type || t.dim() != n || t.size(n - 1) != dim || (tokens >= 0 && t.size(0) != tokens) ||
+                t.stride(n - 1) != 1,
+            std::string(name) + " must be " + c10::toString(type) + (headed ? " [tokens, heads, " : " [tokens, ") +
+                std::to_string(dim) + "] with unit stride along the last axis, one row per token");
+  Rows r;
+  r.p = t.const_data_ptr();
+  r.tokens = t.size(0);
+  r.heads = headed ? count32(t.size(1), name) : 1;
+  r.head = headed && r.heads > 1 ? t.stride(1) : dim;
+  r.tok = r.tokens > 1 ? t.stride(0) : r.head * r.heads;
+  return r;
+}
+const int64_t* freqs_of(const at::Tensor& t, int64_t n) {
+  REFUSE_IF(t.scalar_type() != at::kLong || t.dim() != 1 || (n >= 0 && t.size(0) != n) || !t.is_contiguous(),
+            "freqs must be a contiguous int64 vector, one per rotated pair (mtp_rope_freqs makes it)");
+  return static_cast<const int64_t*>(t.const_data_ptr());
+}
+int32_t rope_dtype(const at::Tensor& t, const char* name) {
+  const int32_t d = dtype_of(t);
+  REFUSE_IF(d < 0, std::string(name) + " must be float32, bfloat16 or float16");
+  return d;
+}
+// Block tables, lengths and boundaries of the sequences that new tokens belong to.
+struct Places {
+  const int32_t *bt, *lens, *cu;
+  int32_t seqs, width;
+};
+Places places_of(PyObject* table_, PyObject* lens_, PyObject* cu_) {
+  const at::Tensor &table = tensor(table_, "block_tables"), &lens = tensor(lens_, "seq_lens");
+  const at::Tensor& cu = tensor(cu_, "cu_seqlens_q");
+  Places p;
+  p.seqs = sequences(cu);
+  vector(lens, "seq_lens", p.seqs);
+  REFUSE_IF(table.scalar_type() != at::kInt || table.dim() != 2 || table.size(0) != p.seqs || !table.is_contiguous(),
+            "block_tables must be a contiguous int32 [B, max_pages] tensor");
+  p.width = count32(table.size(1), "block_tables");
+  p.bt = ints(table);
+  p.lens = ints(lens);
+  p.cu = ints(cu);
+  return p;
+}
+const at::Tensor& latent_cache(PyObject* o) {
+  const at::Tensor& t = tensor(o, "cache");
+  REFUSE_IF(!is_codes(t.scalar_type()) || t.dim() != 3 || t.size(1) != MTPATTN_PAGE_SIZE || t.size(2) != MTP_LATENT_ROW ||
+                !t.is_contiguous(),
+            "cache must be contiguous uint8 or float8_e4m3fn codes [num_pages, 16, 576]");
+  return t;
+}
+at::Tensor rotated_out(PyObject* o, const at::Tensor& q, int64_t dim) {
+  if (given(o)) return tensor(o, "q_out");
+  return at::empty({q.size(0), q.size(1), dim}, q.options().dtype(at::kBFloat16));
+}
+
+// q, k, v, positions, freqs, k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q, k_descale, v_descale,
+// mscale, interleaved, q_out, status, stream
+PyObject* rope_append(PyObject* const* a) {
+  const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &positions = tensor(a[3], "positions");
+  const at::Tensor &kc = tensor(a[5], "k_cache"), &vc = tensor(a[6], "v_cache");
+  void* stream = stream_of(a[16], k);
+  const int32_t dtype = rope_dtype(k, "k");
+  const Rows kr = rows_of(k, "k", k.scalar_type(), -1, MTPATTN_HEAD_DIM, true);
+  const Rows vr = rows_of(v, "v", k.scalar_type(), kr.tokens, MTPATTN_HEAD_DIM, true);
+  REFUSE_IF(vr.heads != kr.heads, "k and v must have the same heads");
+  const int32_t total = count32(kr.tokens, "k");
+  vector(positions, "positions", total);
+  const int64_t* freqs = nullptr;
+  int32_t rot = 0;
+  if (given(a[4])) {
+    freqs = freqs_of(tensor(a[4], "freqs"), -1);
+    REFUSE_IF(tensor(a[4], "freqs").size(0) > MTPATTN_HEAD_DIM / 2, "freqs has more than 128 pairs");
+    rot = static_cast<int32_t>(2 * tensor(a[4], "freqs").size(0));
+  }
+  REFUSE_IF(!is_codes(kc.scalar_type()) || vc.scalar_type() != kc.scalar_type() || kc.dim() != 4 ||
+                kc.size(1) != MTPATTN_PAGE_SIZE || kc.size(2) != kr.heads || kc.size(3) != MTPATTN_HEAD_DIM ||
+                vc.sizes() != kc.sizes() || !kc.is_contiguous() || !vc.is_contiguous(),
+            "k_cache and v_cache must be contiguous uint8 or float8_e4m3fn codes [num_pages, 16, H_kv, 256], H_kv as in k");
+  const Places at_ = places_of(a[7], a[8], a[9]);
+  const float *kd = one_float(a[10], "k_descale"), *vd = one_float(a[11], "v_descale");
+  Rows qr{}, outr{};
+  at::Tensor out;
+  if (given(a[0])) {
+    const at::Tensor& q = tensor(a[0], "q");
+    qr = rows_of(q, "q", k.scalar_type(), total, MTPATTN_HEAD_DIM, true);
+    out = rotated_out(a[14], q, MTPATTN_HEAD_DIM);
+    outr = rows_of(out, "q_out", at::kBFloat16, total, MTPATTN_HEAD_DIM, true);
+    REFUSE_IF(outr.heads != qr.heads, "q_out must have q's heads");
+  } else {
+    REFUSE_IF(given(a[14]), "q_out without q");
+  }
+  const int rc = mtp_rope_append(qr.heads ? qr.p : nullptr, qr.tok, qr.head, kr.p, kr.tok, kr.head, vr.p, vr.tok, vr.head, dtype,
+                                 ints(positions), freqs, rot, truth(a[13], "interleaved"), number(a[12], "mscale"),
+                                 kc.data_ptr(), vc.data_ptr(), kc.size(0), at_.bt, at_.width, at_.lens, at_.cu, at_.seqs,
+                                 total, qr.heads, kr.heads, kd, vd, qr.heads ? out.data_ptr() : nullptr, outr.tok, outr.head,
+                                 status_of(a[15]), stream);
+  return finish(rc, rc ? nullptr : out.defined() ? THPVariable_Wrap(std::move(out)) : Py_NewRef(Py_None));
+}
+
+// q_rope, latent, k_rope, positions, freqs, cache, block_tables, seq_lens, cu_seqlens_q, descale, mscale,
+// interleaved, q_out, status, stream
+PyObject* rope_latent_append(PyObject* const* a) {
+  const at::Tensor &c = tensor(a[1], "latent"), &kr = tensor(a[2], "k_rope"), &positions = tensor(a[3], "positions");
+  void* stream = stream_of(a[14], c);
+  const int32_t dtype = rope_dtype(c, "latent");
+  const Rows cr = rows_of(c, "latent", c.scalar_type(), -1, MTP_LATENT_DIM, false);
+  const Rows rr = rows_of(kr, "k_rope", c.scalar_type(), cr.tokens, MTP_LATENT_ROPE_DIM, false);
+  const int32_t total = count32(cr.tokens, "latent");
+  vector(positions, "positions", total);
+  const int64_t* freqs = freqs_of(tensor(a[4], "freqs"), MTP_LATENT_ROPE_DIM / 2);
+  const at::Tensor& cache = latent_cache(a[5]);
+  const Places at_ = places_of(a[6], a[7], a[8]);
+  Rows qr{}, outr{};
+  at::Tensor out;
+  if (given(a[0])) {
+    const at::Tensor& q = tensor(a[0], "q_rope");
+    qr = rows_of(q, "q_rope", c.scalar_type(), total, MTP_LATENT_ROPE_DIM, true);
+    out = rotated_out(a[12], q, MTP_LATENT_ROPE_DIM);
+    outr = rows_of(out, "q_out", at::kBFloat16, total, MTP_LATENT_ROPE_DIM, true);
+    REFUSE_IF(outr.heads != qr.heads, "q_out must have q_rope's heads");
+  } else {
+    REFUSE_IF(given(a[12]), "q_out without q_rope");
+  }
+  const int rc = mtp_rope_latent_append(qr.heads ? qr.p : nullptr, qr.tok, qr.head, cr.p, cr.tok, rr.p, rr.tok, dtype,
+                                        ints(positions), freqs, truth(a[11], "interleaved"), number(a[10], "mscale"),
+                                        cache.data_ptr(), cache.size(0), at_.bt, at_.width, at_.lens, at_.cu, at_.seqs,
+                                        total, qr.heads, one_float(a[9], "descale"), qr.heads ? out.data_ptr() : nullptr,
+                                        outr.tok, outr.head, status_of(a[13]), stream);
+  return finish(rc, rc ? nullptr : out.defined() ? THPVariable_Wrap(std::move(out)) : Py_NewRef(Py_None));
+}
+
+at::Tensor codes_out(PyObject* o, const char* name, const at::Tensor& like, int64_t heads, int64_t dim) {
+  at::Tensor t = given(o) ? tensor(o, name) : at::empty({like.size(0), heads, dim}, like.options().dtype(at::kFloat8_e4m3fn));
+  REFUSE_IF(!is_codes(t.scalar_type()) || t.dim() != 3 || t.size(0) != like.size(0) || t.size(1) != heads ||
+                t.size(2) != dim || !t.is_contiguous(),
+            std::string(name) + " must be contiguous uint8 or float8_e4m3fn [tokens, heads, " + std::to_string(dim) + "]");
+  return t;
+}
+
+// q, k, k_rope, v, positions, freqs, q_descale, k_descale, v_descale, mscale, interleaved, q_out, k_out,
+// v_out, stream
+PyObject* rope_prefill(PyObject* const* a) {
+  constexpr int64_t kNope = 128, kQk = kNope + MTP_LATENT_ROPE_DIM, kV = 128;
+  const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &kr = tensor(a[2], "k_rope"), &v = tensor(a[3], "v");
+  const at::Tensor& positions = tensor(a[4], "positions");
+  void* stream = stream_of(a[14], q);
+  const int32_t dtype = rope_dtype(q, "q");
+  const Rows qr = rows_of(q, "q", q.scalar_type(), -1, kQk, true);
+  const Rows nr = rows_of(k, "k", q.scalar_type(), qr.tokens, kNope, true);
+  const Rows rr = rows_of(kr, "k_rope", q.scalar_type(), qr.tokens, MTP_LATENT_ROPE_DIM, false);
+  const Rows vr = rows_of(v, "v", q.scalar_type(), qr.tokens, kV, true);
+  REFUSE_IF(vr.heads != nr.heads, "k and v must have the same heads");
+  const int32_t total = count32(qr.tokens, "q");
+  vector(positions, "positions", total);
+  const int64_t* freqs = freqs_of(tensor(a[5], "freqs"), MTP_LATENT_ROPE_DIM / 2);
+  const float *qd = one_float(a[6], "q_descale"), *kd = one_float(a[7], "k_descale"), *vd = one_float(a[8], "v_descale");
+  const float mscale = number(a[9], "mscale");
+  const int32_t interleaved = truth(a[10], "interleaved");
+  at::Tensor q8 = codes_out(a[11], "q_out", q, qr.heads, kQk), k8 = codes_out(a[12], "k_out", q, nr.heads, kQk);
+  at::Tensor v8 = codes_out(a[13], "v_out", q, nr.heads, kV);
+  const int rc = mtp_rope_prefill(qr.p, qr.tok, qr.head, nr.p, nr.tok, nr.head, rr.p, rr.tok, vr.p, vr.tok, vr.head, dtype,
+                                  ints(positions), freqs, interleaved, mscale, total, qr.heads, nr.heads, qd, kd, vd,
+                                  q8.data_ptr(), k8.data_ptr(), v8.data_ptr(), stream);
+  if (rc) return finish(rc, nullptr);
+  PyObject* t = PyTuple_New(3);
+  if (!t) return nullptr;
+  PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(std::move(q8)));
+  PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(std::move(k8)));
+  PyTuple_SET_ITEM(t, 2, THPVariable_Wrap(std::move(v8)));
+  return t;
+}
+
+// ---- latent attention (include/mtp_latent.h) -----------------------------------------------------
+
+// q, cache, block_tables, seq_lens, cu_seqlens_q, descale, softmax_scale, tree_mask, out, workspace, status,
+// stream
+PyObject* latent_attn(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  void* stream = stream_of(a[11], q);
+  const Rows qr = rows_of(q, "q", at::kBFloat16, -1, MTP_LATENT_ROW, true);
+  const int32_t total = count32(qr.tokens, "q");
+  const at::Tensor& cache = latent_cache(a[1]);
+  const Places at_ = places_of(a[2], a[3], a[4]);
+  const float* descale = one_float(a[5], "descale");
+  const uint64_t* mask = nullptr;
+  if (given(a[7])) {
+    words(tensor(a[7], "tree_mask"), "tree_mask", total);
+    mask = static_cast<const uint64_t*>(tensor(a[7], "").const_data_ptr());
+  }
+  at::Tensor out = given(a[8]) ? tensor(a[8], "out") : at::empty({qr.tokens, qr.heads, MTP_LATENT_DIM}, q.options());
+  const Rows outr = rows_of(out, "out", at::kBFloat16, qr.tokens, MTP_LATENT_DIM, true);
+  REFUSE_IF(outr.heads != qr.heads, "out must have q's heads");
+  at::Tensor made;
+  const at::Tensor& ws = given(a[9]) ? tensor(a[9], "workspace") : made;
+  if (!ws.defined()) {
+    const size_t need = mtp_latent_attn_workspace_size(at_.seqs, total, qr.heads, at_.width);
+    made = at::empty({static_cast<int64_t>(need < 256 ? 256 : need)}, q.options().dtype(at::kByte));
+  }
+  const int rc = mtp_latent_attn_fwd(qr.p, qr.tok, qr.head, cache.const_data_ptr(), cache.size(0), at_.bt, at_.width, at_.lens,
+                                     at_.cu, mask, at_.seqs, total, qr.heads, descale, number(a[6], "softmax_scale"),
+                                     ws.data_ptr(), ws.nbytes(), out.data_ptr(), outr.tok, outr.head, status_of(a[10]), stream);
+  return finish(rc, rc ? nullptr : THPVariable_Wrap(std::move(out)));
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_XDECREF(g_error);
   g_error = Py_NewRef(cls);
@@ -419,6 +656,7 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 PyMethodDef kMethods[] = {
     ENTRY(tree_mask, 5),        ENTRY(tree_attn, 14),        ENTRY(verify_greedy, 10), ENTRY(verify_sample, 12),
     ENTRY(cache_resize, 9),     ENTRY(cache_fork, 10),       ENTRY(cache_copy_pages, 6), ENTRY(cache_compact, 10),
+    ENTRY(rope_append, 17),     ENTRY(rope_latent_append, 15), ENTRY(rope_prefill, 15), ENTRY(latent_attn, 12),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
