@@ -1,12 +1,53 @@
-// Latent attention over the paged cache (mtp_latent.h): the plain kernel.  A CTA has up to 8 heads of one
-// new token, and goes over the sequence's keys 32 at a time with a running maximum and sum, everything in
-// float32.
+// Latent attention over the paged cache (mtp_latent.h) on the sm_100-family tensor cores (tcgen05, TMA,
+// TMEM).
+//
+// The products are the other way round than usual: keys (and the values' dims) are the rows M = 128 of
+// a tcgen05.mma and the queries its columns,
+//   S^T [128 keys x rows] = C [128 x 576] Q^T,      O^T [512 dims x rows] = C[:, :512]^T P^T,
+// so that few query rows cost few columns, and all 512 dims of the output of up to 64 rows fit into half of
+// TMEM (the usual way 128 rows would take all of it, and P none).  A tile of 128 keys is read once, into
+// shared memory as TMA puts it, and is an operand of both products as it lies there: K-major for the first,
+// M-major (transposed) for the second.  Nothing is widened or copied.
+//
+// Work.  A sequence's query rows are its new tokens times the heads, row r being token r / heads, head
+// r % heads; a unit is up to N of them (16, 32 or 64) over all of the sequence's keys.  All units stand in a
+// line, a place for each tile of 128 keys and kUnitTiles ahead of them for the unit's Q and output; the line
+// is cut into equal pieces, one per CTA (worked out from seq_lens and cu_seqlens_q on the device, so a
+// captured call follows its buffers).  A unit that lies in one piece is written out at once; one that is cut
+// leaves its sums, references and outputs in the workspace (two slots a CTA: its first and its last unit),
+// and latent_join_kernel joins them, going by the notes that the CTAs with first tiles leave.
+//
+// Roles (384 threads): warp 0 walks over the CTA's piece and fetches tiles by TMA, a lane a page, in four
+// 128-byte columns and one of 64; warp 1 issues the products; warps 4-11 do the softmax: a warp has 32
+// keys (TMEM lanes) of half of the rows, makes Q's operand, and writes the output.
+//
+// Precision.  Codes enter as they are, Q as two e4m3 terms of x = q 2^a (a per row, max |x| in [128,
+// 256)): hi = e4m3(x), lo = e4m3(x - hi), as 2 N columns of one product, added in float32.  A bf16 value
+// has 8 significant bits and each term keeps 4, so x = hi + lo within 2^-9 of the row's largest, and
+// to 2^-17 of it below.  The weights p = 2^(s - ref), at most 2^8.75, are two e4m3 terms as well, of which
+// the smallest step is 2^-9: 2^-16 of the row's largest weight.  Plain rounding would drop all weights
+// below half of that, which many keys behind one large weight can be (30000 at 2^-19 are 5% of the sum);
+// so the second term is rounded with a dither, a number in (-1/2, 1/2) steps that goes through 128
+// evenly spread values over a tile's keys (their bits reversed): sums of small weights keep their size to
+// 2^-23, and the same bits come every time.  The sums of weights are of the unrounded ones, in float32.
+//
+// Online softmax in the log2 domain with a lazy reference: raised, and O rescaled in TMEM, only when a
+// logit exceeds it by more than kTau.  So a tile's maxima over keys (across lanes and warps, which this
+// orientation makes dear) are only needed where that happens.
+//
+// Masks.  A tile that reaches into the new tokens takes each row's word.  Places that no row sees in full
+// are kept out of the second product by value too, since 0 * NaN is NaN: rows behind the sequence are
+// stored as zeros, NaN codes of new tokens too (a row that sees one has a NaN logit, and its sum tells).
+//
+// Shared memory (N = 64): two stages of a tile (147456), Q's terms (73728), the second terms of P (8192;
+// the first ones take the place of the tile's 64-byte column, which only the first product reads).
+// TMEM: S double buffer at columns 0 and 128, O at 256, N columns for each 128 dims.
 #include "common.cuh"
 #include "host_checks.cuh"
+#include "sm100.cuh"
 
 #include "../../include/mtp_latent.h"
 
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
@@ -15,14 +56,48 @@
 namespace mtpattn {
 namespace {
 
+using namespace sm100;
+
 constexpr int kRow = MTP_LATENT_ROW, kDim = MTP_LATENT_DIM;
-constexpr int kPlainThreads = 128, kPlainRows = 8, kPlainKeys = 32;
-constexpr int kPlainSmem = (kPlainRows + kPlainKeys) * kRow * 4 + kPlainRows * kPlainKeys * 4;
+constexpr int kLatentThreads = 384;
+constexpr int kKeys = 128, kTilePages = kKeys / kPage;
+constexpr int kColumns = 4;                          // of 128 bytes; the fifth has 64
+constexpr int kColumn = kKeys * 128;                 // 16 KB
+constexpr int kRopeColumn = kKeys * MTP_LATENT_ROPE_DIM;
+constexpr int kStage = kColumns * kColumn + kRopeColumn;
+constexpr int kStages = 2;
+constexpr int kWarpSoft = 4, kSoftWarps = 8;
+constexpr int kSBuf = 128, kOCol = 256, kTmemCols = 512;
+constexpr int kSegRing = 4;
+constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at the reference, and at most
+                                                     // 2^(kShift + kTau) = 430 < 448
+constexpr float kNoRef = -1e30f;                     // no key seen yet
+constexpr int kUnitTiles = 2;
+constexpr int kMaxCtas = 160;
+constexpr uint32_t kBadSum = 0x7fd0bad1u;            // a sum of a sequence with a bad page (a NaN that no
+                                                     // arithmetic makes)
+
+template <int N>
+constexpr int q_column() { return 2 * N * 128; }     // 128 elements of all rows' two terms
+template <int N>
+constexpr int off_q() { return kStages * kStage; }
+template <int N>
+constexpr int off_p() { return off_q<N>() + 2 * N * kRow; }
+template <int N>
+constexpr int off_bars() { return off_p<N>() + kRopeColumn; }
+
+// What the join goes by: a unit's note, written by the CTA that has its first tile.
+struct JoinNote {
+  int pieces;                // it lies in; 1: written out whole
+  int first, first_slot;     // the first of them, and the unit's slot there (in the others, 0)
+  int q0, m, rows;           // its sequence's first row of tokens, row tile, valid rows
+  int pad[2];
+};
 
 struct LatentParams {
+  CUtensorMap tmap, tmap_rope;
   const __nv_bfloat16* q;
   int64_t q_stride_tok, q_stride_head;
-  const uint8_t* cache;
   int64_t num_pages;
   const int32_t* block_tables;
   int32_t max_pages;
@@ -35,109 +110,1048 @@ struct LatentParams {
   __nv_bfloat16* out;
   int64_t out_stride_tok, out_stride_head;
   int32_t* status;
+  int32_t ctas;
+  float* o_part;             // [ctas][2][N][512]
+  float2* sum_part;          // [ctas][2][N]: reference, sum
+  int32_t* units;            // for the join: their number
+  JoinNote* notes;
+  int32_t unit_bound;
 };
 
-__global__ void __launch_bounds__(kPlainThreads) latent_plain_kernel(const LatentParams p) {
-  extern __shared__ float smem[];
-  float* s_q = smem;                                    // [8][576]
-  float* s_k = s_q + kPlainRows * kRow;                 // [32][576]
-  float* s_p = s_k + kPlainKeys * kRow;                 // [8][32]
-  __shared__ float s_m[kPlainRows], s_l[kPlainRows], s_f[kPlainRows];
-  const int b = blockIdx.x, i = blockIdx.y, h0 = blockIdx.z * kPlainRows, tid = threadIdx.x;
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], n = q1 - q0, L = p.seq_lens[b];
-  if (q0 < 0 || q1 < q0 || q1 > p.total_q) {
-    if (tid == 0 && i == 0) set_status(p.status, MTPATTN_ERR_QLEN);
-    return;
+struct Segment {             // part of one unit: tiles t0 .. t1 - 1 of nt
+  int q0, n, L, b;
+  int m, t0, t1, nt;
+  int slot;                  // 0: the first of the CTA's piece
+  int end, bad;
+};
+
+struct Bars {
+  uint64_t full[kStages][kColumns], empty[kStages][kColumns];
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full, pv_done, q_full, final_mma;
+  uint64_t meet[3];          // the softmax warps of a row half, of both
+  uint64_t seg_full[kSegRing], seg_free[kSegRing];
+  Segment seg[kSegRing];
+  uint32_t tmem_base;
+  int32_t abort;
+};
+template <int N>
+struct Shared {
+  Bars bars;
+  alignas(16) float2 row[N];           // factor of the row's logits (log2 domain), reference - kShift
+  float f[N];                          // factor of a rescale; of the output
+  uint64_t word[N];                    // new tokens that the row sees
+  float xch[2][4][N / 2];              // row half, key quarter
+  uint8_t over[2][2][4];               // by turns; row half, key quarter
+};
+template <int N>
+constexpr int smem_bytes() { return off_bars<N>() + static_cast<int>(sizeof(Shared<N>)); }
+static_assert(smem_bytes<64>() <= 232448, "more than a block may have");
+
+// ---- the line of tiles ---------------------------------------------------------------------------
+
+// One sequence on the line: T units of nt tiles.  Rows whose place is not known (cu_seqlens_q out of order)
+// take no part; other errors cost one tile a unit.
+struct Seq {
+  int q0, n, L, T, nt, w, err;
+};
+template <int N>
+__device__ __forceinline__ Seq seq_at(const LatentParams& p, int b) {
+  Seq s;
+  s.q0 = s.n = s.L = s.T = s.nt = s.w = s.err = 0;
+  if (b >= p.num_seqs) return s;
+  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+  s.q0 = q0;
+  s.L = p.seq_lens[b];
+  if (q0 < 0 || q1 <= q0 || q1 > p.total_q) {
+    s.err = MTPATTN_ERR_QLEN;
+    return s;
   }
-  int err = 0;
-  if (n < 1 || n > MTP_LATENT_MAX_NODES) err = MTPATTN_ERR_QLEN;
-  else if (n > L) err = MTPATTN_ERR_QLEN_GT_SEQ;
-  else if (L > p.max_pages * kPage) err = MTPATTN_ERR_SEQ_TOO_LONG;
-  const int rows = min(kPlainRows, p.heads - h0);
-  const int32_t* bt = p.block_tables + static_cast<int64_t>(b) * p.max_pages;
-  if (!err) {
-    int bad = 0;
-    for (int j = tid; j < (L + kPage - 1) / kPage; j += kPlainThreads) bad |= bt[j] < 0 || bt[j] >= p.num_pages;
-    if (__syncthreads_or(bad)) err = MTPATTN_ERR_PAGE;
-  }
-  if (err) {
-    if (tid == 0) set_status(p.status, err);
-    for (int t = i; t < n; t += gridDim.y)
-      for (int r = 0; r < rows; ++r)
-        for (int d = tid; d < kDim; d += kPlainThreads)
-          p.out[(q0 + t) * p.out_stride_tok + (h0 + r) * p.out_stride_head + d] = __float2bfloat16(0.f);
-    return;
-  }
-  if (i >= n) return;
-  for (int x = tid; x < rows * kRow; x += kPlainThreads)
-    s_q[x] = __bfloat162float(p.q[(q0 + i) * p.q_stride_tok + (h0 + x / kRow) * p.q_stride_head + x % kRow]);
-  __syncthreads();
-  if (tid < kPlainRows) {
-    s_m[tid] = -INFINITY;
-    s_l[tid] = 0.f;
-    if (tid < rows)
-      for (int x = 0; x < kRow; ++x)
-        if (!isfinite(s_q[tid * kRow + x])) s_l[tid] = NAN;
-  }
-  const float scale = p.scale_log2 * *p.descale;
-  const uint64_t word = p.mask ? p.mask[q0 + i] : (2ull << i) - 1;
-  float o[kPlainRows][4] = {};
-  for (int j0 = 0; j0 < L; j0 += kPlainKeys) {
-    __syncthreads();
-    const int keys = min(kPlainKeys, L - j0);
-    for (int x = tid; x < kPlainKeys * kRow; x += kPlainThreads) {
-      const int j = j0 + x / kRow;
-      float v = 0.f;
-      if (j < L && (j < L - n || (word >> (j - L + n) & 1))) {
-        __nv_fp8_e4m3 c;
-        c.__x = p.cache[(static_cast<int64_t>(bt[j / kPage]) * kPage + j % kPage) * kRow + x % kRow];
-        v = static_cast<float>(c);
-      }
-      s_k[x] = v;
-    }
-    __syncthreads();
-    for (int x = tid; x < rows * kPlainKeys; x += kPlainThreads) {
-      const int r = x / kPlainKeys, k = x % kPlainKeys, j = j0 + k;
-      float s = -INFINITY;
-      if (k < keys && (j < L - n || (word >> (j - L + n) & 1))) {
-        s = 0.f;
-        for (int d = 0; d < kRow; ++d) s += s_q[r * kRow + d] * s_k[k * kRow + d];
-        s *= scale;
-      }
-      s_p[x] = s;
-    }
-    __syncthreads();
-    if (tid < rows) {
-      float top = s_m[tid], sum = 0.f;
-      for (int k = 0; k < kPlainKeys; ++k) top = fmaxf(top, s_p[tid * kPlainKeys + k]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      for (int k = 0; k < kPlainKeys; ++k) {
-        const float e = exp2f(s_p[tid * kPlainKeys + k] - ref);
-        s_p[tid * kPlainKeys + k] = e;
-        sum += e;
-      }
-      s_f[tid] = exp2f(s_m[tid] - ref);
-      s_l[tid] = s_l[tid] * s_f[tid] + sum;
-      s_m[tid] = top;
-    }
-    __syncthreads();
-    for (int r = 0; r < rows; ++r) {
-      const float f = s_f[r];
+  s.n = q1 - q0;
+  if (s.n > MTP_LATENT_MAX_NODES) s.err = MTPATTN_ERR_QLEN;
+  else if (s.n > s.L) s.err = MTPATTN_ERR_QLEN_GT_SEQ;
+  else if (s.L > p.max_pages * kPage) s.err = MTPATTN_ERR_SEQ_TOO_LONG;
+  s.T = static_cast<int>((static_cast<int64_t>(s.n) * p.heads + N - 1) / N);
+  s.nt = s.err ? 1 : (s.L + kKeys - 1) / kKeys;
+  s.w = s.T * (s.nt + kUnitTiles);
+  return s;
+}
+
+__device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float acc = o[r][c] * f;
-        for (int k = 0; k < kPlainKeys; ++k) acc += s_p[r * kPlainKeys + k] * s_k[k * kRow + c * 128 + tid];
-        o[r][c] = acc;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ int64_t warp_total(int64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A CTA's walk over the units of its piece, by one warp; 32 sequences are held, one a lane.
+template <int N>
+struct Walker {
+  int pos, hi, lo, C, length, units;
+  int b0, before, units_before;        // the held sequences; the line and the units before them
+  Seq mine;
+  int upto, units_upto;                // running sums of the held sequences' weights and units
+  int unit, unit0, unit_places;        // the last segment's unit: its number, and place on the line
+
+  __device__ __forceinline__ void start(const LatentParams& p, int lane) {
+    b0 = before = units_before = unit = unit0 = unit_places = 0;
+    mine = seq_at<N>(p, lane);
+    int64_t W = mine.w, rows = mine.n, U = mine.T;
+#pragma unroll 1
+    for (int b = 32; b < p.num_seqs; b += 32) {
+      const Seq x = seq_at<N>(p, b + lane);
+      W += x.w;
+      rows += x.n;
+      U += x.T;
+    }
+    W = warp_total(W);
+    rows = warp_total(rows);
+    U = warp_total(U);
+    // Sequences that claim the same rows again and again (cu_seqlens_q far out of order) could make the line
+    // longer than any call's is: then nothing is computed.
+    if (W > INT32_MAX || rows > 2ll * p.total_q) {
+      if (blockIdx.x == 0 && lane == 0) set_status(p.status, MTPATTN_ERR_QLEN);
+      W = U = 0;
+    }
+    length = static_cast<int>(W);
+    units = static_cast<int>(U);
+    C = max(1, static_cast<int>((W + p.ctas - 1) / p.ctas));
+    upto = warp_scan(mine.w, lane);
+    units_upto = warp_scan(mine.T, lane);
+    lo = pos = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(blockIdx.x) * C));
+    hi = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(lo) + C));
+  }
+  // The next segment; s.end if there is none.  Returns the sequence's error bits.
+  __device__ __forceinline__ int next(const LatentParams& p, int lane, Segment& s) {
+    s.end = 1;
+#pragma unroll 1
+    while (pos < hi) {
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+      if (pos >= before + all) {
+        before += all;
+        units_before += __shfl_sync(0xffffffffu, units_upto, 31);
+        b0 += 32;
+        if (b0 >= p.num_seqs) return 0;             // lengths changed under the call
+        mine = seq_at<N>(p, b0 + lane);
+        upto = warp_scan(mine.w, lane);
+        units_upto = warp_scan(mine.T, lane);
+        continue;
       }
+      const int at = pos - before;
+      const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+      const int nt = __shfl_sync(0xffffffffu, mine.nt, f);
+      const int places = nt + kUnitTiles;
+      const int in = at - (f ? __shfl_sync(0xffffffffu, upto, f - 1) : 0);
+      const int nth = in / places, in_unit = in - nth * places;
+      unit = units_before + nth + (f ? __shfl_sync(0xffffffffu, units_upto, f - 1) : 0);
+      unit0 = pos - in_unit;
+      unit_places = places;
+      const int to = min(places, in_unit + hi - pos);                // of the unit, in this piece
+      s.t0 = max(0, in_unit - kUnitTiles);
+      s.t1 = min(nt, to - kUnitTiles);
+      pos += to - in_unit;
+      if (s.t0 >= s.t1) continue;                   // none of its tiles
+      s.b = b0 + f;
+      s.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
+      s.n = __shfl_sync(0xffffffffu, mine.n, f);
+      s.L = __shfl_sync(0xffffffffu, mine.L, f);
+      s.m = nth;
+      s.nt = nt;
+      s.slot = unit0 <= lo ? 0 : 1;
+      s.end = s.bad = 0;
+      return __shfl_sync(0xffffffffu, mine.err, f);
+    }
+    return 0;
+  }
+  // What the join has to know of the last segment's unit.
+  __device__ __forceinline__ JoinNote note(const LatentParams& p, const Segment& s) const {
+    JoinNote n;
+    // (its first tile is at place kUnitTiles: the pieces are those of its tiles)
+    n.first = blockIdx.x;
+    n.pieces = (unit0 + unit_places - 1) / C - n.first + 1;
+    n.first_slot = s.slot;
+    n.q0 = s.q0;
+    n.m = s.m;
+    n.rows = min(N, s.n * p.heads - s.m * N);
+    n.pad[0] = n.pad[1] = 0;
+    return n;
+  }
+};
+
+// ---- arithmetic and operands ---------------------------------------------------------------------
+
+__device__ __forceinline__ float exp2_hw(float x) {   // 2^x, hardware approximation
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// The largest of the warp's 32 numbers; NaN is passed over.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two f16x2 words (four values, lowest first) as e4m3 codes hi + lo; `dither` is added to what lo is of.
+__device__ __forceinline__ void two_terms(uint32_t x0, uint32_t x1, uint32_t dither, uint32_t& hi, uint32_t& lo) {
+  asm("{\n"
+      " .reg .b16 h0, h1, l0, l1;\n"
+      " .reg .b32 g0, g1, y0, y1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h0, %2;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h1, %3;\n"
+      " cvt.rn.f16x2.e4m3x2 g0, h0;\n"
+      " cvt.rn.f16x2.e4m3x2 g1, h1;\n"
+      " sub.rn.f16x2 y0, %2, g0;\n"
+      " sub.rn.f16x2 y1, %3, g1;\n"
+      " add.rn.f16x2 y0, y0, %4;\n"
+      " add.rn.f16x2 y1, y1, %4;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l0, y0;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l1, y1;\n"
+      " mov.b32 %0, {h0, h1};\n"
+      " mov.b32 %1, {l0, l1};\n"
+      "}\n"
+      : "=r"(hi), "=r"(lo)
+      : "r"(x0), "r"(x1), "r"(dither));
+}
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {   // a in the low half
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+// A bf16 pair scaled by f, as an f16 pair: exact down to 2^-17 of a scaled value.
+__device__ __forceinline__ uint32_t scaled_half2(uint32_t w, float f) {
+  return half2_of(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+}
+
+// n columns of a lane each, n 8, 16 or 32.
+template <int n>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[n]) {
+  if constexpr (n == 32) {
+    tmem_ld32(addr, v);
+  } else if constexpr (n == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+  } else {
+    static_assert(n == 8);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr));
+  }
+}
+// Waits for the loads above; the registers go through it, so that none is used before.
+template <int n>
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[n]) {
+  if constexpr (n == 32) {
+    tmem_ld_wait(v);
+  } else if constexpr (n == 16) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+                 :
+                 : "memory");
+  }
+}
+template <int n>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[n]) {
+  if constexpr (n == 32) {
+    tmem_st32(addr, v);
+  } else if constexpr (n == 16) {
+    tmem_st16(addr, v);
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(addr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  }
+}
+
+// Descriptors of a 64-byte-swizzled operand (as sdesc_sw128, layout 4): 8-row groups `sbo` apart.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (4ull << 61);
+}
+constexpr uint32_t kAMajorM = 1u << 15;              // instruction descriptor: A is M-major
+
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int page,
+                                         uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(page), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void st_shared8(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// Codes with the NaN ones (0x7f, 0xff) as zeros.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+  return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// Sums over the warp's lanes of n numbers: lane r gets that of v[r % n].
+template <int n>
+__device__ __forceinline__ float row_sums(float (&v)[n], int lane) {
+#pragma unroll
+  for (int o = n / 2; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+#pragma unroll
+  for (int o = n; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+static_assert(kWaitCycles < (1ll << 32), "32-bit clock");
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (static_cast<uint32_t>(clock()) - t0 > static_cast<uint32_t>(kWaitCycles)) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
+}
+
+// Warps that meet, with a limit (a named barrier has none): false after an abort.
+struct Meeting {
+  uint32_t bar;
+  uint32_t turns;
+  __device__ __forceinline__ bool operator()(int lane, volatile int* abort) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    return warp_wait(bar, turns++ & 1, abort);
+  }
+};
+
+// ---- the kernel ----------------------------------------------------------------------------------
+
+template <int N>
+__global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __grid_constant__ LatentParams p) {
+  extern __shared__ __align__(1024) unsigned char base[];
+  if (smem_u32(base) & 1023) {                     // the operands' swizzle needs it; no kernel sets
+    if (threadIdx.x == 0) set_status(p.status, MTPATTN_ERR_TIMEOUT);   // other shared memory aside
+    return;
+  }
+  constexpr int kHalf = N / 2;                     // rows of a softmax warp
+  Shared<N>& sh = *reinterpret_cast<Shared<N>*>(base + off_bars<N>());
+  Bars& bars = sh.bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &bars.abort;
+  const uint32_t smem = smem_u32(base);
+
+  // ---- set-up ------------------------------------------------------------------------------
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i)
+      for (int c = 0; c < kColumns; ++c) {
+        mbar_init(smem_u32(&bars.full[i][c]), 1);
+        mbar_init(smem_u32(&bars.empty[i][c]), 1);
+      }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.s_full[i]), 1);
+      mbar_init(smem_u32(&bars.s_free[i]), kSoftWarps);
+    }
+    mbar_init(smem_u32(&bars.p_full), kSoftWarps);
+    mbar_init(smem_u32(&bars.pv_done), 1);
+    mbar_init(smem_u32(&bars.q_full), kSoftWarps);
+    mbar_init(smem_u32(&bars.final_mma), 1);
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&bars.meet[i]), i < 2 ? kSoftWarps / 2 : kSoftWarps);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(smem_u32(&bars.seg_full[i]), 1);
+      mbar_init(smem_u32(&bars.seg_free[i]), kSoftWarps + 1);
+    }
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  // A programmatic dependent of the previous work on the stream: nothing global was touched so far; and
+  // the join may be scheduled (it waits for this grid before it reads partials).
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+  if (warp == 0) {
+    // ============================== the walk, and the tiles by TMA ================================
+    if (lane == 0) {
+      prefetch_tmap(&p.tmap);
+      prefetch_tmap(&p.tmap_rope);
+    }
+    if (blockIdx.x == 0)                           // tell of sequences whose rows are not known
+      for (int b = lane; b < p.num_seqs; b += 32) {
+        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+        if (q0 < 0 || q1 <= q0 || q1 > p.total_q) set_status(p.status, MTPATTN_ERR_QLEN);
+      }
+    __syncwarp();
+    Walker<N> walk;
+    walk.start(p, lane);
+    if (blockIdx.x == 0 && lane == 0) *p.units = min(walk.units, p.unit_bound);
+    const uint64_t once = l2_policy_evict_first();
+    uint64_t again;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
+    uint32_t u = 0;                                // tiles so far
+    int e = 0, columns = 0;                        // segments; columns of the last tile asked for
+    bool ok = true;
+#pragma unroll 1
+    while (ok) {
+      Segment s;
+      const int err = walk.next(p, lane, s);
+      if (!s.end && lane == 0 && s.t0 == 0 && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
+      if (!s.end && err) {
+        // zeros for the rows of a sequence that cannot be computed, here: it has no tiles
+        if (lane == 0) set_status(p.status, err);
+        const int rows = min(N, s.n * p.heads - s.m * N);
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i) {
+          const int rr = s.m * N + i, t = rr / p.heads;
+          uint4* out = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.q0 + t) * p.out_stride_tok +
+                                                static_cast<int64_t>(rr - t * p.heads) * p.out_stride_head);
+          out[lane] = out[lane + 32] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      ok = warp_wait(smem_u32(&bars.seg_free[e % kSegRing]), ((e / kSegRing) & 1) ^ 1, abort_flag);
+      if (!ok) break;
+      if (lane == 0) {
+        bars.seg[e % kSegRing] = s;
+        mbar_arrive(smem_u32(&bars.seg_full[e % kSegRing]));
+      }
+      if (s.end) break;
+      const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
+      const uint64_t policy = static_cast<int64_t>(s.n) * p.heads <= N ? once : again;
+      const int pages = (s.L + kPage - 1) / kPage;
+      // table entries, a lane one of four tiles' 32, with the next 32 on the way
+      auto entries = [&](int t) -> int {
+        const int64_t pg = static_cast<int64_t>(t) * kTilePages + lane;
+        return pg < pages ? bt[pg] : 0;
+      };
+      int now = entries(s.t0), ahead = entries(s.t0 + 4);
+#pragma unroll 1
+      for (int t = s.t0; t < s.t1 && ok; ++t, ++u) {
+        const int k = (t - s.t0) & 3;
+        if (k == 0 && t > s.t0) {
+          now = ahead;
+          ahead = entries(t + 4);
+        }
+        const int page = __shfl_sync(0xffffffffu, now, k * kTilePages + (lane & 7));
+        const int np = min(kTilePages, pages - t * kTilePages);
+        const bool bad = __any_sync(0xffffffffu, lane < np && (page < 0 || page >= p.num_pages));
+        if (bad && lane == 0) {
+          *const_cast<volatile int*>(&bars.seg[e % kSegRing].bad) = 1;
+          set_status(p.status, MTPATTN_ERR_PAGE);
+        }
+        const int st = u % kStages;
+        const uint32_t parity = ((u / kStages) & 1) ^ 1;
+        const uint32_t stage = smem + st * kStage;
+#pragma unroll 1
+        for (int c = 0; c < kColumns; ++c) {
+          ok = warp_wait(smem_u32(&bars.empty[st][c]), parity, abort_flag);
+          if (!ok) break;
+          columns = c + 1;
+          const uint32_t bar = smem_u32(&bars.full[st][c]);
+          const bool last = c == kColumns - 1;
+          if (lane == 0) {
+            if (bad) mbar_arrive(bar);             // nothing is fetched: the segment's rows become zeros
+            else mbar_arrive_expect_tx(bar, np * kPage * (128 + (last ? MTP_LATENT_ROPE_DIM : 0)));
+          }
+          __syncwarp();
+          if (!bad && lane < np) {
+            tma_page(stage + c * kColumn + lane * (kPage * 128), &p.tmap, bar, c * 128, page, policy);
+            if (last)
+              tma_page(stage + kColumns * kColumn + lane * (kPage * MTP_LATENT_ROPE_DIM), &p.tmap_rope, bar, kDim, page,
+                       policy);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      ++e;
+    }
+    // What was asked for has to arrive before the block may end: u tiles whole, and columns of one more
+    // after an abort.
+    volatile int no_abort = 0;
+    if (!ok && columns < kColumns)
+      for (int c = 0; c < columns; ++c) wait_for(smem_u32(&bars.full[u % kStages][c]), (u / kStages) & 1, &no_abort);
+    for (uint32_t k = 1; k <= kStages && k <= u; ++k)
+      for (int c = 0; c < kColumns; ++c)
+        if (*abort_flag) wait_for(smem_u32(&bars.full[(u - k) % kStages][c]), ((u - k) / kStages) & 1, &no_abort);
+  } else if (warp == 1) {
+    // ============================== the products ==================================================
+    if (elect_one()) {
+      auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_for(smem_u32(&bar), parity, abort_flag); };
+      constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 2 * N, false);
+      constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true) | kAMajorM;
+      const uint32_t q = smem + off_q<N>();
+      uint32_t u = 0;
+      bool alive = true;
+      auto scores = [&](uint32_t v) -> bool {      // S(v) = C Q^T
+        const uint32_t st = v % kStages, stage = smem + st * kStage, d = tmem + (v & 1) * kSBuf;
+        if (!wait(bars.s_free[v & 1], ((v >> 1) & 1) ^ 1)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < kColumns; ++c) {
+          if (!wait(bars.full[st][c], (v / kStages) & 1)) return false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f8_ss(d, sdesc_sw128(stage + c * kColumn + 32 * k, 16, 1024),
+                      sdesc_sw128(q + c * q_column<N>() + 32 * k, 16, 1024), kIdescS, c | k);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          mma_f8_ss(d, sdesc_sw64(stage + kColumns * kColumn + 32 * k, 16, 512),
+                    sdesc_sw64(q + kColumns * q_column<N>() + 32 * k, 16, 512), kIdescS, 1);
+        mma_commit(smem_u32(&bars.s_full[v & 1]));
+        return true;
+      };
+      auto outputs = [&](uint32_t v, bool first) -> bool {   // O += C^T P^T
+        const uint32_t st = v % kStages, stage = smem + st * kStage;
+        if (!wait(bars.p_full, v & 1)) return false;
+        tc_fence_after();
+        const uint32_t hi = stage + kColumns * kColumn, lo = smem + off_p<N>();
+#pragma unroll 1
+        for (int c = 0; c < kColumns; ++c) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 32; ++k) {
+            const uint64_t a = sdesc_sw128(stage + c * kColumn + k * (32 * 128), kColumn, 1024);
+            mma_f8_ss(tmem + kOCol + c * N, a, sdesc_sw64(hi + k * (32 * 64), 512, 512), kIdescO, !first || k);
+            mma_f8_ss(tmem + kOCol + c * N, a, sdesc_sw64(lo + k * (32 * 64), 512, 512), kIdescO, 1);
+          }
+          // (the last column's barrier also stands for the 64-byte one, where P's first terms lie)
+          mma_commit(smem_u32(&bars.empty[st][c]));
+        }
+        mma_commit(smem_u32(&bars.pv_done));
+        return true;
+      };
+#pragma unroll 1
+      for (int e = 0; alive; ++e) {
+        if (!(alive = wait(bars.seg_full[e % kSegRing], (e / kSegRing) & 1))) break;
+        const volatile Segment& s = bars.seg[e % kSegRing];
+        const bool end = s.end;
+        const int tiles = s.t1 - s.t0;
+        mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
+        if (end) break;
+        if (!(alive = wait(bars.q_full, e & 1))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i <= tiles && alive; ++i) {
+          if (i < tiles) alive = scores(u + i);
+          if (alive && i > 0) alive = outputs(u + i - 1, i == 1);
+        }
+        u += tiles;
+      }
+      mma_commit(smem_u32(&bars.final_mma));       // no product may run on when the block ends
+      volatile int no_abort = 0;
+      wait_for(smem_u32(&bars.final_mma), 0, &no_abort);
+    }
+  } else if (warp >= kWarpSoft) {
+    // ============================== softmax, Q's operand, the output ==============================
+    const int w = warp - kWarpSoft, quarter = warp & 3, half = w >> 2;
+    const int key = quarter * 32 + lane;             // of the tile
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t dither_h = half2_of((static_cast<float>(__brev(key) >> 25) - 63.5f) * 0x1p-16f, 0.f) & 0xffffu;
+    const uint32_t dither = dither_h | dither_h << 16;
+    const float descale = *p.descale, factor = p.scale_log2 * descale;
+    const int row0 = half * kHalf;
+    Meeting meet{smem_u32(&bars.meet[half]), 0}, meet_all{smem_u32(&bars.meet[2]), 0};
+    uint32_t u = 0;
+    bool alive = true;
+#pragma unroll 1
+    for (int e = 0; alive; ++e) {
+      if (!warp_wait(smem_u32(&bars.seg_full[e % kSegRing]), (e / kSegRing) & 1, abort_flag)) break;
+      const Segment s = bars.seg[e % kSegRing];
+      if (s.end) break;
+      // ---- Q's two terms: a warp a row.  (The last product that reads the previous ones is done: its S
+      // has been read.)
+      const int rows = min(N, s.n * p.heads - s.m * N);
+      constexpr int kBatch = N / kSoftWarps < 4 ? N / kSoftWarps : 4;   // rows in flight
+#pragma unroll 1
+      for (int r0 = w; r0 < N; r0 += kBatch * kSoftWarps) {
+        uint4 x[kBatch][3];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = r0 + k * kSoftWarps, rr = s.m * N + r, tok = r < rows ? rr / p.heads : 0;
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(s.q0 + tok) * p.q_stride_tok +
+                                                            static_cast<int64_t>(rr - tok * p.heads) * p.q_stride_head);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            x[k][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows && lane + 32 * i < kRow / 8) x[k][i] = src[lane + 32 * i];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = r0 + k * kSoftWarps;
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[k][i].x & 0x7fff7fffu, x[k][i].y & 0x7fff7fffu),
+                                         __vmaxu2(x[k][i].z & 0x7fff7fffu, x[k][i].w & 0x7fff7fffu)));
+          const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+          const int exponent = most >> 7;            // biased; 255: not finite
+          const int a = min(134 - exponent, 126);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int j = lane + 32 * i;             // 8 elements
+            if (j >= kRow / 8) continue;
+            uint32_t h0, h1, l0, l1;
+            two_terms(scaled_half2(x[k][i].x, up), scaled_half2(x[k][i].y, up), 0u, h0, l0);
+            two_terms(scaled_half2(x[k][i].z, up), scaled_half2(x[k][i].w, up), 0u, h1, l1);
+            if (exponent == 255) h0 = h1 = l0 = l1 = 0x7f7f7f7fu;
+            uint32_t at = smem + off_q<N>(), low;
+            if (j < kDim / 8) {                      // 16 blocks a column's row, swizzled in pairs
+              const uint32_t b = j & 15;
+              at += (j >> 4) * q_column<N>() + r * 128 + (((b >> 1) ^ (r & 7)) << 4) + (b & 1) * 8;
+              low = at + N * 128;
+            } else {
+              const uint32_t b = j - kDim / 8;
+              at += kColumns * q_column<N>() + r * 64 + (((b >> 1) ^ ((r >> 1) & 3)) << 4) + (b & 1) * 8;
+              low = at + N * 64;
+            }
+            st_shared8(at, h0, h1);
+            st_shared8(low, l0, l1);
+          }
+          if (lane == 0) {
+            const int tok = r < rows ? (s.m * N + r) / p.heads : 0;
+            sh.row[r] = make_float2(r < rows ? factor * __uint_as_float(static_cast<uint32_t>(127 - a) << 23) : 0.f, kNoRef);
+            uint64_t word = 0;
+            if (r < rows) word = p.mask ? p.mask[s.q0 + tok] : (2ull << tok) - 1ull;
+            if (s.n < 64) word &= (1ull << s.n) - 1ull;
+            sh.word[r] = word;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+      if (!(alive = meet_all(lane, abort_flag))) break;   // every row's factor and word
+
+      float l[kHalf];
+#pragma unroll
+      for (int r = 0; r < kHalf; ++r) l[r] = 0.f;
+      const int start = s.L - s.n;                   // first new token
+#pragma unroll 1
+      for (int t = s.t0; t < s.t1; ++t, ++u) {
+        if (!(alive = warp_wait(smem_u32(&bars.s_full[u & 1]), (u >> 1) & 1, abort_flag))) break;
+        tc_fence_after();
+        float y[kHalf];
+        {
+          uint32_t h[kHalf], lo[kHalf];
+          const uint32_t at = tmem + lanes + (u & 1) * kSBuf + row0;
+          tmem_ld<kHalf>(at, h);
+          tmem_ld<kHalf>(at + N, lo);
+          tmem_wait<kHalf>(h);
+          tmem_wait<kHalf>(lo);
+#pragma unroll
+          for (int r = 0; r < kHalf; ++r) y[r] = __uint_as_float(h[r]) + __uint_as_float(lo[r]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.s_free[u & 1]));
+        bool over = t == s.t0;
+        const int j = t * kKeys + key;
+        const bool ragged = (t + 1) * kKeys > start;  // new tokens, or places behind the sequence
+#pragma unroll
+        for (int r = 0; r < kHalf; ++r) y[r] *= sh.row[row0 + r].x;
+        if (ragged && j >= start) {
+#pragma unroll
+          for (int r = 0; r < kHalf; ++r)
+            if (j >= s.L || !((sh.word[row0 + r] >> (j - start)) & 1)) y[r] = -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < kHalf; ++r) over |= y[r] - sh.row[row0 + r].y > kShift + kTau;
+        {
+          uint8_t (&all)[4] = sh.over[meet.turns & 1][half];
+          over = __any_sync(0xffffffffu, over);
+          if (lane == 0) all[quarter] = over;
+          if (!(alive = meet(lane, abort_flag))) break;
+          over = *reinterpret_cast<volatile uint32_t*>(all) != 0;
+        }
+        // the previous tile's products are in O, and P may be written
+        if (u > 0 && !(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
+        if (over) {
+          float mine = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < kHalf; ++r) {
+            const float top = warp_max(y[r]);
+            if (lane == r) mine = top;
+          }
+          if (lane < kHalf) sh.xch[half][quarter][lane] = mine;
+          if (!(alive = meet(lane, abort_flag))) break;
+          if (quarter == 0 && lane < kHalf) {
+            const float (&x)[4][kHalf] = sh.xch[half];
+            const float top = fmaxf(fmaxf(x[0][lane], x[1][lane]), fmaxf(x[2][lane], x[3][lane])) - kShift;
+            const float ref = sh.row[row0 + lane].y;
+            const bool raise = top > (ref == kNoRef ? ref : ref + kTau);
+            sh.f[row0 + lane] = raise ? exp2_hw(ref - top) : 1.f;
+            if (raise) sh.row[row0 + lane].y = top;
+          }
+          if (!(alive = meet(lane, abort_flag))) break;
+          if (t > s.t0) {
+            tc_fence_after();
+#pragma unroll
+            for (int r = 0; r < kHalf; ++r) l[r] *= sh.f[row0 + r];
+#pragma unroll 1
+            for (int c = 0; c < kColumns; ++c) {
+              const uint32_t at = tmem + lanes + kOCol + c * N + row0;
+              uint32_t o[kHalf];
+              tmem_ld<kHalf>(at, o);
+              tmem_wait<kHalf>(o);
+#pragma unroll
+              for (int r = 0; r < kHalf; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.f[row0 + r]);
+              tmem_st<kHalf>(at, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        // ---- the weights, and their two terms
+        uint32_t hi[kHalf / 4], lo[kHalf / 4];
+#pragma unroll
+        for (int r = 0; r < kHalf; r += 4) {
+          float w4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w4[i] = exp2_hw(y[r + i] - sh.row[row0 + r + i].y);
+            l[r + i] += w4[i];
+          }
+          two_terms(half2_of(w4[0], w4[1]), half2_of(w4[2], w4[3]), dither, hi[r / 4], lo[r / 4]);
+        }
+        const uint32_t stage = smem + (u % kStages) * kStage;
+        const uint32_t swz = (key >> 1) & 3;
+        const uint32_t at_hi = stage + kColumns * kColumn + key * 64, at_lo = smem + off_p<N>() + key * 64;
+        if constexpr (kHalf == 8) {
+          const uint32_t off = (swz << 4) + half * 8;
+          st_shared8(at_hi + off, hi[0], hi[1]);
+          st_shared8(at_lo + off, lo[0], lo[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kHalf / 16; ++i) {
+            const uint32_t off = ((half * (kHalf / 16) + i) ^ swz) << 4;
+            st_shared16(at_hi + off, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+            st_shared16(at_lo + off, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          }
+        }
+        if (ragged && j >= start) {
+          // this half's 256 of the key's values: none behind the sequence, no NaN among the new tokens
+#pragma unroll 1
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t at = stage + (2 * half + (i >> 3)) * kColumn + key * 128 +
+                                (((i + key) & 7) << 4);   // (any order; this one meets all banks)
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (j < s.L) {
+              x = ld_shared16(at);
+              x.x = without_nan(x.x);
+              x.y = without_nan(x.y);
+              x.z = without_nan(x.z);
+              x.w = without_nan(x.w);
+            }
+            st_shared16(at, x.x, x.y, x.z, x.w);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full));
+      }
+      if (!alive) break;
+      // ---- the output
+      if (!(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      const bool bad = *const_cast<volatile int*>(&bars.seg[e % kSegRing].bad);
+      const bool whole = s.t0 == 0 && s.t1 == s.nt;
+      const int64_t slot = 2 * blockIdx.x + s.slot;
+      {
+        const float sum = row_sums<kHalf>(l, lane);
+        if (lane < kHalf) sh.xch[half][quarter][lane] = sum;
+      }
+      if (!(alive = meet(lane, abort_flag))) break;
+      if (quarter == 0 && lane < kHalf) {
+        const float (&x)[4][kHalf] = sh.xch[half];
+        const float sum = (x[0][lane] + x[1][lane]) + (x[2][lane] + x[3][lane]);
+        sh.f[row0 + lane] = bad || sum == 0.f ? 0.f : descale / sum;   // (NaN: the row sees one, or holds one)
+        if (!whole)
+          p.sum_part[slot * N + row0 + lane] =
+              make_float2(sh.row[row0 + lane].y, bad ? __uint_as_float(kBadSum) : sum);
+        // the words have served: where the row goes
+        const int rr = s.m * N + row0 + lane, tok = rr / p.heads;
+        sh.word[row0 + lane] = static_cast<uint64_t>(static_cast<int64_t>(s.q0 + tok) * p.out_stride_tok +
+                                                     static_cast<int64_t>(rr - tok * p.heads) * p.out_stride_head);
+      }
+      if (!(alive = meet(lane, abort_flag))) break;
+      const int valid = min(kHalf, rows - row0);     // of this half's
+#pragma unroll 1
+      for (int c = 0; c < kColumns; ++c) {
+        uint32_t o[kHalf];
+        tmem_ld<kHalf>(tmem + lanes + kOCol + c * N + row0, o);
+        tmem_wait<kHalf>(o);
+        const int d = c * 128 + key;                 // (a TMEM lane is a dim here)
+        if (whole) {
+#pragma unroll
+          for (int r = 0; r < kHalf; ++r)
+            if (r < valid) {
+              const float f = sh.f[row0 + r];
+              p.out[static_cast<int64_t>(sh.word[row0 + r]) + d] =
+                  __float2bfloat16(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
+            }
+        } else {
+#pragma unroll
+          for (int r = 0; r < kHalf; ++r)
+            if (r < valid) p.o_part[(slot * N + row0 + r) * kDim + d] = __uint_as_float(o[r]);
+        }
+      }
+      tc_fence_before();
+      // every softmax warp is done with this segment's row data before the next one's are written
+      if (!(alive = meet_all(lane, abort_flag))) break;
+      if (lane == 0) mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
     }
   }
+
+  // ---- teardown ------------------------------------------------------------------------------
+  __syncwarp();
+  tc_fence_before();
   __syncthreads();
-  for (int r = 0; r < rows; ++r) {
-    const float l = s_l[r], w = l == 0.f ? 0.f : *p.descale / l;
-    for (int c = 0; c < 4; ++c)
-      p.out[(q0 + i) * p.out_stride_tok + (h0 + r) * p.out_stride_head + c * 128 + tid] =
-          __float2bfloat16(l == 0.f ? 0.f : o[r][c] * w);
+  if (*abort_flag && tid == 0) set_status(p.status, MTPATTN_ERR_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// The join: out = descale sum_j w_j O_j / sum_j w_j l_j over a unit's pieces, w_j = 2^(ref_j - max ref).
+// A CTA takes kRows rows of a unit, a thread four dims of one at a time, the pieces shared out over kGroups
+// groups of 128 threads.  Reads what the main kernel has just written, out of L2.
+constexpr int kJoinThreads = 256;
+
+template <int N, int kRows, int kGroups>
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentParams p) {
+  static_assert(kRows * kGroups * 128 % kJoinThreads == 0);
+  constexpr int kAhead = 8;
+  __shared__ float s_w[kRows][kMaxCtas];
+  __shared__ float s_inv[kRows];
+  __shared__ float4 s_acc[kGroups > 1 ? kGroups - 1 : 1][128];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
+  const int units = __ldcg(p.units);
+  const int4 a = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x));
+  const int4 b = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x) + 1);
+  if (static_cast<int>(blockIdx.x) >= units || a.x <= 1) return;
+  const int n = a.x, first = a.y, q0 = a.w, m = b.x;
+  const int r0 = blockIdx.y * kRows, rows = min(kRows, b.y - r0);
+  // A CTA whose wait ran out may have left no note: what stands there then is not followed.
+  if (n > p.ctas || first < 0 || first > p.ctas - n || (a.z & ~1) || q0 < 0 || m < 0 ||
+      m >= MTP_LATENT_MAX_NODES * MTP_LATENT_MAX_HEADS / N || b.y <= 0 || b.y > N ||
+      q0 > p.total_q - 1 - (m * N + b.y - 1) / p.heads)
+    return;
+  if (rows <= 0) return;
+  auto slot_of = [&](int i) -> int64_t { return 2 * (first + i) + (i == 0 ? a.z : 0); };
+  // ---- the pieces' weights: a warp a row
+#pragma unroll 1
+  for (int r = warp; r < rows; r += kJoinThreads / 32) {
+    float ref[kMaxCtas / 32], sum[kMaxCtas / 32], top = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kMaxCtas / 32; ++k) {
+      const int i = lane + 32 * k;
+      float2 x = make_float2(kNoRef, 0.f);
+      if (i < n) x = __ldcg(p.sum_part + slot_of(i) * N + r0 + r);
+      ref[k] = x.x;
+      sum[k] = x.y;
+      bad |= __float_as_uint(x.y) == kBadSum;
+      top = fmaxf(top, x.x);
+    }
+    top = warp_max(top);
+    bad = __any_sync(0xffffffffu, bad);
+    float total = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxCtas / 32; ++k) {
+      const int i = lane + 32 * k;
+      if (i >= n) continue;
+      const float w = exp2_hw(ref[k] - top);
+      s_w[r][i] = w;
+      total += w * sum[k];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_inv[r] = bad || total == 0.f ? 0.f : *p.descale / total;
+  }
+  __syncthreads();
+  // ---- their sum
+  const int d4 = tid & 127, g = kGroups > 1 ? tid >> 7 : 0;
+#pragma unroll 1
+  for (int r = kGroups > 1 ? 0 : tid >> 7; r < rows; r += kGroups > 1 ? 1 : 2) {
+    const float4* src = reinterpret_cast<const float4*>(p.o_part) + (r0 + r) * (kDim / 4) + d4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = g; i0 < n; i0 += kAhead * kGroups) {
+      float4 x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j * kGroups < n) x[j] = __ldcg(src + slot_of(i0 + j * kGroups) * (N * kDim / 4));
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + j * kGroups < n) {
+          const float w = s_w[r][i0 + j * kGroups];
+          acc.x = fmaf(w, x[j].x, acc.x);
+          acc.y = fmaf(w, x[j].y, acc.y);
+          acc.z = fmaf(w, x[j].z, acc.z);
+          acc.w = fmaf(w, x[j].w, acc.w);
+        }
+    }
+    if constexpr (kGroups > 1) {
+      if (g > 0) s_acc[g - 1][d4] = acc;
+      __syncthreads();
+      if (g > 0) continue;
+#pragma unroll
+      for (int o = 0; o < kGroups - 1; ++o) {
+        const float4 x = s_acc[o][d4];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+    }
+    const float inv = s_inv[r];
+    if (inv == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    const int rr = m * N + r0 + r, tok = rr / p.heads;
+    reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q0 + tok) * p.out_stride_tok +
+                             static_cast<int64_t>(rr - tok * p.heads) * p.out_stride_head)[d4] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+
+// Rows of a unit: as many columns of the products as an average sequence fills.
+int unit_rows(int32_t num_seqs, int32_t total_q, int32_t heads) {
+  const int64_t rows = (static_cast<int64_t>(total_q) * heads + num_seqs - 1) / std::max(num_seqs, 1);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+int64_t units_bound(int32_t num_seqs, int32_t total_q, int32_t heads, int rows) {
+  return static_cast<int64_t>(total_q) * heads / rows + num_seqs;
+}
+int64_t line_bound(int64_t units, int32_t max_pages) {
+  return units * ((max_pages + kTilePages - 1) / kTilePages + kUnitTiles);
+}
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// The workspace's parts.
+struct Parts {
+  int rows;
+  int64_t units, ctas;
+  size_t o, sums, notes, total;        // bytes of partial outputs, sums, notes; of all and the units' number
+};
+bool parts_of(int32_t num_seqs, int32_t total_q, int32_t heads, int32_t max_pages, int sms, Parts* w) {
+  w->rows = unit_rows(num_seqs, total_q, heads);
+  w->units = units_bound(num_seqs, total_q, heads, w->rows);
+  const int64_t line = line_bound(w->units, max_pages);
+  if (line > INT32_MAX) return false;
+  w->ctas = std::min<int64_t>(std::min(sms, kMaxCtas), line);
+  w->o = align256(static_cast<size_t>(w->ctas) * 2 * w->rows * kDim * sizeof(float));
+  w->sums = align256(static_cast<size_t>(w->ctas) * 2 * w->rows * sizeof(float2));
+  w->notes = align256(static_cast<size_t>(w->units) * sizeof(JoinNote));
+  w->total = w->o + w->sums + w->notes + 256;
+  return true;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return static_cast<EncodeFn>(nullptr);
+    }
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+// A box is `width` bytes of a page's 16 rows.
+bool encode_map(CUtensorMap* map, const void* cache, int64_t num_pages, uint32_t width, CUtensorMapSwizzle swizzle) {
+  const EncodeFn encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {kRow, kPage, static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t strides[2] = {kRow, kRow * kPage};
+  const cuuint32_t box[3] = {width, kPage, 1}, step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_pdl(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, LatentParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&p};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+template <int N>
+int launch_latent(LatentParams& p, int device, cudaStream_t stream) {
+  static std::atomic<bool> allowed[64];              // per device; setting it twice is harmless
+  const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<N>);
+  if (!allowed[device].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<N>()) != cudaSuccess) {
+      cudaGetLastError();
+      return MTPATTN_E_LAUNCH;
+    }
+    allowed[device].store(true, std::memory_order_release);
+  }
+  if (launch_pdl(kernel, dim3(p.ctas), kLatentThreads, smem_bytes<N>(), stream, p) != cudaSuccess) return MTPATTN_E_LAUNCH;
+  if (p.max_pages <= kTilePages) return MTPATTN_OK;  // units of one tile are never cut
+  const bool few = p.unit_bound <= 32;
+  const void* join = few ? reinterpret_cast<const void*>(latent_join_kernel<N, 1, 2>)
+                         : reinterpret_cast<const void*>(latent_join_kernel<N, 8, 1>);
+  return launch_pdl(join, dim3(p.unit_bound, N / (few ? 1 : 8)), kJoinThreads, 0, stream, p) == cudaSuccess
+             ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
 
 }  // namespace
@@ -149,7 +1163,9 @@ extern "C" size_t mtp_latent_attn_workspace_size(int32_t num_seqs, int32_t total
                                                  int32_t max_pages_per_seq) {
   if (num_seqs < 0 || total_q < 0 || num_heads <= 0 || num_heads > MTP_LATENT_MAX_HEADS || max_pages_per_seq < 0)
     return 0;
-  return device_sm_count(-1) > 0 ? 256 : 0;
+  const int sms = device_sm_count(-1);
+  Parts w;
+  return sms > 0 && parts_of(num_seqs, total_q, num_heads, max_pages_per_seq, sms, &w) ? w.total : 0;
 }
 
 extern "C" int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_head,
@@ -178,23 +1194,28 @@ extern "C" int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t 
     return MTPATTN_E_ARG;
   // 2. the supported envelope
   if (num_heads > MTP_LATENT_MAX_HEADS || total_q > static_cast<int64_t>(num_seqs) * MTP_LATENT_MAX_NODES ||
-      num_pages > INT32_MAX || max_pages_per_seq > INT32_MAX / kPage - 8)
+      num_pages > INT32_MAX || max_pages_per_seq > INT32_MAX / kPage - kTilePages)
     return MTPATTN_E_UNSUPPORTED;
   // 3. the workspace
   const int device = current_device();
   if (device < 0 || device >= 64) return MTPATTN_E_DEVICE;
-  const size_t need = mtp_latent_attn_workspace_size(num_seqs, total_q, num_heads, max_pages_per_seq);
-  if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < need) return MTPATTN_E_WORKSPACE;
+  const int sms = device_sm_count(device);
+  if (sms <= 0) return MTPATTN_E_DEVICE;
+  Parts w;
+  if (!parts_of(num_seqs, total_q, num_heads, max_pages_per_seq, sms, &w)) return MTPATTN_E_UNSUPPORTED;
+  if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < w.total) return MTPATTN_E_WORKSPACE;
   // 4. every pointer must be memory the kernels can read on the current device
   const void* const ptrs[] = {q, cache, block_tables, seq_lens, cu_seqlens_q, descale, workspace, out};
   if (!all_on_device(ptrs, device) || (tree_mask && !ptr_on_device(tree_mask, device)) ||
       (status && !ptr_on_device(status, device)))
     return MTPATTN_E_DEVICE;
   LatentParams p{};
+  if (!encode_map(&p.tmap, cache, num_pages, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&p.tmap_rope, cache, num_pages, MTP_LATENT_ROPE_DIM, CU_TENSOR_MAP_SWIZZLE_64B))
+    return MTPATTN_E_LAUNCH;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride_tok = q_stride_tok;
   p.q_stride_head = q_stride_head;
-  p.cache = static_cast<const uint8_t*>(cache);
   p.num_pages = num_pages;
   p.block_tables = block_tables;
   p.max_pages = max_pages_per_seq;
@@ -210,16 +1231,15 @@ extern "C" int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t 
   p.out_stride_tok = out_stride_tok;
   p.out_stride_head = out_stride_head;
   p.status = status;
-  static std::atomic<bool> attr_set[64];               // per device; setting it twice is harmless
-  if (!attr_set[device].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(latent_plain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlainSmem) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return MTPATTN_E_LAUNCH;
-    }
-    attr_set[device].store(true, std::memory_order_release);
-  }
-  const dim3 grid(num_seqs, std::min(MTP_LATENT_MAX_NODES, total_q), (num_heads + kPlainRows - 1) / kPlainRows);
-  latent_plain_kernel<<<grid, kPlainThreads, kPlainSmem, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
+  p.ctas = static_cast<int32_t>(w.ctas);
+  char* ws = static_cast<char*>(workspace);
+  p.o_part = reinterpret_cast<float*>(ws);
+  p.sum_part = reinterpret_cast<float2*>(ws + w.o);
+  p.notes = reinterpret_cast<JoinNote*>(ws + w.o + w.sums);
+  p.units = reinterpret_cast<int32_t*>(ws + w.o + w.sums + w.notes);
+  p.unit_bound = static_cast<int32_t>(w.units);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return w.rows == 16 ? launch_latent<16>(p, device, st)
+         : w.rows == 32 ? launch_latent<32>(p, device, st)
+                        : launch_latent<64>(p, device, st);
 }
