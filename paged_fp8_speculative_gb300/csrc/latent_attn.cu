@@ -61,18 +61,26 @@ using namespace sm100;
 constexpr int kRow = MTP_LATENT_ROW, kDim = MTP_LATENT_DIM;
 constexpr int kLatentThreads = 384;
 constexpr int kKeys = 128, kTilePages = kKeys / kPage;
-constexpr int kColumns = 4;                          // of 128 bytes; the fifth has 64
-constexpr int kColumn = kKeys * 128;                 // 16 KB
-constexpr int kRopeColumn = kKeys * MTP_LATENT_ROPE_DIM;
-constexpr int kStage = kColumns * kColumn + kRopeColumn;
+constexpr int kColumns = 4;                          // of 128 dims; the rotated 64 apart
+constexpr int kAtom = 8 * 128;                       // 8 keys of a column, 128-byte swizzled
+constexpr int kGroup = kColumns * kAtom;             // 8 keys
+constexpr int kBlocks = 4, kBlockKeys = kKeys / kBlocks;   // what is fetched and given back at a time
+constexpr int kRopeAt = kKeys / 8 * kGroup, kRopeColumn = kKeys * MTP_LATENT_ROPE_DIM;
+constexpr int kStage = kRopeAt + kRopeColumn;
+constexpr int kBlockPages = kBlockKeys / kPage;
+constexpr int kWarpBlocks = kBlocks / 2, kWarpPages = kWarpBlocks * kBlockPages;   // of a tile, a fetching warp's
 constexpr int kStages = 2;
 constexpr int kWarpSoft = 4, kSoftWarps = 8;
+constexpr int kLaunchRegisters = 168;                // a thread, as the block is launched (checked by the host)
+constexpr int kFewRegisters = 104, kManyRegisters = 200;   // ... and as the roles share them out
 constexpr int kSBuf = 128, kOCol = 256, kTmemCols = 512;
 constexpr int kSegRing = 4;
+constexpr int kPrefetch = 1;                         // tiles ahead, into L2
 constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at the reference, and at most
                                                      // 2^(kShift + kTau) = 430 < 448
+constexpr float kRoom = 4.f;                         // a raised reference is so far above the row's maximum
 constexpr float kNoRef = -1e30f;                     // no key seen yet
-constexpr int kUnitTiles = 2;
+constexpr int kUnitTiles = 7;
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kBadSum = 0x7fd0bad1u;            // a sum of a sequence with a bad page (a NaN that no
                                                      // arithmetic makes)
@@ -96,6 +104,7 @@ struct JoinNote {
 
 struct LatentParams {
   CUtensorMap tmap, tmap_rope;
+  const uint8_t* cache;
   const __nv_bfloat16* q;
   int64_t q_stride_tok, q_stride_head;
   int64_t num_pages;
@@ -126,9 +135,9 @@ struct Segment {             // part of one unit: tiles t0 .. t1 - 1 of nt
 };
 
 struct Bars {
-  uint64_t full[kStages][kColumns], empty[kStages][kColumns];
+  uint64_t full[kStages][kBlocks], empty[kStages][kBlocks];
   uint64_t s_full[2], s_free[2];
-  uint64_t p_full, pv_done, q_full, final_mma;
+  uint64_t p_full[kBlocks], pv_done, q_full, final_mma[2];
   uint64_t meet[3];          // the softmax warps of a row half, of both
   uint64_t seg_full[kSegRing], seg_free[kSegRing];
   Segment seg[kSegRing];
@@ -138,14 +147,17 @@ struct Bars {
 template <int N>
 struct Shared {
   Bars bars;
-  alignas(16) float2 row[N];           // factor of the row's logits (log2 domain), reference - kShift
-  float f[N];                          // factor of a rescale; of the output
+  alignas(16) float factor[N];         // of the row's logits (log2 domain)
+  alignas(16) float ref[N];            // reference - kShift
+  alignas(16) float step[N];           // what it was raised by, negative
+  alignas(16) float f[N];              // 2^step; the output's factor
   uint64_t word[N];                    // new tokens that the row sees
-  float xch[2][4][N / 2];              // row half, key quarter
+  alignas(16) float xch[2][4][N / 2];  // row half, key quarter
   uint8_t over[2][2][4];               // by turns; row half, key quarter
 };
 template <int N>
 constexpr int smem_bytes() { return off_bars<N>() + static_cast<int>(sizeof(Shared<N>)); }
+static_assert(kBlockKeys == 32, "a softmax warp's keys");
 static_assert(smem_bytes<64>() <= 232448, "more than a block may have");
 
 // ---- the line of tiles ---------------------------------------------------------------------------
@@ -185,10 +197,12 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {    // inclusive
   }
   return x;
 }
-__device__ __forceinline__ int64_t warp_total(int64_t v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Sum over the warp of numbers from 0 to 2^31 - 1.
+__device__ __forceinline__ int64_t warp_total(int v) {
+  return (static_cast<int64_t>(__reduce_add_sync(0xffffffffu, v >> 16)) << 16) + __reduce_add_sync(0xffffffffu, v & 0xffff);
+}
+__device__ __forceinline__ int add_up_to_max(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), static_cast<uint32_t>(INT32_MAX)));
 }
 
 // A CTA's walk over the units of its piece, by one warp; 32 sequences are held, one a lane.
@@ -203,17 +217,16 @@ struct Walker {
   __device__ __forceinline__ void start(const LatentParams& p, int lane) {
     b0 = before = units_before = unit = unit0 = unit_places = 0;
     mine = seq_at<N>(p, lane);
-    int64_t W = mine.w, rows = mine.n, U = mine.T;
+    int w = mine.w, n = mine.n, T = mine.T;
 #pragma unroll 1
     for (int b = 32; b < p.num_seqs; b += 32) {
       const Seq x = seq_at<N>(p, b + lane);
-      W += x.w;
-      rows += x.n;
-      U += x.T;
+      w = add_up_to_max(w, x.w);
+      n = add_up_to_max(n, x.n);
+      T = add_up_to_max(T, x.T);
     }
-    W = warp_total(W);
-    rows = warp_total(rows);
-    U = warp_total(U);
+    int64_t W = warp_total(w), U = warp_total(T);
+    const int64_t rows = warp_total(n);
     // Sequences that claim the same rows again and again (cu_seqlens_q far out of order) could make the line
     // longer than any call's is: then nothing is computed.
     if (W > INT32_MAX || rows > 2ll * p.total_q) {
@@ -385,12 +398,49 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t addr, uint32_t lbo, uint
 }
 constexpr uint32_t kAMajorM = 1u << 15;              // instruction descriptor: A is M-major
 
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int page,
-                                         uint64_t policy) {
+// Descriptors (sdesc_sw128 of sm100.cuh, sdesc_sw64) in two words: operands differ in the first one only, by
+// constants.  A thread that issues products shares its scheduler with two softmax warps, and a tile's 50
+// products have to go out in less than 2500 clocks.
+struct Desc {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc desc_of(uint64_t d) { return {static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)}; }
+
+// D (+)= A B
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n}\n" ::"r"(d_tmem),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+// D (+)= A B0, D += A B1: the second product takes A from the collector.  (Measured, M 128, N 64: 78 clocks the
+// pair, 96 with A fetched twice; shared memory gives 128 bytes a clock, and A is 4 KB, B 2 KB.)
+__device__ __forceinline__ void mma_two(uint32_t d_tmem, uint32_t a, uint32_t a_hi, uint32_t b0, uint32_t b1, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y, z;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %5};\n mov.b64 z, {%4, %5};\n"
+      " setp.ne.b32 p, %7, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], x, y, %6, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], x, z, %6, 1;\n}\n" ::"r"(d_tmem),
+      "r"(a), "r"(a_hi), "r"(b0), "r"(b1), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
+}
+// 8 keys of a page: four columns of 128 bytes of each, column by column.
+__device__ __forceinline__ void tma_half_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row, int page,
+                                              uint64_t policy) {
+  tma_load_4d(dst, map, bar, 0, row, 0, page, policy);
+}
+__device__ __forceinline__ void tma_rope_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int page, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(page), "r"(bar), "l"(policy)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(kDim), "r"(0), "r"(page), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -410,20 +460,29 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
   return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// Sums over the warp's lanes of n numbers: lane r gets that of v[r % n].
-template <int n>
-__device__ __forceinline__ float row_sums(float (&v)[n], int lane) {
+// What n numbers of every lane come to over the warp, by sums or by the largest (NaN is passed over): lane r
+// gets that of v[r % n].
+template <int n, typename Join>
+__device__ __forceinline__ float over_lanes(float (&v)[n], int lane, Join join) {
 #pragma unroll
   for (int o = n / 2; o; o >>= 1)
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const bool up = lane & o;
       const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
 #pragma unroll
-  for (int o = n; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  for (int o = n; o < 32; o <<= 1) v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
   return v[0];
+}
+template <int n>
+__device__ __forceinline__ float row_sums(float (&v)[n], int lane) {
+  return over_lanes(v, lane, [](float a, float b) { return a + b; });
+}
+template <int n>
+__device__ __forceinline__ float row_maxima(float (&v)[n], int lane) {
+  return over_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
 }
 
 static_assert(kWaitCycles < (1ll << 32), "32-bit clock");
@@ -445,10 +504,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 struct Meeting {
   uint32_t bar;
   uint32_t turns;
-  __device__ __forceinline__ bool operator()(int lane, volatile int* abort) {
+  __device__ __forceinline__ void arrive(int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    return warp_wait(bar, turns++ & 1, abort);
+  }
+  __device__ __forceinline__ bool wait(volatile int* abort) { return warp_wait(bar, turns++ & 1, abort); }
+  __device__ __forceinline__ bool operator()(int lane, volatile int* abort) {
+    arrive(lane);
+    return wait(abort);
   }
 };
 
@@ -475,7 +538,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
   }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i)
-      for (int c = 0; c < kColumns; ++c) {
+      for (int c = 0; c < kBlocks; ++c) {
         mbar_init(smem_u32(&bars.full[i][c]), 1);
         mbar_init(smem_u32(&bars.empty[i][c]), 1);
       }
@@ -483,14 +546,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
       mbar_init(smem_u32(&bars.s_full[i]), 1);
       mbar_init(smem_u32(&bars.s_free[i]), kSoftWarps);
     }
-    mbar_init(smem_u32(&bars.p_full), kSoftWarps);
+    for (int i = 0; i < kBlocks; ++i) mbar_init(smem_u32(&bars.p_full[i]), kSoftWarps / kBlocks);
     mbar_init(smem_u32(&bars.pv_done), 1);
     mbar_init(smem_u32(&bars.q_full), kSoftWarps);
-    mbar_init(smem_u32(&bars.final_mma), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars.final_mma[i]), 1);
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&bars.meet[i]), i < 2 ? kSoftWarps / 2 : kSoftWarps);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(smem_u32(&bars.seg_full[i]), 1);
-      mbar_init(smem_u32(&bars.seg_free[i]), kSoftWarps + 1);
+      mbar_init(smem_u32(&bars.seg_free[i]), kSoftWarps + 3);
     }
     bars.abort = 0;
     fence_mbar_init();
@@ -504,33 +567,29 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
+  static_assert(kWarpSoft * 32 * kFewRegisters + kSoftWarps * 32 * kManyRegisters <= kLatentThreads * kLaunchRegisters,
+                "registers of the block: a larger sum would wait forever");
+  if (warp < kWarpSoft) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kFewRegisters));
   if (warp == 0) {
-    // ============================== the walk, and the tiles by TMA ================================
-    if (lane == 0) {
-      prefetch_tmap(&p.tmap);
-      prefetch_tmap(&p.tmap_rope);
-    }
-    if (blockIdx.x == 0)                           // tell of sequences whose rows are not known
-      for (int b = lane; b < p.num_seqs; b += 32) {
-        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-        if (q0 < 0 || q1 <= q0 || q1 > p.total_q) set_status(p.status, MTPATTN_ERR_QLEN);
-      }
-    __syncwarp();
+    // ============================== the walk, and the scores =====================================
     Walker<N> walk;
     walk.start(p, lane);
     if (blockIdx.x == 0 && lane == 0) *p.units = min(walk.units, p.unit_bound);
-    const uint64_t once = l2_policy_evict_first();
-    uint64_t again;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
+    constexpr uint32_t kIdesc = idesc_e4m3_f32(128, 2 * N, false);
+    const Desc q = desc_of(sdesc_sw128(smem + off_q<N>(), 16, 1024));
+    const Desc q_rope = desc_of(sdesc_sw64(smem + off_q<N>() + kColumns * q_column<N>(), 16, 512));
+    const Desc c0 = desc_of(sdesc_sw128(smem, 16, kGroup)), r0 = desc_of(sdesc_sw64(smem + kRopeAt, 16, 512));
     uint32_t u = 0;                                // tiles so far
-    int e = 0, columns = 0;                        // segments; columns of the last tile asked for
-    bool ok = true;
 #pragma unroll 1
-    while (ok) {
+    for (int e = 0;;) {
       Segment s;
       const int err = walk.next(p, lane, s);
-      if (!s.end && lane == 0 && s.t0 == 0 && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
+      auto leave_note = [&]() {
+        if (lane == 0 && s.t0 == 0 && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
+      };
       if (!s.end && err) {
+        leave_note();
         // zeros for the rows of a sequence that cannot be computed, here: it has no tiles
         if (lane == 0) set_status(p.status, err);
         const int rows = min(N, s.n * p.heads - s.m * N);
@@ -543,140 +602,187 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         }
         continue;
       }
-      ok = warp_wait(smem_u32(&bars.seg_free[e % kSegRing]), ((e / kSegRing) & 1) ^ 1, abort_flag);
-      if (!ok) break;
+      if (!warp_wait(smem_u32(&bars.seg_free[e % kSegRing]), ((e / kSegRing) & 1) ^ 1, abort_flag)) break;
       if (lane == 0) {
         bars.seg[e % kSegRing] = s;
         mbar_arrive(smem_u32(&bars.seg_full[e % kSegRing]));
       }
       if (s.end) break;
+      leave_note();
+      if (!warp_wait(smem_u32(&bars.q_full), e & 1, abort_flag)) break;
+      const uint32_t end = u + (s.t1 - s.t0);
+      if (elect_one()) {
+        tc_fence_after();
+#pragma unroll 1
+        for (; u < end; ++u) {                     // S(u) = C Q^T
+          const uint32_t st = u % kStages, parity = (u / kStages) & 1, d = tmem + (u & 1) * kSBuf;
+          bool ok = wait_for(smem_u32(&bars.s_free[u & 1]), ((u >> 1) & 1) ^ 1, abort_flag);
+#pragma unroll
+          for (int c = 0; c < kBlocks; ++c) ok = ok && wait_for(smem_u32(&bars.full[st][c]), parity, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = c0.lo + st * (kStage >> 4), ar = r0.lo + st * (kStage >> 4);
+          mma_one<false>(d, a, c0.hi, q.lo, q.hi, kIdesc);
+#pragma unroll
+          for (int k = 1; k < 4 * kColumns; ++k)   // 32 dims
+            mma_one<true>(d, a + (((k >> 2) * kAtom + 32 * (k & 3)) >> 4), c0.hi,
+                          q.lo + (((k >> 2) * q_column<N>() + 32 * (k & 3)) >> 4), q.hi, kIdesc);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) mma_one<true>(d, ar + (32 * k >> 4), r0.hi, q_rope.lo + (32 * k >> 4), q_rope.hi, kIdesc);
+          mma_commit(smem_u32(&bars.s_full[u & 1]));
+        }
+      }
+      __syncwarp();
+      if (*abort_flag) break;
+      u = end;
+      ++e;
+    }
+    if (blockIdx.x == 0)                           // tell of sequences whose rows are not known
+      for (int b = lane; b < p.num_seqs; b += 32) {
+        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+        if (q0 < 0 || q1 <= q0 || q1 > p.total_q) set_status(p.status, MTPATTN_ERR_QLEN);
+      }
+    __syncwarp();
+    if (elect_one()) {                             // no product may run on when the CTA ends
+      mma_commit(smem_u32(&bars.final_mma[0]));
+      volatile int no_abort = 0;
+      wait_for(smem_u32(&bars.final_mma[0]), 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ============================== the tiles by TMA, two blocks a warp ===========================
+    const int first = (warp - 2) * kWarpBlocks;
+    if (lane == 0) {
+      prefetch_tmap(&p.tmap);
+      prefetch_tmap(&p.tmap_rope);
+    }
+    const uint64_t once = l2_policy_evict_first();
+    uint64_t again;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
+    uint32_t u = 0;                                // tiles so far
+    int asked = 0;                                 // blocks of the last one asked for
+    bool ok = true;
+#pragma unroll 1
+    for (int e = 0; ok; ++e) {
+      ok = warp_wait(smem_u32(&bars.seg_full[e % kSegRing]), (e / kSegRing) & 1, abort_flag);
+      if (!ok) break;
+      Segment& s = bars.seg[e % kSegRing];
+      if (s.end) break;
+      const int t0 = s.t0, t1 = s.t1, pages = (s.L + kPage - 1) / kPage;
       const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
       const uint64_t policy = static_cast<int64_t>(s.n) * p.heads <= N ? once : again;
-      const int pages = (s.L + kPage - 1) / kPage;
-      // table entries, a lane one of four tiles' 32, with the next 32 on the way
+      // table entries, a lane one of eight tiles' 4 that are this warp's, with the next 32 on the way
       auto entries = [&](int t) -> int {
-        const int64_t pg = static_cast<int64_t>(t) * kTilePages + lane;
+        const int64_t pg = static_cast<int64_t>(t + lane / kWarpPages) * kTilePages + first * kBlockPages + lane % kWarpPages;
         return pg < pages ? bt[pg] : 0;
       };
-      int now = entries(s.t0), ahead = entries(s.t0 + 4);
+      int now = entries(t0), ahead = entries(t0 + 32 / kWarpPages);
 #pragma unroll 1
-      for (int t = s.t0; t < s.t1 && ok; ++t, ++u) {
-        const int k = (t - s.t0) & 3;
-        if (k == 0 && t > s.t0) {
+      for (int t = t0; t < t1; ++t, ++u) {
+        const int k = (t - t0) % (32 / kWarpPages);
+        if (k == 0 && t > t0) {
           now = ahead;
-          ahead = entries(t + 4);
+          ahead = entries(t + 32 / kWarpPages);
         }
-        const int page = __shfl_sync(0xffffffffu, now, k * kTilePages + (lane & 7));
-        const int np = min(kTilePages, pages - t * kTilePages);
-        const bool bad = __any_sync(0xffffffffu, lane < np && (page < 0 || page >= p.num_pages));
+        // lanes 0-3 of 6 a half page's latent vectors each, 4-5 a page's rotated parts; the next 6 the second
+        // block's, were there no wait between them
+        const int np = min(kTilePages, pages - t * kTilePages) - first * kBlockPages;   // this warp's, if above 0
+        const int mine = __shfl_sync(0xffffffffu, now, k * kWarpPages + lane % kWarpPages);
+        const bool bad = __any_sync(0xffffffffu, lane < min(np, kWarpPages) && (mine < 0 || mine >= p.num_pages));
         if (bad && lane == 0) {
-          *const_cast<volatile int*>(&bars.seg[e % kSegRing].bad) = 1;
+          *const_cast<volatile int*>(&s.bad) = 1;
           set_status(p.status, MTPATTN_ERR_PAGE);
         }
+        // A stage is free late, and a fetch from memory would be the longest part of its turn: pages are brought
+        // into L2 some tiles ahead.
+        {
+          const int k2 = k + kPrefetch;
+          const int far = __shfl_sync(0xffffffffu, k2 < 32 / kWarpPages ? now : ahead, (k2 % (32 / kWarpPages)) * kWarpPages + lane % kWarpPages);
+          if (lane < kWarpPages && t + kPrefetch < t1 &&
+              (t + kPrefetch) * kTilePages + first * kBlockPages + lane < pages && far >= 0 && far < p.num_pages)
+            prefetch_l2(p.cache + static_cast<int64_t>(far) * (kPage * kRow), kPage * kRow);
+        }
         const int st = u % kStages;
-        const uint32_t parity = ((u / kStages) & 1) ^ 1;
         const uint32_t stage = smem + st * kStage;
 #pragma unroll 1
-        for (int c = 0; c < kColumns; ++c) {
-          ok = warp_wait(smem_u32(&bars.empty[st][c]), parity, abort_flag);
+        for (int c = 0; c < kWarpBlocks; ++c) {
+          ok = warp_wait(smem_u32(&bars.empty[st][first + c]), ((u / kStages) & 1) ^ 1, abort_flag);
           if (!ok) break;
-          columns = c + 1;
-          const uint32_t bar = smem_u32(&bars.full[st][c]);
-          const bool last = c == kColumns - 1;
+          asked = c + 1;
+          const uint32_t bar = smem_u32(&bars.full[st][first + c]);
+          const int here = bad ? 0 : max(0, min(kBlockPages, np - c * kBlockPages));   // pages to fetch
           if (lane == 0) {
-            if (bad) mbar_arrive(bar);             // nothing is fetched: the segment's rows become zeros
-            else mbar_arrive_expect_tx(bar, np * kPage * (128 + (last ? MTP_LATENT_ROPE_DIM : 0)));
+            if (here == 0) mbar_arrive(bar);       // (of a bad page nothing: the segment's rows become zeros)
+            else mbar_arrive_expect_tx(bar, here * kPage * kRow);
           }
-          __syncwarp();
-          if (!bad && lane < np) {
-            tma_page(stage + c * kColumn + lane * (kPage * 128), &p.tmap, bar, c * 128, page, policy);
-            if (last)
-              tma_page(stage + kColumns * kColumn + lane * (kPage * MTP_LATENT_ROPE_DIM), &p.tmap_rope, bar, kDim, page,
-                       policy);
+          const int i = lane < 4 ? lane >> 1 : lane & 1;
+          const int pg = __shfl_sync(0xffffffffu, mine, c * kBlockPages + i);
+          if (lane < 6 && i < here) {
+            const int at = (first + c) * kBlockPages + i;        // page of the tile
+            if (lane < 4)
+              tma_half_page(stage + (2 * at + (lane & 1)) * kGroup, &p.tmap, bar, (lane & 1) * 8, pg, policy);
+            else
+              tma_rope_page(stage + kRopeAt + at * (kPage * MTP_LATENT_ROPE_DIM), &p.tmap_rope, bar, pg, policy);
           }
           __syncwarp();
         }
         if (!ok) break;
       }
-      ++e;
+      if (ok && lane == 0) mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
     }
-    // What was asked for has to arrive before the block may end: u tiles whole, and columns of one more
-    // after an abort.
-    volatile int no_abort = 0;
-    if (!ok && columns < kColumns)
-      for (int c = 0; c < columns; ++c) wait_for(smem_u32(&bars.full[u % kStages][c]), (u / kStages) & 1, &no_abort);
-    for (uint32_t k = 1; k <= kStages && k <= u; ++k)
-      for (int c = 0; c < kColumns; ++c)
-        if (*abort_flag) wait_for(smem_u32(&bars.full[(u - k) % kStages][c]), ((u - k) / kStages) & 1, &no_abort);
+    // What was asked for has to arrive before the CTA may end: u tiles whole, and blocks of one more after
+    // an abort.
+    if (*abort_flag) {
+      volatile int no_abort = 0;
+      if (!ok && asked < kWarpBlocks)
+        for (int c = 0; c < asked; ++c) wait_for(smem_u32(&bars.full[u % kStages][first + c]), (u / kStages) & 1, &no_abort);
+      for (uint32_t k = 1; k <= kStages && k <= u; ++k)
+        for (int c = 0; c < kWarpBlocks; ++c)
+          wait_for(smem_u32(&bars.full[(u - k) % kStages][first + c]), ((u - k) / kStages) & 1, &no_abort);
+    }
   } else if (warp == 1) {
-    // ============================== the products ==================================================
+    // ============================== the outputs ===================================================
+    // (Issued apart from the scores, so that neither waits for what the other lacks.)
     if (elect_one()) {
       auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_for(smem_u32(&bar), parity, abort_flag); };
-      constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 2 * N, false);
-      constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true) | kAMajorM;
-      const uint32_t q = smem + off_q<N>();
+      constexpr uint32_t kIdesc = idesc_e4m3_f32(128, N, true) | kAMajorM;
+      const Desc lo = desc_of(sdesc_sw64(smem + off_p<N>(), 512, 512)), hi = desc_of(sdesc_sw64(smem + kRopeAt, 512, 512));
+      const Desc v0 = desc_of(sdesc_sw128(smem, kAtom, kGroup));
       uint32_t u = 0;
       bool alive = true;
-      auto scores = [&](uint32_t v) -> bool {      // S(v) = C Q^T
-        const uint32_t st = v % kStages, stage = smem + st * kStage, d = tmem + (v & 1) * kSBuf;
-        if (!wait(bars.s_free[v & 1], ((v >> 1) & 1) ^ 1)) return false;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < kColumns; ++c) {
-          if (!wait(bars.full[st][c], (v / kStages) & 1)) return false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f8_ss(d, sdesc_sw128(stage + c * kColumn + 32 * k, 16, 1024),
-                      sdesc_sw128(q + c * q_column<N>() + 32 * k, 16, 1024), kIdescS, c | k);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          mma_f8_ss(d, sdesc_sw64(stage + kColumns * kColumn + 32 * k, 16, 512),
-                    sdesc_sw64(q + kColumns * q_column<N>() + 32 * k, 16, 512), kIdescS, 1);
-        mma_commit(smem_u32(&bars.s_full[v & 1]));
-        return true;
-      };
-      auto outputs = [&](uint32_t v, bool first) -> bool {   // O += C^T P^T
-        const uint32_t st = v % kStages, stage = smem + st * kStage;
-        if (!wait(bars.p_full, v & 1)) return false;
-        tc_fence_after();
-        const uint32_t hi = stage + kColumns * kColumn, lo = smem + off_p<N>();
-#pragma unroll 1
-        for (int c = 0; c < kColumns; ++c) {
-#pragma unroll
-          for (int k = 0; k < kKeys / 32; ++k) {
-            const uint64_t a = sdesc_sw128(stage + c * kColumn + k * (32 * 128), kColumn, 1024);
-            mma_f8_ss(tmem + kOCol + c * N, a, sdesc_sw64(hi + k * (32 * 64), 512, 512), kIdescO, !first || k);
-            mma_f8_ss(tmem + kOCol + c * N, a, sdesc_sw64(lo + k * (32 * 64), 512, 512), kIdescO, 1);
-          }
-          // (the last column's barrier also stands for the 64-byte one, where P's first terms lie)
-          mma_commit(smem_u32(&bars.empty[st][c]));
-        }
-        mma_commit(smem_u32(&bars.pv_done));
-        return true;
-      };
 #pragma unroll 1
       for (int e = 0; alive; ++e) {
         if (!(alive = wait(bars.seg_full[e % kSegRing], (e / kSegRing) & 1))) break;
         const volatile Segment& s = bars.seg[e % kSegRing];
-        const bool end = s.end;
-        const int tiles = s.t1 - s.t0;
+        const bool last = s.end;
+        const uint32_t end = u + (s.t1 - s.t0);
         mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
-        if (end) break;
-        if (!(alive = wait(bars.q_full, e & 1))) break;
-        tc_fence_after();
+        if (last) break;
 #pragma unroll 1
-        for (int i = 0; i <= tiles && alive; ++i) {
-          if (i < tiles) alive = scores(u + i);
-          if (alive && i > 0) alive = outputs(u + i - 1, i == 1);
+        for (uint32_t more = 0; u < end && alive; ++u, more = 1) {   // O (+)= C^T P^T
+          const uint32_t st = u % kStages, at = st * (kStage >> 4);
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k) {
+            if (!(alive = wait(bars.p_full[k], u & 1))) break;
+            tc_fence_after();
+            // Both terms of P one after the other, the second with the A operand that the first has brought in.
+#pragma unroll
+            for (int c = 0; c < kColumns; ++c)
+              mma_two(tmem + kOCol + c * N, v0.lo + at + ((k * (kBlockKeys / 8) * kGroup + c * kAtom) >> 4), v0.hi,
+                      lo.lo + (k * kBlockKeys * 64 >> 4), hi.lo + at + (k * kBlockKeys * 64 >> 4), lo.hi, kIdesc, k ? 1u : more);
+            mma_commit(smem_u32(&bars.empty[st][k]));    // (with the rows of both of P's terms)
+          }
+          if (!alive) break;
+          mma_commit(smem_u32(&bars.pv_done));
         }
-        u += tiles;
       }
-      mma_commit(smem_u32(&bars.final_mma));       // no product may run on when the block ends
+      mma_commit(smem_u32(&bars.final_mma[1]));
       volatile int no_abort = 0;
-      wait_for(smem_u32(&bars.final_mma), 0, &no_abort);
+      wait_for(smem_u32(&bars.final_mma[1]), 0, &no_abort);
     }
-  } else if (warp >= kWarpSoft) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kManyRegisters));
     // ============================== softmax, Q's operand, the output ==============================
     const int w = warp - kWarpSoft, quarter = warp & 3, half = w >> 2;
     const int key = quarter * 32 + lane;             // of the tile
@@ -686,89 +792,87 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
     const float descale = *p.descale, factor = p.scale_log2 * descale;
     const int row0 = half * kHalf;
     Meeting meet{smem_u32(&bars.meet[half]), 0}, meet_all{smem_u32(&bars.meet[2]), 0};
-    uint32_t u = 0;
+    uint32_t u = 0, votes_at = 0;
     bool alive = true;
-#pragma unroll 1
-    for (int e = 0; alive; ++e) {
-      if (!warp_wait(smem_u32(&bars.seg_full[e % kSegRing]), (e / kSegRing) & 1, abort_flag)) break;
-      const Segment s = bars.seg[e % kSegRing];
-      if (s.end) break;
-      // ---- Q's two terms: a warp a row.  (The last product that reads the previous ones is done: its S
-      // has been read.)
-      const int rows = min(N, s.n * p.heads - s.m * N);
-      constexpr int kBatch = N / kSoftWarps < 4 ? N / kSoftWarps : 4;   // rows in flight
-#pragma unroll 1
-      for (int r0 = w; r0 < N; r0 += kBatch * kSoftWarps) {
-        uint4 x[kBatch][3];
+    // Q's two terms of a segment, kSide lanes a row, and what there is of each row.  Asks that the last product
+    // that reads the previous ones is done: that all S of their segment has been read.
+    auto prepare = [&](const Segment& of) {
+      const int q0 = of.q0, n = of.n, m = of.m, rows = min(N, n * p.heads - m * N);
+      constexpr int kSide = kSoftWarps * 32 / N, kParts = (kRow / 8 + kSide - 1) / kSide;   // blocks of 8 a lane
+      const int r = (w * 32 + lane) / kSide, side = lane % kSide;
+      const int rr = m * N + r, tok = r < rows ? rr / p.heads : 0;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(q0 + tok) * p.q_stride_tok +
+                                                        static_cast<int64_t>(rr - tok * p.heads) * p.q_stride_head);
+      uint64_t word = 0;
+      if (r < rows) word = p.mask ? p.mask[q0 + tok] : (2ull << tok) - 1ull;
+      uint4 x[kParts];
+      uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = r0 + k * kSoftWarps, rr = s.m * N + r, tok = r < rows ? rr / p.heads : 0;
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(s.q0 + tok) * p.q_stride_tok +
-                                                            static_cast<int64_t>(rr - tok * p.heads) * p.q_stride_head);
+      for (int i = 0; i < kParts; ++i) {
+        const int j = side + i * kSide;
+        x[i] = r < rows && j < kRow / 8 ? src[j] : make_uint4(0u, 0u, 0u, 0u);
+      }
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            x[k][i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows && lane + 32 * i < kRow / 8) x[k][i] = src[lane + 32 * i];
-          }
-        }
+      for (int i = 0; i < kParts; ++i)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = r0 + k * kSoftWarps;
-          uint32_t top = 0;
+      for (int o = 1; o < kSide; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int exponent = max(top & 0xffffu, top >> 16) >> 7;   // biased; 255: not finite
+      const int a = min(134 - exponent, 126);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
+      const uint32_t at0 = smem + off_q<N>() + r * 128, at1 = smem + off_q<N>() + kColumns * q_column<N>() + r * 64;
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[k][i].x & 0x7fff7fffu, x[k][i].y & 0x7fff7fffu),
-                                         __vmaxu2(x[k][i].z & 0x7fff7fffu, x[k][i].w & 0x7fff7fffu)));
-          const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-          const int exponent = most >> 7;            // biased; 255: not finite
-          const int a = min(134 - exponent, 126);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const int j = lane + 32 * i;             // 8 elements
-            if (j >= kRow / 8) continue;
-            uint32_t h0, h1, l0, l1;
-            two_terms(scaled_half2(x[k][i].x, up), scaled_half2(x[k][i].y, up), 0u, h0, l0);
-            two_terms(scaled_half2(x[k][i].z, up), scaled_half2(x[k][i].w, up), 0u, h1, l1);
-            if (exponent == 255) h0 = h1 = l0 = l1 = 0x7f7f7f7fu;
-            uint32_t at = smem + off_q<N>(), low;
-            if (j < kDim / 8) {                      // 16 blocks a column's row, swizzled in pairs
-              const uint32_t b = j & 15;
-              at += (j >> 4) * q_column<N>() + r * 128 + (((b >> 1) ^ (r & 7)) << 4) + (b & 1) * 8;
-              low = at + N * 128;
-            } else {
-              const uint32_t b = j - kDim / 8;
-              at += kColumns * q_column<N>() + r * 64 + (((b >> 1) ^ ((r >> 1) & 3)) << 4) + (b & 1) * 8;
-              low = at + N * 64;
-            }
-            st_shared8(at, h0, h1);
-            st_shared8(low, l0, l1);
-          }
-          if (lane == 0) {
-            const int tok = r < rows ? (s.m * N + r) / p.heads : 0;
-            sh.row[r] = make_float2(r < rows ? factor * __uint_as_float(static_cast<uint32_t>(127 - a) << 23) : 0.f, kNoRef);
-            uint64_t word = 0;
-            if (r < rows) word = p.mask ? p.mask[s.q0 + tok] : (2ull << tok) - 1ull;
-            if (s.n < 64) word &= (1ull << s.n) - 1ull;
-            sh.word[r] = word;
-          }
-        }
+      for (int i = 0; i < kParts; ++i) {
+        const uint32_t j = side + i * kSide;
+        if (kParts * kSide > kRow / 8 && j >= kRow / 8) continue;
+        uint32_t h0, h1, l0, l1;
+        two_terms(scaled_half2(x[i].x, up), scaled_half2(x[i].y, up), 0u, h0, l0);
+        two_terms(scaled_half2(x[i].z, up), scaled_half2(x[i].w, up), 0u, h1, l1);
+        if (exponent == 255) h0 = h1 = l0 = l1 = 0x7f7f7f7fu;
+        // 16 blocks a column's row, 8 of the rotated part, swizzled in pairs
+        const bool rope = j >= kDim / 8;
+        const uint32_t at = rope ? at1 + ((((j - kDim / 8) >> 1) ^ ((r >> 1) & 3)) << 4) + (j & 1) * 8
+                                 : at0 + (j >> 4) * q_column<N>() + ((((j & 15) >> 1) ^ (r & 7)) << 4) + (j & 1) * 8;
+        st_shared8(at, h0, h1);
+        st_shared8(at + (rope ? N * 64 : N * 128), l0, l1);
+      }
+      if (side == 0) {
+        sh.factor[r] = r < rows ? factor * __uint_as_float(static_cast<uint32_t>(127 - a) << 23) : 0.f;
+        sh.ref[r] = kNoRef;
+        if (n < 64) word &= (1ull << n) - 1ull;
+        sh.word[r] = word;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
-      if (!(alive = meet_all(lane, abort_flag))) break;   // every row's factor and word
-
-      float l[kHalf];
+    };
+    if ((alive = warp_wait(smem_u32(&bars.seg_full[0]), 0, abort_flag)) && !bars.seg[0].end) {
+      prepare(bars.seg[0]);
+      alive = meet_all(lane, abort_flag);            // every row's factor and word
+    }
+#pragma unroll 1
+    for (int e = 0; alive; ++e) {
+      const Segment s = bars.seg[e % kSegRing];
+      if (s.end) break;
+      const int rows = min(N, s.n * p.heads - s.m * N);
+      // of the rows of this warp, in every lane: a load from shared memory waits for the products' reads
+      float l[kHalf], fac[kHalf], ref[kHalf];
 #pragma unroll
-      for (int r = 0; r < kHalf; ++r) l[r] = 0.f;
+      for (int r = 0; r < kHalf; ++r) {
+        l[r] = ref[r] = 0.f;
+        fac[r] = sh.factor[row0 + r];
+      }
       const int start = s.L - s.n;                   // first new token
+      const bool late = (s.t0 + 1) * kKeys > start;  // a row may see nothing of the first tile
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++u) {
         if (!(alive = warp_wait(smem_u32(&bars.s_full[u & 1]), (u >> 1) & 1, abort_flag))) break;
         tc_fence_after();
-        float y[kHalf];
-        {
+        const int j = t * kKeys + key;
+        const bool ragged = (t + 1) * kKeys > start;  // new tokens, or places behind the sequence
+        float y[kHalf];                              // logits above the reference, then weights
+        auto logits = [&]() {
           uint32_t h[kHalf], lo[kHalf];
           const uint32_t at = tmem + lanes + (u & 1) * kSBuf + row0;
           tmem_ld<kHalf>(at, h);
@@ -776,51 +880,77 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           tmem_wait<kHalf>(h);
           tmem_wait<kHalf>(lo);
 #pragma unroll
-          for (int r = 0; r < kHalf; ++r) y[r] = __uint_as_float(h[r]) + __uint_as_float(lo[r]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.s_free[u & 1]));
-        bool over = t == s.t0;
-        const int j = t * kKeys + key;
-        const bool ragged = (t + 1) * kKeys > start;  // new tokens, or places behind the sequence
+          for (int r = 0; r < kHalf; ++r) y[r] = fmaf(__uint_as_float(h[r]) + __uint_as_float(lo[r]), fac[r], -ref[r]);
+          if (ragged && j >= start) {
 #pragma unroll
-        for (int r = 0; r < kHalf; ++r) y[r] *= sh.row[row0 + r].x;
-        if (ragged && j >= start) {
-#pragma unroll
-          for (int r = 0; r < kHalf; ++r)
-            if (j >= s.L || !((sh.word[row0 + r] >> (j - start)) & 1)) y[r] = -INFINITY;
-        }
-#pragma unroll
-        for (int r = 0; r < kHalf; ++r) over |= y[r] - sh.row[row0 + r].y > kShift + kTau;
-        {
-          uint8_t (&all)[4] = sh.over[meet.turns & 1][half];
-          over = __any_sync(0xffffffffu, over);
-          if (lane == 0) all[quarter] = over;
-          if (!(alive = meet(lane, abort_flag))) break;
-          over = *reinterpret_cast<volatile uint32_t*>(all) != 0;
-        }
-        // the previous tile's products are in O, and P may be written
-        if (u > 0 && !(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
-        if (over) {
-          float mine = -INFINITY;
-#pragma unroll
-          for (int r = 0; r < kHalf; ++r) {
-            const float top = warp_max(y[r]);
-            if (lane == r) mine = top;
+            for (int r = 0; r < kHalf; ++r)
+              if (j >= s.L || !((sh.word[row0 + r] >> (j - start)) & 1)) y[r] = -INFINITY;
           }
+        };
+        uint32_t hi[kHalf / 4], lo[kHalf / 4];
+        auto weights = [&]() {
+#pragma unroll
+          for (int r = 0; r < kHalf; r += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[r + i] = exp2_hw(y[r + i]);
+            two_terms(half2_of(y[r], y[r + 1]), half2_of(y[r + 2], y[r + 3]), dither, hi[r / 4], lo[r / 4]);
+          }
+        };
+        logits();
+        // A reference is raised where a logit is too far above it, and at first.  While the warps of these rows
+        // tell one another, the weights are worked out as if there was none.
+        const bool forced = t == s.t0 || (ragged && late);
+        bool over = forced;
+        if (!over) {
+          float a = y[0], b = y[1];
+#pragma unroll
+          for (int r = 2; r < kHalf; r += 2) {
+            a = fmaxf(a, y[r]);
+            b = fmaxf(b, y[r + 1]);
+          }
+          over = __any_sync(0xffffffffu, fmaxf(a, b) > kShift + kTau);
+        }
+        if (!forced) {
+          uint8_t (&votes)[4] = sh.over[votes_at ^= 1][half];
+          if (lane == 0) votes[quarter] = over;
+          meet.arrive(lane);
+          weights();
+          if (!(alive = meet.wait(abort_flag))) break;
+          over = *reinterpret_cast<volatile uint32_t*>(votes) != 0;
+        }
+        if (over) {
+          if (!forced) logits();
+          float tops[kHalf];
+#pragma unroll
+          for (int r = 0; r < kHalf; ++r) tops[r] = y[r];
+          const float mine = row_maxima<kHalf>(tops, lane);
           if (lane < kHalf) sh.xch[half][quarter][lane] = mine;
-          if (!(alive = meet(lane, abort_flag))) break;
+          meet.arrive(lane);
+          if (!(alive = meet.wait(abort_flag))) break;
           if (quarter == 0 && lane < kHalf) {
             const float (&x)[4][kHalf] = sh.xch[half];
-            const float top = fmaxf(fmaxf(x[0][lane], x[1][lane]), fmaxf(x[2][lane], x[3][lane])) - kShift;
-            const float ref = sh.row[row0 + lane].y;
-            const bool raise = top > (ref == kNoRef ? ref : ref + kTau);
-            sh.f[row0 + lane] = raise ? exp2_hw(ref - top) : 1.f;
-            if (raise) sh.row[row0 + lane].y = top;
+            const float top = fmaxf(fmaxf(x[0][lane], x[1][lane]), fmaxf(x[2][lane], x[3][lane]));
+            const float old = sh.ref[row0 + lane];   // kNoRef: the row has seen nothing, y is above 0
+            float step = 0.f, f = 1.f;
+            if (top > (old == kNoRef ? -INFINITY : kShift + kTau)) {
+              step = kShift - top - (s.t1 - t > 2 ? kRoom : 0.f);   // (the last tiles will not raise it much)
+              f = old == kNoRef ? 0.f : exp2_hw(step);
+              sh.ref[row0 + lane] = (old == kNoRef ? 0.f : old) - step;
+            }
+            sh.step[row0 + lane] = step;
+            sh.f[row0 + lane] = f;
           }
-          if (!(alive = meet(lane, abort_flag))) break;
+          meet.arrive(lane);
+          if (!(alive = meet.wait(abort_flag))) break;
+#pragma unroll
+          for (int r = 0; r < kHalf; ++r) {
+            const float step = sh.step[row0 + r];
+            y[r] += step;
+            ref[r] -= step;
+          }
           if (t > s.t0) {
+            // (O may be touched once the previous tile's products are in it)
+            if (!(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
             tc_fence_after();
 #pragma unroll
             for (int r = 0; r < kHalf; ++r) l[r] *= sh.f[row0 + r];
@@ -836,39 +966,31 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             }
             tmem_st_wait();
           }
-        }
-        // ---- the weights, and their two terms
-        uint32_t hi[kHalf / 4], lo[kHalf / 4];
-#pragma unroll
-        for (int r = 0; r < kHalf; r += 4) {
-          float w4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w4[i] = exp2_hw(y[r + i] - sh.row[row0 + r + i].y);
-            l[r + i] += w4[i];
-          }
-          two_terms(half2_of(w4[0], w4[1]), half2_of(w4[2], w4[3]), dither, hi[r / 4], lo[r / 4]);
+          weights();
         }
         const uint32_t stage = smem + (u % kStages) * kStage;
         const uint32_t swz = (key >> 1) & 3;
-        const uint32_t at_hi = stage + kColumns * kColumn + key * 64, at_lo = smem + off_p<N>() + key * 64;
-        if constexpr (kHalf == 8) {
-          const uint32_t off = (swz << 4) + half * 8;
-          st_shared8(at_hi + off, hi[0], hi[1]);
-          st_shared8(at_lo + off, lo[0], lo[1]);
-        } else {
+        auto write = [&](uint32_t at, const uint32_t (&x)[kHalf / 4]) {
+          at += key * 64;
+          if constexpr (kHalf == 8) {
+            st_shared8(at + (swz << 4) + half * 8, x[0], x[1]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < kHalf / 16; ++i) {
-            const uint32_t off = ((half * (kHalf / 16) + i) ^ swz) << 4;
-            st_shared16(at_hi + off, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-            st_shared16(at_lo + off, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            for (int i = 0; i < kHalf / 16; ++i)
+              st_shared16(at + (((half * (kHalf / 16) + i) ^ swz) << 4), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
-        }
+        };
+        write(stage + kRopeAt, hi);
+        // the previous tile's second terms of these keys have been read: a quarter is a block
+        if (u > 0 &&
+            !(alive = warp_wait(smem_u32(&bars.empty[(u - 1) % kStages][quarter]), ((u - 1) / kStages) & 1, abort_flag)))
+          break;
+        write(smem + off_p<N>(), lo);
         if (ragged && j >= start) {
           // this half's 256 of the key's values: none behind the sequence, no NaN among the new tokens
 #pragma unroll 1
           for (int i = 0; i < 16; ++i) {
-            const uint32_t at = stage + (2 * half + (i >> 3)) * kColumn + key * 128 +
+            const uint32_t at = stage + (key >> 3) * kGroup + (2 * half + (i >> 3)) * kAtom + (key & 7) * 128 +
                                 (((i + key) & 7) << 4);   // (any order; this one meets all banks)
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (j < s.L) {
@@ -884,12 +1006,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars.p_full[quarter]));
+          mbar_arrive(smem_u32(&bars.s_free[u & 1]));
+        }
+#pragma unroll
+        for (int r = 0; r < kHalf; ++r) l[r] += y[r];
       }
       if (!alive) break;
-      // ---- the output
-      if (!(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
-      tc_fence_after();
+      // ---- the sums, and the next segment's Q while the last products run
       const bool bad = *const_cast<volatile int*>(&bars.seg[e % kSegRing].bad);
       const bool whole = s.t0 == 0 && s.t1 == s.nt;
       const int64_t slot = 2 * blockIdx.x + s.slot;
@@ -898,42 +1023,102 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         if (lane < kHalf) sh.xch[half][quarter][lane] = sum;
       }
       if (!(alive = meet(lane, abort_flag))) break;
-      if (quarter == 0 && lane < kHalf) {
+      if (quarter == 0) {
         const float (&x)[4][kHalf] = sh.xch[half];
-        const float sum = (x[0][lane] + x[1][lane]) + (x[2][lane] + x[3][lane]);
-        sh.f[row0 + lane] = bad || sum == 0.f ? 0.f : descale / sum;   // (NaN: the row sees one, or holds one)
-        if (!whole)
-          p.sum_part[slot * N + row0 + lane] =
-              make_float2(sh.row[row0 + lane].y, bad ? __uint_as_float(kBadSum) : sum);
-        // the words have served: where the row goes
-        const int rr = s.m * N + row0 + lane, tok = rr / p.heads;
-        sh.word[row0 + lane] = static_cast<uint64_t>(static_cast<int64_t>(s.q0 + tok) * p.out_stride_tok +
-                                                     static_cast<int64_t>(rr - tok * p.heads) * p.out_stride_head);
+        const int r = lane % kHalf, rr = s.m * N + row0 + r, tok = rr / p.heads;
+        const float sum = (x[0][r] + x[1][r]) + (x[2][r] + x[3][r]);
+        __syncwarp();
+        if (lane < kHalf) {
+          sh.f[row0 + r] = bad || sum == 0.f ? 0.f : descale / sum;   // (NaN: the row sees one, or holds one)
+          // where the row goes, over the sums
+          reinterpret_cast<int64_t*>(sh.xch[half])[r] = static_cast<int64_t>(s.q0 + tok) * p.out_stride_tok +
+                                                        static_cast<int64_t>(rr - tok * p.heads) * p.out_stride_head;
+          if (!whole)
+            p.sum_part[slot * N + row0 + r] = make_float2(sh.ref[row0 + r], bad ? __uint_as_float(kBadSum) : sum);
+        }
       }
-      if (!(alive = meet(lane, abort_flag))) break;
+      if (!(alive = meet_all(lane, abort_flag) &&
+                    warp_wait(smem_u32(&bars.seg_full[(e + 1) % kSegRing]), ((e + 1) / kSegRing) & 1, abort_flag)))
+        break;
+      const bool last = bars.seg[(e + 1) % kSegRing].end;
+      if (!last) prepare(bars.seg[(e + 1) % kSegRing]);
+      // ---- the output
+      if (!(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
+      tc_fence_after();
       const int valid = min(kHalf, rows - row0);     // of this half's
+      // A lane has one dim of all rows; exchanged between lanes (a butterfly on their lower bits), it stores 16
+      // bytes of a row at a time, 4 dims of partial outputs or 8 of the output.  (4 or 2 bytes at a time took
+      // 4100 clocks.)
 #pragma unroll 1
       for (int c = 0; c < kColumns; ++c) {
         uint32_t o[kHalf];
         tmem_ld<kHalf>(tmem + lanes + kOCol + c * N + row0, o);
         tmem_wait<kHalf>(o);
-        const int d = c * 128 + key;                 // (a TMEM lane is a dim here)
+        const int d0 = c * 128 + quarter * 32;       // (a TMEM lane is a dim here)
         if (whole) {
+          uint32_t x[kHalf / 2];
 #pragma unroll
-          for (int r = 0; r < kHalf; ++r)
-            if (r < valid) {
-              const float f = sh.f[row0 + r];
-              p.out[static_cast<int64_t>(sh.word[row0 + r]) + d] =
-                  __float2bfloat16(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
+          for (int i = 0; i < kHalf / 2; ++i) {      // rows 2i + bit 0, dims of the pair of lanes
+            const float f0 = sh.f[row0 + 2 * i], f1 = sh.f[row0 + 2 * i + 1];
+            const float v0 = f0 == 0.f ? 0.f : __uint_as_float(o[2 * i]) * f0;
+            const float v1 = f1 == 0.f ? 0.f : __uint_as_float(o[2 * i + 1]) * f1;
+            const float keep = lane & 1 ? v1 : v0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+            const __nv_bfloat162 pair = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
+            x[i] = *reinterpret_cast<const uint32_t*>(&pair);
+          }
+          uint32_t z[kHalf / 8][4];
+#pragma unroll
+          for (int i = 0; i < kHalf / 8; ++i) {      // rows 8i + bits 0 .. 2, dims of 8 lanes
+            uint32_t k2[2], g2[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w0 = x[4 * i + 2 * h], w1 = x[4 * i + 2 * h + 1];
+              k2[h] = lane & 2 ? w1 : w0;
+              g2[h] = __shfl_xor_sync(0xffffffffu, lane & 2 ? w0 : w1, 2);
             }
+            const uint32_t a0[2] = {lane & 2 ? g2[0] : k2[0], lane & 2 ? k2[0] : g2[0]};
+            const uint32_t a1[2] = {lane & 2 ? g2[1] : k2[1], lane & 2 ? k2[1] : g2[1]};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t keep = lane & 4 ? a1[h] : a0[h], got = __shfl_xor_sync(0xffffffffu, lane & 4 ? a0[h] : a1[h], 4);
+              z[i][h] = lane & 4 ? got : keep;
+              z[i][2 + h] = lane & 4 ? keep : got;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kHalf / 8; ++i) {
+            const int r = 8 * i + (lane & 7);
+            if (r < valid)
+              *reinterpret_cast<uint4*>(p.out + reinterpret_cast<const int64_t*>(sh.xch[half])[r] + d0 + (lane & 24)) =
+                  make_uint4(z[i][0], z[i][1], z[i][2], z[i][3]);
+          }
         } else {
 #pragma unroll
-          for (int r = 0; r < kHalf; ++r)
-            if (r < valid) p.o_part[(slot * N + row0 + r) * kDim + d] = __uint_as_float(o[r]);
+          for (int i = 0; i < kHalf / 4; ++i) {      // rows 4i + bits 0 and 1, dims of 4 lanes
+            uint32_t x[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w0 = o[4 * i + 2 * h], w1 = o[4 * i + 2 * h + 1];
+              const uint32_t keep = lane & 1 ? w1 : w0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? w0 : w1, 1);
+              x[h][0] = lane & 1 ? got : keep;
+              x[h][1] = lane & 1 ? keep : got;
+            }
+            uint32_t z[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t keep = lane & 2 ? x[1][h] : x[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[0][h] : x[1][h], 2);
+              z[h] = lane & 2 ? got : keep;
+              z[2 + h] = lane & 2 ? keep : got;
+            }
+            const int r = 4 * i + (lane & 3);
+            if (r < valid)
+              *reinterpret_cast<uint4*>(p.o_part + (slot * N + row0 + r) * kDim + d0 + (lane & 28)) = make_uint4(z[0], z[1], z[2], z[3]);
+          }
         }
       }
       tc_fence_before();
-      // every softmax warp is done with this segment's row data before the next one's are written
+      if (last) break;
+      // every softmax warp is done with this segment's data, and has written its part of the next one's
       if (!(alive = meet_all(lane, abort_flag))) break;
       if (lane == 0) mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
     }
@@ -1105,15 +1290,20 @@ EncodeFn encode_fn() {
   }();
   return fn;
 }
-// A box is `width` bytes of a page's 16 rows.
-bool encode_map(CUtensorMap* map, const void* cache, int64_t num_pages, uint32_t width, CUtensorMapSwizzle swizzle) {
+// A page as 128-byte columns of its keys (a box: 8 keys of all four), and its rotated parts (a box: 16 keys).
+bool encode_maps(LatentParams& p, const void* cache, int64_t num_pages) {
   const EncodeFn encode = encode_fn();
   if (!encode) return false;
-  const cuuint64_t dims[3] = {kRow, kPage, static_cast<cuuint64_t>(num_pages)};
-  const cuuint64_t strides[2] = {kRow, kRow * kPage};
-  const cuuint32_t box[3] = {width, kPage, 1}, step[3] = {1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t pages = static_cast<cuuint64_t>(num_pages);
+  const cuuint64_t dims[4] = {128, kPage, kColumns, pages}, strides[3] = {kRow, 128, kRow * kPage};
+  const cuuint32_t box[4] = {128, 8, kColumns, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint64_t dims_r[3] = {kRow, kPage, pages}, strides_r[2] = {kRow, kRow * kPage};
+  const cuuint32_t box_r[3] = {MTP_LATENT_ROPE_DIM, kPage, 1};
+  return encode(&p.tmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         encode(&p.tmap_rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims_r, strides_r, box_r, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1140,6 +1330,11 @@ int launch_latent(LatentParams& p, int device, cudaStream_t stream) {
   const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<N>);
   if (!allowed[device].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<N>()) != cudaSuccess) {
+      cudaGetLastError();
+      return MTPATTN_E_LAUNCH;
+    }
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs != kLaunchRegisters) {
       cudaGetLastError();
       return MTPATTN_E_LAUNCH;
     }
@@ -1210,12 +1405,11 @@ extern "C" int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t 
       (status && !ptr_on_device(status, device)))
     return MTPATTN_E_DEVICE;
   LatentParams p{};
-  if (!encode_map(&p.tmap, cache, num_pages, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&p.tmap_rope, cache, num_pages, MTP_LATENT_ROPE_DIM, CU_TENSOR_MAP_SWIZZLE_64B))
-    return MTPATTN_E_LAUNCH;
+  if (!encode_maps(p, cache, num_pages)) return MTPATTN_E_LAUNCH;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride_tok = q_stride_tok;
   p.q_stride_head = q_stride_head;
+  p.cache = static_cast<const uint8_t*>(cache);
   p.num_pages = num_pages;
   p.block_tables = block_tables;
   p.max_pages = max_pages_per_seq;
