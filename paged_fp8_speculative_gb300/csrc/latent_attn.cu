@@ -61,12 +61,15 @@ using namespace sm100;
 constexpr int kRow = MTP_LATENT_ROW, kDim = MTP_LATENT_DIM;
 constexpr int kLatentThreads = 384;
 constexpr int kKeys = 128, kTilePages = kKeys / kPage;
-constexpr int kColumns = 4;                          // of 128 dims; the rotated 64 apart
-constexpr int kAtom = 8 * 128;                       // 8 keys of a column, 128-byte swizzled
-constexpr int kGroup = kColumns * kAtom;             // 8 keys
+constexpr int kColumns = 4;                          // of 128 dims of the output
+constexpr int kSlices = kRow / 64;                   // of 64 dims of a key, the last the rotated ones
+constexpr int kAtom = 8 * 64;                        // 8 keys of a slice, 64-byte swizzled
+constexpr int kGroup = kSlices * kAtom;              // 8 keys
 constexpr int kBlocks = 4, kBlockKeys = kKeys / kBlocks;   // what is fetched and given back at a time
-constexpr int kRopeAt = kKeys / 8 * kGroup, kRopeColumn = kKeys * MTP_LATENT_ROPE_DIM;
-constexpr int kStage = kRopeAt + kRopeColumn;
+constexpr int kRopeAt = (kSlices - 1) * kAtom;       // in a group
+constexpr int kPLow = kKeys * 64;                    // P's second terms
+constexpr int kStage = kKeys / 8 * kGroup;
+static_assert(kStage % 1024 == 0, "Q's operand behind the stages");
 constexpr int kBlockPages = kBlockKeys / kPage;
 constexpr int kWarpBlocks = kBlocks / 2, kWarpPages = kWarpBlocks * kBlockPages;   // of a tile, a fetching warp's
 constexpr int kStages = 2;
@@ -92,7 +95,7 @@ constexpr int off_q() { return kStages * kStage; }
 template <int N>
 constexpr int off_p() { return off_q<N>() + 2 * N * kRow; }
 template <int N>
-constexpr int off_bars() { return off_p<N>() + kRopeColumn; }
+constexpr int off_bars() { return (off_p<N>() + kPLow + 15) / 16 * 16; }
 
 // What the join goes by: a unit's note, written by the CTA that has its first tile.
 struct JoinNote {
@@ -103,7 +106,7 @@ struct JoinNote {
 };
 
 struct LatentParams {
-  CUtensorMap tmap, tmap_rope;
+  CUtensorMap tmap;
   const uint8_t* cache;
   const __nv_bfloat16* q;
   int64_t q_stride_tok, q_stride_head;
@@ -417,33 +420,20 @@ __device__ __forceinline__ void mma_one(uint32_t d_tmem, uint32_t a, uint32_t a_
 }
 // D (+)= A B0, D += A B1: the second product takes A from the collector.  (Measured, M 128, N 64: 78 clocks the
 // pair, 96 with A fetched twice; shared memory gives 128 bytes a clock, and A is 4 KB, B 2 KB.)
-__device__ __forceinline__ void mma_two(uint32_t d_tmem, uint32_t a, uint32_t a_hi, uint32_t b0, uint32_t b1, uint32_t b_hi,
-                                        uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_two(uint32_t d_tmem, uint32_t a, uint32_t a_hi, uint32_t b0, uint32_t b0_hi, uint32_t b1,
+                                        uint32_t b1_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y, z;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %5};\n mov.b64 z, {%4, %5};\n"
-      " setp.ne.b32 p, %7, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], x, y, %6, p;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], x, z, %6, 1;\n}\n" ::"r"(d_tmem),
-      "r"(a), "r"(a_hi), "r"(b0), "r"(b1), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 x, y, z;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n mov.b64 z, {%5, %6};\n"
+      " setp.ne.b32 p, %8, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], x, y, %7, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], x, z, %7, 1;\n}\n" ::"r"(d_tmem),
+      "r"(a), "r"(a_hi), "r"(b0), "r"(b0_hi), "r"(b1), "r"(b1_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
 }
-// 8 keys of a page: four columns of 128 bytes of each, column by column.
-__device__ __forceinline__ void tma_half_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row, int page,
-                                              uint64_t policy) {
-  tma_load_4d(dst, map, bar, 0, row, 0, page, policy);
-}
-__device__ __forceinline__ void tma_rope_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int page, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(kDim), "r"(0), "r"(page), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 __device__ __forceinline__ void st_shared8(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -579,7 +569,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
     constexpr uint32_t kIdesc = idesc_e4m3_f32(128, 2 * N, false);
     const Desc q = desc_of(sdesc_sw128(smem + off_q<N>(), 16, 1024));
     const Desc q_rope = desc_of(sdesc_sw64(smem + off_q<N>() + kColumns * q_column<N>(), 16, 512));
-    const Desc c0 = desc_of(sdesc_sw128(smem, 16, kGroup)), r0 = desc_of(sdesc_sw64(smem + kRopeAt, 16, 512));
+    const Desc c0 = desc_of(sdesc_sw64(smem, 16, kGroup));
     uint32_t u = 0;                                // tiles so far
 #pragma unroll 1
     for (int e = 0;;) {
@@ -621,14 +611,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           for (int c = 0; c < kBlocks; ++c) ok = ok && wait_for(smem_u32(&bars.full[st][c]), parity, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = c0.lo + st * (kStage >> 4), ar = r0.lo + st * (kStage >> 4);
+          const uint32_t a = c0.lo + st * (kStage >> 4);
           mma_one<false>(d, a, c0.hi, q.lo, q.hi, kIdesc);
 #pragma unroll
           for (int k = 1; k < 4 * kColumns; ++k)   // 32 dims
-            mma_one<true>(d, a + (((k >> 2) * kAtom + 32 * (k & 3)) >> 4), c0.hi,
+            mma_one<true>(d, a + (((k >> 1) * kAtom + 32 * (k & 1)) >> 4), c0.hi,
                           q.lo + (((k >> 2) * q_column<N>() + 32 * (k & 3)) >> 4), q.hi, kIdesc);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) mma_one<true>(d, ar + (32 * k >> 4), r0.hi, q_rope.lo + (32 * k >> 4), q_rope.hi, kIdesc);
+          for (int k = 0; k < 2; ++k) mma_one<true>(d, a + ((kRopeAt + 32 * k) >> 4), c0.hi, q_rope.lo + (32 * k >> 4), q_rope.hi, kIdesc);
           mma_commit(smem_u32(&bars.s_full[u & 1]));
         }
       }
@@ -652,10 +642,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
   } else if (warp >= 2) {
     // ============================== the tiles by TMA, two blocks a warp ===========================
     const int first = (warp - 2) * kWarpBlocks;
-    if (lane == 0) {
-      prefetch_tmap(&p.tmap);
-      prefetch_tmap(&p.tmap_rope);
-    }
+    if (lane == 0) prefetch_tmap(&p.tmap);
     const uint64_t once = l2_policy_evict_first();
     uint64_t again;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
@@ -684,8 +671,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           now = ahead;
           ahead = entries(t + 32 / kWarpPages);
         }
-        // lanes 0-3 of 6 a half page's latent vectors each, 4-5 a page's rotated parts; the next 6 the second
-        // block's, were there no wait between them
+        // a lane half a page
         const int np = min(kTilePages, pages - t * kTilePages) - first * kBlockPages;   // this warp's, if above 0
         const int mine = __shfl_sync(0xffffffffu, now, k * kWarpPages + lane % kWarpPages);
         const bool bad = __any_sync(0xffffffffu, lane < min(np, kWarpPages) && (mine < 0 || mine >= p.num_pages));
@@ -702,6 +688,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
               (t + kPrefetch) * kTilePages + first * kBlockPages + lane < pages && far >= 0 && far < p.num_pages)
             prefetch_l2(p.cache + static_cast<int64_t>(far) * (kPage * kRow), kPage * kRow);
         }
+        // At first all CTAs ask at once: the first tile, then Q, which the first product wants too, then more.
+        if (u == 1 && !(ok = warp_wait(smem_u32(&bars.q_full), 0, abort_flag))) break;
         const int st = u % kStages;
         const uint32_t stage = smem + st * kStage;
 #pragma unroll 1
@@ -715,15 +703,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             if (here == 0) mbar_arrive(bar);       // (of a bad page nothing: the segment's rows become zeros)
             else mbar_arrive_expect_tx(bar, here * kPage * kRow);
           }
-          const int i = lane < 4 ? lane >> 1 : lane & 1;
-          const int pg = __shfl_sync(0xffffffffu, mine, c * kBlockPages + i);
-          if (lane < 6 && i < here) {
-            const int at = (first + c) * kBlockPages + i;        // page of the tile
-            if (lane < 4)
-              tma_half_page(stage + (2 * at + (lane & 1)) * kGroup, &p.tmap, bar, (lane & 1) * 8, pg, policy);
-            else
-              tma_rope_page(stage + kRopeAt + at * (kPage * MTP_LATENT_ROPE_DIM), &p.tmap_rope, bar, pg, policy);
-          }
+          const int pg = __shfl_sync(0xffffffffu, mine, (c * kBlockPages + (lane >> 1)) % kWarpPages);
+          if (lane < 2 * here)
+            tma_load_4d(stage + (2 * (first + c) * kBlockPages + lane) * kGroup, &p.tmap, bar, 0, (lane & 1) * 8, 0, pg, policy);
           __syncwarp();
         }
         if (!ok) break;
@@ -746,8 +728,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
     if (elect_one()) {
       auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_for(smem_u32(&bar), parity, abort_flag); };
       constexpr uint32_t kIdesc = idesc_e4m3_f32(128, N, true) | kAMajorM;
-      const Desc lo = desc_of(sdesc_sw64(smem + off_p<N>(), 512, 512)), hi = desc_of(sdesc_sw64(smem + kRopeAt, 512, 512));
-      const Desc v0 = desc_of(sdesc_sw128(smem, kAtom, kGroup));
+      const Desc lo = desc_of(sdesc_sw64(smem + off_p<N>(), 512, 512)), hi = desc_of(sdesc_sw64(smem + kRopeAt, 512, kGroup));
+      const Desc v0 = desc_of(sdesc_sw64(smem, kAtom, kGroup));
       uint32_t u = 0;
       bool alive = true;
 #pragma unroll 1
@@ -768,8 +750,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             // Both terms of P one after the other, the second with the A operand that the first has brought in.
 #pragma unroll
             for (int c = 0; c < kColumns; ++c)
-              mma_two(tmem + kOCol + c * N, v0.lo + at + ((k * (kBlockKeys / 8) * kGroup + c * kAtom) >> 4), v0.hi,
-                      lo.lo + (k * kBlockKeys * 64 >> 4), hi.lo + at + (k * kBlockKeys * 64 >> 4), lo.hi, kIdesc, k ? 1u : more);
+              mma_two(tmem + kOCol + c * N, v0.lo + at + ((k * (kBlockKeys / 8) * kGroup + 2 * c * kAtom) >> 4), v0.hi,
+                      lo.lo + (k * kBlockKeys * 64 >> 4), lo.hi, hi.lo + at + (k * (kBlockKeys / 8) * kGroup >> 4), hi.hi, kIdesc,
+                      k ? 1u : more);
             mma_commit(smem_u32(&bars.empty[st][k]));    // (with the rows of both of P's terms)
           }
           if (!alive) break;
@@ -971,7 +954,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         const uint32_t stage = smem + (u % kStages) * kStage;
         const uint32_t swz = (key >> 1) & 3;
         auto write = [&](uint32_t at, const uint32_t (&x)[kHalf / 4]) {
-          at += key * 64;
+          at += (key & 7) * 64;
           if constexpr (kHalf == 8) {
             st_shared8(at + (swz << 4) + half * 8, x[0], x[1]);
           } else {
@@ -980,18 +963,18 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
               st_shared16(at + (((half * (kHalf / 16) + i) ^ swz) << 4), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         };
-        write(stage + kRopeAt, hi);
+        write(stage + (key >> 3) * kGroup + kRopeAt, hi);
         // the previous tile's second terms of these keys have been read: a quarter is a block
         if (u > 0 &&
             !(alive = warp_wait(smem_u32(&bars.empty[(u - 1) % kStages][quarter]), ((u - 1) / kStages) & 1, abort_flag)))
           break;
-        write(smem + off_p<N>(), lo);
+        write(smem + off_p<N>() + (key >> 3) * kAtom, lo);
         if (ragged && j >= start) {
           // this half's 256 of the key's values: none behind the sequence, no NaN among the new tokens
 #pragma unroll 1
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t at = stage + (key >> 3) * kGroup + (2 * half + (i >> 3)) * kAtom + (key & 7) * 128 +
-                                (((i + key) & 7) << 4);   // (any order; this one meets all banks)
+          for (int i = 0; i < 16; ++i) {             // (in any order; this one meets all banks)
+            const uint32_t at = stage + (key >> 3) * kGroup + (4 * half + (i >> 2)) * kAtom + (key & 7) * 64 +
+                                (((i + (key >> 1)) & 3) << 4);
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (j < s.L) {
               x = ld_shared16(at);
@@ -1290,19 +1273,13 @@ EncodeFn encode_fn() {
   }();
   return fn;
 }
-// A page as 128-byte columns of its keys (a box: 8 keys of all four), and its rotated parts (a box: 16 keys).
-bool encode_maps(LatentParams& p, const void* cache, int64_t num_pages) {
+// A page as slices of 64 dims of its keys; a box is all slices of 8 keys.
+bool encode_map(CUtensorMap* map, const void* cache, int64_t num_pages) {
   const EncodeFn encode = encode_fn();
   if (!encode) return false;
-  const cuuint64_t pages = static_cast<cuuint64_t>(num_pages);
-  const cuuint64_t dims[4] = {128, kPage, kColumns, pages}, strides[3] = {kRow, 128, kRow * kPage};
-  const cuuint32_t box[4] = {128, 8, kColumns, 1}, step[4] = {1, 1, 1, 1};
-  const cuuint64_t dims_r[3] = {kRow, kPage, pages}, strides_r[2] = {kRow, kRow * kPage};
-  const cuuint32_t box_r[3] = {MTP_LATENT_ROPE_DIM, kPage, 1};
-  return encode(&p.tmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
-         encode(&p.tmap_rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims_r, strides_r, box_r, step,
+  const cuuint64_t dims[4] = {64, kPage, kSlices, static_cast<cuuint64_t>(num_pages)}, strides[3] = {kRow, 64, kRow * kPage};
+  const cuuint32_t box[4] = {64, 8, kSlices, 1}, step[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1405,7 +1382,7 @@ extern "C" int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t 
       (status && !ptr_on_device(status, device)))
     return MTPATTN_E_DEVICE;
   LatentParams p{};
-  if (!encode_maps(p, cache, num_pages)) return MTPATTN_E_LAUNCH;
+  if (!encode_map(&p.tmap, cache, num_pages)) return MTPATTN_E_LAUNCH;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride_tok = q_stride_tok;
   p.q_stride_head = q_stride_head;
