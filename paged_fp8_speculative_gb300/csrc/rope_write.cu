@@ -1,11 +1,11 @@
 // Rotary positions, rounding to e4m3 and the way of new tokens into the paged caches: the three entry
 // points of mtp_rope.h are one kernel over streams of rows (q, k, v; or a latent vector and its rotated part).
 //
-// Bound by the bytes: each input is read once, in blocks of 8 elements, and each output written once (16
-// bytes of bf16, 8 codes).  A thread's item is a block of 8 elements, or in the half layout the two blocks
-// whose elements are each other's partners, so that q can be rotated in place.  What the heads of a token
-// share is worked out once per CTA: the token's place in the cache (a warp a token, 32 boundaries of
-// cu_seqlens_q at a time) and its sines and cosines.
+// Bound by the bytes: each input is read once, 16 bytes at a time, and each output written once.  A thread's
+// item is 16 elements of a row: a run, or in the half layout two runs of 8 whose elements are each other's
+// partners, so that q can be rotated in place.  All streams' items of a CTA's tokens are one list.  What the
+// heads of a token share is worked out once per CTA, while the first items are on their way: the token's place
+// in the cache (a warp a token, 32 boundaries of cu_seqlens_q at a time) and its sines and cosines.
 //
 // Angles are 64-bit fixed-point turns: position * freq modulo 2^64 drops whole turns exactly, and the
 // upper 32 bits, at most 2^-33 turns off, go to sincospif: no loss at far positions, no FP64.
@@ -28,6 +28,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kMaxTokens = 8;              // tokens of a CTA: a warp looks each up
 constexpr int kMaxPairs = 128;             // rotated pairs of a head
+constexpr int kManyCtas = 8;               // an SM
 
 enum Target { kRowsBf16, kRowsCodes, kPageCodes };
 
@@ -37,16 +38,16 @@ struct Stream {
   void* dst;
   int64_t d_tok, d_head;                   // elements (bytes of codes); d_tok of a page: bytes a token
   const float* descale;
-  int32_t heads, blocks;                   // blocks of 8 elements a row
-  int32_t items;                           // a row's: its blocks, less one for each pair of blocks
-  int32_t rot0;                            // first rotated element; the rotated ones are rot_dim or none
-  int32_t rot;
+  int32_t end;                             // items a token of this stream and the ones before it
+  int32_t row_items;                       // items a row: 16 elements each
+  uint32_t row_inverse;                    // ceil(2^32 / row_items)
+  int32_t rot0, rot;                       // first rotated element, how many
   int32_t target;
 };
+constexpr int kStreams = 4;
 
 struct RopeParams {
-  Stream s[4];
-  int32_t streams;
+  Stream s[kStreams];                      // those that are not there: no items
   int32_t total, tokens;                   // tokens a CTA
   const int32_t* positions;
   const int64_t* freqs;
@@ -62,28 +63,34 @@ struct RopeParams {
   int32_t* status;
 };
 
+// 8 elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+struct Raw8 {
+  uint4 w[sizeof(T) * 8 / 16];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) * 8 / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+};
+__device__ __forceinline__ void widen8(const Raw8<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.w[i].x);
+    x[4 * i + 1] = __uint_as_float(r.w[i].y);
+    x[4 * i + 2] = __uint_as_float(r.w[i].z);
+    x[4 * i + 3] = __uint_as_float(r.w[i].w);
+  }
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void widen8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float (&x)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void widen8(const Raw8<__half>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -91,7 +98,6 @@ __device__ __forceinline__ void load8<__half>(const __half* p, float (&x)[8]) {
     x[2 * i + 1] = f.y;
   }
 }
-
 __device__ __forceinline__ void store8_bf16(__nv_bfloat16* p, const float (&x)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -101,13 +107,20 @@ __device__ __forceinline__ void store8_bf16(__nv_bfloat16* p, const float (&x)[8
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8_codes(uint8_t* p, const float (&x)[8], float scale) {
+// (a, b) * f in one instruction
+__device__ __forceinline__ void scale_pair(float& a, float& b, float f) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(f));
+}
+__device__ __forceinline__ uint2 codes8(float (&x)[8], float scale) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * scale, x[2 * i + 1] * scale), __NV_SATFINITE,
-                                    __NV_E4M3);
-  *reinterpret_cast<uint2*>(p) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  for (int i = 0; i < 4; ++i) {
+    scale_pair(x[2 * i], x[2 * i + 1], scale);
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
 // The sequence of row t: the last b with cu[b] <= t (32 boundaries at a time), or -1 where row t is
@@ -127,111 +140,155 @@ __device__ int find_sequence(const int32_t* cu, int num_seqs, int t, int lane) {
   return lo;
 }
 
+// One item: where it comes from and goes to.
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads)
-rope_write_kernel(const RopeParams p) {
-  __shared__ float2 s_turn[kMaxTokens][kMaxPairs];    // mscale * (cos, sin)
-  __shared__ int64_t s_place[kMaxTokens];             // row of the cache, -1: none
-  __shared__ bool s_known[kMaxTokens];                // the token belongs to a sequence
+struct Item {
+  Raw8<T> x, y;              // its 8 first elements, and the others
+  int e, e2;                 // where they stand in the row
+  int tok, k;                // token of the CTA, stream
+  int64_t dst;               // of its row, but for the token's part
+  bool rotated;
+
+  // item i of the CTA's list
+  __device__ __forceinline__ void fetch(const RopeParams& p, int i, int t0, int a_token) {
+    tok = static_cast<int>(static_cast<float>(i) * (1.f / static_cast<float>(a_token)));   // off by one at most
+    if (tok * a_token > i) --tok;
+    else if ((tok + 1) * a_token <= i) ++tok;
+    int j = i - tok * a_token;
+    k = (j >= p.s[0].end) + (j >= p.s[1].end) + (j >= p.s[2].end);
+    const Stream& s = p.s[k];
+    if (k) j -= p.s[k - 1].end;
+    const int head = static_cast<int>(__umulhi(j, s.row_inverse));   // (exact: j < 2^22, row_items <= 32)
+    const int item = j - head * s.row_items;
+    // half layout: the pairs of runs first, then what is not rotated
+    e = 16 * item;
+    e2 = e + 8;
+    if (kInterleaved) {
+      rotated = e >= s.rot0 && e < s.rot0 + s.rot;
+    } else {
+      rotated = 16 * item < s.rot;
+      if (rotated) {
+        e = s.rot0 + 8 * item;
+        e2 = e + s.rot / 2;
+      } else if (e - s.rot < s.rot0) {
+        e -= s.rot;
+        e2 -= s.rot;
+      }
+    }
+    dst = head * s.d_head;
+    const T* src = static_cast<const T*>(s.src) + (t0 + tok) * s.s_tok + head * s.s_head;
+    x.load(src + e);
+    y.load(src + e2);
+  }
+  // turn: of the item's token; at: the token's row of the output or the cache
+  __device__ __forceinline__ void store(const RopeParams& p, const float2* turn, int64_t at) const {
+    const Stream& s = p.s[k];
+    float a[8], b[8];
+    widen8(x, a);
+    widen8(y, b);
+    if (rotated) {
+      const float4* c = reinterpret_cast<const float4*>(turn + (kInterleaved ? (e - s.rot0) / 2 : e - s.rot0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = c[i];                       // cosine and sine of two pairs
+        if (kInterleaved) {
+          float(&v)[8] = i < 2 ? a : b;
+          const int h = 4 * (i & 1);
+          const float v0 = v[h], v1 = v[h + 1], v2 = v[h + 2], v3 = v[h + 3];
+          v[h] = v0 * f.x - v1 * f.y;
+          v[h + 1] = v1 * f.x + v0 * f.y;
+          v[h + 2] = v2 * f.z - v3 * f.w;
+          v[h + 3] = v3 * f.z + v2 * f.w;
+        } else {
+          const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
+          a[2 * i] = a0 * f.x - b0 * f.y;
+          b[2 * i] = b0 * f.x + a0 * f.y;
+          a[2 * i + 1] = a1 * f.z - b1 * f.w;
+          b[2 * i + 1] = b1 * f.z + a1 * f.w;
+        }
+      }
+    }
+    if (s.target == kRowsBf16) {
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(s.dst) + at * s.d_tok + dst;
+      store8_bf16(out + e, a);
+      store8_bf16(out + e2, b);
+    } else {
+      const float scale = 1.f / *s.descale;
+      uint8_t* out = static_cast<uint8_t*>(s.dst) + at * s.d_tok + dst;
+      const uint2 u = codes8(a, scale), v = codes8(b, scale);
+      if (kInterleaved || !rotated) {
+        *reinterpret_cast<uint4*>(out + e) = make_uint4(u.x, u.y, v.x, v.y);
+      } else {
+        *reinterpret_cast<uint2*>(out + e) = u;
+        *reinterpret_cast<uint2*>(out + e2) = v;
+      }
+    }
+  }
+};
+
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ alignas(16) float2 s_turn[kMaxTokens][kMaxPairs];    // mscale * (cos, sin)
+  __shared__ int64_t s_place[kMaxTokens];             // row of the cache, kNoPlace or kNotOwned
+  constexpr int64_t kNoPlace = -1, kNotOwned = -2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * p.tokens;
   const int n = min(p.tokens, p.total - t0);
-  if (warp < n) {
+  const int a_token = p.s[kStreams - 1].end, items = n * a_token;
+  const int stride = gridDim.y * kRopeThreads;
+  int i = blockIdx.y * kRopeThreads + tid;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // what came before on the stream is done
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  Item<T, kInterleaved> it;
+  if (i < items) it.fetch(p, i, t0, a_token);
+  for (int j = tid; j < n * p.pairs; j += kRopeThreads) {
+    const int tok = j / p.pairs, pair = j - tok * p.pairs;
+    const int64_t m = p.positions[t0 + tok];
+    const uint64_t turn = static_cast<uint64_t>(m) * static_cast<uint64_t>(p.freqs[pair]);
+    // half turns in [-1, 1): the upper 32 bits, rounded
+    const int32_t top = static_cast<int32_t>(static_cast<uint32_t>(turn >> 32));
+    float sn, cs;
+    sincospif(static_cast<float>(top) * 0x1p-31f, &sn, &cs);
+    s_turn[tok][pair] = make_float2(cs * p.mscale, sn * p.mscale);
+  }
+  if (p.cu_q && warp < n) {
     const int t = t0 + warp;
-    if (p.pairs) {
-      const int64_t m = p.positions[t];
-      for (int i = lane; i < p.pairs; i += 32) {
-        const uint64_t turn = static_cast<uint64_t>(m) * static_cast<uint64_t>(p.freqs[i]);
-        // half turns in [-1, 1): the upper 32 bits, rounded
-        const int32_t top = static_cast<int32_t>(static_cast<uint32_t>(turn >> 32));
-        float sn, cs;
-        sincospif(static_cast<float>(top) * 0x1p-31f, &sn, &cs);
-        s_turn[warp][i] = make_float2(cs * p.mscale, sn * p.mscale);
-      }
-    }
-    if (p.cu_q) {
-      const int b = find_sequence(p.cu_q, p.num_seqs, t, lane);
-      if (lane == 0) {
-        int64_t place = -1;
-        bool known = false;
-        int err = 0;
-        if (b >= 0) {
-          const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], len = p.seq_lens[b];
-          if (q0 < 0 || q0 > t || q1 <= t || q1 > p.total) {
-            err = MTPATTN_ERR_QLEN;
-          } else {
-            known = true;
-            if (q1 - q0 > len) err = MTPATTN_ERR_QLEN_GT_SEQ;
-            else if (len > p.max_pages * kPage) err = MTPATTN_ERR_SEQ_TOO_LONG;
-            else {
-              const int at = len - (q1 - t);
-              const int page = p.bt[static_cast<int64_t>(b) * p.max_pages + at / kPage];
-              if (page < 0 || page >= p.num_pages) err = MTPATTN_ERR_PAGE;
-              else place = static_cast<int64_t>(page) * kPage + at % kPage;
-            }
+    const int b = find_sequence(p.cu_q, p.num_seqs, t, lane);
+    if (lane == 0) {
+      int64_t place = kNotOwned;
+      int err = 0;
+      if (b >= 0) {
+        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], len = p.seq_lens[b];
+        if (q0 < 0 || q0 > t || q1 <= t || q1 > p.total) {
+          err = MTPATTN_ERR_QLEN;
+        } else {
+          place = kNoPlace;
+          if (q1 - q0 > len) err = MTPATTN_ERR_QLEN_GT_SEQ;
+          else if (len > p.max_pages * kPage) err = MTPATTN_ERR_SEQ_TOO_LONG;
+          else {
+            const int at = len - (q1 - t);
+            const int page = p.bt[static_cast<int64_t>(b) * p.max_pages + at / kPage];
+            if (page < 0 || page >= p.num_pages) err = MTPATTN_ERR_PAGE;
+            else place = static_cast<int64_t>(page) * kPage + at % kPage;
           }
         }
-        if (err) set_status(p.status, err);
-        s_place[warp] = place;
-        s_known[warp] = known;
       }
-    } else if (lane == 0) {
-      s_known[warp] = true;
+      if (err) set_status(p.status, err);
+      s_place[warp] = place;
     }
   }
   __syncthreads();
-
-  const int first = blockIdx.y * kRopeThreads + tid, stride = gridDim.y * kRopeThreads;
-  for (int k = 0; k < p.streams; ++k) {
-    const Stream& s = p.s[k];
-    const int row_items = s.heads * s.items;
-    float scale = 1.f;
-    if (s.target != kRowsBf16) scale = 1.f / *s.descale;
-    for (int j = first; j < n * row_items; j += stride) {
-      const int tok = j / row_items, rest = j - tok * row_items;
-      const int head = rest / s.items, item = rest - head * s.items;
-      if (!s_known[tok] || (s.target == kPageCodes && s_place[tok] < 0)) continue;
-      const T* src = static_cast<const T*>(s.src) + (t0 + tok) * s.s_tok + head * s.s_head;
-      const int64_t out = (s.target == kPageCodes ? s_place[tok] : t0 + tok) * s.d_tok + head * s.d_head;
-      // half layout: the pairs of blocks first, then the blocks outside the rotated part
-      int e = item * 8, partner = -1;
-      if (!kInterleaved && s.rot) {
-        if (item < s.rot / 16) {
-          e += s.rot0;
-          partner = e + s.rot / 2;
-        } else {
-          e -= s.rot / 2;
-          if (e >= s.rot0) e += s.rot;
-        }
-      }
-      float x[8], y[8];
-      load8(src + e, x);
-      if (!kInterleaved && partner >= 0) {
-        load8(src + partner, y);
-        const float2* turn = &s_turn[tok][e - s.rot0];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 c = turn[i];
-          const float a = x[i], b = y[i];
-          x[i] = a * c.x - b * c.y;
-          y[i] = b * c.x + a * c.y;
-        }
-        if (s.target == kRowsBf16) store8_bf16(static_cast<__nv_bfloat16*>(s.dst) + out + partner, y);
-        else store8_codes(static_cast<uint8_t*>(s.dst) + out + partner, y, scale);
-      }
-      if (kInterleaved && e >= s.rot0 && e < s.rot0 + s.rot) {
-        const float2* turn = &s_turn[tok][(e - s.rot0) / 2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 c = turn[i];
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = a * c.x - b * c.y;
-          x[2 * i + 1] = b * c.x + a * c.y;
-        }
-      }
-      if (s.target == kRowsBf16) store8_bf16(static_cast<__nv_bfloat16*>(s.dst) + out + e, x);
-      else store8_codes(static_cast<uint8_t*>(s.dst) + out + e, x, scale);
+  while (i < items) {
+    const Item<T, kInterleaved> now = it;
+    i += stride;
+    if (i < items) it.fetch(p, i, t0, a_token);      // the next one is on its way
+    int64_t at = t0 + now.tok;
+    if (p.cu_q) {
+      const int64_t place = s_place[now.tok];
+      if (place == kNotOwned) continue;
+      if (p.s[now.k].target == kPageCodes) at = place;
     }
+    if (at >= 0) now.store(p, s_turn[now.tok], at);
   }
 }
 
@@ -241,10 +298,12 @@ bool rows_ok(const void* p, int64_t s_tok, int64_t s_head) {
   return p && ptr_aligned(p, 16) && s_tok > 0 && s_head > 0 && (s_tok | s_head) % 8 == 0;
 }
 
-Stream stream(const void* src, int64_t s_tok, int64_t s_head, void* dst, int64_t d_tok, int64_t d_head,
-              const float* descale, int32_t heads, int32_t dim, int32_t rot0, int32_t rot, bool interleaved,
-              Target target) {
-  Stream s{};
+// The next stream of a call.
+void add(RopeParams& p, const void* src, int64_t s_tok, int64_t s_head, void* dst, int64_t d_tok, int64_t d_head,
+         const float* descale, int32_t heads, int32_t dim, int32_t rot0, int32_t rot, Target target) {
+  int k = 0;
+  while (p.s[k].row_items) ++k;
+  Stream& s = p.s[k];
   s.src = src;
   s.s_tok = s_tok;
   s.s_head = s_head;
@@ -252,30 +311,41 @@ Stream stream(const void* src, int64_t s_tok, int64_t s_head, void* dst, int64_t
   s.d_tok = d_tok;
   s.d_head = d_head;
   s.descale = descale;
-  s.heads = heads;
-  s.blocks = dim / 8;
-  s.items = dim / 8 - (interleaved ? 0 : rot / 16);
+  s.row_items = dim / 16;
+  s.row_inverse = static_cast<uint32_t>(((1ull << 32) + s.row_items - 1) / s.row_items);
   s.rot0 = rot0;
   s.rot = rot;
   s.target = target;
-  return s;
+  const int32_t end = (k ? p.s[k - 1].end : 0) + heads * s.row_items;
+  for (; k < kStreams; ++k) p.s[k].end = end;
 }
 
 template <typename T>
-cudaError_t launch_typed(const RopeParams& p, dim3 grid, bool interleaved, cudaStream_t st) {
-  if (interleaved) rope_write_kernel<T, true><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_write_kernel<T, false><<<grid, kRopeThreads, 0, st>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_typed(RopeParams& p, dim3 grid, bool interleaved, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = interleaved ? cudaLaunchKernelEx(&cfg, rope_write_kernel<T, true>, p)
+                                    : cudaLaunchKernelEx(&cfg, rope_write_kernel<T, false>, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 int launch_rope(RopeParams& p, int32_t dtype, bool interleaved, int device, void* stream) {
-  int64_t items = 0;
-  for (int k = 0; k < p.streams; ++k) items += static_cast<int64_t>(p.s[k].heads) * p.s[k].items;
   const int sms = device_sm_count(device);
   if (sms <= 0) return MTPATTN_E_DEVICE;
-  p.tokens = 1;
-  const int64_t slices = std::max<int64_t>(1, std::min<int64_t>((items + kRopeThreads - 1) / kRopeThreads,
-                                                                 8 * sms / std::max(1, p.total)));
+  const int64_t a_token = p.s[kStreams - 1].end;
+  // Several tokens a CTA where there are many, so that its start counts less; several CTAs a token where
+  // there are few.
+  p.tokens = std::max(1, std::min(kMaxTokens, p.total / (kManyCtas * sms)));
+  const int64_t slices = std::max<int64_t>(1, std::min<int64_t>((a_token + kRopeThreads - 1) / kRopeThreads,
+                                                                kManyCtas * sms / p.total));
   const dim3 grid((p.total + p.tokens - 1) / p.tokens, static_cast<unsigned>(slices));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == MTP_F32    ? launch_typed<float>(p, grid, interleaved, st)
@@ -370,12 +440,10 @@ extern "C" int mtp_rope_append(const void* q, int64_t q_stride_tok, int64_t q_st
   const int64_t row = static_cast<int64_t>(num_kv_heads) * kHeadDim;
   RopeParams p{};
   if (q)
-    p.s[p.streams++] = stream(q, q_stride_tok, q_stride_head, q_out, q_out_stride_tok, q_out_stride_head, nullptr,
-                              num_q_heads, kHeadDim, 0, rot_dim, il, kRowsBf16);
-  p.s[p.streams++] = stream(k, k_stride_tok, k_stride_head, k_cache, row, kHeadDim, k_descale, num_kv_heads,
-                            kHeadDim, 0, rot_dim, il, kPageCodes);
-  p.s[p.streams++] = stream(v, v_stride_tok, v_stride_head, v_cache, row, kHeadDim, v_descale, num_kv_heads,
-                            kHeadDim, 0, 0, il, kPageCodes);
+    add(p, q, q_stride_tok, q_stride_head, q_out, q_out_stride_tok, q_out_stride_head, nullptr, num_q_heads, kHeadDim, 0,
+        rot_dim, kRowsBf16);
+  add(p, k, k_stride_tok, k_stride_head, k_cache, row, kHeadDim, k_descale, num_kv_heads, kHeadDim, 0, rot_dim, kPageCodes);
+  add(p, v, v_stride_tok, v_stride_head, v_cache, row, kHeadDim, v_descale, num_kv_heads, kHeadDim, 0, 0, kPageCodes);
   p.total = total_q;
   p.positions = positions;
   p.freqs = freqs;
@@ -429,12 +497,11 @@ extern "C" int mtp_rope_latent_append(const void* q_rope, int64_t q_stride_tok, 
   const bool il = interleaved != 0;
   RopeParams p{};
   if (q_rope)
-    p.s[p.streams++] = stream(q_rope, q_stride_tok, q_stride_head, q_out, q_out_stride_tok, q_out_stride_head,
-                              nullptr, num_heads, MTP_LATENT_ROPE_DIM, 0, MTP_LATENT_ROPE_DIM, il, kRowsBf16);
-  p.s[p.streams++] = stream(latent, latent_stride, 0, cache, MTP_LATENT_ROW, 0, descale, 1, MTP_LATENT_DIM, 0, 0,
-                            il, kPageCodes);
-  p.s[p.streams++] = stream(k_rope, k_rope_stride, 0, static_cast<uint8_t*>(cache) + MTP_LATENT_DIM, MTP_LATENT_ROW,
-                            0, descale, 1, MTP_LATENT_ROPE_DIM, 0, MTP_LATENT_ROPE_DIM, il, kPageCodes);
+    add(p, q_rope, q_stride_tok, q_stride_head, q_out, q_out_stride_tok, q_out_stride_head, nullptr, num_heads,
+        MTP_LATENT_ROPE_DIM, 0, MTP_LATENT_ROPE_DIM, kRowsBf16);
+  add(p, latent, latent_stride, 0, cache, MTP_LATENT_ROW, 0, descale, 1, MTP_LATENT_DIM, 0, 0, kPageCodes);
+  add(p, k_rope, k_rope_stride, 0, static_cast<uint8_t*>(cache) + MTP_LATENT_DIM, MTP_LATENT_ROW, 0, descale, 1,
+      MTP_LATENT_ROPE_DIM, 0, MTP_LATENT_ROPE_DIM, kPageCodes);
   p.total = total_q;
   p.positions = positions;
   p.freqs = freqs;
@@ -476,15 +543,14 @@ extern "C" int mtp_rope_prefill(const void* q, int64_t q_stride_tok, int64_t q_s
   if (!all_on_device(ptrs, device)) return MTPATTN_E_DEVICE;
   const bool il = interleaved != 0;
   RopeParams p{};
-  p.streams = 4;
-  p.s[0] = stream(q, q_stride_tok, q_stride_head, q8, static_cast<int64_t>(num_q_heads) * kQk, kQk, q_descale,
-                  num_q_heads, kQk, kNope, kRot, il, kRowsCodes);
-  p.s[1] = stream(k, k_stride_tok, k_stride_head, k8, static_cast<int64_t>(num_kv_heads) * kQk, kQk, k_descale,
-                  num_kv_heads, kNope, 0, 0, il, kRowsCodes);
-  p.s[2] = stream(k_rope, k_rope_stride, 0, static_cast<uint8_t*>(k8) + kNope,
-                  static_cast<int64_t>(num_kv_heads) * kQk, kQk, k_descale, num_kv_heads, kRot, 0, kRot, il, kRowsCodes);
-  p.s[3] = stream(v, v_stride_tok, v_stride_head, v8, static_cast<int64_t>(num_kv_heads) * kV, kV, v_descale,
-                  num_kv_heads, kV, 0, 0, il, kRowsCodes);
+  const int64_t k_row = static_cast<int64_t>(num_kv_heads) * kQk;
+  add(p, q, q_stride_tok, q_stride_head, q8, static_cast<int64_t>(num_q_heads) * kQk, kQk, q_descale, num_q_heads, kQk, kNope,
+      kRot, kRowsCodes);
+  add(p, k, k_stride_tok, k_stride_head, k8, k_row, kQk, k_descale, num_kv_heads, kNope, 0, 0, kRowsCodes);
+  add(p, k_rope, k_rope_stride, 0, static_cast<uint8_t*>(k8) + kNope, k_row, kQk, k_descale, num_kv_heads, kRot, 0, kRot,
+      kRowsCodes);
+  add(p, v, v_stride_tok, v_stride_head, v8, static_cast<int64_t>(num_kv_heads) * kV, kV, v_descale, num_kv_heads, kV, 0, 0,
+      kRowsCodes);
   p.total = total;
   p.positions = positions;
   p.freqs = freqs;
