@@ -28,7 +28,8 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kMaxTokens = 8;              // tokens of a CTA: a warp looks each up
 constexpr int kMaxPairs = 128;             // rotated pairs of a head
-constexpr int kManyCtas = 8;               // an SM
+constexpr int kResident = 4;               // CTAs an SM holds
+constexpr int kCtaItems = 16 * kRopeThreads;
 
 enum Target { kRowsBf16, kRowsCodes, kPageCodes };
 
@@ -341,11 +342,12 @@ int launch_rope(RopeParams& p, int32_t dtype, bool interleaved, int device, void
   const int sms = device_sm_count(device);
   if (sms <= 0) return MTPATTN_E_DEVICE;
   const int64_t a_token = p.s[kStreams - 1].end;
-  // Several tokens a CTA where there are many, so that its start counts less; several CTAs a token where
-  // there are few.
-  p.tokens = std::max(1, std::min(kMaxTokens, p.total / (kManyCtas * sms)));
-  const int64_t slices = std::max<int64_t>(1, std::min<int64_t>((a_token + kRopeThreads - 1) / kRopeThreads,
-                                                                kManyCtas * sms / p.total));
+  // Several CTAs a token where there are few; several tokens a CTA where there are more than the GPU holds
+  // CTAs at once, so that a CTA's start counts less, but not so many that its end does.
+  const int64_t room = kResident * static_cast<int64_t>(sms);
+  p.tokens = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min<int64_t>({kMaxTokens, kCtaItems / a_token, (p.total + room - 1) / room})));
+  const int64_t slices = std::max<int64_t>(1, std::min((a_token + kRopeThreads - 1) / kRopeThreads, room / p.total));
   const dim3 grid((p.total + p.tokens - 1) / p.tokens, static_cast<unsigned>(slices));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == MTP_F32    ? launch_typed<float>(p, grid, interleaved, st)
