@@ -83,7 +83,7 @@ constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at 
                                                      // 2^(kShift + kTau) = 430 < 448
 constexpr float kRoom = 4.f;                         // a raised reference is so far above the row's maximum
 constexpr float kNoRef = -1e30f;                     // no key seen yet
-constexpr int kUnitTiles = 7;
+constexpr int kUnitTiles = 7, kCutTiles = 4, kCutPieces = 40;
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kBadSum = 0x7fd0bad1u;            // a sum of a sequence with a bad page (a NaN that no
                                                      // arithmetic makes)
@@ -211,7 +211,8 @@ __device__ __forceinline__ int add_up_to_max(int a, int b) {
 // A CTA's walk over the units of its piece, by one warp; 32 sequences are held, one a lane.
 template <int N>
 struct Walker {
-  int pos, hi, lo, C, length, units;
+  int pos, hi, lo, length, units;
+  int C, V;                            // places of a piece; of a unit where none is cut (C is a multiple), else 0
   int b0, before, units_before;        // the held sequences; the line and the units before them
   Seq mine;
   int upto, units_upto;                // running sums of the held sequences' weights and units
@@ -220,13 +221,14 @@ struct Walker {
   __device__ __forceinline__ void start(const LatentParams& p, int lane) {
     b0 = before = units_before = unit = unit0 = unit_places = 0;
     mine = seq_at<N>(p, lane);
-    int w = mine.w, n = mine.n, T = mine.T;
+    int w = mine.w, n = mine.n, T = mine.T, longest = mine.nt;
 #pragma unroll 1
     for (int b = 32; b < p.num_seqs; b += 32) {
       const Seq x = seq_at<N>(p, b + lane);
       w = add_up_to_max(w, x.w);
       n = add_up_to_max(n, x.n);
       T = add_up_to_max(T, x.T);
+      longest = max(longest, x.nt);
     }
     int64_t W = warp_total(w), U = warp_total(T);
     const int64_t rows = warp_total(n);
@@ -239,11 +241,24 @@ struct Walker {
     length = static_cast<int>(W);
     units = static_cast<int>(U);
     C = max(1, static_cast<int>((W + p.ctas - 1) / p.ctas));
-    upto = warp_scan(mine.w, lane);
+    V = 0;
+    // Units stay whole where so many of the longest take no longer than equal pieces and what cutting costs
+    // (in tiles): the join, and its bytes, fewer for units that are not full.
+    longest = __reduce_max_sync(0xffffffffu, longest) + kUnitTiles;
+    const float full = fminf(1.f, static_cast<float>(p.total_q) * static_cast<float>(p.heads) / static_cast<float>(N * max(units, 1)));
+    const int join = kCutTiles + static_cast<int>(static_cast<float>(units + p.ctas) * full * (N / 64.f / kCutPieces));
+    const int each = max(1, (units + p.ctas - 1) / p.ctas);
+    if (static_cast<int64_t>(each) * longest <= C + join / each && static_cast<int64_t>(units) * longest <= INT32_MAX) {
+      V = longest;
+      C = each * longest;
+      length = units * longest;
+    }
+    upto = warp_scan(weight(), lane);
     units_upto = warp_scan(mine.T, lane);
     lo = pos = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(blockIdx.x) * C));
     hi = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(lo) + C));
   }
+  __device__ __forceinline__ int weight() const { return V ? mine.T * V : mine.w; }   // of the held sequence
   // The next segment; s.end if there is none.  Returns the sequence's error bits.
   __device__ __forceinline__ int next(const LatentParams& p, int lane, Segment& s) {
     s.end = 1;
@@ -256,14 +271,14 @@ struct Walker {
         b0 += 32;
         if (b0 >= p.num_seqs) return 0;             // lengths changed under the call
         mine = seq_at<N>(p, b0 + lane);
-        upto = warp_scan(mine.w, lane);
+        upto = warp_scan(weight(), lane);
         units_upto = warp_scan(mine.T, lane);
         continue;
       }
       const int at = pos - before;
       const int f = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
       const int nt = __shfl_sync(0xffffffffu, mine.nt, f);
-      const int places = nt + kUnitTiles;
+      const int places = V ? V : nt + kUnitTiles;
       const int in = at - (f ? __shfl_sync(0xffffffffu, upto, f - 1) : 0);
       const int nth = in / places, in_unit = in - nth * places;
       unit = units_before + nth + (f ? __shfl_sync(0xffffffffu, units_upto, f - 1) : 0);
@@ -291,7 +306,7 @@ struct Walker {
     JoinNote n;
     // (its first tile is at place kUnitTiles: the pieces are those of its tiles)
     n.first = blockIdx.x;
-    n.pieces = (unit0 + unit_places - 1) / C - n.first + 1;
+    n.pieces = V ? 1 : (unit0 + unit_places - 1) / C - n.first + 1;
     n.first_slot = s.slot;
     n.q0 = s.q0;
     n.m = s.m;
@@ -314,26 +329,36 @@ __device__ __forceinline__ float warp_max(float x) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// Two f16x2 words (four values, lowest first) as e4m3 codes hi + lo; `dither` is added to what lo is of.
+// Two f16x2 words (four values, lowest first) as e4m3 codes hi + lo; with kDither a number is added to what lo
+// is of.
+template <bool kDither>
 __device__ __forceinline__ void two_terms(uint32_t x0, uint32_t x1, uint32_t dither, uint32_t& hi, uint32_t& lo) {
+  uint32_t y0, y1;
   asm("{\n"
-      " .reg .b16 h0, h1, l0, l1;\n"
-      " .reg .b32 g0, g1, y0, y1;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 h0, %2;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 h1, %3;\n"
+      " .reg .b16 h0, h1;\n"
+      " .reg .b32 g0, g1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h0, %3;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h1, %4;\n"
       " cvt.rn.f16x2.e4m3x2 g0, h0;\n"
       " cvt.rn.f16x2.e4m3x2 g1, h1;\n"
-      " sub.rn.f16x2 y0, %2, g0;\n"
-      " sub.rn.f16x2 y1, %3, g1;\n"
-      " add.rn.f16x2 y0, y0, %4;\n"
-      " add.rn.f16x2 y1, y1, %4;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l0, y0;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l1, y1;\n"
+      " sub.rn.f16x2 %1, %3, g0;\n"
+      " sub.rn.f16x2 %2, %4, g1;\n"
       " mov.b32 %0, {h0, h1};\n"
-      " mov.b32 %1, {l0, l1};\n"
       "}\n"
-      : "=r"(hi), "=r"(lo)
-      : "r"(x0), "r"(x1), "r"(dither));
+      : "=r"(hi), "=r"(y0), "=r"(y1)
+      : "r"(x0), "r"(x1));
+  if (kDither) {
+    asm("add.rn.f16x2 %0, %0, %1;\n" : "+r"(y0) : "r"(dither));
+    asm("add.rn.f16x2 %0, %0, %1;\n" : "+r"(y1) : "r"(dither));
+  }
+  asm("{\n"
+      " .reg .b16 l0, l1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l0, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l1, %2;\n"
+      " mov.b32 %0, {l0, l1};\n"
+      "}\n"
+      : "=r"(lo)
+      : "r"(y0), "r"(y1));
 }
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {   // a in the low half
   uint32_t d;
@@ -565,7 +590,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
     // ============================== the walk, and the scores =====================================
     Walker<N> walk;
     walk.start(p, lane);
-    if (blockIdx.x == 0 && lane == 0) *p.units = min(walk.units, p.unit_bound);
+    if (blockIdx.x == 0 && lane == 0) *p.units = walk.V ? 0 : min(walk.units, p.unit_bound);
     constexpr uint32_t kIdesc = idesc_e4m3_f32(128, 2 * N, false);
     const Desc q = desc_of(sdesc_sw128(smem + off_q<N>(), 16, 1024));
     const Desc q_rope = desc_of(sdesc_sw64(smem + off_q<N>() + kColumns * q_column<N>(), 16, 512));
@@ -576,7 +601,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
       Segment s;
       const int err = walk.next(p, lane, s);
       auto leave_note = [&]() {
-        if (lane == 0 && s.t0 == 0 && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
+        if (lane == 0 && s.t0 == 0 && !walk.V && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
       };
       if (!s.end && err) {
         leave_note();
@@ -810,8 +835,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         const uint32_t j = side + i * kSide;
         if (kParts * kSide > kRow / 8 && j >= kRow / 8) continue;
         uint32_t h0, h1, l0, l1;
-        two_terms(scaled_half2(x[i].x, up), scaled_half2(x[i].y, up), 0u, h0, l0);
-        two_terms(scaled_half2(x[i].z, up), scaled_half2(x[i].w, up), 0u, h1, l1);
+        two_terms<false>(scaled_half2(x[i].x, up), scaled_half2(x[i].y, up), 0u, h0, l0);
+        two_terms<false>(scaled_half2(x[i].z, up), scaled_half2(x[i].w, up), 0u, h1, l1);
         if (exponent == 255) h0 = h1 = l0 = l1 = 0x7f7f7f7fu;
         // 16 blocks a column's row, 8 of the rotated part, swizzled in pairs
         const bool rope = j >= kDim / 8;
@@ -876,7 +901,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           for (int r = 0; r < kHalf; r += 4) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[r + i] = exp2_hw(y[r + i]);
-            two_terms(half2_of(y[r], y[r + 1]), half2_of(y[r + 2], y[r + 3]), dither, hi[r / 4], lo[r / 4]);
+            two_terms<true>(half2_of(y[r], y[r + 1]), half2_of(y[r + 2], y[r + 3]), dither, hi[r / 4], lo[r / 4]);
           }
         };
         logits();
@@ -1118,18 +1143,17 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
   }
 }
 
-// The join: out = descale sum_j w_j O_j / sum_j w_j l_j over a unit's pieces, w_j = 2^(ref_j - max ref).
-// A CTA takes kRows rows of a unit, a thread four dims of one at a time, the pieces shared out over kGroups
-// groups of 128 threads.  Reads what the main kernel has just written, out of L2.
-constexpr int kJoinThreads = 256;
-
-template <int N, int kRows, int kGroups>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentParams p) {
-  static_assert(kRows * kGroups * 128 % kJoinThreads == 0);
-  constexpr int kAhead = 8;
-  __shared__ float s_w[kRows][kMaxCtas];
-  __shared__ float s_inv[kRows];
-  __shared__ float4 s_acc[kGroups > 1 ? kGroups - 1 : 1][128];
+// The join: out = descale sum_j w_j O_j / sum_j w_j l_j over a unit's pieces, w_j = 2^(ref_j - max ref).  128
+// threads take four dims each of kRows rows, kGroups such groups of threads either a part of the pieces
+// (kSplit: few units in many pieces) or more rows.  Reads what the main kernel has just written, out of L2;
+// bound by its chain of notes, sums and partial outputs.
+template <int N, int kRows, int kGroups, bool kSplit>
+__global__ void __launch_bounds__(128 * kGroups) latent_join_kernel(const __grid_constant__ LatentParams p) {
+  constexpr int kThreads = 128 * kGroups, kCtaRows = kSplit ? kRows : kRows * kGroups;
+  constexpr int kAhead = 8 / kRows;                    // pieces in flight
+  __shared__ float s_w[kCtaRows][kMaxCtas];
+  __shared__ float s_inv[kCtaRows];
+  __shared__ float4 s_acc[kSplit ? kGroups - 1 : 1][kRows][128];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
@@ -1138,7 +1162,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
   const int4 b = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x) + 1);
   if (static_cast<int>(blockIdx.x) >= units || a.x <= 1) return;
   const int n = a.x, first = a.y, q0 = a.w, m = b.x;
-  const int r0 = blockIdx.y * kRows, rows = min(kRows, b.y - r0);
+  const int r0 = blockIdx.y * kCtaRows, rows = min(kCtaRows, b.y - r0);
   // A CTA whose wait ran out may have left no note: what stands there then is not followed.
   if (n > p.ctas || first < 0 || first > p.ctas - n || (a.z & ~1) || q0 < 0 || m < 0 ||
       m >= MTP_LATENT_MAX_NODES * MTP_LATENT_MAX_HEADS / N || b.y <= 0 || b.y > N ||
@@ -1146,20 +1170,33 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
     return;
   if (rows <= 0) return;
   auto slot_of = [&](int i) -> int64_t { return 2 * (first + i) + (i == 0 ? a.z : 0); };
+  const int d4 = tid & 127, g = tid >> 7, mine = kSplit ? 0 : g * kRows;   // first row of this thread's
+  const float4* src = reinterpret_cast<const float4*>(p.o_part) + (r0 + mine) * (kDim / 4) + d4;
+  const int step = kSplit ? kGroups : 1;
+  float4 x[kAhead][kRows];
+  auto load = [&](int i0) {                            // pieces i0, i0 + step, ...
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (i0 + j * step < n && mine + r < rows)
+          x[j][r] = __ldcg(src + slot_of(i0 + j * step) * (N * kDim / 4) + r * (kDim / 4));
+  };
+  load(kSplit ? g : 0);                                // (on their way while the weights are worked out)
   // ---- the pieces' weights: a warp a row
 #pragma unroll 1
-  for (int r = warp; r < rows; r += kJoinThreads / 32) {
+  for (int r = warp; r < rows; r += kThreads / 32) {
     float ref[kMaxCtas / 32], sum[kMaxCtas / 32], top = -INFINITY;
     bool bad = false;
 #pragma unroll
     for (int k = 0; k < kMaxCtas / 32; ++k) {
       const int i = lane + 32 * k;
-      float2 x = make_float2(kNoRef, 0.f);
-      if (i < n) x = __ldcg(p.sum_part + slot_of(i) * N + r0 + r);
-      ref[k] = x.x;
-      sum[k] = x.y;
-      bad |= __float_as_uint(x.y) == kBadSum;
-      top = fmaxf(top, x.x);
+      float2 y = make_float2(kNoRef, 0.f);
+      if (i < n) y = __ldcg(p.sum_part + slot_of(i) * N + r0 + r);
+      ref[k] = y.x;
+      sum[k] = y.y;
+      bad |= __float_as_uint(y.y) == kBadSum;
+      top = fmaxf(top, y.x);
     }
     top = warp_max(top);
     bad = __any_sync(0xffffffffu, bad);
@@ -1178,48 +1215,53 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
   }
   __syncthreads();
   // ---- their sum
-  const int d4 = tid & 127, g = kGroups > 1 ? tid >> 7 : 0;
-#pragma unroll 1
-  for (int r = kGroups > 1 ? 0 : tid >> 7; r < rows; r += kGroups > 1 ? 1 : 2) {
-    const float4* src = reinterpret_cast<const float4*>(p.o_part) + (r0 + r) * (kDim / 4) + d4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int i0 = g; i0 < n; i0 += kAhead * kGroups) {
-      float4 x[kAhead];
+  float4 acc[kRows];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (i0 + j * kGroups < n) x[j] = __ldcg(src + slot_of(i0 + j * kGroups) * (N * kDim / 4));
+  for (int r = 0; r < kRows; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int i0 = kSplit ? g : 0; i0 < n;) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (i0 + j * kGroups < n) {
-          const float w = s_w[r][i0 + j * kGroups];
-          acc.x = fmaf(w, x[j].x, acc.x);
-          acc.y = fmaf(w, x[j].y, acc.y);
-          acc.z = fmaf(w, x[j].z, acc.z);
-          acc.w = fmaf(w, x[j].w, acc.w);
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (i0 + j * step < n && mine + r < rows) {
+          const float w = s_w[mine + r][i0 + j * step];
+          acc[r].x = fmaf(w, x[j][r].x, acc[r].x);
+          acc[r].y = fmaf(w, x[j][r].y, acc[r].y);
+          acc[r].z = fmaf(w, x[j][r].z, acc[r].z);
+          acc[r].w = fmaf(w, x[j][r].w, acc[r].w);
         }
-    }
-    if constexpr (kGroups > 1) {
-      if (g > 0) s_acc[g - 1][d4] = acc;
-      __syncthreads();
-      if (g > 0) continue;
+    i0 += kAhead * step;
+    if (i0 < n) load(i0);
+  }
+  if constexpr (kSplit) {
+    if (g > 0)
 #pragma unroll
-      for (int o = 0; o < kGroups - 1; ++o) {
-        const float4 x = s_acc[o][d4];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+      for (int r = 0; r < kRows; ++r) s_acc[g - 1][r][d4] = acc[r];
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int o = 0; o < kGroups - 1; ++o)
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float4 y = s_acc[o][r][d4];
+        acc[r].x += y.x;
+        acc[r].y += y.y;
+        acc[r].z += y.z;
+        acc[r].w += y.w;
       }
-    }
-    const float inv = s_inv[r];
-    if (inv == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    const int rr = m * N + r0 + r, tok = rr / p.heads;
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (mine + r >= rows) continue;
+    const float inv = s_inv[mine + r];
+    if (inv == 0.f) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const __nv_bfloat162 u = __floats2bfloat162_rn(acc[r].x * inv, acc[r].y * inv);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[r].z * inv, acc[r].w * inv);
+    const int rr = m * N + r0 + mine + r, tok = rr / p.heads;
     reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q0 + tok) * p.out_stride_tok +
                              static_cast<int64_t>(rr - tok * p.heads) * p.out_stride_head)[d4] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
   }
 }
 
@@ -1320,10 +1362,10 @@ int launch_latent(LatentParams& p, int device, cudaStream_t stream) {
   if (launch_pdl(kernel, dim3(p.ctas), kLatentThreads, smem_bytes<N>(), stream, p) != cudaSuccess) return MTPATTN_E_LAUNCH;
   if (p.max_pages <= kTilePages) return MTPATTN_OK;  // units of one tile are never cut
   const bool few = p.unit_bound <= 32;
-  const void* join = few ? reinterpret_cast<const void*>(latent_join_kernel<N, 1, 2>)
-                         : reinterpret_cast<const void*>(latent_join_kernel<N, 8, 1>);
-  return launch_pdl(join, dim3(p.unit_bound, N / (few ? 1 : 8)), kJoinThreads, 0, stream, p) == cudaSuccess
-             ? MTPATTN_OK : MTPATTN_E_LAUNCH;
+  const void* join = few ? reinterpret_cast<const void*>(latent_join_kernel<N, 2, 2, true>)
+                         : reinterpret_cast<const void*>(latent_join_kernel<N, 4, 2, false>);
+  return launch_pdl(join, dim3(p.unit_bound, N / (few ? 2 : 8)), 256, 0, stream, p) == cudaSuccess ? MTPATTN_OK
+                                                                                                  : MTPATTN_E_LAUNCH;
 }
 
 }  // namespace
