@@ -156,7 +156,6 @@ struct Shared {
   alignas(16) float f[N];              // 2^step; the output's factor
   uint64_t word[N];                    // new tokens that the row sees
   alignas(16) float xch[2][4][N / 2];  // row half, key quarter
-  uint8_t over[2][2][4];               // by turns; row half, key quarter
 };
 template <int N>
 constexpr int smem_bytes() { return off_bars<N>() + static_cast<int>(sizeof(Shared<N>)); }
@@ -530,6 +529,19 @@ struct Meeting {
   }
 };
 
+// The four warps of a half of the rows meet once a tile, by the hardware's barrier, which has no limit: so none
+// of them leaves the tiles alone.  One whose wait ran out says so here, by a vote, and all leave together.
+__device__ __forceinline__ bool any_of_half(int half, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(y)
+      : "r"(1 + half), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return y != 0;
+}
+__device__ __forceinline__ void meet_half(int half) { asm volatile("barrier.cta.sync %0, 128;\n" ::"r"(1 + half) : "memory"); }
+
 // ---- the kernel ----------------------------------------------------------------------------------
 
 template <int N>
@@ -800,7 +812,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
     const float descale = *p.descale, factor = p.scale_log2 * descale;
     const int row0 = half * kHalf;
     Meeting meet{smem_u32(&bars.meet[half]), 0}, meet_all{smem_u32(&bars.meet[2]), 0};
-    uint32_t u = 0, votes_at = 0;
+    uint32_t u = 0;
     bool alive = true;
     // Q's two terms of a segment, kSide lanes a row, and what there is of each row.  Asks that the last product
     // that reads the previous ones is done: that all S of their segment has been read.
@@ -875,7 +887,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
       const bool late = (s.t0 + 1) * kKeys > start;  // a row may see nothing of the first tile
 #pragma unroll 1
       for (int t = s.t0; t < s.t1; ++t, ++u) {
-        if (!(alive = warp_wait(smem_u32(&bars.s_full[u & 1]), (u >> 1) & 1, abort_flag))) break;
+        alive &= warp_wait(smem_u32(&bars.s_full[u & 1]), (u >> 1) & 1, abort_flag);
         tc_fence_after();
         const int j = t * kKeys + key;
         const bool ragged = (t + 1) * kKeys > start;  // new tokens, or places behind the sequence
@@ -905,36 +917,28 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           }
         };
         logits();
-        // A reference is raised where a logit is too far above it, and at first.  While the warps of these rows
-        // tell one another, the weights are worked out as if there was none.
+        // A reference is raised where a logit is too far above it, and at first.
         const bool forced = t == s.t0 || (ragged && late);
         bool over = forced;
-        if (!over) {
+        if (!forced) {
           float a = y[0], b = y[1];
 #pragma unroll
           for (int r = 2; r < kHalf; r += 2) {
             a = fmaxf(a, y[r]);
             b = fmaxf(b, y[r + 1]);
           }
-          over = __any_sync(0xffffffffu, fmaxf(a, b) > kShift + kTau);
+          over = fmaxf(a, b) > kShift + kTau;
         }
-        if (!forced) {
-          uint8_t (&votes)[4] = sh.over[votes_at ^= 1][half];
-          if (lane == 0) votes[quarter] = over;
-          meet.arrive(lane);
-          weights();
-          if (!(alive = meet.wait(abort_flag))) break;
-          over = *reinterpret_cast<volatile uint32_t*>(votes) != 0;
-        }
+        over = any_of_half(half, over || !alive);
         if (over) {
+          if (!(alive = !any_of_half(half, !alive || *abort_flag))) break;
           if (!forced) logits();
           float tops[kHalf];
 #pragma unroll
           for (int r = 0; r < kHalf; ++r) tops[r] = y[r];
           const float mine = row_maxima<kHalf>(tops, lane);
           if (lane < kHalf) sh.xch[half][quarter][lane] = mine;
-          meet.arrive(lane);
-          if (!(alive = meet.wait(abort_flag))) break;
+          meet_half(half);
           if (quarter == 0 && lane < kHalf) {
             const float (&x)[4][kHalf] = sh.xch[half];
             const float top = fmaxf(fmaxf(x[0][lane], x[1][lane]), fmaxf(x[2][lane], x[3][lane]));
@@ -948,8 +952,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             sh.step[row0 + lane] = step;
             sh.f[row0 + lane] = f;
           }
-          meet.arrive(lane);
-          if (!(alive = meet.wait(abort_flag))) break;
+          meet_half(half);
 #pragma unroll
           for (int r = 0; r < kHalf; ++r) {
             const float step = sh.step[row0 + r];
@@ -958,7 +961,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           }
           if (t > s.t0) {
             // (O may be touched once the previous tile's products are in it)
-            if (!(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
+            alive &= warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag);
             tc_fence_after();
 #pragma unroll
             for (int r = 0; r < kHalf; ++r) l[r] *= sh.f[row0 + r];
@@ -974,8 +977,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             }
             tmem_st_wait();
           }
-          weights();
         }
+        weights();
         const uint32_t stage = smem + (u % kStages) * kStage;
         const uint32_t swz = (key >> 1) & 3;
         auto write = [&](uint32_t at, const uint32_t (&x)[kHalf / 4]) {
@@ -990,9 +993,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         };
         write(stage + (key >> 3) * kGroup + kRopeAt, hi);
         // the previous tile's second terms of these keys have been read: a quarter is a block
-        if (u > 0 &&
-            !(alive = warp_wait(smem_u32(&bars.empty[(u - 1) % kStages][quarter]), ((u - 1) / kStages) & 1, abort_flag)))
-          break;
+        if (u > 0) alive &= warp_wait(smem_u32(&bars.empty[(u - 1) % kStages][quarter]), ((u - 1) / kStages) & 1, abort_flag);
         write(smem + off_p<N>() + (key >> 3) * kAtom, lo);
         if (ragged && j >= start) {
           // this half's 256 of the key's values: none behind the sequence, no NaN among the new tokens
