@@ -239,15 +239,15 @@ struct Walker {
     }
     length = static_cast<int>(W);
     units = static_cast<int>(U);
-    C = max(1, static_cast<int>((W + p.ctas - 1) / p.ctas));
+    C = max(1, static_cast<int>((static_cast<uint32_t>(W) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)));
     V = 0;
     // Units stay whole where so many of the longest take no longer than equal pieces and what cutting costs
     // (in tiles): the join, and its bytes, fewer for units that are not full.
     longest = __reduce_max_sync(0xffffffffu, longest) + kUnitTiles;
     const float full = fminf(1.f, static_cast<float>(p.total_q) * static_cast<float>(p.heads) / static_cast<float>(N * max(units, 1)));
     const int join = kCutTiles + static_cast<int>(static_cast<float>(units + p.ctas) * full * (N / 64.f / kCutPieces));
-    const int each = max(1, (units + p.ctas - 1) / p.ctas);
-    if (static_cast<int64_t>(each) * longest <= C + join / each && static_cast<int64_t>(units) * longest <= INT32_MAX) {
+    const int each = max(1, static_cast<int>((static_cast<uint32_t>(units) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)));
+    if (static_cast<int64_t>(each) * longest <= C + static_cast<int>(static_cast<uint32_t>(join) / each) && static_cast<int64_t>(units) * longest <= INT32_MAX) {
       V = longest;
       C = each * longest;
       length = units * longest;
@@ -364,9 +364,10 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {   // a in the l
   asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(b), "f"(a));
   return d;
 }
-// A bf16 pair scaled by f, as an f16 pair: exact down to 2^-17 of a scaled value.
-__device__ __forceinline__ uint32_t scaled_half2(uint32_t w, float f) {
-  return half2_of(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+// A bf16 pair scaled by f (a power of two, twice), as an f16 pair: exact down to 2^-17 of a scaled value.
+__device__ __forceinline__ uint32_t scaled_half2(uint32_t w, uint32_t f) {
+  asm("mul.rn.bf16x2 %0, %0, %1;\n" : "+r"(w) : "r"(f));
+  return half2_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // n columns of a lane each, n 8, 16 or 32.
@@ -455,6 +456,9 @@ __device__ __forceinline__ void mma_two(uint32_t d_tmem, uint32_t a, uint32_t a_
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_line(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(reinterpret_cast<uint64_t>(p)) : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
 }
@@ -589,7 +593,20 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
-  // A programmatic dependent of the previous work on the stream: nothing global was touched so far; and
+  // What every CTA will want first is asked into L2 while the work before this on the stream still runs (the L2
+  // is where all writes meet, so nothing can be stale there): a line of the block tables and of Q a thread.
+  {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kLatentThreads + tid;
+    const int64_t table_lines = (static_cast<int64_t>(p.num_seqs) * p.max_pages * 4 + 127) / 128;
+    constexpr int kRowLines = kRow * 2 / 128;
+    if (i < table_lines) prefetch_line(reinterpret_cast<const char*>(p.block_tables) + 128 * i);
+    if (i < static_cast<int64_t>(p.total_q) * p.heads * kRowLines) {
+      const uint32_t row = static_cast<uint32_t>(i) / kRowLines, tok = row / static_cast<uint32_t>(p.heads);
+      prefetch_line(p.q + static_cast<int64_t>(tok) * p.q_stride_tok + static_cast<int64_t>(row - tok * p.heads) * p.q_stride_head +
+                    (static_cast<uint32_t>(i) - row * kRowLines) * 64);
+    }
+  }
+  // A programmatic dependent of the previous work on the stream: nothing global was read so far; and
   // the join may be scheduled (it waits for this grid before it reads partials).
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -840,7 +857,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
       for (int o = 1; o < kSide; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int exponent = max(top & 0xffffu, top >> 16) >> 7;   // biased; 255: not finite
       const int a = min(134 - exponent, 126);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
+      const uint32_t up1 = static_cast<uint32_t>(127 + a) << 7, up = up1 | up1 << 16;
       const uint32_t at0 = smem + off_q<N>() + r * 128, at1 = smem + off_q<N>() + kColumns * q_column<N>() + r * 64;
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
