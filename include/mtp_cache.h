@@ -4,7 +4,9 @@
  * mtp_tree_attn_fwd read, and moving the accepted tokens of a draft tree to their places.
  *
  * The cache.  k_cache and v_cache are e4m3 [num_layers][num_pages][16][num_kv_heads][256],
- * contiguous within a layer, layers layer_stride bytes apart (one layer: any stride).  All
+ * contiguous within a layer, layers layer_stride bytes apart (one layer: any stride).  Or it holds
+ * latent vectors (mtp_latent.h): k_cache is e4m3 [num_layers][num_pages][16][576], v_cache NULL and
+ * num_kv_heads 0, in all of these calls; "keys and values" below are then the latent vectors.  All
  * layers share one block table [num_rows][max_pages_per_seq] (int32, logical page -> physical
  * page; entries at and past ceil(seq_lens / 16) mean nothing and are kept at -1 by these calls),
  * seq_lens [num_rows], and ref_counts [num_pages] (int32): in how many table rows each page

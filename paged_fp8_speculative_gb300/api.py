@@ -467,14 +467,15 @@ def mtp_cache_workspace_size(num_rows: int, max_pages_per_seq: int) -> int:
     return int(lib().mtp_cache_workspace_size(num_rows, max_pages_per_seq))
 
 
-def mtp_cache_resize(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+def mtp_cache_resize(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], block_tables: torch.Tensor,
                      seq_lens: torch.Tensor, ref_counts: torch.Tensor, new_lens: torch.Tensor,
                      workspace: Optional[torch.Tensor] = None,
                      status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Set every row's length, in place: pages are given back and handed out.
 
     k_cache / v_cache: one layer's caches [num_pages, 16, H_kv, 256] or a stack's, behind
-    num_layers; block_tables [rows, max_pages], seq_lens [rows], ref_counts [num_pages] int32 are
+    num_layers; or latent vectors [num_pages, 16, 576], or a stack of them, with v_cache None (here
+    and in the calls below); block_tables [rows, max_pages], seq_lens [rows], ref_counts [num_pages] int32 are
     updated; new_lens [rows] int32 (0 frees a row).  A shared, partly filled last page is copied
     first.  With too few free pages nothing is handed out and ERR_FULL is set.
     """
@@ -486,7 +487,7 @@ def mtp_cache_resize(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
                              workspace, status), stream, block_tables.device)
 
 
-def mtp_cache_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+def mtp_cache_fork(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], block_tables: torch.Tensor,
                    seq_lens: torch.Tensor, ref_counts: torch.Tensor, src: torch.Tensor,
                    dst: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -500,7 +501,7 @@ def mtp_cache_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
                              workspace, status), stream, block_tables.device)
 
 
-def mtp_cache_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src_pages: torch.Tensor,
+def mtp_cache_copy_pages(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], src_pages: torch.Tensor,
                          dst_pages: torch.Tensor, status: Optional[torch.Tensor] = None,
                          stream=None) -> None:
     """Page dst_pages[i] gets the contents of page src_pages[i], in all layers."""
@@ -511,7 +512,7 @@ def mtp_cache_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, src_pages
                       k_cache.device)
 
 
-def mtp_cache_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+def mtp_cache_compact(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], block_tables: torch.Tensor,
                       seq_lens: torch.Tensor, cu_seqlens_q: torch.Tensor,
                       accept_index: torch.Tensor, accept_len: torch.Tensor,
                       new_seq_lens: Optional[torch.Tensor] = None,

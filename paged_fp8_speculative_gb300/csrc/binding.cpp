@@ -299,28 +299,33 @@ PyObject* verify_sample(PyObject* const* a) {
 
 // ---- the cache -----------------------------------------------------------------------------------
 
-// One layer's caches [num_pages, 16, H_kv, 256], or a stack's behind num_layers.
+// One layer's caches [num_pages, 16, H_kv, 256], or a stack's behind num_layers; or, without v_cache,
+// latent vectors [num_pages, 16, 576].
 struct Cache {
   void *k, *v;
   int32_t layers, hkv;
   int64_t layer_stride, pages;
 };
-Cache cache_args(const at::Tensor& k, const at::Tensor& v) {
+Cache cache_args(const at::Tensor& k, PyObject* v_) {
+  const bool latent = !given(v_);
+  const at::Tensor& v = latent ? k : tensor(v_, "v_cache");
   REFUSE_IF(!is_codes(k.scalar_type()) || v.scalar_type() != k.scalar_type(),
             "k_cache / v_cache must be uint8 or float8_e4m3fn codes");
-  const int64_t n = k.dim();
-  REFUSE_IF((n != 4 && n != 5) || k.size(n - 3) != MTPATTN_PAGE_SIZE || k.size(n - 1) != MTPATTN_HEAD_DIM,
-            "k_cache must be [num_pages, 16, H_kv, 256], or that behind num_layers");
+  const int64_t n = k.dim(), one = latent ? 3 : 4;            // axes of a layer
+  const int64_t row = latent ? MTP_LATENT_ROW : MTPATTN_HEAD_DIM;
+  REFUSE_IF((n != one && n != one + 1) || k.size(n - one + 1) != MTPATTN_PAGE_SIZE || k.size(n - 1) != row,
+            latent ? "k_cache without v_cache must be [num_pages, 16, 576], or that behind num_layers"
+                   : "k_cache must be [num_pages, 16, H_kv, 256], or that behind num_layers");
   REFUSE_IF(v.sizes() != k.sizes() || v.strides() != k.strides(), "k_cache and v_cache must be of the same shape and strides");
   Cache c;
-  c.layers = n == 5 ? count32(k.size(0), "k_cache") : 1;
-  c.pages = k.size(n - 4);
-  c.hkv = count32(k.size(n - 2), "k_cache");
-  REFUSE_IF(c.layers > 0 && !k.is_contiguous() && !(n == 5 && k.select(0, 0).is_contiguous()),
+  c.layers = n == one + 1 ? count32(k.size(0), "k_cache") : 1;
+  c.pages = k.size(n - one);
+  c.hkv = latent ? 0 : count32(k.size(n - 2), "k_cache");
+  REFUSE_IF(c.layers > 0 && !k.is_contiguous() && !(n == one + 1 && k.select(0, 0).is_contiguous()),
             "a layer's cache must be contiguous");
-  c.layer_stride = c.layers > 1 ? k.stride(0) : c.pages * c.hkv * (MTPATTN_PAGE_SIZE * MTPATTN_HEAD_DIM);
+  c.layer_stride = c.layers > 1 ? k.stride(0) : c.pages * MTPATTN_PAGE_SIZE * (latent ? row : c.hkv * row);
   c.k = k.data_ptr();
-  c.v = v.data_ptr();
+  c.v = latent ? nullptr : v.data_ptr();
   return c;
 }
 struct Table {
@@ -341,10 +346,10 @@ at::Tensor cache_workspace(PyObject* o, const at::Tensor& like, const Table& t) 
 
 // k_cache, v_cache, block_tables, seq_lens, ref_counts, new_lens, workspace, status, stream
 PyObject* cache_resize(PyObject* const* a) {
-  const at::Tensor &k = tensor(a[0], "k_cache"), &v = tensor(a[1], "v_cache"), &table = tensor(a[2], "block_tables");
+  const at::Tensor &k = tensor(a[0], "k_cache"), &table = tensor(a[2], "block_tables");
   const at::Tensor &lens = tensor(a[3], "seq_lens"), &refs = tensor(a[4], "ref_counts"), &to = tensor(a[5], "new_lens");
   void* stream = stream_of(a[8], table);
-  const Cache c = cache_args(k, v);
+  const Cache c = cache_args(k, a[1]);
   const Table t = table_args(table, lens, refs, c.pages);
   vector(to, "new_lens", t.rows);
   const at::Tensor ws = cache_workspace(a[6], table, t);
@@ -356,11 +361,11 @@ PyObject* cache_resize(PyObject* const* a) {
 
 // k_cache, v_cache, block_tables, seq_lens, ref_counts, src, dst, workspace, status, stream
 PyObject* cache_fork(PyObject* const* a) {
-  const at::Tensor &k = tensor(a[0], "k_cache"), &v = tensor(a[1], "v_cache"), &table = tensor(a[2], "block_tables");
+  const at::Tensor &k = tensor(a[0], "k_cache"), &table = tensor(a[2], "block_tables");
   const at::Tensor &lens = tensor(a[3], "seq_lens"), &refs = tensor(a[4], "ref_counts");
   const at::Tensor &src = tensor(a[5], "src"), &dst = tensor(a[6], "dst");
   void* stream = stream_of(a[9], table);
-  const Cache c = cache_args(k, v);
+  const Cache c = cache_args(k, a[1]);
   const Table t = table_args(table, lens, refs, c.pages);
   vector(src, "src", src.numel());
   vector(dst, "dst", src.numel());
@@ -373,10 +378,10 @@ PyObject* cache_fork(PyObject* const* a) {
 
 // k_cache, v_cache, src_pages, dst_pages, status, stream
 PyObject* cache_copy_pages(PyObject* const* a) {
-  const at::Tensor &k = tensor(a[0], "k_cache"), &v = tensor(a[1], "v_cache");
+  const at::Tensor& k = tensor(a[0], "k_cache");
   const at::Tensor &src = tensor(a[2], "src_pages"), &dst = tensor(a[3], "dst_pages");
   void* stream = stream_of(a[5], k);
-  const Cache c = cache_args(k, v);
+  const Cache c = cache_args(k, a[1]);
   vector(src, "src_pages", src.numel());
   vector(dst, "dst_pages", src.numel());
   const int rc = mtp_cache_copy_pages(c.k, c.v, c.layers, c.layer_stride, c.pages, c.hkv, ints(src), ints(dst),
@@ -387,11 +392,11 @@ PyObject* cache_copy_pages(PyObject* const* a) {
 // k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q, accept_index, accept_len, new_seq_lens,
 // status, stream
 PyObject* cache_compact(PyObject* const* a) {
-  const at::Tensor &k = tensor(a[0], "k_cache"), &v = tensor(a[1], "v_cache"), &table = tensor(a[2], "block_tables");
+  const at::Tensor &k = tensor(a[0], "k_cache"), &table = tensor(a[2], "block_tables");
   const at::Tensor &lens = tensor(a[3], "seq_lens"), &cu = tensor(a[4], "cu_seqlens_q");
   const at::Tensor &index = tensor(a[5], "accept_index"), &count = tensor(a[6], "accept_len");
   void* stream = stream_of(a[9], k);
-  const Cache c = cache_args(k, v);
+  const Cache c = cache_args(k, a[1]);
   const int32_t seqs = sequences(cu);
   REFUSE_IF(table.scalar_type() != at::kInt || table.dim() != 2 || table.size(0) != seqs || !table.is_contiguous(),
             "block_tables must be a contiguous int32 [B, max_pages] tensor, cu_seqlens_q [B + 1]");

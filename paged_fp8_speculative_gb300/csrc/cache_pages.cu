@@ -22,6 +22,7 @@
 #include "host_checks.cuh"
 
 #include "../../include/mtp_cache.h"
+#include "../../include/mtp_latent.h"
 #include "../../include/mtp_tree.h"
 
 #include <cooperative_groups.h>
@@ -38,6 +39,9 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanCtas = 8;
 constexpr int kCopyThreads = 256;
+
+// Bytes of a token in one array of a layer: its heads, or (no heads) its latent vector.
+__host__ __device__ constexpr int token_bytes(int hkv) { return hkv ? hkv * kHeadDim : MTP_LATENT_ROW; }
 
 struct PlanParams {
   int32_t* bt;
@@ -324,10 +328,11 @@ cache_plan_kernel(const PlanParams p) {
   }
 }
 
-// Pages from -> to, all layers, K and V: blockIdx.x the pair, blockIdx.y the layer and cache.
+// Pages from -> to, all layers, K and V (or the latent vectors): blockIdx.x the pair, blockIdx.y the layer and
+// cache.
 struct CopyParams {
   uint8_t* k;
-  uint8_t* v;
+  uint8_t* v;                // null: a cache of latent vectors
   int32_t layers;
   int64_t layer_stride;      // bytes
   int64_t num_pages;
@@ -358,8 +363,9 @@ cache_copy_kernel(const CopyParams p) {
     }
     if (from == to) return;
   }
-  for (int l = blockIdx.y; l < 2 * p.layers; l += gridDim.y) {
-    uint8_t* layer = ((l & 1) ? p.v : p.k) + static_cast<int64_t>(l >> 1) * p.layer_stride;
+  const int both = p.v ? 1 : 0;                        // K and V take turns
+  for (int l = blockIdx.y; l < p.layers << both; l += gridDim.y) {
+    uint8_t* layer = ((l & both) ? p.v : p.k) + static_cast<int64_t>(l >> both) * p.layer_stride;
     const uint4* a = reinterpret_cast<const uint4*>(layer + from * p.page_bytes);
     uint4* z = reinterpret_cast<uint4*>(layer + to * p.page_bytes);
     const int n = static_cast<int>(p.page_bytes / 16);
@@ -373,10 +379,11 @@ cache_copy_kernel(const CopyParams p) {
 // (a block's places are below all later nodes' numbers).  16 lanes make a row of 256 bytes.  Bound
 // by its launch and one trip to memory: 2.5 us for one path of one layer, 3.1 us for 64 of 16 layers.
 constexpr int kAhead = 8;
+constexpr int kLatentBlocks = MTP_LATENT_ROW / 16;   // of 16 bytes
 
 struct CompactParams {
   uint8_t* k;
-  uint8_t* v;
+  uint8_t* v;                // null: a cache of latent vectors
   int32_t layers;
   int64_t layer_stride;
   int32_t num_pages;
@@ -415,8 +422,9 @@ cache_compact_kernel(const CompactParams p) {
       const int a = start + node, z = start + t;
       const int pa = row[a / kPage], pz = row[z / kPage];
       if (pa < 0 || pa >= p.num_pages || pz < 0 || pz >= p.num_pages) mine |= MTPATTN_ERR_PAGE;
-      s_from[t] = (static_cast<int64_t>(pa) * kPage + a % kPage) * p.hkv * kHeadDim;
-      s_to[t] = (static_cast<int64_t>(pz) * kPage + z % kPage) * p.hkv * kHeadDim;
+      const int token = token_bytes(p.hkv);
+      s_from[t] = (static_cast<int64_t>(pa) * kPage + a % kPage) * token;
+      s_to[t] = (static_cast<int64_t>(pz) * kPage + z % kPage) * token;
     }
   }
   err |= __syncthreads_or(mine & MTP_CACHE_ERR_LEN) ? MTP_CACHE_ERR_LEN : 0;
@@ -426,12 +434,18 @@ cache_compact_kernel(const CompactParams p) {
     if (err) set_status(p.status, err);
   }
   if (err) return;
-  const int units = p.layers * 2 * p.hkv;          // rows of 256 bytes a token
-  const int unit = blockIdx.x * (kCopyThreads / 16) + (t >> 4);
-  if (unit >= units) return;
-  const int layer = unit / (2 * p.hkv), rest = unit % (2 * p.hkv);
-  uint8_t* base = ((rest & 1) ? p.v : p.k) + static_cast<int64_t>(layer) * p.layer_stride +
-                  (rest >> 1) * kHeadDim + (t & 15) * 16;
+  uint8_t* base;
+  if (p.v) {
+    const int units = p.layers * 2 * p.hkv;        // rows of 256 bytes a token
+    const int unit = blockIdx.x * (kCopyThreads / 16) + (t >> 4);
+    if (unit >= units) return;
+    const int layer = unit / (2 * p.hkv), rest = unit % (2 * p.hkv);
+    base = ((rest & 1) ? p.v : p.k) + static_cast<int64_t>(layer) * p.layer_stride + (rest >> 1) * kHeadDim + (t & 15) * 16;
+  } else {
+    const int at = blockIdx.x * kCopyThreads + t, layer = at / kLatentBlocks;   // a token's 16 bytes of a layer
+    if (layer >= p.layers) return;
+    base = p.k + static_cast<int64_t>(layer) * p.layer_stride + (at - layer * kLatentBlocks) * 16;
+  }
   for (int j0 = 1; j0 <= m; j0 += kAhead) {
     uint4 x[kAhead];
 #pragma unroll
@@ -448,10 +462,11 @@ cache_compact_kernel(const CompactParams p) {
 
 int check_caches(const void* k, const void* v, int32_t layers, int64_t layer_stride,
                  int64_t num_pages, int32_t hkv) {
-  if (!k || !v || layers <= 0 || num_pages <= 0 || hkv <= 0) return MTPATTN_E_ARG;
+  // K and V of some heads, or neither V nor heads: latent vectors
+  if (!k || layers <= 0 || num_pages <= 0 || (v ? hkv <= 0 : hkv != 0)) return MTPATTN_E_ARG;
   if (num_pages > MTP_CACHE_MAX_PAGES || hkv > 65535) return MTPATTN_E_UNSUPPORTED;
   if (!ptr_aligned(k, 16) || !ptr_aligned(v, 16)) return MTPATTN_E_ARG;
-  const int64_t bytes = num_pages * kPage * hkv * kHeadDim;
+  const int64_t bytes = num_pages * kPage * token_bytes(hkv);
   if (layers > 1 && (layer_stride < bytes || layer_stride % 16)) return MTPATTN_E_ARG;
   return MTPATTN_OK;
 }
@@ -495,7 +510,7 @@ cudaError_t launch_plan(const PlanParams& p, int device, cudaStream_t stream) {
 
 cudaError_t launch_copy(const CopyParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.items, std::min(2 * p.layers, 65535));
+  cfg.gridDim = dim3(p.items, std::min(p.layers * (p.v ? 2 : 1), 65535));
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -513,7 +528,7 @@ int plan_and_copy(bool fork, PlanParams& p, CopyParams& c, void* workspace, size
   const size_t need = mtp_cache_workspace_size(p.rows, p.max_pages);
   if (!workspace || !ptr_aligned(workspace, 256) || bytes < need) return MTPATTN_E_WORKSPACE;
   if (device < 0 || device >= kMaxDevices) return MTPATTN_E_DEVICE;
-  const void* const ptrs[] = {c.k, c.v, p.bt, p.seq_lens, p.ref, workspace};
+  const void* const ptrs[] = {c.k, c.v ? c.v : c.k, p.bt, p.seq_lens, p.ref, workspace};
   if (!all_on_device(ptrs, device) || (p.status && !ptr_on_device(p.status, device)) ||
       (fork ? !ptr_on_device(p.src, device) || !ptr_on_device(p.dst, device)
             : !ptr_on_device(p.new_lens, device)))
@@ -573,7 +588,7 @@ extern "C" int mtp_cache_resize(void* k_cache, void* v_cache, int32_t num_layers
   c.layers = num_layers;
   c.layer_stride = layer_stride;
   c.num_pages = num_pages;
-  c.page_bytes = static_cast<int64_t>(kPage) * num_kv_heads * kHeadDim;
+  c.page_bytes = static_cast<int64_t>(kPage) * token_bytes(num_kv_heads);
   return plan_and_copy(false, p, c, workspace, workspace_bytes, current_device(),
                        static_cast<cudaStream_t>(stream));
 }
@@ -609,7 +624,7 @@ extern "C" int mtp_cache_fork(void* k_cache, void* v_cache, int32_t num_layers,
   c.layers = num_layers;
   c.layer_stride = layer_stride;
   c.num_pages = num_pages;
-  c.page_bytes = static_cast<int64_t>(kPage) * num_kv_heads * kHeadDim;
+  c.page_bytes = static_cast<int64_t>(kPage) * token_bytes(num_kv_heads);
   return plan_and_copy(true, p, c, workspace, workspace_bytes, current_device(),
                        static_cast<cudaStream_t>(stream));
 }
@@ -627,7 +642,7 @@ extern "C" int mtp_cache_copy_pages(void* k_cache, void* v_cache, int32_t num_la
     return MTPATTN_E_ARG;
   const int device = current_device();
   if (device < 0) return MTPATTN_E_DEVICE;
-  const void* const ptrs[] = {k_cache, v_cache, src_pages, dst_pages};
+  const void* const ptrs[] = {k_cache, v_cache ? v_cache : k_cache, src_pages, dst_pages};
   if (!all_on_device(ptrs, device) || (status && !ptr_on_device(status, device)))
     return MTPATTN_E_DEVICE;
   CopyParams c{};
@@ -636,7 +651,7 @@ extern "C" int mtp_cache_copy_pages(void* k_cache, void* v_cache, int32_t num_la
   c.layers = num_layers;
   c.layer_stride = layer_stride;
   c.num_pages = num_pages;
-  c.page_bytes = static_cast<int64_t>(kPage) * num_kv_heads * kHeadDim;
+  c.page_bytes = static_cast<int64_t>(kPage) * token_bytes(num_kv_heads);
   c.src = src_pages;
   c.dst = dst_pages;
   c.items = num_pairs;
@@ -665,7 +680,7 @@ extern "C" int mtp_cache_compact(void* k_cache, void* v_cache, int32_t num_layer
     return MTPATTN_E_ARG;
   if (max_path > MTP_TREE_MAX_NODES || num_seqs > 65535 || max_pages_per_seq > INT32_MAX / kPage ||
       total_q > static_cast<int64_t>(num_seqs) * MTP_TREE_MAX_NODES ||
-      static_cast<int64_t>(num_layers) * 2 * num_kv_heads > (1 << 28))
+      static_cast<int64_t>(num_layers) * (v_cache ? 2 * num_kv_heads : 8) > (1 << 28))
     return MTPATTN_E_UNSUPPORTED;
   // every CTA of a sequence reads its inputs, and one of them writes the new length
   const int64_t table_words = static_cast<int64_t>(num_seqs) * max_pages_per_seq;
@@ -678,7 +693,7 @@ extern "C" int mtp_cache_compact(void* k_cache, void* v_cache, int32_t num_layer
     return MTPATTN_E_ARG;
   const int device = current_device();
   if (device < 0) return MTPATTN_E_DEVICE;
-  const void* const ptrs[] = {k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q,
+  const void* const ptrs[] = {k_cache, v_cache ? v_cache : k_cache, block_tables, seq_lens, cu_seqlens_q,
                               accept_index, accept_len, new_seq_lens};
   if (!all_on_device(ptrs, device) || (status && !ptr_on_device(status, device)))
     return MTPATTN_E_DEVICE;
@@ -699,8 +714,9 @@ extern "C" int mtp_cache_compact(void* k_cache, void* v_cache, int32_t num_layer
   p.max_path = max_path;
   p.new_lens = new_seq_lens;
   p.status = status;
-  const int units = num_layers * 2 * num_kv_heads;
-  const dim3 grid((units + kCopyThreads / 16 - 1) / (kCopyThreads / 16), num_seqs);
+  // threads of 16 bytes
+  const int64_t threads = static_cast<int64_t>(num_layers) * (v_cache ? 2 * num_kv_heads * 16 : kLatentBlocks);
+  const dim3 grid(static_cast<unsigned>((threads + kCopyThreads - 1) / kCopyThreads), num_seqs);
   cache_compact_kernel<<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? MTPATTN_OK : MTPATTN_E_LAUNCH;
 }
