@@ -102,7 +102,8 @@ struct JoinNote {
   int pieces;                // it lies in; 1: written out whole
   int first, first_slot;     // the first of them, and the unit's slot there (in the others, 0)
   int q0, m, rows;           // its sequence's first row of tokens, row tile, valid rows
-  int pad[2];
+  int stride;                // from a piece's CTA to the next one's
+  int pad;
 };
 
 struct LatentParams {
@@ -212,6 +213,7 @@ template <int N>
 struct Walker {
   int pos, hi, lo, length, units;
   int C, V;                            // places of a piece; of a unit where none is cut (C is a multiple), else 0
+  int G;                               // CTAs that take a piece together, a row tile each: 1, or all T of a sequence
   int b0, before, units_before;        // the held sequences; the line and the units before them
   Seq mine;
   int upto, units_upto;                // running sums of the held sequences' weights and units
@@ -220,7 +222,8 @@ struct Walker {
   __device__ __forceinline__ void start(const LatentParams& p, int lane) {
     b0 = before = units_before = unit = unit0 = unit_places = 0;
     mine = seq_at<N>(p, lane);
-    int w = mine.w, n = mine.n, T = mine.T, longest = mine.nt;
+    int w = mine.w, n = mine.n, T = mine.T, longest = mine.nt, tall = mine.T;
+    int low = mine.T ? mine.T : INT32_MAX;           // the fewest row tiles of a sequence, and (tall) the most
 #pragma unroll 1
     for (int b = 32; b < p.num_seqs; b += 32) {
       const Seq x = seq_at<N>(p, b + lane);
@@ -228,6 +231,8 @@ struct Walker {
       n = add_up_to_max(n, x.n);
       T = add_up_to_max(T, x.T);
       longest = max(longest, x.nt);
+      tall = max(tall, x.T);
+      low = min(low, x.T ? x.T : INT32_MAX);
     }
     int64_t W = warp_total(w), U = warp_total(T);
     const int64_t rows = warp_total(n);
@@ -252,12 +257,26 @@ struct Walker {
       C = each * longest;
       length = units * longest;
     }
+    // Where all sequences have the same row tiles, the CTAs that have one piece of a sequence's keys between them
+    // go over it at the same time: it comes from memory once.  (On a line of row tiles one after the other, 16 x
+    // 35000 tokens with 2 row tiles were read twice, 654 MB.)
+    G = 1;
+    tall = __reduce_max_sync(0xffffffffu, tall);
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (!V && tall == low && tall > 1 && p.ctas % tall * 10 <= p.ctas) {
+      G = tall;
+      const uint32_t groups = static_cast<uint32_t>(p.ctas) / G;
+      length = static_cast<int>(static_cast<uint32_t>(length) / G);
+      C = static_cast<int>((length + groups - 1) / groups);
+    }
     upto = warp_scan(weight(), lane);
     units_upto = warp_scan(mine.T, lane);
-    lo = pos = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(blockIdx.x) * C));
+    lo = pos = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(blockIdx.x / G) * C));
     hi = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(lo) + C));
   }
-  __device__ __forceinline__ int weight() const { return V ? mine.T * V : mine.w; }   // of the held sequence
+  __device__ __forceinline__ int weight() const {    // of the held sequence
+    return V ? mine.T * V : G > 1 ? (mine.T ? mine.nt + kUnitTiles : 0) : mine.w;
+  }
   // The next segment; s.end if there is none.  Returns the sequence's error bits.
   __device__ __forceinline__ int next(const LatentParams& p, int lane, Segment& s) {
     s.end = 1;
@@ -279,7 +298,7 @@ struct Walker {
       const int nt = __shfl_sync(0xffffffffu, mine.nt, f);
       const int places = V ? V : nt + kUnitTiles;
       const int in = at - (f ? __shfl_sync(0xffffffffu, upto, f - 1) : 0);
-      const int nth = in / places, in_unit = in - nth * places;
+      const int nth = G > 1 ? blockIdx.x % G : in / places, in_unit = G > 1 ? in : in - nth * places;
       unit = units_before + nth + (f ? __shfl_sync(0xffffffffu, units_upto, f - 1) : 0);
       unit0 = pos - in_unit;
       unit_places = places;
@@ -305,12 +324,13 @@ struct Walker {
     JoinNote n;
     // (its first tile is at place kUnitTiles: the pieces are those of its tiles)
     n.first = blockIdx.x;
-    n.pieces = V ? 1 : (unit0 + unit_places - 1) / C - n.first + 1;
+    n.pieces = V ? 1 : (unit0 + unit_places - 1) / C - n.first / G + 1;
     n.first_slot = s.slot;
     n.q0 = s.q0;
     n.m = s.m;
     n.rows = min(N, s.n * p.heads - s.m * N);
-    n.pad[0] = n.pad[1] = 0;
+    n.stride = G;
+    n.pad = 0;
     return n;
   }
 };
@@ -1179,15 +1199,16 @@ __global__ void __launch_bounds__(128 * kGroups) latent_join_kernel(const __grid
   const int4 a = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x));
   const int4 b = __ldcg(reinterpret_cast<const int4*>(p.notes + blockIdx.x) + 1);
   if (static_cast<int>(blockIdx.x) >= units || a.x <= 1) return;
-  const int n = a.x, first = a.y, q0 = a.w, m = b.x;
+  const int n = a.x, first = a.y, q0 = a.w, m = b.x, stride = b.z;
   const int r0 = blockIdx.y * kCtaRows, rows = min(kCtaRows, b.y - r0);
   // A CTA whose wait ran out may have left no note: what stands there then is not followed.
-  if (n > p.ctas || first < 0 || first > p.ctas - n || (a.z & ~1) || q0 < 0 || m < 0 ||
+  if (n > p.ctas || stride < 1 || stride > p.ctas || first < 0 || first + static_cast<int64_t>(n - 1) * stride >= p.ctas ||
+      (a.z & ~1) || q0 < 0 || m < 0 ||
       m >= MTP_LATENT_MAX_NODES * MTP_LATENT_MAX_HEADS / N || b.y <= 0 || b.y > N ||
       q0 > p.total_q - 1 - (m * N + b.y - 1) / p.heads)
     return;
   if (rows <= 0) return;
-  auto slot_of = [&](int i) -> int64_t { return 2 * (first + i) + (i == 0 ? a.z : 0); };
+  auto slot_of = [&](int i) -> int64_t { return 2 * (first + i * stride) + (i == 0 ? a.z : 0); };
   const int d4 = tid & 127, g = tid >> 7, mine = kSplit ? 0 : g * kRows;   // first row of this thread's
   const float4* src = reinterpret_cast<const float4*>(p.o_part) + (r0 + mine) * (kDim / 4) + d4;
   const int step = kSplit ? kGroups : 1;
