@@ -762,8 +762,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
               (t + kPrefetch) * kTilePages + first * kBlockPages + lane < pages && far >= 0 && far < p.num_pages)
             prefetch_l2(p.cache + static_cast<int64_t>(far) * (kPage * kRow), kPage * kRow);
         }
-        // At first all CTAs ask at once: the first tile, then Q, which the first product wants too, then more.
-        if (u == 1 && !(ok = warp_wait(smem_u32(&bars.q_full), 0, abort_flag))) break;
+        // At first all CTAs ask at once: the first tile, then Q, which the first product wants too, then more.  (In the
+        // first segment only: its Q's phase is still the last one there.)
+        if (e == 0 && t == t0 + 1 && !(ok = warp_wait(smem_u32(&bars.q_full), 0, abort_flag))) break;
         const int st = u % kStages;
         const uint32_t stage = smem + st * kStage;
 #pragma unroll 1

@@ -311,6 +311,33 @@ def test_boundaries():
     assert torch.equal(wide2.run(), ref)
 
 
+@pytest.mark.parametrize("lens", [[9000] * 3 + [9100], [300, 20000, 700, 5000], [4000] * 8, [20000, 1, 20000]])
+@pytest.mark.parametrize("heads,nodes", [(128, 1), (128, 2), (64, 3)])
+def test_row_tiles_together(lens, heads, nodes):
+    """Two, four and three row tiles in every sequence, whose pieces several CTAs take together, with one
+    sequence that cannot be computed among them."""
+    lens = [max(n, nodes) for n in lens]
+    b = Batch(lens, [nodes] * len(lens), heads, seed=heads + nodes)
+    out = b.run()
+    assert b.status.item() == 0
+    short = [i for i, n in enumerate(lens) if n < 1000]
+    want = Batch([lens[i] for i in short], [nodes] * len(short), heads) if short else None
+    if want:                                             # (the long ones: rows against the same row computed alone)
+        want.q = torch.cat([b.q[b.cu_list[i]:b.cu_list[i + 1]] for i in short])
+        want.cache, want.bt = b.cache, b.bt[short].contiguous()
+        want.check(torch.cat([out[b.cu_list[i]:b.cu_list[i + 1]] for i in short]))
+    one = Batch([lens[-1]], [nodes], heads)
+    one.q, one.cache, one.bt = b.q[-nodes:], b.cache, b.bt[-1:].contiguous()
+    alone = f64(one.run())
+    # both are within the output's rounding, and each other's, of the same sums
+    assert np.abs(f64(out[-nodes:]) - alone).max() <= 2.0 ** -6 * np.abs(alone).max()
+    b.bt[1, 0] = -1
+    bad = b.run()
+    assert b.status.item() == api.ERR_PAGE and not bad[nodes:2 * nodes].any()
+    bad[nodes:2 * nodes] = out[nodes:2 * nodes]
+    assert torch.equal(bad, out)
+
+
 def test_many_units():
     """More row tiles than SMs, of one to three tokens over short contexts."""
     rng = np.random.default_rng(1)
@@ -365,6 +392,22 @@ def test_repeats_streams_and_graphs():
     torch.cuda.synchronize()
     assert torch.equal(outs[0], b.run())
     b.check(outs[0])
+
+
+@pytest.mark.parametrize("heads,nodes", [(16, 1), (16, 2), (16, 4), (128, 1)])
+def test_no_wait_runs_out(heads, nodes):
+    """Pieces that begin and end anywhere: with ever other lengths, CTAs whose first segment is one tile, two,
+    and so on, one after the other on a stream; every call ends by itself (a wait that ran out would tell)."""
+    b = Batch([9000] * 16, [nodes] * 16, heads, seed=8)
+    d = torch.full((1,), 0.75, device="cuda")
+    out = torch.zeros(b.total, heads, 512, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(api.mtp_latent_attn_workspace_size(16, b.total, heads, b.bt.shape[1]), dtype=torch.uint8, device="cuda")
+    for n in list(range(8200, 9000, 16)) + list(range(1000, 1800, 16)):
+        b.sl.fill_(n)
+        for _ in range(4):
+            api.mtp_latent_attn_fwd(b.q, b.cache, b.bt, b.sl, b.cu, d, b.scale, out=out, workspace=ws, status=b.status)
+    torch.cuda.synchronize()
+    assert b.status.item() == 0
 
 
 def test_a_far_page():
