@@ -634,211 +634,214 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
   static_assert(kWarpSoft * 32 * kFewRegisters + kSoftWarps * 32 * kManyRegisters <= kLatentThreads * kLaunchRegisters,
                 "registers of the block: a larger sum would wait forever");
   if (warp < kWarpSoft) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kFewRegisters));
-  if (warp == 0) {
-    // ============================== the walk, and the scores =====================================
-    Walker<N> walk;
-    walk.start(p, lane);
-    if (blockIdx.x == 0 && lane == 0) *p.units = walk.V ? 0 : min(walk.units, p.unit_bound);
-    constexpr uint32_t kIdesc = idesc_e4m3_f32(128, 2 * N, false);
-    const Desc q = desc_of(sdesc_sw128(smem + off_q<N>(), 16, 1024));
-    const Desc q_rope = desc_of(sdesc_sw64(smem + off_q<N>() + kColumns * q_column<N>(), 16, 512));
-    const Desc c0 = desc_of(sdesc_sw64(smem, 16, kGroup));
-    uint32_t u = 0;                                // tiles so far
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kFewRegisters));
+    if (warp == 0) {
+      // ============================== the walk, and the scores =====================================
+      Walker<N> walk;
+      walk.start(p, lane);
+      if (blockIdx.x == 0 && lane == 0) *p.units = walk.V ? 0 : min(walk.units, p.unit_bound);
+      constexpr uint32_t kIdesc = idesc_e4m3_f32(128, 2 * N, false);
+      const Desc q = desc_of(sdesc_sw128(smem + off_q<N>(), 16, 1024));
+      const Desc q_rope = desc_of(sdesc_sw64(smem + off_q<N>() + kColumns * q_column<N>(), 16, 512));
+      const Desc c0 = desc_of(sdesc_sw64(smem, 16, kGroup));
+      uint32_t u = 0;                                // tiles so far
 #pragma unroll 1
-    for (int e = 0;;) {
-      Segment s;
-      const int err = walk.next(p, lane, s);
-      auto leave_note = [&]() {
-        if (lane == 0 && s.t0 == 0 && !walk.V && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
-      };
-      if (!s.end && err) {
+      for (int e = 0;;) {
+        Segment s;
+        const int err = walk.next(p, lane, s);
+        auto leave_note = [&]() {
+          if (lane == 0 && s.t0 == 0 && !walk.V && walk.unit < p.unit_bound) p.notes[walk.unit] = walk.note(p, s);
+        };
+        if (!s.end && err) {
+          leave_note();
+          // zeros for the rows of a sequence that cannot be computed, here: it has no tiles
+          if (lane == 0) set_status(p.status, err);
+          const int rows = min(N, s.n * p.heads - s.m * N);
+#pragma unroll 1
+          for (int i = 0; i < rows; ++i) {
+            const int rr = s.m * N + i, t = rr / p.heads;
+            uint4* out = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.q0 + t) * p.out_stride_tok +
+                                                  static_cast<int64_t>(rr - t * p.heads) * p.out_stride_head);
+            out[lane] = out[lane + 32] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          continue;
+        }
+        if (!warp_wait(smem_u32(&bars.seg_free[e % kSegRing]), ((e / kSegRing) & 1) ^ 1, abort_flag)) break;
+        if (lane == 0) {
+          bars.seg[e % kSegRing] = s;
+          mbar_arrive(smem_u32(&bars.seg_full[e % kSegRing]));
+        }
+        if (s.end) break;
         leave_note();
-        // zeros for the rows of a sequence that cannot be computed, here: it has no tiles
-        if (lane == 0) set_status(p.status, err);
-        const int rows = min(N, s.n * p.heads - s.m * N);
-#pragma unroll 1
-        for (int i = 0; i < rows; ++i) {
-          const int rr = s.m * N + i, t = rr / p.heads;
-          uint4* out = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.q0 + t) * p.out_stride_tok +
-                                                static_cast<int64_t>(rr - t * p.heads) * p.out_stride_head);
-          out[lane] = out[lane + 32] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        continue;
-      }
-      if (!warp_wait(smem_u32(&bars.seg_free[e % kSegRing]), ((e / kSegRing) & 1) ^ 1, abort_flag)) break;
-      if (lane == 0) {
-        bars.seg[e % kSegRing] = s;
-        mbar_arrive(smem_u32(&bars.seg_full[e % kSegRing]));
-      }
-      if (s.end) break;
-      leave_note();
-      if (!warp_wait(smem_u32(&bars.q_full), e & 1, abort_flag)) break;
-      const uint32_t end = u + (s.t1 - s.t0);
-      if (elect_one()) {
-        tc_fence_after();
-#pragma unroll 1
-        for (; u < end; ++u) {                     // S(u) = C Q^T
-          const uint32_t st = u % kStages, parity = (u / kStages) & 1, d = tmem + (u & 1) * kSBuf;
-          bool ok = wait_for(smem_u32(&bars.s_free[u & 1]), ((u >> 1) & 1) ^ 1, abort_flag);
-#pragma unroll
-          for (int c = 0; c < kBlocks; ++c) ok = ok && wait_for(smem_u32(&bars.full[st][c]), parity, abort_flag);
-          if (!ok) break;
+        if (!warp_wait(smem_u32(&bars.q_full), e & 1, abort_flag)) break;
+        const uint32_t end = u + (s.t1 - s.t0);
+        if (elect_one()) {
           tc_fence_after();
-          const uint32_t a = c0.lo + st * (kStage >> 4);
-          mma_one<false>(d, a, c0.hi, q.lo, q.hi, kIdesc);
+#pragma unroll 1
+          for (; u < end; ++u) {                     // S(u) = C Q^T
+            const uint32_t st = u % kStages, parity = (u / kStages) & 1, d = tmem + (u & 1) * kSBuf;
+            bool ok = wait_for(smem_u32(&bars.s_free[u & 1]), ((u >> 1) & 1) ^ 1, abort_flag);
 #pragma unroll
-          for (int k = 1; k < 4 * kColumns; ++k)   // 32 dims
-            mma_one<true>(d, a + (((k >> 1) * kAtom + 32 * (k & 1)) >> 4), c0.hi,
-                          q.lo + (((k >> 2) * q_column<N>() + 32 * (k & 3)) >> 4), q.hi, kIdesc);
+            for (int c = 0; c < kBlocks; ++c) ok = ok && wait_for(smem_u32(&bars.full[st][c]), parity, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = c0.lo + st * (kStage >> 4);
+            mma_one<false>(d, a, c0.hi, q.lo, q.hi, kIdesc);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) mma_one<true>(d, a + ((kRopeAt + 32 * k) >> 4), c0.hi, q_rope.lo + (32 * k >> 4), q_rope.hi, kIdesc);
-          mma_commit(smem_u32(&bars.s_full[u & 1]));
+            for (int k = 1; k < 4 * kColumns; ++k)   // 32 dims
+              mma_one<true>(d, a + (((k >> 1) * kAtom + 32 * (k & 1)) >> 4), c0.hi,
+                            q.lo + (((k >> 2) * q_column<N>() + 32 * (k & 3)) >> 4), q.hi, kIdesc);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mma_one<true>(d, a + ((kRopeAt + 32 * k) >> 4), c0.hi, q_rope.lo + (32 * k >> 4), q_rope.hi, kIdesc);
+            mma_commit(smem_u32(&bars.s_full[u & 1]));
+          }
         }
+        __syncwarp();
+        if (*abort_flag) break;
+        u = end;
+        ++e;
+      }
+      if (blockIdx.x == 0)                           // tell of sequences whose rows are not known
+        for (int b = lane; b < p.num_seqs; b += 32) {
+          const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+          if (q0 < 0 || q1 <= q0 || q1 > p.total_q) set_status(p.status, MTPATTN_ERR_QLEN);
+        }
+      __syncwarp();
+      if (elect_one()) {                             // no product may run on when the CTA ends
+        mma_commit(smem_u32(&bars.final_mma[0]));
+        volatile int no_abort = 0;
+        wait_for(smem_u32(&bars.final_mma[0]), 0, &no_abort);
       }
       __syncwarp();
-      if (*abort_flag) break;
-      u = end;
-      ++e;
-    }
-    if (blockIdx.x == 0)                           // tell of sequences whose rows are not known
-      for (int b = lane; b < p.num_seqs; b += 32) {
-        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-        if (q0 < 0 || q1 <= q0 || q1 > p.total_q) set_status(p.status, MTPATTN_ERR_QLEN);
-      }
-    __syncwarp();
-    if (elect_one()) {                             // no product may run on when the CTA ends
-      mma_commit(smem_u32(&bars.final_mma[0]));
-      volatile int no_abort = 0;
-      wait_for(smem_u32(&bars.final_mma[0]), 0, &no_abort);
-    }
-    __syncwarp();
-  } else if (warp >= 2) {
-    // ============================== the tiles by TMA, two blocks a warp ===========================
-    const int first = (warp - 2) * kWarpBlocks;
-    if (lane == 0) prefetch_tmap(&p.tmap);
-    const uint64_t once = l2_policy_evict_first();
-    uint64_t again;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
-    uint32_t u = 0;                                // tiles so far
-    int asked = 0;                                 // blocks of the last one asked for
-    bool ok = true;
+    } else if (warp >= 2) {
+      // ============================== the tiles by TMA, two blocks a warp ===========================
+      const int first = (warp - 2) * kWarpBlocks;
+      if (lane == 0) prefetch_tmap(&p.tmap);
+      const uint64_t once = l2_policy_evict_first();
+      uint64_t again;
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(again));
+      uint32_t u = 0;                                // tiles so far
+      int asked = 0;                                 // blocks of the last one asked for
+      bool ok = true;
 #pragma unroll 1
-    for (int e = 0; ok; ++e) {
-      ok = warp_wait(smem_u32(&bars.seg_full[e % kSegRing]), (e / kSegRing) & 1, abort_flag);
-      if (!ok) break;
-      Segment& s = bars.seg[e % kSegRing];
-      if (s.end) break;
-      const int t0 = s.t0, t1 = s.t1, pages = (s.L + kPage - 1) / kPage;
-      const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
-      const uint64_t policy = static_cast<int64_t>(s.n) * p.heads <= N ? once : again;
-      // table entries, a lane one of eight tiles' 4 that are this warp's, with the next 32 on the way
-      auto entries = [&](int t) -> int {
-        const int64_t pg = static_cast<int64_t>(t + lane / kWarpPages) * kTilePages + first * kBlockPages + lane % kWarpPages;
-        return pg < pages ? bt[pg] : 0;
-      };
-      int now = entries(t0), ahead = entries(t0 + 32 / kWarpPages);
-#pragma unroll 1
-      for (int t = t0; t < t1; ++t, ++u) {
-        const int k = (t - t0) % (32 / kWarpPages);
-        if (k == 0 && t > t0) {
-          now = ahead;
-          ahead = entries(t + 32 / kWarpPages);
-        }
-        // a lane half a page
-        const int np = min(kTilePages, pages - t * kTilePages) - first * kBlockPages;   // this warp's, if above 0
-        const int mine = __shfl_sync(0xffffffffu, now, k * kWarpPages + lane % kWarpPages);
-        const bool bad = __any_sync(0xffffffffu, lane < min(np, kWarpPages) && (mine < 0 || mine >= p.num_pages));
-        if (bad && lane == 0) {
-          *const_cast<volatile int*>(&s.bad) = 1;
-          set_status(p.status, MTPATTN_ERR_PAGE);
-        }
-        // A stage is free late, and a fetch from memory would be the longest part of its turn: pages are brought
-        // into L2 some tiles ahead.
-        {
-          const int k2 = k + kPrefetch;
-          const int far = __shfl_sync(0xffffffffu, k2 < 32 / kWarpPages ? now : ahead, (k2 % (32 / kWarpPages)) * kWarpPages + lane % kWarpPages);
-          if (lane < kWarpPages && t + kPrefetch < t1 &&
-              (t + kPrefetch) * kTilePages + first * kBlockPages + lane < pages && far >= 0 && far < p.num_pages)
-            prefetch_l2(p.cache + static_cast<int64_t>(far) * (kPage * kRow), kPage * kRow);
-        }
-        // At first all CTAs ask at once: the first tile, then Q, which the first product wants too, then more.  (In the
-        // first segment only: its Q's phase is still the last one there.)
-        if (e == 0 && t == t0 + 1 && !(ok = warp_wait(smem_u32(&bars.q_full), 0, abort_flag))) break;
-        const int st = u % kStages;
-        const uint32_t stage = smem + st * kStage;
-#pragma unroll 1
-        for (int c = 0; c < kWarpBlocks; ++c) {
-          ok = warp_wait(smem_u32(&bars.empty[st][first + c]), ((u / kStages) & 1) ^ 1, abort_flag);
-          if (!ok) break;
-          asked = c + 1;
-          const uint32_t bar = smem_u32(&bars.full[st][first + c]);
-          const int here = bad ? 0 : max(0, min(kBlockPages, np - c * kBlockPages));   // pages to fetch
-          if (lane == 0) {
-            if (here == 0) mbar_arrive(bar);       // (of a bad page nothing: the segment's rows become zeros)
-            else mbar_arrive_expect_tx(bar, here * kPage * kRow);
-          }
-          const int pg = __shfl_sync(0xffffffffu, mine, (c * kBlockPages + (lane >> 1)) % kWarpPages);
-          if (lane < 2 * here)
-            tma_load_4d(stage + (2 * (first + c) * kBlockPages + lane) * kGroup, &p.tmap, bar, 0, (lane & 1) * 8, 0, pg, policy);
-          __syncwarp();
-        }
+      for (int e = 0; ok; ++e) {
+        ok = warp_wait(smem_u32(&bars.seg_full[e % kSegRing]), (e / kSegRing) & 1, abort_flag);
         if (!ok) break;
-      }
-      if (ok && lane == 0) mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
-    }
-    // What was asked for has to arrive before the CTA may end: u tiles whole, and blocks of one more after
-    // an abort.
-    if (*abort_flag) {
-      volatile int no_abort = 0;
-      if (!ok && asked < kWarpBlocks)
-        for (int c = 0; c < asked; ++c) wait_for(smem_u32(&bars.full[u % kStages][first + c]), (u / kStages) & 1, &no_abort);
-      for (uint32_t k = 1; k <= kStages && k <= u; ++k)
-        for (int c = 0; c < kWarpBlocks; ++c)
-          wait_for(smem_u32(&bars.full[(u - k) % kStages][first + c]), ((u - k) / kStages) & 1, &no_abort);
-    }
-  } else if (warp == 1) {
-    // ============================== the outputs ===================================================
-    // (Issued apart from the scores, so that neither waits for what the other lacks.)
-    if (elect_one()) {
-      auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_for(smem_u32(&bar), parity, abort_flag); };
-      constexpr uint32_t kIdesc = idesc_e4m3_f32(128, N, true) | kAMajorM;
-      const Desc lo = desc_of(sdesc_sw64(smem + off_p<N>(), 512, 512)), hi = desc_of(sdesc_sw64(smem + kRopeAt, 512, kGroup));
-      const Desc v0 = desc_of(sdesc_sw64(smem, kAtom, kGroup));
-      uint32_t u = 0;
-      bool alive = true;
+        Segment& s = bars.seg[e % kSegRing];
+        if (s.end) break;
+        const int t0 = s.t0, t1 = s.t1, pages = (s.L + kPage - 1) / kPage;
+        const int32_t* bt = p.block_tables + static_cast<int64_t>(s.b) * p.max_pages;
+        const uint64_t policy = static_cast<int64_t>(s.n) * p.heads <= N ? once : again;
+        // table entries, a lane one of eight tiles' 4 that are this warp's, with the next 32 on the way
+        auto entries = [&](int t) -> int {
+          const int64_t pg = static_cast<int64_t>(t + lane / kWarpPages) * kTilePages + first * kBlockPages + lane % kWarpPages;
+          return pg < pages ? bt[pg] : 0;
+        };
+        int now = entries(t0), ahead = entries(t0 + 32 / kWarpPages);
 #pragma unroll 1
-      for (int e = 0; alive; ++e) {
-        if (!(alive = wait(bars.seg_full[e % kSegRing], (e / kSegRing) & 1))) break;
-        const volatile Segment& s = bars.seg[e % kSegRing];
-        const bool last = s.end;
-        const uint32_t end = u + (s.t1 - s.t0);
-        mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
-        if (last) break;
-#pragma unroll 1
-        for (uint32_t more = 0; u < end && alive; ++u, more = 1) {   // O (+)= C^T P^T
-          const uint32_t st = u % kStages, at = st * (kStage >> 4);
-#pragma unroll
-          for (int k = 0; k < kBlocks; ++k) {
-            if (!(alive = wait(bars.p_full[k], u & 1))) break;
-            tc_fence_after();
-            // Both terms of P one after the other, the second with the A operand that the first has brought in.
-#pragma unroll
-            for (int c = 0; c < kColumns; ++c)
-              mma_two(tmem + kOCol + c * N, v0.lo + at + ((k * (kBlockKeys / 8) * kGroup + 2 * c * kAtom) >> 4), v0.hi,
-                      lo.lo + (k * kBlockKeys * 64 >> 4), lo.hi, hi.lo + at + (k * (kBlockKeys / 8) * kGroup >> 4), hi.hi, kIdesc,
-                      k ? 1u : more);
-            mma_commit(smem_u32(&bars.empty[st][k]));    // (with the rows of both of P's terms)
+        for (int t = t0; t < t1; ++t, ++u) {
+          const int k = (t - t0) % (32 / kWarpPages);
+          if (k == 0 && t > t0) {
+            now = ahead;
+            ahead = entries(t + 32 / kWarpPages);
           }
-          if (!alive) break;
-          mma_commit(smem_u32(&bars.pv_done));
+          // a lane half a page
+          const int np = min(kTilePages, pages - t * kTilePages) - first * kBlockPages;   // this warp's, if above 0
+          const int mine = __shfl_sync(0xffffffffu, now, k * kWarpPages + lane % kWarpPages);
+          const bool bad = __any_sync(0xffffffffu, lane < min(np, kWarpPages) && (mine < 0 || mine >= p.num_pages));
+          if (bad && lane == 0) {
+            *const_cast<volatile int*>(&s.bad) = 1;
+            set_status(p.status, MTPATTN_ERR_PAGE);
+          }
+          // A stage is free late, and a fetch from memory would be the longest part of its turn: pages are brought
+          // into L2 some tiles ahead.
+          {
+            const int k2 = k + kPrefetch;
+            const int far = __shfl_sync(0xffffffffu, k2 < 32 / kWarpPages ? now : ahead, (k2 % (32 / kWarpPages)) * kWarpPages + lane % kWarpPages);
+            if (lane < kWarpPages && t + kPrefetch < t1 &&
+                (t + kPrefetch) * kTilePages + first * kBlockPages + lane < pages && far >= 0 && far < p.num_pages)
+              prefetch_l2(p.cache + static_cast<int64_t>(far) * (kPage * kRow), kPage * kRow);
+          }
+          // At first all CTAs ask at once: the first tile, then Q, which the first product wants too, then more.  (In the
+          // first segment only: its Q's phase is still the last one there.)
+          if (e == 0 && t == t0 + 1 && !(ok = warp_wait(smem_u32(&bars.q_full), 0, abort_flag))) break;
+          const int st = u % kStages;
+          const uint32_t stage = smem + st * kStage;
+#pragma unroll 1
+          for (int c = 0; c < kWarpBlocks; ++c) {
+            ok = warp_wait(smem_u32(&bars.empty[st][first + c]), ((u / kStages) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+#ifdef MTPATTN_TEST_STALL
+            if (s.b == 0 && s.m == 0 && t == 0 && first + c == 0) continue;   // test builds: the wait for it runs out
+#endif
+            asked = c + 1;
+            const uint32_t bar = smem_u32(&bars.full[st][first + c]);
+            const int here = bad ? 0 : max(0, min(kBlockPages, np - c * kBlockPages));   // pages to fetch
+            if (lane == 0) {
+              if (here == 0) mbar_arrive(bar);       // (of a bad page nothing: the segment's rows become zeros)
+              else mbar_arrive_expect_tx(bar, here * kPage * kRow);
+            }
+            const int pg = __shfl_sync(0xffffffffu, mine, (c * kBlockPages + (lane >> 1)) % kWarpPages);
+            if (lane < 2 * here)
+              tma_load_4d(stage + (2 * (first + c) * kBlockPages + lane) * kGroup, &p.tmap, bar, 0, (lane & 1) * 8, 0, pg, policy);
+            __syncwarp();
+          }
+          if (!ok) break;
         }
+        if (ok && lane == 0) mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
       }
-      mma_commit(smem_u32(&bars.final_mma[1]));
-      volatile int no_abort = 0;
-      wait_for(smem_u32(&bars.final_mma[1]), 0, &no_abort);
+      // What was asked for has to arrive before the CTA may end: u tiles whole, and blocks of one more after
+      // an abort.
+      if (*abort_flag) {
+        volatile int no_abort = 0;
+        if (!ok && asked < kWarpBlocks)
+          for (int c = 0; c < asked; ++c) wait_for(smem_u32(&bars.full[u % kStages][first + c]), (u / kStages) & 1, &no_abort);
+        for (uint32_t k = 1; k <= kStages && k <= u; ++k)
+          for (int c = 0; c < kWarpBlocks; ++c)
+            wait_for(smem_u32(&bars.full[(u - k) % kStages][first + c]), ((u - k) / kStages) & 1, &no_abort);
+      }
+    } else if (warp == 1) {
+      // ============================== the outputs ===================================================
+      // (Issued apart from the scores, so that neither waits for what the other lacks.)
+      if (elect_one()) {
+        auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_for(smem_u32(&bar), parity, abort_flag); };
+        constexpr uint32_t kIdesc = idesc_e4m3_f32(128, N, true) | kAMajorM;
+        const Desc lo = desc_of(sdesc_sw64(smem + off_p<N>(), 512, 512)), hi = desc_of(sdesc_sw64(smem + kRopeAt, 512, kGroup));
+        const Desc v0 = desc_of(sdesc_sw64(smem, kAtom, kGroup));
+        uint32_t u = 0;
+        bool alive = true;
+#pragma unroll 1
+        for (int e = 0; alive; ++e) {
+          if (!(alive = wait(bars.seg_full[e % kSegRing], (e / kSegRing) & 1))) break;
+          const volatile Segment& s = bars.seg[e % kSegRing];
+          const bool last = s.end;
+          const uint32_t end = u + (s.t1 - s.t0);
+          mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
+          if (last) break;
+#pragma unroll 1
+          for (uint32_t more = 0; u < end && alive; ++u, more = 1) {   // O (+)= C^T P^T
+            const uint32_t st = u % kStages, at = st * (kStage >> 4);
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+              if (!(alive = wait(bars.p_full[k], u & 1))) break;
+              tc_fence_after();
+              // Both terms of P one after the other, the second with the A operand that the first has brought in.
+#pragma unroll
+              for (int c = 0; c < kColumns; ++c)
+                mma_two(tmem + kOCol + c * N, v0.lo + at + ((k * (kBlockKeys / 8) * kGroup + 2 * c * kAtom) >> 4), v0.hi,
+                        lo.lo + (k * kBlockKeys * 64 >> 4), lo.hi, hi.lo + at + (k * (kBlockKeys / 8) * kGroup >> 4), hi.hi, kIdesc,
+                        k ? 1u : more);
+              mma_commit(smem_u32(&bars.empty[st][k]));    // (with the rows of both of P's terms)
+            }
+            if (!alive) break;
+            mma_commit(smem_u32(&bars.pv_done));
+          }
+        }
+        mma_commit(smem_u32(&bars.final_mma[1]));
+        volatile int no_abort = 0;
+        wait_for(smem_u32(&bars.final_mma[1]), 0, &no_abort);
+      }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kManyRegisters));
     // ============================== softmax, Q's operand, the output ==============================
@@ -852,322 +855,344 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
     Meeting meet{smem_u32(&bars.meet[half]), 0}, meet_all{smem_u32(&bars.meet[2]), 0};
     uint32_t u = 0;
     bool alive = true;
-    // Q's two terms of a segment, kSide lanes a row, and what there is of each row.  Asks that the last product
-    // that reads the previous ones is done: that all S of their segment has been read.
+    // Q's two terms of a segment, kSide lanes a row, and what there is of each row.  Asks that the last product that
+    // reads the previous ones is done: that all S of their segment has been read.
     auto prepare = [&](const Segment& of) {
       const int q0 = of.q0, n = of.n, m = of.m, rows = min(N, n * p.heads - m * N);
-      constexpr int kSide = kSoftWarps * 32 / N, kParts = (kRow / 8 + kSide - 1) / kSide;   // blocks of 8 a lane
-      const int r = (w * 32 + lane) / kSide, side = lane % kSide;
-      const int rr = m * N + r, tok = r < rows ? rr / p.heads : 0;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(q0 + tok) * p.q_stride_tok +
-                                                        static_cast<int64_t>(rr - tok * p.heads) * p.q_stride_head);
-      uint64_t word = 0;
-      if (r < rows) word = p.mask ? p.mask[q0 + tok] : (2ull << tok) - 1ull;
+      constexpr int kSide = N == 16 ? 16 : 8, kParts = (kRow / 8 + kSide - 1) / kSide;   // blocks of 8 a lane
+      constexpr int kStep = kSoftWarps * 32 / kSide;   // rows at a time; a multiple of 8
+      const int side = lane % kSide, first = (w * 32 + lane) / kSide;
       uint4 x[kParts];
-      uint32_t top = 0;
+      uint64_t word = 0;
+      auto fetch = [&](int r) {
+        const int rr = m * N + r, tok = r < rows ? rr / p.heads : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(q0 + tok) * p.q_stride_tok +
+                                                          static_cast<int64_t>(rr - tok * p.heads) * p.q_stride_head) + side;
 #pragma unroll
-      for (int i = 0; i < kParts; ++i) {
-        const int j = side + i * kSide;
-        x[i] = r < rows && j < kRow / 8 ? src[j] : make_uint4(0u, 0u, 0u, 0u);
-      }
+        for (int i = 0; i < kParts; ++i)
+          x[i] = r < rows && (kParts * kSide == kRow / 8 || side + i * kSide < kRow / 8) ? src[i * kSide]
+                                                                                       : make_uint4(0u, 0u, 0u, 0u);
+        word = r < rows ? (p.mask ? p.mask[q0 + tok] : (2ull << tok) - 1ull) : 0;
+      };
+      // Where a row's blocks go.  Block j of the 64 of the latent part is half of a 16-byte place, column j / 16,
+      // swizzled by the row's lowest bits, which are the same in all of a lane's rows.
+      const uint32_t q = smem + off_q<N>();
+      uint32_t place[16 / kSide];
 #pragma unroll
-      for (int i = 0; i < kParts; ++i)
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-#pragma unroll
-      for (int o = 1; o < kSide; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int exponent = max(top & 0xffffu, top >> 16) >> 7;   // biased; 255: not finite
-      const int a = min(134 - exponent, 126);
-      const uint32_t up1 = static_cast<uint32_t>(127 + a) << 7, up = up1 | up1 << 16;
-      const uint32_t at0 = smem + off_q<N>() + r * 128, at1 = smem + off_q<N>() + kColumns * q_column<N>() + r * 64;
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) {
+      for (int i = 0; i < 16 / kSide; ++i) {
         const uint32_t j = side + i * kSide;
-        if (kParts * kSide > kRow / 8 && j >= kRow / 8) continue;
-        uint32_t h0, h1, l0, l1;
-        two_terms<false>(scaled_half2(x[i].x, up), scaled_half2(x[i].y, up), 0u, h0, l0);
-        two_terms<false>(scaled_half2(x[i].z, up), scaled_half2(x[i].w, up), 0u, h1, l1);
-        if (exponent == 255) h0 = h1 = l0 = l1 = 0x7f7f7f7fu;
-        // 16 blocks a column's row, 8 of the rotated part, swizzled in pairs
-        const bool rope = j >= kDim / 8;
-        const uint32_t at = rope ? at1 + ((((j - kDim / 8) >> 1) ^ ((r >> 1) & 3)) << 4) + (j & 1) * 8
-                                 : at0 + (j >> 4) * q_column<N>() + ((((j & 15) >> 1) ^ (r & 7)) << 4) + (j & 1) * 8;
-        st_shared8(at, h0, h1);
-        st_shared8(at + (rope ? N * 64 : N * 128), l0, l1);
+        place[i] = q + first * 128 + (((j >> 1) ^ (first & 7)) << 4) + (j & 1) * 8;
       }
-      if (side == 0) {
-        sh.factor[r] = r < rows ? factor * __uint_as_float(static_cast<uint32_t>(127 - a) << 23) : 0.f;
-        sh.ref[r] = kNoRef;
-        if (n < 64) word &= (1ull << n) - 1ull;
-        sh.word[r] = word;
+      const uint32_t rope_place = q + kColumns * q_column<N>() + first * 64 + (((side >> 1) ^ ((first >> 1) & 3)) << 4) + (side & 1) * 8;
+      fetch(first);
+#pragma unroll 1
+      for (int r = first, go = 0; go < N / kStep; ++go, r += kStep) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                       __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+#pragma unroll
+        for (int o = 1; o < kSide; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int exponent = max(top & 0xffffu, top >> 16) >> 7;   // biased; 255: not finite
+        const int a = min(134 - exponent, 126);
+        uint32_t up = static_cast<uint32_t>(127 + a) << 7;
+        if (exponent == 255) up = 0x7fc0u;           // NaN, and so all of the row's codes
+        up |= up << 16;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          uint32_t h0, h1, l0, l1;
+          two_terms<false>(scaled_half2(x[i].x, up), scaled_half2(x[i].y, up), 0u, h0, l0);
+          two_terms<false>(scaled_half2(x[i].z, up), scaled_half2(x[i].w, up), 0u, h1, l1);
+          if (i * kSide < kDim / 8) {
+            const uint32_t at = place[i % (16 / kSide)] + i * kSide / 16 * q_column<N>() + go * kStep * 128;
+            st_shared8(at, h0, h1);
+            st_shared8(at + N * 128, l0, l1);
+          } else if (side < 8) {
+            const uint32_t at = rope_place + go * kStep * 64;
+            st_shared8(at, h0, h1);
+            st_shared8(at + N * 64, l0, l1);
+          }
+        }
+        if (side == 0) {
+          sh.factor[r] = r < rows ? factor * __uint_as_float(static_cast<uint32_t>(127 - a) << 23) : 0.f;
+          sh.ref[r] = kNoRef;
+          sh.word[r] = n < 64 ? word & ((1ull << n) - 1ull) : word;
+        }
+        if (go + 1 < N / kStep) fetch(r + kStep);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
     };
-    if ((alive = warp_wait(smem_u32(&bars.seg_full[0]), 0, abort_flag)) && !bars.seg[0].end) {
-      prepare(bars.seg[0]);
-      alive = meet_all(lane, abort_flag);            // every row's factor and word
-    }
+    // Turn e: segment e, and between its products and its output the next one's Q (turn -1: the first one's).
 #pragma unroll 1
-    for (int e = 0; alive; ++e) {
-      const Segment s = bars.seg[e % kSegRing];
-      if (s.end) break;
-      const int rows = min(N, s.n * p.heads - s.m * N);
-      // of the rows of this warp, in every lane: a load from shared memory waits for the products' reads
-      float l[kHalf], fac[kHalf], ref[kHalf];
+    for (int e = -1; alive; ++e) {
+      Segment s;
+      int rows = 0;
+      bool whole = false;
+      if (e >= 0) {
+        s = bars.seg[e % kSegRing];
+        rows = min(N, s.n * p.heads - s.m * N);
+        // of the rows of this warp, in every lane: a load from shared memory waits for the products' reads
+        float l[kHalf], fac[kHalf], ref[kHalf];
 #pragma unroll
-      for (int r = 0; r < kHalf; ++r) {
-        l[r] = ref[r] = 0.f;
-        fac[r] = sh.factor[row0 + r];
-      }
-      const int start = s.L - s.n;                   // first new token
-      const bool late = (s.t0 + 1) * kKeys > start;  // a row may see nothing of the first tile
+        for (int r = 0; r < kHalf; ++r) {
+          l[r] = ref[r] = 0.f;
+          fac[r] = sh.factor[row0 + r];
+        }
+        const int start = s.L - s.n;                   // first new token
+        const bool late = (s.t0 + 1) * kKeys > start;  // a row may see nothing of the first tile
 #pragma unroll 1
-      for (int t = s.t0; t < s.t1; ++t, ++u) {
-        alive &= warp_wait(smem_u32(&bars.s_full[u & 1]), (u >> 1) & 1, abort_flag);
-        tc_fence_after();
-        const int j = t * kKeys + key;
-        const bool ragged = (t + 1) * kKeys > start;  // new tokens, or places behind the sequence
-        float y[kHalf];                              // logits above the reference, then weights
-        auto logits = [&]() {
-          uint32_t h[kHalf], lo[kHalf];
-          const uint32_t at = tmem + lanes + (u & 1) * kSBuf + row0;
-          tmem_ld<kHalf>(at, h);
-          tmem_ld<kHalf>(at + N, lo);
-          tmem_wait<kHalf>(h);
-          tmem_wait<kHalf>(lo);
+        for (int t = s.t0; t < s.t1; ++t, ++u) {
+          alive &= warp_wait(smem_u32(&bars.s_full[u & 1]), (u >> 1) & 1, abort_flag);
+          tc_fence_after();
+          const int j = t * kKeys + key;
+          const bool ragged = (t + 1) * kKeys > start;  // new tokens, or places behind the sequence
+          uint32_t seen = ~0u;                         // the rows of this warp that see the key
+          if (ragged) {
+            if (j >= start) seen = 0u;
+            const uint64_t word = lane < kHalf ? sh.word[row0 + lane] : 0;
+            const int first = t * kKeys + quarter * 32 - start;   // new token that lane 0's key is
+#pragma unroll 1
+            for (int k = max(0, -first); k < min(32, s.n - first); ++k) {
+              const uint32_t rows_of = __ballot_sync(0xffffffffu, (word >> (first + k)) & 1);
+              if (lane == k) seen = rows_of;
+            }
+          }
+          float y[kHalf];                              // logits above the reference, then weights
+          auto logits = [&]() {
+            uint32_t h[kHalf], lo[kHalf];
+            const uint32_t at = tmem + lanes + (u & 1) * kSBuf + row0;
+            tmem_ld<kHalf>(at, h);
+            tmem_ld<kHalf>(at + N, lo);
+            tmem_wait<kHalf>(h);
+            tmem_wait<kHalf>(lo);
 #pragma unroll
-          for (int r = 0; r < kHalf; ++r) y[r] = fmaf(__uint_as_float(h[r]) + __uint_as_float(lo[r]), fac[r], -ref[r]);
+            for (int r = 0; r < kHalf; ++r) y[r] = fmaf(__uint_as_float(h[r]) + __uint_as_float(lo[r]), fac[r], -ref[r]);
+            if (ragged) {
+#pragma unroll
+              for (int r = 0; r < kHalf; ++r)
+                if (!((seen >> r) & 1u)) y[r] = -INFINITY;
+            }
+          };
+          uint32_t hi[kHalf / 4], lo[kHalf / 4];
+          auto weights = [&]() {
+#pragma unroll
+            for (int r = 0; r < kHalf; r += 4) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[r + i] = exp2_hw(y[r + i]);
+              two_terms<true>(half2_of(y[r], y[r + 1]), half2_of(y[r + 2], y[r + 3]), dither, hi[r / 4], lo[r / 4]);
+            }
+          };
+          logits();
+          // A reference is raised where a logit is too far above it, and at first.
+          const bool forced = t == s.t0 || (ragged && late);
+          bool over = forced;
+          if (!forced) {
+            float a = y[0], b = y[1];
+#pragma unroll
+            for (int r = 2; r < kHalf; r += 2) {
+              a = fmaxf(a, y[r]);
+              b = fmaxf(b, y[r + 1]);
+            }
+            over = fmaxf(a, b) > kShift + kTau;
+          }
+          over = any_of_half(half, over || !alive);
+          if (over) {
+            if (!(alive = !any_of_half(half, !alive || *abort_flag))) break;
+            if (!forced) logits();
+            float tops[kHalf];
+#pragma unroll
+            for (int r = 0; r < kHalf; ++r) tops[r] = y[r];
+            const float mine = row_maxima<kHalf>(tops, lane);
+            if (lane < kHalf) sh.xch[half][quarter][lane] = mine;
+            meet_half(half);
+            if (quarter == 0 && lane < kHalf) {
+              const float (&x)[4][kHalf] = sh.xch[half];
+              const float top = fmaxf(fmaxf(x[0][lane], x[1][lane]), fmaxf(x[2][lane], x[3][lane]));
+              const float old = sh.ref[row0 + lane];   // kNoRef: the row has seen nothing, y is above 0
+              float step = 0.f, f = 1.f;
+              if (top > (old == kNoRef ? -INFINITY : kShift + kTau)) {
+                step = kShift - top - (s.t1 - t > 2 ? kRoom : 0.f);   // (the last tiles will not raise it much)
+                f = old == kNoRef ? 0.f : exp2_hw(step);
+                sh.ref[row0 + lane] = (old == kNoRef ? 0.f : old) - step;
+              }
+              sh.step[row0 + lane] = step;
+              sh.f[row0 + lane] = f;
+            }
+            meet_half(half);
+#pragma unroll
+            for (int r = 0; r < kHalf; ++r) {
+              const float step = sh.step[row0 + r];
+              y[r] += step;
+              ref[r] -= step;
+            }
+            if (t > s.t0) {
+              // (O may be touched once the previous tile's products are in it)
+              alive &= warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag);
+              tc_fence_after();
+#pragma unroll
+              for (int r = 0; r < kHalf; ++r) l[r] *= sh.f[row0 + r];
+#pragma unroll 1
+              for (int c = 0; c < kColumns; ++c) {
+                const uint32_t at = tmem + lanes + kOCol + c * N + row0;
+                uint32_t o[kHalf];
+                tmem_ld<kHalf>(at, o);
+                tmem_wait<kHalf>(o);
+#pragma unroll
+                for (int r = 0; r < kHalf; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.f[row0 + r]);
+                tmem_st<kHalf>(at, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          weights();
+          const uint32_t stage = smem + (u % kStages) * kStage;
+          const uint32_t swz = (key >> 1) & 3;
+          auto write = [&](uint32_t at, const uint32_t (&x)[kHalf / 4]) {
+            at += (key & 7) * 64;
+            if constexpr (kHalf == 8) {
+              st_shared8(at + (swz << 4) + half * 8, x[0], x[1]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kHalf / 16; ++i)
+                st_shared16(at + (((half * (kHalf / 16) + i) ^ swz) << 4), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          };
+          write(stage + (key >> 3) * kGroup + kRopeAt, hi);
+          // the previous tile's second terms of these keys have been read: a quarter is a block
+          if (u > 0) alive &= warp_wait(smem_u32(&bars.empty[(u - 1) % kStages][quarter]), ((u - 1) / kStages) & 1, abort_flag);
+          write(smem + off_p<N>() + (key >> 3) * kAtom, lo);
           if (ragged && j >= start) {
-#pragma unroll
-            for (int r = 0; r < kHalf; ++r)
-              if (j >= s.L || !((sh.word[row0 + r] >> (j - start)) & 1)) y[r] = -INFINITY;
-          }
-        };
-        uint32_t hi[kHalf / 4], lo[kHalf / 4];
-        auto weights = [&]() {
-#pragma unroll
-          for (int r = 0; r < kHalf; r += 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[r + i] = exp2_hw(y[r + i]);
-            two_terms<true>(half2_of(y[r], y[r + 1]), half2_of(y[r + 2], y[r + 3]), dither, hi[r / 4], lo[r / 4]);
-          }
-        };
-        logits();
-        // A reference is raised where a logit is too far above it, and at first.
-        const bool forced = t == s.t0 || (ragged && late);
-        bool over = forced;
-        if (!forced) {
-          float a = y[0], b = y[1];
-#pragma unroll
-          for (int r = 2; r < kHalf; r += 2) {
-            a = fmaxf(a, y[r]);
-            b = fmaxf(b, y[r + 1]);
-          }
-          over = fmaxf(a, b) > kShift + kTau;
-        }
-        over = any_of_half(half, over || !alive);
-        if (over) {
-          if (!(alive = !any_of_half(half, !alive || *abort_flag))) break;
-          if (!forced) logits();
-          float tops[kHalf];
-#pragma unroll
-          for (int r = 0; r < kHalf; ++r) tops[r] = y[r];
-          const float mine = row_maxima<kHalf>(tops, lane);
-          if (lane < kHalf) sh.xch[half][quarter][lane] = mine;
-          meet_half(half);
-          if (quarter == 0 && lane < kHalf) {
-            const float (&x)[4][kHalf] = sh.xch[half];
-            const float top = fmaxf(fmaxf(x[0][lane], x[1][lane]), fmaxf(x[2][lane], x[3][lane]));
-            const float old = sh.ref[row0 + lane];   // kNoRef: the row has seen nothing, y is above 0
-            float step = 0.f, f = 1.f;
-            if (top > (old == kNoRef ? -INFINITY : kShift + kTau)) {
-              step = kShift - top - (s.t1 - t > 2 ? kRoom : 0.f);   // (the last tiles will not raise it much)
-              f = old == kNoRef ? 0.f : exp2_hw(step);
-              sh.ref[row0 + lane] = (old == kNoRef ? 0.f : old) - step;
+            // this half's 256 of the key's values: none behind the sequence, no NaN among the new tokens
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {             // (in any order; this one meets all banks)
+              const uint32_t at = stage + (key >> 3) * kGroup + (4 * half + (i >> 2)) * kAtom + (key & 7) * 64 +
+                                  (((i + (key >> 1)) & 3) << 4);
+              uint4 x = make_uint4(0u, 0u, 0u, 0u);
+              if (j < s.L) {
+                x = ld_shared16(at);
+                x.x = without_nan(x.x);
+                x.y = without_nan(x.y);
+                x.z = without_nan(x.z);
+                x.w = without_nan(x.w);
+              }
+              st_shared16(at, x.x, x.y, x.z, x.w);
             }
-            sh.step[row0 + lane] = step;
-            sh.f[row0 + lane] = f;
           }
-          meet_half(half);
-#pragma unroll
-          for (int r = 0; r < kHalf; ++r) {
-            const float step = sh.step[row0 + r];
-            y[r] += step;
-            ref[r] -= step;
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&bars.p_full[quarter]));
+            mbar_arrive(smem_u32(&bars.s_free[u & 1]));
           }
-          if (t > s.t0) {
-            // (O may be touched once the previous tile's products are in it)
-            alive &= warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag);
-            tc_fence_after();
 #pragma unroll
-            for (int r = 0; r < kHalf; ++r) l[r] *= sh.f[row0 + r];
-#pragma unroll 1
-            for (int c = 0; c < kColumns; ++c) {
-              const uint32_t at = tmem + lanes + kOCol + c * N + row0;
-              uint32_t o[kHalf];
-              tmem_ld<kHalf>(at, o);
-              tmem_wait<kHalf>(o);
-#pragma unroll
-              for (int r = 0; r < kHalf; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.f[row0 + r]);
-              tmem_st<kHalf>(at, o);
-            }
-            tmem_st_wait();
+          for (int r = 0; r < kHalf; ++r) l[r] += y[r];
+        }
+        if (!alive) break;
+        // ---- the sums, and the next segment's Q while the last products run
+        const bool bad = *const_cast<volatile int*>(&bars.seg[e % kSegRing].bad);
+        whole = s.t0 == 0 && s.t1 == s.nt;
+        {
+          const float sum = row_sums<kHalf>(l, lane);
+          if (lane < kHalf) sh.xch[half][quarter][lane] = sum;
+        }
+        if (!(alive = meet(lane, abort_flag))) break;
+        if (quarter == 0) {
+          const float (&x)[4][kHalf] = sh.xch[half];
+          const int r = lane % kHalf, rr = s.m * N + row0 + r, tok = rr / p.heads;
+          const float sum = (x[0][r] + x[1][r]) + (x[2][r] + x[3][r]);
+          __syncwarp();
+          if (lane < kHalf) {
+            sh.f[row0 + r] = bad || sum == 0.f ? 0.f : descale / sum;   // (NaN: the row sees one, or holds one)
+            // where the row goes, over the sums
+            reinterpret_cast<int64_t*>(sh.xch[half])[r] = static_cast<int64_t>(s.q0 + tok) * p.out_stride_tok +
+                                                          static_cast<int64_t>(rr - tok * p.heads) * p.out_stride_head;
+            if (!whole)
+              p.sum_part[(2 * static_cast<int64_t>(blockIdx.x) + s.slot) * N + row0 + r] = make_float2(sh.ref[row0 + r], bad ? __uint_as_float(kBadSum) : sum);
           }
         }
-        weights();
-        const uint32_t stage = smem + (u % kStages) * kStage;
-        const uint32_t swz = (key >> 1) & 3;
-        auto write = [&](uint32_t at, const uint32_t (&x)[kHalf / 4]) {
-          at += (key & 7) * 64;
-          if constexpr (kHalf == 8) {
-            st_shared8(at + (swz << 4) + half * 8, x[0], x[1]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kHalf / 16; ++i)
-              st_shared16(at + (((half * (kHalf / 16) + i) ^ swz) << 4), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          }
-        };
-        write(stage + (key >> 3) * kGroup + kRopeAt, hi);
-        // the previous tile's second terms of these keys have been read: a quarter is a block
-        if (u > 0) alive &= warp_wait(smem_u32(&bars.empty[(u - 1) % kStages][quarter]), ((u - 1) / kStages) & 1, abort_flag);
-        write(smem + off_p<N>() + (key >> 3) * kAtom, lo);
-        if (ragged && j >= start) {
-          // this half's 256 of the key's values: none behind the sequence, no NaN among the new tokens
-#pragma unroll 1
-          for (int i = 0; i < 16; ++i) {             // (in any order; this one meets all banks)
-            const uint32_t at = stage + (key >> 3) * kGroup + (4 * half + (i >> 2)) * kAtom + (key & 7) * 64 +
-                                (((i + (key >> 1)) & 3) << 4);
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (j < s.L) {
-              x = ld_shared16(at);
-              x.x = without_nan(x.x);
-              x.y = without_nan(x.y);
-              x.z = without_nan(x.z);
-              x.w = without_nan(x.w);
-            }
-            st_shared16(at, x.x, x.y, x.z, x.w);
-          }
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars.p_full[quarter]));
-          mbar_arrive(smem_u32(&bars.s_free[u & 1]));
-        }
-#pragma unroll
-        for (int r = 0; r < kHalf; ++r) l[r] += y[r];
+        if (!(alive = meet_all(lane, abort_flag))) break;
       }
-      if (!alive) break;
-      // ---- the sums, and the next segment's Q while the last products run
-      const bool bad = *const_cast<volatile int*>(&bars.seg[e % kSegRing].bad);
-      const bool whole = s.t0 == 0 && s.t1 == s.nt;
-      const int64_t slot = 2 * blockIdx.x + s.slot;
-      {
-        const float sum = row_sums<kHalf>(l, lane);
-        if (lane < kHalf) sh.xch[half][quarter][lane] = sum;
-      }
-      if (!(alive = meet(lane, abort_flag))) break;
-      if (quarter == 0) {
-        const float (&x)[4][kHalf] = sh.xch[half];
-        const int r = lane % kHalf, rr = s.m * N + row0 + r, tok = rr / p.heads;
-        const float sum = (x[0][r] + x[1][r]) + (x[2][r] + x[3][r]);
-        __syncwarp();
-        if (lane < kHalf) {
-          sh.f[row0 + r] = bad || sum == 0.f ? 0.f : descale / sum;   // (NaN: the row sees one, or holds one)
-          // where the row goes, over the sums
-          reinterpret_cast<int64_t*>(sh.xch[half])[r] = static_cast<int64_t>(s.q0 + tok) * p.out_stride_tok +
-                                                        static_cast<int64_t>(rr - tok * p.heads) * p.out_stride_head;
-          if (!whole)
-            p.sum_part[slot * N + row0 + r] = make_float2(sh.ref[row0 + r], bad ? __uint_as_float(kBadSum) : sum);
-        }
-      }
-      if (!(alive = meet_all(lane, abort_flag) &&
-                    warp_wait(smem_u32(&bars.seg_full[(e + 1) % kSegRing]), ((e + 1) / kSegRing) & 1, abort_flag)))
-        break;
+      if (!(alive = warp_wait(smem_u32(&bars.seg_full[(e + 1) % kSegRing]), ((e + 1) / kSegRing) & 1, abort_flag))) break;
       const bool last = bars.seg[(e + 1) % kSegRing].end;
       if (!last) prepare(bars.seg[(e + 1) % kSegRing]);
-      // ---- the output
-      if (!(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
-      tc_fence_after();
-      const int valid = min(kHalf, rows - row0);     // of this half's
-      // A lane has one dim of all rows; exchanged between lanes (a butterfly on their lower bits), it stores 16
-      // bytes of a row at a time, 4 dims of partial outputs or 8 of the output.  (4 or 2 bytes at a time took
-      // 4100 clocks.)
+      if (e >= 0) {
+        // ---- the output
+        if (!(alive = warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag))) break;
+        tc_fence_after();
+        const int valid = min(kHalf, rows - row0);     // of this half's
+        // A lane has one dim of all rows; exchanged between lanes (a butterfly on their lower bits), it stores 16
+        // bytes of a row at a time, 4 dims of partial outputs or 8 of the output.  (4 or 2 bytes at a time took
+        // 4100 clocks.)
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + s.slot;
 #pragma unroll 1
-      for (int c = 0; c < kColumns; ++c) {
-        uint32_t o[kHalf];
-        tmem_ld<kHalf>(tmem + lanes + kOCol + c * N + row0, o);
-        tmem_wait<kHalf>(o);
-        const int d0 = c * 128 + quarter * 32;       // (a TMEM lane is a dim here)
-        if (whole) {
-          uint32_t x[kHalf / 2];
+        for (int at = 0; at < kColumns * kHalf / 8; ++at) {   // 8 rows of 128 dims
+          const int c = at / (kHalf / 8), r0 = at % (kHalf / 8) * 8;
+          uint32_t o[8];
+          tmem_ld<8>(tmem + lanes + kOCol + c * N + row0 + r0, o);
+          tmem_wait<8>(o);
+          const int d0 = c * 128 + quarter * 32;       // (a TMEM lane is a dim here)
+          if (whole) {
+            uint32_t x[4];
 #pragma unroll
-          for (int i = 0; i < kHalf / 2; ++i) {      // rows 2i + bit 0, dims of the pair of lanes
-            const float f0 = sh.f[row0 + 2 * i], f1 = sh.f[row0 + 2 * i + 1];
-            const float v0 = f0 == 0.f ? 0.f : __uint_as_float(o[2 * i]) * f0;
-            const float v1 = f1 == 0.f ? 0.f : __uint_as_float(o[2 * i + 1]) * f1;
-            const float keep = lane & 1 ? v1 : v0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-            const __nv_bfloat162 pair = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
-            x[i] = *reinterpret_cast<const uint32_t*>(&pair);
-          }
-          uint32_t z[kHalf / 8][4];
-#pragma unroll
-          for (int i = 0; i < kHalf / 8; ++i) {      // rows 8i + bits 0 .. 2, dims of 8 lanes
-            uint32_t k2[2], g2[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w0 = x[4 * i + 2 * h], w1 = x[4 * i + 2 * h + 1];
-              k2[h] = lane & 2 ? w1 : w0;
-              g2[h] = __shfl_xor_sync(0xffffffffu, lane & 2 ? w0 : w1, 2);
+            for (int i = 0; i < 4; ++i) {              // rows 2i + bit 0, dims of the pair of lanes
+              const float f0 = sh.f[row0 + r0 + 2 * i], f1 = sh.f[row0 + r0 + 2 * i + 1];
+              const float v0 = f0 == 0.f ? 0.f : __uint_as_float(o[2 * i]) * f0;
+              const float v1 = f1 == 0.f ? 0.f : __uint_as_float(o[2 * i + 1]) * f1;
+              const float keep = lane & 1 ? v1 : v0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+              const __nv_bfloat162 pair = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
+              x[i] = *reinterpret_cast<const uint32_t*>(&pair);
             }
-            const uint32_t a0[2] = {lane & 2 ? g2[0] : k2[0], lane & 2 ? k2[0] : g2[0]};
-            const uint32_t a1[2] = {lane & 2 ? g2[1] : k2[1], lane & 2 ? k2[1] : g2[1]};
+            uint32_t y[2][2], z[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t keep = lane & 4 ? a1[h] : a0[h], got = __shfl_xor_sync(0xffffffffu, lane & 4 ? a0[h] : a1[h], 4);
-              z[i][h] = lane & 4 ? got : keep;
-              z[i][2 + h] = lane & 4 ? keep : got;
+            for (int h = 0; h < 2; ++h) {              // rows 4h + bits 0 and 1, dims of 4 lanes
+              const uint32_t keep = lane & 2 ? x[2 * h + 1] : x[2 * h];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[2 * h] : x[2 * h + 1], 2);
+              y[h][0] = lane & 2 ? got : keep;
+              y[h][1] = lane & 2 ? keep : got;
             }
-          }
 #pragma unroll
-          for (int i = 0; i < kHalf / 8; ++i) {
-            const int r = 8 * i + (lane & 7);
+            for (int h = 0; h < 2; ++h) {              // rows bits 0 .. 2, dims of 8 lanes
+              const uint32_t keep = lane & 4 ? y[1][h] : y[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 4 ? y[0][h] : y[1][h], 4);
+              z[h] = lane & 4 ? got : keep;
+              z[2 + h] = lane & 4 ? keep : got;
+            }
+            const int r = r0 + (lane & 7);
             if (r < valid)
               *reinterpret_cast<uint4*>(p.out + reinterpret_cast<const int64_t*>(sh.xch[half])[r] + d0 + (lane & 24)) =
-                  make_uint4(z[i][0], z[i][1], z[i][2], z[i][3]);
-          }
-        } else {
+                  make_uint4(z[0], z[1], z[2], z[3]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < kHalf / 4; ++i) {      // rows 4i + bits 0 and 1, dims of 4 lanes
-            uint32_t x[2][2];
+            for (int i = 0; i < 2; ++i) {              // rows 4i + bits 0 and 1, dims of 4 lanes
+              uint32_t x[2][2], z[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w0 = o[4 * i + 2 * h], w1 = o[4 * i + 2 * h + 1];
-              const uint32_t keep = lane & 1 ? w1 : w0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? w0 : w1, 1);
-              x[h][0] = lane & 1 ? got : keep;
-              x[h][1] = lane & 1 ? keep : got;
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w0 = o[4 * i + 2 * h], w1 = o[4 * i + 2 * h + 1];
+                const uint32_t keep = lane & 1 ? w1 : w0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? w0 : w1, 1);
+                x[h][0] = lane & 1 ? got : keep;
+                x[h][1] = lane & 1 ? keep : got;
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t keep = lane & 2 ? x[1][h] : x[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[0][h] : x[1][h], 2);
+                z[h] = lane & 2 ? got : keep;
+                z[2 + h] = lane & 2 ? keep : got;
+              }
+              const int r = r0 + 4 * i + (lane & 3);
+              if (r < valid)
+                *reinterpret_cast<uint4*>(p.o_part + (slot * N + row0 + r) * kDim + d0 + (lane & 28)) = make_uint4(z[0], z[1], z[2], z[3]);
             }
-            uint32_t z[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t keep = lane & 2 ? x[1][h] : x[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[0][h] : x[1][h], 2);
-              z[h] = lane & 2 ? got : keep;
-              z[2 + h] = lane & 2 ? keep : got;
-            }
-            const int r = 4 * i + (lane & 3);
-            if (r < valid)
-              *reinterpret_cast<uint4*>(p.o_part + (slot * N + row0 + r) * kDim + d0 + (lane & 28)) = make_uint4(z[0], z[1], z[2], z[3]);
           }
         }
+        tc_fence_before();
       }
-      tc_fence_before();
       if (last) break;
       // every softmax warp is done with this segment's data, and has written its part of the next one's
       if (!(alive = meet_all(lane, abort_flag))) break;
-      if (lane == 0) mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
+      if (e >= 0 && lane == 0) mbar_arrive(smem_u32(&bars.seg_free[e % kSegRing]));
     }
   }
 

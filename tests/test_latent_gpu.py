@@ -7,7 +7,10 @@ bf16's eps):
   2^-17 of it, and float32 sums of 576 products add 2^-18 of the same: 2^-16.4 `reach` on a logit, twice
   that on a weight relative to the others;
 * a weight in two e4m3 terms: 2^-8 of it (4 significant bits, then 4 of the rest), 2^-11 for float16 on the
-  way, and an absolute part of 2^-9 against a largest weight of at least 2^7: 2^-16 of the largest.
+  way, and an absolute part of 2^-9 against a largest weight of at least 2^7: 2^-16 of the largest.  (Where a
+  reference has been raised in the middle of a long row, with room, the largest weight may be 2^3, and one key's
+  absolute part 2^-12 of it.  The dither spreads such parts evenly about zero over a tile's keys, so that sums of
+  many keep to 2^-16 all the same; rows of up to two tiles have no room.)
 """
 from __future__ import annotations
 
@@ -407,6 +410,63 @@ def test_no_wait_runs_out(heads, nodes):
         for _ in range(4):
             api.mtp_latent_attn_fwd(b.q, b.cache, b.bt, b.sl, b.cu, d, b.scale, out=out, workspace=ws, status=b.status)
     torch.cuda.synchronize()
+    assert b.status.item() == 0
+
+
+def test_two_streams():
+    """Two calls at once, each with its own workspace, in turn many times."""
+    a, b = Batch([9000, 300], [4, 1], 16, seed=20), Batch([2000, 5000, 70], [1, 1, 1], 128, seed=21)
+    refs = [a.run(), b.run()]
+    d = torch.full((1,), 0.75, device="cuda")
+    sets = []
+    for x in (a, b):
+        need = api.mtp_latent_attn_workspace_size(len(x.lens), x.total, x.heads, x.bt.shape[1])
+        sets.append((x, torch.zeros(need, dtype=torch.uint8, device="cuda"), torch.cuda.Stream(),
+                     [torch.zeros(x.total, x.heads, 512, dtype=torch.bfloat16, device="cuda") for _ in range(10)]))
+    torch.cuda.synchronize()
+    for i in range(10):
+        for x, ws, stream, outs in sets:
+            api.mtp_latent_attn_fwd(x.q, x.cache, x.bt, x.sl, x.cu, d, x.scale, out=outs[i], workspace=ws, status=x.status, stream=stream)
+    torch.cuda.synchronize()
+    for (x, _, _, outs), ref in zip(sets, refs):
+        assert x.status.item() == 0 and all(torch.equal(o, ref) for o in outs)
+
+
+@pytest.mark.parametrize("lens,nodes,heads", [([9000, 300], [4, 1], 16), ([700] * 5, [3] * 5, 100), ([40] * 300, [1] * 300, 5),
+                                              ([20000, 20000], [1, 1], 128), ([1], [1], 1)])
+def test_nothing_else_is_written(lens, nodes, heads):
+    """The bytes around a workspace of exactly the size that is asked for, and around the output."""
+    b = Batch(lens, nodes, heads, seed=30)
+    need = api.mtp_latent_attn_workspace_size(len(lens), b.total, heads, b.bt.shape[1])
+    room = torch.full((need + 2048,), 0xAB, dtype=torch.uint8, device="cuda")
+    store = torch.full((b.total + 2, heads, 512), 9.0, dtype=torch.bfloat16, device="cuda")
+    b.run(out=store[1:-1], workspace=room[1024:1024 + need])
+    assert b.status.item() == 0 and torch.equal(store[1:-1], b.run())
+    assert (room[:1024] == 0xAB).all() and (room[1024 + need:] == 0xAB).all()
+    assert (store[0] == 9.0).all() and (store[-1] == 9.0).all()
+
+
+def test_trees_in_a_graph():
+    """A captured call with a tree mask follows the mask's, the lengths' and the tables' buffers."""
+    masks = tree(20, 1) + tree(7, 2)
+    b = Batch([700, 300], [20, 7], 16, seed=31, masks=masks)
+    d = torch.full((1,), 0.75, device="cuda")
+    ws = torch.zeros(api.mtp_latent_attn_workspace_size(2, b.total, 16, b.bt.shape[1]), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(b.total, 16, 512, dtype=torch.bfloat16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.mtp_latent_attn_fwd(b.q, b.cache, b.bt, b.sl, b.cu, d, b.scale, tree_mask=b.mask, out=out, workspace=ws, status=b.status)
+    g.replay()
+    torch.cuda.synchronize()
+    b.check(out)
+    b.masks = tree(20, 3) + chain(7)
+    b.mask.copy_(torch.tensor(b.masks, dtype=torch.int64))
+    b.bt[:, :18] = b.bt[:, :18].flip(1)
+    b.sl.copy_(torch.tensor([290, 288], dtype=torch.int32))
+    b.lens = [290, 288]
+    g.replay()
+    torch.cuda.synchronize()
+    b.check(out)
     assert b.status.item() == 0
 
 
