@@ -84,6 +84,7 @@ constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at 
 constexpr float kRoom = 4.f;                         // a raised reference is so far above the row's maximum
 constexpr float kNoRef = -1e30f;                     // no key seen yet
 constexpr int kUnitTiles = 7, kCutTiles = 4, kCutPieces = 40;
+constexpr int kFewTiles = 8;
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kBadSum = 0x7fd0bad1u;            // a sum of a sequence with a bad page (a NaN that no
                                                      // arithmetic makes)
@@ -1211,13 +1212,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
 // threads take four dims each of kRows rows, kGroups such groups of threads either a part of the pieces
 // (kSplit: few units in many pieces) or more rows.  Reads what the main kernel has just written, out of L2;
 // bound by its chain of notes, sums and partial outputs.
-template <int N, int kRows, int kGroups, bool kSplit>
-__global__ void __launch_bounds__(128 * kGroups) latent_join_kernel(const __grid_constant__ LatentParams p) {
-  constexpr int kThreads = 128 * kGroups, kCtaRows = kSplit ? kRows : kRows * kGroups;
-  constexpr int kAhead = 8 / kRows;                    // pieces in flight
+template <int N, int kRows, int kDims, int kGroups, bool kSplit, int kAhead>
+__global__ void __launch_bounds__(kDims / 4 * kGroups) latent_join_kernel(const __grid_constant__ LatentParams p) {
+  constexpr int kSide = kDims / 4, kThreads = kSide * kGroups, kCtaRows = kSplit ? kRows : kRows * kGroups;
   __shared__ float s_w[kCtaRows][kMaxCtas];
   __shared__ float s_inv[kCtaRows];
-  __shared__ float4 s_acc[kSplit ? kGroups - 1 : 1][kRows][128];
+  __shared__ float4 s_acc[kSplit ? kGroups - 1 : 1][kRows][kSide];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // every partial is written and visible
@@ -1235,7 +1235,8 @@ __global__ void __launch_bounds__(128 * kGroups) latent_join_kernel(const __grid
     return;
   if (rows <= 0) return;
   auto slot_of = [&](int i) -> int64_t { return 2 * (first + i * stride) + (i == 0 ? a.z : 0); };
-  const int d4 = tid & 127, g = tid >> 7, mine = kSplit ? 0 : g * kRows;   // first row of this thread's
+  const int in = tid % kSide, d4 = blockIdx.z * kSide + in, g = tid / kSide;
+  const int mine = kSplit ? 0 : g * kRows;             // first row of this thread's
   const float4* src = reinterpret_cast<const float4*>(p.o_part) + (r0 + mine) * (kDim / 4) + d4;
   const int step = kSplit ? kGroups : 1;
   float4 x[kAhead][kRows];
@@ -1302,14 +1303,14 @@ __global__ void __launch_bounds__(128 * kGroups) latent_join_kernel(const __grid
   if constexpr (kSplit) {
     if (g > 0)
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) s_acc[g - 1][r][d4] = acc[r];
+      for (int r = 0; r < kRows; ++r) s_acc[g - 1][r][in] = acc[r];
     __syncthreads();
     if (g > 0) return;
 #pragma unroll
     for (int o = 0; o < kGroups - 1; ++o)
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        const float4 y = s_acc[o][r][d4];
+        const float4 y = s_acc[o][r][in];
         acc[r].x += y.x;
         acc[r].y += y.y;
         acc[r].z += y.z;
@@ -1332,16 +1333,20 @@ __global__ void __launch_bounds__(128 * kGroups) latent_join_kernel(const __grid
 
 // ---- host side -----------------------------------------------------------------------------------
 
-// Rows of a unit: as many columns of the products as an average sequence fills.
-int unit_rows(int32_t num_seqs, int32_t total_q, int32_t heads) {
-  const int64_t rows = (static_cast<int64_t>(total_q) * heads + num_seqs - 1) / std::max(num_seqs, 1);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
 int64_t units_bound(int32_t num_seqs, int32_t total_q, int32_t heads, int rows) {
   return static_cast<int64_t>(total_q) * heads / rows + num_seqs;
 }
 int64_t line_bound(int64_t units, int32_t max_pages) {
   return units * ((max_pages + kTilePages - 1) / kTilePages + kUnitTiles);
+}
+// Rows of a unit: as many columns of the products as an average sequence fills.  But 16, whose Q, sums and output
+// take 6 us less than those of 64, while then no CTA has more than kFewTiles tiles of a table's length (4 tokens of
+// 16 heads over 300 keys 16.4 -> 10.7 us, over 20000 21.8 -> 19.4; over 50000, which is above it, 24.1 against 28.8).
+int unit_rows(int32_t num_seqs, int32_t total_q, int32_t heads, int32_t max_pages, int64_t ctas) {
+  const int64_t rows = (static_cast<int64_t>(total_q) * heads + num_seqs - 1) / std::max(num_seqs, 1);
+  const int64_t tiles = (max_pages + kTilePages - 1) / kTilePages;
+  if (rows <= 16 || units_bound(num_seqs, total_q, heads, 16) * tiles <= kFewTiles * ctas) return 16;
+  return rows <= 32 ? 32 : 64;
 }
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -1352,7 +1357,7 @@ struct Parts {
   size_t o, sums, notes, total;        // bytes of partial outputs, sums, notes; of all and the units' number
 };
 bool parts_of(int32_t num_seqs, int32_t total_q, int32_t heads, int32_t max_pages, int sms, Parts* w) {
-  w->rows = unit_rows(num_seqs, total_q, heads);
+  w->rows = unit_rows(num_seqs, total_q, heads, max_pages, std::min(sms, kMaxCtas));
   w->units = units_bound(num_seqs, total_q, heads, w->rows);
   const int64_t line = line_bound(w->units, max_pages);
   if (line > INT32_MAX) return false;
@@ -1426,11 +1431,15 @@ int launch_latent(LatentParams& p, int device, cudaStream_t stream) {
   }
   if (launch_pdl(kernel, dim3(p.ctas), kLatentThreads, smem_bytes<N>(), stream, p) != cudaSuccess) return MTPATTN_E_LAUNCH;
   if (p.max_pages <= kTilePages) return MTPATTN_OK;  // units of one tile are never cut
-  const bool few = p.unit_bound <= 32;
-  const void* join = few ? reinterpret_cast<const void*>(latent_join_kernel<N, 2, 2, true>)
-                         : reinterpret_cast<const void*>(latent_join_kernel<N, 4, 2, false>);
-  return launch_pdl(join, dim3(p.unit_bound, N / (few ? 2 : 8)), 256, 0, stream, p) == cudaSuccess ? MTPATTN_OK
-                                                                                                  : MTPATTN_E_LAUNCH;
+  // Few rows in many pieces (one row of 105000 keys in 152: 47 -> 31 us a call) are joined by 4 CTAs for each 2 rows,
+  // where at most 16 pieces cost 0.7 us more so.
+  const bool one = p.unit_bound * N <= 320 && p.max_pages > 16 * kTilePages, few = p.unit_bound <= 32;
+  const void* join = one   ? reinterpret_cast<const void*>(latent_join_kernel<N, 2, 128, 8, true, 8>)
+                     : few ? reinterpret_cast<const void*>(latent_join_kernel<N, 2, 512, 2, true, 4>)
+                           : reinterpret_cast<const void*>(latent_join_kernel<N, 4, 512, 2, false, 2>);
+  return launch_pdl(join, dim3(p.unit_bound, N / (few ? 2 : 8), one ? 4 : 1), 256, 0, stream, p) == cudaSuccess
+             ? MTPATTN_OK
+             : MTPATTN_E_LAUNCH;
 }
 
 }  // namespace
