@@ -114,6 +114,81 @@ def test_trees(heads, nodes):
     b.check(b.run())
 
 
+WIDE = 20000                                             # pages a table: too many tiles for units of 16 rows
+
+
+@pytest.mark.parametrize("heads", [5, 17, 32, 64, 100, 128])
+@pytest.mark.parametrize("nodes", [1, 2, 4])
+def test_wide_tables(heads, nodes):
+    """Tables far longer than the sequences, so that a unit takes as many rows as there are, up to 64."""
+    b = Batch([300, 129, 128, nodes], [nodes] * 4, heads, seed=heads + nodes, behind=1, base=1, width=WIDE)
+    out = b.run()
+    assert b.status.item() == 0
+    b.check(out)
+
+
+@pytest.mark.parametrize("length", [3, 15, 16, 17, 31, 33, 63, 64, 65, 112, 113, 127, 128, 129, 143, 144, 145, 255, 256, 257, 385])
+@pytest.mark.parametrize("heads", [10, 20])
+def test_lengths_of_wide_tables(length, heads):
+    b = Batch([length, 3, length], [2, 3, 3], heads, seed=length, width=WIDE)
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("heads", [1, 4, 16, 128])
+@pytest.mark.parametrize("nodes", [[64], [5, 64, 1], [33, 17]])
+def test_trees_of_wide_tables(heads, nodes):
+    lens = [n + 50 * i for i, n in enumerate(nodes)]
+    b = Batch(lens, nodes, heads, seed=heads, masks=sum((tree(n, i) for i, n in enumerate(nodes)), []), width=WIDE)
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("length", [3, 200])
+@pytest.mark.parametrize("heads", [10, 20])
+def test_rows_of_wide_tables_that_see_little(length, heads):
+    b = Batch([length, length], [3, 3], heads, masks=[0, 4, 1, 2, 0, 7], width=WIDE)
+    out = b.run()
+    b.check(out)
+    if length == 3:
+        assert not out[0].any() and not out[4].any()
+
+
+@pytest.mark.parametrize("heads", [10, 20])
+def test_codes_of_wide_tables_that_do_not_matter(heads):
+    """NaN codes behind the sequences, and in a token that only itself sees; a row of q that is not finite."""
+    b = Batch([70, 200], [3, 3], heads, masks=[1, 3, 5, 1, 3, 5], width=WIDE)
+    clean = b.run()
+    b.check(clean)
+    used = torch.zeros(b.pages, 16, dtype=torch.bool)
+    for s, n in enumerate(b.lens):
+        at = torch.arange(n)
+        used[b.bt[s].cpu().long()[at // 16], at % 16] = True
+    b.cache[~used.cuda()] = 0x7f
+    assert torch.equal(b.run(), clean)
+    for s, n in enumerate(b.lens):
+        b.cache[b.bt[s, (n - 1) // 16].long(), (n - 1) % 16] = 0xff
+    b.q[1, 3, 570] = float("inf")
+    out = b.run()
+    assert torch.isnan(out[2]).all() and torch.isnan(out[5]).all() and torch.isnan(out[1, 3]).all()
+    out[1, 3] = clean[1, 3]
+    assert torch.equal(out[[0, 1, 3, 4]], clean[[0, 1, 3, 4]])
+
+
+def test_errors_of_wide_tables():
+    b = Batch([300, 300, 2000, 70], [4, 4, 4, 4], 16, width=WIDE)
+    good = b.run()
+    b.check(good)
+    for change, bit in ((lambda: b.bt.__setitem__((1, 3), b.pages), api.ERR_PAGE), (lambda: b.sl.__setitem__(1, 3), api.ERR_QLEN_GT_SEQ),
+                        (lambda: b.sl.__setitem__(1, WIDE * 16 + 1), api.ERR_SEQ_TOO_LONG)):
+        bt, sl = b.bt.clone(), b.sl.clone()
+        b.status.zero_()
+        change()
+        out = b.run()
+        assert b.status.item() == bit and not out[4:8].any()
+        out[4:8] = good[4:8]
+        assert torch.equal(out, good)
+        b.bt, b.sl = bt, sl
+
+
 def test_chain_is_a_mask():
     """The same bits with the chain's words as without."""
     a, b = Batch([300, 70], [7, 20], 16), Batch([300, 70], [7, 20], 16, masks=chain(7) + chain(20))
