@@ -15,17 +15,21 @@
 // is cut into equal pieces, one per CTA (worked out from seq_lens and cu_seqlens_q on the device, so a
 // captured call follows its buffers).  A unit that lies in one piece is written out at once; one that is cut
 // leaves its sums, references and outputs in the workspace (two slots a CTA: its first and its last unit),
-// and latent_join_kernel joins them, going by the notes that the CTAs with first tiles leave.
+// and latent_join_kernel joins them, going by the notes that the CTAs with first tiles leave.  Units stay whole
+// where cutting them would cost more, and CTAs go over a sequence's keys together where they have its row tiles
+// (Walker::start).
 //
-// Roles (384 threads): warp 0 walks over the CTA's piece and fetches tiles by TMA, a lane a page, in four
-// 128-byte columns and one of 64; warp 1 issues the products; warps 4-11 do the softmax: a warp has 32
-// keys (TMEM lanes) of half of the rows, makes Q's operand, and writes the output.
+// Roles (384 threads, one CTA an SM): warp 0 walks over the CTA's piece and issues S's products, warp 1 O's;
+// warps 2 and 3 fetch tiles, each two blocks of 32 keys, by TMA: half a page a lane, a box of 9 slices of 64
+// bytes of 8 keys, so that one instruction brings 4608 bytes.  Warps 4-11 do the softmax: a warp has 32 keys
+// (TMEM lanes) of half of the rows, makes Q's operand, and writes the output.  They get 200 registers a thread,
+// the others 104.
 //
 // Precision.  Codes enter as they are, Q as two e4m3 terms of x = q 2^a (a per row, max |x| in [128,
 // 256)): hi = e4m3(x), lo = e4m3(x - hi), as 2 N columns of one product, added in float32.  A bf16 value
 // has 8 significant bits and each term keeps 4, so x = hi + lo within 2^-9 of the row's largest, and
 // to 2^-17 of it below.  The weights p = 2^(s - ref), at most 2^8.75, are two e4m3 terms as well, of which
-// the smallest step is 2^-9: 2^-16 of the row's largest weight.  Plain rounding would drop all weights
+// the smallest step is 2^-9.  Plain rounding would drop all weights
 // below half of that, which many keys behind one large weight can be (30000 at 2^-19 are 5% of the sum);
 // so the second term is rounded with a dither, a number in (-1/2, 1/2) steps that goes through 128
 // evenly spread values over a tile's keys (their bits reversed): sums of small weights keep their size to
@@ -33,15 +37,27 @@
 //
 // Online softmax in the log2 domain with a lazy reference: raised, and O rescaled in TMEM, only when a
 // logit exceeds it by more than kTau.  So a tile's maxima over keys (across lanes and warps, which this
-// orientation makes dear) are only needed where that happens.
+// orientation makes dear) are only needed where that happens.  A reference that is raised with tiles to come
+// goes kRoom above what it has to, so that it is raised less often; the largest weight is then 2^3.5 or more
+// instead of 2^7, and the step 2^-12.5 of it.  kRoom's sides, measured (error of the output against 64 bits, of which its
+// rounding is 0.00166, over 8191 keys of 64-node trees, the worst of 9 shapes; time of those trees, and of 16 x 35000
+// keys with 128 heads): 0: 0.00170, 154 and 156 us; 2.5: 0.00187, 145 and 145; 3.5: 0.00214, 138 and 136; 4: 0.00232,
+// 135 and 134.
 //
 // Masks.  A tile that reaches into the new tokens takes each row's word.  Places that no row sees in full
 // are kept out of the second product by value too, since 0 * NaN is NaN: rows behind the sequence are
 // stored as zeros, NaN codes of new tokens too (a row that sees one has a NaN logit, and its sum tells).
 //
 // Shared memory (N = 64): two stages of a tile (147456), Q's terms (73728), the second terms of P (8192;
-// the first ones take the place of the tile's 64-byte column, which only the first product reads).
+// the first ones take the place of the tile's 64-byte slice of rotated dims, which only the first product reads).
 // TMEM: S double buffer at columns 0 and 128, O at 256, N columns for each 128 dims.
+//
+// What bounds it.  The products of a tile of 64 rows take 2430 clocks of the tensor cores (S 64 an instruction, 18
+// of them; O's two terms 78 a pair, 16), and two stages of tiles are all that fits, so that a tile's chain S, softmax, P, O
+// overlaps with one other tile's only: 3400 to 3900 clocks a tile.  Measured, in graphs: 16 x 35000 keys with
+// 4 tokens of 16 heads 84 us (memory's floor 48.5, the products' 41.6 at the bf16 rate), with one token 62; 128 heads
+// 136 (83 at the bf16 rate); 64-node trees over 8191 keys 138 (78).  A call begins with 9 to 10 us (launch, lengths, Q's terms, first
+// tiles of all CTAs at once) and ends with 2.5 of output and 4 to 7 of the join.
 #include "common.cuh"
 #include "host_checks.cuh"
 #include "sm100.cuh"
@@ -81,7 +97,7 @@ constexpr int kSegRing = 4;
 constexpr int kPrefetch = 1;                         // tiles ahead, into L2
 constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at the reference, and at most
                                                      // 2^(kShift + kTau) = 430 < 448
-constexpr float kRoom = 4.f;                         // a raised reference is so far above the row's maximum
+constexpr float kRoom = 3.5f;                        // a raised reference is so far above the row's maximum
 constexpr float kNoRef = -1e30f;                     // no key seen yet
 constexpr int kUnitTiles = 7, kCutTiles = 4, kCutPieces = 40;
 constexpr int kFewTiles = 8;

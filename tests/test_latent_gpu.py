@@ -8,8 +8,8 @@ bf16's eps):
   that on a weight relative to the others;
 * a weight in two e4m3 terms: 2^-8 of it (4 significant bits, then 4 of the rest), 2^-11 for float16 on the
   way, and an absolute part of 2^-9 against a largest weight of at least 2^7: 2^-16 of the largest.  (Where a
-  reference has been raised in the middle of a long row, with room, the largest weight may be 2^3, and one key's
-  absolute part 2^-12 of it.  The dither spreads such parts evenly about zero over a tile's keys, so that sums of
+  reference has been raised in the middle of a long row, with room, the largest weight may be 2^3.5, and one key's
+  absolute part 2^-12.5 of it.  The dither spreads such parts evenly about zero over a tile's keys, so that sums of
   many keep to 2^-16 all the same; rows of up to two tiles have no room.)
 """
 from __future__ import annotations
