@@ -231,18 +231,19 @@ def hbm_peak() -> tuple[float, str]:
 
 # The prefill kernel's translation unit; the verify kernels (main, reduce) build from the rest.
 PREFILL_SOURCES = ("fmha_prefill.cu",)
-TREE_SOURCES = ("tree_attn.cu", "tree_verify.cu", "cache_pages.cu", "host_checks.cuh", "binding.cpp")
+OTHER_SOURCES = ("tree_attn.cu", "tree_verify.cu", "cache_pages.cu", "host_checks.cuh", "binding.cpp", "rope_write.cu",
+                 "latent_attn.cu")
 
 
 def source_digest(kernel: str = "verify") -> str:
     """Digest of a kernel's sources with comments and blank space removed, so that a profile
     summary stays attached to the code it measured when only comments change.  "verify" covers
-    every csrc file but the prefill kernel's own and those of the draft trees and the cache's
-    upkeep; "prefill" covers that one and the headers it includes."""
+    every csrc file but the prefill kernel's own and those of the draft trees, the cache's upkeep,
+    the rotary writes and the latent attention; "prefill" covers that one and the headers it includes."""
     h = hashlib.sha256()
     for path in sorted(glob.glob(os.path.join(ROOT, "paged_fp8_speculative_gb300", "csrc", "*"))):
         name = os.path.basename(path)
-        if kernel == "verify" and name in PREFILL_SOURCES + TREE_SOURCES:
+        if kernel == "verify" and name in PREFILL_SOURCES + OTHER_SOURCES:
             continue
         if kernel == "prefill" and name not in PREFILL_SOURCES + ("common.cuh", "sm100.cuh"):
             continue

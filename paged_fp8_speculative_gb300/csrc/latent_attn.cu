@@ -35,14 +35,14 @@
 // evenly spread values over a tile's keys (their bits reversed): sums of small weights keep their size to
 // 2^-23, and the same bits come every time.  The sums of weights are of the unrounded ones, in float32.
 //
-// Online softmax in the log2 domain with a lazy reference: raised, and O rescaled in TMEM, only when a
-// logit exceeds it by more than kTau.  So a tile's maxima over keys (across lanes and warps, which this
-// orientation makes dear) are only needed where that happens.  A reference that is raised with tiles to come
-// goes kRoom above what it has to, so that it is raised less often; the largest weight is then 2^3.5 or more
-// instead of 2^7, and the step 2^-12.5 of it.  kRoom's sides, measured (error of the output against 64 bits, of which its
-// rounding is 0.00166, over 8191 keys of 64-node trees, the worst of 9 shapes; time of those trees, and of 16 x 35000
-// keys with 128 heads): 0: 0.00170, 154 and 156 us; 2.5: 0.00187, 145 and 145; 3.5: 0.00214, 138 and 136; 4: 0.00232,
-// 135 and 134.
+// Online softmax in the log2 domain with a lazy reference: raised, and O rescaled in TMEM, only when a logit
+// exceeds it by more than kTau.  So a tile's maxima over keys (across lanes and warps, which this orientation
+// makes dear) are only needed where that happens.  A reference that is raised with tiles to come goes kRoom
+// above what it has to, so that it is raised less often; the largest weight is then 2^3.5 or more instead of
+// 2^7, and the step 2^-12.5 of it.  kRoom's sides, measured (error of the output against 64 bits, of which its
+// rounding is 0.00166, over 8191 keys of 64-node trees, the worst of 9 shapes; time of those trees, and of 16 x
+// 35000 keys with 128 heads): 0: 0.00170, 154 and 156 us; 2.5: 0.00187, 145 and 145; 3.5: 0.00214, 138 and 136;
+// 4: 0.00232, 135 and 134.
 //
 // Masks.  A tile that reaches into the new tokens takes each row's word.  Places that no row sees in full
 // are kept out of the second product by value too, since 0 * NaN is NaN: rows behind the sequence are
@@ -52,12 +52,13 @@
 // the first ones take the place of the tile's 64-byte slice of rotated dims, which only the first product reads).
 // TMEM: S double buffer at columns 0 and 128, O at 256, N columns for each 128 dims.
 //
-// What bounds it.  The products of a tile of 64 rows take 2430 clocks of the tensor cores (S 64 an instruction, 18
-// of them; O's two terms 78 a pair, 16), and two stages of tiles are all that fits, so that a tile's chain S, softmax, P, O
-// overlaps with one other tile's only: 3400 to 3900 clocks a tile.  Measured, in graphs: 16 x 35000 keys with
-// 4 tokens of 16 heads 84 us (memory's floor 48.5, the products' 41.6 at the bf16 rate), with one token 62; 128 heads
-// 136 (83 at the bf16 rate); 64-node trees over 8191 keys 138 (78).  A call begins with 9 to 10 us (launch, lengths, Q's terms, first
-// tiles of all CTAs at once) and ends with 2.5 of output and 4 to 7 of the join.
+// What bounds it.  The products of a tile of 64 rows take 2430 clocks of the tensor cores (S 64 an instruction,
+// 18 of them; O's two terms 78 a pair, 16), and two stages of tiles are all that fits, so that a tile's chain
+// S, softmax, P, O overlaps with one other tile's only: 3400 to 3900 clocks a tile.  Measured, in graphs: 16 x
+// 35000 keys with 4 tokens of 16 heads 84 us (memory's floor 48.8, the products' 41.4 at the bf16 rate), with
+// one token 62; 128 heads 136 (82.8 at the bf16 rate); 64-node trees over 8191 keys 138 (77.0).  A call begins
+// with 7 to 9 us (launch, lengths, Q's terms, first tiles of all CTAs at once) and ends with 2.5 of output and
+// 4 to 7 of the join.
 #include "common.cuh"
 #include "host_checks.cuh"
 #include "sm100.cuh"
