@@ -188,14 +188,19 @@ static_assert(smem_bytes<64>() <= 232448, "more than a block may have");
 struct Seq {
   int q0, n, L, T, nt, w, err;
 };
+struct RawSeq {
+  int q0, q1, L;
+};
+__device__ __forceinline__ RawSeq raw_at(const LatentParams& p, int b) {
+  if (b >= p.num_seqs) return RawSeq{0, 0, 0};       // (no rows)
+  return RawSeq{p.cu_q[b], p.cu_q[b + 1], p.seq_lens[b]};
+}
 template <int N>
-__device__ __forceinline__ Seq seq_at(const LatentParams& p, int b) {
+__device__ __forceinline__ Seq seq_of(const LatentParams& p, const RawSeq& raw) {
   Seq s;
-  s.q0 = s.n = s.L = s.T = s.nt = s.w = s.err = 0;
-  if (b >= p.num_seqs) return s;
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-  s.q0 = q0;
-  s.L = p.seq_lens[b];
+  s.n = s.T = s.nt = s.w = s.err = 0;
+  const int q0 = s.q0 = raw.q0, q1 = raw.q1;
+  s.L = raw.L;
   if (q0 < 0 || q1 <= q0 || q1 > p.total_q) {
     s.err = MTPATTN_ERR_QLEN;
     return s;
@@ -239,18 +244,37 @@ struct Walker {
 
   __device__ __forceinline__ void start(const LatentParams& p, int lane) {
     b0 = before = units_before = unit = unit0 = unit_places = 0;
-    mine = seq_at<N>(p, lane);
+    mine = seq_of<N>(p, raw_at(p, lane));
     int w = mine.w, n = mine.n, T = mine.T, longest = mine.nt, tall = mine.T;
     int low = mine.T ? mine.T : INT32_MAX;           // the fewest row tiles of a sequence, and (tall) the most
+    uint32_t group_w = 0, group_T = 0;               // of the 32 sequences from 32 * lane on
+    if (p.num_seqs > 32) {
+      group_w = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w));   // (lane 0's)
+      group_T = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(T));
+      constexpr int kFlight = 4;                     // groups on their way at a time
 #pragma unroll 1
-    for (int b = 32; b < p.num_seqs; b += 32) {
-      const Seq x = seq_at<N>(p, b + lane);
-      w = add_up_to_max(w, x.w);
-      n = add_up_to_max(n, x.n);
-      T = add_up_to_max(T, x.T);
-      longest = max(longest, x.nt);
-      tall = max(tall, x.T);
-      low = min(low, x.T ? x.T : INT32_MAX);
+      for (int b = 32; b < p.num_seqs; b += 32 * kFlight) {
+        RawSeq raw[kFlight];
+#pragma unroll
+        for (int g = 0; g < kFlight; ++g) raw[g] = raw_at(p, b + 32 * g + lane);
+#pragma unroll
+        for (int g = 0; g < kFlight; ++g) {
+          if (b + 32 * g >= p.num_seqs) break;
+          const Seq x = seq_of<N>(p, raw[g]);
+          w = add_up_to_max(w, x.w);
+          n = add_up_to_max(n, x.n);
+          T = add_up_to_max(T, x.T);
+          longest = max(longest, x.nt);
+          tall = max(tall, x.T);
+          low = min(low, x.T ? x.T : INT32_MAX);
+          const uint32_t all_w = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x.w));
+          const uint32_t all_T = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x.T));
+          if (lane == b / 32 + g) {
+            group_w = all_w;
+            group_T = all_T;
+          }
+        }
+      }
     }
     int64_t W = warp_total(w), U = warp_total(T);
     const int64_t rows = warp_total(n);
@@ -287,10 +311,19 @@ struct Walker {
       length = static_cast<int>(static_cast<uint32_t>(length) / G);
       C = static_cast<int>((length + groups - 1) / groups);
     }
-    upto = warp_scan(weight(), lane);
-    units_upto = warp_scan(mine.T, lane);
     lo = pos = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(blockIdx.x / G) * C));
     hi = static_cast<int>(min(static_cast<int64_t>(length), static_cast<int64_t>(lo) + C));
+    if (p.num_seqs > 32) {                           // the first sequences of the piece, or the last whose sums are known
+      const int gw = V ? group_T * V : group_w / G;
+      const int w_upto = warp_scan(gw, lane), T_upto = warp_scan(group_T, lane);
+      const int k = min(31, __popc(__ballot_sync(0xffffffffu, w_upto <= lo)));
+      before = __shfl_sync(0xffffffffu, w_upto - gw, k);
+      units_before = __shfl_sync(0xffffffffu, T_upto - static_cast<int>(group_T), k);
+      b0 = 32 * k;
+      mine = seq_of<N>(p, raw_at(p, b0 + lane));
+    }
+    upto = warp_scan(weight(), lane);
+    units_upto = warp_scan(mine.T, lane);
   }
   __device__ __forceinline__ int weight() const {    // of the held sequence
     return V ? mine.T * V : G > 1 ? (mine.T ? mine.nt + kUnitTiles : 0) : mine.w;
@@ -306,7 +339,7 @@ struct Walker {
         units_before += __shfl_sync(0xffffffffu, units_upto, 31);
         b0 += 32;
         if (b0 >= p.num_seqs) return 0;             // lengths changed under the call
-        mine = seq_at<N>(p, b0 + lane);
+        mine = seq_of<N>(p, raw_at(p, b0 + lane));
         upto = warp_scan(weight(), lane);
         units_upto = warp_scan(mine.T, lane);
         continue;

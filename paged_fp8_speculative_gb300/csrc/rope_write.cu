@@ -8,7 +8,7 @@
 // in the cache (a warp a token, 32 boundaries of cu_seqlens_q at a time) and its sines and cosines.
 //
 // Angles are 64-bit fixed-point turns: position * freq modulo 2^64 drops whole turns exactly, and the
-// upper 32 bits, at most 2^-33 turns off, go to sincospif: no loss at far positions, no FP64.
+// upper 32 bits go to sincospif, rounded to float32 (2^-26 turns): as good at far positions as at near ones, no FP64.
 #include "common.cuh"
 #include "host_checks.cuh"
 

@@ -424,6 +424,27 @@ def test_many_units():
     b.check(b.run())
 
 
+@pytest.mark.parametrize("count,heads,nodes,width", [(33, 16, 1, 0), (160, 16, 2, 0), (1000, 2, 1, 0), (1024, 20, 2, WIDE // 100),
+                                                     (1500, 3, 3, 0), (5000, 1, 1, 0)])
+def test_many_sequences(count, heads, nodes, width):
+    """The walk over batches of more than 32, 128 and 1024 sequences, some longer, one of which has no tokens."""
+    rng = np.random.default_rng(count)
+    lens = [int(x) for x in rng.integers(nodes, 40, count)]
+    for i in (0, count // 2, count - 1):
+        lens[i] = 600 + i % 100
+    b = Batch(lens, [nodes] * count, heads, seed=count, width=width)
+    good = b.run()
+    assert b.status.item() == 0
+    b.check(good)
+    b.cu[10:count // 2 + 1] -= nodes                     # sequence 9 has none, and the long one twice as many
+    b.cu_list = b.cu.tolist()
+    b.nodes = [y - x for x, y in zip(b.cu_list, b.cu_list[1:])]
+    assert b.nodes[9] == 0 and b.nodes[count // 2] == 2 * nodes
+    out = b.run()
+    assert b.status.item() == api.ERR_QLEN
+    b.check(out)
+
+
 def test_strides_and_outputs():
     b = Batch([300, 50], [3, 2], 5, pad=8)
     ref = b.run()
