@@ -44,9 +44,11 @@
 // 35000 keys with 128 heads): 0: 0.00170, 154 and 156 us; 2.5: 0.00187, 145 and 145; 3.5: 0.00214, 138 and 136;
 // 4: 0.00232, 135 and 134.
 //
-// Masks.  A tile that reaches into the new tokens takes each row's word.  Places that no row sees in full
-// are kept out of the second product by value too, since 0 * NaN is NaN: rows behind the sequence are
-// stored as zeros, NaN codes of new tokens too (a row that sees one has a NaN logit, and its sum tells).
+// Masks.  A tile that reaches into the new tokens takes each row's word.  NaN codes that no row, or not every
+// row, sees are kept out of the second product by value, since 0 * NaN is NaN: those of new tokens become zeros
+// (a row that sees one has a NaN logit, and its sum tells), and so does what stands behind the sequence, where
+// that holds NaN.  A key's logit is NaN in every row, if a code of it is: only such keys are gone over (the
+// last tile of a unit took 2900 clocks more when all were).
 //
 // Shared memory (N = 64): two stages of a tile (147456), Q's terms (73728), the second terms of P (8192;
 // the first ones take the place of the tile's 64-byte slice of rotated dims, which only the first product reads).
@@ -574,6 +576,19 @@ __device__ __forceinline__ float row_maxima(float (&v)[n], int lane) {
   return over_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// What shared memory holds of n rows, 16 bytes at a time; from a 16-byte boundary.
+template <int n>
+__device__ __forceinline__ void load_rows(const float* p, float (&x)[n]) {
+#pragma unroll
+  for (int i = 0; i < n / 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(p)[i];
+    x[4 * i] = v.x;
+    x[4 * i + 1] = v.y;
+    x[4 * i + 2] = v.z;
+    x[4 * i + 3] = v.w;
+  }
+}
+
 static_assert(kWaitCycles < (1ll << 32), "32-bit clock");
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -724,6 +739,17 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         }
         if (s.end) break;
         leave_note();
+        // Its Q is asked into L2 while the softmax warps are with the one before (the first ones are there already).
+        if (e > 0) {
+          constexpr int kRowLines = kRow * 2 / 128;
+          const int lines = min(N, s.n * p.heads - s.m * N) * kRowLines;
+#pragma unroll 1
+          for (int i = lane; i < lines; i += 32) {
+            const int r = i / kRowLines, rr = s.m * N + r, t = rr / p.heads;
+            prefetch_line(p.q + static_cast<int64_t>(s.q0 + t) * p.q_stride_tok +
+                          static_cast<int64_t>(rr - t * p.heads) * p.q_stride_head + (i - r * kRowLines) * 64);
+          }
+        }
         if (!warp_wait(smem_u32(&bars.q_full), e & 1, abort_flag)) break;
         const uint32_t end = u + (s.t1 - s.t0);
         if (elect_one()) {
@@ -987,11 +1013,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         rows = min(N, s.n * p.heads - s.m * N);
         // of the rows of this warp, in every lane: a load from shared memory waits for the products' reads
         float l[kHalf], fac[kHalf], ref[kHalf];
+        load_rows(sh.factor + row0, fac);
 #pragma unroll
-        for (int r = 0; r < kHalf; ++r) {
-          l[r] = ref[r] = 0.f;
-          fac[r] = sh.factor[row0 + r];
-        }
+        for (int r = 0; r < kHalf; ++r) l[r] = ref[r] = 0.f;
         const int start = s.L - s.n;                   // first new token
         const bool late = (s.t0 + 1) * kKeys > start;  // a row may see nothing of the first tile
 #pragma unroll 1
@@ -1001,6 +1025,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           const int j = t * kKeys + key;
           const bool ragged = (t + 1) * kKeys > start;  // new tokens, or places behind the sequence
           uint32_t seen = ~0u;                         // the rows of this warp that see the key
+          bool nan = false;                            // the key may hold a NaN code
           if (ragged) {
             if (j >= start) seen = 0u;
             const uint64_t word = lane < kHalf ? sh.word[row0 + lane] : 0;
@@ -1022,6 +1047,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
 #pragma unroll
             for (int r = 0; r < kHalf; ++r) y[r] = fmaf(__uint_as_float(h[r]) + __uint_as_float(lo[r]), fac[r], -ref[r]);
             if (ragged) {
+              nan = !(y[0] == y[0]);
 #pragma unroll
               for (int r = 0; r < kHalf; ++r)
                 if (!((seen >> r) & 1u)) y[r] = -INFINITY;
@@ -1074,17 +1100,26 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             }
             meet_half(half);
 #pragma unroll
-            for (int r = 0; r < kHalf; ++r) {
-              const float step = sh.step[row0 + r];
-              y[r] += step;
-              ref[r] -= step;
+            for (int r = 0; r < kHalf; r += 4) {
+              float step[4];
+              load_rows(sh.step + row0 + r, step);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                y[r + i] += step[i];
+                ref[r + i] -= step[i];
+              }
             }
             if (t > s.t0) {
               // (O may be touched once the previous tile's products are in it)
               alive &= warp_wait(smem_u32(&bars.pv_done), (u - 1) & 1, abort_flag);
               tc_fence_after();
 #pragma unroll
-              for (int r = 0; r < kHalf; ++r) l[r] *= sh.f[row0 + r];
+              for (int r = 0; r < kHalf; r += 4) {
+                float f[4];
+                load_rows(sh.f + row0 + r, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l[r + i] *= f[i];
+              }
 #pragma unroll 1
               for (int c = 0; c < kColumns; ++c) {
                 const uint32_t at = tmem + lanes + kOCol + c * N + row0;
@@ -1092,7 +1127,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
                 tmem_ld<kHalf>(at, o);
                 tmem_wait<kHalf>(o);
 #pragma unroll
-                for (int r = 0; r < kHalf; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sh.f[row0 + r]);
+                for (int r = 0; r < kHalf; r += 4) {
+                  float f[4];
+                  load_rows(sh.f + row0 + r, f);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[r + i] = __float_as_uint(__uint_as_float(o[r + i]) * f[i]);
+                }
                 tmem_st<kHalf>(at, o);
               }
               tmem_st_wait();
@@ -1115,8 +1155,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
           // the previous tile's second terms of these keys have been read: a quarter is a block
           if (u > 0) alive &= warp_wait(smem_u32(&bars.empty[(u - 1) % kStages][quarter]), ((u - 1) / kStages) & 1, abort_flag);
           write(smem + off_p<N>() + (key >> 3) * kAtom, lo);
-          if (ragged && j >= start) {
-            // this half's 256 of the key's values: none behind the sequence, no NaN among the new tokens
+          if (ragged && j >= start && nan) {
+            // this half's 256 of the key's values, without its NaN; none at all behind the sequence
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {             // (in any order; this one meets all banks)
               const uint32_t at = stage + (key >> 3) * kGroup + (4 * half + (i >> 2)) * kAtom + (key & 7) * 64 +
@@ -1179,62 +1219,76 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         // bytes of a row at a time, 4 dims of partial outputs or 8 of the output.  (4 or 2 bytes at a time took
         // 4100 clocks.)
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + s.slot;
+        constexpr int kTurn = 4;         // 8 rows of 128 dims at a time, so many beside one another
 #pragma unroll 1
-        for (int at = 0; at < kColumns * kHalf / 8; ++at) {   // 8 rows of 128 dims
-          const int c = at / (kHalf / 8), r0 = at % (kHalf / 8) * 8;
-          uint32_t o[8];
-          tmem_ld<8>(tmem + lanes + kOCol + c * N + row0 + r0, o);
-          tmem_wait<8>(o);
-          const int d0 = c * 128 + quarter * 32;       // (a TMEM lane is a dim here)
+        for (int at = 0; at < kColumns * kHalf / 8; at += kTurn) {
+          uint32_t o[kTurn][8];
+#pragma unroll
+          for (int q = 0; q < kTurn; ++q) {
+            const int c = (at + q) / (kHalf / 8), r0 = (at + q) % (kHalf / 8) * 8;
+            tmem_ld<8>(tmem + lanes + kOCol + c * N + row0 + r0, o[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < kTurn; ++q) tmem_wait<8>(o[q]);
           if (whole) {
-            uint32_t x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {              // rows 2i + bit 0, dims of the pair of lanes
-              const float f0 = sh.f[row0 + r0 + 2 * i], f1 = sh.f[row0 + r0 + 2 * i + 1];
-              const float v0 = f0 == 0.f ? 0.f : __uint_as_float(o[2 * i]) * f0;
-              const float v1 = f1 == 0.f ? 0.f : __uint_as_float(o[2 * i + 1]) * f1;
-              const float keep = lane & 1 ? v1 : v0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-              const __nv_bfloat162 pair = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
-              x[i] = *reinterpret_cast<const uint32_t*>(&pair);
-            }
-            uint32_t y[2][2], z[4];
+            for (int q = 0; q < kTurn; ++q) {
+              const int c = (at + q) / (kHalf / 8), r0 = (at + q) % (kHalf / 8) * 8;
+              const int d0 = c * 128 + quarter * 32;   // (a TMEM lane is a dim here)
+              uint32_t x[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {              // rows 4h + bits 0 and 1, dims of 4 lanes
-              const uint32_t keep = lane & 2 ? x[2 * h + 1] : x[2 * h];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[2 * h] : x[2 * h + 1], 2);
-              y[h][0] = lane & 2 ? got : keep;
-              y[h][1] = lane & 2 ? keep : got;
-            }
+              for (int i = 0; i < 4; ++i) {            // rows 2i + bit 0, dims of the pair of lanes
+                const float f0 = sh.f[row0 + r0 + 2 * i], f1 = sh.f[row0 + r0 + 2 * i + 1];
+                const float v0 = f0 == 0.f ? 0.f : __uint_as_float(o[q][2 * i]) * f0;
+                const float v1 = f1 == 0.f ? 0.f : __uint_as_float(o[q][2 * i + 1]) * f1;
+                const float keep = lane & 1 ? v1 : v0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+                const __nv_bfloat162 pair = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
+                x[i] = *reinterpret_cast<const uint32_t*>(&pair);
+              }
+              uint32_t y[2][2], z[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {              // rows bits 0 .. 2, dims of 8 lanes
-              const uint32_t keep = lane & 4 ? y[1][h] : y[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 4 ? y[0][h] : y[1][h], 4);
-              z[h] = lane & 4 ? got : keep;
-              z[2 + h] = lane & 4 ? keep : got;
+              for (int h = 0; h < 2; ++h) {            // rows 4h + bits 0 and 1, dims of 4 lanes
+                const uint32_t keep = lane & 2 ? x[2 * h + 1] : x[2 * h];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[2 * h] : x[2 * h + 1], 2);
+                y[h][0] = lane & 2 ? got : keep;
+                y[h][1] = lane & 2 ? keep : got;
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {            // rows bits 0 .. 2, dims of 8 lanes
+                const uint32_t keep = lane & 4 ? y[1][h] : y[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 4 ? y[0][h] : y[1][h], 4);
+                z[h] = lane & 4 ? got : keep;
+                z[2 + h] = lane & 4 ? keep : got;
+              }
+              const int r = r0 + (lane & 7);
+              if (r < valid)
+                *reinterpret_cast<uint4*>(p.out + reinterpret_cast<const int64_t*>(sh.xch[half])[r] + d0 + (lane & 24)) =
+                    make_uint4(z[0], z[1], z[2], z[3]);
             }
-            const int r = r0 + (lane & 7);
-            if (r < valid)
-              *reinterpret_cast<uint4*>(p.out + reinterpret_cast<const int64_t*>(sh.xch[half])[r] + d0 + (lane & 24)) =
-                  make_uint4(z[0], z[1], z[2], z[3]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {              // rows 4i + bits 0 and 1, dims of 4 lanes
-              uint32_t x[2][2], z[4];
+            for (int q = 0; q < kTurn; ++q) {
+              const int c = (at + q) / (kHalf / 8), r0 = (at + q) % (kHalf / 8) * 8;
+              const int d0 = c * 128 + quarter * 32;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t w0 = o[4 * i + 2 * h], w1 = o[4 * i + 2 * h + 1];
-                const uint32_t keep = lane & 1 ? w1 : w0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? w0 : w1, 1);
-                x[h][0] = lane & 1 ? got : keep;
-                x[h][1] = lane & 1 ? keep : got;
-              }
+              for (int i = 0; i < 2; ++i) {            // rows 4i + bits 0 and 1, dims of 4 lanes
+                uint32_t x[2][2], z[4];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t keep = lane & 2 ? x[1][h] : x[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[0][h] : x[1][h], 2);
-                z[h] = lane & 2 ? got : keep;
-                z[2 + h] = lane & 2 ? keep : got;
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t w0 = o[q][4 * i + 2 * h], w1 = o[q][4 * i + 2 * h + 1];
+                  const uint32_t keep = lane & 1 ? w1 : w0, got = __shfl_xor_sync(0xffffffffu, lane & 1 ? w0 : w1, 1);
+                  x[h][0] = lane & 1 ? got : keep;
+                  x[h][1] = lane & 1 ? keep : got;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t keep = lane & 2 ? x[1][h] : x[0][h], got = __shfl_xor_sync(0xffffffffu, lane & 2 ? x[0][h] : x[1][h], 2);
+                  z[h] = lane & 2 ? got : keep;
+                  z[2 + h] = lane & 2 ? keep : got;
+                }
+                const int r = r0 + 4 * i + (lane & 3);
+                if (r < valid)
+                  *reinterpret_cast<uint4*>(p.o_part + (slot * N + row0 + r) * kDim + d0 + (lane & 28)) = make_uint4(z[0], z[1], z[2], z[3]);
               }
-              const int r = r0 + 4 * i + (lane & 3);
-              if (r < valid)
-                *reinterpret_cast<uint4*>(p.o_part + (slot * N + row0 + r) * kDim + d0 + (lane & 28)) = make_uint4(z[0], z[1], z[2], z[3]);
             }
           }
         }
