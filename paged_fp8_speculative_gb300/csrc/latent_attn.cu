@@ -44,11 +44,10 @@
 // 35000 keys with 128 heads): 0: 0.00170, 154 and 156 us; 2.5: 0.00187, 145 and 145; 3.5: 0.00214, 138 and 136;
 // 4: 0.00232, 135 and 134.
 //
-// Masks.  A tile that reaches into the new tokens takes each row's word.  NaN codes that no row, or not every
-// row, sees are kept out of the second product by value, since 0 * NaN is NaN: those of new tokens become zeros
-// (a row that sees one has a NaN logit, and its sum tells), and so does what stands behind the sequence, where
-// that holds NaN.  A key's logit is NaN in every row, if a code of it is: only such keys are gone over (the
-// last tile of a unit took 2900 clocks more when all were).
+// Masks.  A tile that reaches into the new tokens takes each row's word.  Places that no row sees in full
+// are kept out of the second product by value too, since 0 * NaN is NaN: rows behind the sequence are
+// stored as zeros, NaN codes of new tokens too (a row that sees one has a NaN logit, and its sum tells).  A
+// key's logit is NaN, whatever the row, exactly where a code of it is: so only such keys are gone over.
 //
 // Shared memory (N = 64): two stages of a tile (147456), Q's terms (73728), the second terms of P (8192;
 // the first ones take the place of the tile's 64-byte slice of rotated dims, which only the first product reads).
@@ -939,17 +938,18 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
       constexpr int kSide = N == 16 ? 16 : 8, kParts = (kRow / 8 + kSide - 1) / kSide;   // blocks of 8 a lane
       constexpr int kStep = kSoftWarps * 32 / kSide;   // rows at a time; a multiple of 8
       const int side = lane % kSide, first = (w * 32 + lane) / kSide;
-      uint4 x[kParts];
-      uint64_t word = 0;
-      auto fetch = [&](int r) {
+      constexpr int kTurns = N / kStep;
+      uint4 x[kTurns][kParts];                       // all on their way at once
+      uint64_t word[kTurns];
+      auto fetch = [&](int r, int go) {
         const int rr = m * N + r, tok = r < rows ? rr / p.heads : 0;
         const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(q0 + tok) * p.q_stride_tok +
                                                           static_cast<int64_t>(rr - tok * p.heads) * p.q_stride_head) + side;
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-          x[i] = r < rows && (kParts * kSide == kRow / 8 || side + i * kSide < kRow / 8) ? src[i * kSide]
+          x[go][i] = r < rows && (kParts * kSide == kRow / 8 || side + i * kSide < kRow / 8) ? src[i * kSide]
                                                                                        : make_uint4(0u, 0u, 0u, 0u);
-        word = r < rows ? (p.mask ? p.mask[q0 + tok] : (2ull << tok) - 1ull) : 0;
+        word[go] = r < rows ? (p.mask ? p.mask[q0 + tok] : (2ull << tok) - 1ull) : 0;
       };
       // Where a row's blocks go.  Block j of the 64 of the latent part is half of a 16-byte place, column j / 16,
       // swizzled by the row's lowest bits, which are the same in all of a lane's rows.
@@ -961,14 +961,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         place[i] = q + first * 128 + (((j >> 1) ^ (first & 7)) << 4) + (j & 1) * 8;
       }
       const uint32_t rope_place = q + kColumns * q_column<N>() + first * 64 + (((side >> 1) ^ ((first >> 1) & 3)) << 4) + (side & 1) * 8;
-      fetch(first);
+#pragma unroll
+      for (int go = 0; go < kTurns; ++go) fetch(first + go * kStep, go);
 #pragma unroll 1
-      for (int r = first, go = 0; go < N / kStep; ++go, r += kStep) {
+      for (int r = first, go = 0; go < kTurns; ++go, r += kStep) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                       __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[0][i].x & 0x7fff7fffu, x[0][i].y & 0x7fff7fffu),
+                                       __vmaxu2(x[0][i].z & 0x7fff7fffu, x[0][i].w & 0x7fff7fffu)));
 #pragma unroll
         for (int o = 1; o < kSide; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int exponent = max(top & 0xffffu, top >> 16) >> 7;   // biased; 255: not finite
@@ -979,8 +980,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
           uint32_t h0, h1, l0, l1;
-          two_terms<false>(scaled_half2(x[i].x, up), scaled_half2(x[i].y, up), 0u, h0, l0);
-          two_terms<false>(scaled_half2(x[i].z, up), scaled_half2(x[i].w, up), 0u, h1, l1);
+          two_terms<false>(scaled_half2(x[0][i].x, up), scaled_half2(x[0][i].y, up), 0u, h0, l0);
+          two_terms<false>(scaled_half2(x[0][i].z, up), scaled_half2(x[0][i].w, up), 0u, h1, l1);
           if (i * kSide < kDim / 8) {
             const uint32_t at = place[i % (16 / kSide)] + i * kSide / 16 * q_column<N>() + go * kStep * 128;
             st_shared8(at, h0, h1);
@@ -994,9 +995,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         if (side == 0) {
           sh.factor[r] = r < rows ? factor * __uint_as_float(static_cast<uint32_t>(127 - a) << 23) : 0.f;
           sh.ref[r] = kNoRef;
-          sh.word[r] = n < 64 ? word & ((1ull << n) - 1ull) : word;
+          sh.word[r] = n < 64 ? word[0] & ((1ull << n) - 1ull) : word[0];
         }
-        if (go + 1 < N / kStep) fetch(r + kStep);
+#pragma unroll
+        for (int k = 1; k < kTurns; ++k) {
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) x[k - 1][i] = x[k][i];
+          word[k - 1] = word[k];
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
