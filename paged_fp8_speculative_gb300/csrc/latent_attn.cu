@@ -56,10 +56,11 @@
 // What bounds it.  The products of a tile of 64 rows take 2430 clocks of the tensor cores (S 64 an instruction,
 // 18 of them; O's two terms 78 a pair, 16), and two stages of tiles are all that fits, so that a tile's chain
 // S, softmax, P, O overlaps with one other tile's only: 3400 to 3900 clocks a tile.  Measured, in graphs: 16 x
-// 35000 keys with 4 tokens of 16 heads 84 us (memory's floor 48.8, the products' 41.4 at the bf16 rate), with
-// one token 62; 128 heads 136 (82.8 at the bf16 rate); 64-node trees over 8191 keys 138 (77.0).  A call begins
-// with 7 to 9 us (launch, lengths, Q's terms, first tiles of all CTAs at once) and ends with 2.5 of output and
-// 4 to 7 of the join.
+// 35000 keys with 4 tokens of 16 heads 83 us (memory's floor 48.8, the products' 41.4 at the bf16 rate), with
+// one token 62; 128 heads 135 (82.8 at the bf16 rate); 64-node trees over 8191 keys 135 (77.0); 300 keys 10.4.
+// A call begins with 7 to 9 us (launch, lengths, Q's terms, first tiles of all CTAs at once) and ends with 2.5
+// of output and 4 to 7 of the join; a unit costs 8 to 10 more (sums, Q, output), which short sequences pay one
+// by one.
 #include "common.cuh"
 #include "host_checks.cuh"
 #include "sm100.cuh"
