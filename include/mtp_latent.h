@@ -37,7 +37,7 @@ extern "C" {
  * up to itself (tree_mask NULL: a chain), or those whose bit is set in tree_mask (as in mtp_tree_attn_fwd:
  * bits >= n_b are ignored, the token's own bit is not implied).  A token that sees nothing gets zeros.
  * Tokens that a row does not see do not influence it, whatever codes they hold.  A row of q that
- * holds an infinity or a NaN gets NaN.
+ * holds an infinity or a NaN gets NaN, and so does one whose logits leave float32's range.
  *
  *  q            device bf16 [total_q][num_heads][576], strides in elements (multiples of 8), unit stride
  *               along the row, 16-byte aligned
@@ -67,7 +67,7 @@ int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_he
                         int64_t out_stride_head, int32_t* status, void* stream);
 
 /* Bytes of workspace mtp_latent_attn_fwd needs on the current device (0 for invalid arguments or without
- * a device). */
+ * a device).  It grows with the arguments: a workspace for the largest batch does for all smaller ones. */
 size_t mtp_latent_attn_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads,
                                       int32_t max_pages_per_seq);
 

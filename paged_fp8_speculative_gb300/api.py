@@ -649,7 +649,8 @@ def mtp_latent_attn_fwd(q: torch.Tensor, cache: torch.Tensor, block_tables: torc
     cu_seqlens_q as in mtp_verify_attn_fwd.  Token i of a sequence's new ones (its last in the cache)
     sees what is before them and the new ones up to itself, or those of its word of ``tree_mask``
     [total_q] int64 (mtp_tree_mask).  ``workspace``: at least mtp_latent_attn_workspace_size(...) bytes,
-    kept by a decode loop so that no call allocates; it needs no initialisation.
+    kept by a decode loop so that no call allocates (made for the largest batch, it does for all); it needs
+    no initialisation.
     """
     call = (_BINDING or binding()).latent_attn
     descale, = _descales(q.device, stream, descale)

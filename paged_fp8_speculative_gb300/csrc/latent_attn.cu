@@ -1476,7 +1476,11 @@ bool parts_of(int32_t num_seqs, int32_t total_q, int32_t heads, int32_t max_page
   w->o = align256(static_cast<size_t>(w->ctas) * 2 * w->rows * kDim * sizeof(float));
   w->sums = align256(static_cast<size_t>(w->ctas) * 2 * w->rows * sizeof(float2));
   w->notes = align256(static_cast<size_t>(w->units) * sizeof(JoinNote));
-  w->total = w->o + w->sums + w->notes + 256;
+  // What a call asks for grows with its arguments, whatever its units' rows are: a workspace made for the largest
+  // batch does for the smaller ones.
+  const size_t slots = static_cast<size_t>(std::min(sms, kMaxCtas)) * 2 * 64;
+  w->total = align256(slots * kDim * sizeof(float)) + align256(slots * sizeof(float2)) +
+             align256(static_cast<size_t>(units_bound(num_seqs, total_q, heads, 16)) * sizeof(JoinNote)) + 256;
   return true;
 }
 

@@ -509,6 +509,19 @@ def test_no_wait_runs_out(heads, nodes):
     assert b.status.item() == 0
 
 
+def test_one_workspace_for_all_batches():
+    """The size grows with every argument, and batches of all kinds run in the largest one's."""
+    most = (40, 160, 128, 600)
+    need = api.mtp_latent_attn_workspace_size(*most)
+    for i, values in enumerate(((1, 2, 3, 39, 40), (40, 41, 99, 160), (1, 5, 16, 17, 127, 128), (1, 8, 9, 100, 600))):
+        sizes = [api.mtp_latent_attn_workspace_size(*most[:i], v, *most[i + 1:]) for v in values]
+        assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] == need
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for lens, nodes, heads in (([9000], [4], 16), ([300] * 40, [4] * 40, 128), ([9000, 5], [1, 1], 5), ([300] * 40, [1] * 40, 16), ([1], [1], 1)):
+        b = Batch(lens, nodes, heads, seed=40 + heads)
+        assert torch.equal(b.run(workspace=ws), b.run())
+
+
 def test_two_streams():
     """Two calls at once, each with its own workspace, in turn many times."""
     a, b = Batch([9000, 300], [4, 1], 16, seed=20), Batch([2000, 5000, 70], [1, 1, 1], 128, seed=21)
