@@ -1,6 +1,6 @@
 // The Python binding of the draft-tree, cache, rotary and latent entry points (include/mtp_tree.h,
-// include/mtp_cache.h, include/mtp_rope.h, include/mtp_latent.h): argument checks, the outputs that were not given, and the call.  These calls
-// take 3 to 20 us on the GPU; the same steps in Python took 10 to 17 us of host time a call on a
+// include/mtp_cache.h, include/mtp_rope.h, include/mtp_latent.h): argument checks, the outputs that were
+// not given, and the call.  These calls take 3 to 20 us on the GPU; the same steps in Python took 10 to 17 us of host time a call on a
 // Grace core (an attribute of a tensor 0.1 us, torch.empty 1.6 us, a call through ctypes 1.5 us).
 // Nothing is computed here.
 //
