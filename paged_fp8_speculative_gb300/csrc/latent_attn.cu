@@ -53,14 +53,16 @@
 // the first ones take the place of the tile's 64-byte slice of rotated dims, which only the first product reads).
 // TMEM: S double buffer at columns 0 and 128, O at 256, N columns for each 128 dims.
 //
-// What bounds it.  The products of a tile of 64 rows take 2430 clocks of the tensor cores (S 64 an instruction,
-// 18 of them; O's two terms 78 a pair, 16), and two stages of tiles are all that fits, so that a tile's chain
-// S, softmax, P, O overlaps with one other tile's only: 3400 to 3900 clocks a tile.  Measured, in graphs: 16 x
-// 35000 keys with 4 tokens of 16 heads 83 us (memory's floor 48.8, the products' 41.4 at the bf16 rate), with
-// one token 62; 128 heads 135 (82.8 at the bf16 rate); 64-node trees over 8191 keys 135 (77.0); 300 keys 10.4.
-// A call begins with 7 to 9 us (launch, lengths, Q's terms, first tiles of all CTAs at once) and ends with 2.5
-// of output and 4 to 7 of the join; a unit costs 8 to 10 more (sums, Q, output), which short sequences pay one
-// by one.
+// What bounds it.  Shared memory's 128 bytes a clock: for 64 rows a tile's S reads the codes and Q (147 KB; 18
+// instructions of 64 clocks, measured alone), O the codes once for P's two terms and those for each 128 dims
+// (128 KB; 16 pairs of 78 clocks), the tile itself is written (74 KB), and P (16 KB): about 3100 clocks.  A
+// tile takes 3460 where the cache is in L2 (64-node trees) and 3740 where it comes from memory (whose rate
+// alone asks for 3230 over all CTAs); what is lost is the chain S, softmax, P, O, of which two tiles, all that
+// fits, overlap.  Measured, in graphs: 16 x 35000 keys with 4 tokens of 16 heads 83 us (memory's floor 48.8,
+// the products' 41.4 at the bf16 rate), with one token 62; 128 heads 135 (82.8 at the bf16 rate); 64-node trees
+// over 8191 keys 135 (77.0); 300 keys 10.4.  A call begins with 7 to 9 us (launch, lengths, Q's terms, first
+// tiles of all CTAs at once) and ends with 2.5 of output and 4 to 7 of the join; a unit costs 6 to 10 more
+// (sums, Q, output), which short sequences pay one by one.
 #include "common.cuh"
 #include "host_checks.cuh"
 #include "sm100.cuh"
