@@ -548,8 +548,6 @@ def mtp_rope_freqs(inv_freq, device=None) -> torch.Tensor:
 
 
 def _descales(device, stream, *values):
-    if all(isinstance(x, torch.Tensor) for x in values):
-        return values
     with _temporaries_on(stream, device, True):
         return tuple(_descale(x, device) for x in values)
 
@@ -571,7 +569,8 @@ def mtp_rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     (bf16) may be q itself.
     """
     call = (_BINDING or binding()).rope_append
-    k_descale, v_descale = _descales(k.device, stream, k_descale, v_descale)
+    if not (isinstance(k_descale, torch.Tensor) and isinstance(v_descale, torch.Tensor)):
+        k_descale, v_descale = _descales(k.device, stream, k_descale, v_descale)
     if stream is None:
         return call(q, k, v, positions, freqs, k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q,
                     k_descale, v_descale, mscale, interleaved, q_out, status, None)
@@ -595,7 +594,8 @@ def mtp_rope_latent_append(q_rope: Optional[torch.Tensor], latent: torch.Tensor,
     mtp_rope_append; freqs has 32 entries.
     """
     call = (_BINDING or binding()).rope_latent_append
-    descale, = _descales(latent.device, stream, descale)
+    if not isinstance(descale, torch.Tensor):
+        descale, = _descales(latent.device, stream, descale)
     if stream is None:
         return call(q_rope, latent, k_rope, positions, freqs, cache, block_tables, seq_lens,
                     cu_seqlens_q, descale, mscale, interleaved, q_out, status, None)
@@ -617,7 +617,9 @@ def mtp_rope_prefill(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v: 
     [tokens, H_kv, 128].
     """
     call = (_BINDING or binding()).rope_prefill
-    q_descale, k_descale, v_descale = _descales(q.device, stream, q_descale, k_descale, v_descale)
+    if not (isinstance(q_descale, torch.Tensor) and isinstance(k_descale, torch.Tensor) and
+            isinstance(v_descale, torch.Tensor)):
+        q_descale, k_descale, v_descale = _descales(q.device, stream, q_descale, k_descale, v_descale)
     if stream is None:
         return call(q, k, k_rope, v, positions, freqs, q_descale, k_descale, v_descale, mscale,
                     interleaved, q_out, k_out, v_out, None)
@@ -653,7 +655,8 @@ def mtp_latent_attn_fwd(q: torch.Tensor, cache: torch.Tensor, block_tables: torc
     no initialisation.
     """
     call = (_BINDING or binding()).latent_attn
-    descale, = _descales(q.device, stream, descale)
+    if not isinstance(descale, torch.Tensor):
+        descale, = _descales(q.device, stream, descale)
     if stream is None:
         return call(q, cache, block_tables, seq_lens, cu_seqlens_q, descale, softmax_scale, tree_mask, out,
                     workspace, status, None)
