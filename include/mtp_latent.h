@@ -56,7 +56,7 @@ extern "C" {
  * ascend within total_q are unknown and not written.  Rows that belong to no sequence are not written.
  * (MTPATTN_ERR_TIMEOUT: a wait ran out, about two seconds without progress; the rows it concerns are
  * unspecified.)  Results are the same bits in every call with the same arguments.  Two kernels are
- * launched, or one where tables have no more than 8 pages.
+ * launched, or one where tables have no more than 32 pages.
  */
 int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t q_stride_head, const void* cache,
                         int64_t num_pages, const int32_t* block_tables, int32_t max_pages_per_seq,

@@ -108,6 +108,10 @@ constexpr int kUnitTiles = 6, kCutTiles = 7, kCutPieces = 40;   // what a unit's
                                                      // tiles (8 x 1000 keys, 4 tokens of 16 heads: 16.6 us at
                                                      // kUnitTiles 7, 15.7 at 6; 1 x 300, 1 token, 9.6 and 10.4 at 5)
 constexpr int kFewTiles = 8;
+constexpr int kWholeTiles = 4;                       // tables no longer: units stay whole, and no join is launched
+                                                     // (64 x 300 keys, 1 token of 128 heads, 22.9 us with cuts, 19.4
+                                                     // without; 256 x 500 90.9 and 81.6; 1 x 500, 4 tokens of 16, 10.3
+                                                     // and 11.1; 1 x 700 would take 10.1 and 13.5)
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kBadSum = 0x7fd0bad1u;            // a sum of a sequence with a bad page (a NaN that no
                                                      // arithmetic makes)
@@ -153,6 +157,7 @@ struct LatentParams {
   int32_t* units;            // for the join: their number
   JoinNote* notes;
   int32_t unit_bound;
+  int32_t whole;             // no unit is cut, nothing is joined: tables are that short
 };
 
 struct Segment {             // part of one unit: tiles t0 .. t1 - 1 of nt
@@ -286,7 +291,8 @@ struct Walker {
     const int64_t rows = warp_total(n);
     // Sequences that claim the same rows again and again (cu_seqlens_q far out of order) could make the line
     // longer than any call's is: then nothing is computed.
-    if (W > INT32_MAX || rows > 2ll * p.total_q) {
+    longest = __reduce_max_sync(0xffffffffu, longest) + kUnitTiles;
+    if (W > INT32_MAX || rows > 2ll * p.total_q || (p.whole && U * longest > INT32_MAX)) {
       if (blockIdx.x == 0 && lane == 0) set_status(p.status, MTPATTN_ERR_QLEN);
       W = U = 0;
     }
@@ -298,11 +304,11 @@ struct Walker {
     // (in tiles): the join, and its bytes, fewer for units that are not full.  (kCutTiles: 16 x 500 keys, 4 tokens
     // of 16 heads, take 16.2 us at 4, 12.8 at 7; one of them 10.1 at 7, 11.7 at 10.  kCutPieces: 64-node trees over
     // 8 x 8191 keys take 135 us at 40, 140 at 80.)
-    longest = __reduce_max_sync(0xffffffffu, longest) + kUnitTiles;
     const float full = fminf(1.f, static_cast<float>(p.total_q) * static_cast<float>(p.heads) / static_cast<float>(N * max(units, 1)));
     const int join = kCutTiles + static_cast<int>(static_cast<float>(units + p.ctas) * full * (N / 64.f / kCutPieces));
     const int each = max(1, static_cast<int>((static_cast<uint32_t>(units) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)));
-    if (static_cast<int64_t>(each) * longest <= C + static_cast<int>(static_cast<uint32_t>(join) / each) && static_cast<int64_t>(units) * longest <= INT32_MAX) {
+    if (static_cast<int64_t>(units) * longest <= INT32_MAX &&
+        (p.whole || static_cast<int64_t>(each) * longest <= C + static_cast<int>(static_cast<uint32_t>(join) / each))) {
       V = longest;
       C = each * longest;
       length = units * longest;
@@ -1551,7 +1557,7 @@ int launch_latent(LatentParams& p, int device, cudaStream_t stream) {
     allowed[device].store(true, std::memory_order_release);
   }
   if (launch_pdl(kernel, dim3(p.ctas), kLatentThreads, smem_bytes<N>(), stream, p) != cudaSuccess) return MTPATTN_E_LAUNCH;
-  if (p.max_pages <= kTilePages) return MTPATTN_OK;  // units of one tile are never cut
+  if (p.whole) return MTPATTN_OK;
   // Few rows in many pieces (one row of 105000 keys in 152: 47 -> 31 us a call) are joined by 4 CTAs for each 2 rows,
   // where at most 16 pieces cost 0.7 us more so.
   const bool one = p.unit_bound * N <= 320 && p.max_pages > 16 * kTilePages, few = p.unit_bound <= 32;
@@ -1646,6 +1652,7 @@ extern "C" int mtp_latent_attn_fwd(const void* q, int64_t q_stride_tok, int64_t 
   p.notes = reinterpret_cast<JoinNote*>(ws + w.o + w.sums);
   p.units = reinterpret_cast<int32_t*>(ws + w.o + w.sums + w.notes);
   p.unit_bound = static_cast<int32_t>(w.units);
+  p.whole = max_pages_per_seq <= kWholeTiles * kTilePages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return w.rows == 16 ? launch_latent<16>(p, device, st)
          : w.rows == 32 ? launch_latent<32>(p, device, st)

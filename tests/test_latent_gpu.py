@@ -522,6 +522,18 @@ def test_one_workspace_for_all_batches():
         assert torch.equal(b.run(workspace=ws), b.run())
 
 
+@pytest.mark.parametrize("width", [8, 9, 31, 32, 33, 40])
+@pytest.mark.parametrize("heads,nodes", [(16, 1), (16, 4), (128, 1), (4, 30)])
+def test_short_tables(width, heads, nodes):
+    """Tables of up to 32 pages, whose units are never cut, and a little longer ones; more units than SMs."""
+    lens = [max(nodes, n) for n in (width * 16, 1, 127, 129, width * 16 - 15) + (60,) * 30]
+    lens = [min(n, width * 16) for n in lens]
+    b = Batch(lens, [nodes] * len(lens), heads, seed=width + heads, width=width)
+    out = b.run()
+    assert b.status.item() == 0
+    b.check(out)
+
+
 def test_two_streams():
     """Two calls at once, each with its own workspace, in turn many times."""
     a, b = Batch([9000, 300], [4, 1], 16, seed=20), Batch([2000, 5000, 70], [1, 1, 1], 128, seed=21)
