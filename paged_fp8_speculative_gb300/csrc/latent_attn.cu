@@ -60,7 +60,7 @@
 // alone asks for 3230 over all CTAs); what is lost is the chain S, softmax, P, O, of which two tiles, all that
 // fits, overlap.  Measured, in graphs: 16 x 35000 keys with 4 tokens of 16 heads 83 us (memory's floor 48.8,
 // the products' 41.4 at the bf16 rate), with one token 62; 128 heads 135 (82.8 at the bf16 rate); 64-node trees
-// over 8191 keys 135 (77.0); 300 keys 10.4.  A call begins with 7 to 9 us (launch, lengths, Q's terms, first
+// over 8191 keys 136 (77.0); 300 keys 9.8.  A call begins with 7 to 9 us (launch, lengths, Q's terms, first
 // tiles of all CTAs at once) and ends with 2.5 of output and 4 to 7 of the join; a unit costs 6 to 10 more
 // (sums, Q, output), which short sequences pay one by one.
 #include "common.cuh"
