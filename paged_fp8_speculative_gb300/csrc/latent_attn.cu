@@ -27,22 +27,27 @@
 //
 // Precision.  Codes enter as they are, Q as two e4m3 terms of x = q 2^a (a per row, max |x| in [128,
 // 256)): hi = e4m3(x), lo = e4m3(x - hi), as 2 N columns of one product, added in float32.  A bf16 value
-// has 8 significant bits and each term keeps 4, so x = hi + lo within 2^-9 of the row's largest, and
-// to 2^-17 of it below.  The weights p = 2^(s - ref), at most 2^8.75, are two e4m3 terms as well, of which
-// the smallest step is 2^-9.  Plain rounding would drop all weights
-// below half of that, which many keys behind one large weight can be (30000 at 2^-19 are 5% of the sum);
-// so the second term is rounded with a dither, a number in (-1/2, 1/2) steps that goes through 128
-// evenly spread values over a tile's keys (their bits reversed): sums of small weights keep their size to
-// 2^-23, and the same bits come every time.  The sums of weights are of the unrounded ones, in float32.
+// has 8 significant bits and the terms keep 4 each, so x = hi + lo, but for what is below lo's smallest step: at most
+// 2^-10, 2^-17 of the row's largest.
+// The weights p = 2^(s - ref), at most 2^8.75, are an e4m3 term and an e5m2 one of what it leaves, of 4 and 3
+// significant bits: within 2^-8 of p, as a bf16 weight is.  e4m3's smallest step is 2^-9, e5m2's 2^-16: of a weight
+// below 2^-6 the second term is what counts, and of one below 2^-10 it is all.  There rounding to nearest would
+// bend the sum of many equal weights behind a large one (30000 at 2^-19 are 5% of all).  So a second term below 2^-10
+// is rounded up or down in the proportion of the bits that go, by a number of the key's own (its dither): it is off by
+// less than 2^-13, and sums are not.  The numbers of a tile's keys are 128 evenly spread ones, the place's bits
+// reversed, and each tile has them in another order, so that keys whose values repeat with any period have evenly spread
+// ones too; the same bits come every time.  (Two e4m3 terms with one order for all tiles lost the weights below 2^-9
+// of whole classes of keys: with a first key 9.5 nats above 8190 others and values of period 2 the output was 0.4 off, in
+// 2-norm, where it is now 0.0017.)  The sums of weights are of the unrounded ones, in float32.
 //
 // Online softmax in the log2 domain with a lazy reference: raised, and O rescaled in TMEM, only when a logit
 // exceeds it by more than kTau.  So a tile's maxima over keys (across lanes and warps, which this orientation
 // makes dear) are only needed where that happens.  A reference that is raised with tiles to come goes kRoom
-// above what it has to, so that it is raised less often; the largest weight is then 2^3.5 or more instead of
-// 2^7, and the step 2^-12.5 of it.  kRoom's sides, measured (error of the output against 64 bits, of which its
-// rounding is 0.00166, over 8191 keys of 64-node trees, the worst of 9 shapes; time of those trees, and of 16 x
-// 35000 keys with 128 heads): 0: 0.00170, 154 and 156 us; 2.5: 0.00187, 145 and 145; 3.5: 0.00214, 138 and 136;
-// 4: 0.00232, 135 and 134.
+// above what it has to, so that it is raised less often; the largest weight is then 2^3 or more instead of
+// 2^7, and what the dither leaves below 2^-16 of it.  kRoom's sides, measured (error of the output against 64 bits, of
+// which its rounding is 0.00166, over 8191 keys of 64-node trees; time of those trees, and of 16 x 35000 keys with
+// 128 heads): 0: 0.00178, 158 and 159 us; 2.5: 0.00181, 147 and 147; 4: 0.00185, 137 and 138; 5: 0.00187, 135 and
+// 135, but 0.0030 instead of 0.0018 where 30000 keys of unlike values are 8.5 nats below one.
 //
 // Masks.  A tile that reaches into the new tokens takes each row's word.  Places that no row sees in full
 // are kept out of the second product by value too, since 0 * NaN is NaN: rows behind the sequence are
@@ -54,13 +59,13 @@
 // TMEM: S double buffer at columns 0 and 128, O at 256, N columns for each 128 dims.
 //
 // What bounds it.  Shared memory's 128 bytes a clock: for 64 rows a tile's S reads the codes and Q (147 KB; 18
-// instructions of 64 clocks, measured alone), O the codes once for P's two terms and those for each 128 dims
-// (128 KB; 16 pairs of 78 clocks), the tile itself is written (74 KB), and P (16 KB): about 3100 clocks.  A
-// tile takes 3460 where the cache is in L2 (64-node trees) and 3740 where it comes from memory (whose rate
-// alone asks for 3230 over all CTAs); what is lost is the chain S, softmax, P, O, of which two tiles, all that
-// fits, overlap.  Measured, in graphs: 16 x 35000 keys with 4 tokens of 16 heads 83 us (memory's floor 48.8,
-// the products' 41.4 at the bf16 rate), with one token 62; 128 heads 135 (82.8 at the bf16 rate); 64-node trees
-// over 8191 keys 136 (77.0); 300 keys 9.8.  A call begins with 7 to 9 us (launch, lengths, Q's terms, first
+// instructions of 64 clocks, measured alone), O the codes for each of P's two terms and those for each 128 dims
+// (192 KB; 16 pairs of 96 clocks), the tile itself is written (74 KB), and P (16 KB): about 3350 clocks.  A
+// tile takes 3830 where the cache is in L2 and 4570 where all CTAs have their own from memory (5.1 TB/s; sequences of 4096
+// and 12288 tokens, 64 rows each, compared); what is lost is the chain S, softmax, P, O, of which two tiles, all that
+// fits, overlap.  Measured, in graphs: 16 x 35000 keys with 4 tokens of 16 heads 84 us (memory's floor 48.8,
+// the products' 41.4 at the bf16 rate), with one token 63; 128 heads 138 (82.8 at the bf16 rate); 64-node trees
+// over 8191 keys 137 (77.0); 300 keys 10.2.  A call begins with 7 to 9 us (launch, lengths, Q's terms, first
 // tiles of all CTAs at once) and ends with 2.5 of output and 4 to 7 of the join; a unit costs 6 to 10 more
 // (sums, Q, output), which short sequences pay one by one.
 #include "common.cuh"
@@ -69,6 +74,7 @@
 
 #include "../../include/mtp_latent.h"
 
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include <algorithm>
@@ -102,7 +108,7 @@ constexpr int kSegRing = 4;
 constexpr int kPrefetch = 1;                         // tiles ahead, into L2
 constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at the reference, and at most
                                                      // 2^(kShift + kTau) = 430 < 448
-constexpr float kRoom = 3.5f;                        // a raised reference is so far above the row's maximum
+constexpr float kRoom = 4.f;                        // a raised reference is so far above the row's maximum
 constexpr float kNoRef = -1e30f;                     // no key seen yet
 constexpr int kUnitTiles = 6, kCutTiles = 7, kCutPieces = 40;   // what a unit's ends, and cutting units, cost, in
                                                      // tiles (8 x 1000 keys, 4 tokens of 16 heads: 16.6 us at
@@ -413,11 +419,9 @@ __device__ __forceinline__ float warp_max(float x) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// Two f16x2 words (four values, lowest first) as e4m3 codes hi + lo; with kDither a number is added to what lo
-// is of.
-template <bool kDither>
-__device__ __forceinline__ void two_terms(uint32_t x0, uint32_t x1, uint32_t dither, uint32_t& hi, uint32_t& lo) {
-  uint32_t y0, y1;
+// Two f16x2 words (four values, lowest first) as e4m3 codes hi, and what they leave, as f16x2 words.
+__device__ __forceinline__ uint32_t first_term(uint32_t x0, uint32_t x1, uint32_t& y0, uint32_t& y1) {
+  uint32_t hi;
   asm("{\n"
       " .reg .b16 h0, h1;\n"
       " .reg .b32 g0, g1;\n"
@@ -431,10 +435,12 @@ __device__ __forceinline__ void two_terms(uint32_t x0, uint32_t x1, uint32_t dit
       "}\n"
       : "=r"(hi), "=r"(y0), "=r"(y1)
       : "r"(x0), "r"(x1));
-  if (kDither) {
-    asm("add.rn.f16x2 %0, %0, %1;\n" : "+r"(y0) : "r"(dither));
-    asm("add.rn.f16x2 %0, %0, %1;\n" : "+r"(y1) : "r"(dither));
-  }
+  return hi;
+}
+// Q's: e4m3 codes hi + lo.
+__device__ __forceinline__ void two_terms(uint32_t x0, uint32_t x1, uint32_t& hi, uint32_t& lo) {
+  uint32_t y0, y1;
+  hi = first_term(x0, x1, y0, y1);
   asm("{\n"
       " .reg .b16 l0, l1;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 l0, %1;\n"
@@ -443,6 +449,20 @@ __device__ __forceinline__ void two_terms(uint32_t x0, uint32_t x1, uint32_t dit
       "}\n"
       : "=r"(lo)
       : "r"(y0), "r"(y1));
+}
+// A weight's: hi is an e4m3 code, lo an e5m2 one, which is the upper byte of an f16.  What is added to the lower byte
+// first rounds it: half a step to the nearest, where lo is 2^-10 or more; below, the key's dither, 0 to 255 in both
+// halves, up or down in the proportion of the bits that go.  (No weight stays none.  A NaN's lo is lost, but not its hi,
+// and no carry leaves its half.)
+__device__ __forceinline__ uint32_t round_e5m2(uint32_t y, uint32_t dither) {
+  const __half2 v = *reinterpret_cast<const __half2*>(&y);
+  const uint32_t large = __hgeu2_mask(__habs2(v), __half2half2(__ushort_as_half(0x1400)));   // 2^-10
+  return y + ((dither & ~large) | (0x00800080u & large));
+}
+__device__ __forceinline__ void weight_terms(uint32_t x0, uint32_t x1, uint32_t dither, uint32_t& hi, uint32_t& lo) {
+  uint32_t y0, y1;
+  hi = first_term(x0, x1, y0, y1);
+  lo = __byte_perm(round_e5m2(y0, dither), round_e5m2(y1, dither), 0x7531);
 }
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {   // a in the low half
   uint32_t d;
@@ -510,6 +530,7 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t addr, uint32_t lbo, uint
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (4ull << 61);
 }
 constexpr uint32_t kAMajorM = 1u << 15;              // instruction descriptor: A is M-major
+constexpr uint32_t kBE5m2 = 1u << 10;                // ... B is of e5m2
 
 // Descriptors (sdesc_sw128 of sm100.cuh, sdesc_sw64) in two words: operands differ in the first one only, by
 // constants.  A thread that issues products shares its scheduler with two softmax warps, and a tile's 50
@@ -528,16 +549,17 @@ __device__ __forceinline__ void mma_one(uint32_t d_tmem, uint32_t a, uint32_t a_
       "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
       : "memory");
 }
-// D (+)= A B0, D += A B1: the second product takes A from the collector.  (Measured, M 128, N 64: 78 clocks the
-// pair, 96 with A fetched twice; shared memory gives 128 bytes a clock, and A is 4 KB, B 2 KB.)
+// D (+)= A B0, D += A B1, B0 and B1 of two formats.  (Measured, M 128, N 64: 96 clocks the pair; shared memory gives 128
+// bytes a clock, and A is 4 KB, B 2 KB.  Kept in the collector for the second product, A would come once, in 78, but
+// then both products take B in the first one's format, as measured.)
 __device__ __forceinline__ void mma_two(uint32_t d_tmem, uint32_t a, uint32_t a_hi, uint32_t b0, uint32_t b0_hi, uint32_t b1,
-                                        uint32_t b1_hi, uint32_t idesc, uint32_t accumulate) {
+                                        uint32_t b1_hi, uint32_t idesc0, uint32_t idesc1, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 x, y, z;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n mov.b64 z, {%5, %6};\n"
-      " setp.ne.b32 p, %8, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], x, y, %7, p;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], x, z, %7, 1;\n}\n" ::"r"(d_tmem),
-      "r"(a), "r"(a_hi), "r"(b0), "r"(b0_hi), "r"(b1), "r"(b1_hi), "r"(idesc), "r"(accumulate)
+      " setp.ne.b32 p, %9, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %7, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, z, %8, 1;\n}\n" ::"r"(d_tmem),
+      "r"(a), "r"(a_hi), "r"(b0), "r"(b0_hi), "r"(b1), "r"(b1_hi), "r"(idesc0), "r"(idesc1), "r"(accumulate)
       : "memory");
 }
 
@@ -914,12 +936,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             for (int k = 0; k < kBlocks; ++k) {
               if (!(alive = wait(bars.p_full[k], u & 1))) break;
               tc_fence_after();
-              // Both terms of P one after the other, the second with the A operand that the first has brought in.
+              // Both terms of P one after the other, the e5m2 one first.
 #pragma unroll
               for (int c = 0; c < kColumns; ++c)
                 mma_two(tmem + kOCol + c * N, v0.lo + at + ((k * (kBlockKeys / 8) * kGroup + 2 * c * kAtom) >> 4), v0.hi,
-                        lo.lo + (k * kBlockKeys * 64 >> 4), lo.hi, hi.lo + at + (k * (kBlockKeys / 8) * kGroup >> 4), hi.hi, kIdesc,
-                        k ? 1u : more);
+                        lo.lo + (k * kBlockKeys * 64 >> 4), lo.hi, hi.lo + at + (k * (kBlockKeys / 8) * kGroup >> 4), hi.hi,
+                        kIdesc | kBE5m2, kIdesc, k ? 1u : more);
               mma_commit(smem_u32(&bars.empty[st][k]));    // (with the rows of both of P's terms)
             }
             if (!alive) break;
@@ -937,8 +959,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
     const int w = warp - kWarpSoft, quarter = warp & 3, half = w >> 2;
     const int key = quarter * 32 + lane;             // of the tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t dither_h = half2_of((static_cast<float>(__brev(key) >> 25) - 63.5f) * 0x1p-16f, 0.f) & 0xffffu;
-    const uint32_t dither = dither_h | dither_h << 16;
     const float descale = *p.descale, factor = p.scale_log2 * descale;
     const int row0 = half * kHalf;
     Meeting meet{smem_u32(&bars.meet[half]), 0}, meet_all{smem_u32(&bars.meet[2]), 0};
@@ -993,8 +1013,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
           uint32_t h0, h1, l0, l1;
-          two_terms<false>(scaled_half2(x[0][i].x, up), scaled_half2(x[0][i].y, up), 0u, h0, l0);
-          two_terms<false>(scaled_half2(x[0][i].z, up), scaled_half2(x[0][i].w, up), 0u, h1, l1);
+          two_terms(scaled_half2(x[0][i].x, up), scaled_half2(x[0][i].y, up), h0, l0);
+          two_terms(scaled_half2(x[0][i].z, up), scaled_half2(x[0][i].w, up), h1, l1);
           if (i * kSide < kDim / 8) {
             const uint32_t at = place[i % (16 / kSide)] + i * kSide / 16 * q_column<N>() + go * kStep * 128;
             st_shared8(at, h0, h1);
@@ -1072,13 +1092,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
                 if (!((seen >> r) & 1u)) y[r] = -INFINITY;
             }
           };
+          // The dither: a tile's 128 keys have evenly spread numbers, and other ones in every tile of the sequence.
+          const uint32_t dither = ((__brev(key) ^ static_cast<uint32_t>(t) * 0x9E3779B1u) >> 24) * 0x00010001u;
           uint32_t hi[kHalf / 4], lo[kHalf / 4];
           auto weights = [&]() {
 #pragma unroll
             for (int r = 0; r < kHalf; r += 4) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) y[r + i] = exp2_hw(y[r + i]);
-              two_terms<true>(half2_of(y[r], y[r + 1]), half2_of(y[r + 2], y[r + 3]), dither, hi[r / 4], lo[r / 4]);
+              weight_terms(half2_of(y[r], y[r + 1]), half2_of(y[r + 2], y[r + 3]), dither, hi[r / 4], lo[r / 4]);
             }
           };
           logits();
