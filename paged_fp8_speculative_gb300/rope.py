@@ -50,7 +50,8 @@ def inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor:
     def pair_of(turns: float) -> float:       # the pair (not a whole one) that turns so often
         return half * math.log(original_length / (2.0 * math.pi * turns)) / math.log(base)
 
-    first, last = max(math.floor(pair_of(fast)), 0), min(math.ceil(pair_of(slow)), half - 1)
+    # (the upper border may lie behind the last pair, half - 1: then no pair is slow enough for the whole factor)
+    first, last = max(math.floor(pair_of(fast)), 0), min(math.ceil(pair_of(slow)), rot_dim - 1)
     out = []
     for i, f in enumerate(plain):
         if scaling == "parts":
