@@ -378,17 +378,17 @@ extern "C" int mtp_rope_freqs(const double* inv_freq, int32_t n, int64_t* freqs)
   if (n < 0 || (n > 0 && (!inv_freq || !freqs))) return MTPATTN_E_ARG;
   for (int32_t i = 0; i < n; ++i)
     if (!(inv_freq[i] >= 0) || inv_freq[i] > 1048576.0) return MTPATTN_E_ARG;
-  // 1 / (2 pi) as the sum of two doubles; the fraction of a turn in two pieces, each a whole number of
-  // 2^-64 after its rounding (explicit fma: the same on every host)
+  // 1 / (2 pi) as the sum of two doubles; the fraction of a turn in two pieces, the upper one a whole number of
+  // 2^-32, and one rounding of the lower (in units of 2^-64: below 2^33, so summed to 2^-20 of one).  Every fma is
+  // written out, so that no compiler's choice of them can change a bit.
   const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
   for (int32_t i = 0; i < n; ++i) {
     const double a = inv_freq[i] * hi;
-    const double b = fma(inv_freq[i], hi, -a) + inv_freq[i] * lo;
+    const double b = fma(inv_freq[i], lo, fma(inv_freq[i], hi, -a));
     const double turns = a - floor(a);                             // exact
     const double whole = floor(ldexp(turns, 32)), part = turns - ldexp(whole, -32);   // exact
-    uint64_t f = static_cast<uint64_t>(whole) << 32;               // (below 2^32)
-    f += static_cast<uint64_t>(llrint(ldexp(part, 64)));           // below 2^32, exact but for the last bit
-    f += static_cast<uint64_t>(llrint(ldexp(b, 64)));              // a few units, either sign
+    const uint64_t f = (static_cast<uint64_t>(whole) << 32) +      // (below 2^32)
+                       static_cast<uint64_t>(llrint(ldexp(part, 64) + ldexp(b, 64)));
     freqs[i] = static_cast<int64_t>(f);
   }
   return MTPATTN_OK;
