@@ -68,8 +68,9 @@ int mtp_rope_freqs(const double* inv_freq, int32_t n, int64_t* freqs);
  * Rows that belong to no sequence (before cu_seqlens_q[0], behind the last) are not written anywhere.
  * A sequence with more tokens than seq_lens[b] (MTPATTN_ERR_QLEN_GT_SEQ) or more than its table holds
  * (_SEQ_TOO_LONG), and a token whose page is outside [0, num_pages) (_PAGE), are left out of the caches;
- * their q is rotated all the same.  Where cu_seqlens_q does not ascend within total_q, a row of unknown
- * sequence is left out and sets MTPATTN_ERR_QLEN.
+ * their q is rotated all the same.  Where cu_seqlens_q does not ascend from 0 to total_q everywhere,
+ * MTPATTN_ERR_QLEN is set: then a row is known if one sequence alone, whose own two entries ascend within
+ * total_q, claims it, and other rows are not written anywhere.
  */
 int mtp_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head, const void* k,
                     int64_t k_stride_tok, int64_t k_stride_head, const void* v, int64_t v_stride_tok,
