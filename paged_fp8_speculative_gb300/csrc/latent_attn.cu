@@ -1055,6 +1055,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
         load_rows(sh.factor + row0, fac);
 #pragma unroll
         for (int r = 0; r < kHalf; ++r) l[r] = ref[r] = 0.f;
+        // A row's products are below 2^26 (256 x 448 x 576): only past this factor can a logit leave float32's range.
+        const bool wild = __any_sync(0xffffffffu, lane < kHalf && !(fabsf(sh.factor[row0 + lane % kHalf]) < 0x1p101f));
         const int start = s.L - s.n;                   // first new token
         const bool late = (s.t0 + 1) * kKeys > start;  // a row may see nothing of the first tile
 #pragma unroll 1
@@ -1085,6 +1087,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             tmem_wait<kHalf>(lo);
 #pragma unroll
             for (int r = 0; r < kHalf; ++r) y[r] = fmaf(__uint_as_float(h[r]) + __uint_as_float(lo[r]), fac[r], -ref[r]);
+            if (wild) {                                // a logit that does makes its row NaN, at either end
+#pragma unroll
+              for (int r = 0; r < kHalf; ++r)
+                if (isinf((__uint_as_float(h[r]) + __uint_as_float(lo[r])) * fac[r])) y[r] = NAN;
+            }
             if (ragged) {
               nan = !(y[0] == y[0]);
 #pragma unroll
