@@ -109,7 +109,7 @@ constexpr int kPrefetch = 1;                         // tiles ahead, into L2
 constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at the reference, and at most
                                                      // 2^(kShift + kTau) = 430 < 448
 constexpr float kRoom = 4.f;                        // a raised reference is so far above the row's maximum
-constexpr float kNoRef = -1e30f;                     // no key seen yet
+constexpr float kNoRef = -INFINITY;                  // no key seen yet (a reference is finite)
 constexpr int kUnitTiles = 6, kCutTiles = 7, kCutPieces = 40;   // what a unit's ends, and cutting units, cost, in
                                                      // tiles (8 x 1000 keys, 4 tokens of 16 heads: 16.6 us at
                                                      // kUnitTiles 7, 15.7 at 6; 1 x 300, 1 token, 9.6 and 10.4 at 5)
@@ -1423,7 +1423,7 @@ __global__ void __launch_bounds__(kDims / 4 * kGroups) latent_join_kernel(const 
     for (int k = 0; k < kMaxCtas / 32; ++k) {
       const int i = lane + 32 * k;
       if (i >= n) continue;
-      const float w = exp2_hw(ref[k] - top);
+      const float w = ref[k] == kNoRef ? 0.f : exp2_hw(ref[k] - top);   // (nothing seen: sum 0, or NaN)
       s_w[r][i] = w;
       total += w * sum[k];
     }
