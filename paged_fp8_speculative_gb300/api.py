@@ -121,6 +121,8 @@ def _verify_fwd(entry, q, k_cache, v_cache, block_tables, seq_lens, cu_seqlens_q
         # length); a workspace made here is sized for the S it will choose, a given one is
         # checked by the library.
         chosen = int(num_segments or 0)
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")     # (taken as the bytes from its first one on)
         if out is None:
             out = torch.empty(total_q, hq, HEAD_DIM, dtype=torch.bfloat16, device=dev)
         if workspace is None:
@@ -243,7 +245,9 @@ def mtp_verify_attn_get_scheduling() -> int:
 
 def mtpattn_stream_read(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, blocks: int = 0,
                         stream=None) -> torch.Tensor:
-    """Read every byte of ``buf`` once (streaming-read ceiling probe); returns the sink."""
+    """Read every byte of ``buf`` once (streaming-read ceiling probe); returns the sink (int32, one word a block)."""
+    if not buf.is_contiguous():
+        raise ValueError("buf must be contiguous")
     if blocks == 0:
         blocks = int(lib().mtpattn_stream_read_default_blocks())
         if blocks <= 0:
@@ -251,6 +255,8 @@ def mtpattn_stream_read(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, 
     with _temporaries_on(stream, buf.device, sink is None):
         if sink is None:
             sink = torch.empty(blocks, dtype=torch.int32, device=buf.device)
+    if sink.dtype != torch.int32 or not sink.is_contiguous() or sink.numel() < blocks:
+        raise ValueError(f"sink must be a contiguous int32 tensor of at least {blocks} words")
     nbytes = buf.numel() * buf.element_size()
     rc = lib().mtpattn_stream_read(_ptr(buf), nbytes, _ptr(sink), blocks, _stream_handle(stream))
     if rc != OK:

@@ -75,6 +75,12 @@ int32_t count32(int64_t n, const char* name) {
 }
 const int32_t* ints(const at::Tensor& t) { return static_cast<const int32_t*>(t.const_data_ptr()); }
 int32_t* ints_out(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+// A workspace is taken as the bytes from its first one on.
+const at::Tensor& workspace_of(PyObject* o) {
+  const at::Tensor& t = tensor(o, "workspace");
+  REFUSE_IF(!t.is_contiguous(), "workspace must be contiguous");
+  return t;
+}
 int32_t* status_of(PyObject* o) {
   if (!given(o)) return nullptr;
   const at::Tensor& t = tensor(o, "status");
@@ -188,7 +194,7 @@ PyObject* tree_attn(PyObject* const* a) {
   REFUSE_IF(out.scalar_type() != at::kBFloat16 || out.sizes() != q.sizes() || out.stride(2) != 1,
             "out must be bf16 [total_q, H_q, 256] with unit stride on head_dim");
   at::Tensor made;
-  const at::Tensor& ws = given(a[11]) ? tensor(a[11], "workspace") : made;
+  const at::Tensor& ws = given(a[11]) ? workspace_of(a[11]) : made;
   if (!ws.defined()) {
     const size_t need = mtp_tree_attn_workspace_size(seqs, total, hq, hkv, width);
     made = at::empty({static_cast<int64_t>(need < 256 ? 256 : need)}, q.options().dtype(at::kByte));
@@ -339,7 +345,7 @@ Table table_args(const at::Tensor& t, const at::Tensor& lens, const at::Tensor& 
   return {count32(t.size(0), "block_tables"), count32(t.size(1), "block_tables")};
 }
 at::Tensor cache_workspace(PyObject* o, const at::Tensor& like, const Table& t) {
-  if (given(o)) return tensor(o, "workspace");
+  if (given(o)) return workspace_of(o);
   const size_t need = mtp_cache_workspace_size(t.rows, t.width);
   return at::empty({static_cast<int64_t>(need < 256 ? 256 : need)}, like.options().dtype(at::kByte));
 }
@@ -638,7 +644,7 @@ PyObject* latent_attn(PyObject* const* a) {
   const Rows outr = rows_of(out, "out", at::kBFloat16, qr.tokens, MTP_LATENT_DIM, true);
   REFUSE_IF(outr.heads != qr.heads, "out must have q's heads");
   at::Tensor made;
-  const at::Tensor& ws = given(a[9]) ? tensor(a[9], "workspace") : made;
+  const at::Tensor& ws = given(a[9]) ? workspace_of(a[9]) : made;
   if (!ws.defined()) {
     const size_t need = mtp_latent_attn_workspace_size(at_.seqs, total, qr.heads, at_.width);
     made = at::empty({static_cast<int64_t>(need < 256 ? 256 : need)}, q.options().dtype(at::kByte));
