@@ -111,13 +111,15 @@ constexpr float kShift = 7.f, kTau = 1.75f;          // a weight is 2^kShift at 
 constexpr float kRoom = 4.f;                        // a raised reference is so far above the row's maximum
 constexpr float kNoRef = -INFINITY;                  // no key seen yet (a reference is finite)
 constexpr int kUnitTiles = 6, kCutTiles = 7, kCutPieces = 40;   // what a unit's ends, and cutting units, cost, in
-                                                     // tiles (8 x 1000 keys, 4 tokens of 16 heads: 16.6 us at
-                                                     // kUnitTiles 7, 15.7 at 6; 1 x 300, 1 token, 9.6 and 10.4 at 5)
+                                                     // tiles (kUnitTiles 5, 6 and 7: 8 x 1000 keys, 4 tokens of 16
+                                                     // heads, 16.1, 16.0 and 17.0 us; 20 x 2000, 1 token of 128, 29.7,
+                                                     // 29.0 and 30.8; the others: Walker::start)
 constexpr int kFewTiles = 8;
 constexpr int kWholeTiles = 4;                       // tables no longer: units stay whole, and no join is launched
-                                                     // (64 x 300 keys, 1 token of 128 heads, 22.9 us with cuts, 19.4
-                                                     // without; 256 x 500 90.9 and 81.6; 1 x 500, 4 tokens of 16, 10.3
-                                                     // and 11.1; 1 x 700 would take 10.1 and 13.5)
+                                                     // (with cuts and without: 64 x 300 keys, 1 token of 128 heads,
+                                                     // 22.7 and 19.3 us; 256 x 500 90.9 and 81.8; 16 x 500, 4 tokens of
+                                                     // 16, 13.4 and 12.2; but one such 10.3 and 11.3, and 1 x 700 would
+                                                     // take 10.4 and 13.8)
 constexpr int kMaxCtas = 160;
 constexpr uint32_t kBadSum = 0x7fd0bad1u;            // a sum of a sequence with a bad page (a NaN that no
                                                      // arithmetic makes)
@@ -307,9 +309,11 @@ struct Walker {
     C = max(1, static_cast<int>((static_cast<uint32_t>(W) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)));
     V = 0;
     // Units stay whole where so many of the longest take no longer than equal pieces and what cutting costs
-    // (in tiles): the join, and its bytes, fewer for units that are not full.  (kCutTiles: 16 x 500 keys, 4 tokens
-    // of 16 heads, take 16.2 us at 4, 12.8 at 7; one of them 10.1 at 7, 11.7 at 10.  kCutPieces: 64-node trees over
-    // 8 x 8191 keys take 135 us at 40, 140 at 80.)
+    // (in tiles): the join, and its bytes, fewer for units that are not full.  Both sides, of tables above kWholeTiles;
+    // 4 tokens of 16 heads where no heads are given.  kCutTiles 4, 7 and 10: 16 x 700 keys 16.2, 15.7 and 15.7 us; 8 x 1000
+    // 16.0, 16.0 and 18.4; in tables of 8192 pages 1 x 500 15.7, 19.8 and 19.8, 1 x 1000 15.9, 15.9 and 28.5.  kCutPieces
+    // 20, 40 and 80: 64-node trees over 8 x 8191 keys 136.7, 136.6 and 140.1; 20 x 2000, 1 token of 128 heads, 44.2, 29.0
+    // and 29.0; in tables of 8192 pages 1 x 500 19.8, 19.8 and 15.7, 1 x 1000 28.4, 15.9 and 15.9.
     const float full = fminf(1.f, static_cast<float>(p.total_q) * static_cast<float>(p.heads) / static_cast<float>(N * max(units, 1)));
     const int join = kCutTiles + static_cast<int>(static_cast<float>(units + p.ctas) * full * (N / 64.f / kCutPieces));
     const int each = max(1, static_cast<int>((static_cast<uint32_t>(units) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)));
@@ -1493,7 +1497,9 @@ int64_t line_bound(int64_t units, int32_t max_pages) {
 }
 // Rows of a unit: as many columns of the products as an average sequence fills.  But 16, whose Q, sums and output
 // take 6 us less than those of 64, while then no CTA has more than kFewTiles tiles of a table's length (4 tokens of
-// 16 heads over 300 keys 16.4 -> 10.7 us, over 20000 21.8 -> 19.4; over 50000, which is above it, 24.1 against 28.8).
+// 16 heads over 300 keys 17.3 -> 10.3 us, over 20000 21.3 -> 18.2; above it, over 50000, 16 rows would take 27.2
+// instead of 24.4, and 20 x 2000 keys with 1 token of 128 heads 39.8 instead of 29.0).  A table's length, not the
+// sequences', which the host does not know: in one of 8192 pages 300 keys take 18.7.
 int unit_rows(int32_t num_seqs, int32_t total_q, int32_t heads, int32_t max_pages, int64_t ctas) {
   const int64_t rows = (static_cast<int64_t>(total_q) * heads + num_seqs - 1) / std::max(num_seqs, 1);
   const int64_t tiles = (max_pages + kTilePages - 1) / kTilePages;
@@ -1587,8 +1593,8 @@ int launch_latent(LatentParams& p, int device, cudaStream_t stream) {
   }
   if (launch_pdl(kernel, dim3(p.ctas), kLatentThreads, smem_bytes<N>(), stream, p) != cudaSuccess) return MTPATTN_E_LAUNCH;
   if (p.whole) return MTPATTN_OK;
-  // Few rows in many pieces (one row of 105000 keys in 152: 47 -> 31 us a call) are joined by 4 CTAs for each 2 rows,
-  // where at most 16 pieces cost 0.7 us more so.
+  // Few rows in many pieces are joined by 4 CTAs for each 2 rows (4 tokens of 16 heads over 50000 keys 41.0 -> 24.4 us, 1
+  // token over 105000 29.4 -> 21.5), where at most 16 pieces cost 0.1 to 0.4 us more so (1 x 700 10.4 against 10.8).
   const bool one = p.unit_bound * N <= 320 && p.max_pages > 16 * kTilePages, few = p.unit_bound <= 32;
   const void* join = one   ? reinterpret_cast<const void*>(latent_join_kernel<N, 2, 128, 8, true, 8>)
                      : few ? reinterpret_cast<const void*>(latent_join_kernel<N, 2, 512, 2, true, 4>)
