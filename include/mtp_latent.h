@@ -36,8 +36,9 @@ extern "C" {
  * seq_lens[b] cached tokens.  New token i sees all tokens before the new ones, and of the new ones those
  * up to itself (tree_mask NULL: a chain), or those whose bit is set in tree_mask (as in mtp_tree_attn_fwd:
  * bits >= n_b are ignored, the token's own bit is not implied).  A token that sees nothing gets zeros.
- * Tokens that a row does not see do not influence it, whatever codes they hold.  A row of q that
- * holds an infinity or a NaN gets NaN, and so does one whose logits leave float32's range.
+ * Tokens that a row does not see do not influence it, whatever codes they hold.  Logits are float32: a row of
+ * q that holds an infinity or a NaN gets NaN, and so does one that sees a logit (times log2 e) outside float32's range,
+ * at either end.
  *
  *  q            device bf16 [total_q][num_heads][576], strides in elements (multiples of 8), unit stride
  *               along the row, 16-byte aligned
@@ -50,10 +51,11 @@ extern "C" {
  *               initialised and holds nothing between calls.  Calls that overlap on the GPU must use
  *               different workspaces.
  *  out          device bf16 [total_q][num_heads][512], strides in elements (multiples of 8), 16-byte
- *               aligned
+ *               aligned; its rows apart from one another and from all inputs
  * Sequences with a device-side error (MTPATTN_ERR_QLEN: n_b outside [1, 64]; _QLEN_GT_SEQ;
  * _SEQ_TOO_LONG; _PAGE) get zeros, except that the rows of a sequence whose cu_seqlens_q entries do not
- * ascend within total_q are unknown and not written.  Rows that belong to no sequence are not written.
+ * ascend within total_q are unknown and not written.  Rows that belong to no sequence are not written, and rows
+ * that several sequences claim (then some entries do not ascend: _QLEN) are unspecified.
  * (MTPATTN_ERR_TIMEOUT: a wait ran out, about two seconds without progress; the rows it concerns are
  * unspecified.)  Results are the same bits in every call with the same arguments.  Two kernels are
  * launched, or one where tables have no more than 32 pages.

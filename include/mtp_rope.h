@@ -64,7 +64,7 @@ int mtp_rope_freqs(const double* inv_freq, int32_t n, int64_t* freqs);
  *               as in mtp_verify_attn_fwd; the pages under the new tokens belong to their row alone
  *  k_descale, v_descale   device float32, one element each
  *  q_out        device bf16 [total_q][num_q_heads][256], strides as the inputs'.  q itself, if that is
- *               bf16, with q's strides; else apart from all inputs.
+ *               bf16, with q's strides; else apart from all inputs.  Its rows are apart from one another.
  * Rows that belong to no sequence (before cu_seqlens_q[0], behind the last) are not written anywhere.
  * A sequence with more tokens than seq_lens[b] (MTPATTN_ERR_QLEN_GT_SEQ) or more than its table holds
  * (_SEQ_TOO_LONG), and a token whose page is outside [0, num_pages) (_PAGE), are left out of the caches;
