@@ -38,7 +38,8 @@
 // reversed, and each tile has them in another order, so that keys whose values repeat with any period have evenly spread
 // ones too; the same bits come every time.  (Two e4m3 terms with one order for all tiles lost the weights below 2^-9
 // of whole classes of keys: with a first key 9.5 nats above 8190 others and values of period 2 the output was 0.4 off, in
-// 2-norm, where it is now 0.0017.)  The sums of weights are of the unrounded ones, in float32.
+// 2-norm, where it is now 0.0017.)  The sums of weights, in float32, are of what the terms stand for: a weight that is
+// nearly all of its row's comes out whole, where its rounding of up to 2^-8 would be the output's.
 //
 // Online softmax in the log2 domain with a lazy reference: raised, and O rescaled in TMEM, only when a logit
 // exceeds it by more than kTau.  So a tile's maxima over keys (across lanes and warps, which this orientation
@@ -467,6 +468,30 @@ __device__ __forceinline__ void weight_terms(uint32_t x0, uint32_t x1, uint32_t 
   uint32_t y0, y1;
   hi = first_term(x0, x1, y0, y1);
   lo = __byte_perm(round_e5m2(y0, dither), round_e5m2(y1, dither), 0x7531);
+}
+// What four weights' terms stand for together, added to l.
+__device__ __forceinline__ void add_weights(float* l, uint32_t hi, uint32_t lo) {
+  uint32_t x[2];
+  asm("{\n"
+      " .reg .b16 h0, h1;\n"
+      " mov.b32 {h0, h1}, %2;\n"
+      " cvt.rn.f16x2.e4m3x2 %0, h0;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h1;\n"
+      "}\n"
+      : "=r"(x[0]), "=r"(x[1])
+      : "r"(hi));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm("{\n"
+        " .reg .b16 a, b;\n"
+        " .reg .b32 both;\n"
+        " add.rn.f16x2 both, %2, %3;\n"
+        " mov.b32 {a, b}, both;\n"
+        " add.rn.f32.f16 %0, a, %0;\n"
+        " add.rn.f32.f16 %1, b, %1;\n"
+        "}\n"
+        : "+f"(l[2 * i]), "+f"(l[2 * i + 1])
+        : "r"(x[i]), "r"(__byte_perm(lo, 0u, i ? 0x3424 : 0x1404)));
 }
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {   // a in the low half
   uint32_t d;
@@ -1232,7 +1257,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(const __
             mbar_arrive(smem_u32(&bars.s_free[u & 1]));
           }
 #pragma unroll
-          for (int r = 0; r < kHalf; ++r) l[r] += y[r];
+          for (int r = 0; r < kHalf; r += 4) add_weights(l + r, hi[r / 4], lo[r / 4]);
         }
         if (!alive) break;
         // ---- the sums, and the next segment's Q while the last products run

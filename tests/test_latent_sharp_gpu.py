@@ -135,3 +135,17 @@ def test_the_large_weight_elsewhere(at):
     s.keys = s.keys.clone()
     s.keys[rows, 0], s.keys[rows, at] = s.keys[rows, at].clone(), s.keys[rows, 0].clone()
     s.check((0, 127))
+
+
+@pytest.mark.parametrize("seqs,length,heads", [(128, 4000, 16), (152, 3000, 64), (1, 20000, 16)])
+def test_a_large_weight_that_raises_no_reference(seqs, length, heads):
+    """A second key 2 to 3.9 nats above the first large one: its weight is whatever the reference that the first one has
+    left makes it, no power of two, and most of the row's."""
+    s = Sharp(seqs, length, heads, 1, 9.5, 0, seed=heads)
+    at = torch.randint(1, length - 1, (seqs,), generator=torch.Generator().manual_seed(1)).cuda()
+    rows = torch.arange(seqs, device="cuda")
+    s.cache.view(-1, 576)[s.bt.long()[rows, at // 16] * 16 + at % 16, 514] = 0x38
+    s.keys[rows, at, 514] = 0x38
+    above = 2.0 + 1.9 * torch.rand(seqs, heads, generator=torch.Generator("cuda").manual_seed(2), device="cuda")
+    s.q[..., 514] = s.q[..., 512] + (above / (SCALE * DESCALE)).bfloat16()
+    s.check(sorted({0, seqs // 2, seqs - 1}))
