@@ -68,7 +68,7 @@ int mtp_rope_freqs(const double* inv_freq, int32_t n, int64_t* freqs);
  * Rows that belong to no sequence (before cu_seqlens_q[0], behind the last) are not written anywhere.
  * A sequence with more tokens than seq_lens[b] (MTPATTN_ERR_QLEN_GT_SEQ) or more than its table holds
  * (_SEQ_TOO_LONG), and a token whose page is outside [0, num_pages) (_PAGE), are left out of the caches;
- * their q is rotated all the same.  Where cu_seqlens_q does not ascend from 0 to total_q everywhere,
+ * their q is rotated all the same.  Where cu_seqlens_q does not ascend, or leaves 0 .. total_q,
  * MTPATTN_ERR_QLEN is set: then a row is known if one sequence alone, whose own two entries ascend within
  * total_q, claims it, and other rows are not written anywhere.
  */
